@@ -38,12 +38,20 @@ EXPORTS = (
     "qsa_compress_keys_paged", "qsa_score_paged", "qsa_decode_paged", "qsa_score_chunk",
     "qsa_resolve", "qsa_sparse_attn_rows", "qsa_test_chunk_timeout", "qsa_trace_read",
 )
+# and those of include/qsa_kv.h, the operators round the paged cache
+KV_EXPORTS = (
+    "qsa_rope_table", "qsa_rope", "qsa_kv_workspace_size", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn",
+)
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
 
 MAX_DRAFT_GAP = 64  # QSA_MAX_DRAFT_GAP
 MAX_CHUNK = 65536  # QSA_MAX_CHUNK
 MAX_SCORE_BATCH = 16384  # QSA_MAX_SCORE_BATCH
+MAX_KV_HEADS = 1024  # QSA_MAX_KV_HEADS
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # qsa_rope_layout
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}  # qsa_rope_scaling
 
 
 class QSAError(RuntimeError):
@@ -64,6 +72,31 @@ class Dims(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class Strides(ctypes.Structure):
+    """qsa_strides: element strides of a [batch][token][head][dim] tensor."""
+
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    """qsa_rope_spec: what a table of rotary frequencies is made from."""
+
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+        ("alpha", ctypes.c_double), ("beta", ctypes.c_double), ("amplitude", ctypes.c_double),
+    ]
+
+
+class RopeArgs(ctypes.Structure):
+    """qsa_rope_args: a rotation as the kernels take it."""
+
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_void_p),
+    ]
 
 
 def _load() -> ctypes.CDLL:
@@ -95,6 +128,15 @@ def _load() -> ctypes.CDLL:
         "qsa_sparse_attn_rows": (I, [D, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_trace_read": (I, [ctypes.c_int32, P, ctypes.c_int32, ctypes.c_int32]),
     }
+    R, S, N = ctypes.POINTER(RopeArgs), ctypes.POINTER(Strides), ctypes.c_int32
+    sig.update({
+        "qsa_rope_table": (I, [ctypes.POINTER(RopeSpec), P, ctypes.POINTER(ctypes.c_float)]),
+        "qsa_rope": (I, [R, N, N, N, N, N, P, S, P, P, S, P]),
+        "qsa_kv_workspace_size": (I, [D, ctypes.POINTER(SZ)]),
+        "qsa_kv_append": (I, [D, N, R, P, S, P, S, P, S, P, S, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_kv_gather": (I, [D, N, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_paged_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -402,6 +444,210 @@ def decode(d: Dims, q_idx, kc, q, k_cache, v_cache, k_scale, v_scale, page_table
     _check(lib.qsa_decode(ctypes.byref(d), _ptr(q_idx), _ptr(kc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                           _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(q_pos), _ptr(scores),
                           _ptr(sel_blk), _ptr(sel_pos), _ptr(out), w, n, _stream(stream)), "qsa_decode")
+
+
+# ---------------------------------------------------------------------------
+# operators round the paged cache (include/qsa_kv.h)
+# ---------------------------------------------------------------------------
+class Rope:
+    """A rotation of the first ``rot_dim`` components of every head, made by
+    make_rope: its frequencies on the device and its amplitude."""
+
+    def __init__(self, args: RopeArgs, table: torch.Tensor):
+        self.args, self.table = args, table  # the table owns the memory args.turns points to
+        self.device_index = table.get_device()
+
+    @property
+    def rot_dim(self) -> int:
+        return self.args.rot_dim
+
+    @property
+    def amplitude(self) -> float:
+        return self.args.amplitude
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+               factor: float = 1.0, orig_len: float = 0.0, alpha: float = 0.0, beta: float = 0.0,
+               amplitude: float = 0.0) -> Tuple[np.ndarray, float]:
+    """qsa_rope_table (host): the pairs' frequencies in turns per position
+    times 2^64 (numpy uint64 [rot_dim / 2]) and the amplitude."""
+    spec = RopeSpec(rot_dim, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], base, factor, orig_len, alpha, beta,
+                    amplitude)
+    turns = np.zeros(max(1, rot_dim // 2), dtype=np.uint64)
+    amp = ctypes.c_float(0)
+    _check(lib.qsa_rope_table(ctypes.byref(spec), turns.ctypes.data, ctypes.byref(amp)), "qsa_rope_table")
+    return turns, amp.value
+
+
+def make_rope(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+              factor: float = 1.0, orig_len: float = 0.0, alpha: float = 0.0, beta: float = 0.0,
+              amplitude: float = 0.0, device="cuda") -> Rope:
+    """A rotation for rope and kv_append: layout "half" (component i pairs
+    with i + rot_dim / 2) or "interleaved" (2 i with 2 i + 1); scaling "none",
+    "linear", "ntk" or "yarn" (qsa_rope_spec says what each does)."""
+    turns, amp = rope_table(rot_dim, base, layout, scaling, factor, orig_len, alpha, beta, amplitude)
+    table = torch.from_numpy(turns.view(np.int64)).to(device)
+    return Rope(RopeArgs(rot_dim, ROPE_LAYOUTS[layout], amp, table.data_ptr()), table)
+
+
+def _want_on(dev: int, t: torch.Tensor, name: str, shape, dtype):
+    """_want, and on the current device (whose stream and SMs the call uses)."""
+    _want(t, name, shape, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _want_strided(dev: int, t: torch.Tensor, name: str, shape):
+    """A BF16 [batch][token][head][dim] tensor on the current device whose
+    last dimension is contiguous; its strides (None: contiguous)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return Strides(st[0], st[1], st[2])
+
+
+def _rope_args(rope: Rope, dev: int):
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope (make_rope)")
+    if rope.device_index != dev:
+        raise ValueError(f"rope is on cuda:{rope.device_index}, the current device is cuda:{dev}")
+    return rope.args
+
+
+def rope(rope: Rope, x, pos, y, inverse: bool = False, stream=None):
+    """Rotary positions: y[r][j] = x[r][j] rotated to position pos[r][j], every
+    head (x, y bf16 [B][n][H][D], any strides with a contiguous last dimension;
+    pos int32 [B][n]; rows with pos < 0 are left as they are). y may be x.
+    inverse rotates back: the gradient of the forward call."""
+    dev = torch.cuda.current_device()
+    args = _rope_args(rope, dev)
+    if x.dim() != 4:
+        raise ValueError("x must be [B][n][H][D]")
+    xs = _want_strided(dev, x, "x", x.shape)
+    ys = _want_strided(dev, y, "y", x.shape)
+    B, n, H, D = x.shape
+    _want_on(dev, pos, "pos", (B, n), torch.int32)
+    _check(lib.qsa_rope(args, B, n, H, D, int(inverse), x.data_ptr(), xs, pos.data_ptr(), y.data_ptr(), ys,
+                        _stream(stream)), "qsa_rope")
+
+
+def kv_workspace_size(d: Dims) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.qsa_kv_workspace_size(ctypes.byref(d), ctypes.byref(n)), "qsa_kv_workspace_size")
+    return n.value
+
+
+def make_kv_workspace(d: Dims, device="cuda", stream=None) -> torch.Tensor:
+    """Allocate and zero a workspace for kv_append, kv_gather and paged_attn
+    with ``d`` (torch owns the memory)."""
+    n = kv_workspace_size(d)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    _check(lib.qsa_workspace_init(ctypes.c_void_p(ws.data_ptr()), n, _stream(stream)), "qsa_workspace_init")
+    return ws
+
+
+def _cache_ptrs(dev: int, d: Dims, k_cache, v_cache, k_scale, v_scale, page_table):
+    """Checks the paged cache and returns its pointers (the scales' are null
+    for a BF16 cache without them)."""
+    shape = (d.num_pages, d.n_kv_heads, d.page_size, d.head_dim)
+    dt = _kv_dtype(d)
+    _want_on(dev, k_cache, "k_cache", shape, dt)
+    _want_on(dev, v_cache, "v_cache", shape, dt)
+    ks = vs = None
+    if d.kv_dtype == KV_FP8_E4M3 or k_scale is not None or v_scale is not None:
+        _want_on(dev, k_scale, "k_scale", (d.n_kv_heads,), torch.float32)
+        _want_on(dev, v_scale, "v_scale", (d.n_kv_heads,), torch.float32)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    _want_on(dev, page_table, "page_table", (d.batch, d.max_pages), torch.int32)
+    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, page_table.data_ptr()
+
+
+def _ws_on(dev: int, ws: torch.Tensor):
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws, rope: Optional[Rope] = None,
+              q=None, q_out=None, stream=None):
+    """New keys and values (bf16 [B][n][H_kv][D], any strides) into the cache
+    at positions pos [B][n] (consecutive per request, -1 for no token): keys
+    rotated by ``rope`` if given, both quantised for an E4M3 cache. With q
+    (bf16 [B][n][H_q][D]) the same tokens' queries are rotated into q_out."""
+    dev = torch.cuda.current_device()
+    if k.dim() != 4:
+        raise ValueError("k must be [B][n][H_kv][D]")
+    n = k.shape[1]
+    shape = (d.batch, n, d.n_kv_heads, d.head_dim)
+    ks = _want_strided(dev, k, "k", shape)
+    vs = _want_strided(dev, v, "v", shape)
+    args = None if rope is None else _rope_args(rope, dev)
+    qs = qos = qp = qop = None
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or rope is None:
+            raise ValueError("q needs q_out and rope")
+        qshape = (d.batch, n, d.n_q_heads, d.head_dim)
+        qs = _want_strided(dev, q, "q", qshape)
+        qos = _want_strided(dev, q_out, "q_out", qshape)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
+    _want_on(dev, pos, "pos", (d.batch, n), torch.int32)
+    w, nb = _ws_on(dev, ws)
+    _check(lib.qsa_kv_append(d, n, args, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qop, qos, pos.data_ptr(), pt,
+                             kc, vc, ksc, vsc, w, nb, _stream(stream)), "qsa_kv_append")
+
+
+def kv_gather(d: Dims, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_out, v_out, ws, stream=None):
+    """Reads the cache back: k_out, v_out (bf16 [B][n][H_kv][D]) = the values
+    at positions pos [B][n] (any order; rows at -1 are left as they are)."""
+    dev = torch.cuda.current_device()
+    if pos.dim() != 2:
+        raise ValueError("pos must be [B][n]")
+    n = pos.shape[1]
+    _want_on(dev, pos, "pos", (d.batch, n), torch.int32)
+    shape = (d.batch, n, d.n_kv_heads, d.head_dim)
+    _want_on(dev, k_out, "k_out", shape, torch.bfloat16)
+    _want_on(dev, v_out, "v_out", shape, torch.bfloat16)
+    kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
+    w, nb = _ws_on(dev, ws)
+    _check(lib.qsa_kv_gather(d, n, kc, vc, ksc, vsc, pt, pos.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), w, nb,
+                             _stream(stream)), "qsa_kv_gather")
+
+
+def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, ws, lse=None,
+               window: int = 0, stream=None):
+    """Dense attention of the newest tokens over the paged cache: query j of
+    request r attends to positions 0 .. q_pos[r][j] (the last ``window`` of
+    them if window > 0); rows at -1 give zeros. lse (fp32 [B][n_q][H_q], may
+    be None) receives the log of each row's softmax sum."""
+    dev = torch.cuda.current_device()
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be 0 or a number of positions below 2^31")
+    shape = (d.batch, d.n_q, d.n_q_heads, d.head_dim)
+    _want_on(dev, q, "q", shape, torch.bfloat16)
+    _want_on(dev, out, "out", shape, torch.bfloat16)
+    kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
+    _want_on(dev, q_pos, "q_pos", shape[:2], torch.int32)
+    lp = None
+    if lse is not None:
+        _want_on(dev, lse, "lse", shape[:3], torch.float32)
+        lp = lse.data_ptr()
+    w, nb = _ws_on(dev, ws)
+    _check(lib.qsa_paged_attn(d, window, q.data_ptr(), kc, vc, ksc, vsc, pt, q_pos.data_ptr(), out.data_ptr(), lp,
+                              w, nb, _stream(stream)), "qsa_paged_attn")
 
 
 def check_errors(ws: torch.Tensor, stream=None) -> Tuple[int, Tuple[int, int, int, int]]:

@@ -22,6 +22,9 @@
  * (attention without a caller workspace), and qsa_resolve /
  * qsa_sparse_attn_rows (qsa_sparse_attn's two launches, separately).
  *
+ * qsa_kv.h declares the operators round the paged cache: rotary positions,
+ * writing and reading the cache, and dense attention over it.
+ *
  * Readings where the pages are silent:
  *   - full blocks of a query at position p: b < (p + 1) / 4; the unfilled
  *     block holds positions 4 * ((p + 1) / 4) .. p, (p + 1) % 4 of them;
@@ -350,8 +353,9 @@ qsa_status qsa_draft_attn(const qsa_dims* dims, const void* q, const void* k_cac
  * Returns QSA_OK if no device-side error was recorded since the last check,
  * else QSA_ERR_BAD_INDEX (or QSA_ERR_TIMEOUT). `info` (may be NULL) receives
  * 4 int32: error kind (1 query position, 2 page id, 3 selected position,
- * 4 draft query not after its reused selection, 5 a bounded wait inside the
- * chunked-scoring kernel gave up), request, query, offending value. */
+ * 4 draft query not after its reused selection, 5 a bounded wait inside a
+ * kernel gave up, 6 new tokens of a request that are not consecutive, see
+ * qsa_kv.h), request, query, offending value. */
 qsa_status qsa_check_errors(void* ws, void* stream, int32_t* info);
 
 #ifdef __cplusplus

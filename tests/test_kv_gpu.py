@@ -1,0 +1,725 @@
+"""The operators round the paged cache on the GPU against 64-bit references.
+
+Tolerances. BF16 values are off by at most 2^-8 of themselves (half a step),
+E4M3 codes by 2^-4 of themselves, or 2^-10 below the normal range. Rotation: a
+pair's products and sincospi carry FP32 errors of a few 2^-24 of |x_a| + |x_b|;
+2^-20 of it is allowed. Attention: see _attn_tol.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _kv_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qsa():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    from block_sparse_attention_qsa_gb300 import qsa as q
+
+    return q
+
+
+def _ok(qsa, ws):
+    st, info = qsa.check_errors(ws)
+    assert st == qsa.OK, info
+
+
+def _normal(shape, seed):
+    return torch.randn(shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").to(torch.bfloat16)
+
+
+def _i32(a):
+    return torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()
+
+
+def _dims(qsa, B, max_pages, num_pages, kv="bf16", n_q=1, hq=16, hk=2, D=128, ps=64, **kw):
+    return qsa.make_dims(B, n_q, max(1, max_pages * ps // 4), max_pages, num_pages, 1, kv, ps, hq, hk, D, **kw)
+
+
+# --------------------------------------------------------------------------
+# rotary positions
+# --------------------------------------------------------------------------
+SCALINGS = [dict(), dict(base=1e6, scaling="linear", factor=8.0), dict(scaling="ntk", factor=4.0),
+            dict(scaling="yarn", factor=16.0, orig_len=4096.0)]
+
+
+def _check_rotation(got, x, pos, w, amp, layout, inverse=False):
+    x64 = R.f64(x)
+    ref = R.rotate(x64, pos, w, amp, layout, inverse)
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * amp * R.pair_size(x64, w, layout)
+    err = np.abs(R.f64(got) - ref)
+    assert np.all(err <= tol), (err - tol).max()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(64, 64), (128, 128), (256, 256), (128, 32), (128, 2), (256, 66), (64, 10), (128, 72)])
+@pytest.mark.parametrize("kw", SCALINGS, ids=lambda k: k.get("scaling", "none"))
+def test_rope(qsa, layout, D, rot, kw):
+    if rot == 2 and kw.get("scaling") == "ntk":
+        pytest.skip("no NTK base for one pair")
+    B, n, H = 2, 7, 3
+    x = _normal((B, n, H, D), rot + D)
+    pos = np.array([[0, 1, 2, 63, 4095, 131071, 1048575], [5, -1, 2 ** 31 - 1, 1000003, -1, 77, 12]])
+    rope = qsa.make_rope(rot, layout=layout, **kw)
+    w, amp = R.frequencies(rot, **kw)
+    for inverse in (False, True):
+        y = torch.full_like(x, 7.0)
+        qsa.rope(rope, x, _i32(pos), y, inverse=inverse)
+        live = pos >= 0
+        xs, ys = x.cpu()[torch.from_numpy(live)], y.cpu()[torch.from_numpy(live)]
+        _check_rotation(ys, xs, pos[live], w, amp, layout, inverse)
+        assert torch.all(y.cpu()[torch.from_numpy(~live)] == 7.0)  # no token: left as it was
+        # from component rot on: the same bits
+        assert torch.equal(ys[..., rot:], xs[..., rot:])
+    z = x.clone()
+    qsa.rope(rope, z, _i32(pos), z, inverse=True)  # in place
+    assert torch.equal(z[torch.from_numpy(live).cuda()], y[torch.from_numpy(live).cuda()])
+
+
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 700])
+@pytest.mark.parametrize("H", [1, 16, 65])
+def test_rope_sizes(qsa, n, H):
+    x = _normal((3, n, H, 128), n + H)
+    pos = np.arange(3)[:, None] * 1000 + np.arange(n)
+    rope = qsa.make_rope(64)
+    y = torch.empty_like(x)
+    qsa.rope(rope, x, _i32(pos), y)
+    w, amp = R.frequencies(64)
+    _check_rotation(y, x, pos, w, amp, "half")
+
+
+def test_rope_strides(qsa):
+    # heads of a packed projection, tokens and heads in another order, an odd
+    # row start, a broadcast batch: all the same values as contiguous copies
+    B, n, H, D = 2, 5, 4, 64
+    pos = _i32(np.arange(B * n).reshape(B, n) * 37)
+    rope = qsa.make_rope(64)
+    views = {
+        "packed": _normal((B, n, H + 3, D), 1)[:, :, 2:2 + H],
+        "heads first": _normal((B, H, n, D), 2).transpose(1, 2),
+        "tokens first": _normal((n, B, H, D), 3).transpose(0, 1),
+        "odd start": _normal((B, n, H, D + 1), 4)[..., 1:],
+        "broadcast": _normal((1, n, H, D), 5).expand(B, n, H, D),
+        "one head for all": _normal((B, n, 1, D), 6).expand(B, n, H, D),
+    }
+    for name, x in views.items():
+        want, got = torch.empty((B, n, H, D), dtype=torch.bfloat16, device="cuda"), None
+        qsa.rope(rope, x.contiguous(), pos, want)
+        got = torch.empty_like(want)
+        qsa.rope(rope, x, pos, got)
+        assert torch.equal(want, got), name
+        buf = torch.full((B, n, H + 1, D + 1), 3.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[:, :, 1:, :D]
+        qsa.rope(rope, x, pos, out)
+        assert torch.equal(want, out), name
+        assert torch.all(buf[:, :, 0] == 3.0) and torch.all(buf[..., D] == 3.0), name
+    packed = views["packed"]
+    want = torch.empty((B, n, H, D), dtype=torch.bfloat16, device="cuda")
+    qsa.rope(rope, packed.contiguous(), pos, want)
+    qsa.rope(rope, packed, pos, packed)
+    assert torch.equal(want, packed)
+
+
+def test_rope_gradient(qsa):
+    # inverse is the gradient: the transpose of the forward matrix (formula),
+    # and <dy, rope(x + h e) - rope(x - h e)> / 2h (differences)
+    B, n, H, D, rot = 1, 3, 2, 64, 32
+    kw = dict(scaling="yarn", factor=16.0, orig_len=64.0)
+    rope = qsa.make_rope(rot, layout="interleaved", **kw)
+    w, amp = R.frequencies(rot, **kw)
+    pos = np.array([[3, 500, 100000]])
+    x, dy = _normal((B, n, H, D), 11), _normal((B, n, H, D), 12)
+    dx = torch.empty_like(dy)
+    qsa.rope(rope, dy, _i32(pos), dx, inverse=True)
+    _check_rotation(dx, dy, pos, w, amp, "interleaved", inverse=True)
+    x64, dy64, dx64 = R.f64(x), R.f64(dy), R.f64(dx)
+    # the forward map is linear, so a step of 1 has no truncation error
+    for at in [(0, 0, 0, 0), (0, 1, 1, 7), (0, 2, 0, 30), (0, 2, 1, 31), (0, 1, 0, 40)]:
+        e = np.zeros_like(x64)
+        e[at] = 1.0
+        diff = (R.rotate(x64 + e, pos, w, amp, "interleaved") - R.rotate(x64 - e, pos, w, amp, "interleaved")) / 2
+        want = float((dy64 * diff).sum())
+        assert abs(dx64[at] - want) <= 2.0 ** -8 * abs(want) + 2.0 ** -20 * 4
+
+
+# --------------------------------------------------------------------------
+# cache write
+# --------------------------------------------------------------------------
+def _positions(starts, lengths, n):
+    pos = np.full((len(starts), n), -1, dtype=np.int32)
+    for r, (s, m) in enumerate(zip(starts, lengths)):
+        pos[r, :m] = np.arange(s, s + m)
+    return pos
+
+
+APPENDS = [
+    # starts, lengths, n, hq, hk, D, page_size
+    ([0], [1], 1, 16, 2, 128, 64),
+    ([62, 0, 127], [4, 0, 3], 4, 16, 2, 128, 64),
+    ([5, 1000], [33, 17], 33, 3, 1, 64, 16),
+    ([250, 3], [9, 9], 9, 4, 4, 256, 256),
+    ([1], [701], 701, 8, 8, 128, 32),
+    ([7, 7, 7, 7, 7], [2, 1, 2, 0, 2], 2, 64, 1, 128, 128),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"n{c[2]}-{c[3]}/{c[4]}-d{c[5]}-p{c[6]}")
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("rot,layout", [(0, "half"), (1, "half"), (1, "interleaved"), (6, "half"), (6, "interleaved")])
+@pytest.mark.parametrize("packed", [False, True])
+def test_append(qsa, case, kv, rot, layout, packed):
+    starts, lengths, n, hq, hk, D, ps = case
+    rot = {0: 0, 1: D}.get(rot, rot)  # none, all of the head, three pairs
+    B = len(starts)
+    pos = _positions(starts, lengths, n)
+    table, num_pages = R.page_table([s + m for s, m in zip(starts, lengths)], ps, 3)
+    kc, vc, ks, vs = R.make_cache(num_pages, hk, ps, D, kv, 21)
+    before = [f.clone() for f in (kc, vc)]
+    qkv = _normal((B, n, hq + 2 * hk, D), 22)
+    qkv[0, 0, hq, 0] = 1e4  # past the largest code: clamped
+    q, k, v = (qkv[:, :, :hq], qkv[:, :, hq:hq + hk], qkv[:, :, hq + hk:])
+    if not packed:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    d = _dims(qsa, B, table.shape[1], num_pages, kv, hq=hq, hk=hk, D=D, ps=ps)
+    ws = qsa.make_kv_workspace(d)
+    rope = qsa.make_rope(rot, layout=layout) if rot else None
+    q_out = torch.full((B, n, hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    extra = dict(rope=rope, q=q, q_out=q_out) if rope else {}
+    qsa.kv_append(d, k, v, kc, vc, ks, vs, table.cuda(), _i32(pos), ws, **extra)
+    _ok(qsa, ws)
+    w, amp = R.frequencies(rot) if rot else (np.zeros(0), 1.0)
+    live = torch.from_numpy(pos >= 0)
+    if rope:
+        _check_rotation(q_out.cpu()[live], q.cpu()[live], pos[pos >= 0], w, amp, layout)
+        assert torch.all(q_out.cpu()[~live] == 7.0)
+    table = table.numpy()
+    sk, sv = R.f64(ks)[:, None], R.f64(vs)[:, None]
+    touched = np.zeros((num_pages, ps), dtype=bool)
+    got = [R.f64(kc), R.f64(vc)]
+    for r in range(B):
+        p = pos[r, :lengths[r]]
+        page, slot = table[r, p // ps], p % ps
+        touched[page, slot] = True
+        k64, v64 = R.f64(k[r, :lengths[r]]), R.f64(v[r, :lengths[r]])
+        rk = R.rotate(k64, p, w, amp, layout)
+        slack = 2.0 ** -20 * R.pair_size(k64, w, layout)
+        gk, gv = got[0][page, :, slot], got[1][page, :, slot]
+        if kv == "bf16":
+            assert np.all(np.abs(gk - rk) <= 2.0 ** -8 * np.abs(rk) + slack)
+            assert np.array_equal(gv, v64)
+        else:
+            z = np.clip(rk / sk, -448, 448)
+            # half a step of the code, and FP32's division on top (2^-24, far inside the slack)
+            assert np.all(np.abs(gk - z) <= 2.0 ** -4 * np.abs(z) + 2.0 ** -10 + slack / sk + 2.0 ** -22 * np.abs(z))
+            want = (v[r, :lengths[r]].float() / vs.view(1, -1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+            assert np.array_equal(gv, want.float().cpu().numpy().astype(np.float64))
+    for c, b in zip((kc, vc), before):  # every other slot as it was
+        other = torch.from_numpy(~touched).cuda()
+        assert torch.equal(c.transpose(1, 2)[other], b.transpose(1, 2)[other])
+
+
+def test_append_special_values(qsa):
+    # E4M3: NaN stays NaN, infinities and large values clamp, ties go to even,
+    # the range below the normals; BF16: every bit pattern is kept
+    d = _dims(qsa, 1, 1, 1, "fp8", hq=1, hk=1, D=64)
+    ws = qsa.make_kv_workspace(d)
+    vals = [math.nan, math.inf, -math.inf, 448.0, 464.0, 465.0, 1e30, -1e30, 0.0, -0.0, 2.0 ** -9, 2.0 ** -10,
+            3 * 2.0 ** -10, 2.0 ** -11, 17.0, 18.0, 19.0, 25.0, 27.0, -17.0, 1.0625, 1.1875, 2.0 ** -6, 2.0 ** -7]
+    x = torch.zeros(1, 1, 1, 64)
+    x[0, 0, 0, :len(vals)] = torch.tensor(vals)
+    x = x.to(torch.bfloat16).cuda()
+    kc, vc = (torch.full((1, 1, 64, 64), 0x33, dtype=torch.uint8, device="cuda") for _ in range(2))
+    one = torch.ones(1, device="cuda")
+    qsa.kv_append(d, x, x, kc, vc, one, one, _i32([[0]]), _i32([[9]]), ws)
+    _ok(qsa, ws)
+    f = x.float().cpu().view(-1)
+    want = torch.where(f.isnan(), f, f.clamp(-448, 448)).to(torch.float8_e4m3fn).float()
+    for c in (kc, vc):
+        got = c.cpu().view(torch.float8_e4m3fn)[0, 0, 9].float()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(), want.nan_to_num())
+        assert torch.equal(torch.signbit(got[~got.isnan()]), torch.signbit(want[~want.isnan()]))
+        rest = torch.ones(64, dtype=torch.bool)
+        rest[9] = False
+        assert torch.all(c.cpu()[0, 0, rest] == 0x33)
+    bits = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int16).view(1, 512, 2, 64).view(torch.bfloat16).cuda()
+    d = _dims(qsa, 1, 8, 8, "bf16", hq=2, hk=2, D=64)
+    kc, vc = (torch.zeros((8, 2, 64, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = qsa.make_kv_workspace(d)
+    pos = _i32(np.arange(512)[None])
+    qsa.kv_append(d, bits, bits, kc, vc, None, None, _i32([np.arange(8)]), pos, ws)
+    ko, vo = torch.empty_like(bits), torch.empty_like(bits)
+    qsa.kv_gather(d, kc, vc, None, None, _i32([np.arange(8)]), pos, ko, vo, ws)
+    _ok(qsa, ws)
+    nan = bits.isnan()
+    for o in (ko, vo):
+        assert torch.equal(o.view(torch.int16)[~nan], bits.view(torch.int16)[~nan]) and torch.all(o[nan].isnan())
+
+
+def test_append_reports_and_skips(qsa):
+    ps, B, n = 16, 4, 3
+    table = np.array([[0, 1], [2, 3], [4, 99], [6, 7]], dtype=np.int32)
+    kc, vc, ks, vs = R.make_cache(8, 2, ps, 64, "bf16", 5)
+    x = _normal((B, n, 4, 64), 6)
+    d = _dims(qsa, B, 2, 8, "bf16", hq=2, hk=2, D=64, ps=ps)
+    ws = qsa.make_kv_workspace(d)
+    rope = qsa.make_rope(64)
+    cases = [
+        # positions, (kind, request, token, value) of one of the faults (None: not the only one), skipped
+        # (request, token)s; K and V only for kind 2
+        ([[0, 1, 2], [4, 6, 5], [0, 1, 2], [0, 1, 2]], (6, 1, None, None), [(1, 1), (1, 2)]),
+        ([[30, 31, 32], [4, 5, 6], [0, 1, 2], [0, 1, 2]], (1, 0, 2, 32), [(0, 2)]),
+        ([[0, 1, -2], [4, 5, 6], [0, 1, 2], [0, 1, 2]], (1, 0, 2, -2), [(0, 2)]),
+        ([[0, 1, 2], [4, 5, 6], [15, 16, 17], [0, 1, 2]], (2, 2, None, 99), [(2, 1), (2, 2)]),
+        ([[0, 1, 2], [-1, 5, 6], [0, -1, 2], [0, 1, 2]], (6, 1, None, None), [(1, 0), (1, 1), (1, 2), (2, 1)]),
+    ]
+    for pos, want, skipped in cases:
+        kc.fill_(9.0), vc.fill_(9.0)
+        q_out = torch.full((B, n, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        qsa.kv_append(d, x[:, :, :2], x[:, :, 2:], kc, vc, None, None, _i32(table), _i32(pos), ws, rope=rope,
+                      q=x[:, :, :2], q_out=q_out)
+        st, info = qsa.check_errors(ws)
+        assert st == qsa.ERR_BAD_INDEX
+        assert all(b is None or a == b for a, b in zip(info, want)), (info, want)
+        written = np.zeros((8, ps), dtype=bool)
+        for r in range(B):
+            for j in range(n):
+                if (r, j) not in skipped:
+                    written[table[r, pos[r][j] // ps], pos[r][j] % ps] = True
+                assert torch.all(q_out[r, j] == 7.0).item() == ((r, j) in skipped and want[0] != 2)
+        w = torch.from_numpy(written).cuda()
+        for c in (kc, vc):
+            assert torch.all(c.transpose(1, 2)[~w] == 9.0)
+            assert not torch.any(torch.all(c.transpose(1, 2)[w] == 9.0, -1))
+        assert qsa.check_errors(ws)[0] == qsa.OK
+
+
+# --------------------------------------------------------------------------
+# reading back
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,n,hk,D,ps", [(1, 1, 2, 128, 64), (3, 45, 2, 128, 64), (2, 300, 1, 64, 16), (2, 33, 8, 256, 256)])
+def test_gather(qsa, kv, B, n, hk, D, ps):
+    tokens = [n + 17 * r for r in range(B)]
+    table, num_pages = R.page_table(tokens, ps, 4)
+    kc, vc, ks, vs = R.make_cache(num_pages, hk, ps, D, kv, 31)
+    rng = np.random.RandomState(8)
+    pos = np.stack([rng.randint(0, t, n) for t in tokens])  # any order, some twice
+    if n > 4:
+        pos[0, 3] = pos[-1, n - 1] = -1
+    d = _dims(qsa, B, table.shape[1], num_pages, kv, hq=hk, hk=hk, D=D, ps=ps)
+    ws = qsa.make_kv_workspace(d)
+    ko, vo = (torch.full((B, n, hk, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qsa.kv_gather(d, kc, vc, ks, vs, table.cuda(), _i32(pos), ko, vo, ws)
+    _ok(qsa, ws)
+    for c, s, o in ((kc, ks, ko), (vc, vs, vo)):
+        val = c.cpu() if kv == "bf16" else c.cpu().view(torch.float8_e4m3fn).float() * s.cpu().view(1, -1, 1, 1)
+        for r in range(B):
+            p = pos[r]
+            want = val[table.numpy()[r, p // ps].astype(np.int64), :, p % ps].to(torch.bfloat16)
+            want[torch.from_numpy(p < 0)] = 7.0
+            assert torch.equal(o[r].cpu(), want)
+
+
+def test_gather_reports_and_skips(qsa):
+    kc, vc, ks, vs = R.make_cache(3, 2, 16, 64, "fp8", 5)
+    d = _dims(qsa, 2, 2, 3, "fp8", hq=2, hk=2, D=64, ps=16)
+    ws = qsa.make_kv_workspace(d)
+    table = _i32([[0, 1], [2, -1]])
+    for pos, want, bad in (([[0, 32], [1, 2]], (1, 0, 1, 32), (0, 1)), ([[0, 1], [16, 2]], (2, 1, 0, -1), (1, 0)),
+                           ([[0, -5], [1, 2]], (1, 0, 1, -5), (0, 1))):
+        ko, vo = (torch.full((2, 2, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        qsa.kv_gather(d, kc, vc, ks, vs, table, _i32(pos), ko, vo, ws)
+        assert qsa.check_errors(ws) == (qsa.ERR_BAD_INDEX, want)
+        for o in (ko, vo):
+            for r in range(2):
+                for j in range(2):
+                    assert torch.all(o[r, j] == 7.0).item() == ((r, j) == bad)
+
+
+# --------------------------------------------------------------------------
+# dense attention
+# --------------------------------------------------------------------------
+def _attn_tol(ref, mag, lse, qk, D, kv):
+    """Output: half a BF16 step of the result; every weight is off by its own
+    rounding (2^-8 of it in BF16, 2^-11 in FP16), by the score's error as an
+    exponent, and by the exponential and the sums (2^-18 covers a few thousand
+    FP32 steps taken in trees); the score's error is that of an FP32 sum of D
+    products, at most 2^-23 of the sum of their magnitudes for each of about
+    D / 8 + 8 partial sums. lse: the score's error and a few FP32 steps."""
+    eps_s = (D / 8 + 8) * 2.0 ** -23 * qk
+    w = (2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -18
+    fin = np.where(np.isfinite(lse), np.abs(lse), 0.0)
+    return 2.0 ** -8 * np.abs(ref) + (w + 2 * eps_s)[..., None] * mag, eps_s + 2.0 ** -18 * (1 + fin)
+
+
+def _attn_case(qsa, ctx, n_q, hq, hk, D, ps, kv, window=0, q_pos=None, seed=41, mutate=None, sm_scale=0.0,
+               stream=None, max_pages=None):
+    """Runs paged_attn on requests of ctx tokens (their n_q newest are the
+    queries) and compares every row with the reference; returns the state."""
+    B = len(ctx)
+    table, num_pages = R.page_table([max(c, 1) for c in ctx], ps, seed)
+    if max_pages:
+        table = torch.nn.functional.pad(table, (0, max_pages - table.shape[1]), value=-7)
+    kc, vc, ks, vs = R.make_cache(num_pages, hk, ps, D, kv, seed + 1)
+    q = _normal((B, n_q, hq, D), seed + 2)
+    if q_pos is None:
+        q_pos = [[max(-1, c - n_q + j) for j in range(n_q)] for c in ctx]
+    if mutate:
+        mutate(kc, vc, q, table)
+    d = _dims(qsa, B, table.shape[1], num_pages, kv, n_q, hq, hk, D, ps, sm_scale=sm_scale)
+    ws = qsa.make_kv_workspace(d)
+    out = torch.full((B, n_q, hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, n_q, hq), 7.0, device="cuda")
+    args = (d, q, kc, vc, ks, vs, table.cuda(), _i32(q_pos), out, ws)
+    qsa.paged_attn(*args, lse=lse, window=window)
+    _ok(qsa, ws)
+    _compare_attn(args, lse, window)
+    return args, lse
+
+
+def _compare_attn(args, lse, window=0, bad_pages=None):
+    d, q, kc, vc, ks, vs, table, q_pos, out, _ = args
+    kv = "bf16" if kc.dtype == torch.bfloat16 else "fp8"
+    sc = [R.f64(s)[None, :, None] if kv == "fp8" else 1.0 for s in (ks, vs)]
+    caches = [R.f64(kc), R.f64(vc)]
+    table, q_pos, q64 = table.cpu().numpy(), q_pos.cpu().numpy(), R.f64(q)
+    got, got_lse = R.f64(out), R.f64(lse)
+    scale = d.sm_scale if d.sm_scale > 0 else 1.0 / math.sqrt(d.head_dim)
+    for r in range(d.batch):
+        top = int(q_pos[r].max()) + 1
+        k, v = (R.rows(c, table[r], top) * s for c, s in zip(caches, sc)) if top > 0 else (None, None)
+        for j in range(d.n_q):
+            p = int(q_pos[r, j])
+            lo = max(0, p - window + 1) if window else 0
+            if p < 0:
+                assert np.all(got[r, j] == 0) and np.all(got_lse[r, j] == -np.inf), (r, j)
+                continue
+            ref, rl, mag, qk = R.attention(q64[r, j], k, v, scale, lo, p + 1)
+            tol, tol_l = _attn_tol(ref, mag, rl, qk, d.head_dim, kv)
+            err, err_l = np.abs(got[r, j] - ref), np.abs(got_lse[r, j] - rl)
+            assert np.all(err <= tol), (r, j, err.max(), (err - tol).max())
+            assert np.all(err_l <= tol_l), (r, j, err_l.max())
+
+
+HEADS = [(16, 2, 128), (8, 1, 64), (4, 4, 256), (12, 4, 64), (7, 1, 128), (32, 2, 128), (24, 1, 256), (40, 1, 64)]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hk,D", HEADS)
+@pytest.mark.parametrize("n_q", [1, 4])
+def test_attn_heads(qsa, kv, hq, hk, D, n_q):
+    _attn_case(qsa, [333, 70, 1500], n_q, hq, hk, D, 64, kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("ps", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("window", [0, 1, 50])
+def test_attn_lengths(qsa, kv, ps, window):
+    # one position, sizes round every tile and page border, empty requests
+    ctx = [1, 2, 3, 15, 16, 17, 31, 33, 63, 64, 65, 66, 127, 128, 129, 191, 193, 255, 256, 257, 0, 700]
+    _attn_case(qsa, ctx, 3, 8, 2, 128, ps, kv, window=window)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,ctx,window,n_q", [(1, 20011, 0, 4), (1, 9000, 4097, 1), (5, 6007, 0, 2), (40, 900, 0, 1)])
+def test_attn_long_and_wide(qsa, kv, B, ctx, window, n_q):
+    _attn_case(qsa, [ctx - 131 * r % 500 for r in range(B)], n_q, 16, 2, 128, 64, kv, window=window)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_positions_of_any_order(qsa, kv):
+    # queries far apart, the same position twice, padding rows between, a page
+    # table wider than the requests with ids in it that nothing may read
+    pos = [[5, 900, -1, 0], [-1, -1, -1, -1], [1000, 10, 1000, 500]]
+    for window in (0, 300):
+        _attn_case(qsa, [901, 64, 1001], 4, 16, 2, 128, 32, kv, window=window, q_pos=pos, max_pages=200)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("sm_scale", [1e-3, 3.0])
+def test_attn_scale(qsa, kv, sm_scale):
+    _attn_case(qsa, [500, 130], 2, 16, 2, 128, 64, kv, sm_scale=sm_scale)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("factor", [1e5, 1e-6])
+def test_attn_query_magnitudes(qsa, kv, factor):
+    # queries outside FP16's range keep their BF16 values with either cache
+    def scale_q(kc, vc, q, table):
+        q.mul_(factor)
+
+    _attn_case(qsa, [300, 90], 4, 16, 2, 128, 64, kv, mutate=scale_q, sm_scale=0.05 / factor)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_what_is_masked_never_arrives(qsa, kv, bad, D):
+    # everything that a query does not see is NaN or infinite: slots behind the
+    # last position, positions before the window, the spare page; and position
+    # p_j + 1 .. p_3 for the earlier queries of a verify step
+    if kv == "fp8" and not math.isnan(bad):
+        pytest.skip("E4M3 has no infinities")
+    ctx, n_q, window, ps = [77, 130, 66], 4, 40, 16
+    code = torch.tensor(bad).to(torch.bfloat16) if kv == "bf16" else 0x7F
+    keep = {}
+
+    def poison(kc, vc, q, table):
+        seen = torch.zeros(kc.shape[0], ps, dtype=torch.bool)
+        for r, c in enumerate(ctx):
+            lo = max(0, c - n_q - window + 1)
+            p = np.arange(lo, c)
+            seen[torch.from_numpy(table.numpy()[r, p // ps].astype(np.int64)), torch.from_numpy(p % ps)] = True
+        for c in (kc, vc):
+            c.transpose(1, 2)[~seen.cuda()] = code
+        keep["cache"] = (kc, vc)
+
+    args, lse = _attn_case(qsa, ctx, n_q, 16, 2, D, ps, kv, window=window, mutate=poison)
+    # now the newest token and the oldest of the window: rows that see neither keep their bits
+    clean, clean_lse = args[8].clone(), lse.clone()
+    table = args[6].cpu().numpy()
+    for r, c in enumerate(ctx):
+        for p in (c - 1, c - n_q - window + 1):
+            if p >= 0:
+                for x in keep["cache"]:
+                    x[int(table[r, p // ps]), :, p % ps] = code
+    qsa.paged_attn(*args, lse=lse, window=window)
+    _ok(qsa, args[9])
+    out, lse = args[8].float(), lse
+    for r, c in enumerate(ctx):
+        for j in (1, 2):
+            if c - n_q - window + 1 >= 0 or j == 1 or True:
+                assert torch.isfinite(out[r, j]).all() and torch.isfinite(lse[r, j]).all(), (r, j)
+                err = (out[r, j] - clean[r, j].float()).abs().max().item()
+                assert err <= 2.0 ** -7 * clean[r, j].float().abs().max().item(), (r, j, err)
+                assert (lse[r, j] - clean_lse[r, j]).abs().max().item() <= 2.0 ** -16 * 10
+        assert torch.isnan(out[r, 3]).all()  # it sees the newest token (0 * inf and inf - inf are NaN)
+
+
+def test_attn_infinite_values_arrive(qsa):
+    # an infinite V that a row does see gives the infinity that arithmetic gives
+    def plant(kc, vc, q, table):
+        vc[int(table[0, 1]), 0, 3, 5] = math.inf
+
+    B, hq = 1, 8
+    table, num_pages = R.page_table([200], 64, 1)
+    kc, vc, ks, vs = R.make_cache(num_pages, 1, 64, 128, "bf16", 2)
+    q = _normal((1, 4, hq, 128), 3)
+    plant(kc, vc, q, table)
+    d = _dims(qsa, B, table.shape[1], num_pages, "bf16", 4, hq, 1)
+    ws = qsa.make_kv_workspace(d)
+    out = torch.empty_like(q)
+    # query 0 and 1 do not see position 67, 2 and 3 do
+    qsa.paged_attn(d, q, kc, vc, None, None, table.cuda(), _i32([[66, 60, 67, 199]]), out, ws)
+    _ok(qsa, ws)
+    assert torch.isfinite(out[0, :2]).all()
+    assert torch.all(out[0, 2:, :, 5] == math.inf)
+    rest = torch.ones(128, dtype=torch.bool)
+    rest[5] = False
+    assert torch.isfinite(out[0, 2:, :, rest]).all()
+
+
+def test_attn_reports_and_skips(qsa):
+    ps, hk, D = 16, 2, 128
+    table, num_pages = R.page_table([100, 100], ps, 9)
+    kc, vc, ks, vs = R.make_cache(num_pages, hk, ps, D, "bf16", 10)
+    q = _normal((2, 2, 16, D), 11)
+    d = _dims(qsa, 2, table.shape[1], num_pages, "bf16", 2, 16, hk, D, ps)
+    ws = qsa.make_kv_workspace(d)
+    out, lse = torch.empty_like(q), torch.empty((2, 2, 16), device="cuda")
+    cap = table.shape[1] * ps
+    for p, in ((cap,), (-2,)):
+        qsa.paged_attn(d, q, kc, vc, ks, vs, table.cuda(), _i32([[98, 99], [p, 50]]), out, ws, lse=lse)
+        assert qsa.check_errors(ws) == (qsa.ERR_BAD_INDEX, (1, 1, 0, p))
+        good = torch.tensor([[98, 99], [-1, 50]])
+        _compare_attn((d, q, kc, vc, ks, vs, table.cuda(), good, out, ws), lse)
+    for bad in (num_pages, -1, 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[1, 2] = bad
+        qsa.paged_attn(d, q, kc, vc, ks, vs, t.cuda(), _i32([[98, 99], [98, 99]]), out, ws, lse=lse)
+        st, info = qsa.check_errors(ws)
+        assert st == qsa.ERR_BAD_INDEX and info[0] == 2 and info[1] == 1 and info[3] == bad
+        # the same as a cache where those 16 positions weigh nothing
+        keep = np.r_[0:32, 48:100]
+        k, v = (R.rows(R.f64(c), table.numpy()[1], 100)[keep] for c in (kc, vc))
+        for j in range(2):
+            n = len(keep) - 1 + j
+            ref, rl, mag, qk = R.attention(R.f64(q[1, j]), k, v, 1 / math.sqrt(D), 0, n)
+            tol, tol_l = _attn_tol(ref, mag, rl, qk, D, "bf16")
+            assert np.all(np.abs(R.f64(out[1, j]) - ref) <= tol)
+            assert np.all(np.abs(R.f64(lse[1, j]) - rl) <= tol_l)
+    # a request whose pages are all bad has nothing to attend to
+    t = table.clone()
+    t[1] = -1
+    qsa.paged_attn(d, q, kc, vc, ks, vs, t.cuda(), _i32([[98, 99], [98, 99]]), out, ws, lse=lse)
+    assert qsa.check_errors(ws)[0] == qsa.ERR_BAD_INDEX
+    assert torch.all(out[1] == 0) and torch.all(lse[1] == -math.inf)
+
+
+def test_attn_closed_forms(qsa):
+    # one position: its V row bit for bit; keys of zero: the mean of V
+    D = 128
+    table, num_pages = R.page_table([1, 700], 64, 12)
+    kc, vc, ks, vs = R.make_cache(num_pages, 2, 64, D, "bf16", 13)
+    kc.zero_()
+    q = _normal((2, 1, 16, D), 14)
+    d = _dims(qsa, 2, table.shape[1], num_pages)
+    ws = qsa.make_kv_workspace(d)
+    out, lse = torch.empty_like(q), torch.empty((2, 1, 16), device="cuda")
+    qsa.paged_attn(d, q, kc, vc, ks, vs, table.cuda(), _i32([[0], [699]]), out, ws, lse=lse)
+    _ok(qsa, ws)
+    row = vc[int(table[0, 0]), :, 0]
+    assert torch.equal(out[0, 0], row.repeat_interleave(8, 0)) and torch.all(lse[0] == 0)
+    mean = R.rows(R.f64(vc), table.numpy()[1], 700).mean(0).repeat(8, 0)
+    assert np.all(np.abs(R.f64(out[1, 0]) - mean) <= 2.0 ** -8 * np.abs(mean) + 2.0 ** -17)
+    assert (lse[1] - math.log(700)).abs().max().item() <= 2.0 ** -20 * 8
+
+
+def test_attn_without_lse_and_repeated(qsa):
+    # the same bits on every call, with and without lse, whatever ws held before
+    args, lse = _attn_case(qsa, [3000, 41, 1, 777], 4, 16, 2, 128, 64, "fp8")
+    first, first_lse = args[8].clone(), lse.clone()
+    for k in range(4):
+        args[8].fill_(3.0)
+        lse.fill_(3.0)
+        if k:
+            args[9][256:].random_(0, 256)
+        qsa.paged_attn(*args, lse=lse if k % 2 else None)
+        assert torch.equal(args[8], first)
+        assert not k % 2 or torch.equal(lse, first_lse)
+    _ok(qsa, args[9])
+
+
+# --------------------------------------------------------------------------
+# streams, graphs, far offsets, and the operators together
+# --------------------------------------------------------------------------
+def test_other_stream_and_graph(qsa):
+    # a step (append, attention) on a side stream, captured and replayed with
+    # new inputs in the same buffers, against direct calls
+    B, n_q, ps = 3, 4, 64
+    ctx = [500, 64, 1301]
+    table, num_pages = R.page_table(ctx, ps, 51)
+    d = _dims(qsa, B, table.shape[1], num_pages, "fp8", n_q)
+    kc, vc, ks, vs = R.make_cache(num_pages, 2, ps, 128, "fp8", 52)
+    pt, pos = table.cuda(), _i32([[c - n_q + j for j in range(n_q)] for c in ctx])
+    rope = qsa.make_rope(128)
+    qkv = _normal((B, n_q, 20, 128), 53)
+    ws = qsa.make_kv_workspace(d)
+    q_rot, out = (torch.empty((B, n_q, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step(stream=None):
+        qsa.kv_append(d, qkv[:, :, 16:18], qkv[:, :, 18:], kc, vc, ks, vs, pt, pos, ws, rope=rope, q=qkv[:, :, :16],
+                      q_out=q_rot, stream=stream)
+        qsa.paged_attn(d, q_rot, kc, vc, ks, vs, pt, pos, out, ws, stream=stream)
+
+    side = torch.cuda.Stream()
+    inputs = [qkv.clone(), _normal(qkv.shape, 54), _normal(qkv.shape, 55)]
+    want = []
+    for x in inputs:
+        qkv.copy_(x)
+        step()
+        want.append((out.clone(), q_rot.clone(), kc.clone(), vc.clone()))
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for x, ref in zip(inputs, want):
+        qkv.copy_(x)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((out, q_rot, kc, vc), ref):
+            assert torch.equal(a, b)
+        out.zero_()
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            step()
+        step(stream=side)  # named, from another current stream
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref[0])
+    _ok(qsa, ws)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_offsets_past_32_bits(qsa, kv):
+    # a cache of more than 2^31 elements (2^32 bytes), used at its far end
+    ps, hk, D = 64, 2, 128
+    num_pages = (1 << 31) // (ps * hk * D) + 40
+    dt = torch.bfloat16 if kv == "bf16" else torch.uint8
+    kc, vc = (torch.empty((num_pages, hk, ps, D), dtype=dt, device="cuda") for _ in range(2))
+    kc[-40:], vc[-40:], ks, vs = R.make_cache(40, hk, ps, D, kv, 61)
+    table = torch.arange(num_pages - 10, num_pages, dtype=torch.int32).flip(0).view(1, -1)
+    d = _dims(qsa, 1, 10, num_pages, kv, 4)
+    ws = qsa.make_kv_workspace(d)
+    k, v, q = _normal((1, 4, hk, D), 62), _normal((1, 4, hk, D), 63), _normal((1, 4, 16, D), 64)
+    pos = _i32([[600, 601, 602, 603]])
+    qsa.kv_append(d, k, v, kc, vc, ks, vs, table.cuda(), pos, ws)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    qsa.kv_gather(d, kc, vc, ks, vs, table.cuda(), pos, ko, vo, ws)
+    out, lse = torch.empty_like(q), torch.empty((1, 4, 16), device="cuda")
+    qsa.paged_attn(d, q, kc, vc, ks, vs, table.cuda(), pos, out, ws, lse=lse)
+    _ok(qsa, ws)
+    if kv == "bf16":
+        assert torch.equal(ko, k) and torch.equal(vo, v)
+    small = (d, q, kc[-40:], vc[-40:], ks, vs, table.cuda() - (num_pages - 40), pos, out, ws)
+    _compare_attn(small, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_request_from_prefill_to_decode(qsa, kv):
+    # prefill (append a chunk, compress its keys), a sparse verify step and a
+    # dense one over the same pages: while every block fits the selection, the
+    # sparse step is dense attention. One workspace serves both headers.
+    ps, n_ctx, n_q = 64, 1500, 4
+    total = n_ctx + n_q
+    table, num_pages = R.page_table([total], ps, 71)
+    pt = table.cuda()
+    d = qsa.make_dims(1, n_q, total // 4, table.shape[1], num_pages, 1, kv)
+    kc, vc, ks, vs = R.make_cache(num_pages, 2, ps, 128, kv, 72)
+    kc.zero_(), vc.zero_()
+    n = max(qsa.workspace_size(d), qsa.kv_workspace_size(d))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    rope = qsa.make_rope(128)
+    x = _normal((1, total, 2 * 2 + 16, 128), 73)
+    idx = _normal((1, total, 1, 128), 74)
+    q_rot = torch.empty((1, total, 16, 128), dtype=torch.bfloat16, device="cuda")
+    pos = _i32(np.arange(total)[None])
+    for lo, hi in ((0, 1000), (1000, n_ctx), (n_ctx, total)):  # two prefill chunks and the verify step's tokens
+        s = slice(lo, hi)
+        qsa.kv_append(d, x[:, s, 16:18], x[:, s, 18:], kc, vc, ks, vs, pt, pos[:, s].contiguous(), ws, rope=rope,
+                      q=x[:, s, :16], q_out=q_rot[:, s])
+    idx_keys = torch.zeros((1, 4 * d.max_blocks, 1, 128), dtype=torch.bfloat16, device="cuda")
+    qsa.rope(rope, idx[:, :4 * d.max_blocks], pos[:, :4 * d.max_blocks].contiguous(), idx_keys)
+    q_pos = pos[:, n_ctx:].contiguous()
+    kcomp = torch.zeros((1, d.max_blocks, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q, q_idx = q_rot[:, n_ctx:].contiguous(), idx[:, n_ctx:].contiguous()
+    sparse, dense = torch.empty_like(q), torch.empty_like(q)
+    lse = torch.empty((1, n_q, 16), device="cuda")
+    qsa.compress_keys(d, idx_keys, q_pos, kcomp, ws)
+    for _ in range(2):
+        qsa.decode(d, q_idx, kcomp, q, kc, vc, ks, vs, pt, q_pos, sparse, ws)
+        qsa.paged_attn(d, q, kc, vc, ks, vs, pt, q_pos, dense, ws, lse=lse)
+        _ok(qsa, ws)
+        _compare_attn((d, q, kc, vc, ks, vs, pt, q_pos, dense, ws), lse)
+        _compare_attn((d, q, kc, vc, ks, vs, pt, q_pos, sparse, ws), lse)
+    # what was written reads back
+    ko, vo = (torch.empty((1, total, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qsa.kv_gather(d, kc, vc, ks, vs, pt, pos, ko, vo, ws)
+    _ok(qsa, ws)
+    if kv == "bf16":
+        assert torch.equal(vo, x[:, :, 18:])
+        want = torch.empty_like(ko)
+        qsa.rope(rope, x[:, :, 16:18], pos, want)
+        assert torch.equal(ko, want)
+    else:
+        v = x[:, :, 18:].float()
+        assert torch.all((vo.float() - v).abs() <= 2.0 ** -4 * v.abs() + 2.0 ** -10 * vs.max() + 2.0 ** -8 * v.abs())
