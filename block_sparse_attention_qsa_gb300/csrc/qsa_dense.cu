@@ -3,9 +3,51 @@
 //   o = sum_t softmax_t(c q . k_t) v_t   over  max(0, p - window + 1) <= t <= p,
 //   lse = ln sum_t exp(c q . k_t)
 //
-// One warp takes one (query, head) row and one of `splits` equal parts of its
-// positions, with a running maximum and sum (exp2 domain, FP32); a second
-// kernel joins the parts of a row in order.
+// One pass over K and V with the running maximum and sum of a softmax (FP32,
+// exp2 domain). All n_q x group query rows that share a KV head are worked on
+// together, so K and V are read once: 4 D flops a row and position against
+// 4 D (BF16) or 2 D (E4M3) bytes, which is far below the card's ratio for up
+// to 32 rows. HBM is the bound, and the design follows from it:
+//
+//  * Split. A unit is one (request, KV head, block of rows); the units' tiles
+//    of 64 positions form one stream that is cut into equal contiguous shares,
+//    one per persistent CTA, so no SM waits for a long request. The lengths
+//    are on the device, so every CTA works the stream out from q_pos itself
+//    (one block scan). A unit that ends up in several CTAs leaves (max, sum,
+//    acc) pieces in the workspace, which a second kernel, chained with
+//    programmatic dependent launch, joins in order (no atomics: the same bits
+//    on every call).
+//  * Feeding. One warp looks the pages up (32 boxes ahead) and issues the TMA
+//    copies of whole tiles, swizzled, into a ring of as many stages as shared
+//    memory holds (about 160 KB in flight on every SM, several times what
+//    HBM's latency needs), across unit borders.
+//  * Eight warps compute: 16 positions of a tile each (four slices, two tiles
+//    at a time; with more rows than two MMA tiles hold, the two groups of four
+//    warps take half of the rows each instead), S = Q K^T and O += P V with
+//    mma.sync m16n8k16. These contractions have 8 to 64 rows and are a few
+//    per cent of the tensor pipe; tcgen05's 128-row tiles would be mostly
+//    padding and need P back through tensor memory. Each warp has its own
+//    running maximum, so warps meet only at the end of a unit.
+//  * E4M3 codes are widened to FP16 in registers (exact). K: a 32-bit word of
+//    an ldmatrix row holds 4 consecutive codes of a position, taken as
+//    components 2c, 2c+1, 2c+8, 2c+9 of the MMA's k dimension, an order that Q
+//    is stored in too. V: a transposed ldmatrix word holds two adjacent
+//    components of two positions; one byte permute sorts them by component.
+//    The BF16 query is scaled per row by a power of two into FP16's range
+//    (exact) and the factor goes into the row's softmax scale.
+//  * P is rounded to BF16 (FP16 for an E4M3 cache) as the MMA's operand: an
+//    error of 2^-9 a weight, random in sign, below the output's own rounding.
+//    The sum keeps the unrounded weights.
+//
+// What is masked never arrives: scores of masked positions are replaced, not
+// added to; V of positions that no row of the unit sees is zeroed in
+// registers; and where a tile holds a position that only some rows see and
+// its V is not finite (0 x NaN would reach the other rows), that tile's PV is
+// done row by row on the FP32 pipe.
+//
+// Every wait is bounded by a clock limit (kind 5, see the abort flag).
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "qsa_kv_internal.cuh"
@@ -16,150 +58,983 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr unsigned kFull = 0xffffffffu;
+
+constexpr int kTile = 64;          // positions of a tile
+constexpr int kSlice = 16;         // positions of a warp step
+constexpr int kComputeWarps = 8;
+constexpr int kWarps = kComputeWarps + 4;  // and the copy warp's warpgroup, whose other warps leave at once
+constexpr int kThreads = 32 * kWarps;
+// The compute warps' accumulators want more registers than 384 threads can be
+// launched with (168): the copy warpgroup hands most of its own over.
+// 232 x 256 + 40 x 128 = 168 x 384.
+constexpr int kComputeRegs = 216, kCopyRegs = 72;
+static_assert(kComputeRegs * 32 * kComputeWarps + kCopyRegs * 128 <= 168 * kThreads, "register split");
+constexpr int kMaxSmem = 232448;   // 227 KB a CTA
+constexpr int kStaticSmem = 512;   // barriers and the like
+constexpr int kMinTiles = 2;       // tiles a CTA takes at least (see Split)
+constexpr long long kWaitCycles = 1LL << 31;  // about one second
+
+template <int D_, bool FP8_, int MT_, int RG_>
+struct Cfg {
+  static constexpr int D = D_, MT = MT_, RG = RG_;
+  static constexpr bool FP8 = FP8_;
+  static constexpr int kGroupRows = 16 * MT;         // rows of a warp
+  static constexpr int kRows = kGroupRows * RG;      // rows of a unit
+  static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a TMA box's row
+  static constexpr int kLines = kRowBytes / kLine;
+  static constexpr int kHalf = kTile * kRowBytes;    // K (or V) of a tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kQPitch = D * 2 + 16;         // bytes, conflict-free for ldmatrix
+  static constexpr int kQBytes = kRows * kQPitch;
+  // slab of the units' joint: 16 columns of every warp's accumulators (BF16
+  // rows padded against bank conflicts of the 8-byte stores)
+  static constexpr int kSlabPitch = FP8 ? 16 : 20;
+  static constexpr int kSlabBytes = kComputeWarps * kGroupRows * kSlabPitch * 4;
+  static constexpr int kFixed = kQBytes + kSlabBytes + 2 * kComputeWarps * kGroupRows * 4 + kRows * 4 + 1024;
+  static constexpr int kFit = (kMaxSmem - kStaticSmem - kFixed) / kStage;
+  // With every other tile for a group of warps (RG 1) the number of stages is
+  // even: a stage then always belongs to the same group, which so meets every
+  // phase of its barrier (a parity says nothing about a phase two ahead).
+  static constexpr int kStages = kFit >= 12 ? 12 : RG == 1 ? kFit & ~1 : kFit;
+  static constexpr int kSmem = kStages * kStage + kFixed;
+  static constexpr int kPieceFloats = kRows * (D + 2);  // m, l, acc of a piece
+  static constexpr bool kQInRegs = D * MT <= 128;
+  static_assert(kStages >= 2 && kSlabBytes >= kComputeWarps * kGroupRows * kSlice * 4, "shared memory");
+};
 
 struct DenseArgs {
   const __nv_bfloat16* q;
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
   const float* k_scale;
   const float* v_scale;
   const int32_t* page_table;
   const int32_t* q_pos;
   __nv_bfloat16* out;
   float* lse;
-  float* parts;  // [row][splits][2 + D]: maximum, sum, accumulator
+  long long* total;     // tiles of the stream
+  long long* unit_at;   // first tile of a split unit, -1: the unit is whole
+  float* parts;         // [grid][2][kPieceFloats]
   int32_t* err;
-  int rows, splits, n_q, n_q_heads, n_kv_heads, page_size, max_pages, num_pages, window;
+  int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
+  int page_size, max_pages, num_pages, window, grid;
   float sm_scale;
 };
 
-template <int E>
-__device__ __forceinline__ void load_vals(const uint8_t* cache, long long at, bool fp8, float (&f)[E]) {
-  if (fp8) {
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = h2_to_f2(e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(cache + at + e)));
-      f[e] = v.x;
-      f[e + 1] = v.y;
-    }
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void compute_sync() {  // the compute warps only
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(cache + 2 * (at + e));
-      f[e] = bf_lo(w);
-      f[e + 1] = bf_hi(w);
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+// 2^x on the special-function unit (relative error about 2^-22, 2^-inf = 0)
+__device__ __forceinline__ float exp2_sfu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf(lo, hi);
+  }
+}
+// the four E4M3 codes of a word as two FP16 pairs (exact)
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ float pow2(int s) { return __uint_as_float((uint32_t)(127 + s) << 23); }
+
+// address of 16-byte chunk `chunk` of row `row` (0..63) of a staged K or V
+// tile, as the TMA swizzle lays it out
+template <class C>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int chunk) {
+  if constexpr (C::kLine == 128)
+    return base + (uint32_t)((chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+  else
+    return base + (uint32_t)(row * 64 + (((chunk & 3) ^ ((row >> 1) & 3)) << 4));
+}
+
+// ---------------------------------------------------------------------------
+// the stream of tiles
+// ---------------------------------------------------------------------------
+// Positions lo .. hi - 1 that any query of request r sees (hi = 0: none).
+struct Range {
+  int lo, hi;
+  __device__ __forceinline__ int t0() const { return lo / kTile; }
+  __device__ __forceinline__ int tiles() const { return hi > 0 ? (hi - 1) / kTile + 1 - lo / kTile : 0; }
+};
+__device__ __forceinline__ int capacity(const DenseArgs& a) { return a.max_pages * a.page_size; }
+__device__ __forceinline__ bool valid_pos(const DenseArgs& a, int p) { return p >= 0 && p < capacity(a); }
+__device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
+  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+__device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
+  Range g{0x7fffffff, 0};
+  for (int j = 0; j < a.n_q; ++j) {
+    const int p = a.q_pos[(size_t)r * a.n_q + j];
+    if (!valid_pos(a, p)) continue;
+    g.lo = min(g.lo, low_of(a, p));
+    g.hi = max(g.hi, p + 1);
+  }
+  return g.hi > 0 ? g : Range{0, 0};
+}
+// CTAs that share a stream of `total` tiles, the first tile of CTA c's share,
+// and the CTA that has tile w
+__device__ __forceinline__ int ctas_of(const DenseArgs& a, long long total) {
+  return (int)min((long long)a.grid, (total + kMinTiles - 1) / kMinTiles);
+}
+__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return c * total / ctas; }
+__device__ __forceinline__ int cta_of_tile(long long total, int ctas, long long w) {
+  return (int)(((w + 1) * ctas - 1) / total);
+}
+
+// A place in the stream: unit x = 0 .. n_kv_heads * row_blocks - 1 of request
+// r, tile t of its `tiles`.
+struct Place {
+  int r, x, t, tiles;
+  Range g;
+  __device__ __forceinline__ void next_unit(const DenseArgs& a) {
+    t = 0;
+    if (++x < a.n_kv_heads * a.row_blocks) return;
+    x = 0;
+    do {
+      if (++r >= a.batch) return;
+      g = range_of(a, r);
+      tiles = g.tiles();
+    } while (tiles == 0);
+  }
+};
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ CUtensorMap tm_k,
+                                                            const __grid_constant__ CUtensorMap tm_v,
+                                                            const DenseArgs a) {
+  constexpr int D = C::D, MT = C::MT, RG = C::RG;
+  constexpr bool FP8 = C::FP8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem;
+  uint8_t* s_q = ring + C::kStages * C::kStage;
+  float* slab = reinterpret_cast<float*>(s_q + C::kQBytes);
+  float* s_m = slab + C::kSlabBytes / 4;                      // [warp][group row]
+  float* s_l = s_m + kComputeWarps * C::kGroupRows;
+  float* s_qs = s_l + kComputeWarps * C::kGroupRows;          // [row] softmax scale (exp2 domain)
+  __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages];
+  __shared__ uint32_t s_bad[C::kStages];  // bit s: slice s of the staged tile has no page
+  __shared__ long long s_scan[kWarps];
+  __shared__ long long s_first;
+  __shared__ int s_first_r;
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int units = a.n_kv_heads * a.row_blocks;  // of a request
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), RG == 1 ? 4 : 8);
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();     // positions, queries and the cache may come from the kernel before
+  pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
+
+  // every thread sums the tiles of a contiguous run of requests
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles();
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_scan[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine;
+  for (int w = 0; w < warp; ++w) before += s_scan[w];
+  long long total = 0;
+  for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+  total *= units;
+  const int ctas = ctas_of(a, total);
+  if (blockIdx.x == 0 && tid == 0) *a.total = total;
+  if (blockIdx.x == 0) {  // positions that are none are reported once
+    for (int r = r0; r < r1; ++r)
+      for (int j = 0; j < a.n_q; ++j) {
+        const int p = a.q_pos[(size_t)r * a.n_q + j];
+        if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
+      }
+  }
+  if ((int)blockIdx.x >= ctas) return;
+  const long long w0 = share_begin(total, ctas, blockIdx.x), w1 = share_begin(total, ctas, blockIdx.x + 1);
+  // the request that holds tile w0
+  if (before * units <= w0 && w0 < (before + mine) * units) {
+    long long at = before;
+    for (int r = r0; r < r1; ++r) {
+      const int t = range_of(a, r).tiles();
+      if (w0 < (at + t) * units) {
+        s_first_r = r;
+        s_first = at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  Place at;
+  at.r = s_first_r;
+  at.g = range_of(a, at.r);
+  at.tiles = at.g.tiles();
+  {
+    const long long off = w0 - s_first * units;
+    at.x = (int)(off / at.tiles);
+    at.t = (int)(off - (long long)at.x * at.tiles);
+  }
+
+  // bounded wait; once one role has given up, every other does at once
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return true;
+    const long long start = clock64();
+    while (!mbar_try_wait(b, parity)) {
+      if (s_abort) return false;
+      if (clock64() - start > kWaitCycles) {
+        s_abort = 1;
+        record_error(a.err, kErrTimeout, 0, 0, warp);
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp >= kComputeWarps) {
+    // ---- the copy warp ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    if (warp > kComputeWarps) return;
+    const int box = min(kTile, a.page_size);  // positions of a box
+    const int boxes = kTile / box;            // boxes of a tile, each in one page
+    const int ops = boxes * C::kLines * 2;    // TMA copies of a tile
+    int stage = 0;
+    uint32_t phase = 0;
+    long long w = w0;
+    bool ok = true;
+    while (w < w1 && ok) {
+      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+      const int g = at.x / a.row_blocks;
+      // page of box i of the segment's tiles, for 32 boxes at a time (one a
+      // lane), the next 32 on their way; -1: no position of it is seen
+      const int first_box = (at.g.t0() + at.t) * boxes, n_boxes = n * boxes;
+      auto page_of = [&](int i) {
+        const long long p = (long long)(first_box + i) * box;
+        if (i >= n_boxes || p >= at.g.hi || p + box <= at.g.lo) return -1;
+        const int page = a.page_table[(size_t)at.r * a.max_pages + (int)(p / a.page_size)];
+        if ((unsigned)page < (unsigned)a.num_pages) return page;
+        record_error(a.err, kErrPage, at.r, 0, page);
+        return -1;
+      };
+      int cur = page_of(lane), nxt = page_of(32 + lane);
+      for (int k = 0; k < n && ok; ++k) {
+        const int b0 = k * boxes;
+        if (b0 > 0 && (b0 & 31) == 0) {
+          cur = nxt;
+          nxt = page_of(b0 + 32 + lane);
+        }
+        // this lane's box within the tile, and its page
+        const int my_box = lane % boxes;
+        const int page = __shfl_sync(kFull, cur, (b0 & 31) + my_box);
+        const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
+        ok = wait(&empty_bar[stage], phase ^ 1u);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&full_bar[stage]);
+        if (lane == 0) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int s = 0; s < kTile / kSlice; ++s)
+            if ((bad_boxes >> (s * kSlice / box)) & 1u) bad |= 1u << s;
+          s_bad[stage] = bad;
+          mbar_expect_tx(bar, C::kStage);
+        }
+        __syncwarp();
+        const int slot = (int)(((long long)(first_box + b0 + my_box) * box) % a.page_size);
+        const uint32_t base = smem_u32(ring + stage * C::kStage);
+        for (int i = lane; i < ops; i += 32) {  // (32 is a multiple of boxes: i % boxes == my_box)
+          const int line = (i / boxes) % C::kLines, v = i / (boxes * C::kLines);
+          tma_load_4d(base + (uint32_t)(v * C::kHalf + line * (kTile * C::kLine) + my_box * box * C::kLine),
+                      v ? &tm_v : &tm_k, line * (C::kLine / (FP8 ? 1 : 2)), slot, g,
+                      page < 0 ? a.num_pages : page /* outside: zeros */, bar);
+        }
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      w += n;
+      if (w < w1) at.next_unit(a);
+    }
+    if (s_abort) {
+      // copies in flight land before the CTA leaves: the last kStages issued
+      // (bounded; a stage whose phase already completed answers at once)
+      for (int s = 0; s < C::kStages; ++s) {
+        const uint32_t par = s < stage ? phase : phase ^ 1u;
+        const long long start = clock64();
+        while (!mbar_try_wait(smem_u32(&full_bar[s]), par) && clock64() - start < kWaitCycles / 64) {
+        }
+      }
+    }
+    return;
+  }
+
+  // ---- the compute warps ----
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+  const int slice = warp & 3, grp = warp >> 2;  // grp: every other tile (RG 1) or half of the rows (RG 2)
+  const int gq = lane >> 2, c4 = lane & 3;
+  const int row_base = RG == 2 ? grp * C::kGroupRows : 0;
+  const uint32_t q_addr = smem_u32(s_q) + (uint32_t)((row_base + (lane & 15)) * C::kQPitch + (lane >> 4) * 16);
+  long long w = w0;
+  long long it = 0;  // tiles of this CTA so far
+  while (w < w1) {
+    const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+    const int g = at.x / a.row_blocks, rb = at.x - g * a.row_blocks;
+    const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);  // of this unit
+    const float vscale = FP8 ? a.v_scale[g] : 1.f;
+
+    // the unit's query rows into shared memory
+    {
+      constexpr int kLanes = D / 8;  // lanes of a row, 16 bytes each
+      const float base_scale = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
+      for (int row = tid / kLanes; row < C::kRows; row += 32 * kComputeWarps / kLanes) {
+        const int c = tid % kLanes;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          const int i = rb * C::kRows + row, j = i / a.group, h = g * a.group + (i - j * a.group);
+          v = ld16(a.q + (((size_t)at.r * a.n_q + j) * a.n_q_heads + h) * D + c * 8);
+        }
+        uint8_t* dst = s_q + row * C::kQPitch;
+        if constexpr (FP8) {
+          // magnitudes of BF16 values order like their bit patterns
+          uint32_t big = 0;
+          const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+          // 2^-sh brings the row's largest value into [2^14, 2^15)
+          const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
+          const float down = pow2(-sh);
+          uint32_t h2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h2[e] = pack2<true>(bf_lo(wd[e]) * down, bf_hi(wd[e]) * down);
+          // components 8c + 0..7 of k step c / 2: words 4x..4x+3 of K go to k
+          // slots 2x, 2x+1 and 2x+8, 2x+9
+          const int x = (c & 1) * 2;
+          uint32_t* d32 = reinterpret_cast<uint32_t*>(dst + (c >> 1) * 32);
+          d32[x] = h2[0];
+          d32[x + 4] = h2[1];
+          d32[x + 1] = h2[2];
+          d32[x + 5] = h2[3];
+          if (c == 0) s_qs[row] = base_scale * pow2(sh);
+        } else {
+          *reinterpret_cast<uint4*>(dst + c * 16) = v;
+          if (c == 0) s_qs[row] = base_scale;
+        }
+      }
+    }
+    // positions that the lane's rows see, and that all rows of the unit see
+    int lo[2 * MT], hi[2 * MT];
+#pragma unroll
+    for (int k = 0; k < 2 * MT; ++k) {
+      const int row = row_base + 8 * k + gq;
+      lo[k] = hi[k] = 0;
+      if (row < rows) {
+        const int p = a.q_pos[(size_t)at.r * a.n_q + (rb * C::kRows + row) / a.group];
+        if (valid_pos(a, p)) {
+          lo[k] = low_of(a, p);
+          hi[k] = p + 1;
+        }
+      }
+    }
+    int all_lo = 0, all_hi = 0x7fffffff;
+    {
+      const int j0 = rb * C::kRows / a.group, j1 = (rb * C::kRows + rows - 1) / a.group;
+      for (int j = j0; j <= j1; ++j) {
+        const int p = a.q_pos[(size_t)at.r * a.n_q + j];
+        all_lo = max(all_lo, valid_pos(a, p) ? low_of(a, p) : 0);
+        all_hi = min(all_hi, valid_pos(a, p) ? p + 1 : 0);
+      }
+    }
+    compute_sync();
+
+    float scale[2 * MT];
+#pragma unroll
+    for (int k = 0; k < 2 * MT; ++k) scale[k] = s_qs[row_base + 8 * k + gq];
+    uint32_t qr[C::kQInRegs ? MT * D / 16 : 1][4];
+    if constexpr (C::kQInRegs) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          ldsm4(q_addr + (uint32_t)(mt * 16 * C::kQPitch + ks * 32), qr[mt * (D / 16) + ks]);
+    }
+    float m[2 * MT], l[2 * MT], o[MT][D / 8][4];
+#pragma unroll
+    for (int k = 0; k < 2 * MT; ++k) {
+      m[k] = kNegInf;
+      l[k] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+
+    for (int k = 0; k < n; ++k, ++it) {
+      if (RG == 1 && (int)(it & 1) != grp) continue;
+      const int stage = (int)(it % C::kStages);
+      if (!wait(&full_bar[stage], (uint32_t)(it / C::kStages) & 1u)) continue;
+      const int p0 = (at.g.t0() + at.t + k) * kTile + slice * kSlice;
+      if (!((s_bad[stage] >> slice) & 1u) && p0 < at.g.hi && p0 + kSlice > at.g.lo) {
+        const uint32_t kb = smem_u32(ring + stage * C::kStage), vb = kb + C::kHalf;
+        const int r8 = lane & 7, q8 = lane >> 3;  // ldmatrix: this lane's row of matrix q8
+        // ---- S = Q K^T: 16 x MT rows, 16 positions ----
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += FP8 ? 2 : 1) {
+          uint32_t kr[4];
+          if constexpr (FP8) {
+            // matrices: positions 0-7 and 8-15 of k step ks, then of ks + 1
+            ldsm4(chunk_at<C>(kb, slice * kSlice + (q8 & 1) * 8 + r8, ks + (q8 >> 1)), kr);
+          } else {
+            // matrices: the two 8-component halves for positions 0-7, then 8-15
+            ldsm4(chunk_at<C>(kb, slice * kSlice + (q8 >> 1) * 8 + r8, 2 * ks + (q8 & 1)), kr);
+          }
+#pragma unroll
+          for (int u = 0; u < (FP8 ? 2 : 1); ++u) {
+            uint32_t b[2][2];
+            if constexpr (FP8) {
+              widen4(kr[2 * u], b[0][0], b[0][1]);
+              widen4(kr[2 * u + 1], b[1][0], b[1][1]);
+            } else {
+              b[0][0] = kr[0], b[0][1] = kr[1], b[1][0] = kr[2], b[1][1] = kr[3];
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if constexpr (C::kQInRegs) {
+                mma<FP8>(s[mt][0], qr[mt * (D / 16) + ks + u], b[0][0], b[0][1]);
+                mma<FP8>(s[mt][1], qr[mt * (D / 16) + ks + u], b[1][0], b[1][1]);
+              } else {
+                uint32_t qa[4];
+                ldsm4(q_addr + (uint32_t)(mt * 16 * C::kQPitch + (ks + u) * 32), qa);
+                mma<FP8>(s[mt][0], qa, b[0][0], b[0][1]);
+                mma<FP8>(s[mt][1], qa, b[1][0], b[1][1]);
+              }
+            }
+          }
+        }
+        // ---- softmax ----
+        // lane's values: s[mt][i][2 half + e] is row 16 mt + 8 half + gq,
+        // position p0 + 8 i + 2 c4 + e
+        const bool edge = p0 < all_lo || p0 + kSlice > all_hi;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[mt][i][e] *= scale[2 * mt + (e >> 1)];
+              if (edge) {
+                const int p = p0 + 8 * i + 2 * c4 + (e & 1), kk = 2 * mt + (e >> 1);
+                if (p < lo[kk] || p >= hi[kk]) s[mt][i][e] = kNegInf;
+              }
+            }
+        float mn[2 * MT];
+        bool grew = false;
+#pragma unroll
+        for (int kk = 0; kk < 2 * MT; ++kk) {
+          const int mt = kk >> 1, e = 2 * (kk & 1);
+          float x = fmaxf(fmaxf(s[mt][0][e], s[mt][0][e + 1]), fmaxf(s[mt][1][e], s[mt][1][e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+          mn[kk] = fmaxf(m[kk], x);
+          grew |= mn[kk] > m[kk];
+        }
+        if (__any_sync(kFull, grew)) {
+#pragma unroll
+          for (int kk = 0; kk < 2 * MT; ++kk) {
+            const float f = exp2_sfu(m[kk] - (mn[kk] == kNegInf ? 0.f : mn[kk]));
+            m[kk] = mn[kk];
+            l[kk] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[kk >> 1][i][2 * (kk & 1)] *= f;
+              o[kk >> 1][i][2 * (kk & 1) + 1] *= f;
+            }
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2 * MT; ++kk) {
+          const int mt = kk >> 1, e = 2 * (kk & 1);
+          const float mu = m[kk] == kNegInf ? 0.f : m[kk];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s[mt][i][e] = exp2_sfu(s[mt][i][e] - mu);
+            s[mt][i][e + 1] = exp2_sfu(s[mt][i][e + 1] - mu);
+            l[kk] += s[mt][i][e] + s[mt][i][e + 1];
+          }
+        }
+        // ---- O += P V ----
+        // V words: BF16: positions 2 c4, 2 c4 + 1 (+ 8) of one component;
+        // E4M3 (after the permute): those positions of two components
+        uint32_t keep[2] = {kFull, kFull};
+        bool by_row = false;
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int p = p0 + 8 * i + 2 * c4;
+            const bool ok0 = p >= at.g.lo && p < at.g.hi, ok1 = p + 1 >= at.g.lo && p + 1 < at.g.hi;
+            keep[i] = FP8 ? (ok0 ? 0x00ff00ffu : 0u) | (ok1 ? 0xff00ff00u : 0u)
+                          : (ok0 ? 0x0000ffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
+          }
+          bool odd = false;  // some V that is seen is not finite
+#pragma unroll 4
+          for (int i = 0; i < C::kRowBytes / 16; i += 2) {
+            uint32_t vr[4];
+            ldsm4t(chunk_at<C>(vb, slice * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (FP8) {
+                const uint32_t x = __byte_perm(vr[e], 0, 0x3120) & keep[e & 1] & 0x7f7f7f7fu;
+                odd |= ((x + 0x01010101u) & 0x80808080u) != 0;
+              } else {
+                const uint32_t x = vr[e] & keep[e & 1];
+                odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+          }
+          by_row = __any_sync(kFull, odd);
+        }
+        if (!by_row) {
+          uint32_t pa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            pa[mt][0] = pack2<FP8>(s[mt][0][0], s[mt][0][1]);
+            pa[mt][1] = pack2<FP8>(s[mt][0][2], s[mt][0][3]);
+            pa[mt][2] = pack2<FP8>(s[mt][1][0], s[mt][1][1]);
+            pa[mt][3] = pack2<FP8>(s[mt][1][2], s[mt][1][3]);
+          }
+#pragma unroll
+          for (int i = 0; i < C::kRowBytes / 16; i += 2) {
+            uint32_t vr[4];  // positions 0-7 and 8-15 of chunk i, then of chunk i + 1
+            ldsm4t(chunk_at<C>(vb, slice * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if constexpr (FP8) {
+                uint32_t ev[2], od[2];  // even and odd components of the chunk's 16
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t x = __byte_perm(vr[2 * u + e], 0, 0x3120);
+                  if (edge) x &= keep[e];
+                  widen4(x, ev[e], od[e]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  mma<true>(o[mt][2 * (i + u)], pa[mt], ev[0], ev[1]);
+                  mma<true>(o[mt][2 * (i + u) + 1], pa[mt], od[0], od[1]);
+                }
+              } else {
+                if (edge) {
+                  vr[2 * u] &= keep[0];
+                  vr[2 * u + 1] &= keep[1];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma<false>(o[mt][i + u], pa[mt], vr[2 * u], vr[2 * u + 1]);
+              }
+            }
+          }
+        } else {
+          float* pw = slab + warp * C::kGroupRows * kSlice;  // this warp's P, [row][position]
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                pw[(16 * mt + 8 * (e >> 1) + gq) * kSlice + 8 * i + 2 * c4 + (e & 1)] = s[mt][i][e];
+          __syncwarp();
+#pragma unroll 1
+          for (int t = 0; t < kSlice; ++t) {
+            const int p = p0 + t, row = slice * kSlice + t;
+            float pv[2 * MT];
+            bool see[2 * MT];
+#pragma unroll
+            for (int kk = 0; kk < 2 * MT; ++kk) {
+              see[kk] = p >= lo[kk] && p < hi[kk];
+              pv[kk] = pw[(8 * kk + gq) * kSlice + t];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; i += FP8 ? 2 : 1) {
+              // the lane's components of tile i (BF16: 8 i + 2 c4 + 0, 1) or
+              // of tiles i, i + 1 (E4M3: 8 i + 4 c4 + 0..3, even ones in tile i)
+              const int comp = FP8 ? 8 * i + 4 * c4 : 8 * i + 2 * c4;
+              const int byte = comp * (FP8 ? 1 : 2);
+              uint32_t word;
+              asm volatile("ld.shared.u32 %0, [%1];"
+                           : "=r"(word)
+                           : "r"(chunk_at<C>(vb, row, byte >> 4) + (uint32_t)(byte & 15)));
+              float v[4];
+              if constexpr (FP8) {
+                uint32_t x, y;
+                widen4(word, x, y);
+                const float2 f0 = h2_to_f2(x), f1 = h2_to_f2(y);
+                v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
+              } else {
+                v[0] = bf_lo(word), v[1] = bf_hi(word);
+              }
+#pragma unroll
+              for (int kk = 0; kk < 2 * MT; ++kk) {
+                if (!see[kk]) continue;
+                float(&acc)[4] = o[kk >> 1][i];
+                const int e = 2 * (kk & 1);
+                if constexpr (FP8) {
+                  float(&odd)[4] = o[kk >> 1][i + 1];
+                  acc[e] = fmaf(pv[kk], v[0], acc[e]);
+                  odd[e] = fmaf(pv[kk], v[1], odd[e]);
+                  acc[e + 1] = fmaf(pv[kk], v[2], acc[e + 1]);
+                  odd[e + 1] = fmaf(pv[kk], v[3], odd[e + 1]);
+                } else {
+                  acc[e] = fmaf(pv[kk], v[0], acc[e]);
+                  acc[e + 1] = fmaf(pv[kk], v[1], acc[e + 1]);
+                }
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
+    }
+
+    // ---- the segment's end: join the warps ----
+    const bool whole = n == at.tiles;
+    const long long unit = (long long)at.r * units + at.x;
+    if (tid == 0 && at.t == 0) a.unit_at[unit] = whole ? -1 : w;
+    // a CTA's first segment has its slot 0, a later one (its last) slot 1
+    float* piece = a.parts + ((size_t)blockIdx.x * 2 + (w == w0 ? 0 : 1)) * C::kPieceFloats;
+    const int wrow = warp * C::kGroupRows;
+#pragma unroll
+    for (int kk = 0; kk < 2 * MT; ++kk) {
+      l[kk] += __shfl_xor_sync(kFull, l[kk], 1);
+      l[kk] += __shfl_xor_sync(kFull, l[kk], 2);
+      if (c4 == 0) {
+        s_m[wrow + 8 * kk + gq] = m[kk];
+        s_l[wrow + 8 * kk + gq] = l[kk];
+      }
+    }
+    compute_sync();
+    constexpr int kJoin = RG == 1 ? 8 : 4;  // warps that hold a row
+    const int j0 = RG == 1 ? 0 : 4 * grp;
+#pragma unroll
+    for (int kk = 0; kk < 2 * MT; ++kk) {
+      float big = kNegInf;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) big = fmaxf(big, s_m[(j0 + u) * C::kGroupRows + 8 * kk + gq]);
+      const float f = exp2_sfu(m[kk] - (big == kNegInf ? 0.f : big));
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[kk >> 1][i][2 * (kk & 1)] *= f;
+        o[kk >> 1][i][2 * (kk & 1) + 1] *= f;
+      }
+    }
+    // each thread adds up column col of rows row0, row0 + 16, ..
+    const int col = tid & 15, row0 = tid >> 4;
+    constexpr int kSteps = C::kRows / 16;
+    float big_r[kSteps], sum_r[kSteps];
+#pragma unroll
+    for (int z = 0; z < kSteps; ++z) {
+      const int row = row0 + 16 * z, u0 = row / C::kGroupRows * 4, gr = row % C::kGroupRows;
+      big_r[z] = kNegInf;
+      sum_r[z] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) big_r[z] = fmaxf(big_r[z], s_m[(u0 + u) * C::kGroupRows + gr]);
+      const float mu = big_r[z] == kNegInf ? 0.f : big_r[z];
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u)
+        sum_r[z] += s_l[(u0 + u) * C::kGroupRows + gr] * exp2_sfu(s_m[(u0 + u) * C::kGroupRows + gr] - mu);
+    }
+#pragma unroll
+    for (int ch = 0; ch < D / 16; ++ch) {
+#pragma unroll
+      for (int kk = 0; kk < 2 * MT; ++kk) {
+        float* dst = slab + (wrow + 8 * kk + gq) * C::kSlabPitch;
+        const int mt = kk >> 1, e = 2 * (kk & 1);
+        if constexpr (FP8) {
+          *reinterpret_cast<float4*>(dst + 4 * c4) =
+              make_float4(o[mt][2 * ch][e], o[mt][2 * ch + 1][e], o[mt][2 * ch][e + 1], o[mt][2 * ch + 1][e + 1]);
+        } else {
+          *reinterpret_cast<float2*>(dst + 2 * c4) = make_float2(o[mt][2 * ch][e], o[mt][2 * ch][e + 1]);
+          *reinterpret_cast<float2*>(dst + 8 + 2 * c4) = make_float2(o[mt][2 * ch + 1][e], o[mt][2 * ch + 1][e + 1]);
+        }
+      }
+      compute_sync();
+#pragma unroll
+      for (int z = 0; z < kSteps; ++z) {
+        const int row = row0 + 16 * z, u0 = row / C::kGroupRows * 4, gr = row % C::kGroupRows;
+        float acc = 0.f;
+#pragma unroll
+        for (int u = 0; u < kJoin; ++u) acc += slab[((u0 + u) * C::kGroupRows + gr) * C::kSlabPitch + col];
+        if (row < rows) {
+          if (whole) {
+            const int i = rb * C::kRows + row, j = i / a.group, h = g * a.group + (i - j * a.group);
+            const size_t orow = ((size_t)at.r * a.n_q + j) * a.n_q_heads + h;
+            const float v = sum_r[z] == 0.f ? 0.f : acc / sum_r[z] * vscale;
+            a.out[orow * D + ch * 16 + col] = __float2bfloat16_rn(v);
+            if (a.lse && ch == 0 && col == 0)
+              a.lse[orow] = sum_r[z] == 0.f ? kNegInf : (big_r[z] + log2f(sum_r[z])) * kLn2;
+          } else {
+            piece[2 * C::kRows + row * D + ch * 16 + col] = acc;
+            if (ch == 0 && col == 0) {
+              piece[row] = big_r[z];
+              piece[C::kRows + row] = sum_r[z];
+            }
+          }
+        }
+      }
+      compute_sync();
+    }
+    w += n;
+    if (w < w1) at.next_unit(a);
   }
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) dense_part_kernel(const DenseArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (long long)a.rows * a.splits) return;
-  const int row = (int)(w / a.splits), split = (int)(w - (long long)row * a.splits);
-  const int rj = row / a.n_q_heads, h = row - rj * a.n_q_heads, r = rj / a.n_q;
-  const int g = h / (a.n_q_heads / a.n_kv_heads);
-  int p = a.q_pos[rj];
-  if (p < -1 || p >= a.max_pages * a.page_size) {
-    if (h == 0 && split == 0 && lane == 0) record_error(a.err, kErrQueryPos, r, rj - r * a.n_q, p);
-    p = -1;
-  }
-  const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  const long long n = p + 1 - lo;
-  const int t0 = lo + (int)(n * split / a.splits), t1 = lo + (int)(n * (split + 1) / a.splits);
-  float q[E], acc[E];
-  const __nv_bfloat16* qp = a.q + (long long)row * D + lane * E;
-  const float c = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qp[e]);
-    acc[e] = 0.f;
-  }
-  float m = kNegInf, l = 0.f;
-  for (int t = t0; t < t1; ++t) {
-    const int page = a.page_table[(long long)r * a.max_pages + t / a.page_size];
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-      if (lane == 0) record_error(a.err, kErrPage, r, rj - r * a.n_q, page);
-      continue;
-    }
-    const long long at =
-        (((long long)page * a.n_kv_heads + g) * a.page_size + t % a.page_size) * D + lane * E;
-    float k[E], v[E];
-    load_vals<E>(a.k_cache, at, FP8, k);
-    load_vals<E>(a.v_cache, at, FP8, v);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= c;
-    const float mn = fmaxf(m, s), mu = mn == kNegInf ? 0.f : mn;
-    const float f = exp2f(m - mu), x = exp2f(s - mu);
-    l = l * f + x;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + x * v[e];
-    m = mn;
-  }
-  float* part = a.parts + w * (2 + D);
-  if (lane == 0) {
-    part[0] = m;
-    part[1] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[2 + lane * E + e] = acc[e];
-}
-
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) dense_join_kernel(const DenseArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= a.rows) return;
-  const int h = row % a.n_q_heads, g = h / (a.n_q_heads / a.n_kv_heads);
-  const float* part = a.parts + (long long)row * a.splits * (2 + D);
+// Joins the pieces of split units and writes the rows of requests without
+// positions. One block of WARPS warps a row, the pieces dealt to the warps.
+template <class C, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs a) {
+  constexpr int D = C::D, E = D / 32;
+  __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int orow = blockIdx.x;
+  const int rj = orow / a.n_q_heads, h = orow - rj * a.n_q_heads, r = rj / a.n_q, j = rj - r * a.n_q;
+  const int g = h / a.group, i = j * a.group + (h - g * a.group);
+  const int rb = i / C::kRows, row = i - rb * C::kRows;
+  pdl_wait();
+  const int tiles = range_of(a, r).tiles();
   float m = kNegInf, l = 0.f, acc[E];
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, part[(long long)s * (2 + D)]);
-  const float mu = m == kNegInf ? 0.f : m;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float* ps = part + (long long)s * (2 + D);
-    const float f = exp2f(ps[0] - mu);
-    if (f == 0.f) continue;
-    l += f * ps[1];
+  if (tiles > 0) {
+    const long long u0 = a.unit_at[((long long)r * a.n_kv_heads + g) * a.row_blocks + rb];
+    if (u0 < 0) return;  // a whole unit: its CTA wrote the row
+    const long long total = *a.total;
+    const int ctas = ctas_of(a, total);
+    const int c0 = cta_of_tile(total, ctas, u0), c1 = cta_of_tile(total, ctas, u0 + tiles - 1);
+    // slot 1 of a CTA whose share began before the unit
+    const int odd = share_begin(total, ctas, c0) < u0 ? 1 : 0;
+    for (int c = c0 + warp; c <= c1; c += WARPS) {
+      const float* p = a.parts + ((size_t)c * 2 + (c == c0 ? odd : 0)) * C::kPieceFloats;
+      const float pm = p[row], pl = p[C::kRows + row];
+      float pa[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += f * ps[2 + lane * E + e];
+      for (int e = 0; e < E; ++e) pa[e] = p[2 * C::kRows + row * D + lane * E + e];
+      const float mn = fmaxf(m, pm), mu = mn == kNegInf ? 0.f : mn;
+      const float f = exp2_sfu(m - mu), x = exp2_sfu(pm - mu);
+      l = l * f + pl * x;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + pa[e] * x;
+      m = mn;
+    }
   }
-  const float scale = l > 0.f || l != l ? (FP8 ? a.v_scale[g] : 1.f) / l : 0.f;
-  __nv_bfloat16* o = a.out + (long long)row * D + lane * E;
+  if constexpr (WARPS > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] * scale);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+    float big = kNegInf;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) big = fmaxf(big, s_m[u]);
+    const float mu = big == kNegInf ? 0.f : big;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) {
+      const float f = exp2_sfu(s_m[u] - mu);
+      l += s_l[u] * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[u][lane * E + e] * f;
+    }
+    m = big;
+  }
+  const float inv = (C::FP8 ? a.v_scale[g] : 1.f) / l;
+  __nv_bfloat16* o = a.out + (size_t)orow * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(o + e) = l == 0.f ? 0u : pack_bf(acc[e] * inv, acc[e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 
-int splits_of(const qsa_dims& d, int num_sms) {
-  const long long rows = (long long)d.batch * d.n_q * d.n_q_heads;
-  return (int)std::max<long long>(1, std::min<long long>(64, 32LL * num_sms / rows));
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+// Rows of a unit: two MMA row tiles a warp (one for head dim 256, whose
+// accumulators fill the registers), and twice that when the two warp groups
+// take half of the rows each; more rows than that become several units that
+// each read K and V.
+struct Shape {
+  int mt, rg;
+  int rows() const { return 16 * mt * rg; }
+};
+Shape shape_of(const qsa_dims& d) {
+  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
+  const int mt = rows <= 16 || d.head_dim == 256 ? 1 : 2;
+  return {mt, rows > 16 * mt ? 2 : 1};
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// the cache [num_pages][n_kv_heads][page_size][head_dim] with boxes of one
+// page's (or 64) positions of one head, at most 128 bytes of a row wide
+template <class C>
+bool make_map(CUtensorMap* map, const qsa_dims& d, const void* cache) {
+  const EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  constexpr int eb = C::FP8 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.n_kv_heads,
+                              (cuuint64_t)d.num_pages};
+  const cuuint64_t row = (cuuint64_t)d.head_dim * eb;
+  const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.n_kv_heads};
+  const cuuint32_t box[4] = {(cuuint32_t)(C::kLine / eb), (cuuint32_t)std::min(kTile, d.page_size), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             C::kLine == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
+  alignas(64) CUtensorMap tk, tv;
+  if (!make_map<C>(&tk, d, k_cache) || !make_map<C>(&tv, d, v_cache)) return cudaErrorInvalidValue;
+  static DeviceSlots slots;
+  cudaError_t e = slots.raise_smem(dense_kernel<C>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
+  e = launch_k(dense_kernel<C>, dim3(a.grid), dim3(kThreads), C::kSmem, s, true, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  // many rows: their units have few pieces, one warp joins a row's; few rows:
+  // up to the grid's number of pieces each
+  const unsigned rows = (unsigned)(a.batch * a.n_q * a.n_q_heads);
+  if (rows >= 8u * a.grid) return launch_k(dense_join_kernel<C, 1>, dim3(rows), dim3(32), 0, s, true, a);
+  return launch_k(dense_join_kernel<C, 8>, dim3(rows), dim3(256), 0, s, true, a);
 }
 
 template <int D, bool FP8>
-cudaError_t launch(const DenseArgs& a, cudaStream_t s) {
-  const long long warps = (long long)a.rows * a.splits;
-  const cudaError_t e =
-      launch_k(dense_part_kernel<D, FP8>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, false, a);
-  if (e != cudaSuccess) return e;
-  return launch_k(dense_join_kernel<D, FP8>, dim3((unsigned)((a.rows + 3) / 4)), dim3(128), 0, s, false, a);
+cudaError_t launch(const Shape& sh, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v,
+                   cudaStream_t s) {
+  if constexpr (D == 256) {
+    return sh.rg == 1 ? launch<Cfg<D, FP8, 1, 1>>(d, a, k, v, s) : launch<Cfg<D, FP8, 1, 2>>(d, a, k, v, s);
+  } else {
+    if (sh.mt == 1) return launch<Cfg<D, FP8, 1, 1>>(d, a, k, v, s);
+    return sh.rg == 1 ? launch<Cfg<D, FP8, 2, 1>>(d, a, k, v, s) : launch<Cfg<D, FP8, 2, 2>>(d, a, k, v, s);
+  }
 }
 
 }  // namespace
 
 DenseWs dense_ws(const qsa_dims& d, int num_sms) {
   DenseWs w;
-  w.parts = 256 + align_up((size_t)d.batch * d.n_q * d.n_kv_heads * sizeof(int32_t), 256);
-  const size_t rows = (size_t)d.batch * d.n_q * d.n_q_heads;
-  w.total = align_up(w.parts + rows * splits_of(d, num_sms) * (2 + d.head_dim) * sizeof(float), 256);
+  const Shape sh = shape_of(d);
+  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
+  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + sh.rows() - 1) / sh.rows());
+  w.units = 256 + align_up((size_t)d.batch * d.n_q * d.n_kv_heads * sizeof(int32_t), 256);
+  w.parts = align_up(w.units + (1 + units) * sizeof(long long), 256);
+  w.total = align_up(w.parts + (size_t)num_sms * 2 * sh.rows() * (d.head_dim + 2) * sizeof(float), 256);
   return w;
 }
 
@@ -167,33 +1042,39 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
                               const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s) {
   const int sms = device_sm_count();
+  const DenseWs w = dense_ws(d, sms);
+  uint8_t* base = static_cast<uint8_t*>(ws);
   DenseArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k_cache = static_cast<const uint8_t*>(k_cache);
-  a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.page_table = page_table;
   a.q_pos = q_pos;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dense_ws(d, sms).parts);
+  a.total = reinterpret_cast<long long*>(base + w.units);
+  a.unit_at = a.total + 1;
+  a.parts = reinterpret_cast<float*>(base + w.parts);
   a.err = static_cast<int32_t*>(ws);
-  a.rows = d.batch * d.n_q * d.n_q_heads;
-  a.splits = splits_of(d, sms);
+  a.batch = d.batch;
   a.n_q = d.n_q;
   a.n_q_heads = d.n_q_heads;
   a.n_kv_heads = d.n_kv_heads;
+  a.group = d.n_q_heads / d.n_kv_heads;
   a.page_size = d.page_size;
   a.max_pages = d.max_pages;
   a.num_pages = d.num_pages;
   a.window = window;
+  a.grid = sms;
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
+  const Shape sh = shape_of(d);
   const bool fp8 = d.kv_dtype == QSA_KV_FP8_E4M3;
   switch (d.head_dim) {
-    case 64: return fp8 ? launch<64, true>(a, s) : launch<64, false>(a, s);
-    case 128: return fp8 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-    default: return fp8 ? launch<256, true>(a, s) : launch<256, false>(a, s);
+    case 64: return fp8 ? launch<64, true>(sh, d, a, k_cache, v_cache, s) : launch<64, false>(sh, d, a, k_cache, v_cache, s);
+    case 128:
+      return fp8 ? launch<128, true>(sh, d, a, k_cache, v_cache, s) : launch<128, false>(sh, d, a, k_cache, v_cache, s);
+    default:
+      return fp8 ? launch<256, true>(sh, d, a, k_cache, v_cache, s) : launch<256, false>(sh, d, a, k_cache, v_cache, s);
   }
 }
 

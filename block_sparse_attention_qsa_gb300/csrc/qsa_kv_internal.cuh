@@ -34,7 +34,7 @@ cudaError_t launch_kv_gather(const qsa_dims& d, int n_tok, const void* k_cache, 
 // Workspace of qsa_paged_attn behind the header and the ticket counters that
 // qsa.h's entry points keep there for the same dims.
 struct DenseWs {
-  size_t parts, total;
+  size_t units, parts, total;
 };
 DenseWs dense_ws(const qsa_dims& d, int num_sms);
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,

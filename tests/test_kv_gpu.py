@@ -565,6 +565,21 @@ def test_attn_reports_and_skips(qsa):
     assert torch.all(out[1] == 0) and torch.all(lse[1] == -math.inf)
 
 
+@pytest.mark.parametrize("ps", [16, 64, 256])
+def test_attn_pages_outside_the_window_are_not_looked_up(qsa, ps):
+    # pages that slid out of the window were given back, those behind the last
+    # position do not exist yet: their ids mean nothing and nothing is reported
+    ctx, window, n_q = [1000, 333], 100, 2
+
+    def free(kc, vc, q, table):
+        for r, c in enumerate(ctx):
+            lo = c - n_q - window + 1
+            table[r, :lo // ps] = -5
+            table[r, -(-c // ps):] = 1 << 30
+
+    _attn_case(qsa, ctx, n_q, 16, 2, 128, ps, "bf16", window=window, mutate=free)
+
+
 def test_attn_closed_forms(qsa):
     # one position: its V row bit for bit; keys of zero: the mean of V
     D = 128
