@@ -490,32 +490,50 @@ def make_rope(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling
     return Rope(RopeArgs(rot_dim, ROPE_LAYOUTS[layout], amp, table.data_ptr()), table)
 
 
-def _want_on(dev: int, t: torch.Tensor, name: str, shape, dtype):
-    """_want, and on the current device (whose stream and SMs the call uses)."""
-    _want(t, name, shape, dtype)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+# A decode step makes these calls once per layer, next to kernels of a few
+# microseconds, so each argument is looked at once, cheaply, and only one that
+# is not as expected goes to the function that says what is wrong with it.
+_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+
+
+def _want_on(dev: int, t: torch.Tensor, name: str, shape, dtype) -> int:
+    """The address of ``t``, a contiguous tensor of this shape and type on the
+    current device (whose stream and SMs the call uses)."""
+    if not (type(t) is _Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _want(t, name, shape, dtype)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
 def _want_strided(dev: int, t: torch.Tensor, name: str, shape):
-    """A BF16 [batch][token][head][dim] tensor on the current device whose
-    last dimension is contiguous; its strides (None: contiguous)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    """(address, strides or None: contiguous) of a BF16 [batch][token][head][dim]
+    tensor on the current device whose last dimension is contiguous."""
+    if not (type(t) is _Tensor and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
-        return None
-    st = t.stride()
-    if st[3] != 1:
+        return t.data_ptr(), None
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return Strides(st[0], st[1], st[2])
+    return t.data_ptr(), Strides(sb, st, sh)
+
+
+def _raw_stream(stream, dev: int):
+    """The cudaStream_t of ``stream``, by default the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rope_args(rope: Rope, dev: int):
@@ -535,12 +553,14 @@ def rope(rope: Rope, x, pos, y, inverse: bool = False, stream=None):
     args = _rope_args(rope, dev)
     if x.dim() != 4:
         raise ValueError("x must be [B][n][H][D]")
-    xs = _want_strided(dev, x, "x", x.shape)
-    ys = _want_strided(dev, y, "y", x.shape)
-    B, n, H, D = x.shape
-    _want_on(dev, pos, "pos", (B, n), torch.int32)
-    _check(lib.qsa_rope(args, B, n, H, D, int(inverse), x.data_ptr(), xs, pos.data_ptr(), y.data_ptr(), ys,
-                        _stream(stream)), "qsa_rope")
+    shape = x.shape
+    xp, xs = _want_strided(dev, x, "x", shape)
+    yp, ys = _want_strided(dev, y, "y", shape)
+    B, n, H, D = shape
+    pp = _want_on(dev, pos, "pos", (B, n), _I32)
+    st = lib.qsa_rope(args, B, n, H, D, 1 if inverse else 0, xp, xs, pp, yp, ys, _raw_stream(stream, dev))
+    if st:
+        _check(st, "qsa_rope")
 
 
 def kv_workspace_size(d: Dims) -> int:
@@ -562,23 +582,22 @@ def make_kv_workspace(d: Dims, device="cuda", stream=None) -> torch.Tensor:
 def _cache_ptrs(dev: int, d: Dims, k_cache, v_cache, k_scale, v_scale, page_table):
     """Checks the paged cache and returns its pointers (the scales' are null
     for a BF16 cache without them)."""
-    shape = (d.num_pages, d.n_kv_heads, d.page_size, d.head_dim)
-    dt = _kv_dtype(d)
-    _want_on(dev, k_cache, "k_cache", shape, dt)
-    _want_on(dev, v_cache, "v_cache", shape, dt)
+    hk, fp8 = d.n_kv_heads, d.kv_dtype == KV_FP8_E4M3
+    shape = (d.num_pages, hk, d.page_size, d.head_dim)
+    dt = torch.uint8 if fp8 else _BF16
+    kc = _want_on(dev, k_cache, "k_cache", shape, dt)
+    vc = _want_on(dev, v_cache, "v_cache", shape, dt)
     ks = vs = None
-    if d.kv_dtype == KV_FP8_E4M3 or k_scale is not None or v_scale is not None:
-        _want_on(dev, k_scale, "k_scale", (d.n_kv_heads,), torch.float32)
-        _want_on(dev, v_scale, "v_scale", (d.n_kv_heads,), torch.float32)
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    _want_on(dev, page_table, "page_table", (d.batch, d.max_pages), torch.int32)
-    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, page_table.data_ptr()
+    if fp8 or k_scale is not None or v_scale is not None:
+        ks = _want_on(dev, k_scale, "k_scale", (hk,), _F32)
+        vs = _want_on(dev, v_scale, "v_scale", (hk,), _F32)
+    return kc, vc, ks, vs, _want_on(dev, page_table, "page_table", (d.batch, d.max_pages), _I32)
 
 
 def _ws_on(dev: int, ws: torch.Tensor):
     if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the current device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws, rope: Optional[Rope] = None,
@@ -590,24 +609,25 @@ def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos
     dev = torch.cuda.current_device()
     if k.dim() != 4:
         raise ValueError("k must be [B][n][H_kv][D]")
-    n = k.shape[1]
-    shape = (d.batch, n, d.n_kv_heads, d.head_dim)
-    ks = _want_strided(dev, k, "k", shape)
-    vs = _want_strided(dev, v, "v", shape)
+    B, n, D = d.batch, k.shape[1], d.head_dim
+    shape = (B, n, d.n_kv_heads, D)
+    kp, ks = _want_strided(dev, k, "k", shape)
+    vp, vs = _want_strided(dev, v, "v", shape)
     args = None if rope is None else _rope_args(rope, dev)
     qs = qos = qp = qop = None
     if q is not None or q_out is not None:
         if q is None or q_out is None or rope is None:
             raise ValueError("q needs q_out and rope")
-        qshape = (d.batch, n, d.n_q_heads, d.head_dim)
-        qs = _want_strided(dev, q, "q", qshape)
-        qos = _want_strided(dev, q_out, "q_out", qshape)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
+        shape = (B, n, d.n_q_heads, D)
+        qp, qs = _want_strided(dev, q, "q", shape)
+        qop, qos = _want_strided(dev, q_out, "q_out", shape)
     kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
-    _want_on(dev, pos, "pos", (d.batch, n), torch.int32)
+    pp = _want_on(dev, pos, "pos", (B, n), _I32)
     w, nb = _ws_on(dev, ws)
-    _check(lib.qsa_kv_append(d, n, args, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qop, qos, pos.data_ptr(), pt,
-                             kc, vc, ksc, vsc, w, nb, _stream(stream)), "qsa_kv_append")
+    st = lib.qsa_kv_append(d, n, args, kp, ks, vp, vs, qp, qs, qop, qos, pp, pt, kc, vc, ksc, vsc, w, nb,
+                           _raw_stream(stream, dev))
+    if st:
+        _check(st, "qsa_kv_append")
 
 
 def kv_gather(d: Dims, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_out, v_out, ws, stream=None):
@@ -617,14 +637,15 @@ def kv_gather(d: Dims, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_ou
     if pos.dim() != 2:
         raise ValueError("pos must be [B][n]")
     n = pos.shape[1]
-    _want_on(dev, pos, "pos", (d.batch, n), torch.int32)
+    pp = _want_on(dev, pos, "pos", (d.batch, n), _I32)
     shape = (d.batch, n, d.n_kv_heads, d.head_dim)
-    _want_on(dev, k_out, "k_out", shape, torch.bfloat16)
-    _want_on(dev, v_out, "v_out", shape, torch.bfloat16)
+    ko = _want_on(dev, k_out, "k_out", shape, _BF16)
+    vo = _want_on(dev, v_out, "v_out", shape, _BF16)
     kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
     w, nb = _ws_on(dev, ws)
-    _check(lib.qsa_kv_gather(d, n, kc, vc, ksc, vsc, pt, pos.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), w, nb,
-                             _stream(stream)), "qsa_kv_gather")
+    st = lib.qsa_kv_gather(d, n, kc, vc, ksc, vsc, pt, pp, ko, vo, w, nb, _raw_stream(stream, dev))
+    if st:
+        _check(st, "qsa_kv_gather")
 
 
 def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, ws, lse=None,
@@ -636,18 +657,17 @@ def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos
     dev = torch.cuda.current_device()
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 or a number of positions below 2^31")
-    shape = (d.batch, d.n_q, d.n_q_heads, d.head_dim)
-    _want_on(dev, q, "q", shape, torch.bfloat16)
-    _want_on(dev, out, "out", shape, torch.bfloat16)
+    B, n_q, H = d.batch, d.n_q, d.n_q_heads
+    shape = (B, n_q, H, d.head_dim)
+    qp = _want_on(dev, q, "q", shape, _BF16)
+    op = _want_on(dev, out, "out", shape, _BF16)
     kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
-    _want_on(dev, q_pos, "q_pos", shape[:2], torch.int32)
-    lp = None
-    if lse is not None:
-        _want_on(dev, lse, "lse", shape[:3], torch.float32)
-        lp = lse.data_ptr()
+    pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
+    lp = None if lse is None else _want_on(dev, lse, "lse", (B, n_q, H), _F32)
     w, nb = _ws_on(dev, ws)
-    _check(lib.qsa_paged_attn(d, window, q.data_ptr(), kc, vc, ksc, vsc, pt, q_pos.data_ptr(), out.data_ptr(), lp,
-                              w, nb, _stream(stream)), "qsa_paged_attn")
+    st = lib.qsa_paged_attn(d, window, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _raw_stream(stream, dev))
+    if st:
+        _check(st, "qsa_paged_attn")
 
 
 def check_errors(ws: torch.Tensor, stream=None) -> Tuple[int, Tuple[int, int, int, int]]:
