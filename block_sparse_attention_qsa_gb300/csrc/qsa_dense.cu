@@ -60,8 +60,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
 
-constexpr int kTile = 64;          // positions of a tile
-constexpr int kSlice = 16;         // positions of a warp step
+constexpr int kSlice = 16;         // positions of an MMA
+constexpr float kSlack = 8.f;      // a row's reference may trail its maximum by a factor 2^8
 constexpr int kComputeWarps = 8;
 constexpr int kWarps = kComputeWarps + 4;  // and the copy warp's warpgroup, whose other warps leave at once
 constexpr int kThreads = 32 * kWarps;
@@ -82,6 +82,10 @@ struct Cfg {
   static constexpr int kGroupRows = 16 * MT;         // rows of a warp
   static constexpr int kRows = kGroupRows * RG;      // rows of a unit
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  // positions of a tile, four warps' steps: 16 each, or 32 where rows are
+  // short and the registers allow it
+  static constexpr int kTile = kRowBytes <= 128 && D * MT <= 128 ? 128 : 64;
+  static constexpr int NS = kTile / (4 * kSlice);
   static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a TMA box's row
   static constexpr int kLines = kRowBytes / kLine;
   static constexpr int kHalf = kTile * kRowBytes;    // K (or V) of a tile
@@ -203,12 +207,12 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 __device__ __forceinline__ float pow2(int s) { return __uint_as_float((uint32_t)(127 + s) << 23); }
 
-// address of 16-byte chunk `chunk` of row `row` (0..63) of a staged K or V
+// address of 16-byte chunk `chunk` of row `row` (a position) of a staged K or V
 // tile, as the TMA swizzle lays it out
 template <class C>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int chunk) {
   if constexpr (C::kLine == 128)
-    return base + (uint32_t)((chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    return base + (uint32_t)((chunk >> 3) * (C::kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
   else
     return base + (uint32_t)(row * 64 + (((chunk & 3) ^ ((row >> 1) & 3)) << 4));
 }
@@ -219,8 +223,7 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int chunk) 
 // Positions lo .. hi - 1 that any query of request r sees (hi = 0: none).
 struct Range {
   int lo, hi;
-  __device__ __forceinline__ int t0() const { return lo / kTile; }
-  __device__ __forceinline__ int tiles() const { return hi > 0 ? (hi - 1) / kTile + 1 - lo / kTile : 0; }
+  __device__ __forceinline__ int tiles(int tile) const { return hi > 0 ? (hi - 1) / tile + 1 - lo / tile : 0; }
 };
 __device__ __forceinline__ int capacity(const DenseArgs& a) { return a.max_pages * a.page_size; }
 __device__ __forceinline__ bool valid_pos(const DenseArgs& a, int p) { return p >= 0 && p < capacity(a); }
@@ -247,8 +250,9 @@ __device__ __forceinline__ int cta_of_tile(long long total, int ctas, long long 
   return (int)(((w + 1) * ctas - 1) / total);
 }
 
-// A place in the stream: unit x = 0 .. n_kv_heads * row_blocks - 1 of request
+// A place in the stream (of tiles of TILE positions): unit x = 0 .. n_kv_heads * row_blocks - 1 of request
 // r, tile t of its `tiles`.
+template <int TILE>
 struct Place {
   int r, x, t, tiles;
   Range g;
@@ -259,7 +263,7 @@ struct Place {
     do {
       if (++r >= a.batch) return;
       g = range_of(a, r);
-      tiles = g.tiles();
+      tiles = g.tiles(TILE);
     } while (tiles == 0);
   }
 };
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
                                                             const DenseArgs a) {
   constexpr int D = C::D, MT = C::MT, RG = C::RG;
   constexpr bool FP8 = C::FP8;
+  constexpr int kTile = C::kTile, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   const int per = (a.batch + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles();
+  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles(kTile);
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   if (before * units <= w0 && w0 < (before + mine) * units) {
     long long at = before;
     for (int r = r0; r < r1; ++r) {
-      const int t = range_of(a, r).tiles();
+      const int t = range_of(a, r).tiles(kTile);
       if (w0 < (at + t) * units) {
         s_first_r = r;
         s_first = at;
@@ -341,10 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  Place at;
+  Place<kTile> at;
   at.r = s_first_r;
   at.g = range_of(a, at.r);
-  at.tiles = at.g.tiles();
+  at.tiles = at.g.tiles(kTile);
   {
     const long long off = w0 - s_first * units;
     at.x = (int)(off / at.tiles);
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       const int g = at.x / a.row_blocks;
       // page of box i of the segment's tiles, for 32 boxes at a time (one a
       // lane), the next 32 on their way; -1: no position of it is seen
-      const int first_box = (at.g.t0() + at.t) * boxes, n_boxes = n * boxes;
+      const int first_box = (at.g.lo / kTile + at.t) * boxes, n_boxes = n * boxes;
       auto page_of = [&](int i) {
         const long long p = (long long)(first_box + i) * box;
         if (i >= n_boxes || p >= at.g.hi || p + box <= at.g.lo) return -1;
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         if (lane == 0) {
           uint32_t bad = 0;
 #pragma unroll
-          for (int s = 0; s < kTile / kSlice; ++s)
+          for (int s = 0; s < kTile / kSlice; ++s)  // a box holds whole sub-slices
             if ((bad_boxes >> (s * kSlice / box)) & 1u) bad |= 1u << s;
           s_bad[stage] = bad;
           mbar_expect_tx(bar, C::kStage);
@@ -553,88 +558,106 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       if (RG == 1 && (int)(it & 1) != grp) continue;
       const int stage = (int)(it % C::kStages);
       if (!wait(&full_bar[stage], (uint32_t)(it / C::kStages) & 1u)) continue;
-      const int p0 = (at.g.t0() + at.t + k) * kTile + slice * kSlice;
-      if (!((s_bad[stage] >> slice) & 1u) && p0 < at.g.hi && p0 + kSlice > at.g.lo) {
+      const int row0 = slice * (NS * kSlice);  // this warp's positions within the tile
+      const int p0 = (at.g.lo / kTile + at.t + k) * kTile + row0;
+      // sub-slices without a page are masked
+      const uint32_t bad = (s_bad[stage] >> (slice * NS)) & ((1u << NS) - 1u);
+      if (bad != (1u << NS) - 1u && p0 < at.g.hi && p0 + NS * kSlice > at.g.lo) {
         const uint32_t kb = smem_u32(ring + stage * C::kStage), vb = kb + C::kHalf;
         const int r8 = lane & 7, q8 = lane >> 3;  // ldmatrix: this lane's row of matrix q8
-        // ---- S = Q K^T: 16 x MT rows, 16 positions ----
-        float s[MT][2][4];
+        // ---- S = Q K^T: 16 x MT rows, 16 x NS positions ----
+        float s[NS][MT][2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[ns][mt][i][e] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks += FP8 ? 2 : 1) {
-          uint32_t kr[4];
-          if constexpr (FP8) {
-            // matrices: positions 0-7 and 8-15 of k step ks, then of ks + 1
-            ldsm4(chunk_at<C>(kb, slice * kSlice + (q8 & 1) * 8 + r8, ks + (q8 >> 1)), kr);
-          } else {
-            // matrices: the two 8-component halves for positions 0-7, then 8-15
-            ldsm4(chunk_at<C>(kb, slice * kSlice + (q8 >> 1) * 8 + r8, 2 * ks + (q8 & 1)), kr);
+          uint32_t kr[NS][4];
+#pragma unroll
+          for (int ns = 0; ns < NS; ++ns) {
+            const int row = row0 + ns * kSlice + r8;
+            if constexpr (FP8) {
+              // matrices: positions 0-7 and 8-15 of k step ks, then of ks + 1
+              ldsm4(chunk_at<C>(kb, row + (q8 & 1) * 8, ks + (q8 >> 1)), kr[ns]);
+            } else {
+              // matrices: the two 8-component halves for positions 0-7, then 8-15
+              ldsm4(chunk_at<C>(kb, row + (q8 >> 1) * 8, 2 * ks + (q8 & 1)), kr[ns]);
+            }
           }
 #pragma unroll
           for (int u = 0; u < (FP8 ? 2 : 1); ++u) {
-            uint32_t b[2][2];
-            if constexpr (FP8) {
-              widen4(kr[2 * u], b[0][0], b[0][1]);
-              widen4(kr[2 * u + 1], b[1][0], b[1][1]);
-            } else {
-              b[0][0] = kr[0], b[0][1] = kr[1], b[1][0] = kr[2], b[1][1] = kr[3];
+            uint32_t b[NS][2][2];
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns) {
+              if constexpr (FP8) {
+                widen4(kr[ns][2 * u], b[ns][0][0], b[ns][0][1]);
+                widen4(kr[ns][2 * u + 1], b[ns][1][0], b[ns][1][1]);
+              } else {
+                b[ns][0][0] = kr[ns][0], b[ns][0][1] = kr[ns][1], b[ns][1][0] = kr[ns][2], b[ns][1][1] = kr[ns][3];
+              }
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (C::kQInRegs) {
-                mma<FP8>(s[mt][0], qr[mt * (D / 16) + ks + u], b[0][0], b[0][1]);
-                mma<FP8>(s[mt][1], qr[mt * (D / 16) + ks + u], b[1][0], b[1][1]);
-              } else {
-                uint32_t qa[4];
-                ldsm4(q_addr + (uint32_t)(mt * 16 * C::kQPitch + (ks + u) * 32), qa);
-                mma<FP8>(s[mt][0], qa, b[0][0], b[0][1]);
-                mma<FP8>(s[mt][1], qa, b[1][0], b[1][1]);
+              uint32_t qa[4];
+              if constexpr (!C::kQInRegs) ldsm4(q_addr + (uint32_t)(mt * 16 * C::kQPitch + (ks + u) * 32), qa);
+              const uint32_t(&qf)[4] = C::kQInRegs ? qr[C::kQInRegs ? mt * (D / 16) + ks + u : 0] : qa;
+#pragma unroll
+              for (int ns = 0; ns < NS; ++ns) {
+                mma<FP8>(s[ns][mt][0], qf, b[ns][0][0], b[ns][0][1]);
+                mma<FP8>(s[ns][mt][1], qf, b[ns][1][0], b[ns][1][1]);
               }
             }
           }
         }
         // ---- softmax ----
-        // lane's values: s[mt][i][2 half + e] is row 16 mt + 8 half + gq,
-        // position p0 + 8 i + 2 c4 + e
-        const bool edge = p0 < all_lo || p0 + kSlice > all_hi;
+        // lane's values: s[ns][mt][i][2 half + e] is row 16 mt + 8 half + gq,
+        // position p0 + 16 ns + 8 i + 2 c4 + e
+        const bool edge = p0 < all_lo || p0 + NS * kSlice > all_hi || bad != 0;
+        bool grew = false;  // some score is more than 2^kSlack above its row's reference
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[mt][i][e] *= scale[2 * mt + (e >> 1)];
-              if (edge) {
-                const int p = p0 + 8 * i + 2 * c4 + (e & 1), kk = 2 * mt + (e >> 1);
-                if (p < lo[kk] || p >= hi[kk]) s[mt][i][e] = kNegInf;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int kk = 2 * mt + (e >> 1);
+                float& x = s[ns][mt][i][e];
+                x *= scale[kk];
+                if (edge) {
+                  const int p = p0 + kSlice * ns + 8 * i + 2 * c4 + (e & 1);
+                  if (p < lo[kk] || p >= hi[kk] || ((bad >> ns) & 1u)) x = kNegInf;
+                }
+                grew |= x > m[kk] + kSlack;
               }
-            }
-        float mn[2 * MT];
-        bool grew = false;
-#pragma unroll
-        for (int kk = 0; kk < 2 * MT; ++kk) {
-          const int mt = kk >> 1, e = 2 * (kk & 1);
-          float x = fmaxf(fmaxf(s[mt][0][e], s[mt][0][e + 1]), fmaxf(s[mt][1][e], s[mt][1][e + 1]));
-          x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
-          mn[kk] = fmaxf(m[kk], x);
-          grew |= mn[kk] > m[kk];
-        }
+        // The reference m of a row (which its weights are relative to) only
+        // has to keep the weights in range, so it moves when a score passes it
+        // by 2^8, not with every new maximum: of 16 or 32 rows one has a new
+        // maximum in most early steps, and moving costs D / 2 products a lane
+        // and row pair. (From -infinity it moves with the first position.)
         if (__any_sync(kFull, grew)) {
 #pragma unroll
           for (int kk = 0; kk < 2 * MT; ++kk) {
-            const float f = exp2_sfu(m[kk] - (mn[kk] == kNegInf ? 0.f : mn[kk]));
-            m[kk] = mn[kk];
+            const int mt = kk >> 1, e = 2 * (kk & 1);
+            float x = m[kk];
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns)
+              x = fmaxf(x, fmaxf(fmaxf(s[ns][mt][0][e], s[ns][mt][0][e + 1]), fmaxf(s[ns][mt][1][e], s[ns][mt][1][e + 1])));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+            const float f = exp2_sfu(m[kk] - (x == kNegInf ? 0.f : x));
+            m[kk] = x;
             l[kk] *= f;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-              o[kk >> 1][i][2 * (kk & 1)] *= f;
-              o[kk >> 1][i][2 * (kk & 1) + 1] *= f;
+              o[mt][i][e] *= f;
+              o[mt][i][e + 1] *= f;
             }
           }
         }
@@ -643,139 +666,153 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           const int mt = kk >> 1, e = 2 * (kk & 1);
           const float mu = m[kk] == kNegInf ? 0.f : m[kk];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            s[mt][i][e] = exp2_sfu(s[mt][i][e] - mu);
-            s[mt][i][e + 1] = exp2_sfu(s[mt][i][e + 1] - mu);
-            l[kk] += s[mt][i][e] + s[mt][i][e + 1];
-          }
+          for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s[ns][mt][i][e] = exp2_sfu(s[ns][mt][i][e] - mu);
+              s[ns][mt][i][e + 1] = exp2_sfu(s[ns][mt][i][e + 1] - mu);
+              l[kk] += s[ns][mt][i][e] + s[ns][mt][i][e + 1];
+            }
         }
         // ---- O += P V ----
         // V words: BF16: positions 2 c4, 2 c4 + 1 (+ 8) of one component;
         // E4M3 (after the permute): those positions of two components
-        uint32_t keep[2] = {kFull, kFull};
+        uint32_t keep[NS][2];
         bool by_row = false;
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int p = p0 + 8 * i + 2 * c4;
-            const bool ok0 = p >= at.g.lo && p < at.g.hi, ok1 = p + 1 >= at.g.lo && p + 1 < at.g.hi;
-            keep[i] = FP8 ? (ok0 ? 0x00ff00ffu : 0u) | (ok1 ? 0xff00ff00u : 0u)
-                          : (ok0 ? 0x0000ffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
-          }
-          bool odd = false;  // some V that is seen is not finite
-#pragma unroll 4
-          for (int i = 0; i < C::kRowBytes / 16; i += 2) {
-            uint32_t vr[4];
-            ldsm4t(chunk_at<C>(vb, slice * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
+          for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (FP8) {
-                const uint32_t x = __byte_perm(vr[e], 0, 0x3120) & keep[e & 1] & 0x7f7f7f7fu;
-                odd |= ((x + 0x01010101u) & 0x80808080u) != 0;
-              } else {
-                const uint32_t x = vr[e] & keep[e & 1];
-                odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+            for (int i = 0; i < 2; ++i) {
+              const int p = p0 + ns * kSlice + 8 * i + 2 * c4;
+              const bool ok0 = p >= at.g.lo && p < at.g.hi, ok1 = p + 1 >= at.g.lo && p + 1 < at.g.hi;
+              keep[ns][i] = FP8 ? (ok0 ? 0x00ff00ffu : 0u) | (ok1 ? 0xff00ff00u : 0u)
+                                : (ok0 ? 0x0000ffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
+            }
+          bool odd = false;  // some V that is seen is not finite
+#pragma unroll
+          for (int ns = 0; ns < NS; ++ns)
+#pragma unroll 4
+            for (int i = 0; i < C::kRowBytes / 16; i += 2) {
+              uint32_t vr[4];
+              ldsm4t(chunk_at<C>(vb, row0 + ns * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (FP8) {
+                  const uint32_t x = __byte_perm(vr[e], 0, 0x3120) & keep[ns][e & 1] & 0x7f7f7f7fu;
+                  odd |= ((x + 0x01010101u) & 0x80808080u) != 0;
+                } else {
+                  const uint32_t x = vr[e] & keep[ns][e & 1];
+                  odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+                }
               }
             }
-          }
           by_row = __any_sync(kFull, odd);
         }
         if (!by_row) {
-          uint32_t pa[MT][4];
+          uint32_t pa[NS][MT][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            pa[mt][0] = pack2<FP8>(s[mt][0][0], s[mt][0][1]);
-            pa[mt][1] = pack2<FP8>(s[mt][0][2], s[mt][0][3]);
-            pa[mt][2] = pack2<FP8>(s[mt][1][0], s[mt][1][1]);
-            pa[mt][3] = pack2<FP8>(s[mt][1][2], s[mt][1][3]);
-          }
+          for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              pa[ns][mt][0] = pack2<FP8>(s[ns][mt][0][0], s[ns][mt][0][1]);
+              pa[ns][mt][1] = pack2<FP8>(s[ns][mt][0][2], s[ns][mt][0][3]);
+              pa[ns][mt][2] = pack2<FP8>(s[ns][mt][1][0], s[ns][mt][1][1]);
+              pa[ns][mt][3] = pack2<FP8>(s[ns][mt][1][2], s[ns][mt][1][3]);
+            }
 #pragma unroll
           for (int i = 0; i < C::kRowBytes / 16; i += 2) {
-            uint32_t vr[4];  // positions 0-7 and 8-15 of chunk i, then of chunk i + 1
-            ldsm4t(chunk_at<C>(vb, slice * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if constexpr (FP8) {
-                uint32_t ev[2], od[2];  // even and odd components of the chunk's 16
+            for (int ns = 0; ns < NS; ++ns) {
+              uint32_t vr[4];  // positions 0-7 and 8-15 of chunk i, then of chunk i + 1
+              ldsm4t(chunk_at<C>(vb, row0 + ns * kSlice + (q8 & 1) * 8 + r8, i + (q8 >> 1)), vr);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  uint32_t x = __byte_perm(vr[2 * u + e], 0, 0x3120);
-                  if (edge) x &= keep[e];
-                  widen4(x, ev[e], od[e]);
+              for (int u = 0; u < 2; ++u) {
+                if constexpr (FP8) {
+                  uint32_t ev[2], od[2];  // even and odd components of the chunk's 16
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    uint32_t x = __byte_perm(vr[2 * u + e], 0, 0x3120);
+                    if (edge) x &= keep[ns][e];
+                    widen4(x, ev[e], od[e]);
+                  }
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) {
+                    mma<true>(o[mt][2 * (i + u)], pa[ns][mt], ev[0], ev[1]);
+                    mma<true>(o[mt][2 * (i + u) + 1], pa[ns][mt], od[0], od[1]);
+                  }
+                } else {
+                  if (edge) {
+                    vr[2 * u] &= keep[ns][0];
+                    vr[2 * u + 1] &= keep[ns][1];
+                  }
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) mma<false>(o[mt][i + u], pa[ns][mt], vr[2 * u], vr[2 * u + 1]);
                 }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma<true>(o[mt][2 * (i + u)], pa[mt], ev[0], ev[1]);
-                  mma<true>(o[mt][2 * (i + u) + 1], pa[mt], od[0], od[1]);
-                }
-              } else {
-                if (edge) {
-                  vr[2 * u] &= keep[0];
-                  vr[2 * u + 1] &= keep[1];
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma<false>(o[mt][i + u], pa[mt], vr[2 * u], vr[2 * u + 1]);
               }
             }
           }
         } else {
-          float* pw = slab + warp * C::kGroupRows * kSlice;  // this warp's P, [row][position]
+          float* pw = slab + warp * C::kGroupRows * kSlice;  // this warp's P of one sub-slice, [row][position]
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int ns = 0; ns < NS; ++ns) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                pw[(16 * mt + 8 * (e >> 1) + gq) * kSlice + 8 * i + 2 * c4 + (e & 1)] = s[mt][i][e];
-          __syncwarp();
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  pw[(16 * mt + 8 * (e >> 1) + gq) * kSlice + 8 * i + 2 * c4 + (e & 1)] = s[ns][mt][i][e];
+            __syncwarp();
 #pragma unroll 1
-          for (int t = 0; t < kSlice; ++t) {
-            const int p = p0 + t, row = slice * kSlice + t;
-            float pv[2 * MT];
-            bool see[2 * MT];
-#pragma unroll
-            for (int kk = 0; kk < 2 * MT; ++kk) {
-              see[kk] = p >= lo[kk] && p < hi[kk];
-              pv[kk] = pw[(8 * kk + gq) * kSlice + t];
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; i += FP8 ? 2 : 1) {
-              // the lane's components of tile i (BF16: 8 i + 2 c4 + 0, 1) or
-              // of tiles i, i + 1 (E4M3: 8 i + 4 c4 + 0..3, even ones in tile i)
-              const int comp = FP8 ? 8 * i + 4 * c4 : 8 * i + 2 * c4;
-              const int byte = comp * (FP8 ? 1 : 2);
-              uint32_t word;
-              asm volatile("ld.shared.u32 %0, [%1];"
-                           : "=r"(word)
-                           : "r"(chunk_at<C>(vb, row, byte >> 4) + (uint32_t)(byte & 15)));
-              float v[4];
-              if constexpr (FP8) {
-                uint32_t x, y;
-                widen4(word, x, y);
-                const float2 f0 = h2_to_f2(x), f1 = h2_to_f2(y);
-                v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
-              } else {
-                v[0] = bf_lo(word), v[1] = bf_hi(word);
-              }
+            for (int t = 0; t < kSlice; ++t) {
+              const int p = p0 + ns * kSlice + t, row = row0 + ns * kSlice + t;
+              float pv[2 * MT];
+              bool see[2 * MT];
 #pragma unroll
               for (int kk = 0; kk < 2 * MT; ++kk) {
-                if (!see[kk]) continue;
-                float(&acc)[4] = o[kk >> 1][i];
-                const int e = 2 * (kk & 1);
+                see[kk] = p >= lo[kk] && p < hi[kk];
+                pv[kk] = pw[(8 * kk + gq) * kSlice + t];
+              }
+#pragma unroll
+              for (int i = 0; i < D / 8; i += FP8 ? 2 : 1) {
+                // the lane's components of tile i (BF16: 8 i + 2 c4 + 0, 1) or
+                // of tiles i, i + 1 (E4M3: 8 i + 4 c4 + 0..3, even ones in tile i)
+                const int comp = FP8 ? 8 * i + 4 * c4 : 8 * i + 2 * c4;
+                const int byte = comp * (FP8 ? 1 : 2);
+                uint32_t word;
+                asm volatile("ld.shared.u32 %0, [%1];"
+                             : "=r"(word)
+                             : "r"(chunk_at<C>(vb, row, byte >> 4) + (uint32_t)(byte & 15)));
+                float v[4];
                 if constexpr (FP8) {
-                  float(&odd)[4] = o[kk >> 1][i + 1];
-                  acc[e] = fmaf(pv[kk], v[0], acc[e]);
-                  odd[e] = fmaf(pv[kk], v[1], odd[e]);
-                  acc[e + 1] = fmaf(pv[kk], v[2], acc[e + 1]);
-                  odd[e + 1] = fmaf(pv[kk], v[3], odd[e + 1]);
+                  uint32_t x, y;
+                  widen4(word, x, y);
+                  const float2 f0 = h2_to_f2(x), f1 = h2_to_f2(y);
+                  v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
                 } else {
-                  acc[e] = fmaf(pv[kk], v[0], acc[e]);
-                  acc[e + 1] = fmaf(pv[kk], v[1], acc[e + 1]);
+                  v[0] = bf_lo(word), v[1] = bf_hi(word);
+                }
+#pragma unroll
+                for (int kk = 0; kk < 2 * MT; ++kk) {
+                  if (!see[kk]) continue;
+                  float(&acc)[4] = o[kk >> 1][i];
+                  const int e = 2 * (kk & 1);
+                  if constexpr (FP8) {
+                    float(&odd)[4] = o[kk >> 1][i + 1];
+                    acc[e] = fmaf(pv[kk], v[0], acc[e]);
+                    odd[e] = fmaf(pv[kk], v[1], odd[e]);
+                    acc[e + 1] = fmaf(pv[kk], v[2], acc[e + 1]);
+                    odd[e + 1] = fmaf(pv[kk], v[3], odd[e + 1]);
+                  } else {
+                    acc[e] = fmaf(pv[kk], v[0], acc[e]);
+                    acc[e + 1] = fmaf(pv[kk], v[1], acc[e + 1]);
+                  }
                 }
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       __syncwarp();
@@ -886,7 +923,7 @@ __global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs 
   const int g = h / a.group, i = j * a.group + (h - g * a.group);
   const int rb = i / C::kRows, row = i - rb * C::kRows;
   pdl_wait();
-  const int tiles = range_of(a, r).tiles();
+  const int tiles = range_of(a, r).tiles(C::kTile);
   float m = kNegInf, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -989,7 +1026,7 @@ bool make_map(CUtensorMap* map, const qsa_dims& d, const void* cache) {
                               (cuuint64_t)d.num_pages};
   const cuuint64_t row = (cuuint64_t)d.head_dim * eb;
   const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.n_kv_heads};
-  const cuuint32_t box[4] = {(cuuint32_t)(C::kLine / eb), (cuuint32_t)std::min(kTile, d.page_size), 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)(C::kLine / eb), (cuuint32_t)std::min(C::kTile, d.page_size), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
