@@ -46,20 +46,12 @@
 // done row by row on the FP32 pipe.
 //
 // Every wait is bounded by a clock limit (kind 5, see the abort flag).
-#include <cuda.h>
-
-#include <algorithm>
-
-#include "qsa_kv_internal.cuh"
+#include "qsa_dense.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -__builtin_huge_valf();
-constexpr unsigned kFull = 0xffffffffu;
-
+constexpr int kStaticSmem = 768;   // barriers and the like
 constexpr int kSlice = 16;         // positions of an MMA
 constexpr float kSlack = 8.f;      // a row's reference may trail its maximum by a factor 2^8
 constexpr int kComputeWarps = 8;
@@ -70,11 +62,6 @@ constexpr int kThreads = 32 * kWarps;
 // 232 x 256 + 40 x 128 = 168 x 384.
 constexpr int kComputeRegs = 216, kCopyRegs = 72;
 static_assert(kComputeRegs * 32 * kComputeWarps + kCopyRegs * 128 <= 168 * kThreads, "register split");
-constexpr int kMaxSmem = 232448;   // 227 KB a CTA
-constexpr int kStaticSmem = 512;   // barriers and the like
-constexpr int kMinTiles = 2;       // tiles a CTA takes at least (see Split)
-constexpr long long kWaitCycles = 1LL << 31;  // about one second
-
 template <int D_, bool FP8_, int MT_, int RG_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_, RG = RG_;
@@ -108,53 +95,6 @@ struct Cfg {
   static_assert(kStages >= 2 && kSlabBytes >= kComputeWarps * kGroupRows * kSlice * 4, "shared memory");
 };
 
-struct DenseArgs {
-  const __nv_bfloat16* q;
-  const float* k_scale;
-  const float* v_scale;
-  const int32_t* page_table;
-  const int32_t* q_pos;
-  __nv_bfloat16* out;
-  float* lse;
-  long long* total;     // tiles of the stream
-  long long* unit_at;   // first tile of a split unit, -1: the unit is whole
-  float* parts;         // [grid][2][kPieceFloats]
-  int32_t* err;
-  int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
-  int page_size, max_pages, num_pages, window, grid;
-  float sm_scale;
-};
-
-// ---------------------------------------------------------------------------
-// instructions
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void compute_sync() {  // the compute warps only
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
 }
@@ -184,12 +124,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 }
-// 2^x on the special-function unit (relative error about 2^-22, 2^-inf = 0)
-__device__ __forceinline__ float exp2_sfu(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (F16) {
@@ -199,14 +133,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return pack_bf(lo, hi);
   }
 }
-// the four E4M3 codes of a word as two FP16 pairs (exact)
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-__device__ __forceinline__ float pow2(int s) { return __uint_as_float((uint32_t)(127 + s) << 23); }
-
 // address of 16-byte chunk `chunk` of row `row` (a position) of a staged K or V
 // tile, as the TMA swizzle lays it out
 template <class C>
@@ -216,57 +142,6 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int chunk) 
   else
     return base + (uint32_t)(row * 64 + (((chunk & 3) ^ ((row >> 1) & 3)) << 4));
 }
-
-// ---------------------------------------------------------------------------
-// the stream of tiles
-// ---------------------------------------------------------------------------
-// Positions lo .. hi - 1 that any query of request r sees (hi = 0: none).
-struct Range {
-  int lo, hi;
-  __device__ __forceinline__ int tiles(int tile) const { return hi > 0 ? (hi - 1) / tile + 1 - lo / tile : 0; }
-};
-__device__ __forceinline__ int capacity(const DenseArgs& a) { return a.max_pages * a.page_size; }
-__device__ __forceinline__ bool valid_pos(const DenseArgs& a, int p) { return p >= 0 && p < capacity(a); }
-__device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
-  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
-}
-__device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
-  Range g{0x7fffffff, 0};
-  for (int j = 0; j < a.n_q; ++j) {
-    const int p = a.q_pos[(size_t)r * a.n_q + j];
-    if (!valid_pos(a, p)) continue;
-    g.lo = min(g.lo, low_of(a, p));
-    g.hi = max(g.hi, p + 1);
-  }
-  return g.hi > 0 ? g : Range{0, 0};
-}
-// CTAs that share a stream of `total` tiles, the first tile of CTA c's share,
-// and the CTA that has tile w
-__device__ __forceinline__ int ctas_of(const DenseArgs& a, long long total) {
-  return (int)min((long long)a.grid, (total + kMinTiles - 1) / kMinTiles);
-}
-__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return c * total / ctas; }
-__device__ __forceinline__ int cta_of_tile(long long total, int ctas, long long w) {
-  return (int)(((w + 1) * ctas - 1) / total);
-}
-
-// A place in the stream (of tiles of TILE positions): unit x = 0 .. n_kv_heads * row_blocks - 1 of request
-// r, tile t of its `tiles`.
-template <int TILE>
-struct Place {
-  int r, x, t, tiles;
-  Range g;
-  __device__ __forceinline__ void next_unit(const DenseArgs& a) {
-    t = 0;
-    if (++x < a.n_kv_heads * a.row_blocks) return;
-    x = 0;
-    do {
-      if (++r >= a.batch) return;
-      g = range_of(a, r);
-      tiles = g.tiles(TILE);
-    } while (tiles == 0);
-  }
-};
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -285,9 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   float* s_qs = s_l + kComputeWarps * C::kGroupRows;          // [row] softmax scale (exp2 domain)
   __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages];
   __shared__ uint32_t s_bad[C::kStages];  // bit s: slice s of the staged tile has no page
-  __shared__ long long s_scan[kWarps];
-  __shared__ long long s_first;
-  __shared__ int s_first_r;
+  __shared__ StartSmem<kThreads> s_start;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
@@ -303,82 +176,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   pdl_wait();     // positions, queries and the cache may come from the kernel before
   pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
 
-  // every thread sums the tiles of a contiguous run of requests
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles(kTile);
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) s_scan[warp] = inc;
-  __syncthreads();
-  long long before = inc - mine;
-  for (int w = 0; w < warp; ++w) before += s_scan[w];
-  long long total = 0;
-  for (int w = 0; w < kWarps; ++w) total += s_scan[w];
-  total *= units;
-  const int ctas = ctas_of(a, total);
-  if (blockIdx.x == 0 && tid == 0) *a.total = total;
-  if (blockIdx.x == 0) {  // positions that are none are reported once
-    for (int r = r0; r < r1; ++r)
-      for (int j = 0; j < a.n_q; ++j) {
-        const int p = a.q_pos[(size_t)r * a.n_q + j];
-        if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
-      }
-  }
-  if ((int)blockIdx.x >= ctas) return;
-  const long long w0 = share_begin(total, ctas, blockIdx.x), w1 = share_begin(total, ctas, blockIdx.x + 1);
-  // the request that holds tile w0
-  if (before * units <= w0 && w0 < (before + mine) * units) {
-    long long at = before;
-    for (int r = r0; r < r1; ++r) {
-      const int t = range_of(a, r).tiles(kTile);
-      if (w0 < (at + t) * units) {
-        s_first_r = r;
-        s_first = at;
-        break;
-      }
-      at += t;
-    }
-  }
-  __syncthreads();
+  Split sp;
+  long long w0, w1;
   Place<kTile> at;
-  at.r = s_first_r;
-  at.g = range_of(a, at.r);
-  at.tiles = at.g.tiles(kTile);
-  {
-    const long long off = w0 - s_first * units;
-    at.x = (int)(off / at.tiles);
-    at.t = (int)(off - (long long)at.x * at.tiles);
-  }
-
-  // bounded wait; once one role has given up, every other does at once
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const uint32_t b = smem_u32(bar);
-    if (mbar_try_wait(b, parity)) return true;
-    const long long start = clock64();
-    while (!mbar_try_wait(b, parity)) {
-      if (s_abort) return false;
-      if (clock64() - start > kWaitCycles) {
-        s_abort = 1;
-        record_error(a.err, kErrTimeout, 0, 0, warp);
-        return false;
-      }
-    }
-    return true;
-  };
+  if (!find_start<kTile, kThreads>(a, s_start, sp, w0, w1, at)) return;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
   if (warp >= kComputeWarps) {
     // ---- the copy warp ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     if (warp > kComputeWarps) return;
-    const int box = min(kTile, a.page_size);  // positions of a box
-    const int boxes = kTile / box;            // boxes of a tile, each in one page
-    const int ops = boxes * C::kLines * 2;    // TMA copies of a tile
     int stage = 0;
     uint32_t phase = 0;
     long long w = w0;
@@ -386,46 +193,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     while (w < w1 && ok) {
       const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
       const int g = at.x / a.row_blocks;
-      // page of box i of the segment's tiles, for 32 boxes at a time (one a
-      // lane), the next 32 on their way; -1: no position of it is seen
-      const int first_box = (at.g.lo / kTile + at.t) * boxes, n_boxes = n * boxes;
-      auto page_of = [&](int i) {
-        const long long p = (long long)(first_box + i) * box;
-        if (i >= n_boxes || p >= at.g.hi || p + box <= at.g.lo) return -1;
-        const int page = a.page_table[(size_t)at.r * a.max_pages + (int)(p / a.page_size)];
-        if ((unsigned)page < (unsigned)a.num_pages) return page;
-        record_error(a.err, kErrPage, at.r, 0, page);
-        return -1;
-      };
-      int cur = page_of(lane), nxt = page_of(32 + lane);
+      PageFeed<kTile> feed(a, at, n);
+      const int ops = feed.boxes * C::kLines * 2, my_box = lane % feed.boxes;
       for (int k = 0; k < n && ok; ++k) {
-        const int b0 = k * boxes;
-        if (b0 > 0 && (b0 & 31) == 0) {
-          cur = nxt;
-          nxt = page_of(b0 + 32 + lane);
-        }
-        // this lane's box within the tile, and its page
-        const int my_box = lane % boxes;
-        const int page = __shfl_sync(kFull, cur, (b0 & 31) + my_box);
+        const int page = feed.of_tile(a, at, k);
         const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
-        ok = wait(&empty_bar[stage], phase ^ 1u);
-        ok = __all_sync(kFull, ok);
+        ok = __all_sync(kFull, wait(&empty_bar[stage], phase ^ 1u));
         if (!ok) break;
         const uint32_t bar = smem_u32(&full_bar[stage]);
         if (lane == 0) {
           uint32_t bad = 0;
 #pragma unroll
           for (int s = 0; s < kTile / kSlice; ++s)  // a box holds whole sub-slices
-            if ((bad_boxes >> (s * kSlice / box)) & 1u) bad |= 1u << s;
+            if ((bad_boxes >> (s * kSlice / feed.box)) & 1u) bad |= 1u << s;
           s_bad[stage] = bad;
           mbar_expect_tx(bar, C::kStage);
         }
         __syncwarp();
-        const int slot = (int)(((long long)(first_box + b0 + my_box) * box) % a.page_size);
+        const int slot = feed.slot_of(a, k);
         const uint32_t base = smem_u32(ring + stage * C::kStage);
         for (int i = lane; i < ops; i += 32) {  // (32 is a multiple of boxes: i % boxes == my_box)
-          const int line = (i / boxes) % C::kLines, v = i / (boxes * C::kLines);
-          tma_load_4d(base + (uint32_t)(v * C::kHalf + line * (kTile * C::kLine) + my_box * box * C::kLine),
+          const int line = (i / feed.boxes) % C::kLines, v = i / (feed.boxes * C::kLines);
+          tma_load_4d(base + (uint32_t)(v * C::kHalf + line * (kTile * C::kLine) + my_box * feed.box * C::kLine),
                       v ? &tm_v : &tm_k, line * (C::kLine / (FP8 ? 1 : 2)), slot, g,
                       page < 0 ? a.num_pages : page /* outside: zeros */, bar);
         }
@@ -822,9 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // ---- the segment's end: join the warps ----
     const bool whole = n == at.tiles;
     const long long unit = (long long)at.r * units + at.x;
-    if (tid == 0 && at.t == 0) a.unit_at[unit] = whole ? -1 : w;
     // a CTA's first segment has its slot 0, a later one (its last) slot 1
-    float* piece = a.parts + ((size_t)blockIdx.x * 2 + (w == w0 ? 0 : 1)) * C::kPieceFloats;
+    const int pslot = w == w0 ? 0 : 1;
+    if (tid == 0 && at.t == 0)
+      a.unit_desc[unit] = whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.of_tile(w + at.tiles - 1), pslot);
+    float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
     const int wrow = warp * C::kGroupRows;
 #pragma unroll
     for (int kk = 0; kk < 2 * MT; ++kk) {
@@ -911,77 +702,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   }
 }
 
-// Joins the pieces of split units and writes the rows of requests without
-// positions. One block of WARPS warps a row, the pieces dealt to the warps.
-template <class C, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs a) {
-  constexpr int D = C::D, E = D / 32;
-  __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int orow = blockIdx.x;
-  const int rj = orow / a.n_q_heads, h = orow - rj * a.n_q_heads, r = rj / a.n_q, j = rj - r * a.n_q;
-  const int g = h / a.group, i = j * a.group + (h - g * a.group);
-  const int rb = i / C::kRows, row = i - rb * C::kRows;
-  pdl_wait();
-  const int tiles = range_of(a, r).tiles(C::kTile);
-  float m = kNegInf, l = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (tiles > 0) {
-    const long long u0 = a.unit_at[((long long)r * a.n_kv_heads + g) * a.row_blocks + rb];
-    if (u0 < 0) return;  // a whole unit: its CTA wrote the row
-    const long long total = *a.total;
-    const int ctas = ctas_of(a, total);
-    const int c0 = cta_of_tile(total, ctas, u0), c1 = cta_of_tile(total, ctas, u0 + tiles - 1);
-    // slot 1 of a CTA whose share began before the unit
-    const int odd = share_begin(total, ctas, c0) < u0 ? 1 : 0;
-    for (int c = c0 + warp; c <= c1; c += WARPS) {
-      const float* p = a.parts + ((size_t)c * 2 + (c == c0 ? odd : 0)) * C::kPieceFloats;
-      const float pm = p[row], pl = p[C::kRows + row];
-      float pa[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) pa[e] = p[2 * C::kRows + row * D + lane * E + e];
-      const float mn = fmaxf(m, pm), mu = mn == kNegInf ? 0.f : mn;
-      const float f = exp2_sfu(m - mu), x = exp2_sfu(pm - mu);
-      l = l * f + pl * x;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + pa[e] * x;
-      m = mn;
-    }
-  }
-  if constexpr (WARPS > 1) {
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    if (warp > 0) return;
-    float big = kNegInf;
-#pragma unroll
-    for (int u = 0; u < WARPS; ++u) big = fmaxf(big, s_m[u]);
-    const float mu = big == kNegInf ? 0.f : big;
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int u = 0; u < WARPS; ++u) {
-      const float f = exp2_sfu(s_m[u] - mu);
-      l += s_l[u] * f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += s_acc[u][lane * E + e] * f;
-    }
-    m = big;
-  }
-  const float inv = (C::FP8 ? a.v_scale[g] : 1.f) / l;
-  __nv_bfloat16* o = a.out + (size_t)orow * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(o + e) = l == 0.f ? 0u : pack_bf(acc[e] * inv, acc[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-}
-
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
@@ -999,56 +719,18 @@ Shape shape_of(const qsa_dims& d) {
   return {mt, rows > 16 * mt ? 2 : 1};
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-  static EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
-// the cache [num_pages][n_kv_heads][page_size][head_dim] with boxes of one
-// page's (or 64) positions of one head, at most 128 bytes of a row wide
-template <class C>
-bool make_map(CUtensorMap* map, const qsa_dims& d, const void* cache) {
-  const EncodeTiled enc = encode_fn();
-  if (!enc) return false;
-  constexpr int eb = C::FP8 ? 1 : 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.n_kv_heads,
-                              (cuuint64_t)d.num_pages};
-  const cuuint64_t row = (cuuint64_t)d.head_dim * eb;
-  const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.n_kv_heads};
-  const cuuint32_t box[4] = {(cuuint32_t)(C::kLine / eb), (cuuint32_t)std::min(C::kTile, d.page_size), 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-             const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             C::kLine == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class C>
 cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
   alignas(64) CUtensorMap tk, tv;
-  if (!make_map<C>(&tk, d, k_cache) || !make_map<C>(&tv, d, v_cache)) return cudaErrorInvalidValue;
+  if (!make_cache_map(&tk, d, k_cache, C::kTile, C::kLine) || !make_cache_map(&tv, d, v_cache, C::kTile, C::kLine))
+    return cudaErrorInvalidValue;
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(dense_kernel<C>, C::kSmem);
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
   e = launch_k(dense_kernel<C>, dim3(a.grid), dim3(kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  // many rows: their units have few pieces, one warp joins a row's; few rows:
-  // up to the grid's number of pieces each
-  const unsigned rows = (unsigned)(a.batch * a.n_q * a.n_q_heads);
-  if (rows >= 8u * a.grid) return launch_k(dense_join_kernel<C, 1>, dim3(rows), dim3(32), 0, s, true, a);
-  return launch_k(dense_join_kernel<C, 8>, dim3(rows), dim3(256), 0, s, true, a);
+  return launch_join<C::D, C::kRows, C::FP8>(a, s);
 }
 
 template <int D, bool FP8>
@@ -1062,16 +744,30 @@ cudaError_t launch(const Shape& sh, const qsa_dims& d, const DenseArgs& a, const
   }
 }
 
+// rows of a unit of these dims
+int unit_rows(const qsa_dims& d) { return d.head_dim == 128 ? dense_tc_rows(d) : shape_of(d).rows(); }
+
 }  // namespace
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
 
 DenseWs dense_ws(const qsa_dims& d, int num_sms) {
   DenseWs w;
-  const Shape sh = shape_of(d);
-  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
-  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + sh.rows() - 1) / sh.rows());
+  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads), per = unit_rows(d);
+  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per);
   w.units = 256 + align_up((size_t)d.batch * d.n_q * d.n_kv_heads * sizeof(int32_t), 256);
-  w.parts = align_up(w.units + (1 + units) * sizeof(long long), 256);
-  w.total = align_up(w.parts + (size_t)num_sms * 2 * sh.rows() * (d.head_dim + 2) * sizeof(float), 256);
+  w.parts = align_up(w.units + units * sizeof(long long), 256);
+  w.total = align_up(w.parts + (size_t)num_sms * 2 * per * (d.head_dim + 2) * sizeof(float), 256);
   return w;
 }
 
@@ -1089,8 +785,7 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.q_pos = q_pos;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.total = reinterpret_cast<long long*>(base + w.units);
-  a.unit_at = a.total + 1;
+  a.unit_desc = reinterpret_cast<long long*>(base + w.units);
   a.parts = reinterpret_cast<float*>(base + w.parts);
   a.err = static_cast<int32_t*>(ws);
   a.batch = d.batch;
@@ -1104,15 +799,12 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.window = window;
   a.grid = sms;
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
+  if (d.head_dim == 128) return launch_dense_tc(d, a, k_cache, v_cache, s);
   const Shape sh = shape_of(d);
   const bool fp8 = d.kv_dtype == QSA_KV_FP8_E4M3;
-  switch (d.head_dim) {
-    case 64: return fp8 ? launch<64, true>(sh, d, a, k_cache, v_cache, s) : launch<64, false>(sh, d, a, k_cache, v_cache, s);
-    case 128:
-      return fp8 ? launch<128, true>(sh, d, a, k_cache, v_cache, s) : launch<128, false>(sh, d, a, k_cache, v_cache, s);
-    default:
-      return fp8 ? launch<256, true>(sh, d, a, k_cache, v_cache, s) : launch<256, false>(sh, d, a, k_cache, v_cache, s);
-  }
+  if (d.head_dim == 64)
+    return fp8 ? launch<64, true>(sh, d, a, k_cache, v_cache, s) : launch<64, false>(sh, d, a, k_cache, v_cache, s);
+  return fp8 ? launch<256, true>(sh, d, a, k_cache, v_cache, s) : launch<256, false>(sh, d, a, k_cache, v_cache, s);
 }
 
 }  // namespace qsa

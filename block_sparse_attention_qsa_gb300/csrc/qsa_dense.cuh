@@ -1,0 +1,409 @@
+// What the two dense-attention kernels share: the stream of tiles and its
+// split, instruction wrappers, tensor maps, and the kernel that joins the
+// pieces of split units. The mathematics is in qsa_dense.cu.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "qsa_kv_internal.cuh"
+
+namespace qsa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxSmem = 232448;  // 227 KB a CTA
+constexpr int kMinTiles = 2;      // tiles a CTA takes at least
+constexpr long long kWaitCycles = 1LL << 31;  // bound of every wait: about one second
+
+struct DenseArgs {
+  const __nv_bfloat16* q;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* q_pos;
+  __nv_bfloat16* out;
+  float* lse;
+  long long* unit_desc;  // where each unit's pieces are (see unit_* below)
+  float* parts;          // [grid][2] pieces: m[rows], l[rows], acc[rows][D]
+  int32_t* err;
+  int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
+  int page_size, max_pages, num_pages, window, grid;
+  float sm_scale;
+};
+
+// Unit descriptors: written whole, without positions, or the pieces of CTAs
+// first .. last (the first CTA's in its slot `slot`, the others' in slot 0).
+constexpr long long kUnitWhole = -1, kUnitEmpty = -2;
+__device__ __forceinline__ long long unit_pieces(int first, int last, int slot) {
+  return (long long)first | ((long long)last << 24) | ((long long)slot << 48);
+}
+
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for a phase of a barrier. The first wait that runs out records
+// the timeout and sets the CTA's abort flag; the others then give up too.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  const long long start = clock64();
+  while (!mbar_try_wait(b, parity)) {
+    if (*abort) return false;
+    if (clock64() - start > kWaitCycles) {
+      *abort = 1;
+      record_error(err, kErrTimeout, 0, 0, (int)threadIdx.x);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// 2^x on the special-function unit (relative error about 2^-22, 2^-inf = 0)
+__device__ __forceinline__ float exp2_sfu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the four E4M3 codes of a word as two FP16 pairs (exact)
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ float pow2(int s) { return __uint_as_float((uint32_t)(127 + s) << 23); }
+
+// ---------------------------------------------------------------------------
+// the stream of tiles
+// ---------------------------------------------------------------------------
+// Positions lo .. hi - 1 that any query of request r sees (hi = 0: none).
+struct Range {
+  int lo, hi;
+  __device__ __forceinline__ int tiles(int tile) const { return hi > 0 ? (hi - 1) / tile + 1 - lo / tile : 0; }
+};
+__device__ __forceinline__ int capacity(const DenseArgs& a) { return a.max_pages * a.page_size; }
+__device__ __forceinline__ bool valid_pos(const DenseArgs& a, int p) { return p >= 0 && p < capacity(a); }
+__device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
+  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+__device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
+  int p[kMaxNq];
+#pragma unroll
+  for (int j = 0; j < kMaxNq; ++j) p[j] = j < a.n_q ? a.q_pos[(size_t)r * a.n_q + j] : -1;
+  Range g{0x7fffffff, 0};
+#pragma unroll
+  for (int j = 0; j < kMaxNq; ++j) {
+    if (!valid_pos(a, p[j])) continue;
+    g.lo = min(g.lo, low_of(a, p[j]));
+    g.hi = max(g.hi, p[j] + 1);
+  }
+  return g.hi > 0 ? g : Range{0, 0};
+}
+
+// quotient of non-negative numbers; most streams fit the 32-bit division
+__device__ __forceinline__ long long quot(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// The stream's shares: `ctas` CTAs, the first `rem` of them with one tile more
+// than `q`.
+struct Split {
+  long long q;
+  int ctas, rem;
+  __device__ __forceinline__ void init(const DenseArgs& a, long long tiles) {
+    ctas = (int)min((long long)a.grid, quot(tiles + kMinTiles - 1, kMinTiles));
+    q = ctas > 0 ? quot(tiles, ctas) : 0;
+    rem = (int)(tiles - q * ctas);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ int of_tile(long long w) const {
+    const long long wide = rem * (q + 1);
+    return (int)(w < wide ? quot(w, q + 1) : rem + quot(w - wide, q));
+  }
+};
+
+// A place in the stream (of tiles of TILE positions): unit x = 0 ..
+// n_kv_heads * row_blocks - 1 of request r, tile t of its `tiles`.
+template <int TILE>
+struct Place {
+  int r, x, t, tiles;
+  Range g;
+  __device__ __forceinline__ void next_unit(const DenseArgs& a) {
+    t = 0;
+    if (++x < a.n_kv_heads * a.row_blocks) return;
+    x = 0;
+    do {
+      if (++r >= a.batch) return;
+      g = range_of(a, r);
+      tiles = g.tiles(TILE);
+    } while (tiles == 0);
+  }
+};
+
+// Shared memory of find_start.
+template <int THREADS>
+struct StartSmem {
+  long long scan[THREADS / 32], first;
+  int first_r;
+};
+
+// Every thread of the block: works the stream out from q_pos (each thread sums
+// the tiles of a contiguous run of requests, one block scan), and finds the
+// CTA's share w0 .. w1 - 1 and where it begins. Block 0 reports positions that
+// are none and marks the units that have no tile. False: nothing to do.
+template <int TILE, int THREADS>
+__device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS>& sm, Split& sp, long long& w0,
+                                           long long& w1, Place<TILE>& at) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int units = a.n_kv_heads * a.row_blocks;  // of a request
+  const int per = (a.batch + THREADS - 1) / THREADS;
+  const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles(TILE);
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sm.scan[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const long long v = sm.scan[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  sp.init(a, total * units);
+  if (blockIdx.x == 0) {
+    for (int r = r0; r < r1; ++r) {
+      for (int j = 0; j < a.n_q; ++j) {
+        const int p = a.q_pos[(size_t)r * a.n_q + j];
+        if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
+      }
+      if (range_of(a, r).tiles(TILE) == 0)
+        for (int x = 0; x < units; ++x) a.unit_desc[(long long)r * units + x] = kUnitEmpty;
+    }
+  }
+  if ((int)blockIdx.x >= sp.ctas) return false;
+  w0 = sp.begin(blockIdx.x);
+  w1 = sp.begin(blockIdx.x + 1);
+  if (before * units <= w0 && w0 < (before + mine) * units) {  // one thread: tile w0 is in one of its requests
+    long long b = before;
+    for (int r = r0; r < r1; ++r) {
+      const int t = range_of(a, r).tiles(TILE);
+      if (w0 < (b + t) * units) {
+        sm.first_r = r;
+        sm.first = b;
+        break;
+      }
+      b += t;
+    }
+  }
+  __syncthreads();
+  at.r = sm.first_r;
+  at.g = range_of(a, at.r);
+  at.tiles = at.g.tiles(TILE);
+  const long long off = w0 - sm.first * units;
+  at.x = (int)quot(off, at.tiles);
+  at.t = (int)(off - (long long)at.x * at.tiles);
+  return true;
+}
+
+// The pages of a segment's boxes (box = the positions that one TMA copy takes,
+// all in one page), looked up by a whole warp 32 boxes ahead. A box that no
+// query sees has none (and is not looked up: its entry may mean nothing).
+template <int TILE>
+struct PageFeed {
+  int cur, nxt, first_box, n_boxes, box, boxes;
+  __device__ __forceinline__ int page_of(const DenseArgs& a, const Place<TILE>& at, int i) const {
+    const long long p = (long long)(first_box + i) * box;
+    if (i >= n_boxes || p >= at.g.hi || p + box <= at.g.lo) return -1;
+    const int page = a.page_table[(size_t)at.r * a.max_pages + (int)(p / a.page_size)];
+    if ((unsigned)page < (unsigned)a.num_pages) return page;
+    record_error(a.err, kErrPage, at.r, 0, page);
+    return -1;
+  }
+  __device__ __forceinline__ PageFeed(const DenseArgs& a, const Place<TILE>& at, int n_tiles) {
+    box = min(TILE, a.page_size);
+    boxes = TILE / box;
+    first_box = (at.g.lo / TILE + at.t) * boxes;
+    n_boxes = n_tiles * boxes;
+    cur = page_of(a, at, threadIdx.x & 31);
+    nxt = page_of(a, at, 32 + (threadIdx.x & 31));
+  }
+  // page of this lane's box (lane % boxes) of the segment's tile k
+  __device__ __forceinline__ int of_tile(const DenseArgs& a, const Place<TILE>& at, int k) {
+    const int b0 = k * boxes, lane = threadIdx.x & 31;
+    if (b0 > 0 && (b0 & 31) == 0) {
+      cur = nxt;
+      nxt = page_of(a, at, b0 + 32 + lane);
+    }
+    return __shfl_sync(kFull, cur, (b0 & 31) + lane % boxes);
+  }
+  __device__ __forceinline__ int slot_of(const DenseArgs& a, int k) const {
+    return (int)(((long long)(first_box + k * boxes + (threadIdx.x & 31) % boxes) * box) % a.page_size);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// joining split units
+// ---------------------------------------------------------------------------
+// Joins the pieces of split units and writes the rows of requests without
+// positions: one block of WARPS warps a row, the pieces dealt to the warps,
+// every warp's loads issued before their maxima are looked at.
+template <int D, int ROWS, bool FP8, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs a) {
+  constexpr int E = D / 32, kPiece = ROWS * (D + 2), kBatch = 8;
+  __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int orow = blockIdx.x;
+  const int rj = orow / a.n_q_heads, h = orow - rj * a.n_q_heads, r = rj / a.n_q, j = rj - r * a.n_q;
+  const int g = h / a.group, i = j * a.group + (h - g * a.group);
+  const int rb = i / ROWS, row = i - rb * ROWS;
+  const float vscale = FP8 ? a.v_scale[g] : 1.f;
+  pdl_wait();
+  const long long desc = a.unit_desc[((long long)r * a.n_kv_heads + g) * a.row_blocks + rb];
+  if (desc == kUnitWhole) return;  // its CTA wrote the row
+  float m = kNegInf, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (desc != kUnitEmpty) {
+    const int c0 = (int)(desc & 0xffffff), c1 = (int)((desc >> 24) & 0xffffff), slot = (int)(desc >> 48);
+    for (int c = c0 + warp; c <= c1; c += WARPS * kBatch) {
+      float pm[kBatch], pl[kBatch], pa[kBatch][E];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int cc = c + b * WARPS;
+        pm[b] = kNegInf;
+        pl[b] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) pa[b][e] = 0.f;
+        if (cc <= c1) {
+          const float* p = a.parts + ((size_t)cc * 2 + (cc == c0 ? slot : 0)) * kPiece;
+          pm[b] = p[row];
+          pl[b] = p[ROWS + row];
+#pragma unroll
+          for (int e = 0; e < E; ++e) pa[b][e] = p[2 * ROWS + row * D + e * 32 + lane];
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) mn = fmaxf(mn, pm[b]);
+      const float mu = mn == kNegInf ? 0.f : mn, f = exp2_sfu(m - mu);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float x = exp2_sfu(pm[b] - mu);
+        l = fmaf(pl[b], x, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(pa[b][e], x, acc[e]);
+      }
+    }
+  }
+  if constexpr (WARPS > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+    float big = kNegInf;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) big = fmaxf(big, s_m[u]);
+    const float mu = big == kNegInf ? 0.f : big;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) {
+      const float f = exp2_sfu(s_m[u] - mu);
+      l += s_l[u] * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[u][e * 32 + lane] * f;
+    }
+    m = big;
+  }
+  const float inv = vscale / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    a.out[(size_t)orow * D + e * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] * inv);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled();  // cuTensorMapEncodeTiled through the runtime, or null
+
+// the cache [num_pages][n_kv_heads][page_size][head_dim] with boxes of one
+// page's (or `tile`) positions of one head, `line` (64 or 128) bytes of a row wide
+inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cache, int tile, int line) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const int eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.n_kv_heads,
+                              (cuuint64_t)d.num_pages};
+  const cuuint64_t row = (cuuint64_t)d.head_dim * eb;
+  const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.n_kv_heads};
+  const cuuint32_t box[4] = {(cuuint32_t)(line / eb), (cuuint32_t)std::min(tile, d.page_size), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// the joining kernel: with many rows a unit has few pieces, and one warp joins
+// a row's; with few rows there are up to the grid's number of pieces each
+template <int D, int ROWS, bool FP8>
+cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
+  const unsigned rows = (unsigned)(a.batch * a.n_q * a.n_q_heads);
+  if (rows >= 8u * a.grid)
+    return launch_k(dense_join_kernel<D, ROWS, FP8, 1>, dim3(rows), dim3(32), 0, s, true, a);
+  return launch_k(dense_join_kernel<D, ROWS, FP8, 8>, dim3(rows), dim3(256), 0, s, true, a);
+}
+
+// head dim 128 (qsa_dense_tc.cu)
+int dense_tc_rows(const qsa_dims& d);  // rows of a unit
+cudaError_t launch_dense_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s);
+
+}  // namespace qsa

@@ -1,0 +1,818 @@
+// Dense attention for head dim 128 on the fifth-generation tensor cores.
+//
+// The mathematics, the stream of tiles and its split are qsa_dense.cu's. This
+// kernel takes tiles of 128 positions, and computes both products transposed,
+// so that the long dimension fills the MMA's 128 rows (M) and the few query
+// rows are its columns (N):
+//   S^T[position][row] = K Q^T      (A = K, as the cache holds it; B = Q)
+//   O^T[d][row]       += V^T P^T    (A = V read along its other dimension:
+//                                    tcgen05 takes it from the same TMA tile)
+// with S^T and O^T in tensor memory. A softmax thread owns one position (one
+// TMEM lane) and all 8, 16 or 32 rows of its warpgroup, so there are no
+// shuffles, every row's arithmetic is independent of the others', and at the
+// end of a unit a thread owns one component d of every row: no joint of the
+// warps is left, the pieces go out as they are.
+//
+// What it is for: with mma.sync the same loop was bound by its warps' issue
+// and latency, not by memory: at 32 rows (4 verify queries x 8 heads), batch
+// 32 and about 55,600 tokens it took 289 us on an E4M3 cache, where the bytes
+// take 136 (fragments are loaded by ldmatrix and E4M3 is widened in
+// registers, about 550 instructions per 16 positions of a warp). Here K and V
+// never pass through registers.
+//
+// E4M3 cache: the MMA's operands are E4M3 as well, so the cache's codes are
+// used as they are, and Q and P become two E4M3 terms each, x = hi + lo / 32,
+// as 32 + 32 columns. A code has 4 significant bits, so the two together have
+// 8, as many as BF16: Q (its row scaled by a power of two to at most 2^8) is
+// exact down to 2^-15 of its row's largest value and off by at most 2^-23 of
+// that below; P keeps 2^-8 of each weight, like the BF16 path's rounding,
+// down to 2^-20 of the largest.
+//
+// The reference of a row: weights are 2^(s - mu), where mu only has to keep
+// the largest weight between 1 and 2^8 (E4M3 ends at 448): it starts 6 below
+// the row's first maximum and moves when a score passes mu + 8, which after a
+// row's first tiles hardly happens. Moving it rescales O in tensor memory.
+//
+// Roles: a copy warp (pages, TMA: K and V tiles in a ring of slots), an MMA
+// warp (S of tile i, then PV of tile i - 1), and one warpgroup of softmax per
+// 32 rows. S and P are double-buffered, so the tensor cores and the copies
+// run ahead of the softmax.
+//
+// Masks: as in qsa_dense.cu. A tile in which a row does not see every position
+// is an edge tile; there the thread that owns a position that no row sees
+// zeroes its V row in shared memory, and a V row that is not finite is taken
+// out of the MMA and added in FP32 to the rows that see it.
+#include "qsa_dense.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kDimTc = 128;
+constexpr int kTileTc = 128;
+constexpr float kRefBelow = 6.f;  // log2 of a row's first largest weight
+constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
+constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing: any score passes it
+constexpr int kBadRing = 16;      // page marks of the tiles in flight (at most 6)
+
+// RC: rows of a warpgroup (8, 16 or 32), WGS: softmax warpgroups
+template <bool FP8_, int RC_, int WGS_>
+struct Tc {
+  static constexpr bool FP8 = FP8_;
+  static constexpr int RC = RC_, WGS = WGS_;
+  static constexpr int kRows = RC * WGS;
+  static constexpr int kRowBytes = kDimTc * (FP8 ? 1 : 2);
+  static constexpr int kLines = kRowBytes / 128;
+  static constexpr int kSlot = kTileTc * kRowBytes;  // K or V of a tile
+  static constexpr int N = FP8 ? 64 : 32;            // MMA columns of a warpgroup (those past its rows idle)
+  static constexpr int kQ = N * kRowBytes;           // a warpgroup's Q
+  static constexpr int kP = kTileTc * 64;            // a warpgroup's P: 64 bytes a position
+  static constexpr int kFixed = 2 * WGS * (kQ + kP) + 1024;
+  static constexpr int kStatic = WGS == 1 ? 1792 : 3072;  // barriers and tables
+  static constexpr int kFit = (kMaxSmem - kStatic - kFixed) / kSlot;
+  static constexpr int kSlots = kFit < 12 ? kFit : 12;
+  static constexpr int kSmem = kSlots * kSlot + kFixed;
+  static constexpr int kThreads = 128 * WGS + 64;
+  static constexpr int kCopyWarp = 4 * WGS, kMmaWarp = kCopyWarp + 1;
+  static constexpr uint32_t kO = 2 * WGS * N;        // TMEM: two S buffers, then O
+  static constexpr uint32_t kNeed = 3 * WGS * N;
+  static constexpr uint32_t kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static constexpr int kPieceFloats = kRows * (kDimTc + 2);
+  static_assert(kSlots >= 4 && kSlots / 2 + 2 < kBadRing, "ring");
+};
+
+// ---------------------------------------------------------------------------
+// tensor-core instructions
+// ---------------------------------------------------------------------------
+// Shared-memory matrix descriptor: start address >> 4 (bits 0-13), leading
+// byte offset >> 4 (16-29), stride byte offset >> 4 (32-45), version 1
+// (46-47), swizzle mode (61-63: 2 = 128 bytes, 4 = 64 bytes).
+//  K-major, 128-byte rows: 8-row groups are the stride (1,024 bytes).
+//  MN-major: the stride steps over 8 rows of the k dimension (8 times the row
+//  pitch), the leading offset to the next 128-byte (64-byte) column block.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((lead >> 4) & 0x3fffu) << 16) |
+         ((uint64_t)((stride >> 4) & 0x3fffu) << 32) | ((uint64_t)1 << 46) | (swizzle << 61);
+}
+// Instruction descriptor: FP32 accumulator (bits 4-5), A and B types (7-9,
+// 10-12: 1 BF16 in kind::f16, 0 E4M3 in kind::f8f6f4), A and B MN-major (15,
+// 16), N / 8 (17-22), M / 16 (24-28).
+template <class C>
+__host__ __device__ constexpr uint32_t mma_desc(bool mn_major) {
+  return (1u << 4) | (C::FP8 ? 0u : (1u << 7) | (1u << 10)) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
+         ((uint32_t)(C::N >> 3) << 17) | ((uint32_t)(kTileTc >> 4) << 24);
+}
+template <bool FP8>
+__device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if constexpr (FP8) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, "
+        "p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, "
+        "p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void commit_tc(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// generic writes to shared memory, made visible to TMA and tensor cores
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// N consecutive 32-bit TMEM columns of this thread's lane
+template <int N>
+struct Tmem;
+template <>
+struct Tmem<8> {
+  static __device__ __forceinline__ void load(uint32_t addr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void store(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  }
+};
+template <>
+struct Tmem<16> {
+  static __device__ __forceinline__ void load(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+                 " [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                   "=r"(v[15])
+                 : "r"(addr)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void store(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                   "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+  }
+};
+template <>
+struct Tmem<32> {
+  static __device__ __forceinline__ void load(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                   "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+                   "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+                   "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 : "r"(addr)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void store(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                   "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+                   "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+                   "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                 : "memory");
+  }
+};
+
+// barriers of one softmax warpgroup (id 1 + wg) or of all of them (id 3)
+__device__ __forceinline__ void group_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, "
+      "q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// Reduces v[i] over the warp's lanes for every i < RC; the result for i is in
+// v[0] of the lanes with lane % RC == i. Halving: at each step a lane hands
+// the half of its values that it gives up to its partner.
+template <int RC, class Op>
+__device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o >= RC; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < RC; ++i) v[i] = op(v[i], __shfl_xor_sync(kFull, v[i], o));
+#pragma unroll
+  for (int o = RC / 2; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(kFull, give, o));
+    }
+  }
+  return v[0];
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
+                                                                  const __grid_constant__ CUtensorMap tm_v,
+                                                                  const DenseArgs a) {
+  constexpr bool FP8 = C::FP8;
+  constexpr int RC = C::RC, WGS = C::WGS, N = C::N, kTile = kTileTc, D = kDimTc;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = ring + C::kSlots * C::kSlot;   // [buffer][warpgroup]
+  uint8_t* s_p = s_q + 2 * WGS * C::kQ;         // [buffer][warpgroup]
+  __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], fin;
+  __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_bad[kBadRing];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
+  __shared__ int s_keep;                // a unit's first PV adds to what O holds
+  __shared__ volatile int s_abort;
+  __shared__ StartSmem<C::kThreads> s_start;
+  __shared__ int2 s_rng[2][C::kRows];   // [buffer][row]: positions the row sees, first and one past the last
+  __shared__ int2 s_all[2];             // positions that all rows of the unit see
+  __shared__ __align__(16) float s_scale[2][C::kRows];
+  __shared__ float s_red[WGS][4][RC];
+  __shared__ uint32_t s_odd[WGS][4];    // positions whose V is not finite
+  __shared__ uint32_t s_see[WGS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int units = a.n_kv_heads * a.row_blocks;
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(smem_u32(&slot_full[s]), 1);
+      mbar_init(smem_u32(&slot_empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&s_full[b]), 1);
+      mbar_init(smem_u32(&p_full[b]), 128 * WGS);
+      mbar_init(smem_u32(&pv_done[b]), 1);
+      mbar_init(smem_u32(&q_full[b]), 128 * WGS);
+    }
+    mbar_init(smem_u32(&fin), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();     // positions, queries and the cache may come from the kernel before
+  pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
+  Split sp;
+  long long w0, w1;
+  Place<kTile> at;
+  if (!find_start<kTile, C::kThreads>(a, s_start, sp, w0, w1, at)) return;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(C::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == C::kCopyWarp) {
+    // ---- copies: K then V of each tile ----
+    int slot = 0;
+    uint32_t phase = 0;
+    long long w = w0;
+    int it = 0;
+    bool ok = true;
+    while (w < w1 && ok) {
+      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+      const int g = at.x / a.row_blocks;
+      PageFeed<kTile> feed(a, at, n);
+      const int ops = feed.boxes * C::kLines, my_box = lane % feed.boxes;
+      for (int k = 0; k < n && ok; ++k, ++it) {
+        const int page = feed.of_tile(a, at, k);
+        const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
+        const int first = feed.slot_of(a, k);
+#pragma unroll 1
+        for (int v = 0; v < 2 && ok; ++v) {
+          ok = __all_sync(kFull, wait(&slot_empty[slot], phase ^ 1u));
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&slot_full[slot]);
+          if (lane == 0) {
+            if (v == 0) {
+              uint32_t bad = 0;
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                if ((bad_boxes >> (s * 16 / feed.box)) & 1u) bad |= 1u << s;
+              s_bad[it % kBadRing] = bad;
+            }
+            mbar_expect_tx(bar, C::kSlot);
+          }
+          __syncwarp();
+          const uint32_t base = smem_u32(ring + slot * C::kSlot);
+          if (lane < ops) {  // boxes * lines <= 16
+            const int line = lane / feed.boxes;
+            tma_load_4d(base + (uint32_t)(line * (kTile * 128) + my_box * feed.box * 128), v ? &tm_v : &tm_k,
+                        line * 64, first, g, page < 0 ? a.num_pages : page /* outside: zeros */, bar);
+          }
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      w += n;
+      if (w < w1) at.next_unit(a);
+    }
+    if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
+      for (int s = 0; s < C::kSlots; ++s) {
+        const uint32_t par = s < slot ? phase : phase ^ 1u;
+        const long long start = clock64();
+        while (!mbar_try_wait(smem_u32(&slot_full[s]), par) && clock64() - start < kWaitCycles / 64) {
+        }
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---- MMAs: S of tile i, then PV of tile i - 1 ----
+    if (lane == 0) {
+      constexpr uint32_t kS = mma_desc<C>(false), kPv = mma_desc<C>(true);
+      // k steps (32 bytes of a row, 16 or 32 positions) of the two products
+      constexpr int kSteps = C::kRowBytes / 32, kPvSteps = kTile / (FP8 ? 32 : 16);
+      int it = 0, seg = 0;
+      bool ok = true, pv_first = true, first = true;
+      auto pv = [&](int i, bool unit_first) -> bool {  // PV of tile i
+        const int vs = (2 * i + 1) % C::kSlots;
+        if (!wait(&p_full[i & 1], (uint32_t)(i >> 1) & 1u)) return false;
+        if (!wait(&slot_full[vs], (uint32_t)((2 * i + 1) / C::kSlots) & 1u)) return false;
+        tc_after();
+        const bool fresh = unit_first && *reinterpret_cast<volatile int*>(&s_keep) == 0;
+        const uint32_t v0 = smem_u32(ring + vs * C::kSlot);
+#pragma unroll
+        for (int g = 0; g < WGS; ++g) {
+          const uint32_t p0 = smem_u32(s_p + ((i & 1) * WGS + g) * C::kP);
+#pragma unroll
+          for (int ks = 0; ks < kPvSteps; ++ks) {
+            // A: positions as k, 128-byte rows, the second 64 components one line further on
+            const uint64_t da = smem_desc(v0 + (uint32_t)(ks * (kTile / kPvSteps) * 128), kTile * 128, 1024, 2);
+            // B: positions as k, 64-byte rows
+            const uint64_t db = smem_desc(p0 + (uint32_t)(ks * (kTile / kPvSteps) * 64), 512, 512, 4);
+            mma_tc<FP8>(tmem + C::kO + (uint32_t)(g * N), da, db, kPv, !(fresh && ks == 0));
+          }
+        }
+        commit_tc(&slot_empty[vs]);
+        commit_tc(&pv_done[i & 1]);
+        return true;
+      };
+      long long w = w0;
+      while (w < w1 && ok) {
+        const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+        ok = wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u);
+        for (int k = 0; k < n && ok; ++k, ++it) {
+          const int kslot = (2 * it) % C::kSlots;
+          ok = wait(&slot_full[kslot], (uint32_t)((2 * it) / C::kSlots) & 1u);
+          if (!ok) break;
+          tc_after();
+          const uint32_t k0 = smem_u32(ring + kslot * C::kSlot);
+#pragma unroll
+          for (int g = 0; g < WGS; ++g) {
+            const uint32_t q0 = smem_u32(s_q + ((seg & 1) * WGS + g) * C::kQ);
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+              const uint32_t line = (uint32_t)(ks >> 2), step = (uint32_t)(ks & 3) * 32u;
+              mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * WGS + g) * N),
+                          smem_desc(k0 + line * (kTile * 128) + step, 16, 1024, 2),
+                          smem_desc(q0 + line * (N * 128) + step, 16, 1024, 2), kS, ks > 0);
+            }
+          }
+          commit_tc(&slot_empty[kslot]);
+          commit_tc(&s_full[it & 1]);
+          if (it > 0) ok = pv(it - 1, pv_first);
+          pv_first = k == 0;
+          first = false;
+        }
+        w += n;
+        ++seg;
+        if (w < w1) at.next_unit(a);
+      }
+      if (ok && !first) ok = pv(it - 1, pv_first);
+      // the tensor cores are done before the CTA gives its memory back
+      commit_tc(&fin);
+      const long long start = clock64();
+      while (!mbar_try_wait(smem_u32(&fin), 0) && clock64() - start < kWaitCycles) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax ----
+    const int wg = warp >> 2, quarter = warp & 3, t = tid & 127;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(wg * N);
+    const int row_off = wg * RC;
+
+    // the rows of the unit at `u` into Q buffer `buf`, with what is known of them
+    auto stage_q = [&](const Place<kTile>& u, int buf) {
+      const int g = u.x / a.row_blocks, rb = u.x - g * a.row_blocks;
+      const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
+      const float base_scale = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
+      uint8_t* dst = s_q + (buf * WGS + wg) * C::kQ;
+#pragma unroll
+      for (int z = 0; z < RC / 8; ++z) {
+        const int r = (t >> 4) + 8 * z, c = t & 15;  // 16 lanes a row, 8 components each
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row_off + r < rows) {
+          const int i = rb * C::kRows + row_off + r, j = i / a.group, h = g * a.group + (i - j * a.group);
+          v = ld16(a.q + (((size_t)u.r * a.n_q + j) * a.n_q_heads + h) * D + c * 8);
+        }
+        if constexpr (FP8) {
+          uint32_t big = 0;  // magnitudes of BF16 values order like their bit patterns
+          const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+          // 2^-sh brings the row's largest value into [2^7, 2^8)
+          const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 7));
+          const float down = pow2(-sh);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = bf_lo(wd[e]) * down, y = bf_hi(wd[e]) * down;
+            hi[e] = e4m3x2(x, y);
+            const float2 f = h2_to_f2(e4m3x2_to_h2(hi[e]));
+            lo[e] = e4m3x2((x - f.x) * 32.f, (y - f.y) * 32.f);
+          }
+          uint8_t* d8 = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(d8) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(d8 + 32 * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          if (c == 0) s_scale[buf][row_off + r] = base_scale * pow2(sh);
+        } else {
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+          if (c == 0) s_scale[buf][row_off + r] = base_scale;
+        }
+      }
+      if (t < RC) {
+        int2 rg = make_int2(0, 0);
+        if (row_off + t < rows) {
+          const int p = a.q_pos[(size_t)u.r * a.n_q + (rb * C::kRows + row_off + t) / a.group];
+          if (valid_pos(a, p)) rg = make_int2(low_of(a, p), p + 1);
+        }
+        s_rng[buf][row_off + t] = rg;
+      }
+      if (tid == 0) {
+        int2 all = make_int2(0, 0x7fffffff);
+        for (int j = rb * C::kRows / a.group; j <= (rb * C::kRows + rows - 1) / a.group; ++j) {
+          const int p = a.q_pos[(size_t)u.r * a.n_q + j];
+          all.x = max(all.x, valid_pos(a, p) ? low_of(a, p) : 0);
+          all.y = min(all.y, valid_pos(a, p) ? p + 1 : 0);
+        }
+        s_all[buf] = all;
+      }
+      async_fence();
+      mbar_arrive(smem_u32(&q_full[buf]));
+    };
+
+    stage_q(at, 0);
+    long long w = w0;
+    int it = 0, seg = 0;
+    while (w < w1) {
+      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+      const int buf = seg & 1;
+      if (w + n < w1) {  // the next unit's rows (the last one's are done with)
+        Place<kTile> next = at;
+        next.next_unit(a);
+        stage_q(next, buf ^ 1);
+      }
+      if constexpr (WGS == 1)
+        group_sync(1 + wg, 128);  // the tables of this unit
+      else
+        group_sync(3, 128 * WGS);
+      const int2 all = s_all[buf];
+      float mu[RC], l[RC];
+      const float sc = s_scale[buf][row_off];  // BF16: all rows' scale
+#pragma unroll
+      for (int r = 0; r < RC; ++r) {
+        mu[r] = kNoRef;
+        l[r] = 0.f;
+      }
+
+      for (int k = 0; k < n; ++k, ++it) {
+        const bool ok = wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u);
+        (void)ok;  // given up: the loop runs on without meaning, to the same barriers
+        __syncwarp();
+        tc_after();
+        const uint32_t s_addr = tmem + lane_base + (uint32_t)(((it & 1) * WGS + wg) * N);
+        const int p0 = (at.g.lo / kTile + at.t + k) * kTile, p = p0 + t;
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&s_bad[it % kBadRing]);
+        const bool edge = p0 < all.x || p0 + kTile > all.y || bad != 0;
+        const bool paged = !((bad >> (t >> 4)) & 1u);
+        float y[RC];
+        // scores (exp2 domain), -infinity where masked, less the reference
+        auto scores = [&](bool relative) {
+          uint32_t v[RC];
+          Tmem<RC>::load(s_addr, v);
+          if constexpr (FP8) {
+            uint32_t u[RC];
+            Tmem<RC>::load(s_addr + 32, u);
+            tc_wait_ld();
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+              const float s = fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r]));
+              y[r] = fmaf(s, s_scale[buf][row_off + r], relative ? -mu[r] : 0.f);
+            }
+          } else {
+            tc_wait_ld();
+#pragma unroll
+            for (int r = 0; r < RC; ++r) y[r] = fmaf(__uint_as_float(v[r]), sc, relative ? -mu[r] : 0.f);
+          }
+          if (edge) {
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+              const int2 rg = s_rng[buf][row_off + r];
+              if (p < rg.x || p >= rg.y || !paged) y[r] = kNegInf;
+            }
+          }
+        };
+        scores(true);
+        bool grew = false;
+#pragma unroll
+        for (int r = 0; r < RC; ++r) grew |= y[r] > kRefMost;
+        if (group_any(1 + wg, 128, grew)) {
+          scores(false);
+          {
+            float v[RC];
+#pragma unroll
+            for (int r = 0; r < RC; ++r) v[r] = y[r];
+            const float x = reduce_rows<RC>(v, [](float c, float d) { return fmaxf(c, d); });
+            if (lane < RC) s_red[wg][quarter][lane] = x;
+          }
+          group_sync(1 + wg, 128);
+          if (k > 0) wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
+          __syncwarp();
+          tc_after();
+          uint32_t o[RC];
+          float f[RC];
+          if (k > 0) {
+            Tmem<RC>::load(o_addr, o);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int r = 0; r < RC; ++r) {
+            const float top = fmaxf(fmaxf(s_red[wg][0][r], s_red[wg][1][r]), fmaxf(s_red[wg][2][r], s_red[wg][3][r]));
+            const float to = top > mu[r] + kRefMost || mu[r] == kNoRef ? fmaxf(top - kRefBelow, kNoRef) : mu[r];
+            f[r] = exp2_sfu(mu[r] - to);
+            mu[r] = to;
+            l[r] *= f[r];
+            y[r] -= to;
+          }
+          if (k > 0) {
+#pragma unroll
+            for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+            Tmem<RC>::store(o_addr, o);
+            if constexpr (FP8) {
+              Tmem<RC>::load(o_addr + 32, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+              Tmem<RC>::store(o_addr + 32, o);
+            }
+            tc_wait_st();
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RC; ++r) {
+          y[r] = exp2_sfu(y[r]);
+          l[r] += y[r];
+        }
+        if (k == 0 && tid == 0) s_keep = 0;
+        if (edge) {
+          const int vs = (2 * it + 1) % C::kSlots;
+          wait(&slot_full[vs], (uint32_t)((2 * it + 1) / C::kSlots) & 1u);
+          uint8_t* vrow = ring + vs * C::kSlot;
+          auto zero_row = [&]() {
+#pragma unroll 1
+            for (int c = 0; c < C::kRowBytes / 16; ++c)
+              *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kTile * 128) + t * 128 + ((c & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          };
+          bool odd = false;
+          if (p < at.g.lo || p >= at.g.hi || !paged) {
+            zero_row();
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < C::kRowBytes / 16; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * (kTile * 128) + t * 128 +
+                                                              (((c + lane) & 7) << 4));
+              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (FP8)
+                  odd |= (((wd[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                else
+                  odd |= (wd[e] & 0x7f80u) == 0x7f80u || (wd[e] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+          }
+          if (group_any(3, 128 * WGS, odd)) {
+            // these rows go to O by hand (FP32), where they are seen, and leave the MMA
+            const uint32_t mask = __ballot_sync(kFull, odd);
+            if (lane == 0) s_odd[wg][quarter] = mask;
+            if (k > 0) wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
+            __syncwarp();
+            tc_after();
+            uint32_t o[RC];
+#pragma unroll
+            for (int r = 0; r < RC; ++r) o[r] = 0;
+            if (k > 0) {
+              Tmem<RC>::load(o_addr, o);
+              tc_wait_ld();
+            } else if (FP8) {
+              Tmem<RC>::store(o_addr + 32, o);
+            }
+            group_sync(1 + wg, 128);
+#pragma unroll 1
+            for (int u = 0; u < kTile; ++u) {
+              if (!((s_odd[wg][u >> 5] >> (u & 31)) & 1u)) continue;
+              if (t == u) {
+                uint32_t see = 0;
+#pragma unroll
+                for (int r = 0; r < RC; ++r) {
+                  const int2 rg = s_rng[buf][row_off + r];
+                  if (p >= rg.x && p < rg.y) see |= 1u << r;
+                  s_red[wg][0][r] = y[r];
+                }
+                s_see[wg] = see;
+              }
+              group_sync(1 + wg, 128);
+              float v;
+              if constexpr (FP8) {
+                const uint8_t code = vrow[u * 128 + (((t >> 4) ^ (u & 7)) << 4) + (t & 15)];
+                v = h2_to_f2(e4m3x2_to_h2(code)).x;
+              } else {
+                v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                    vrow + (t >> 6) * (kTile * 128) + u * 128 + ((((t >> 3) & 7) ^ (u & 7)) << 4) + (t & 7) * 2));
+              }
+#pragma unroll
+              for (int r = 0; r < RC; ++r)
+                if ((s_see[wg] >> r) & 1u) o[r] = __float_as_uint(fmaf(s_red[wg][0][r], v, __uint_as_float(o[r])));
+              group_sync(1 + wg, 128);
+            }
+            Tmem<RC>::store(o_addr, o);
+            tc_wait_st();
+            group_sync(3, 128 * WGS);  // every warpgroup has read the rows
+            if (odd) {
+              zero_row();
+#pragma unroll
+              for (int r = 0; r < RC; ++r) y[r] = 0.f;
+            }
+            if (k == 0 && tid == 0) s_keep = 1;
+          }
+        }
+        // P of the tile before last has been read
+        if (it >= 2) wait(&pv_done[it & 1], (uint32_t)((it - 2) >> 1) & 1u);
+        uint8_t* prow = s_p + ((it & 1) * WGS + wg) * C::kP + t * 64;
+        const int x4 = (t >> 1) & 3;
+        if constexpr (FP8) {
+          uint32_t hi[RC / 2], lo[RC / 2];
+#pragma unroll
+          for (int r = 0; r < RC; r += 2) {
+            hi[r / 2] = e4m3x2(y[r], y[r + 1]);
+            const float2 f = h2_to_f2(e4m3x2_to_h2(hi[r / 2]));
+            lo[r / 2] = e4m3x2((y[r] - f.x) * 32.f, (y[r + 1] - f.y) * 32.f);
+          }
+#pragma unroll
+          for (int c = 0; c < RC / 8; ++c) {  // 8 rows at a time: half a chunk
+            const int off = (c & 1) * 8;
+            *reinterpret_cast<uint2*>(prow + (((c >> 1) ^ x4) << 4) + off) =
+                make_uint2(hi[4 * c] | (hi[4 * c + 1] << 16), hi[4 * c + 2] | (hi[4 * c + 3] << 16));
+            *reinterpret_cast<uint2*>(prow + (((2 + (c >> 1)) ^ x4) << 4) + off) =
+                make_uint2(lo[4 * c] | (lo[4 * c + 1] << 16), lo[4 * c + 2] | (lo[4 * c + 3] << 16));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < RC / 8; ++c)
+            *reinterpret_cast<uint4*>(prow + ((c ^ x4) << 4)) =
+                make_uint4(pack_bf(y[8 * c], y[8 * c + 1]), pack_bf(y[8 * c + 2], y[8 * c + 3]),
+                           pack_bf(y[8 * c + 4], y[8 * c + 5]), pack_bf(y[8 * c + 6], y[8 * c + 7]));
+        }
+        async_fence();
+        tc_before();
+        mbar_arrive(smem_u32(&p_full[it & 1]));
+      }
+
+      // ---- the segment's end: component t of every row ----
+      const int g = at.x / a.row_blocks, rb = at.x - g * a.row_blocks;
+      const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
+      const bool whole = n == at.tiles;
+      const int pslot = w == w0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
+      if (tid == 0 && at.t == 0)
+        a.unit_desc[(long long)at.r * units + at.x] =
+            whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.of_tile(w + at.tiles - 1), pslot);
+      {
+        const float x = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
+        group_sync(1 + wg, 128);  // (s_red's last readers are done)
+        if (lane < RC) s_red[wg][quarter][lane] = x;
+      }
+      wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
+      __syncwarp();
+      tc_after();
+      uint32_t o[RC];
+      Tmem<RC>::load(o_addr, o);
+      if constexpr (FP8) {
+        uint32_t u[RC];
+        Tmem<RC>::load(o_addr + 32, u);
+        tc_wait_ld();
+#pragma unroll
+        for (int r = 0; r < RC; ++r)
+          o[r] = __float_as_uint(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(o[r])));
+      } else {
+        tc_wait_ld();
+      }
+      group_sync(1 + wg, 128);
+      const float vscale = FP8 ? a.v_scale[g] : 1.f;
+      float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
+      const int i0 = rb * C::kRows + row_off;
+      int j = i0 / a.group, hh = i0 - j * a.group;
+#pragma unroll
+      for (int r = 0; r < RC; ++r) {
+        if (row_off + r < rows) {
+          const float sum = (s_red[wg][0][r] + s_red[wg][1][r]) + (s_red[wg][2][r] + s_red[wg][3][r]);
+          const float acc = __uint_as_float(o[r]);
+          if (whole) {
+            const size_t orow = ((size_t)at.r * a.n_q + j) * a.n_q_heads + g * a.group + hh;
+            a.out[orow * D + t] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum * vscale);
+            if (a.lse && t == 0) a.lse[orow] = sum == 0.f ? kNegInf : (mu[r] + log2f(sum)) * kLn2;
+          } else {
+            piece[2 * C::kRows + (row_off + r) * D + t] = acc;
+            if (t == 0) {
+              piece[row_off + r] = mu[r] == kNoRef ? kNegInf : mu[r];
+              piece[C::kRows + row_off + r] = sum;
+            }
+          }
+        }
+        if (++hh == a.group) {
+          hh = 0;
+          ++j;
+        }
+      }
+      tc_before();
+      w += n;
+      ++seg;
+      if (w < w1) at.next_unit(a);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == C::kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+}
+
+template <bool FP8, int RC, int WGS>
+cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
+  using C = Tc<FP8, RC, WGS>;
+  alignas(64) CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, d, k_cache, kTileTc, 128) || !make_cache_map(&tv, d, v_cache, kTileTc, 128))
+    return cudaErrorInvalidValue;
+  static DeviceSlots slots;
+  cudaError_t e = slots.raise_smem(dense_tc_kernel<C>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
+  e = launch_k(dense_tc_kernel<C>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  return launch_join<kDimTc, C::kRows, FP8>(a, s);
+}
+
+template <bool FP8>
+cudaError_t launch(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, cudaStream_t s) {
+  switch (rows) {
+    case 8: return launch<FP8, 8, 1>(d, a, k, v, s);
+    case 16: return launch<FP8, 16, 1>(d, a, k, v, s);
+    case 32: return launch<FP8, 32, 1>(d, a, k, v, s);
+    default: return launch<FP8, 32, 2>(d, a, k, v, s);
+  }
+}
+
+}  // namespace
+
+// Rows of a unit: a softmax thread's work grows with its warpgroup's rows, so
+// the smallest of 8, 16, 32 that holds them; a second warpgroup for up to 64;
+// more rows are several units, which each read K and V.
+int dense_tc_rows(const qsa_dims& d) {
+  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+cudaError_t launch_dense_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
+  const int rows = dense_tc_rows(d);
+  return d.kv_dtype == QSA_KV_FP8_E4M3 ? launch<true>(rows, d, a, k_cache, v_cache, s)
+                                       : launch<false>(rows, d, a, k_cache, v_cache, s);
+}
+
+}  // namespace qsa

@@ -59,12 +59,14 @@ def f64(t):
 
 def attention(q, k, v, scale, lo, hi):
     """q [H][D], k, v [T][H_kv][D] float64; positions lo .. hi - 1. Returns
-    (out [H][D], lse [H], sum of weight * |v| [H][D], largest sum of |q k| [H])."""
-    H, G = q.shape[0], q.shape[0] // k.shape[1]
-    out, mag = np.zeros_like(q), np.zeros_like(q)
+    (out [H][D], lse [H], sum of weight * |v| [H][D], largest sum of |q k| [H],
+    largest weight * sum of |v| [H][D])."""
+    H = q.shape[0]
+    out, mag, small = np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
     lse, qk = np.full(H, -np.inf), np.zeros(H)
     if hi <= lo:
-        return out, lse, mag, qk
+        return out, lse, mag, qk, small
+    G = H // k.shape[1]
     for h in range(H):
         kk, vv = k[lo:hi, h // G], v[lo:hi, h // G]
         s = kk @ q[h] * scale
@@ -72,9 +74,10 @@ def attention(q, k, v, scale, lo, hi):
         e = np.exp(s - m)
         p = e / e.sum()
         out[h], mag[h] = p @ vv, p @ np.abs(vv)
+        small[h] = p.max() * np.abs(vv).sum(0)
         lse[h] = m + math.log(e.sum())
         qk[h] = (np.abs(kk) @ np.abs(q[h])).max() * scale
-    return out, lse, mag, qk
+    return out, lse, mag, qk, small
 
 
 def page_table(tokens, page_size, seed, spare=1):

@@ -348,17 +348,25 @@ def test_gather_reports_and_skips(qsa):
 # --------------------------------------------------------------------------
 # dense attention
 # --------------------------------------------------------------------------
-def _attn_tol(ref, mag, lse, qk, D, kv):
+def _attn_tol(ref, mag, lse, qk, D, kv, small):
     """Output: half a BF16 step of the result; every weight is off by its own
-    rounding (2^-8 of it in BF16, 2^-11 in FP16), by the score's error as an
-    exponent, and by the exponential and the sums (2^-18 covers a few thousand
-    FP32 steps taken in trees); the score's error is that of an FP32 sum of D
-    products, at most 2^-23 of the sum of their magnitudes for each of about
-    D / 8 + 8 partial sums. lse: the score's error and a few FP32 steps."""
+    rounding, by the score's error as an exponent, and by the exponential and
+    the sums (2^-18 covers a few thousand FP32 steps taken in trees); the
+    score's error is that of an FP32 sum of D products, at most 2^-23 of the
+    sum of their magnitudes for each of about D / 8 + 8 partial sums. lse: the
+    score's error and a few FP32 steps.
+
+    The weights' rounding: 2^-8 in BF16, 2^-11 in FP16 (E4M3 cache, head dims
+    64 and 256). With an E4M3 cache and head dim 128 a weight p is hi + lo / 32,
+    two E4M3 codes: hi is off by at most 2^-4 p, and lo holds that rest to
+    2^-4 of it, so 2^-8 p in all; below the normal codes lo is off by up to
+    2^-10, that is 2^-15 after the division, where the row's largest weight is
+    at least 2^6: at most 2^-21 of the largest weight for every position."""
     eps_s = (D / 8 + 8) * 2.0 ** -23 * qk
-    w = (2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -18
+    w = (2.0 ** -11 if kv == "fp8" and D != 128 else 2.0 ** -8) + 2.0 ** -18
+    tiny = 2.0 ** -21 * small if kv == "fp8" and D == 128 else 0.0
     fin = np.where(np.isfinite(lse), np.abs(lse), 0.0)
-    return 2.0 ** -8 * np.abs(ref) + (w + 2 * eps_s)[..., None] * mag, eps_s + 2.0 ** -18 * (1 + fin)
+    return 2.0 ** -8 * np.abs(ref) + (w + 2 * eps_s)[..., None] * mag + tiny, eps_s + 2.0 ** -18 * (1 + fin)
 
 
 def _attn_case(qsa, ctx, n_q, hq, hk, D, ps, kv, window=0, q_pos=None, seed=41, mutate=None, sm_scale=0.0,
@@ -403,8 +411,8 @@ def _compare_attn(args, lse, window=0, bad_pages=None):
             if p < 0:
                 assert np.all(got[r, j] == 0) and np.all(got_lse[r, j] == -np.inf), (r, j)
                 continue
-            ref, rl, mag, qk = R.attention(q64[r, j], k, v, scale, lo, p + 1)
-            tol, tol_l = _attn_tol(ref, mag, rl, qk, d.head_dim, kv)
+            ref, rl, mag, qk, small = R.attention(q64[r, j], k, v, scale, lo, p + 1)
+            tol, tol_l = _attn_tol(ref, mag, rl, qk, d.head_dim, kv, small)
             err, err_l = np.abs(got[r, j] - ref), np.abs(got_lse[r, j] - rl)
             assert np.all(err <= tol), (r, j, err.max(), (err - tol).max())
             assert np.all(err_l <= tol_l), (r, j, err_l.max())
@@ -553,8 +561,8 @@ def test_attn_reports_and_skips(qsa):
         k, v = (R.rows(R.f64(c), table.numpy()[1], 100)[keep] for c in (kc, vc))
         for j in range(2):
             n = len(keep) - 1 + j
-            ref, rl, mag, qk = R.attention(R.f64(q[1, j]), k, v, 1 / math.sqrt(D), 0, n)
-            tol, tol_l = _attn_tol(ref, mag, rl, qk, D, "bf16")
+            ref, rl, mag, qk, small = R.attention(R.f64(q[1, j]), k, v, 1 / math.sqrt(D), 0, n)
+            tol, tol_l = _attn_tol(ref, mag, rl, qk, D, "bf16", small)
             assert np.all(np.abs(R.f64(out[1, j]) - ref) <= tol)
             assert np.all(np.abs(R.f64(lse[1, j]) - rl) <= tol_l)
     # a request whose pages are all bad has nothing to attend to
