@@ -72,6 +72,7 @@ struct Cfg {
   // positions of a tile, four warps' steps: 16 each, or 32 where rows are
   // short and the registers allow it
   static constexpr int kTile = kRowBytes <= 128 && D * MT <= 128 ? 128 : 64;
+  static constexpr int kTileShift = kTile == 128 ? 7 : 6;
   static constexpr int NS = kTile / (4 * kSlice);
   static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a TMA box's row
   static constexpr int kLines = kRowBytes / kLine;
@@ -186,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // ---- the copy warp ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     if (warp > kComputeWarps) return;
+    PageFeed<kTile> feed(a);
+    const int box_bytes = C::kLine << feed.box_shift, line_ops = feed.boxes * C::kLines;
     int stage = 0;
     uint32_t phase = 0;
     long long w = w0;
@@ -193,28 +196,24 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     while (w < w1 && ok) {
       const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
       const int g = at.x / a.row_blocks;
-      PageFeed<kTile> feed(a, at, n);
-      const int ops = feed.boxes * C::kLines * 2, my_box = lane % feed.boxes;
+      feed.start(a, at, n);
       for (int k = 0; k < n && ok; ++k) {
         const int page = feed.of_tile(a, at, k);
-        const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
+        const uint32_t bad = feed.bad_groups(page);  // (a box holds whole sub-slices)
         ok = __all_sync(kFull, wait(&empty_bar[stage], phase ^ 1u));
         if (!ok) break;
         const uint32_t bar = smem_u32(&full_bar[stage]);
         if (lane == 0) {
-          uint32_t bad = 0;
-#pragma unroll
-          for (int s = 0; s < kTile / kSlice; ++s)  // a box holds whole sub-slices
-            if ((bad_boxes >> (s * kSlice / feed.box)) & 1u) bad |= 1u << s;
           s_bad[stage] = bad;
           mbar_expect_tx(bar, C::kStage);
         }
         __syncwarp();
         const int slot = feed.slot_of(a, k);
         const uint32_t base = smem_u32(ring + stage * C::kStage);
-        for (int i = lane; i < ops; i += 32) {  // (32 is a multiple of boxes: i % boxes == my_box)
-          const int line = (i / feed.boxes) % C::kLines, v = i / (feed.boxes * C::kLines);
-          tma_load_4d(base + (uint32_t)(v * C::kHalf + line * (kTile * C::kLine) + my_box * feed.box * C::kLine),
+        for (int i = lane; i < 2 * line_ops; i += 32) {  // (32 is a multiple of boxes: lane i's box is my_box)
+          const bool v = i >= line_ops;
+          const int line = (v ? i - line_ops : i) >> (C::kTileShift - feed.box_shift);
+          tma_load_4d(base + (uint32_t)((v ? C::kHalf : 0) + line * (kTile * C::kLine) + feed.my_box * box_bytes),
                       v ? &tm_v : &tm_k, line * (C::kLine / (FP8 ? 1 : 2)), slot, g,
                       page < 0 ? a.num_pages : page /* outside: zeros */, bar);
         }
@@ -794,6 +793,7 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.n_kv_heads = d.n_kv_heads;
   a.group = d.n_q_heads / d.n_kv_heads;
   a.page_size = d.page_size;
+  while ((1 << a.page_shift) < d.page_size) ++a.page_shift;
   a.max_pages = d.max_pages;
   a.num_pages = d.num_pages;
   a.window = window;

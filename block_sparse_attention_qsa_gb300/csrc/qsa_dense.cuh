@@ -31,7 +31,7 @@ struct DenseArgs {
   float* parts;          // [grid][2] pieces: m[rows], l[rows], acc[rows][D]
   int32_t* err;
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
-  int page_size, max_pages, num_pages, window, grid;
+  int page_size, page_shift, max_pages, num_pages, window, grid;
   float sm_scale;
 };
 
@@ -243,36 +243,52 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS
 // The pages of a segment's boxes (box = the positions that one TMA copy takes,
 // all in one page), looked up by a whole warp 32 boxes ahead. A box that no
 // query sees has none (and is not looked up: its entry may mean nothing).
+// Everything is a power of two: the copy warp feeds the SM alone, and integer
+// divisions here were most of what a tile cost it.
 template <int TILE>
 struct PageFeed {
-  int cur, nxt, first_box, n_boxes, box, boxes;
+  int box_shift, boxes;  // log2 of a box's positions; boxes of a tile
+  int my_box;            // this lane's box of a tile (lane % boxes)
+  int cur, nxt, first_box, n_boxes;
+  __device__ __forceinline__ explicit PageFeed(const DenseArgs& a) {
+    constexpr int kTileShift = TILE == 128 ? 7 : 6;
+    static_assert(TILE == 1 << kTileShift, "tile");
+    box_shift = min(kTileShift, a.page_shift);
+    boxes = TILE >> box_shift;
+    my_box = (int)(threadIdx.x & 31) & (boxes - 1);
+  }
   __device__ __forceinline__ int page_of(const DenseArgs& a, const Place<TILE>& at, int i) const {
-    const long long p = (long long)(first_box + i) * box;
-    if (i >= n_boxes || p >= at.g.hi || p + box <= at.g.lo) return -1;
-    const int page = a.page_table[(size_t)at.r * a.max_pages + (int)(p / a.page_size)];
+    const unsigned p = (unsigned)(first_box + i) << box_shift;  // (a box that is seen starts below 2^31)
+    if (i >= n_boxes || p >= (unsigned)at.g.hi || p + (1u << box_shift) <= (unsigned)at.g.lo) return -1;
+    const int page = a.page_table[(size_t)at.r * a.max_pages + (p >> a.page_shift)];
     if ((unsigned)page < (unsigned)a.num_pages) return page;
     record_error(a.err, kErrPage, at.r, 0, page);
     return -1;
   }
-  __device__ __forceinline__ PageFeed(const DenseArgs& a, const Place<TILE>& at, int n_tiles) {
-    box = min(TILE, a.page_size);
-    boxes = TILE / box;
+  __device__ __forceinline__ void start(const DenseArgs& a, const Place<TILE>& at, int n_tiles) {
     first_box = (at.g.lo / TILE + at.t) * boxes;
     n_boxes = n_tiles * boxes;
     cur = page_of(a, at, threadIdx.x & 31);
     nxt = page_of(a, at, 32 + (threadIdx.x & 31));
   }
-  // page of this lane's box (lane % boxes) of the segment's tile k
+  // page of this lane's box of the segment's tile k
   __device__ __forceinline__ int of_tile(const DenseArgs& a, const Place<TILE>& at, int k) {
-    const int b0 = k * boxes, lane = threadIdx.x & 31;
+    const int b0 = k * boxes;
     if (b0 > 0 && (b0 & 31) == 0) {
       cur = nxt;
-      nxt = page_of(a, at, b0 + 32 + lane);
+      nxt = page_of(a, at, b0 + 32 + (int)(threadIdx.x & 31));
     }
-    return __shfl_sync(kFull, cur, (b0 & 31) + lane % boxes);
+    return __shfl_sync(kFull, cur, (b0 & 31) + my_box);
   }
+  // its first position's slot in the page
   __device__ __forceinline__ int slot_of(const DenseArgs& a, int k) const {
-    return (int)(((long long)(first_box + k * boxes + (threadIdx.x & 31) % boxes) * box) % a.page_size);
+    return (int)(((unsigned)(first_box + k * boxes + my_box) << box_shift) & (unsigned)(a.page_size - 1));
+  }
+  // bit i: positions 16 i .. 16 i + 15 of the tile have no page (this lane's box: `page`)
+  __device__ __forceinline__ uint32_t bad_groups(int page) const {
+    const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
+    const int group = (int)(threadIdx.x & 31) & (TILE / 16 - 1);
+    return __ballot_sync(kFull, (bad_boxes >> ((group * 16) >> box_shift)) & 1u) & ((1u << (TILE / 16)) - 1u);
   }
 };
 

@@ -67,7 +67,7 @@ struct Tc {
   static constexpr int kQ = N * kRowBytes;           // a warpgroup's Q
   static constexpr int kP = kTileTc * 64;            // a warpgroup's P: 64 bytes a position
   static constexpr int kFixed = 2 * WGS * (kQ + kP) + 1024;
-  static constexpr int kStatic = WGS == 1 ? 1792 : 3072;  // barriers and tables
+  static constexpr int kStatic = WGS == 1 ? (FP8 ? 2304 : 2048) : 4608;  // barriers and tables
   static constexpr int kFit = (kMaxSmem - kStatic - kFixed) / kSlot;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
   static constexpr int kSmem = kSlots * kSlot + kFixed;
@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   __shared__ int2 s_rng[2][C::kRows];   // [buffer][row]: positions the row sees, first and one past the last
   __shared__ int2 s_all[2];             // positions that all rows of the unit see
   __shared__ __align__(16) float s_scale[2][C::kRows];
+  __shared__ int s_out[2][C::kRows];    // [buffer][row]: its row of q and out, -1: none
   __shared__ float s_red[WGS][4][RC];
+  __shared__ __align__(16) float s_mu[WGS][RC];
   __shared__ uint32_t s_odd[WGS][4];    // positions whose V is not finite
   __shared__ uint32_t s_see[WGS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -286,6 +288,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
 
   if (warp == C::kCopyWarp) {
     // ---- copies: K then V of each tile ----
+    PageFeed<kTile> feed(a);
+    const int line = lane >> (7 - feed.box_shift);  // this lane's line of a K or V tile; at most 16 copies
+    const uint32_t dst = (uint32_t)(line * (kTile * 128) + (feed.my_box << feed.box_shift) * 128);
     int slot = 0;
     uint32_t phase = 0;
     long long w = w0;
@@ -294,34 +299,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     while (w < w1 && ok) {
       const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
       const int g = at.x / a.row_blocks;
-      PageFeed<kTile> feed(a, at, n);
-      const int ops = feed.boxes * C::kLines, my_box = lane % feed.boxes;
+      feed.start(a, at, n);
       for (int k = 0; k < n && ok; ++k, ++it) {
         const int page = feed.of_tile(a, at, k);
-        const uint32_t bad_boxes = __ballot_sync(kFull, page < 0);  // bit i (i < boxes): box i
-        const int first = feed.slot_of(a, k);
-#pragma unroll 1
-        for (int v = 0; v < 2 && ok; ++v) {
-          ok = __all_sync(kFull, wait(&slot_empty[slot], phase ^ 1u));
-          if (!ok) break;
+        const uint32_t bad = feed.bad_groups(page);
+        const int first = feed.slot_of(a, k), at_page = page < 0 ? a.num_pages : page /* outside: zeros */;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (!__all_sync(kFull, wait(&slot_empty[slot], phase ^ 1u))) {
+            ok = false;
+            break;
+          }
           const uint32_t bar = smem_u32(&slot_full[slot]);
           if (lane == 0) {
-            if (v == 0) {
-              uint32_t bad = 0;
-#pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                if ((bad_boxes >> (s * 16 / feed.box)) & 1u) bad |= 1u << s;
-              s_bad[it % kBadRing] = bad;
-            }
+            if (v == 0) s_bad[it % kBadRing] = bad;
             mbar_expect_tx(bar, C::kSlot);
           }
           __syncwarp();
-          const uint32_t base = smem_u32(ring + slot * C::kSlot);
-          if (lane < ops) {  // boxes * lines <= 16
-            const int line = lane / feed.boxes;
-            tma_load_4d(base + (uint32_t)(line * (kTile * 128) + my_box * feed.box * 128), v ? &tm_v : &tm_k,
-                        line * 64, first, g, page < 0 ? a.num_pages : page /* outside: zeros */, bar);
-          }
+          if (line < C::kLines)
+            tma_load_4d(smem_u32(ring + slot * C::kSlot) + dst, v ? &tm_v : &tm_k, line * 64, first, g, at_page, bar);
           if (++slot == C::kSlots) {
             slot = 0;
             phase ^= 1u;
@@ -459,11 +455,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       }
       if (t < RC) {
         int2 rg = make_int2(0, 0);
+        int o = -1;
         if (row_off + t < rows) {
-          const int p = a.q_pos[(size_t)u.r * a.n_q + (rb * C::kRows + row_off + t) / a.group];
+          const int i = rb * C::kRows + row_off + t, j = i / a.group, h = g * a.group + (i - j * a.group);
+          const int p = a.q_pos[(size_t)u.r * a.n_q + j];
           if (valid_pos(a, p)) rg = make_int2(low_of(a, p), p + 1);
+          o = (u.r * a.n_q + j) * a.n_q_heads + h;
         }
         s_rng[buf][row_off + t] = rg;
+        s_out[buf][row_off + t] = o;
       }
       if (tid == 0) {
         int2 all = make_int2(0, 0x7fffffff);
@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         next.next_unit(a);
         stage_q(next, buf ^ 1);
       }
+      if (t < RC) s_mu[wg][t] = kNoRef;
       if constexpr (WGS == 1)
         group_sync(1 + wg, 128);  // the tables of this unit
       else
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       const float sc = s_scale[buf][row_off];  // BF16: all rows' scale
 #pragma unroll
       for (int r = 0; r < RC; ++r) {
-        mu[r] = kNoRef;
+        mu[r] = 0.f;
         l[r] = 0.f;
       }
 
@@ -513,23 +514,29 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const bool edge = p0 < all.x || p0 + kTile > all.y || bad != 0;
         const bool paged = !((bad >> (t >> 4)) & 1u);
         float y[RC];
-        // scores (exp2 domain), -infinity where masked, less the reference
-        auto scores = [&](bool relative) {
-          uint32_t v[RC];
-          Tmem<RC>::load(s_addr, v);
-          if constexpr (FP8) {
-            uint32_t u[RC];
-            Tmem<RC>::load(s_addr + 32, u);
-            tc_wait_ld();
+        // Scores (exp2 domain) less the reference. Where the reference has to
+        // move, and in a unit's first tile, they are taken as they are first
+        // (mu = 0), for the rows' maxima; then again. (One copy of the code:
+        // what runs once a unit runs from a cold instruction cache, where its
+        // length is its cost.)
+        bool raw = k == 0, moved = false;
+        while (true) {
+          {
+            uint32_t v[RC];
+            Tmem<RC>::load(s_addr, v);
+            if constexpr (FP8) {
+              uint32_t u[RC];
+              Tmem<RC>::load(s_addr + 32, u);
+              tc_wait_ld();
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
-              const float s = fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r]));
-              y[r] = fmaf(s, s_scale[buf][row_off + r], relative ? -mu[r] : 0.f);
+              for (int r = 0; r < RC; ++r)
+                y[r] = fmaf(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r])), s_scale[buf][row_off + r],
+                            -mu[r]);
+            } else {
+              tc_wait_ld();
+#pragma unroll
+              for (int r = 0; r < RC; ++r) y[r] = fmaf(__uint_as_float(v[r]), sc, -mu[r]);
             }
-          } else {
-            tc_wait_ld();
-#pragma unroll
-            for (int r = 0; r < RC; ++r) y[r] = fmaf(__uint_as_float(v[r]), sc, relative ? -mu[r] : 0.f);
           }
           if (edge) {
 #pragma unroll
@@ -538,52 +545,52 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
               if (p < rg.x || p >= rg.y || !paged) y[r] = kNegInf;
             }
           }
-        };
-        scores(true);
-        bool grew = false;
+          if (moved) break;
+          if (!raw) {
+            bool grew = false;
 #pragma unroll
-        for (int r = 0; r < RC; ++r) grew |= y[r] > kRefMost;
-        if (group_any(1 + wg, 128, grew)) {
-          scores(false);
+            for (int r = 0; r < RC; ++r) grew |= y[r] > kRefMost;
+            if (!group_any(1 + wg, 128, grew)) break;
+            raw = true;
+#pragma unroll
+            for (int r = 0; r < RC; ++r) mu[r] = 0.f;
+            continue;
+          }
           {
-            float v[RC];
-#pragma unroll
-            for (int r = 0; r < RC; ++r) v[r] = y[r];
-            const float x = reduce_rows<RC>(v, [](float c, float d) { return fmaxf(c, d); });
+            const float x = reduce_rows<RC>(y, [](float c, float d) { return fmaxf(c, d); });
             if (lane < RC) s_red[wg][quarter][lane] = x;
           }
           group_sync(1 + wg, 128);
-          if (k > 0) wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
-          __syncwarp();
-          tc_after();
-          uint32_t o[RC];
-          float f[RC];
-          if (k > 0) {
-            Tmem<RC>::load(o_addr, o);
-            tc_wait_ld();
+          if (t < RC) {
+            const float top = fmaxf(fmaxf(s_red[wg][0][t], s_red[wg][1][t]), fmaxf(s_red[wg][2][t], s_red[wg][3][t]));
+            const float from = s_mu[wg][t];
+            const float to =
+                top > from + kRefMost || from == kNoRef ? fmaxf(top - kRefBelow, kNoRef) : from;
+            s_red[wg][0][t] = exp2_sfu(from - to);  // the row's factor
+            s_mu[wg][t] = to;
           }
+          group_sync(1 + wg, 128);
 #pragma unroll
           for (int r = 0; r < RC; ++r) {
-            const float top = fmaxf(fmaxf(s_red[wg][0][r], s_red[wg][1][r]), fmaxf(s_red[wg][2][r], s_red[wg][3][r]));
-            const float to = top > mu[r] + kRefMost || mu[r] == kNoRef ? fmaxf(top - kRefBelow, kNoRef) : mu[r];
-            f[r] = exp2_sfu(mu[r] - to);
-            mu[r] = to;
-            l[r] *= f[r];
-            y[r] -= to;
+            mu[r] = s_mu[wg][r];
+            l[r] *= s_red[wg][0][r];
           }
-          if (k > 0) {
-#pragma unroll
-            for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
-            Tmem<RC>::store(o_addr, o);
-            if constexpr (FP8) {
-              Tmem<RC>::load(o_addr + 32, o);
+          if (k > 0) {  // what O holds so far
+            wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
+            __syncwarp();
+            tc_after();
+#pragma unroll 1
+            for (int term = 0; term < (FP8 ? 2 : 1); ++term) {
+              uint32_t o[RC];
+              Tmem<RC>::load(o_addr + 32 * term, o);
               tc_wait_ld();
 #pragma unroll
-              for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
-              Tmem<RC>::store(o_addr + 32, o);
+              for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s_red[wg][0][r]);
+              Tmem<RC>::store(o_addr + 32 * term, o);
             }
             tc_wait_st();
           }
+          moved = true;
         }
 #pragma unroll
         for (int r = 0; r < RC; ++r) {
@@ -707,8 +714,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       }
 
       // ---- the segment's end: component t of every row ----
-      const int g = at.x / a.row_blocks, rb = at.x - g * a.row_blocks;
-      const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
+      const int g = at.x / a.row_blocks;
       const bool whole = n == at.tiles;
       const int pslot = w == w0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
       if (tid == 0 && at.t == 0)
@@ -716,12 +722,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.of_tile(w + at.tiles - 1), pslot);
       {
         const float x = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
-        group_sync(1 + wg, 128);  // (s_red's last readers are done)
         if (lane < RC) s_red[wg][quarter][lane] = x;
       }
       wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
       __syncwarp();
       tc_after();
+      group_sync(1 + wg, 128);
+      float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
+      if (t < RC) {  // a row's sum, its factor, and lse
+        const float sum = (s_red[wg][0][t] + s_red[wg][1][t]) + (s_red[wg][2][t] + s_red[wg][3][t]);
+        const float ref = s_mu[wg][t];
+        const int orow = s_out[buf][row_off + t];
+        if (!whole) {
+          piece[row_off + t] = ref == kNoRef ? kNegInf : ref;
+          piece[C::kRows + row_off + t] = sum;
+        } else {
+          s_red[wg][0][t] = sum == 0.f ? 0.f : (FP8 ? a.v_scale[g] : 1.f) / sum;
+          if (a.lse && orow >= 0) a.lse[orow] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+        }
+      }
       uint32_t o[RC];
       Tmem<RC>::load(o_addr, o);
       if constexpr (FP8) {
@@ -734,31 +753,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       } else {
         tc_wait_ld();
       }
-      group_sync(1 + wg, 128);
-      const float vscale = FP8 ? a.v_scale[g] : 1.f;
-      float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
-      const int i0 = rb * C::kRows + row_off;
-      int j = i0 / a.group, hh = i0 - j * a.group;
+      if (!whole) {
+        float* dst = piece + 2 * C::kRows + row_off * D + t;
 #pragma unroll
-      for (int r = 0; r < RC; ++r) {
-        if (row_off + r < rows) {
-          const float sum = (s_red[wg][0][r] + s_red[wg][1][r]) + (s_red[wg][2][r] + s_red[wg][3][r]);
-          const float acc = __uint_as_float(o[r]);
-          if (whole) {
-            const size_t orow = ((size_t)at.r * a.n_q + j) * a.n_q_heads + g * a.group + hh;
-            a.out[orow * D + t] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum * vscale);
-            if (a.lse && t == 0) a.lse[orow] = sum == 0.f ? kNegInf : (mu[r] + log2f(sum)) * kLn2;
-          } else {
-            piece[2 * C::kRows + (row_off + r) * D + t] = acc;
-            if (t == 0) {
-              piece[row_off + r] = mu[r] == kNoRef ? kNegInf : mu[r];
-              piece[C::kRows + row_off + r] = sum;
-            }
-          }
-        }
-        if (++hh == a.group) {
-          hh = 0;
-          ++j;
+        for (int r = 0; r < RC; ++r) dst[r * D] = __uint_as_float(o[r]);  // (rows that are none: never read)
+      } else {
+        group_sync(1 + wg, 128);
+#pragma unroll
+        for (int r = 0; r < RC; ++r) {
+          const int orow = s_out[buf][row_off + r];
+          // a row that sees nothing (factor 0) is zero whatever O holds
+          const float f = s_red[wg][0][r];
+          if (orow >= 0) a.out[(size_t)orow * D + t] = __float2bfloat16_rn(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
         }
       }
       tc_before();
