@@ -33,10 +33,12 @@
 // the row's first maximum and moves when a score passes mu + 8, which after a
 // row's first tiles hardly happens. Moving it rescales O in tensor memory.
 //
-// Roles: a copy warp (pages, TMA: K and V tiles in a ring of slots), an MMA
-// warp (S of tile i, then PV of tile i - 1), and one warpgroup of softmax per
-// 32 rows. S and P are double-buffered, so the tensor cores and the copies
-// run ahead of the softmax.
+// Roles: a copy warp (pages, TMA: K and V tiles in a ring of slots), a warp
+// that issues the MMAs of S and one for those of PV (issuing a tile's takes
+// each 500 to 700 cycles, about half of the time that HBM takes for an E4M3
+// tile; one warp for both was the loop's bound), and one or two warpgroups of
+// softmax. S and P are double-buffered, so the tensor cores and the copies run
+// ahead of the softmax.
 //
 // Masks: as in qsa_dense.cu. A tile in which a row does not see every position
 // is an edge tile; there the thread that owns a position that no row sees
@@ -54,27 +56,28 @@ constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
 constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing: any score passes it
 constexpr int kBadRing = 16;      // page marks of the tiles in flight (at most 6)
 
-// RC: rows of a warpgroup (8, 16 or 32), WGS: softmax warpgroups
+// RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax warpgroups, BLK:
+// blocks of up to 32 rows, each one set of MMA columns
 template <bool FP8_, int RC_, int WGS_>
 struct Tc {
   static constexpr bool FP8 = FP8_;
   static constexpr int RC = RC_, WGS = WGS_;
-  static constexpr int kRows = RC * WGS;
+  static constexpr int kRows = RC * WGS, BLK = kRows > 32 ? kRows / 32 : 1;
   static constexpr int kRowBytes = kDimTc * (FP8 ? 1 : 2);
   static constexpr int kLines = kRowBytes / 128;
   static constexpr int kSlot = kTileTc * kRowBytes;  // K or V of a tile
-  static constexpr int N = FP8 ? 64 : 32;            // MMA columns of a warpgroup (those past its rows idle)
-  static constexpr int kQ = N * kRowBytes;           // a warpgroup's Q
-  static constexpr int kP = kTileTc * 64;            // a warpgroup's P: 64 bytes a position
-  static constexpr int kFixed = 2 * WGS * (kQ + kP) + 1024;
-  static constexpr int kStatic = WGS == 1 ? (FP8 ? 2304 : 2048) : 4608;  // barriers and tables
+  static constexpr int N = FP8 ? 64 : 32;            // MMA columns of a block (those past its rows idle)
+  static constexpr int kQ = N * kRowBytes;           // a block's Q
+  static constexpr int kP = kTileTc * 64;            // a block's P: 64 bytes a position
+  static constexpr int kFixed = 2 * BLK * (kQ + kP) + 1024;
+  static constexpr int kStatic = BLK == 1 ? (FP8 ? 2304 : 2048) : 4608;  // barriers and tables
   static constexpr int kFit = (kMaxSmem - kStatic - kFixed) / kSlot;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
   static constexpr int kSmem = kSlots * kSlot + kFixed;
-  static constexpr int kThreads = 128 * WGS + 64;
-  static constexpr int kCopyWarp = 4 * WGS, kMmaWarp = kCopyWarp + 1;
-  static constexpr uint32_t kO = 2 * WGS * N;        // TMEM: two S buffers, then O
-  static constexpr uint32_t kNeed = 3 * WGS * N;
+  static constexpr int kThreads = 128 * WGS + 96;
+  static constexpr int kCopyWarp = 4 * WGS, kSWarp = kCopyWarp + 1, kPvWarp = kCopyWarp + 2;
+  static constexpr uint32_t kO = 2 * BLK * N;        // TMEM: two S buffers, then O
+  static constexpr uint32_t kNeed = 3 * BLK * N;
   static constexpr uint32_t kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static constexpr int kPieceFloats = kRows * (kDimTc + 2);
   static_assert(kSlots >= 4 && kSlots / 2 + 2 < kBadRing, "ring");
@@ -230,11 +233,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap tm_v,
                                                                   const DenseArgs a) {
   constexpr bool FP8 = C::FP8;
-  constexpr int RC = C::RC, WGS = C::WGS, N = C::N, kTile = kTileTc, D = kDimTc;
+  constexpr int RC = C::RC, WGS = C::WGS, BLK = C::BLK, N = C::N, kTile = kTileTc, D = kDimTc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_q = ring + C::kSlots * C::kSlot;   // [buffer][warpgroup]
-  uint8_t* s_p = s_q + 2 * WGS * C::kQ;         // [buffer][warpgroup]
+  uint8_t* s_q = ring + C::kSlots * C::kSlot;   // [buffer][block]
+  uint8_t* s_p = s_q + 2 * BLK * C::kQ;         // [buffer][block]
   __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], fin;
   __shared__ uint32_t s_tmem;
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   __shared__ StartSmem<C::kThreads> s_start;
   __shared__ int2 s_rng[2][C::kRows];   // [buffer][row]: positions the row sees, first and one past the last
   __shared__ int2 s_all[2];             // positions that all rows of the unit see
-  __shared__ __align__(16) float s_scale[2][C::kRows];
+  __shared__ __align__(16) float s_scale[2][FP8 ? C::kRows : 1];  // softmax scale of a row (BF16: of all)
   __shared__ int s_out[2][C::kRows];    // [buffer][row]: its row of q and out, -1: none
   __shared__ float s_red[WGS][4][RC];
   __shared__ __align__(16) float s_mu[WGS][RC];
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       mbar_init(smem_u32(&pv_done[b]), 1);
       mbar_init(smem_u32(&q_full[b]), 128 * WGS);
     }
-    mbar_init(smem_u32(&fin), 1);
+    mbar_init(smem_u32(&fin), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();     // positions, queries and the cache may come from the kernel before
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   Place<kTile> at;
   if (!find_start<kTile, C::kThreads>(a, s_start, sp, w0, w1, at)) return;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
-  if (warp == C::kMmaWarp) {
+  if (warp == C::kPvWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(C::kTmem)
                  : "memory");
@@ -335,73 +338,83 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         }
       }
     }
-  } else if (warp == C::kMmaWarp) {
-    // ---- MMAs: S of tile i, then PV of tile i - 1 ----
+  } else if (warp == C::kSWarp) {
+    // ---- S^T = K Q^T ----
     if (lane == 0) {
-      constexpr uint32_t kS = mma_desc<C>(false), kPv = mma_desc<C>(true);
-      // k steps (32 bytes of a row, 16 or 32 positions) of the two products
-      constexpr int kSteps = C::kRowBytes / 32, kPvSteps = kTile / (FP8 ? 32 : 16);
+      constexpr uint32_t kIdesc = mma_desc<C>(false);
+      constexpr int kSteps = C::kRowBytes / 32;  // 32 bytes of a row each
       int it = 0, seg = 0;
-      bool ok = true, pv_first = true, first = true;
-      auto pv = [&](int i, bool unit_first) -> bool {  // PV of tile i
-        const int vs = (2 * i + 1) % C::kSlots;
-        if (!wait(&p_full[i & 1], (uint32_t)(i >> 1) & 1u)) return false;
-        if (!wait(&slot_full[vs], (uint32_t)((2 * i + 1) / C::kSlots) & 1u)) return false;
-        tc_after();
-        const bool fresh = unit_first && *reinterpret_cast<volatile int*>(&s_keep) == 0;
-        const uint32_t v0 = smem_u32(ring + vs * C::kSlot);
-#pragma unroll
-        for (int g = 0; g < WGS; ++g) {
-          const uint32_t p0 = smem_u32(s_p + ((i & 1) * WGS + g) * C::kP);
-#pragma unroll
-          for (int ks = 0; ks < kPvSteps; ++ks) {
-            // A: positions as k, 128-byte rows, the second 64 components one line further on
-            const uint64_t da = smem_desc(v0 + (uint32_t)(ks * (kTile / kPvSteps) * 128), kTile * 128, 1024, 2);
-            // B: positions as k, 64-byte rows
-            const uint64_t db = smem_desc(p0 + (uint32_t)(ks * (kTile / kPvSteps) * 64), 512, 512, 4);
-            mma_tc<FP8>(tmem + C::kO + (uint32_t)(g * N), da, db, kPv, !(fresh && ks == 0));
-          }
-        }
-        commit_tc(&slot_empty[vs]);
-        commit_tc(&pv_done[i & 1]);
-        return true;
-      };
+      bool ok = true;
       long long w = w0;
       while (w < w1 && ok) {
         const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
         ok = wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u);
         for (int k = 0; k < n && ok; ++k, ++it) {
-          const int kslot = (2 * it) % C::kSlots;
-          ok = wait(&slot_full[kslot], (uint32_t)((2 * it) / C::kSlots) & 1u);
+          const int slot = (2 * it) % C::kSlots;
+          ok = wait(&slot_full[slot], (uint32_t)((2 * it) / C::kSlots) & 1u) &&
+               (it < 2 || wait(&p_full[it & 1], (uint32_t)((it - 2) >> 1) & 1u));  // its S has been read
           if (!ok) break;
           tc_after();
-          const uint32_t k0 = smem_u32(ring + kslot * C::kSlot);
+          const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 1024, 2);
 #pragma unroll
-          for (int g = 0; g < WGS; ++g) {
-            const uint32_t q0 = smem_u32(s_q + ((seg & 1) * WGS + g) * C::kQ);
+          for (int b = 0; b < BLK; ++b) {
+            const uint64_t dq = smem_desc(smem_u32(s_q + ((seg & 1) * BLK + b) * C::kQ), 16, 1024, 2);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-              const uint32_t line = (uint32_t)(ks >> 2), step = (uint32_t)(ks & 3) * 32u;
-              mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * WGS + g) * N),
-                          smem_desc(k0 + line * (kTile * 128) + step, 16, 1024, 2),
-                          smem_desc(q0 + line * (N * 128) + step, 16, 1024, 2), kS, ks > 0);
+              // (addresses are in units of 16 bytes; a line is 64 BF16 components or all E4M3 ones)
+              const uint32_t line = (uint32_t)(ks >> 2), step = (uint32_t)(ks & 3) * 2u;
+              mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * BLK + b) * N), dk + (line * (kTile * 8) + step),
+                          dq + (line * (N * 8) + step), kIdesc, ks > 0);
             }
           }
-          commit_tc(&slot_empty[kslot]);
           commit_tc(&s_full[it & 1]);
-          if (it > 0) ok = pv(it - 1, pv_first);
-          pv_first = k == 0;
-          first = false;
+          commit_tc(&slot_empty[slot]);
         }
         w += n;
         ++seg;
         if (w < w1) at.next_unit(a);
       }
-      if (ok && !first) ok = pv(it - 1, pv_first);
+      commit_tc(&fin);
+    }
+    __syncwarp();
+  } else if (warp == C::kPvWarp) {
+    // ---- O^T += V^T P^T ----
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = mma_desc<C>(true);
+      constexpr int kSteps = kTile / (FP8 ? 32 : 16), kPos = kTile / kSteps;  // positions of an MMA
+      int it = 0;
+      bool ok = true;
+      long long w = w0;
+      while (w < w1 && ok) {
+        const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+        for (int k = 0; k < n && ok; ++k, ++it) {
+          const int slot = (2 * it + 1) % C::kSlots;
+          ok = wait(&p_full[it & 1], (uint32_t)(it >> 1) & 1u) &&
+               wait(&slot_full[slot], (uint32_t)((2 * it + 1) / C::kSlots) & 1u);
+          if (!ok) break;
+          tc_after();
+          const bool fresh = k == 0 && *reinterpret_cast<volatile int*>(&s_keep) == 0;
+          // A: positions as k, 128-byte rows, the second 64 BF16 components one line further on
+          const uint64_t dv = smem_desc(smem_u32(ring + slot * C::kSlot), kTile * 128, 1024, 2);
+#pragma unroll
+          for (int b = 0; b < BLK; ++b) {
+            // B: positions as k, 64-byte rows
+            const uint64_t dp = smem_desc(smem_u32(s_p + ((it & 1) * BLK + b) * C::kP), 512, 512, 4);
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks)
+              mma_tc<FP8>(tmem + C::kO + (uint32_t)(b * N), dv + (uint32_t)(ks * kPos * 8),
+                          dp + (uint32_t)(ks * kPos * 4), kIdesc, !(fresh && ks == 0));
+          }
+          commit_tc(&pv_done[it & 1]);
+          commit_tc(&slot_empty[slot]);
+        }
+        w += n;
+        if (w < w1) at.next_unit(a);
+      }
       // the tensor cores are done before the CTA gives its memory back
       commit_tc(&fin);
       const long long start = clock64();
-      while (!mbar_try_wait(smem_u32(&fin), 0) && clock64() - start < kWaitCycles) {
+      while (!mbar_try_wait(smem_u32(&fin), 0) && clock64() - start < 2 * kWaitCycles) {
       }
     }
     __syncwarp();
@@ -409,15 +422,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     // ---- softmax ----
     const int wg = warp >> 2, quarter = warp & 3, t = tid & 127;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(wg * N);
-    const int row_off = wg * RC;
+    // the warpgroup's rows: row_off .. + RC - 1 of the unit, columns col .. of block blk
+    const int row_off = wg * RC, blk = row_off / 32, col = row_off % 32;
+    const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(blk * N + col);
 
     // the rows of the unit at `u` into Q buffer `buf`, with what is known of them
     auto stage_q = [&](const Place<kTile>& u, int buf) {
       const int g = u.x / a.row_blocks, rb = u.x - g * a.row_blocks;
       const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
       const float base_scale = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
-      uint8_t* dst = s_q + (buf * WGS + wg) * C::kQ;
+      uint8_t* dst = s_q + (buf * BLK + blk) * C::kQ + col * 128;
 #pragma unroll
       for (int z = 0; z < RC / 8; ++z) {
         const int r = (t >> 4) + 8 * z, c = t & 15;  // 16 lanes a row, 8 components each
@@ -450,7 +464,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           if (c == 0) s_scale[buf][row_off + r] = base_scale * pow2(sh);
         } else {
           *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-          if (c == 0) s_scale[buf][row_off + r] = base_scale;
+          if (tid == 0) s_scale[buf][0] = base_scale;
         }
       }
       if (t < RC) {
@@ -496,7 +510,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         group_sync(3, 128 * WGS);
       const int2 all = s_all[buf];
       float mu[RC], l[RC];
-      const float sc = s_scale[buf][row_off];  // BF16: all rows' scale
+      const float sc = FP8 ? 0.f : s_scale[buf][0];
 #pragma unroll
       for (int r = 0; r < RC; ++r) {
         mu[r] = 0.f;
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         (void)ok;  // given up: the loop runs on without meaning, to the same barriers
         __syncwarp();
         tc_after();
-        const uint32_t s_addr = tmem + lane_base + (uint32_t)(((it & 1) * WGS + wg) * N);
+        const uint32_t s_addr = tmem + lane_base + (uint32_t)(((it & 1) * BLK + blk) * N + col);
         const int p0 = (at.g.lo / kTile + at.t + k) * kTile, p = p0 + t;
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&s_bad[it % kBadRing]);
         const bool edge = p0 < all.x || p0 + kTile > all.y || bad != 0;
@@ -683,7 +697,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         }
         // P of the tile before last has been read
         if (it >= 2) wait(&pv_done[it & 1], (uint32_t)((it - 2) >> 1) & 1u);
-        uint8_t* prow = s_p + ((it & 1) * WGS + wg) * C::kP + t * 64;
+        uint8_t* prow = s_p + ((it & 1) * BLK + blk) * C::kP + t * 64;
         const int x4 = (t >> 1) & 3;
         if constexpr (FP8) {
           uint32_t hi[RC / 2], lo[RC / 2];
@@ -693,18 +707,27 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             const float2 f = h2_to_f2(e4m3x2_to_h2(hi[r / 2]));
             lo[r / 2] = e4m3x2((y[r] - f.x) * 32.f, (y[r + 1] - f.y) * 32.f);
           }
+          const int c0 = col / 16;  // a 16-byte chunk has 16 rows: hi in chunks 0 and 1, lo in 2 and 3
+          if constexpr (RC == 8) {
+            *reinterpret_cast<uint2*>(prow + ((c0 ^ x4) << 4)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(prow + (((2 + c0) ^ x4) << 4)) =
+                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          } else {
 #pragma unroll
-          for (int c = 0; c < RC / 8; ++c) {  // 8 rows at a time: half a chunk
-            const int off = (c & 1) * 8;
-            *reinterpret_cast<uint2*>(prow + (((c >> 1) ^ x4) << 4) + off) =
-                make_uint2(hi[4 * c] | (hi[4 * c + 1] << 16), hi[4 * c + 2] | (hi[4 * c + 3] << 16));
-            *reinterpret_cast<uint2*>(prow + (((2 + (c >> 1)) ^ x4) << 4) + off) =
-                make_uint2(lo[4 * c] | (lo[4 * c + 1] << 16), lo[4 * c + 2] | (lo[4 * c + 3] << 16));
+            for (int c = 0; c < RC / 16; ++c) {
+              const uint32_t* h = hi + 8 * c;
+              const uint32_t* g = lo + 8 * c;
+              *reinterpret_cast<uint4*>(prow + (((c0 + c) ^ x4) << 4)) = make_uint4(
+                  h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+              *reinterpret_cast<uint4*>(prow + (((2 + c0 + c) ^ x4) << 4)) = make_uint4(
+                  g[0] | (g[1] << 16), g[2] | (g[3] << 16), g[4] | (g[5] << 16), g[6] | (g[7] << 16));
+            }
           }
         } else {
+          const int c0 = col / 8;
 #pragma unroll
           for (int c = 0; c < RC / 8; ++c)
-            *reinterpret_cast<uint4*>(prow + ((c ^ x4) << 4)) =
+            *reinterpret_cast<uint4*>(prow + (((c0 + c) ^ x4) << 4)) =
                 make_uint4(pack_bf(y[8 * c], y[8 * c + 1]), pack_bf(y[8 * c + 2], y[8 * c + 3]),
                            pack_bf(y[8 * c + 4], y[8 * c + 5]), pack_bf(y[8 * c + 6], y[8 * c + 7]));
         }
@@ -776,7 +799,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == C::kMmaWarp)
+  if (warp == C::kPvWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
 }
 
@@ -800,7 +823,7 @@ cudaError_t launch(int rows, const qsa_dims& d, const DenseArgs& a, const void* 
   switch (rows) {
     case 8: return launch<FP8, 8, 1>(d, a, k, v, s);
     case 16: return launch<FP8, 16, 1>(d, a, k, v, s);
-    case 32: return launch<FP8, 32, 1>(d, a, k, v, s);
+    case 32: return launch<FP8, 16, 2>(d, a, k, v, s);
     default: return launch<FP8, 32, 2>(d, a, k, v, s);
   }
 }
@@ -808,8 +831,8 @@ cudaError_t launch(int rows, const qsa_dims& d, const DenseArgs& a, const void* 
 }  // namespace
 
 // Rows of a unit: a softmax thread's work grows with its warpgroup's rows, so
-// the smallest of 8, 16, 32 that holds them; a second warpgroup for up to 64;
-// more rows are several units, which each read K and V.
+// the smallest of 8, 16, 32 (two warpgroups of 16) and 64 (two of 32) that
+// holds them; more rows are several units, which each read K and V.
 int dense_tc_rows(const qsa_dims& d) {
   const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
