@@ -56,6 +56,12 @@ __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turns) {
   return make_float2(c, s);
 }
 
+__device__ __forceinline__ void rotate(float& xa, float& xb, float2 cs) {
+  const float a = xa, b = xb;
+  xa = a * cs.x - b * cs.y;
+  xb = b * cs.x + a * cs.y;
+}
+
 template <int W>
 struct Vec;
 template <>
@@ -95,11 +101,14 @@ constexpr int kItems = 256;
 
 template <int W, int TOK>
 __global__ void __launch_bounds__(kItems) token_kernel(const TokenArgs a) {
-  __shared__ float2 s_cs[TOK][kMaxHalf];
+  // (cos, sin) of a token's pairs. W = 8: the 16-byte unit of pairs 8 i + 2 u,
+  // 8 i + 2 u + 1 is at [u][i], so that items i = 0, 1, .. of a warp read
+  // consecutive units; W = 1: in order
+  __shared__ __align__(16) float2 s_cs[TOK][kMaxHalf];
   __shared__ long long s_row[TOK];  // cache row of KV head 0; -1: K and V are not written
   __shared__ int s_live[TOK];       // the token is there and in order
   const int tid = threadIdx.x;
-  const long long tok0 = (long long)blockIdx.x * TOK;
+  const long long tok0 = (long long)blockIdx.x * TOK;  // (below 2^31)
   const int half = a.rope.rot_dim >> 1;
   const int per_head = a.head_dim / (2 * W);  // items of a head
   const int item = blockIdx.y * kItems + tid;
@@ -114,15 +123,22 @@ __global__ void __launch_bounds__(kItems) token_kernel(const TokenArgs a) {
   const int o0 = split ? i * W : i * 2 * W, o1 = split ? half + i * W : o0 + W;
   const Strided& in = seg == 0 ? a.q : seg == 1 ? a.k : a.v;
 
+  // (request, token) of the block's first token; the others follow by counting
+  const int rb = (int)((unsigned)tok0 / (unsigned)a.n_tok), jb = (int)tok0 - rb * a.n_tok;
   Vec<W> x0[TOK], x1[TOK];
+  {
+    int r = rb, j = jb;
 #pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    const long long tok = tok0 + t;
-    if (mine && tok < a.tokens) {
-      const long long r = tok / a.n_tok, j = tok - r * a.n_tok;
-      const __nv_bfloat16* p = in.p + r * in.batch + j * in.token + g * in.head;
-      x0[t].load(p + o0);
-      x1[t].load(p + o1);
+    for (int t = 0; t < TOK; ++t) {
+      if (mine && tok0 + t < a.tokens) {
+        const __nv_bfloat16* p = in.p + r * in.batch + j * in.token + g * in.head;
+        x0[t].load(p + o0);
+        x1[t].load(p + o1);
+      }
+      if (++j == a.n_tok) {
+        j = 0;
+        ++r;
+      }
     }
   }
   // the tokens' checks and cache rows
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(kItems) token_kernel(const TokenArgs a) {
       const int p = a.pos[tok];
       live = p >= 0;
       if (a.hk > 0 && p != -1) {
-        const int r = (int)(tok / a.n_tok), j = (int)(tok - (long long)r * a.n_tok);
+        const int r = (int)((unsigned)tok / (unsigned)a.n_tok), j = (int)tok - r * a.n_tok;
         const bool report = blockIdx.y == 0;
         if (p < 0 || p >= a.max_pages * a.page_size) {
           live = 0;
@@ -158,43 +174,48 @@ __global__ void __launch_bounds__(kItems) token_kernel(const TokenArgs a) {
     const int t = e / half, f = e - t * half;
     if (tok0 + t < a.tokens) {
       const float2 cs = cos_sin(a.pos[tok0 + t], a.rope.turns[f]);
-      s_cs[t][f] = make_float2(cs.x * a.rope.amplitude, cs.y * a.rope.amplitude * a.sign);
+      const int at = W == 1 ? f : (((f >> 1) & 3) * (half >> 3) + (f >> 3)) * 2 + (f & 1);
+      s_cs[t][at] = make_float2(cs.x * a.rope.amplitude, cs.y * a.rope.amplitude * a.sign);
     }
   }
   __syncthreads();
   if (!mine) return;
 
   const float scale = seg == 0 || !a.fp8 ? 1.f : seg == 1 ? a.k_scale[g] : a.v_scale[g];
+  int rn = rb, jn = jb;
 #pragma unroll
   for (int t = 0; t < TOK; ++t) {
-    const long long tok = tok0 + t;
-    if (tok >= a.tokens || !s_live[t]) continue;
+    const int r = rn, j = jn;
+    if (++jn == a.n_tok) {
+      jn = 0;
+      ++rn;
+    }
+    if (tok0 + t >= a.tokens || !s_live[t]) continue;
     float f0[W], f1[W];
     x0[t].get(f0);
     x1[t].get(f1);
     if (turn) {
-      if (W > 1 && a.rope.interleaved) {
-#pragma unroll
-        for (int e = 0; e + 1 < W; e += 2) {
-          const float2 u = s_cs[t][i * W + e / 2], w = s_cs[t][i * W + W / 2 + e / 2];
-          const float a0 = f0[e], b0 = f0[e + 1], a1 = f1[e], b1 = f1[e + 1];
-          f0[e] = a0 * u.x - b0 * u.y;
-          f0[e + 1] = b0 * u.x + a0 * u.y;
-          f1[e] = a1 * w.x - b1 * w.y;
-          f1[e + 1] = b1 * w.x + a1 * w.y;
-        }
+      if constexpr (W == 1) {
+        rotate(f0[0], f1[0], s_cs[t][i]);
       } else {
+        const float4* cs = reinterpret_cast<const float4*>(s_cs[t]) + i;
+        const int step = half >> 3;
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float2 u = s_cs[t][i * W + e];
-          const float xa = f0[e], xb = f1[e];
-          f0[e] = xa * u.x - xb * u.y;
-          f1[e] = xb * u.x + xa * u.y;
+        for (int u = 0; u < 4; ++u) {
+          const float4 w = cs[u * step];
+          const float2 c0 = make_float2(w.x, w.y), c1 = make_float2(w.z, w.w);
+          if (a.rope.interleaved) {  // pairs 8 i + 2 u, + 1: adjacent components of the first or second vector
+            float(&f)[W] = u < 2 ? f0 : f1;
+            rotate(f[4 * u % W], f[4 * u % W + 1], c0);
+            rotate(f[4 * u % W + 2], f[4 * u % W + 3], c1);
+          } else {
+            rotate(f0[2 * u], f1[2 * u], c0);
+            rotate(f0[2 * u + 1], f1[2 * u + 1], c1);
+          }
         }
       }
     }
     if (seg == 0) {
-      const long long r = tok / a.n_tok, j = tok - r * a.n_tok;
       __nv_bfloat16* p = a.q_out.p + r * a.q_out.batch + j * a.q_out.token + g * a.q_out.head;
       Vec<W>::store_bf(p + o0, f0);
       Vec<W>::store_bf(p + o1, f1);
@@ -235,11 +256,12 @@ cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
   return wide ? launch_tokens<8>(a, s) : launch_tokens<1>(a, s);
 }
 
-// Reading back. A block takes kGatherTok tokens: their cache rows are worked
-// out first, then the 8-component vectors of all heads of K and V are copied,
-// kGatherTok * 2 * heads * head_dim / 8 of them, E4M3 codes widened (exactly,
-// through FP16) and scaled in FP32, one rounding to BF16.
-constexpr int kGatherTok = 32;
+// Reading back. A block takes kGatherTok tokens, whose cache rows are worked
+// out first, and up to 256 items; an item is the same 8 components of the same
+// head of K or V in every token, so a thread decodes its item once and only
+// adds up offsets, with the loads of kGatherDeep tokens in flight. E4M3 codes
+// are widened (exactly, through FP16) and scaled in FP32, one rounding to BF16.
+constexpr int kGatherTok = 32, kGatherDeep = 4;
 
 struct GatherArgs {
   const uint8_t* k_cache;
@@ -255,6 +277,7 @@ struct GatherArgs {
   int n_tok, hk, head_dim, max_pages, num_pages, page_size;
 };
 
+// grid (ceil(tokens / kGatherTok), ceil(items / 256))
 template <bool FP8>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   __shared__ long long s_row[kGatherTok];
@@ -264,46 +287,61 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   if (tid < n) {
     const long long tok = tok0 + tid;
     const int p = a.pos[tok];
+    const bool report = blockIdx.y == 0;
     long long row = -1;
     if (p != -1) {
-      const int r = (int)(tok / a.n_tok), j = (int)(tok - (long long)r * a.n_tok);
+      const int r = (int)((unsigned)tok / (unsigned)a.n_tok), j = (int)tok - r * a.n_tok;
       if (p < 0 || p >= a.max_pages * a.page_size) {
-        record_error(a.err, kErrQueryPos, r, j, p);
+        if (report) record_error(a.err, kErrQueryPos, r, j, p);
       } else {
         const int page = a.page_table[(long long)r * a.max_pages + p / a.page_size];
         if ((unsigned)page < (unsigned)a.num_pages)
-          row = (long long)page * a.hk * a.page_size + p % a.page_size;
-        else
+          row = ((long long)page * a.hk * a.page_size + p % a.page_size) * a.head_dim;
+        else if (report)
           record_error(a.err, kErrPage, r, j, page);
       }
     }
     s_row[tid] = row;
   }
+  const int vecs = a.head_dim / 8, per = a.hk * vecs, items = 2 * per;  // items of a token
+  const int here = min(256, items - (int)blockIdx.y * 256);             // of them in this block
+  const int lanes = 256 / here;                                         // tokens at a time
+  const int sub = tid / here, item = (int)blockIdx.y * 256 + tid - sub * here;
+  const bool is_v = item >= per;
+  const int h = is_v ? item - per : item, g = h / vecs;
+  const uint8_t* cache = is_v ? a.v_cache : a.k_cache;
+  const long long off = ((long long)g * a.page_size) * a.head_dim + (h - g * vecs) * 8;
+  const float s = !FP8 ? 1.f : is_v ? a.v_scale[g] : a.k_scale[g];
+  __nv_bfloat16* out = (is_v ? a.v_out : a.k_out) + tok0 * a.hk * a.head_dim + h * 8;
   __syncthreads();
-  const int vecs = a.head_dim / 8, per_tok = a.hk * vecs;  // of K or of V
-  const int total = n * per_tok;
-#pragma unroll 4
-  for (int e = tid; e < 2 * total; e += 256) {
-    const bool is_v = e >= total;
-    const int f = is_v ? e - total : e;
-    const int t = f / per_tok, h = f - t * per_tok, g = h / vecs, c = h - g * vecs;
-    const long long row = s_row[t];
-    if (row < 0) continue;
-    const long long at = (row + (long long)g * a.page_size) * a.head_dim + c * 8;
-    const uint8_t* cache = is_v ? a.v_cache : a.k_cache;
-    uint4 w;
-    if constexpr (FP8) {
-      const float s = is_v ? a.v_scale[g] : a.k_scale[g];
-      const uint2 u = ld8(cache + at);
-      const float2 f0 = h2_to_f2(e4m3x2_to_h2(u.x)), f1 = h2_to_f2(e4m3x2_to_h2(u.x >> 16));
-      const float2 f2 = h2_to_f2(e4m3x2_to_h2(u.y)), f3 = h2_to_f2(e4m3x2_to_h2(u.y >> 16));
-      w = make_uint4(pack_bf(f0.x * s, f0.y * s), pack_bf(f1.x * s, f1.y * s), pack_bf(f2.x * s, f2.y * s),
-                     pack_bf(f3.x * s, f3.y * s));
-    } else {
-      w = ld16(cache + 2 * at);
+  if (sub >= lanes) return;
+  for (int t0 = sub; t0 < n; t0 += kGatherDeep * lanes) {
+    uint4 w[kGatherDeep];
+#pragma unroll
+    for (int u = 0; u < kGatherDeep; ++u) {
+      const int t = t0 + u * lanes;
+      if (t < n && s_row[t] >= 0) {
+        if constexpr (FP8) {
+          const uint2 c = ld8(cache + s_row[t] + off);
+          w[u].x = c.x;
+          w[u].y = c.y;
+        } else {
+          w[u] = ld16(cache + 2 * (s_row[t] + off));
+        }
+      }
     }
-    __nv_bfloat16* out = (is_v ? a.v_out : a.k_out) + (tok0 + t) * a.hk * a.head_dim;
-    *reinterpret_cast<uint4*>(out + h * 8) = w;
+#pragma unroll
+    for (int u = 0; u < kGatherDeep; ++u) {
+      const int t = t0 + u * lanes;
+      if (t >= n || s_row[t] < 0) continue;
+      if constexpr (FP8) {
+        const float2 f0 = h2_to_f2(e4m3x2_to_h2(w[u].x)), f1 = h2_to_f2(e4m3x2_to_h2(w[u].x >> 16));
+        const float2 f2 = h2_to_f2(e4m3x2_to_h2(w[u].y)), f3 = h2_to_f2(e4m3x2_to_h2(w[u].y >> 16));
+        w[u] = make_uint4(pack_bf(f0.x * s, f0.y * s), pack_bf(f1.x * s, f1.y * s), pack_bf(f2.x * s, f2.y * s),
+                          pack_bf(f3.x * s, f3.y * s));
+      }
+      *reinterpret_cast<uint4*>(out + (long long)t * a.hk * a.head_dim) = w[u];
+    }
   }
 }
 
@@ -374,9 +412,10 @@ cudaError_t launch_kv_gather(const qsa_dims& d, int n_tok, const void* k_cache, 
   a.max_pages = d.max_pages;
   a.num_pages = d.num_pages;
   a.page_size = d.page_size;
-  const unsigned grid = (unsigned)((a.tokens + kGatherTok - 1) / kGatherTok);
+  const unsigned gx = (unsigned)((a.tokens + kGatherTok - 1) / kGatherTok);
+  const unsigned gy = (unsigned)((2 * a.hk * (a.head_dim / 8) + 255) / 256);
   auto kern = d.kv_dtype == QSA_KV_FP8_E4M3 ? gather_kernel<true> : gather_kernel<false>;
-  return launch_k(kern, dim3(grid), dim3(256), 0, s, false, a);
+  return launch_k(kern, dim3(gx, gy), dim3(256), 0, s, false, a);
 }
 
 }  // namespace qsa
