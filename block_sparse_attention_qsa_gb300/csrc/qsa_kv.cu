@@ -14,13 +14,20 @@
 //
 // All of it is streaming: each input is read once and each output written
 // once, with nothing to reuse but the R / 2 (cos, sin) of a token, which all
-// its heads share. So the layout is made for that: a block takes kTok tokens
-// and up to kItems items; an item is the same 2 x W components of the same
-// head in every token (W = 8: two 16-byte vectors that hold 8 whole pairs; W =
-// 1: one pair, for row starts, strides or rotated parts that are not multiples
-// of 16 bytes or 16 components). A thread decodes its item once, issues the
-// loads of all its tokens before anything else, and meets the block's table of
-// (cos, sin), worked out while the loads are in flight, at one barrier.
+// its heads share. Two kernels:
+//
+//  * wide_kernel, where rows can be read 16 bytes at a time and the rotated
+//    part is a multiple of 16 components: a warp takes a token. It works out
+//    the token's (cos, sin) once (each lane one to four of them), and a lane
+//    keeps the 8 that its components need in registers for all heads: an item
+//    is 2 x 8 components that hold 8 whole pairs, D / 16 of them a head, and a
+//    pass of the warp covers 32 / (D / 16) heads. Loads of four passes are in
+//    flight at a time, the first ones while the angles are worked out. No
+//    block barrier: an earlier layout (a block per four tokens, one item a
+//    thread, the table of angles shared through a barrier) was bound by the
+//    warps' waiting for one another, 76 us for 2 x 16,385 tokens of 16 + 2 + 2
+//    heads of 128 into an E4M3 cache.
+//  * pair_kernel for the rest: one pair a thread.
 #include <algorithm>
 
 #include "qsa_kv_internal.cuh"
@@ -62,174 +69,225 @@ __device__ __forceinline__ void rotate(float& xa, float& xb, float2 cs) {
   xb = b * cs.x + a * cs.y;
 }
 
-template <int W>
-struct Vec;
-template <>
-struct Vec<8> {
-  uint4 w;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = ld16(p); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = bf_lo(w.x), f[1] = bf_hi(w.x), f[2] = bf_lo(w.y), f[3] = bf_hi(w.y);
-    f[4] = bf_lo(w.z), f[5] = bf_hi(w.z), f[6] = bf_lo(w.w), f[7] = bf_hi(w.w);
+// The token's checks: its cache row for KV head 0 (-1: K and V are not
+// written), and whether it is there, in order and within the page table.
+__device__ __forceinline__ bool check_token(const TokenArgs& a, int tok, int r, int j, bool report, long long& row) {
+  row = -1;
+  const int p = a.pos[tok];
+  if (a.hk == 0) return p >= 0;  // rotation only
+  if (p == -1) return false;
+  const int first = a.pos[(long long)r * a.n_tok];
+  if (p < 0 || p >= a.max_pages * a.page_size) {
+    if (report) record_error(a.err, kErrQueryPos, r, j, p);
+    return false;
   }
-  static __device__ __forceinline__ void store_bf(__nv_bfloat16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf(f[0], f[1]), pack_bf(f[2], f[3]), pack_bf(f[4], f[5]), pack_bf(f[6], f[7]));
+  if (p != (long long)first + j) {
+    if (report) record_error(a.err, kErrOrder, r, j, p);
+    return false;
   }
-  static __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[8], float scale) {
-    uint32_t c[4];
+  const int page = a.page_table[(long long)r * a.max_pages + p / a.page_size];
+  if ((unsigned)page < (unsigned)a.num_pages)
+    row = ((long long)page * a.hk * a.page_size + p % a.page_size) * a.head_dim;
+  else if (report)
+    record_error(a.err, kErrPage, r, j, page);
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// 16 bytes at a time
+// ---------------------------------------------------------------------------
+constexpr int kWideWarps = 4, kWideDeep = 4;
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  f[0] = bf_lo(w.x), f[1] = bf_hi(w.x), f[2] = bf_lo(w.y), f[3] = bf_hi(w.y);
+  f[4] = bf_lo(w.z), f[5] = bf_hi(w.z), f[6] = bf_lo(w.w), f[7] = bf_hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf(f[0], f[1]), pack_bf(f[2], f[3]), pack_bf(f[4], f[5]), pack_bf(f[6], f[7]));
+}
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
+  uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(f[2 * i] / scale, f[2 * i + 1] / scale);
-    *reinterpret_cast<uint2*>(p) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  }
-};
-template <>
-struct Vec<1> {
-  __nv_bfloat16 w;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *p; }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(w); }
-  static __device__ __forceinline__ void store_bf(__nv_bfloat16* p, const float (&f)[1]) {
-    *p = __float2bfloat16_rn(f[0]);
-  }
-  static __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[1], float scale) {
-    *p = (uint8_t)e4m3x2(f[0] / scale, 0.f);
-  }
-};
+  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(f[2 * i] / scale, f[2 * i + 1] / scale);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
 
-// grid (ceil(tokens / TOK), ceil(items / kItems)), kItems threads
-constexpr int kItems = 256;
-
-template <int W, int TOK>
-__global__ void __launch_bounds__(kItems) token_kernel(const TokenArgs a) {
-  // (cos, sin) of a token's pairs. W = 8: the 16-byte unit of pairs 8 i + 2 u,
-  // 8 i + 2 u + 1 is at [u][i], so that items i = 0, 1, .. of a warp read
-  // consecutive units; W = 1: in order
-  __shared__ __align__(16) float2 s_cs[TOK][kMaxHalf];
-  __shared__ long long s_row[TOK];  // cache row of KV head 0; -1: K and V are not written
-  __shared__ int s_live[TOK];       // the token is there and in order
-  const int tid = threadIdx.x;
-  const long long tok0 = (long long)blockIdx.x * TOK;  // (below 2^31)
+// grid (ceil(tokens / kWideWarps), parts of the passes); PER = head_dim / 16
+template <int PER, bool IL, bool FP8>
+__global__ void __launch_bounds__(32 * kWideWarps) wide_kernel(const TokenArgs a) {
+  constexpr int kHeads = 32 / PER, D = 16 * PER;  // heads of a pass
+  __shared__ __align__(16) float2 s_cs[kWideWarps][kMaxHalf];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = (int)blockIdx.x * kWideWarps + warp;  // (below 2^31)
+  if (tok >= a.tokens) return;
+  const int r = (int)((unsigned)tok / (unsigned)a.n_tok), j = tok - r * a.n_tok;
+  const int i = lane % PER, sub = lane / PER;  // this lane's item of a head, its head within a pass
   const int half = a.rope.rot_dim >> 1;
-  const int per_head = a.head_dim / (2 * W);  // items of a head
-  const int item = blockIdx.y * kItems + tid;
-  const int head = item / per_head, i = item - head * per_head;
+  const bool in_rot = i < (a.rope.rot_dim >> 4);
   const int heads = a.hq + 2 * a.hk;
-  const bool mine = head < heads;
-  const int seg = head < a.hq ? 0 : head < a.hq + a.hk ? 1 : 2;  // q, k, v
-  const int g = seg == 0 ? head : seg == 1 ? head - a.hq : head - a.hq - a.hk;
-  const bool turn = seg < 2 && i < a.rope.rot_dim / (2 * W);
-  // the item's two vectors: 8 whole pairs of a rotated part, else 2 W consecutive components
-  const bool split = turn && !a.rope.interleaved;
-  const int o0 = split ? i * W : i * 2 * W, o1 = split ? half + i * W : o0 + W;
-  const Strided& in = seg == 0 ? a.q : seg == 1 ? a.k : a.v;
-
-  // (request, token) of the block's first token; the others follow by counting
-  const int rb = (int)((unsigned)tok0 / (unsigned)a.n_tok), jb = (int)tok0 - rb * a.n_tok;
-  Vec<W> x0[TOK], x1[TOK];
-  {
-    int r = rb, j = jb;
+  const int passes = (heads + kHeads - 1) / kHeads, per_part = (passes + gridDim.y - 1) / gridDim.y;
+  const int p0 = blockIdx.y * per_part, p1 = min(passes, p0 + per_part);
+  const __nv_bfloat16* q = a.q.p + r * a.q.batch + j * a.q.token;
+  const __nv_bfloat16* k = a.k.p + r * a.k.batch + j * a.k.token;
+  const __nv_bfloat16* v = a.v.p + r * a.v.batch + j * a.v.token;
+  // an item's two vectors: of a rotated part the two that hold whole pairs
+  const int split = IL || !in_rot ? i * 16 : i * 8, other = IL || !in_rot ? 8 : half;
+  uint4 x0[kWideDeep], x1[kWideDeep];
+  auto load = [&](int p) {
 #pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      if (mine && tok0 + t < a.tokens) {
-        const __nv_bfloat16* p = in.p + r * in.batch + j * in.token + g * in.head;
-        x0[t].load(p + o0);
-        x1[t].load(p + o1);
+    for (int u = 0; u < kWideDeep; ++u) {
+      const int h = (p + u) * kHeads + sub;
+      if (p + u < p1 && h < heads) {
+        const __nv_bfloat16* src = h < a.hq             ? q + h * a.q.head + split
+                                   : h < a.hq + a.hk ? k + (h - a.hq) * a.k.head + split
+                                                     : v + (h - a.hq - a.hk) * a.v.head + i * 16;
+        x0[u] = ld16(src);
+        x1[u] = ld16(src + (h < a.hq + a.hk ? other : 8));
       }
-      if (++j == a.n_tok) {
-        j = 0;
-        ++r;
+    }
+  };
+  load(p0);
+  long long row;
+  const bool live = check_token(a, tok, r, j, lane == 0 && blockIdx.y == 0, row);
+  float2 cs[8];
+  if (half > 0) {
+    const int pos = a.pos[tok];
+    for (int f = lane; f < half; f += 32) {
+      const float2 c = cos_sin(pos, a.rope.turns[f]);
+      s_cs[warp][f] = make_float2(c.x * a.rope.amplitude, c.y * a.rope.amplitude * a.sign);
+    }
+    __syncwarp();
+    if (in_rot) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(&s_cs[warp][i * 8 + e]);
+        cs[e] = make_float2(c.x, c.y);
+        cs[e + 1] = make_float2(c.z, c.w);
       }
     }
   }
-  // the tokens' checks and cache rows
-  if (tid < TOK) {
-    const long long tok = tok0 + tid;
-    long long row = -1;
-    int live = 0;
-    if (tok < a.tokens) {
-      const int p = a.pos[tok];
-      live = p >= 0;
-      if (a.hk > 0 && p != -1) {
-        const int r = (int)((unsigned)tok / (unsigned)a.n_tok), j = (int)tok - r * a.n_tok;
-        const bool report = blockIdx.y == 0;
-        if (p < 0 || p >= a.max_pages * a.page_size) {
-          live = 0;
-          if (report) record_error(a.err, kErrQueryPos, r, j, p);
-        } else if (p != (long long)a.pos[(long long)r * a.n_tok] + j) {
-          live = 0;
-          if (report) record_error(a.err, kErrOrder, r, j, p);
+  if (!live) return;
+  __nv_bfloat16* qo = a.q_out.p + r * a.q_out.batch + j * a.q_out.token;
+  for (int p = p0; p < p1; p += kWideDeep) {
+    if (p > p0) load(p);
+#pragma unroll
+    for (int u = 0; u < kWideDeep; ++u) {
+      const int h = (p + u) * kHeads + sub;
+      if (p + u >= p1 || h >= heads) continue;
+      const bool is_v = h >= a.hq + a.hk;
+      float f0[8], f1[8];
+      unpack8(x0[u], f0);
+      unpack8(x1[u], f1);
+      if (in_rot && !is_v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (IL)  // pair e: adjacent components of the first or second vector
+            rotate(e < 4 ? f0[2 * e % 8] : f1[2 * e % 8], e < 4 ? f0[(2 * e + 1) % 8] : f1[(2 * e + 1) % 8], cs[e]);
+          else
+            rotate(f0[e], f1[e], cs[e]);
+        }
+      }
+      if (h < a.hq) {
+        __nv_bfloat16* dst = qo + h * a.q_out.head + split;
+        *reinterpret_cast<uint4*>(dst) = pack8(f0);
+        *reinterpret_cast<uint4*>(dst + other) = pack8(f1);
+      } else if (row >= 0) {
+        const int g = is_v ? h - a.hq - a.hk : h - a.hq;
+        const int o0 = is_v ? i * 16 : split, o1 = o0 + (is_v ? 8 : other);
+        const long long at = row + (long long)g * a.page_size * D;
+        uint8_t* cache = is_v ? a.v_cache : a.k_cache;
+        if constexpr (FP8) {
+          const float scale = is_v ? a.v_scale[g] : a.k_scale[g];
+          *reinterpret_cast<uint2*>(cache + at + o0) = codes8(f0, scale);
+          *reinterpret_cast<uint2*>(cache + at + o1) = codes8(f1, scale);
         } else {
-          const int page = a.page_table[(long long)r * a.max_pages + p / a.page_size];
-          if ((unsigned)page < (unsigned)a.num_pages)
-            row = (long long)page * a.hk * a.page_size + p % a.page_size;
-          else if (report)
-            record_error(a.err, kErrPage, r, j, page);
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(cache) + at;
+          *reinterpret_cast<uint4*>(dst + o0) = pack8(f0);
+          *reinterpret_cast<uint4*>(dst + o1) = pack8(f1);
         }
       }
     }
-    s_row[tid] = row;
-    s_live[tid] = live;
   }
-  for (int e = tid; e < TOK * half; e += kItems) {
+}
+
+// ---------------------------------------------------------------------------
+// one pair (or two components that are not rotated) a thread
+// ---------------------------------------------------------------------------
+constexpr int kPairTok = 4, kPairThreads = 256;
+
+// grid (ceil(tokens / kPairTok), ceil(pairs of a token / kPairThreads)): a
+// thread keeps its pair for kPairTok tokens; the tokens' angles are shared
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const TokenArgs a) {
+  __shared__ float2 s_cs[kPairTok][kMaxHalf];
+  __shared__ long long s_row[kPairTok];
+  __shared__ int s_live[kPairTok];
+  const int tid = threadIdx.x;
+  const int tok0 = (int)blockIdx.x * kPairTok;
+  const int half = a.rope.rot_dim >> 1, per_head = a.head_dim / 2;
+  const int item = blockIdx.y * kPairThreads + tid;
+  const int head = item / per_head, i = item - head * per_head;
+  const bool mine = head < a.hq + 2 * a.hk;
+  const int seg = head < a.hq ? 0 : head < a.hq + a.hk ? 1 : 2;  // q, k, v
+  const int g = seg == 0 ? head : seg == 1 ? head - a.hq : head - a.hq - a.hk;
+  const bool turn = seg < 2 && i < half;
+  const bool apart = turn && !a.rope.interleaved;
+  const int o0 = apart ? i : 2 * i, o1 = apart ? half + i : o0 + 1;
+  const Strided& in = seg == 0 ? a.q : seg == 1 ? a.k : a.v;
+  const int rb = (int)((unsigned)tok0 / (unsigned)a.n_tok), jb = tok0 - rb * a.n_tok;
+  __nv_bfloat16 x0[kPairTok], x1[kPairTok];
+  int r = rb, j = jb;
+#pragma unroll
+  for (int t = 0; t < kPairTok; ++t) {
+    if (mine && tok0 + t < a.tokens) {
+      const __nv_bfloat16* p = in.p + r * in.batch + j * in.token + g * in.head;
+      x0[t] = p[o0];
+      x1[t] = p[o1];
+    }
+    if (++j == a.n_tok) {
+      j = 0;
+      ++r;
+    }
+  }
+  if (tid < kPairTok && tok0 + tid < a.tokens) {
+    const int tok = tok0 + tid, tr = (int)((unsigned)tok / (unsigned)a.n_tok);
+    s_live[tid] = check_token(a, tok, tr, tok - tr * a.n_tok, blockIdx.y == 0, s_row[tid]);
+  }
+  for (int e = tid; e < kPairTok * half; e += kPairThreads) {
     const int t = e / half, f = e - t * half;
     if (tok0 + t < a.tokens) {
-      const float2 cs = cos_sin(a.pos[tok0 + t], a.rope.turns[f]);
-      const int at = W == 1 ? f : (((f >> 1) & 3) * (half >> 3) + (f >> 3)) * 2 + (f & 1);
-      s_cs[t][at] = make_float2(cs.x * a.rope.amplitude, cs.y * a.rope.amplitude * a.sign);
+      const float2 c = cos_sin(a.pos[tok0 + t], a.rope.turns[f]);
+      s_cs[t][f] = make_float2(c.x * a.rope.amplitude, c.y * a.rope.amplitude * a.sign);
     }
   }
   __syncthreads();
   if (!mine) return;
-
   const float scale = seg == 0 || !a.fp8 ? 1.f : seg == 1 ? a.k_scale[g] : a.v_scale[g];
-  int rn = rb, jn = jb;
+  r = rb, j = jb;
 #pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    const int r = rn, j = jn;
-    if (++jn == a.n_tok) {
-      jn = 0;
-      ++rn;
-    }
-    if (tok0 + t >= a.tokens || !s_live[t]) continue;
-    float f0[W], f1[W];
-    x0[t].get(f0);
-    x1[t].get(f1);
-    if (turn) {
-      if constexpr (W == 1) {
-        rotate(f0[0], f1[0], s_cs[t][i]);
-      } else {
-        const float4* cs = reinterpret_cast<const float4*>(s_cs[t]) + i;
-        const int step = half >> 3;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 w = cs[u * step];
-          const float2 c0 = make_float2(w.x, w.y), c1 = make_float2(w.z, w.w);
-          if (a.rope.interleaved) {  // pairs 8 i + 2 u, + 1: adjacent components of the first or second vector
-            float(&f)[W] = u < 2 ? f0 : f1;
-            rotate(f[4 * u % W], f[4 * u % W + 1], c0);
-            rotate(f[4 * u % W + 2], f[4 * u % W + 3], c1);
-          } else {
-            rotate(f0[2 * u], f1[2 * u], c0);
-            rotate(f0[2 * u + 1], f1[2 * u + 1], c1);
-          }
+  for (int t = 0; t < kPairTok; ++t) {
+    if (tok0 + t < a.tokens && s_live[t]) {
+      float f0 = __bfloat162float(x0[t]), f1 = __bfloat162float(x1[t]);
+      if (turn) rotate(f0, f1, s_cs[t][i]);
+      if (seg == 0) {
+        __nv_bfloat16* p = a.q_out.p + r * a.q_out.batch + j * a.q_out.token + g * a.q_out.head;
+        p[o0] = __float2bfloat16_rn(f0);
+        p[o1] = __float2bfloat16_rn(f1);
+      } else if (s_row[t] >= 0) {
+        uint8_t* cache = seg == 1 ? a.k_cache : a.v_cache;
+        const long long at = s_row[t] + (long long)g * a.page_size * a.head_dim;
+        if (a.fp8) {
+          cache[at + o0] = (uint8_t)e4m3x2(f0 / scale, 0.f);
+          cache[at + o1] = (uint8_t)e4m3x2(f1 / scale, 0.f);
+        } else {
+          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(cache) + at;
+          p[o0] = __float2bfloat16_rn(f0);
+          p[o1] = __float2bfloat16_rn(f1);
         }
       }
     }
-    if (seg == 0) {
-      __nv_bfloat16* p = a.q_out.p + r * a.q_out.batch + j * a.q_out.token + g * a.q_out.head;
-      Vec<W>::store_bf(p + o0, f0);
-      Vec<W>::store_bf(p + o1, f1);
-    } else if (s_row[t] >= 0) {
-      uint8_t* cache = seg == 1 ? a.k_cache : a.v_cache;
-      const long long at = (s_row[t] + (long long)g * a.page_size) * a.head_dim;
-      if (a.fp8) {
-        Vec<W>::store_e4m3(cache + at + o0, f0, scale);
-        Vec<W>::store_e4m3(cache + at + o1, f1, scale);
-      } else {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(cache) + at;
-        Vec<W>::store_bf(p + o0, f0);
-        Vec<W>::store_bf(p + o1, f1);
-      }
+    if (++j == a.n_tok) {
+      j = 0;
+      ++r;
     }
   }
 }
@@ -240,20 +298,30 @@ bool vec8(const Strided& t) {
                             t.head % 8 == 0);
 }
 
-template <int W>
-cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
-  const int items = (a.hq + 2 * a.hk) * (a.head_dim / (2 * W));
-  const unsigned gy = (unsigned)((items + kItems - 1) / kItems);
-  constexpr int kTok = 4;
-  if (a.tokens * gy <= 4 * device_sm_count())
-    return launch_k(token_kernel<W, 1>, dim3((unsigned)a.tokens, gy), dim3(kItems), 0, s, false, a);
-  const long long gx = (a.tokens + kTok - 1) / kTok;
-  return launch_k(token_kernel<W, kTok>, dim3((unsigned)gx, gy), dim3(kItems), 0, s, false, a);
+template <int PER, bool FP8>
+cudaError_t launch_wide(const TokenArgs& a, cudaStream_t s) {
+  const int passes = (a.hq + 2 * a.hk + 32 / PER - 1) / (32 / PER);
+  const unsigned gx = (unsigned)((a.tokens + kWideWarps - 1) / kWideWarps);
+  // few tokens: their passes are dealt to several warps, which each work out
+  // the angles (32 tokens of 20 heads of 128: 5 parts)
+  const unsigned gy = (unsigned)std::max<long long>(1, std::min<long long>(passes, 2LL * device_sm_count() / gx));
+  return a.rope.interleaved ? launch_k(wide_kernel<PER, true, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, false, a)
+                            : launch_k(wide_kernel<PER, false, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, false, a);
+}
+template <bool FP8>
+cudaError_t launch_wide(const TokenArgs& a, cudaStream_t s) {
+  return a.head_dim == 64    ? launch_wide<4, FP8>(a, s)
+         : a.head_dim == 128 ? launch_wide<8, FP8>(a, s)
+                             : launch_wide<16, FP8>(a, s);
 }
 
 cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
-  const bool wide = a.rope.rot_dim % 16 == 0 && vec8(a.q) && vec8(a.q_out) && vec8(a.k) && vec8(a.v);
-  return wide ? launch_tokens<8>(a, s) : launch_tokens<1>(a, s);
+  if (a.rope.rot_dim % 16 == 0 && vec8(a.q) && vec8(a.q_out) && vec8(a.k) && vec8(a.v))
+    return a.fp8 ? launch_wide<true>(a, s) : launch_wide<false>(a, s);
+  const int pairs = (a.hq + 2 * a.hk) * (a.head_dim / 2);
+  const dim3 grid((unsigned)((a.tokens + kPairTok - 1) / kPairTok),
+                  (unsigned)((pairs + kPairThreads - 1) / kPairThreads));
+  return launch_k(pair_kernel, grid, dim3(kPairThreads), 0, s, false, a);
 }
 
 // Reading back. A block takes kGatherTok tokens, whose cache rows are worked
