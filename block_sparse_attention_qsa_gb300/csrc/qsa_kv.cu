@@ -21,7 +21,7 @@
 //    the token's (cos, sin) once (each lane one to four of them), and a lane
 //    keeps the 8 that its components need in registers for all heads: an item
 //    is 2 x 8 components that hold 8 whole pairs, D / 16 of them a head, and a
-//    pass of the warp covers 32 / (D / 16) heads. Loads of four passes are in
+//    pass of the warp covers 32 / (D / 16) heads. Loads of five passes are in
 //    flight at a time, the first ones while the angles are worked out. No
 //    block barrier: an earlier layout (a block per four tokens, one item a
 //    thread, the table of angles shared through a barrier) was bound by the
@@ -96,7 +96,7 @@ __device__ __forceinline__ bool check_token(const TokenArgs& a, int tok, int r, 
 // ---------------------------------------------------------------------------
 // 16 bytes at a time
 // ---------------------------------------------------------------------------
-constexpr int kWideWarps = 4, kWideDeep = 4;
+constexpr int kWideWarps = 4, kWideDeep = 5;
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   f[0] = bf_lo(w.x), f[1] = bf_hi(w.x), f[2] = bf_lo(w.y), f[3] = bf_hi(w.y);
@@ -114,7 +114,7 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
 
 // grid (ceil(tokens / kWideWarps), parts of the passes); PER = head_dim / 16
 template <int PER, bool IL, bool FP8>
-__global__ void __launch_bounds__(32 * kWideWarps) wide_kernel(const TokenArgs a) {
+__global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArgs a) {
   constexpr int kHeads = 32 / PER, D = 16 * PER;  // heads of a pass
   __shared__ __align__(16) float2 s_cs[kWideWarps][kMaxHalf];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
