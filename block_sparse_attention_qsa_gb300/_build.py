@@ -4,6 +4,9 @@ Each .cu under csrc/ compiles to an object in parallel; the objects link into
 ``block_sparse_attention_qsa_gb300/libqsa.so`` with the CUDA runtime linked
 statically, so the library only needs the NVIDIA driver at run time.
 
+The binding's fast path (csrc/qsa_fast.cpp, the module ``_fast``) compiles
+beside them with g++ against torch's headers; it is needed by both builds.
+
 ``build(trace=True)`` makes the tracing build instead, ``libqsa_trace.so``
 (the same sources with ``-DQSA_TRACE``: the step's kernels record per-CTA
 phase stamps, read back with ``qsa_trace_read``); ``timeline.py`` uses it.
@@ -16,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
 BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(PKG, "libqsa_trace.so")
+FAST = os.path.join(PKG, "_fast.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -42,10 +47,21 @@ def sources():
 
 
 def _newest_input() -> float:
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
+
+
+def _fast_cmd(out: str):
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    # torch's libraries are found by name in the process that imported torch
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+            os.path.join(CSRC, "qsa_fast.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: bool = False) -> str:
@@ -55,7 +71,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
     lib, bdir = (LIB_TRACE, BUILD_TRACE) if trace else (LIB, BUILD)
     if trace:
         extra_flags = (*extra_flags, "-DQSA_TRACE")
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _newest_input():
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (lib, FAST)):
         return lib
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -66,6 +83,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
         objs.append(obj)
         cmds.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
 
+    cmds.append(_fast_cmd(FAST + ".tmp"))
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -74,7 +93,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
             raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(10, len(cmds))) as ex:
         logs = list(ex.map(run, cmds))
     if verbose:
         for lg in logs:
@@ -83,6 +102,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
     tmp = lib + ".tmp"
     run([cc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib)
+    os.replace(FAST + ".tmp", FAST)
     return lib
 
 

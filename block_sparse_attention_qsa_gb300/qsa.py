@@ -148,6 +148,15 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _fast
+except ImportError as e:
+    raise ImportError(f"the binding's fast path is not built ({e}); run __graft_entry__.build()") from e
+_fast.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+             for f in ("qsa_rope", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn")),
+           getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+           getattr(torch._C, "_cuda_getCurrentRawStream", None))
+
 
 def status_str(status: int) -> str:
     return lib.qsa_status_str(status).decode()
@@ -490,50 +499,50 @@ def make_rope(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling
     return Rope(RopeArgs(rot_dim, ROPE_LAYOUTS[layout], amp, table.data_ptr()), table)
 
 
-# A decode step makes these calls once per layer, next to kernels of a few
-# microseconds, so each argument is looked at once, cheaply, and only one that
-# is not as expected goes to the function that says what is wrong with it.
-_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+# Each function below first hands its arguments to _fast, which makes the call
+# if all of them are as expected and returns its status. Where one is not, it
+# returns None, and the checks here say what is wrong with it (or, for what
+# _fast does not take, such as an empty tensor, make the call).
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _current_device() -> int:
+    """The current device, -1 where there is none (a host tensor is then what
+    the checks complain about)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -1
 
 
 def _want_on(dev: int, t: torch.Tensor, name: str, shape, dtype) -> int:
     """The address of ``t``, a contiguous tensor of this shape and type on the
     current device (whose stream and SMs the call uses)."""
-    if not (type(t) is _Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape
-            and t.is_contiguous()):
-        _want(t, name, shape, dtype)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    _want(t, name, shape, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     return t.data_ptr()
 
 
 def _want_strided(dev: int, t: torch.Tensor, name: str, shape):
     """(address, strides or None: contiguous) of a BF16 [batch][token][head][dim]
     tensor on the current device whose last dimension is contiguous."""
-    if not (type(t) is _Tensor and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), None
     sb, st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr(), Strides(sb, st, sh)
-
-
-def _raw_stream(stream, dev: int):
-    """The cudaStream_t of ``stream``, by default the current one."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rope_args(rope: Rope, dev: int):
@@ -549,7 +558,13 @@ def rope(rope: Rope, x, pos, y, inverse: bool = False, stream=None):
     head (x, y bf16 [B][n][H][D], any strides with a contiguous last dimension;
     pos int32 [B][n]; rows with pos < 0 are left as they are). y may be x.
     inverse rotates back: the gradient of the forward call."""
-    dev = torch.cuda.current_device()
+    if isinstance(rope, Rope):
+        st = _fast.rope(rope.args, rope.device_index, x, pos, y, 1 if inverse else 0, stream)
+        if st == OK:
+            return
+        if st is not None:
+            _check(st, "qsa_rope")
+    dev = _current_device()
     args = _rope_args(rope, dev)
     if x.dim() != 4:
         raise ValueError("x must be [B][n][H][D]")
@@ -558,7 +573,7 @@ def rope(rope: Rope, x, pos, y, inverse: bool = False, stream=None):
     yp, ys = _want_strided(dev, y, "y", shape)
     B, n, H, D = shape
     pp = _want_on(dev, pos, "pos", (B, n), _I32)
-    st = lib.qsa_rope(args, B, n, H, D, 1 if inverse else 0, xp, xs, pp, yp, ys, _raw_stream(stream, dev))
+    st = lib.qsa_rope(args, B, n, H, D, 1 if inverse else 0, xp, xs, pp, yp, ys, _stream(stream))
     if st:
         _check(st, "qsa_rope")
 
@@ -606,7 +621,15 @@ def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos
     at positions pos [B][n] (consecutive per request, -1 for no token): keys
     rotated by ``rope`` if given, both quantised for an E4M3 cache. With q
     (bf16 [B][n][H_q][D]) the same tokens' queries are rotated into q_out."""
-    dev = torch.cuda.current_device()
+    if rope is None or isinstance(rope, Rope):
+        st = _fast.kv_append(d, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws,
+                             None if rope is None else rope.args, None if rope is None else rope.device_index, q,
+                             q_out, stream)
+        if st == OK:
+            return
+        if st is not None:
+            _check(st, "qsa_kv_append")
+    dev = _current_device()
     if k.dim() != 4:
         raise ValueError("k must be [B][n][H_kv][D]")
     B, n, D = d.batch, k.shape[1], d.head_dim
@@ -625,7 +648,7 @@ def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos
     pp = _want_on(dev, pos, "pos", (B, n), _I32)
     w, nb = _ws_on(dev, ws)
     st = lib.qsa_kv_append(d, n, args, kp, ks, vp, vs, qp, qs, qop, qos, pp, pt, kc, vc, ksc, vsc, w, nb,
-                           _raw_stream(stream, dev))
+                           _stream(stream))
     if st:
         _check(st, "qsa_kv_append")
 
@@ -633,7 +656,12 @@ def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos
 def kv_gather(d: Dims, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_out, v_out, ws, stream=None):
     """Reads the cache back: k_out, v_out (bf16 [B][n][H_kv][D]) = the values
     at positions pos [B][n] (any order; rows at -1 are left as they are)."""
-    dev = torch.cuda.current_device()
+    st = _fast.kv_gather(d, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_out, v_out, ws, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_kv_gather")
+    dev = _current_device()
     if pos.dim() != 2:
         raise ValueError("pos must be [B][n]")
     n = pos.shape[1]
@@ -643,7 +671,7 @@ def kv_gather(d: Dims, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_ou
     vo = _want_on(dev, v_out, "v_out", shape, _BF16)
     kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
     w, nb = _ws_on(dev, ws)
-    st = lib.qsa_kv_gather(d, n, kc, vc, ksc, vsc, pt, pp, ko, vo, w, nb, _raw_stream(stream, dev))
+    st = lib.qsa_kv_gather(d, n, kc, vc, ksc, vsc, pt, pp, ko, vo, w, nb, _stream(stream))
     if st:
         _check(st, "qsa_kv_gather")
 
@@ -654,7 +682,12 @@ def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos
     request r attends to positions 0 .. q_pos[r][j] (the last ``window`` of
     them if window > 0); rows at -1 give zeros. lse (fp32 [B][n_q][H_q], may
     be None) receives the log of each row's softmax sum."""
-    dev = torch.cuda.current_device()
+    st = _fast.paged_attn(d, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, lse, ws, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_paged_attn")
+    dev = _current_device()
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 or a number of positions below 2^31")
     B, n_q, H = d.batch, d.n_q, d.n_q_heads
@@ -665,7 +698,7 @@ def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos
     pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
     lp = None if lse is None else _want_on(dev, lse, "lse", (B, n_q, H), _F32)
     w, nb = _ws_on(dev, ws)
-    st = lib.qsa_paged_attn(d, window, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _raw_stream(stream, dev))
+    st = lib.qsa_paged_attn(d, window, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
     if st:
         _check(st, "qsa_paged_attn")
 

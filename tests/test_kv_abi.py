@@ -197,8 +197,7 @@ def test_rope_refusals(qsa):
     assert call(*[qsa.Strides(2000, 256, 64) if k == 7 else a for k, a in enumerate(good)]) == qsa.ERR_INVALID_ARG
 
 
-def test_binding_refuses_host_tensors_and_bad_arguments(qsa, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+def test_binding_refuses_host_tensors_and_bad_arguments(qsa):
     bf, i32 = torch.bfloat16, torch.int32
     d = qsa.make_dims(1, 1, 16, 1, 1)
     x = torch.zeros(1, 1, 16, 128, dtype=bf)
@@ -206,7 +205,7 @@ def test_binding_refuses_host_tensors_and_bad_arguments(qsa, monkeypatch):
     cache = torch.zeros(1, 2, 64, 128, dtype=bf)
     pos, ws = torch.zeros(1, 1, dtype=i32), torch.zeros(4096, dtype=torch.uint8)
     rope = qsa.make_rope(128, device="cpu")
-    with pytest.raises(ValueError, match="current device"):
+    with pytest.raises(ValueError, match="CUDA|current device"):
         qsa.rope(rope, x, pos, x)
     with pytest.raises(TypeError, match="make_rope"):
         qsa.rope(None, x, pos, x)
