@@ -120,6 +120,12 @@ __device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
   }
 }
+// true in one thread of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void commit_tc(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -340,7 +346,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     }
   } else if (warp == C::kSWarp) {
     // ---- S^T = K Q^T ----
-    if (lane == 0) {
+    // (the whole warp walks the loop, one elected thread issues: descriptors
+    // then stay in uniform registers, which is what the instructions take)
+    {
+      const bool one = elect_one();
       constexpr uint32_t kIdesc = mma_desc<C>(false);
       constexpr int kSteps = C::kRowBytes / 32;  // 32 bytes of a row each
       int it = 0, seg = 0;
@@ -348,11 +357,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       long long w = w0;
       while (w < w1 && ok) {
         const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
-        ok = wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u);
+        ok = __all_sync(kFull, wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u));
         for (int k = 0; k < n && ok; ++k, ++it) {
           const int slot = (2 * it) % C::kSlots;
-          ok = wait(&slot_full[slot], (uint32_t)((2 * it) / C::kSlots) & 1u) &&
-               (it < 2 || wait(&p_full[it & 1], (uint32_t)((it - 2) >> 1) & 1u));  // its S has been read
+          ok = __all_sync(kFull, wait(&slot_full[slot], (uint32_t)((2 * it) / C::kSlots) & 1u) &&
+                                     (it < 2 || wait(&p_full[it & 1], (uint32_t)((it - 2) >> 1) & 1u)));  // S was read
           if (!ok) break;
           tc_after();
           const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 1024, 2);
@@ -363,23 +372,28 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             for (int ks = 0; ks < kSteps; ++ks) {
               // (addresses are in units of 16 bytes; a line is 64 BF16 components or all E4M3 ones)
               const uint32_t line = (uint32_t)(ks >> 2), step = (uint32_t)(ks & 3) * 2u;
-              mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * BLK + b) * N), dk + (line * (kTile * 8) + step),
-                          dq + (line * (N * 8) + step), kIdesc, ks > 0);
+              if (one)
+                mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * BLK + b) * N), dk + (line * (kTile * 8) + step),
+                            dq + (line * (N * 8) + step), kIdesc, ks > 0);
             }
           }
-          commit_tc(&s_full[it & 1]);
-          commit_tc(&slot_empty[slot]);
+          if (one) {
+            commit_tc(&s_full[it & 1]);
+            commit_tc(&slot_empty[slot]);
+          }
+          __syncwarp();
         }
         w += n;
         ++seg;
         if (w < w1) at.next_unit(a);
       }
-      commit_tc(&fin);
+      if (one) commit_tc(&fin);
     }
     __syncwarp();
   } else if (warp == C::kPvWarp) {
     // ---- O^T += V^T P^T ----
-    if (lane == 0) {
+    {
+      const bool one = elect_one();
       constexpr uint32_t kIdesc = mma_desc<C>(true);
       constexpr int kSteps = kTile / (FP8 ? 32 : 16), kPos = kTile / kSteps;  // positions of an MMA
       int it = 0;
@@ -389,8 +403,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
         for (int k = 0; k < n && ok; ++k, ++it) {
           const int slot = (2 * it + 1) % C::kSlots;
-          ok = wait(&p_full[it & 1], (uint32_t)(it >> 1) & 1u) &&
-               wait(&slot_full[slot], (uint32_t)((2 * it + 1) / C::kSlots) & 1u);
+          ok = __all_sync(kFull, wait(&p_full[it & 1], (uint32_t)(it >> 1) & 1u) &&
+                                     wait(&slot_full[slot], (uint32_t)((2 * it + 1) / C::kSlots) & 1u));
           if (!ok) break;
           tc_after();
           const bool fresh = k == 0 && *reinterpret_cast<volatile int*>(&s_keep) == 0;
@@ -402,17 +416,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             const uint64_t dp = smem_desc(smem_u32(s_p + ((it & 1) * BLK + b) * C::kP), 512, 512, 4);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks)
-              mma_tc<FP8>(tmem + C::kO + (uint32_t)(b * N), dv + (uint32_t)(ks * kPos * 8),
-                          dp + (uint32_t)(ks * kPos * 4), kIdesc, !(fresh && ks == 0));
+              if (one)
+                mma_tc<FP8>(tmem + C::kO + (uint32_t)(b * N), dv + (uint32_t)(ks * kPos * 8),
+                            dp + (uint32_t)(ks * kPos * 4), kIdesc, !(fresh && ks == 0));
           }
-          commit_tc(&pv_done[it & 1]);
-          commit_tc(&slot_empty[slot]);
+          if (one) {
+            commit_tc(&pv_done[it & 1]);
+            commit_tc(&slot_empty[slot]);
+          }
+          __syncwarp();
         }
         w += n;
         if (w < w1) at.next_unit(a);
       }
       // the tensor cores are done before the CTA gives its memory back
-      commit_tc(&fin);
+      if (one) commit_tc(&fin);
       const long long start = clock64();
       while (!mbar_try_wait(smem_u32(&fin), 0) && clock64() - start < 2 * kWaitCycles) {
       }
