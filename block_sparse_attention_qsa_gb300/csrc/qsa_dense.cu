@@ -178,9 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
 
   Split sp;
-  long long w0, w1;
-  Place<kTile> at;
-  if (!find_start<kTile, kThreads>(a, s_start, sp, w0, w1, at)) return;
+  Walk<kTile> at;
+  if (!find_start<kTile, kThreads>(a, s_start, sp, at)) return;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
   if (warp >= kComputeWarps) {
@@ -191,13 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const int box_bytes = C::kLine << feed.box_shift, line_ops = feed.boxes * C::kLines;
     int stage = 0;
     uint32_t phase = 0;
-    long long w = w0;
     bool ok = true;
-    while (w < w1 && ok) {
-      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+    do {
       const int g = at.x / a.row_blocks;
-      feed.start(a, at, n);
-      for (int k = 0; k < n && ok; ++k) {
+      feed.start(a, at);
+      for (int k = 0; k < at.n && ok; ++k) {
         const int page = feed.of_tile(a, at, k);
         const uint32_t bad = feed.bad_groups(page);  // (a box holds whole sub-slices)
         ok = __all_sync(kFull, wait(&empty_bar[stage], phase ^ 1u));
@@ -222,9 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           phase ^= 1u;
         }
       }
-      w += n;
-      if (w < w1) at.next_unit(a);
-    }
+    } while (ok && at.next(a));
     if (s_abort) {
       // copies in flight land before the CTA leaves: the last kStages issued
       // (bounded; a stage whose phase already completed answers at once)
@@ -244,10 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   const int gq = lane >> 2, c4 = lane & 3;
   const int row_base = RG == 2 ? grp * C::kGroupRows : 0;
   const uint32_t q_addr = smem_u32(s_q) + (uint32_t)((row_base + (lane & 15)) * C::kQPitch + (lane >> 4) * 16);
-  long long w = w0;
   long long it = 0;  // tiles of this CTA so far
-  while (w < w1) {
-    const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+  int pslot = 0;     // a CTA's first segment has its slot 0, a later one (its last) slot 1
+  do {
+    const int n = at.n;
     const int g = at.x / a.row_blocks, rb = at.x - g * a.row_blocks;
     const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);  // of this unit
     const float vscale = FP8 ? a.v_scale[g] : 1.f;
@@ -610,10 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // ---- the segment's end: join the warps ----
     const bool whole = n == at.tiles;
     const long long unit = (long long)at.r * units + at.x;
-    // a CTA's first segment has its slot 0, a later one (its last) slot 1
-    const int pslot = w == w0 ? 0 : 1;
-    if (tid == 0 && at.t == 0)
-      a.unit_desc[unit] = whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.of_tile(w + at.tiles - 1), pslot);
+    if (a.batch > kJoinScan && tid == 0 && at.t == 0)
+      a.unit_desc[unit] = whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.last_cta(at.unit, at.tiles), pslot);
     float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
     const int wrow = warp * C::kGroupRows;
 #pragma unroll
@@ -696,9 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       }
       compute_sync();
     }
-    w += n;
-    if (w < w1) at.next_unit(a);
-  }
+    pslot = 1;
+  } while (at.next(a));
 }
 
 // ---------------------------------------------------------------------------
@@ -729,7 +721,7 @@ cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const vo
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
   e = launch_k(dense_kernel<C>, dim3(a.grid), dim3(kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_join<C::D, C::kRows, C::FP8>(a, s);
+  return launch_join<C::D, C::kRows, C::FP8, C::kTile>(a, s);
 }
 
 template <int D, bool FP8>

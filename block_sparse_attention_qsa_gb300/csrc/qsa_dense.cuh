@@ -16,7 +16,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxSmem = 232448;  // 227 KB a CTA
-constexpr int kMinTiles = 2;      // tiles a CTA takes at least
+constexpr int kMinTiles = 2;      // tiles of a CTA's share at least, where there are
 constexpr long long kWaitCycles = 1LL << 31;  // bound of every wait: about one second
 
 struct DenseArgs {
@@ -134,38 +134,65 @@ __device__ __forceinline__ long long quot(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// The stream's shares: `ctas` CTAs, the first `rem` of them with one tile more
-// than `q`.
+// The stream, in slots: a unit of T > 0 tiles takes kSegCost + T slots. The
+// first kSegCost hold no tile; they stand for what beginning a unit costs its
+// CTA (query rows, first maximum, the end of the unit before), so that equal
+// shares of slots are about equal work. Without them, one request of 50,000
+// tokens (2 units on 152 SMs) waited 5 of 18 us for the one CTA that had the
+// end of one unit and the beginning of the other. The slots are cut into
+// `ctas` shares, the first `rem` of them one slot longer than `q`.
+constexpr int kSegCost = 3;
+__device__ __forceinline__ long long slots_of(int tiles) { return tiles > 0 ? tiles + kSegCost : 0; }
+
 struct Split {
   long long q;
   int ctas, rem;
-  __device__ __forceinline__ void init(const DenseArgs& a, long long tiles) {
-    ctas = (int)min((long long)a.grid, quot(tiles + kMinTiles - 1, kMinTiles));
-    q = ctas > 0 ? quot(tiles, ctas) : 0;
-    rem = (int)(tiles - q * ctas);
+  __device__ __forceinline__ void init(const DenseArgs& a, long long slots) {
+    ctas = (int)min((long long)a.grid, quot(slots + kSegCost + kMinTiles - 1, kSegCost + kMinTiles));
+    q = ctas > 0 ? quot(slots, ctas) : 0;
+    rem = (int)(slots - q * ctas);
   }
   __device__ __forceinline__ long long begin(int c) const { return c * q + min(c, rem); }
-  __device__ __forceinline__ int of_tile(long long w) const {
+  __device__ __forceinline__ int of_slot(long long w) const {
     const long long wide = rem * (q + 1);
     return (int)(w < wide ? quot(w, q + 1) : rem + quot(w - wide, q));
   }
+  // the CTAs with tiles of a unit of `tiles` tiles whose slots begin at `unit`
+  __device__ __forceinline__ int first_cta(long long unit) const { return of_slot(unit + kSegCost); }
+  __device__ __forceinline__ int last_cta(long long unit, int tiles) const {
+    return of_slot(unit + kSegCost + tiles - 1);
+  }
+  // where the first of them has the unit's piece: in its slot 0 if the unit is
+  // its first, else in its slot 1 (the unit is then its last)
+  __device__ __forceinline__ int piece_slot(long long unit, int cta) const { return begin(cta) < unit ? 1 : 0; }
 };
 
-// A place in the stream (of tiles of TILE positions): unit x = 0 ..
-// n_kv_heads * row_blocks - 1 of request r, tile t of its `tiles`.
+// A CTA's way through its share w0 .. w1 - 1: segments, each the tiles t .. t
+// + n - 1 of unit x = 0 .. n_kv_heads * row_blocks - 1 of request r (`tiles`
+// in all, its slots beginning at `unit`).
 template <int TILE>
-struct Place {
-  int r, x, t, tiles;
+struct Walk {
+  long long unit, w0, w1;
+  int r, x, t, n, tiles;
   Range g;
-  __device__ __forceinline__ void next_unit(const DenseArgs& a) {
-    t = 0;
-    if (++x < a.n_kv_heads * a.row_blocks) return;
-    x = 0;
-    do {
-      if (++r >= a.batch) return;
-      g = range_of(a, r);
-      tiles = g.tiles(TILE);
-    } while (tiles == 0);
+  __device__ __forceinline__ bool cut() {  // the share's tiles of this unit
+    const long long first = unit + kSegCost;
+    t = w0 > first ? (int)(w0 - first) : 0;
+    n = (int)min((long long)tiles, w1 - first) - t;
+    return n > 0;
+  }
+  __device__ __forceinline__ bool next(const DenseArgs& a) {
+    unit += kSegCost + tiles;
+    if (unit + kSegCost >= w1) return false;
+    if (++x == a.n_kv_heads * a.row_blocks) {
+      x = 0;
+      do {
+        if (++r >= a.batch) return false;
+        g = range_of(a, r);
+        tiles = g.tiles(TILE);
+      } while (tiles == 0);
+    }
+    return cut();
   }
 };
 
@@ -176,19 +203,22 @@ struct StartSmem {
   int first_r;
 };
 
+// With more requests than this the main kernel writes unit descriptors; with
+// fewer the joining kernel works them out itself while it waits.
+constexpr int kJoinScan = 256;
+
 // Every thread of the block: works the stream out from q_pos (each thread sums
-// the tiles of a contiguous run of requests, one block scan), and finds the
-// CTA's share w0 .. w1 - 1 and where it begins. Block 0 reports positions that
-// are none and marks the units that have no tile. False: nothing to do.
+// the slots of a contiguous run of requests, one block scan) and finds the
+// CTA's share and its first segment. Block 0 reports positions that are none
+// and marks the units that have no tile. False: nothing to do.
 template <int TILE, int THREADS>
-__device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS>& sm, Split& sp, long long& w0,
-                                           long long& w1, Place<TILE>& at) {
+__device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS>& sm, Split& sp, Walk<TILE>& at) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += range_of(a, r).tiles(TILE);
+  for (int r = r0; r < r1; ++r) mine += slots_of(range_of(a, r).tiles(TILE));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -211,18 +241,18 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS
         const int p = a.q_pos[(size_t)r * a.n_q + j];
         if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
       }
-      if (range_of(a, r).tiles(TILE) == 0)
+      if (a.batch > kJoinScan && range_of(a, r).tiles(TILE) == 0)
         for (int x = 0; x < units; ++x) a.unit_desc[(long long)r * units + x] = kUnitEmpty;
     }
   }
   if ((int)blockIdx.x >= sp.ctas) return false;
-  w0 = sp.begin(blockIdx.x);
-  w1 = sp.begin(blockIdx.x + 1);
-  if (before * units <= w0 && w0 < (before + mine) * units) {  // one thread: tile w0 is in one of its requests
+  at.w0 = sp.begin(blockIdx.x);
+  at.w1 = sp.begin(blockIdx.x + 1);
+  if (before * units <= at.w0 && at.w0 < (before + mine) * units) {  // one thread: w0 is in one of its requests
     long long b = before;
     for (int r = r0; r < r1; ++r) {
-      const int t = range_of(a, r).tiles(TILE);
-      if (w0 < (b + t) * units) {
+      const long long t = slots_of(range_of(a, r).tiles(TILE));
+      if (at.w0 < (b + t) * units) {
         sm.first_r = r;
         sm.first = b;
         break;
@@ -234,10 +264,10 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS
   at.r = sm.first_r;
   at.g = range_of(a, at.r);
   at.tiles = at.g.tiles(TILE);
-  const long long off = w0 - sm.first * units;
-  at.x = (int)quot(off, at.tiles);
-  at.t = (int)(off - (long long)at.x * at.tiles);
-  return true;
+  at.unit = sm.first * units;
+  at.x = (int)quot(at.w0 - at.unit, kSegCost + at.tiles);
+  at.unit += (long long)at.x * (kSegCost + at.tiles);
+  return at.cut();
 }
 
 // The pages of a segment's boxes (box = the positions that one TMA copy takes,
@@ -257,7 +287,7 @@ struct PageFeed {
     boxes = TILE >> box_shift;
     my_box = (int)(threadIdx.x & 31) & (boxes - 1);
   }
-  __device__ __forceinline__ int page_of(const DenseArgs& a, const Place<TILE>& at, int i) const {
+  __device__ __forceinline__ int page_of(const DenseArgs& a, const Walk<TILE>& at, int i) const {
     const unsigned p = (unsigned)(first_box + i) << box_shift;  // (a box that is seen starts below 2^31)
     if (i >= n_boxes || p >= (unsigned)at.g.hi || p + (1u << box_shift) <= (unsigned)at.g.lo) return -1;
     const int page = a.page_table[(size_t)at.r * a.max_pages + (p >> a.page_shift)];
@@ -265,14 +295,14 @@ struct PageFeed {
     record_error(a.err, kErrPage, at.r, 0, page);
     return -1;
   }
-  __device__ __forceinline__ void start(const DenseArgs& a, const Place<TILE>& at, int n_tiles) {
+  __device__ __forceinline__ void start(const DenseArgs& a, const Walk<TILE>& at) {
     first_box = (at.g.lo / TILE + at.t) * boxes;
-    n_boxes = n_tiles * boxes;
+    n_boxes = at.n * boxes;
     cur = page_of(a, at, threadIdx.x & 31);
     nxt = page_of(a, at, 32 + (threadIdx.x & 31));
   }
   // page of this lane's box of the segment's tile k
-  __device__ __forceinline__ int of_tile(const DenseArgs& a, const Place<TILE>& at, int k) {
+  __device__ __forceinline__ int of_tile(const DenseArgs& a, const Walk<TILE>& at, int k) {
     const int b0 = k * boxes;
     if (b0 > 0 && (b0 & 31) == 0) {
       cur = nxt;
@@ -297,20 +327,62 @@ struct PageFeed {
 // ---------------------------------------------------------------------------
 // Joins the pieces of split units and writes the rows of requests without
 // positions: one block of WARPS warps a row, the pieces dealt to the warps,
-// every warp's loads issued before their maxima are looked at.
-template <int D, int ROWS, bool FP8, int WARPS>
+// every warp's loads (kBatch pieces) issued before their maxima are looked at.
+// Which pieces a row has follows from q_pos alone. With up to kJoinScan
+// requests the block works that out before it waits for the main kernel
+// (q_pos is older than that kernel's trigger, which its CTAs give after their
+// own wait), so that behind the wait there is one round of loads and the store.
+template <int D, int ROWS, bool FP8, int TILE, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs a) {
-  constexpr int E = D / 32, kPiece = ROWS * (D + 2), kBatch = 8;
+  constexpr int E = D / 32, kPiece = ROWS * (D + 2), kBatch = 10;
   __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
+  __shared__ long long s_sum[2][WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int orow = blockIdx.x;
   const int rj = orow / a.n_q_heads, h = orow - rj * a.n_q_heads, r = rj / a.n_q, j = rj - r * a.n_q;
   const int g = h / a.group, i = j * a.group + (h - g * a.group);
-  const int rb = i / ROWS, row = i - rb * ROWS;
+  const int rb = i / ROWS, row = i - rb * ROWS, units = a.n_kv_heads * a.row_blocks;
   const float vscale = FP8 ? a.v_scale[g] : 1.f;
-  pdl_wait();
-  const long long desc = a.unit_desc[((long long)r * a.n_kv_heads + g) * a.row_blocks + rb];
-  if (desc == kUnitWhole) return;  // its CTA wrote the row
+  long long desc;
+  if (a.batch <= kJoinScan) {
+    long long all = 0, below = 0;
+    for (int q = threadIdx.x; q < a.batch; q += 32 * WARPS) {
+      const long long t = slots_of(range_of(a, q).tiles(TILE));
+      all += t;
+      below += q < r ? t : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(kFull, all, o);
+      below += __shfl_xor_sync(kFull, below, o);
+    }
+    if (lane == 0) {
+      s_sum[0][warp] = all;
+      s_sum[1][warp] = below;
+    }
+    __syncthreads();
+    all = below = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      all += s_sum[0][w];
+      below += s_sum[1][w];
+    }
+    const int tiles = range_of(a, r).tiles(TILE);
+    desc = kUnitEmpty;
+    if (tiles > 0) {
+      Split sp;
+      sp.init(a, all * units);
+      const long long unit = below * units + (g * a.row_blocks + rb) * slots_of(tiles);
+      const int c0 = sp.first_cta(unit), c1 = sp.last_cta(unit, tiles);
+      desc = c0 == c1 ? kUnitWhole : unit_pieces(c0, c1, sp.piece_slot(unit, c0));
+    }
+    if (desc == kUnitWhole) return;  // its CTA writes the row
+    pdl_wait();
+  } else {
+    pdl_wait();
+    desc = a.unit_desc[(long long)r * units + g * a.row_blocks + rb];
+    if (desc == kUnitWhole) return;
+  }
   float m = kNegInf, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -408,14 +480,16 @@ inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cach
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// the joining kernel: with many rows a unit has few pieces, and one warp joins
-// a row's; with few rows there are up to the grid's number of pieces each
-template <int D, int ROWS, bool FP8>
+// the joining kernel: units that are cut into many pieces (few units on many
+// SMs) get 16 warps a row, whose one round of loads takes up to 160 pieces;
+// else 4 (the odd long request among short ones then takes up to 4 rounds)
+template <int D, int ROWS, bool FP8, int TILE>
 cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
   const unsigned rows = (unsigned)(a.batch * a.n_q * a.n_q_heads);
-  if (rows >= 8u * a.grid)
-    return launch_k(dense_join_kernel<D, ROWS, FP8, 1>, dim3(rows), dim3(32), 0, s, true, a);
-  return launch_k(dense_join_kernel<D, ROWS, FP8, 8>, dim3(rows), dim3(256), 0, s, true, a);
+  const long long units = (long long)a.batch * a.n_kv_heads * a.row_blocks;
+  if (a.grid > 24 * units)
+    return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 16>, dim3(rows), dim3(512), 0, s, true, a);
+  return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 4>, dim3(rows), dim3(128), 0, s, true, a);
 }
 
 // head dim 128 (qsa_dense_tc.cu)

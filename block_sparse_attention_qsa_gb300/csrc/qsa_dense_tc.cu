@@ -277,13 +277,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     mbar_init(smem_u32(&fin), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_wait();     // positions, queries and the cache may come from the kernel before
-  pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
-  Split sp;
-  long long w0, w1;
-  Place<kTile> at;
-  if (!find_start<kTile, C::kThreads>(a, s_start, sp, w0, w1, at)) return;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
   if (warp == C::kPvWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(C::kTmem)
@@ -291,8 +284,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
-  __syncthreads();
+  pdl_wait();     // positions, queries and the cache may come from the kernel before
+  pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
+  Split sp;
+  Walk<kTile> at;
+  const bool work = find_start<kTile, C::kThreads>(a, s_start, sp, at);  // (with a barrier behind the allocation)
   tc_after();
+  auto free_tmem = [&]() {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(C::kTmem) : "memory");
+  };
+  if (!work) {
+    if (warp == C::kPvWarp) free_tmem();
+    return;
+  }
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
   const uint32_t tmem = s_tmem;
 
   if (warp == C::kCopyWarp) {
@@ -302,14 +307,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     const uint32_t dst = (uint32_t)(line * (kTile * 128) + (feed.my_box << feed.box_shift) * 128);
     int slot = 0;
     uint32_t phase = 0;
-    long long w = w0;
     int it = 0;
     bool ok = true;
-    while (w < w1 && ok) {
-      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+    do {
       const int g = at.x / a.row_blocks;
-      feed.start(a, at, n);
-      for (int k = 0; k < n && ok; ++k, ++it) {
+      feed.start(a, at);
+      for (int k = 0; k < at.n && ok; ++k, ++it) {
         const int page = feed.of_tile(a, at, k);
         const uint32_t bad = feed.bad_groups(page);
         const int first = feed.slot_of(a, k), at_page = page < 0 ? a.num_pages : page /* outside: zeros */;
@@ -333,9 +336,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
         }
       }
-      w += n;
-      if (w < w1) at.next_unit(a);
-    }
+    } while (ok && at.next(a));
     if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
       for (int s = 0; s < C::kSlots; ++s) {
         const uint32_t par = s < slot ? phase : phase ^ 1u;
@@ -354,11 +355,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       constexpr int kSteps = C::kRowBytes / 32;  // 32 bytes of a row each
       int it = 0, seg = 0;
       bool ok = true;
-      long long w = w0;
-      while (w < w1 && ok) {
-        const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
+      do {
         ok = __all_sync(kFull, wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u));
-        for (int k = 0; k < n && ok; ++k, ++it) {
+        for (int k = 0; k < at.n && ok; ++k, ++it) {
           const int slot = (2 * it) % C::kSlots;
           ok = __all_sync(kFull, wait(&slot_full[slot], (uint32_t)((2 * it) / C::kSlots) & 1u) &&
                                      (it < 2 || wait(&p_full[it & 1], (uint32_t)((it - 2) >> 1) & 1u)));  // S was read
@@ -383,10 +382,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
           __syncwarp();
         }
-        w += n;
         ++seg;
-        if (w < w1) at.next_unit(a);
-      }
+      } while (ok && at.next(a));
       if (one) commit_tc(&fin);
     }
     __syncwarp();
@@ -398,10 +395,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       constexpr int kSteps = kTile / (FP8 ? 32 : 16), kPos = kTile / kSteps;  // positions of an MMA
       int it = 0;
       bool ok = true;
-      long long w = w0;
-      while (w < w1 && ok) {
-        const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
-        for (int k = 0; k < n && ok; ++k, ++it) {
+      do {
+        for (int k = 0; k < at.n && ok; ++k, ++it) {
           const int slot = (2 * it + 1) % C::kSlots;
           ok = __all_sync(kFull, wait(&p_full[it & 1], (uint32_t)(it >> 1) & 1u) &&
                                      wait(&slot_full[slot], (uint32_t)((2 * it + 1) / C::kSlots) & 1u));
@@ -426,9 +421,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
           __syncwarp();
         }
-        w += n;
-        if (w < w1) at.next_unit(a);
-      }
+      } while (ok && at.next(a));
       // the tensor cores are done before the CTA gives its memory back
       if (one) commit_tc(&fin);
       const long long start = clock64();
@@ -445,7 +438,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(blk * N + col);
 
     // the rows of the unit at `u` into Q buffer `buf`, with what is known of them
-    auto stage_q = [&](const Place<kTile>& u, int buf) {
+    auto stage_q = [&](const Walk<kTile>& u, int buf) {
       const int g = u.x / a.row_blocks, rb = u.x - g * a.row_blocks;
       const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
       const float base_scale = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
@@ -511,16 +504,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     };
 
     stage_q(at, 0);
-    long long w = w0;
     int it = 0, seg = 0;
-    while (w < w1) {
-      const int n = (int)min((long long)(at.tiles - at.t), w1 - w);
-      const int buf = seg & 1;
-      if (w + n < w1) {  // the next unit's rows (the last one's are done with)
-        Place<kTile> next = at;
-        next.next_unit(a);
-        stage_q(next, buf ^ 1);
-      }
+    bool more;
+    do {
+      const int n = at.n, buf = seg & 1;
+      Walk<kTile> following = at;
+      more = following.next(a);
+      if (more) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
       if (t < RC) s_mu[wg][t] = kNoRef;
       if constexpr (WGS == 1)
         group_sync(1 + wg, 128);  // the tables of this unit
@@ -757,10 +747,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       // ---- the segment's end: component t of every row ----
       const int g = at.x / a.row_blocks;
       const bool whole = n == at.tiles;
-      const int pslot = w == w0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
-      if (tid == 0 && at.t == 0)
+      const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
+      if (a.batch > kJoinScan && tid == 0 && at.t == 0)
         a.unit_desc[(long long)at.r * units + at.x] =
-            whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.of_tile(w + at.tiles - 1), pslot);
+            whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.last_cta(at.unit, at.tiles), pslot);
       {
         const float x = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
         if (lane < RC) s_red[wg][quarter][lane] = x;
@@ -809,16 +799,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         }
       }
       tc_before();
-      w += n;
       ++seg;
-      if (w < w1) at.next_unit(a);
-    }
+      at = following;
+    } while (more);
   }
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == C::kPvWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+  if (warp == C::kPvWarp) free_tmem();
 }
 
 template <bool FP8, int RC, int WGS>
@@ -833,7 +821,7 @@ cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const vo
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
   e = launch_k(dense_tc_kernel<C>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_join<kDimTc, C::kRows, FP8>(a, s);
+  return launch_join<kDimTc, C::kRows, FP8, kTileTc>(a, s);
 }
 
 template <bool FP8>

@@ -443,6 +443,15 @@ def test_attn_long_and_wide(qsa, kv, B, ctx, window, n_q):
     _attn_case(qsa, [ctx - 131 * r % 500 for r in range(B)], n_q, 16, 2, 128, 64, kv, window=window)
 
 
+@pytest.mark.parametrize("D,B", [(128, 300), (64, 700), (128, 256), (256, 257)])
+def test_attn_many_requests(qsa, D, B):
+    # more requests than threads, empty ones among them; one long request among
+    # short ones, cut into many pieces
+    ctx = [(37 * r) % 190 if r % 7 else 0 for r in range(B)]
+    ctx[B // 2] = 9000
+    _attn_case(qsa, ctx, 1, 4, 2, D, 16, "bf16")
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_attn_positions_of_any_order(qsa, kv):
     # queries far apart, the same position twice, padding rows between, a page
