@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   float* s_qs = s_l + kComputeWarps * C::kGroupRows;          // [row] softmax scale (exp2 domain)
   __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages];
   __shared__ uint32_t s_bad[C::kStages];  // bit s: slice s of the staged tile has no page
-  __shared__ StartSmem<kThreads> s_start;
+  __shared__ long long s_scan[kWarps];
+  __shared__ Share s_share;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
@@ -177,9 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   pdl_wait();     // positions, queries and the cache may come from the kernel before
   pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
 
-  Split sp;
   Walk<kTile> at;
-  if (!find_start<kTile, kThreads>(a, s_start, sp, at)) return;
+  if (!find_start<kTile, kThreads>(a, s_scan, s_share, at)) return;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
   if (warp >= kComputeWarps) {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           phase ^= 1u;
         }
       }
-    } while (ok && at.next(a));
+    } while (ok && at.next(a, s_share));
     if (s_abort) {
       // copies in flight land before the CTA leaves: the last kStages issued
       // (bounded; a stage whose phase already completed answers at once)
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const bool whole = n == at.tiles;
     const long long unit = (long long)at.r * units + at.x;
     if (a.batch > kJoinScan && tid == 0 && at.t == 0)
-      a.unit_desc[unit] = whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.last_cta(at.unit, at.tiles), pslot);
+      a.unit_desc[unit] = whole ? kUnitWhole : unit_pieces(blockIdx.x, s_share.split.last_cta(at.unit, at.tiles), pslot);
     float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
     const int wrow = warp * C::kGroupRows;
 #pragma unroll
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       compute_sync();
     }
     pslot = 1;
-  } while (at.next(a));
+  } while (at.next(a, s_share));
 }
 
 // ---------------------------------------------------------------------------

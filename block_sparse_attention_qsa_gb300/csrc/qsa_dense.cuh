@@ -16,7 +16,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxSmem = 232448;  // 227 KB a CTA
-constexpr int kMinTiles = 2;      // tiles of a CTA's share at least, where there are
 constexpr long long kWaitCycles = 1LL << 31;  // bound of every wait: about one second
 
 struct DenseArgs {
@@ -134,23 +133,35 @@ __device__ __forceinline__ long long quot(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// The stream, in slots: a unit of T > 0 tiles takes kSegCost + T slots. The
-// first kSegCost hold no tile; they stand for what beginning a unit costs its
-// CTA (query rows, first maximum, the end of the unit before), so that equal
-// shares of slots are about equal work. Without them, one request of 50,000
-// tokens (2 units on 152 SMs) waited 5 of 18 us for the one CTA that had the
-// end of one unit and the beginning of the other. The slots are cut into
-// `ctas` shares, the first `rem` of them one slot longer than `q`.
+// The stream, in slots: a unit of T > 0 tiles takes `seg` + T slots. The first
+// `seg` hold no tile; they stand for what beginning a unit costs its CTA (query
+// rows, first maximum, the end of the unit before), so that equal shares of
+// slots are about equal work. Without them, one request of 50,000 tokens (2
+// units on 152 SMs) waited 5 of 18 us for the one CTA that had the end of one
+// unit and the beginning of the other (measured from 0 to 5 tiles: 3 is best or
+// within 2 % of it at every size). Where there is no more than a tile a CTA, no
+// CTA begins two units, and seg is 0. The slots are cut into `ctas` shares, the
+// first `rem` of them one slot longer than `q`.
 constexpr int kSegCost = 3;
-__device__ __forceinline__ long long slots_of(int tiles) { return tiles > 0 ? tiles + kSegCost : 0; }
+
+// Tiles (bits 0-39) and units that have any (40-63) of some requests, for one
+// unit of each.
+__device__ __forceinline__ long long load_of(int tiles) { return tiles > 0 ? (1LL << 40) + tiles : 0; }
 
 struct Split {
   long long q;
-  int ctas, rem;
-  __device__ __forceinline__ void init(const DenseArgs& a, long long slots) {
-    ctas = (int)min((long long)a.grid, quot(slots + kSegCost + kMinTiles - 1, kSegCost + kMinTiles));
-    q = ctas > 0 ? quot(slots, ctas) : 0;
-    rem = (int)(slots - q * ctas);
+  int ctas, rem, seg;
+  __device__ __forceinline__ long long slots(long long load) const {
+    return (load & ((1LL << 40) - 1)) + (load >> 40) * seg;
+  }
+  __device__ __forceinline__ void init(const DenseArgs& a, long long load) {
+    const int units = a.n_kv_heads * a.row_blocks;
+    const long long tiles = (load & ((1LL << 40) - 1)) * units;
+    seg = tiles > a.grid ? kSegCost : 0;
+    const long long all = slots(load) * units;
+    ctas = (int)min((long long)a.grid, quot(all + seg, seg + 1));
+    q = ctas > 0 ? quot(all, ctas) : 0;
+    rem = (int)(all - q * ctas);
   }
   __device__ __forceinline__ long long begin(int c) const { return c * q + min(c, rem); }
   __device__ __forceinline__ int of_slot(long long w) const {
@@ -158,32 +169,38 @@ struct Split {
     return (int)(w < wide ? quot(w, q + 1) : rem + quot(w - wide, q));
   }
   // the CTAs with tiles of a unit of `tiles` tiles whose slots begin at `unit`
-  __device__ __forceinline__ int first_cta(long long unit) const { return of_slot(unit + kSegCost); }
-  __device__ __forceinline__ int last_cta(long long unit, int tiles) const {
-    return of_slot(unit + kSegCost + tiles - 1);
-  }
+  __device__ __forceinline__ int first_cta(long long unit) const { return of_slot(unit + seg); }
+  __device__ __forceinline__ int last_cta(long long unit, int tiles) const { return of_slot(unit + seg + tiles - 1); }
   // where the first of them has the unit's piece: in its slot 0 if the unit is
   // its first, else in its slot 1 (the unit is then its last)
   __device__ __forceinline__ int piece_slot(long long unit, int cta) const { return begin(cta) < unit ? 1 : 0; }
 };
 
-// A CTA's way through its share w0 .. w1 - 1: segments, each the tiles t .. t
-// + n - 1 of unit x = 0 .. n_kv_heads * row_blocks - 1 of request r (`tiles`
-// in all, its slots beginning at `unit`).
+// What find_start leaves in shared memory: the split and the CTA's share of the
+// stream, slots w0 .. w1 - 1.
+struct Share {
+  Split split;
+  long long w0, w1, first;
+  int first_r;
+};
+
+// A CTA's way through its share: segments, each the tiles t .. t + n - 1 of
+// unit x = 0 .. n_kv_heads * row_blocks - 1 of request r (`tiles` in all, its
+// slots beginning at `unit`).
 template <int TILE>
 struct Walk {
-  long long unit, w0, w1;
+  long long unit;
   int r, x, t, n, tiles;
   Range g;
-  __device__ __forceinline__ bool cut() {  // the share's tiles of this unit
-    const long long first = unit + kSegCost;
+  __device__ __forceinline__ bool cut(const Share& sh) {  // the share's tiles of this unit
+    const long long first = unit + sh.split.seg, w0 = sh.w0;
     t = w0 > first ? (int)(w0 - first) : 0;
-    n = (int)min((long long)tiles, w1 - first) - t;
+    n = (int)min((long long)tiles, sh.w1 - first) - t;
     return n > 0;
   }
-  __device__ __forceinline__ bool next(const DenseArgs& a) {
-    unit += kSegCost + tiles;
-    if (unit + kSegCost >= w1) return false;
+  __device__ __forceinline__ bool next(const DenseArgs& a, const Share& sh) {
+    unit += sh.split.seg + tiles;
+    if (unit + sh.split.seg >= sh.w1) return false;
     if (++x == a.n_kv_heads * a.row_blocks) {
       x = 0;
       do {
@@ -192,15 +209,8 @@ struct Walk {
         tiles = g.tiles(TILE);
       } while (tiles == 0);
     }
-    return cut();
+    return cut(sh);
   }
-};
-
-// Shared memory of find_start.
-template <int THREADS>
-struct StartSmem {
-  long long scan[THREADS / 32], first;
-  int first_r;
 };
 
 // With more requests than this the main kernel writes unit descriptors; with
@@ -208,33 +218,35 @@ struct StartSmem {
 constexpr int kJoinScan = 256;
 
 // Every thread of the block: works the stream out from q_pos (each thread sums
-// the slots of a contiguous run of requests, one block scan) and finds the
+// the tiles of a contiguous run of requests, one block scan) and finds the
 // CTA's share and its first segment. Block 0 reports positions that are none
 // and marks the units that have no tile. False: nothing to do.
 template <int TILE, int THREADS>
-__device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS>& sm, Split& sp, Walk<TILE>& at) {
+__device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)[THREADS / 32], Share& sh,
+                                           Walk<TILE>& at) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += slots_of(range_of(a, r).tiles(TILE));
+  for (int r = r0; r < r1; ++r) mine += load_of(range_of(a, r).tiles(TILE));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(kFull, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) sm.scan[warp] = inc;
+  if (lane == 31) scan[warp] = inc;
   __syncthreads();
   long long before = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    const long long v = sm.scan[w];
+    const long long v = scan[w];
     if (w < warp) before += v;
     total += v;
   }
-  sp.init(a, total * units);
+  Split sp;
+  sp.init(a, total);
   if (blockIdx.x == 0) {
     for (int r = r0; r < r1; ++r) {
       for (int j = 0; j < a.n_q; ++j) {
@@ -246,28 +258,30 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, StartSmem<THREADS
     }
   }
   if ((int)blockIdx.x >= sp.ctas) return false;
-  at.w0 = sp.begin(blockIdx.x);
-  at.w1 = sp.begin(blockIdx.x + 1);
-  if (before * units <= at.w0 && at.w0 < (before + mine) * units) {  // one thread: w0 is in one of its requests
+  const long long w0 = sp.begin(blockIdx.x);
+  if (sp.slots(before) * units <= w0 && w0 < sp.slots(before + mine) * units) {  // one thread: w0 is in one of its requests
+    sh.split = sp;
+    sh.w0 = w0;
+    sh.w1 = sp.begin(blockIdx.x + 1);
     long long b = before;
     for (int r = r0; r < r1; ++r) {
-      const long long t = slots_of(range_of(a, r).tiles(TILE));
-      if (at.w0 < (b + t) * units) {
-        sm.first_r = r;
-        sm.first = b;
+      const long long t = load_of(range_of(a, r).tiles(TILE));
+      if (w0 < sp.slots(b + t) * units) {
+        sh.first_r = r;
+        sh.first = sp.slots(b) * units;
         break;
       }
       b += t;
     }
   }
   __syncthreads();
-  at.r = sm.first_r;
+  at.r = sh.first_r;
   at.g = range_of(a, at.r);
   at.tiles = at.g.tiles(TILE);
-  at.unit = sm.first * units;
-  at.x = (int)quot(at.w0 - at.unit, kSegCost + at.tiles);
-  at.unit += (long long)at.x * (kSegCost + at.tiles);
-  return at.cut();
+  at.unit = sh.first;
+  at.x = (int)quot(w0 - at.unit, sp.seg + at.tiles);
+  at.unit += (long long)at.x * (sp.seg + at.tiles);
+  return at.cut(sh);
 }
 
 // The pages of a segment's boxes (box = the positions that one TMA copy takes,
@@ -326,19 +340,23 @@ struct PageFeed {
 // joining split units
 // ---------------------------------------------------------------------------
 // Joins the pieces of split units and writes the rows of requests without
-// positions: one block of WARPS warps a row, the pieces dealt to the warps,
-// every warp's loads (kBatch pieces) issued before their maxima are looked at.
-// Which pieces a row has follows from q_pos alone. With up to kJoinScan
-// requests the block works that out before it waits for the main kernel
-// (q_pos is older than that kernel's trigger, which its CTAs give after their
-// own wait), so that behind the wait there is one round of loads and the store.
+// positions. WARPS warps a row, the pieces dealt to them (WARPS 1: a block of
+// kJoinRows rows), every warp's loads (kBatch pieces) issued before their
+// maxima are looked at. Which pieces a row has follows from q_pos alone. With
+// up to kJoinScan requests that is worked out before the wait for the main
+// kernel (q_pos is older than that kernel's trigger, which its CTAs give after
+// their own wait), so that behind the wait there is one round of loads and the
+// store.
+constexpr int kJoinRows = 8;
+
 template <int D, int ROWS, bool FP8, int TILE, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs a) {
+__global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) dense_join_kernel(const DenseArgs a) {
   constexpr int E = D / 32, kPiece = ROWS * (D + 2), kBatch = 10;
   __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
   __shared__ long long s_sum[2][WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int orow = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0;
+  const int orow = WARPS > 1 ? blockIdx.x : blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  if (WARPS == 1 && orow >= a.batch * a.n_q * a.n_q_heads) return;
   const int rj = orow / a.n_q_heads, h = orow - rj * a.n_q_heads, r = rj / a.n_q, j = rj - r * a.n_q;
   const int g = h / a.group, i = j * a.group + (h - g * a.group);
   const int rb = i / ROWS, row = i - rb * ROWS, units = a.n_kv_heads * a.row_blocks;
@@ -346,8 +364,8 @@ __global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs 
   long long desc;
   if (a.batch <= kJoinScan) {
     long long all = 0, below = 0;
-    for (int q = threadIdx.x; q < a.batch; q += 32 * WARPS) {
-      const long long t = slots_of(range_of(a, q).tiles(TILE));
+    for (int q = warp * 32 + lane; q < a.batch; q += 32 * WARPS) {
+      const long long t = load_of(range_of(a, q).tiles(TILE));
       all += t;
       below += q < r ? t : 0;
     }
@@ -356,23 +374,25 @@ __global__ void __launch_bounds__(32 * WARPS) dense_join_kernel(const DenseArgs 
       all += __shfl_xor_sync(kFull, all, o);
       below += __shfl_xor_sync(kFull, below, o);
     }
-    if (lane == 0) {
-      s_sum[0][warp] = all;
-      s_sum[1][warp] = below;
-    }
-    __syncthreads();
-    all = below = 0;
+    if constexpr (WARPS > 1) {
+      if (lane == 0) {
+        s_sum[0][warp] = all;
+        s_sum[1][warp] = below;
+      }
+      __syncthreads();
+      all = below = 0;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      all += s_sum[0][w];
-      below += s_sum[1][w];
+      for (int w = 0; w < WARPS; ++w) {
+        all += s_sum[0][w];
+        below += s_sum[1][w];
+      }
     }
     const int tiles = range_of(a, r).tiles(TILE);
     desc = kUnitEmpty;
     if (tiles > 0) {
       Split sp;
-      sp.init(a, all * units);
-      const long long unit = below * units + (g * a.row_blocks + rb) * slots_of(tiles);
+      sp.init(a, all);
+      const long long unit = sp.slots(below) * units + (long long)(g * a.row_blocks + rb) * (sp.seg + tiles);
       const int c0 = sp.first_cta(unit), c1 = sp.last_cta(unit, tiles);
       desc = c0 == c1 ? kUnitWhole : unit_pieces(c0, c1, sp.piece_slot(unit, c0));
     }
@@ -480,16 +500,21 @@ inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cach
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// the joining kernel: units that are cut into many pieces (few units on many
+// The joining kernel: units that are cut into many pieces (few units on many
 // SMs) get 16 warps a row, whose one round of loads takes up to 160 pieces;
-// else 4 (the odd long request among short ones then takes up to 4 rounds)
+// many rows one each (4,096 rows of two or three pieces: 4 warps a row made
+// the whole call 10 us slower); else 4. The odd long request among short ones
+// takes more rounds.
 template <int D, int ROWS, bool FP8, int TILE>
 cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
   const unsigned rows = (unsigned)(a.batch * a.n_q * a.n_q_heads);
   const long long units = (long long)a.batch * a.n_kv_heads * a.row_blocks;
   if (a.grid > 24 * units)
     return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 16>, dim3(rows), dim3(512), 0, s, true, a);
-  return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 4>, dim3(rows), dim3(128), 0, s, true, a);
+  if (rows < 8u * a.grid)
+    return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 4>, dim3(rows), dim3(128), 0, s, true, a);
+  return launch_k(dense_join_kernel<D, ROWS, FP8, TILE, 1>, dim3((rows + kJoinRows - 1) / kJoinRows),
+                  dim3(32 * kJoinRows), 0, s, true, a);
 }
 
 // head dim 128 (qsa_dense_tc.cu)

@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   __shared__ uint32_t s_bad[kBadRing];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
   __shared__ int s_keep;                // a unit's first PV adds to what O holds
   __shared__ volatile int s_abort;
-  __shared__ StartSmem<C::kThreads> s_start;
+  __shared__ long long s_scan[C::kThreads / 32];
+  __shared__ Share s_share;
   __shared__ int2 s_rng[2][C::kRows];   // [buffer][row]: positions the row sees, first and one past the last
   __shared__ int2 s_all[2];             // positions that all rows of the unit see
   __shared__ __align__(16) float s_scale[2][FP8 ? C::kRows : 1];  // softmax scale of a row (BF16: of all)
@@ -286,9 +287,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   tc_before();
   pdl_wait();     // positions, queries and the cache may come from the kernel before
   pdl_trigger();  // the joining kernel may be set up; it waits for this one's end
-  Split sp;
   Walk<kTile> at;
-  const bool work = find_start<kTile, C::kThreads>(a, s_start, sp, at);  // (with a barrier behind the allocation)
+  const bool work = find_start<kTile, C::kThreads>(a, s_scan, s_share, at);  // (with a barrier behind the allocation)
   tc_after();
   auto free_tmem = [&]() {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(C::kTmem) : "memory");
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
         }
       }
-    } while (ok && at.next(a));
+    } while (ok && at.next(a, s_share));
     if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
       for (int s = 0; s < C::kSlots; ++s) {
         const uint32_t par = s < slot ? phase : phase ^ 1u;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           __syncwarp();
         }
         ++seg;
-      } while (ok && at.next(a));
+      } while (ok && at.next(a, s_share));
       if (one) commit_tc(&fin);
     }
     __syncwarp();
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
           __syncwarp();
         }
-      } while (ok && at.next(a));
+      } while (ok && at.next(a, s_share));
       // the tensor cores are done before the CTA gives its memory back
       if (one) commit_tc(&fin);
       const long long start = clock64();
@@ -505,12 +505,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
 
     stage_q(at, 0);
     int it = 0, seg = 0;
-    bool more;
     do {
       const int n = at.n, buf = seg & 1;
-      Walk<kTile> following = at;
-      more = following.next(a);
-      if (more) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
+      {
+        Walk<kTile> following = at;
+        if (following.next(a, s_share)) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
+      }
       if (t < RC) s_mu[wg][t] = kNoRef;
       if constexpr (WGS == 1)
         group_sync(1 + wg, 128);  // the tables of this unit
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
       if (a.batch > kJoinScan && tid == 0 && at.t == 0)
         a.unit_desc[(long long)at.r * units + at.x] =
-            whole ? kUnitWhole : unit_pieces(blockIdx.x, sp.last_cta(at.unit, at.tiles), pslot);
+            whole ? kUnitWhole : unit_pieces(blockIdx.x, s_share.split.last_cta(at.unit, at.tiles), pslot);
       {
         const float x = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
         if (lane < RC) s_red[wg][quarter][lane] = x;
@@ -800,8 +800,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       }
       tc_before();
       ++seg;
-      at = following;
-    } while (more);
+    } while (at.next(a, s_share));
   }
   tc_before();
   __syncthreads();

@@ -24,6 +24,7 @@ qsa_status check_kv_dims(const qsa_dims* d) {
     return QSA_ERR_UNSUPPORTED;
   if (d->kv_dtype != QSA_KV_BF16 && d->kv_dtype != QSA_KV_FP8_E4M3) return QSA_ERR_UNSUPPORTED;
   if (!(d->sm_scale >= 0.f) || isinf(d->sm_scale)) return QSA_ERR_INVALID_ARG;
+  if (d->batch > (1 << 22)) return QSA_ERR_UNSUPPORTED;  // the kernels' request counters
   // 32-bit position and row indexes of the kernels
   if ((long long)d->max_pages * d->page_size >= (1LL << 31)) return QSA_ERR_UNSUPPORTED;
   if ((long long)d->batch * d->n_q * d->n_q_heads >= (1LL << 31)) return QSA_ERR_UNSUPPORTED;

@@ -20,7 +20,8 @@
  *
  * Supported geometry: head_dim 64, 128 or 256; n_q_heads any multiple of
  * n_kv_heads (1..1024 heads); page_size a power of two in 16..256; BF16 or
- * E4M3 cache; n_q 1..4. Anything else returns QSA_ERR_UNSUPPORTED.
+ * E4M3 cache; n_q 1..4; at most 2^22 requests. Anything else returns
+ * QSA_ERR_UNSUPPORTED.
  *
  * A position of -1 stands for no token (a padded batch): nothing is read,
  * written or reported for it, except that qsa_paged_attn writes its output
