@@ -159,7 +159,9 @@ struct Split {
     const long long tiles = (load & ((1LL << 40) - 1)) * units;
     seg = tiles > a.grid ? kSegCost : 0;
     const long long all = slots(load) * units;
-    ctas = (int)min((long long)a.grid, quot(all + seg, seg + 1));
+    static_assert(((kSegCost + 1) & kSegCost) == 0, "the least share, kSegCost + 1 slots, is a power of two");
+    const long long most = seg ? (all + kSegCost) / (kSegCost + 1) : all;
+    ctas = (int)min((long long)a.grid, most);
     q = ctas > 0 ? quot(all, ctas) : 0;
     rem = (int)(all - q * ctas);
   }
@@ -217,15 +219,59 @@ struct Walk {
 // fewer the joining kernel works them out itself while it waits.
 constexpr int kJoinScan = 256;
 
-// Every thread of the block: works the stream out from q_pos (each thread sums
-// the tiles of a contiguous run of requests, one block scan) and finds the
-// CTA's share and its first segment. Block 0 reports positions that are none
-// and marks the units that have no tile. False: nothing to do.
+// Positions that are none are reported once, by block 0.
+__device__ __forceinline__ void report_positions(const DenseArgs& a, int r) {
+  for (int j = 0; j < a.n_q; ++j) {
+    const int p = a.q_pos[(size_t)r * a.n_q + j];
+    if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
+  }
+}
+
+// Every thread of the block: works the stream out from q_pos and finds the
+// CTA's share and its first segment. False: nothing to do. It ends with the
+// block's only barrier (up to 32 requests: every warp works it all out by
+// itself, a lane a request), or has several (each thread sums the tiles of a
+// contiguous run of requests, one block scan; units without a tile are marked).
 template <int TILE, int THREADS>
 __device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)[THREADS / 32], Share& sh,
                                            Walk<TILE>& at) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
+  if (a.batch <= 32) {
+    Range g{0, 0};
+    if (lane < a.batch) g = range_of(a, lane);
+    const int tiles = g.tiles(TILE);
+    const long long mine = load_of(tiles);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    Split sp;
+    sp.init(a, __shfl_sync(kFull, inc, 31));
+    const bool work = (int)blockIdx.x < sp.ctas;
+    const long long w0 = sp.begin(blockIdx.x), unit = sp.slots(inc - mine) * units;
+    const uint32_t in = __ballot_sync(kFull, unit <= w0 && w0 < unit + sp.slots(mine) * units);
+    const int src = in ? __ffs(in) - 1 : 0;  // the request that w0 is in
+    at.r = src;
+    at.g.lo = __shfl_sync(kFull, g.lo, src);
+    at.g.hi = __shfl_sync(kFull, g.hi, src);
+    at.tiles = __shfl_sync(kFull, tiles, src);
+    at.unit = __shfl_sync(kFull, unit, src);
+    if (tid == 0) {
+      sh.split = sp;
+      sh.w0 = w0;
+      sh.w1 = sp.begin(blockIdx.x + 1);
+    }
+    if (blockIdx.x == 0 && warp == 0 && lane < a.batch) report_positions(a, lane);
+    if (work) {
+      at.x = (int)quot(w0 - at.unit, sp.seg + at.tiles);
+      at.unit += (long long)at.x * (sp.seg + at.tiles);
+    }
+    __syncthreads();
+    return work && at.cut(sh);
+  }
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, a.batch), r1 = min(r0 + per, a.batch);
   long long mine = 0;
@@ -249,10 +295,7 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)
   sp.init(a, total);
   if (blockIdx.x == 0) {
     for (int r = r0; r < r1; ++r) {
-      for (int j = 0; j < a.n_q; ++j) {
-        const int p = a.q_pos[(size_t)r * a.n_q + j];
-        if (p != -1 && !valid_pos(a, p)) record_error(a.err, kErrQueryPos, r, j, p);
-      }
+      report_positions(a, r);
       if (a.batch > kJoinScan && range_of(a, r).tiles(TILE) == 0)
         for (int x = 0; x < units; ++x) a.unit_desc[(long long)r * units + x] = kUnitEmpty;
     }
