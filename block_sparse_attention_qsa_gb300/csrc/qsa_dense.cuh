@@ -1,6 +1,24 @@
-// What the two dense-attention kernels share: the stream of tiles and its
-// split, instruction wrappers, tensor maps, and the kernel that joins the
-// pieces of split units. The mathematics is in qsa_dense.cu.
+// Dense attention over the paged cache (decode and verify): the stream of
+// tiles and its split, and the kernel that joins the pieces. The kernel that
+// makes them is in qsa_dense_tc.cuh.
+//
+//   o = sum_t softmax_t(c q . k_t) v_t   over  max(0, p - window + 1) <= t <= p,
+//   lse = ln sum_t exp(c q . k_t)
+//
+// One pass over K and V with the running sum of a softmax (FP32, exp2 domain).
+// All n_q x group query rows that share a KV head are worked on together, so K
+// and V are read once: 4 D flops a row and position against 4 D (BF16) or 2 D
+// (E4M3) bytes, for up to 32 rows a tenth or less of the tensor cores' rate at
+// HBM's. HBM is the bound, and so the work is split by bytes: a unit is one
+// (request, KV head, block of rows), and the units' tiles of 128 positions form
+// one stream that is cut into equal contiguous shares, one per persistent CTA,
+// so that no SM waits for a long request. The lengths are on the device; every
+// CTA works the stream out from q_pos by itself. A unit that ends up in several
+// CTAs leaves (reference, sum, acc) pieces in the workspace, which a second
+// kernel, chained with programmatic dependent launch, joins in the order of
+// the positions: no atomics, the same bits on every call. (One CTA joining the
+// pieces of its unit was not tried: the 76 pieces of a unit of 32 rows are 1.2
+// MB, 10 us for one SM, against 3 for the second kernel.)
 #pragma once
 
 #include <cuda.h>
@@ -560,8 +578,12 @@ cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
                   dim3(32 * kJoinRows), 0, s, true, a);
 }
 
-// head dim 128 (qsa_dense_tc.cu)
-int dense_tc_rows(const qsa_dims& d);  // rows of a unit
-cudaError_t launch_dense_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s);
+// the kernels by head dim (qsa_dense_64.cu, _128.cu, _256.cu); rows: of a unit
+cudaError_t launch_dense_64(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
+                            cudaStream_t s);
+cudaError_t launch_dense_128(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
+                             cudaStream_t s);
+cudaError_t launch_dense_256(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
+                             cudaStream_t s);
 
 }  // namespace qsa

@@ -1,9 +1,9 @@
-// Dense attention for head dim 128 on the fifth-generation tensor cores.
+// Dense attention on the fifth-generation tensor cores.
 //
-// The mathematics, the stream of tiles and its split are qsa_dense.cu's. This
-// kernel takes tiles of 128 positions, and computes both products transposed,
-// so that the long dimension fills the MMA's 128 rows (M) and the few query
-// rows are its columns (N):
+// The mathematics, the stream of tiles and its split are in qsa_dense.cuh.
+// This kernel takes tiles of 128 positions, and computes both products
+// transposed, so that the long dimension fills the MMA's 128 rows (M) and the
+// few query rows are its columns (N):
 //   S^T[position][row] = K Q^T      (A = K, as the cache holds it; B = Q)
 //   O^T[d][row]       += V^T P^T    (A = V read along its other dimension:
 //                                    tcgen05 takes it from the same TMA tile)
@@ -11,14 +11,15 @@
 // TMEM lane) and all 8, 16 or 32 rows of its warpgroup, so there are no
 // shuffles, every row's arithmetic is independent of the others', and at the
 // end of a unit a thread owns one component d of every row: no joint of the
-// warps is left, the pieces go out as they are.
+// warps is left, the pieces go out as they are. K and V never pass through
+// registers. (Head dim 64: the MMA's upper 64 rows repeat the lower ones; 256:
+// two MMAs, two components a thread.)
 //
-// What it is for: with mma.sync the same loop was bound by its warps' issue
-// and latency, not by memory: at 32 rows (4 verify queries x 8 heads), batch
-// 32 and about 55,600 tokens it took 289 us on an E4M3 cache, where the bytes
-// take 136 (fragments are loaded by ldmatrix and E4M3 is widened in
-// registers, about 550 instructions per 16 positions of a warp). Here K and V
-// never pass through registers.
+// Before it the same loop ran on mma.sync, fragments by ldmatrix and E4M3
+// widened in registers, and was bound by its warps' issue and latency: batch
+// 32, about 55,600 tokens, 4 verify queries x 16 heads over 2 KV heads of 128:
+// 318 us with a BF16 cache and 290 with E4M3, where the bytes take 273 and 136;
+// this kernel takes 267 and 154.
 //
 // E4M3 cache: the MMA's operands are E4M3 as well, so the cache's codes are
 // used as they are, and Q and P become two E4M3 terms each, x = hi + lo / 32,
@@ -40,47 +41,65 @@
 // softmax. S and P are double-buffered, so the tensor cores and the copies run
 // ahead of the softmax.
 //
-// Masks: as in qsa_dense.cu. A tile in which a row does not see every position
+// Masks. A tile in which a row does not see every position
 // is an edge tile; there the thread that owns a position that no row sees
-// zeroes its V row in shared memory, and a V row that is not finite is taken
-// out of the MMA and added in FP32 to the rows that see it.
+// zeroes its V row in shared memory, and a V row that only some rows see and
+// that is not finite is taken out of the MMA and added in FP32 to those rows.
+#pragma once
+
 #include "qsa_dense.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kDimTc = 128;
 constexpr int kTileTc = 128;
 constexpr float kRefBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
 constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing: any score passes it
-constexpr int kBadRing = 16;      // page marks of the tiles in flight (at most 6)
+constexpr int kBadRing = 16;      // page marks of the tiles in flight
 
-// RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax warpgroups, BLK:
-// blocks of up to 32 rows, each one set of MMA columns
-template <bool FP8_, int RC_, int WGS_>
+// D: head dim, RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax
+// warpgroups, BLK: blocks of up to 32 rows, each one set of MMA columns
+template <int D_, bool FP8_, int RC_, int WGS_>
 struct Tc {
   static constexpr bool FP8 = FP8_;
-  static constexpr int RC = RC_, WGS = WGS_;
+  static constexpr int D = D_, RC = RC_, WGS = WGS_, EB = FP8 ? 1 : 2;
   static constexpr int kRows = RC * WGS, BLK = kRows > 32 ? kRows / 32 : 1;
-  static constexpr int kRowBytes = kDimTc * (FP8 ? 1 : 2);
-  static constexpr int kLines = kRowBytes / 128;
+  static constexpr int kRowBytes = D * EB;
+  static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a TMA box's row
+  static constexpr int kLines = kRowBytes / kLine, kChunks = kLine / 16;
   static constexpr int kSlot = kTileTc * kRowBytes;  // K or V of a tile
   static constexpr int N = FP8 ? 64 : 32;            // MMA columns of a block (those past its rows idle)
+  static constexpr int MB = D > 128 ? D / 128 : 1;   // blocks of 128 output components
   static constexpr int kQ = N * kRowBytes;           // a block's Q
   static constexpr int kP = kTileTc * 64;            // a block's P: 64 bytes a position
-  static constexpr int kFixed = 2 * BLK * (kQ + kP) + 1024;
-  static constexpr int kStatic = BLK == 1 ? (FP8 ? 2304 : 2048) : 4608;  // barriers and tables
+  // Q of the next unit is staged ahead, but for rows of 512 bytes, where its
+  // buffer would cost the third slot
+  static constexpr int kQBufs = kRowBytes > 256 ? 1 : 2;
+  static constexpr int kFixed = BLK * (kQBufs * kQ + 2 * kP) + 1024;
+  static constexpr int kStatic = BLK == 1 ? (FP8 ? 2560 : 2048) : 4608;  // barriers and tables
   static constexpr int kFit = (kMaxSmem - kStatic - kFixed) / kSlot;
-  static constexpr int kSlots = kFit < 12 ? kFit : 12;
+  static constexpr int kSlots = kFit < 24 ? kFit : 24;
+  // K and V have a ring each: every phase of a slot's barriers is then met by
+  // the same warps (a parity says nothing about a phase two ahead). V, which
+  // stays until its PV is done, has the odd slot.
+  static constexpr int kNK = kSlots / 2, kNV = kSlots - kNK;
   static constexpr int kSmem = kSlots * kSlot + kFixed;
   static constexpr int kThreads = 128 * WGS + 96;
   static constexpr int kCopyWarp = 4 * WGS, kSWarp = kCopyWarp + 1, kPvWarp = kCopyWarp + 2;
   static constexpr uint32_t kO = 2 * BLK * N;        // TMEM: two S buffers, then O
-  static constexpr uint32_t kNeed = 3 * BLK * N;
+  static constexpr uint32_t kNeed = (2 + MB) * BLK * N;
   static constexpr uint32_t kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
-  static constexpr int kPieceFloats = kRows * (kDimTc + 2);
-  static_assert(kSlots >= 4 && kSlots / 2 + 2 < kBadRing, "ring");
+  static constexpr int kPieceFloats = kRows * (D + 2);
+  static_assert(kSlots >= 3 && kNV + 2 < kBadRing && kNeed <= 512, "ring, tensor memory");
+  // where 16-byte chunk c of a line is in row `row` (the TMA and MMA swizzle)
+  static __device__ __forceinline__ int swizzled(int row, int c) {
+    return kLine == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+  }
+  // byte offset of byte `b` of row `row` in a slot
+  static __device__ __forceinline__ int at_byte(int row, int b) {
+    return b / kLine * (kTileTc * kLine) + row * kLine + (swizzled(row, b % kLine / 16) << 4) + b % 16;
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -89,9 +108,9 @@ struct Tc {
 // Shared-memory matrix descriptor: start address >> 4 (bits 0-13), leading
 // byte offset >> 4 (16-29), stride byte offset >> 4 (32-45), version 1
 // (46-47), swizzle mode (61-63: 2 = 128 bytes, 4 = 64 bytes).
-//  K-major, 128-byte rows: 8-row groups are the stride (1,024 bytes).
+//  K-major: 8-row groups are the stride (8 times the row pitch).
 //  MN-major: the stride steps over 8 rows of the k dimension (8 times the row
-//  pitch), the leading offset to the next 128-byte (64-byte) column block.
+//  pitch), the leading offset to the next row-pitch of columns.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle) {
   return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((lead >> 4) & 0x3fffu) << 16) |
          ((uint64_t)((stride >> 4) & 0x3fffu) << 32) | ((uint64_t)1 << 46) | (swizzle << 61);
@@ -239,12 +258,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap tm_v,
                                                                   const DenseArgs a) {
   constexpr bool FP8 = C::FP8;
-  constexpr int RC = C::RC, WGS = C::WGS, BLK = C::BLK, N = C::N, kTile = kTileTc, D = kDimTc;
+  constexpr int RC = C::RC, WGS = C::WGS, BLK = C::BLK, N = C::N, kTile = kTileTc, D = C::D, MB = C::MB;
+  constexpr int kLine = C::kLine, kLines = C::kLines, kChunks = C::kChunks;
+  constexpr uint64_t kSwizzle = kLine == 128 ? 2 : 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = ring + C::kSlots * C::kSlot;   // [buffer][block]
-  uint8_t* s_p = s_q + 2 * BLK * C::kQ;         // [buffer][block]
-  __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
+  uint8_t* s_p = s_q + C::kQBufs * BLK * C::kQ; // [buffer][block]
+  __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];  // K's, then V's
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], fin;
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_bad[kBadRing];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
@@ -303,11 +324,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   if (warp == C::kCopyWarp) {
     // ---- copies: K then V of each tile ----
     PageFeed<kTile> feed(a);
-    const int line = lane >> (7 - feed.box_shift);  // this lane's line of a K or V tile; at most 16 copies
-    const uint32_t dst = (uint32_t)(line * (kTile * 128) + (feed.my_box << feed.box_shift) * 128);
-    int slot = 0;
-    uint32_t phase = 0;
-    int it = 0;
+    const int line = lane >> (7 - feed.box_shift);  // this lane's line of a K or V tile; at most 32 copies
+    const uint32_t dst = (uint32_t)(line * (kTile * kLine) + (feed.my_box << feed.box_shift) * kLine);
+    int slot[2] = {0, 0}, it = 0;
+    uint32_t phase[2] = {0, 0};
     bool ok = true;
     do {
       const int g = at.x / a.row_blocks;
@@ -318,30 +338,33 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const int first = feed.slot_of(a, k), at_page = page < 0 ? a.num_pages : page /* outside: zeros */;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          if (!__all_sync(kFull, wait(&slot_empty[slot], phase ^ 1u))) {
+          const int i = (v ? C::kNK : 0) + slot[v];
+          if (!__all_sync(kFull, wait(&slot_empty[i], phase[v] ^ 1u))) {
             ok = false;
             break;
           }
-          const uint32_t bar = smem_u32(&slot_full[slot]);
+          const uint32_t bar = smem_u32(&slot_full[i]);
           if (lane == 0) {
             if (v == 0) s_bad[it % kBadRing] = bad;
             mbar_expect_tx(bar, C::kSlot);
           }
           __syncwarp();
-          if (line < C::kLines)
-            tma_load_4d(smem_u32(ring + slot * C::kSlot) + dst, v ? &tm_v : &tm_k, line * 64, first, g, at_page, bar);
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1u;
+          if (line < kLines)
+            tma_load_4d(smem_u32(ring + i * C::kSlot) + dst, v ? &tm_v : &tm_k, line * (kLine / C::EB), first, g,
+                        at_page, bar);
+          if (++slot[v] == (v ? C::kNV : C::kNK)) {
+            slot[v] = 0;
+            phase[v] ^= 1u;
           }
         }
       }
     } while (ok && at.next(a, s_share));
     if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
-      for (int s = 0; s < C::kSlots; ++s) {
-        const uint32_t par = s < slot ? phase : phase ^ 1u;
+      for (int i = 0; i < C::kSlots; ++i) {
+        const int v = i >= C::kNK ? 1 : 0;
+        const uint32_t par = i - (v ? C::kNK : 0) < slot[v] ? phase[v] : phase[v] ^ 1u;
         const long long start = clock64();
-        while (!mbar_try_wait(smem_u32(&slot_full[s]), par) && clock64() - start < kWaitCycles / 64) {
+        while (!mbar_try_wait(smem_u32(&slot_full[i]), par) && clock64() - start < kWaitCycles / 64) {
         }
       }
     }
@@ -352,28 +375,29 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     {
       const bool one = elect_one();
       constexpr uint32_t kIdesc = mma_desc<C>(false);
-      constexpr int kSteps = C::kRowBytes / 32;  // 32 bytes of a row each
+      constexpr int kSteps = C::kRowBytes / 32, kPerLine = kLine / 32;  // 32 bytes of a row each
       int it = 0, seg = 0;
       bool ok = true;
       do {
-        ok = __all_sync(kFull, wait(&q_full[seg & 1], (uint32_t)(seg >> 1) & 1u));
+        const int buf = seg % C::kQBufs;
+        ok = __all_sync(kFull, wait(&q_full[buf], (uint32_t)(seg / C::kQBufs) & 1u));
         for (int k = 0; k < at.n && ok; ++k, ++it) {
-          const int slot = (2 * it) % C::kSlots;
-          ok = __all_sync(kFull, wait(&slot_full[slot], (uint32_t)((2 * it) / C::kSlots) & 1u) &&
+          const int slot = it % C::kNK;
+          ok = __all_sync(kFull, wait(&slot_full[slot], (uint32_t)(it / C::kNK) & 1u) &&
                                      (it < 2 || wait(&p_full[it & 1], (uint32_t)((it - 2) >> 1) & 1u)));  // S was read
           if (!ok) break;
           tc_after();
-          const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 1024, 2);
+          const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 8 * kLine, kSwizzle);
 #pragma unroll
           for (int b = 0; b < BLK; ++b) {
-            const uint64_t dq = smem_desc(smem_u32(s_q + ((seg & 1) * BLK + b) * C::kQ), 16, 1024, 2);
+            const uint64_t dq = smem_desc(smem_u32(s_q + (buf * BLK + b) * C::kQ), 16, 8 * kLine, kSwizzle);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-              // (addresses are in units of 16 bytes; a line is 64 BF16 components or all E4M3 ones)
-              const uint32_t line = (uint32_t)(ks >> 2), step = (uint32_t)(ks & 3) * 2u;
+              // (addresses are in units of 16 bytes)
+              const uint32_t line = (uint32_t)(ks / kPerLine), step = (uint32_t)(ks % kPerLine) * 2u;
               if (one)
-                mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * BLK + b) * N), dk + (line * (kTile * 8) + step),
-                            dq + (line * (N * 8) + step), kIdesc, ks > 0);
+                mma_tc<FP8>(tmem + (uint32_t)(((it & 1) * BLK + b) * N), dk + (line * (kTile * kLine / 16) + step),
+                            dq + (line * (N * kLine / 16) + step), kIdesc, ks > 0);
             }
           }
           if (one) {
@@ -397,23 +421,30 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       bool ok = true;
       do {
         for (int k = 0; k < at.n && ok; ++k, ++it) {
-          const int slot = (2 * it + 1) % C::kSlots;
+          const int slot = C::kNK + it % C::kNV;
           ok = __all_sync(kFull, wait(&p_full[it & 1], (uint32_t)(it >> 1) & 1u) &&
-                                     wait(&slot_full[slot], (uint32_t)((2 * it + 1) / C::kSlots) & 1u));
+                                     wait(&slot_full[slot], (uint32_t)(it / C::kNV) & 1u));
           if (!ok) break;
           tc_after();
           const bool fresh = k == 0 && *reinterpret_cast<volatile int*>(&s_keep) == 0;
-          // A: positions as k, 128-byte rows, the second 64 BF16 components one line further on
-          const uint64_t dv = smem_desc(smem_u32(ring + slot * C::kSlot), kTile * 128, 1024, 2);
+          // A: positions as k. Its 128 rows are components: one line of 128,
+          // or two of 64 (leading offset: a line), or one of 64 twice (leading
+          // offset 0; the upper half of O is then a copy)
+          constexpr int kPer = kLine / C::EB;  // components of a line
+          const uint64_t dv = smem_desc(smem_u32(ring + slot * C::kSlot), D >= 128 && kPer == 64 ? kTile * kLine : 0,
+                                        8 * kLine, kSwizzle);
 #pragma unroll
           for (int b = 0; b < BLK; ++b) {
             // B: positions as k, 64-byte rows
             const uint64_t dp = smem_desc(smem_u32(s_p + ((it & 1) * BLK + b) * C::kP), 512, 512, 4);
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks)
-              if (one)
-                mma_tc<FP8>(tmem + C::kO + (uint32_t)(b * N), dv + (uint32_t)(ks * kPos * 8),
-                            dp + (uint32_t)(ks * kPos * 4), kIdesc, !(fresh && ks == 0));
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+              for (int ks = 0; ks < kSteps; ++ks)
+                if (one)
+                  mma_tc<FP8>(tmem + C::kO + (uint32_t)((mb * BLK + b) * N),
+                              dv + (uint32_t)((mb * (128 / kPer) * kTile * kLine + ks * kPos * kLine) / 16),
+                              dp + (uint32_t)(ks * kPos * 4), kIdesc, !(fresh && ks == 0));
           }
           if (one) {
             commit_tc(&pv_done[it & 1]);
@@ -442,10 +473,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       const int g = u.x / a.row_blocks, rb = u.x - g * a.row_blocks;
       const int rows = min(C::kRows, a.n_q * a.group - rb * C::kRows);
       const float base_scale = a.sm_scale * kLog2e * (FP8 ? a.k_scale[g] : 1.f);
-      uint8_t* dst = s_q + (buf * BLK + blk) * C::kQ + col * 128;
+      uint8_t* dst = s_q + (buf * BLK + blk) * C::kQ + col * kLine;
+      constexpr int kLanes = D / 8, kPass = 128 / kLanes;  // 8 components a lane
 #pragma unroll
-      for (int z = 0; z < RC / 8; ++z) {
-        const int r = (t >> 4) + 8 * z, c = t & 15;  // 16 lanes a row, 8 components each
+      for (int z = 0; z < (RC + kPass - 1) / kPass; ++z) {
+        const int r = t / kLanes + kPass * z, c = t % kLanes;
+        if (r >= RC) break;  // (a whole warp)
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row_off + r < rows) {
           const int i = rb * C::kRows + row_off + r, j = i / a.group, h = g * a.group + (i - j * a.group);
@@ -457,7 +490,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
 #pragma unroll
-          for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
           // 2^-sh brings the row's largest value into [2^7, 2^8)
           const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 7));
           const float down = pow2(-sh);
@@ -469,12 +502,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             const float2 f = h2_to_f2(e4m3x2_to_h2(hi[e]));
             lo[e] = e4m3x2((x - f.x) * 32.f, (y - f.y) * 32.f);
           }
-          uint8_t* d8 = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+          const int chunk = c >> 1;
+          uint8_t* d8 = dst + chunk / kChunks * (N * kLine) + r * kLine +
+                        (C::swizzled(col + r, chunk % kChunks) << 4) + (c & 1) * 8;
           *reinterpret_cast<uint2*>(d8) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(d8 + 32 * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          *reinterpret_cast<uint2*>(d8 + 32 * kLine) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
           if (c == 0) s_scale[buf][row_off + r] = base_scale * pow2(sh);
         } else {
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(dst + c / kChunks * (N * kLine) + r * kLine +
+                                    (C::swizzled(col + r, c % kChunks) << 4)) = v;
           if (tid == 0) s_scale[buf][0] = base_scale;
         }
       }
@@ -506,8 +542,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
     stage_q(at, 0);
     int it = 0, seg = 0;
     do {
-      const int n = at.n, buf = seg & 1;
-      {
+      const int n = at.n, buf = seg % C::kQBufs;
+      if constexpr (C::kQBufs == 1) {
+        if (seg > 0) stage_q(at, 0);
+      } else {
         Walk<kTile> following = at;
         if (following.next(a, s_share)) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
       }
@@ -602,13 +640,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             __syncwarp();
             tc_after();
 #pragma unroll 1
-            for (int term = 0; term < (FP8 ? 2 : 1); ++term) {
+            for (int part = 0; part < MB * (FP8 ? 2 : 1); ++part) {
+              const uint32_t addr = o_addr + (uint32_t)(FP8 ? (part >> 1) * (BLK * N) + (part & 1) * 32 : part * (BLK * N));
               uint32_t o[RC];
-              Tmem<RC>::load(o_addr + 32 * term, o);
+              Tmem<RC>::load(addr, o);
               tc_wait_ld();
 #pragma unroll
               for (int r = 0; r < RC; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s_red[wg][0][r]);
-              Tmem<RC>::store(o_addr + 32 * term, o);
+              Tmem<RC>::store(addr, o);
             }
             tc_wait_st();
           }
@@ -621,23 +660,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         }
         if (k == 0 && tid == 0) s_keep = 0;
         if (edge) {
-          const int vs = (2 * it + 1) % C::kSlots;
-          wait(&slot_full[vs], (uint32_t)((2 * it + 1) / C::kSlots) & 1u);
+          const int vs = C::kNK + it % C::kNV;
+          wait(&slot_full[vs], (uint32_t)(it / C::kNV) & 1u);
           uint8_t* vrow = ring + vs * C::kSlot;
           auto zero_row = [&]() {
 #pragma unroll 1
             for (int c = 0; c < C::kRowBytes / 16; ++c)
-              *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kTile * 128) + t * 128 + ((c & 7) << 4)) =
+              *reinterpret_cast<uint4*>(vrow + c / kChunks * (kTile * kLine) + t * kLine + (c % kChunks << 4)) =
                   make_uint4(0, 0, 0, 0);
           };
           bool odd = false;
           if (p < at.g.lo || p >= at.g.hi || !paged) {
             zero_row();
-          } else {
+          } else if (p < all.x || p >= all.y) {  // (what every row sees cannot reach a row that does not)
 #pragma unroll 1
             for (int c = 0; c < C::kRowBytes / 16; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * (kTile * 128) + t * 128 +
-                                                              (((c + lane) & 7) << 4));
+              const uint4 x = *reinterpret_cast<const uint4*>(vrow + c / kChunks * (kTile * kLine) + t * kLine +
+                                                              ((c + lane) % kChunks << 4));
               const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -655,45 +694,45 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             if (k > 0) wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
             __syncwarp();
             tc_after();
-            uint32_t o[RC];
-#pragma unroll
-            for (int r = 0; r < RC; ++r) o[r] = 0;
-            if (k > 0) {
-              Tmem<RC>::load(o_addr, o);
-              tc_wait_ld();
-            } else if (FP8) {
-              Tmem<RC>::store(o_addr + 32, o);
-            }
             group_sync(1 + wg, 128);
 #pragma unroll 1
-            for (int u = 0; u < kTile; ++u) {
-              if (!((s_odd[wg][u >> 5] >> (u & 31)) & 1u)) continue;
-              if (t == u) {
-                uint32_t see = 0;
+            for (int mb = 0; mb < MB; ++mb) {
+              const uint32_t addr = o_addr + (uint32_t)(mb * (BLK * N));
+              const int comp = D < 128 ? t % D : mb * 128 + t;
+              uint32_t o[RC];
 #pragma unroll
-                for (int r = 0; r < RC; ++r) {
-                  const int2 rg = s_rng[buf][row_off + r];
-                  if (p >= rg.x && p < rg.y) see |= 1u << r;
-                  s_red[wg][0][r] = y[r];
+              for (int r = 0; r < RC; ++r) o[r] = 0;
+              if (k > 0) {
+                Tmem<RC>::load(addr, o);
+                tc_wait_ld();
+              } else if (FP8) {
+                Tmem<RC>::store(addr + 32, o);
+              }
+#pragma unroll 1
+              for (int u = 0; u < kTile; ++u) {
+                if (!((s_odd[wg][u >> 5] >> (u & 31)) & 1u)) continue;
+                if (t == u) {
+                  uint32_t see = 0;
+#pragma unroll
+                  for (int r = 0; r < RC; ++r) {
+                    const int2 rg = s_rng[buf][row_off + r];
+                    if (p >= rg.x && p < rg.y) see |= 1u << r;
+                    s_red[wg][0][r] = y[r];
+                  }
+                  s_see[wg] = see;
                 }
-                s_see[wg] = see;
-              }
-              group_sync(1 + wg, 128);
-              float v;
-              if constexpr (FP8) {
-                const uint8_t code = vrow[u * 128 + (((t >> 4) ^ (u & 7)) << 4) + (t & 15)];
-                v = h2_to_f2(e4m3x2_to_h2(code)).x;
-              } else {
-                v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                    vrow + (t >> 6) * (kTile * 128) + u * 128 + ((((t >> 3) & 7) ^ (u & 7)) << 4) + (t & 7) * 2));
-              }
+                group_sync(1 + wg, 128);
+                const uint8_t* at_v = vrow + C::at_byte(u, comp * C::EB);
+                const float v = FP8 ? h2_to_f2(e4m3x2_to_h2(*at_v)).x
+                                    : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at_v) << 16);
 #pragma unroll
-              for (int r = 0; r < RC; ++r)
-                if ((s_see[wg] >> r) & 1u) o[r] = __float_as_uint(fmaf(s_red[wg][0][r], v, __uint_as_float(o[r])));
-              group_sync(1 + wg, 128);
+                for (int r = 0; r < RC; ++r)
+                  if ((s_see[wg] >> r) & 1u) o[r] = __float_as_uint(fmaf(s_red[wg][0][r], v, __uint_as_float(o[r])));
+                group_sync(1 + wg, 128);
+              }
+              Tmem<RC>::store(addr, o);
+              tc_wait_st();
             }
-            Tmem<RC>::store(o_addr, o);
-            tc_wait_st();
             group_sync(3, 128 * WGS);  // every warpgroup has read the rows
             if (odd) {
               zero_row();
@@ -772,30 +811,37 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           if (a.lse && orow >= 0) a.lse[orow] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
       }
-      uint32_t o[RC];
-      Tmem<RC>::load(o_addr, o);
-      if constexpr (FP8) {
-        uint32_t u[RC];
-        Tmem<RC>::load(o_addr + 32, u);
-        tc_wait_ld();
+      if (whole) group_sync(1 + wg, 128);
+#pragma unroll 1
+      for (int mb = 0; mb < MB; ++mb) {
+        const uint32_t addr = o_addr + (uint32_t)(mb * (BLK * N));
+        uint32_t o[RC];
+        Tmem<RC>::load(addr, o);
+        if constexpr (FP8) {
+          uint32_t u[RC];
+          Tmem<RC>::load(addr + 32, u);
+          tc_wait_ld();
 #pragma unroll
-        for (int r = 0; r < RC; ++r)
-          o[r] = __float_as_uint(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(o[r])));
-      } else {
-        tc_wait_ld();
-      }
-      if (!whole) {
-        float* dst = piece + 2 * C::kRows + row_off * D + t;
+          for (int r = 0; r < RC; ++r)
+            o[r] = __float_as_uint(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(o[r])));
+        } else {
+          tc_wait_ld();
+        }
+        const int comp = mb * 128 + t;
+        if (D < 128 && t >= D) continue;  // (a copy; no more barriers here)
+        if (!whole) {
+          float* dst = piece + 2 * C::kRows + row_off * D + comp;
 #pragma unroll
-        for (int r = 0; r < RC; ++r) dst[r * D] = __uint_as_float(o[r]);  // (rows that are none: never read)
-      } else {
-        group_sync(1 + wg, 128);
+          for (int r = 0; r < RC; ++r) dst[r * D] = __uint_as_float(o[r]);  // (rows that are none: never read)
+        } else {
 #pragma unroll
-        for (int r = 0; r < RC; ++r) {
-          const int orow = s_out[buf][row_off + r];
-          // a row that sees nothing (factor 0) is zero whatever O holds
-          const float f = s_red[wg][0][r];
-          if (orow >= 0) a.out[(size_t)orow * D + t] = __float2bfloat16_rn(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
+          for (int r = 0; r < RC; ++r) {
+            const int orow = s_out[buf][row_off + r];
+            // a row that sees nothing (factor 0) is zero whatever O holds
+            const float f = s_red[wg][0][r];
+            if (orow >= 0)
+              a.out[(size_t)orow * D + comp] = __float2bfloat16_rn(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
+          }
         }
       }
       tc_before();
@@ -808,11 +854,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   if (warp == C::kPvWarp) free_tmem();
 }
 
-template <bool FP8, int RC, int WGS>
-cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
-  using C = Tc<FP8, RC, WGS>;
+template <int D, bool FP8, int RC, int WGS>
+cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
+  using C = Tc<D, FP8, RC, WGS>;
   alignas(64) CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, d, k_cache, kTileTc, 128) || !make_cache_map(&tv, d, v_cache, kTileTc, 128))
+  if (!make_cache_map(&tk, d, k_cache, kTileTc, C::kLine) || !make_cache_map(&tv, d, v_cache, kTileTc, C::kLine))
     return cudaErrorInvalidValue;
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(dense_tc_kernel<C>, C::kSmem);
@@ -820,33 +866,20 @@ cudaError_t launch(const qsa_dims& d, DenseArgs a, const void* k_cache, const vo
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
   e = launch_k(dense_tc_kernel<C>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_join<kDimTc, C::kRows, FP8, kTileTc>(a, s);
+  return launch_join<D, C::kRows, FP8, kTileTc>(a, s);
 }
 
-template <bool FP8>
-cudaError_t launch(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, cudaStream_t s) {
+template <int D, bool FP8>
+cudaError_t launch_tc(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, cudaStream_t s) {
   switch (rows) {
-    case 8: return launch<FP8, 8, 1>(d, a, k, v, s);
-    case 16: return launch<FP8, 16, 1>(d, a, k, v, s);
-    case 32: return launch<FP8, 16, 2>(d, a, k, v, s);
-    default: return launch<FP8, 32, 2>(d, a, k, v, s);
+    case 8: return launch_tc<D, FP8, 8, 1>(d, a, k, v, s);
+    case 16: return launch_tc<D, FP8, 16, 1>(d, a, k, v, s);
+    case 32: return launch_tc<D, FP8, 16, 2>(d, a, k, v, s);
+    default:
+      if constexpr (D * (FP8 ? 1 : 2) <= 256) return launch_tc<D, FP8, 32, 2>(d, a, k, v, s);
   }
+  return cudaErrorInvalidValue;  // (not reached: dense_tc_rows)
 }
 
 }  // namespace
-
-// Rows of a unit: a softmax thread's work grows with its warpgroup's rows, so
-// the smallest of 8, 16, 32 (two warpgroups of 16) and 64 (two of 32) that
-// holds them; more rows are several units, which each read K and V.
-int dense_tc_rows(const qsa_dims& d) {
-  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads);
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
-cudaError_t launch_dense_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
-  const int rows = dense_tc_rows(d);
-  return d.kv_dtype == QSA_KV_FP8_E4M3 ? launch<true>(rows, d, a, k_cache, v_cache, s)
-                                       : launch<false>(rows, d, a, k_cache, v_cache, s);
-}
-
 }  // namespace qsa

@@ -356,15 +356,15 @@ def _attn_tol(ref, mag, lse, qk, D, kv, small):
     sum of their magnitudes for each of about D / 8 + 8 partial sums. lse: the
     score's error and a few FP32 steps.
 
-    The weights' rounding: 2^-8 in BF16, 2^-11 in FP16 (E4M3 cache, head dims
-    64 and 256). With an E4M3 cache and head dim 128 a weight p is hi + lo / 32,
-    two E4M3 codes: hi is off by at most 2^-4 p, and lo holds that rest to
-    2^-4 of it, so 2^-8 p in all; below the normal codes lo is off by up to
-    2^-10, that is 2^-15 after the division, where the row's largest weight is
-    at least 2^6: at most 2^-21 of the largest weight for every position."""
+    The weights' rounding: 2^-8 in BF16. With an E4M3 cache a weight p is hi +
+    lo / 32, two E4M3 codes: hi is off by at most 2^-4 p, and lo holds that
+    rest to 2^-4 of it, so 2^-8 p in all; below the normal codes lo is off by
+    up to 2^-10, that is 2^-15 after the division, where the row's largest
+    weight is at least 2^6: at most 2^-21 of the largest weight for every
+    position."""
     eps_s = (D / 8 + 8) * 2.0 ** -23 * qk
-    w = (2.0 ** -11 if kv == "fp8" and D != 128 else 2.0 ** -8) + 2.0 ** -18
-    tiny = 2.0 ** -21 * small if kv == "fp8" and D == 128 else 0.0
+    w = 2.0 ** -8 + 2.0 ** -18
+    tiny = 2.0 ** -21 * small if kv == "fp8" else 0.0
     fin = np.where(np.isfinite(lse), np.abs(lse), 0.0)
     return 2.0 ** -8 * np.abs(ref) + (w + 2 * eps_s)[..., None] * mag + tiny, eps_s + 2.0 ** -18 * (1 + fin)
 
