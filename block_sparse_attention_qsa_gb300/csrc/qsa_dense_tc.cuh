@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
           // 2^-sh brings the row's largest value into [2^7, 2^8)
           const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 7));
-          const float down = pow2(-sh);
+          // (a row with an infinity or NaN: every component NaN, as its scores are)
+          const float down = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : pow2(-sh);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(((it & 1) * BLK + blk) * N + col);
         const int p0 = (at.g.lo / kTile + at.t + k) * kTile, p = p0 + t;
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&s_bad[it % kBadRing]);
-        const bool edge = p0 < all.x || p0 + kTile > all.y || bad != 0;
+        const bool edge = p0 < all.x || all.y - p0 < kTile || bad != 0;
         const bool paged = !((bad >> (t >> 4)) & 1u);
         float y[RC];
         // Scores (exp2 domain) less the reference. Where the reference has to
@@ -790,13 +791,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       if (a.batch > kJoinScan && tid == 0 && at.t == 0)
         a.unit_desc[(long long)at.r * units + at.x] =
             whole ? kUnitWhole : unit_pieces(blockIdx.x, s_share.split.last_cta(at.unit, at.tiles), pslot);
-      {
-        const float x = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
-        if (lane < RC) s_red[wg][quarter][lane] = x;
-      }
+      const float part = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
+      // (behind this wait every warp has arrived with the last tile's P, so
+      // none still reads s_red as that tile's factors)
       wait(&pv_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u);
       __syncwarp();
       tc_after();
+      if (lane < RC) s_red[wg][quarter][lane] = part;
       group_sync(1 + wg, 128);
       float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
       if (t < RC) {  // a row's sum, its factor, and lse
@@ -845,6 +846,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         }
       }
       tc_before();
+      group_sync(1 + wg, 128);  // no warp still reads this unit's tables
       ++seg;
     } while (at.next(a, s_share));
   }

@@ -522,6 +522,23 @@ def test_attn_what_is_masked_never_arrives(qsa, kv, bad, D):
         assert torch.isnan(out[r, 3]).all()  # it sees the newest token (0 * inf and inf - inf are NaN)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_attn_not_finite_queries_stay_in_their_rows(qsa, kv, bad):
+    # a query with an infinity or NaN gives NaN (inf - inf, 0 * inf), the others
+    # the same bits as without it
+    args, lse = _attn_case(qsa, [300, 40], 4, 16, 2, 128, 64, kv)
+    clean, clean_lse = args[8].clone(), lse.clone()
+    args[1][0, 2, 5, 77] = bad
+    args[1][1, 0, 15, 0] = bad
+    qsa.paged_attn(*args, lse=lse)
+    _ok(qsa, args[9])
+    hit = torch.zeros((2, 4, 16), dtype=torch.bool, device="cuda")
+    hit[0, 2, 5] = hit[1, 0, 15] = True
+    assert torch.isnan(args[8][hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(args[8][~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
 def test_attn_infinite_values_arrive(qsa):
     # an infinite V that a row does see gives the infinity that arithmetic gives
     def plant(kc, vc, q, table):
