@@ -172,7 +172,7 @@ PyObject* call(F&& f) {
 const int32_t* i32(void* p) { return static_cast<const int32_t*>(p); }
 
 // rope(args, table_device, x, pos, y, inverse, stream)
-PyObject* fast_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* fast_rope(PyObject* const* a, Py_ssize_t n) {
   if (n != 7) Py_RETURN_NONE;
   Where w;
   if (!w.get(a[6])) Py_RETURN_NONE;
@@ -194,7 +194,7 @@ PyObject* fast_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // kv_append(d, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws, rope args or None, rope's device, q,
 //           q_out, stream)
-PyObject* fast_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* fast_append(PyObject* const* a, Py_ssize_t n) {
   if (n != 15) Py_RETURN_NONE;
   Where w;
   if (!w.get(a[14])) Py_RETURN_NONE;
@@ -230,7 +230,7 @@ PyObject* fast_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // kv_gather(d, k_cache, v_cache, k_scale, v_scale, page_table, pos, k_out, v_out, ws, stream)
-PyObject* fast_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* fast_gather(PyObject* const* a, Py_ssize_t n) {
   if (n != 11) Py_RETURN_NONE;
   Where w;
   if (!w.get(a[10])) Py_RETURN_NONE;
@@ -250,7 +250,7 @@ PyObject* fast_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // paged_attn(d, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, lse, ws, stream)
-PyObject* fast_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* fast_attn(PyObject* const* a, Py_ssize_t n) {
   if (n != 13) Py_RETURN_NONE;
   Where w;
   if (!w.get(a[12])) Py_RETURN_NONE;
@@ -295,13 +295,25 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// A function as Python calls it. What throws on the way (a tensor without
+// storage, a sparse one) is not for the fast path either.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return F(a, n);
+  } catch (...) {
+    if (PyErr_Occurred()) PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+}
+
 #define QSA_METHOD(name, fn) \
-  { name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr }
+  { name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&(fn))), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {QSA_METHOD("bind", bind),
-                          QSA_METHOD("rope", fast_rope),
-                          QSA_METHOD("kv_append", fast_append),
-                          QSA_METHOD("kv_gather", fast_gather),
-                          QSA_METHOD("paged_attn", fast_attn),
+                          QSA_METHOD("rope", guarded<fast_rope>),
+                          QSA_METHOD("kv_append", guarded<fast_append>),
+                          QSA_METHOD("kv_gather", guarded<fast_gather>),
+                          QSA_METHOD("paged_attn", guarded<fast_attn>),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -28,6 +28,10 @@
 //    warps' waiting for one another, 76 us for 2 x 16,385 tokens of 16 + 2 + 2
 //    heads of 128 into an E4M3 cache.
 //  * pair_kernel for the rest: one pair a thread.
+//
+// All kernels here are launched with programmatic dependent launch and wait at
+// their start for what is before them in the stream; none lets its own
+// successor start early (other entry points read their query before they wait).
 #include <algorithm>
 
 #include "qsa_kv_internal.cuh"
@@ -117,6 +121,7 @@ template <int PER, bool IL, bool FP8>
 __global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArgs a) {
   constexpr int kHeads = 32 / PER, D = 16 * PER;  // heads of a pass
   __shared__ __align__(16) float2 s_cs[kWideWarps][kMaxHalf];
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tok = (int)blockIdx.x * kWideWarps + warp;  // (below 2^31)
   if (tok >= a.tokens) return;
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const TokenArgs a) {
   __shared__ float2 s_cs[kPairTok][kMaxHalf];
   __shared__ long long s_row[kPairTok];
   __shared__ int s_live[kPairTok];
+  pdl_wait();
   const int tid = threadIdx.x;
   const int tok0 = (int)blockIdx.x * kPairTok;
   const int half = a.rope.rot_dim >> 1, per_head = a.head_dim / 2;
@@ -305,8 +311,8 @@ cudaError_t launch_wide(const TokenArgs& a, cudaStream_t s) {
   // few tokens: their passes are dealt to several warps, which each work out
   // the angles (32 tokens of 20 heads of 128: 5 parts)
   const unsigned gy = (unsigned)std::max<long long>(1, std::min<long long>(passes, 2LL * device_sm_count() / gx));
-  return a.rope.interleaved ? launch_k(wide_kernel<PER, true, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, false, a)
-                            : launch_k(wide_kernel<PER, false, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, false, a);
+  return a.rope.interleaved ? launch_k(wide_kernel<PER, true, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, true, a)
+                            : launch_k(wide_kernel<PER, false, FP8>, dim3(gx, gy), dim3(32 * kWideWarps), 0, s, true, a);
 }
 template <bool FP8>
 cudaError_t launch_wide(const TokenArgs& a, cudaStream_t s) {
@@ -321,7 +327,7 @@ cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
   const int pairs = (a.hq + 2 * a.hk) * (a.head_dim / 2);
   const dim3 grid((unsigned)((a.tokens + kPairTok - 1) / kPairTok),
                   (unsigned)((pairs + kPairThreads - 1) / kPairThreads));
-  return launch_k(pair_kernel, grid, dim3(kPairThreads), 0, s, false, a);
+  return launch_k(pair_kernel, grid, dim3(kPairThreads), 0, s, true, a);
 }
 
 // Reading back. A block takes kGatherTok tokens, whose cache rows are worked
@@ -349,6 +355,7 @@ struct GatherArgs {
 template <bool FP8>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   __shared__ long long s_row[kGatherTok];
+  pdl_wait();
   const int tid = threadIdx.x;
   const long long tok0 = (long long)blockIdx.x * kGatherTok;
   const int n = (int)min((long long)kGatherTok, a.tokens - tok0);
@@ -483,7 +490,7 @@ cudaError_t launch_kv_gather(const qsa_dims& d, int n_tok, const void* k_cache, 
   const unsigned gx = (unsigned)((a.tokens + kGatherTok - 1) / kGatherTok);
   const unsigned gy = (unsigned)((2 * a.hk * (a.head_dim / 8) + 255) / 256);
   auto kern = d.kv_dtype == QSA_KV_FP8_E4M3 ? gather_kernel<true> : gather_kernel<false>;
-  return launch_k(kern, dim3(gx, gy), dim3(256), 0, s, false, a);
+  return launch_k(kern, dim3(gx, gy), dim3(256), 0, s, true, a);
 }
 
 }  // namespace qsa

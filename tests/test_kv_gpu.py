@@ -698,6 +698,85 @@ def test_other_stream_and_graph(qsa):
     _ok(qsa, ws)
 
 
+def test_two_graphs_share_a_workspace(qsa):
+    # replayed in turn, on one stream; and one call's pieces do not need what
+    # another call of other dims left there
+    args, lse = _attn_case(qsa, [5000, 70, 900], 4, 16, 2, 128, 64, "bf16")
+    d2 = qsa.make_dims(3, 1, 1, args[0].max_pages, args[0].num_pages)
+    q2 = _normal((3, 1, 16, 128), 99)
+    out2, pos2 = torch.empty_like(q2), _i32([[4999], [3], [-1]])
+    args2 = (d2, q2, *args[2:7], pos2, out2, args[9])
+    qsa.paged_attn(*args2)
+    want = args[8].clone(), out2.clone()
+    graphs = []
+    for a in (args, args2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qsa.paged_attn(*a)
+        graphs.append(g)
+    for k in (0, 1, 1, 0, 0, 1):
+        (args, args2)[k][8].zero_()
+        graphs[k].replay()
+        assert torch.equal((args, args2)[k][8], want[k])
+    _ok(qsa, args[9])
+
+
+def test_refusals_on_the_device(qsa):
+    # through the binding, on real tensors: what is wrong is said, nothing runs
+    args, lse = _attn_case(qsa, [100, 7], 2, 16, 2, 128, 64, "fp8")
+    d, q, kc, vc, ks, vs, pt, pos, out, ws = args
+    before = out.clone()
+
+    def attn(err, match, **kw):
+        a = dict(q=q, k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, page_table=pt, q_pos=pos, out=out, ws=ws, lse=lse)
+        a.update(kw)
+        with pytest.raises(err, match=match):
+            qsa.paged_attn(d, **a)
+
+    attn(TypeError, "q: dtype", q=q.half())
+    attn(TypeError, "k_cache: dtype", k_cache=kc.view(torch.int8))
+    attn(ValueError, "q: shape", q=q[:1])
+    attn(ValueError, "out must be contiguous", out=torch.empty_like(q).transpose(0, 1).contiguous().transpose(0, 1))
+    attn(ValueError, "lse: shape", lse=lse[:, :, :8])
+    attn(TypeError, "q_pos: dtype", q_pos=pos.long())
+    attn(ValueError, "CUDA", page_table=pt.cpu())
+    attn(TypeError, "k_scale must be a tensor", k_scale=None)
+    attn(ValueError, "window", window=-1)
+    attn(ValueError, "window", window=1 << 31)
+    attn(ValueError, "ws must be", ws=ws.cpu())
+    attn(qsa.QSAError, "WORKSPACE", ws=ws[:256])
+    attn(qsa.QSAError, "WORKSPACE", ws=ws[8:])
+    rope = qsa.make_rope(128)
+    k = _normal((2, 2, 2, 128), 1)
+    for err, match, kw in [
+        (ValueError, "last dimension", dict(k=_normal((2, 2, 128, 2), 1).transpose(2, 3))),
+        (ValueError, "k: shape", dict(k=k[:, :, :1])),
+        (TypeError, "v: dtype", dict(v=k.float())),
+        (ValueError, "q needs", dict(q=q)),
+        (ValueError, "q needs", dict(q=q, q_out=q, rope=None)),
+        (TypeError, "make_rope", dict(rope=1)),
+        (ValueError, "pos: shape", dict(pos=pos[:, :1].contiguous())),
+        (qsa.QSAError, "INVALID_ARG", dict(q=q, q_out=q.as_strided(q.shape, (0, 2048, 128, 1)))),
+        (qsa.QSAError, "INVALID_ARG", dict(rope=qsa.make_rope(256))),
+    ]:
+        a = dict(k=k, v=k, pos=pos, rope=rope)
+        a.update(kw)
+        with pytest.raises(err, match=match):
+            qsa.kv_append(d, a.pop("k"), a.pop("v"), kc, vc, ks, vs, pt, a.pop("pos"), ws, **a)
+    with pytest.raises(qsa.QSAError, match="INVALID_ARG"):  # no token
+        qsa.rope(rope, q[:, :0], pos[:, :0], q[:, :0])
+    with pytest.raises(ValueError, match="x must be"):
+        qsa.rope(rope, q[0], pos, q[0])
+    with pytest.raises(ValueError, match="k_out: shape"):
+        qsa.kv_gather(d, kc, vc, ks, vs, pt, pos, k[:, :, :1], k, ws)
+    _ok(qsa, ws)
+    assert torch.equal(out, before)
+    # a subclass, a tensor that wants gradients and an empty stream argument are fine
+    qsa.paged_attn(d, torch.nn.Parameter(q), kc, vc, ks, vs, pt, pos, out, ws, stream=torch.cuda.current_stream())
+    _ok(qsa, ws)
+    assert torch.equal(out, before)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_offsets_past_32_bits(qsa, kv):
     # a cache of more than 2^31 elements (2^32 bytes), used at its far end
