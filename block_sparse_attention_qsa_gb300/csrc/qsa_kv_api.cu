@@ -43,12 +43,13 @@ bool check_header(const void* ws, size_t bytes) { return ws && aligned(ws, 256) 
 
 qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
 
-Strided strided(const void* p, const qsa_strides* s, int n_tok, int heads, int dim) {
+// (a dimension of one element has no stride, whatever the caller's says)
+Strided strided(const void* p, const qsa_strides* s, int batch, int n_tok, int heads, int dim) {
   Strided t;
   t.p = static_cast<__nv_bfloat16*>(const_cast<void*>(p));
-  t.head = s ? s->head : dim;
-  t.token = s ? s->token : (long long)heads * dim;
-  t.batch = s ? s->batch : (long long)n_tok * heads * dim;
+  t.head = heads == 1 ? 0 : s ? s->head : dim;
+  t.token = n_tok == 1 ? 0 : s ? s->token : (long long)heads * dim;
+  t.batch = batch == 1 ? 0 : s ? s->batch : (long long)n_tok * heads * dim;
   return t;
 }
 
@@ -125,7 +126,8 @@ qsa_status qsa_rope(const qsa_rope_args* rope, int32_t batch, int32_t n_tok, int
   qsa_status st = check_rope(rope, head_dim, &ro);
   if (st != QSA_OK) return st;
   if (!aligned_all(2, {x, y}) || !aligned(pos, 4)) return QSA_ERR_INVALID_ARG;
-  const Strided xi = strided(x, xs, n_tok, n_heads, head_dim), yo = strided(y, ys, n_tok, n_heads, head_dim);
+  const Strided xi = strided(x, xs, batch, n_tok, n_heads, head_dim);
+  const Strided yo = strided(y, ys, batch, n_tok, n_heads, head_dim);
   if (!writable(yo, batch, n_tok, n_heads) || !in_place_or_apart(xi, yo)) return QSA_ERR_INVALID_ARG;
   return from_cuda(launch_rope(ro, batch, n_tok, n_heads, head_dim, inverse != 0, xi, pos, yo,
                                static_cast<cudaStream_t>(stream)));
@@ -156,14 +158,14 @@ qsa_status qsa_kv_append(const qsa_dims* dims, int32_t n_tok, const qsa_rope_arg
   if (!aligned_all(16, {k_cache, v_cache}) || !aligned_all(2, {k, v, q, q_out}) ||
       !aligned_all(4, {pos, page_table, k_scale, v_scale}))
     return QSA_ERR_INVALID_ARG;
-  const int D = dims->head_dim, hk = dims->n_kv_heads, hq = dims->n_q_heads;
-  const Strided qo = strided(q_out, qos, n_tok, hq, D);
-  const Strided qi = strided(q, qs, n_tok, hq, D);
-  if (q && (!writable(qo, dims->batch, n_tok, hq) || !in_place_or_apart(qi, qo))) return QSA_ERR_INVALID_ARG;
+  const int B = dims->batch, D = dims->head_dim, hk = dims->n_kv_heads, hq = dims->n_q_heads;
+  const Strided qo = strided(q_out, qos, B, n_tok, hq, D);
+  const Strided qi = strided(q, qs, B, n_tok, hq, D);
+  if (q && (!writable(qo, B, n_tok, hq) || !in_place_or_apart(qi, qo))) return QSA_ERR_INVALID_ARG;
   if (!check_header(ws, ws_bytes)) return QSA_ERR_WORKSPACE;
-  return from_cuda(launch_kv_append(*dims, n_tok, ro, strided(k, ks, n_tok, hk, D), strided(v, vs, n_tok, hk, D),
-                                    qi, qo, pos, page_table, k_cache, v_cache, k_scale,
-                                    v_scale, static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_append(*dims, n_tok, ro, strided(k, ks, B, n_tok, hk, D),
+                                    strided(v, vs, B, n_tok, hk, D), qi, qo, pos, page_table, k_cache, v_cache,
+                                    k_scale, v_scale, static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 qsa_status qsa_kv_gather(const qsa_dims* dims, int32_t n_tok, const void* k_cache, const void* v_cache,
