@@ -63,6 +63,7 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.window = window;
   a.grid = sms;
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
+  a.one = 1.f;
   const int rows = unit_rows(d);
   switch (d.head_dim) {
     case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, s);

@@ -50,6 +50,7 @@ struct DenseArgs {
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
   int page_size, page_shift, max_pages, num_pages, window, grid;
   float sm_scale;
+  float one;  // 1
 };
 
 // Unit descriptors: written whole, without positions, or the pieces of CTAs
@@ -457,8 +458,9 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) dense
       const int c0 = sp.first_cta(unit), c1 = sp.last_cta(unit, tiles);
       desc = c0 == c1 ? kUnitWhole : unit_pieces(c0, c1, sp.piece_slot(unit, c0));
     }
-    if (desc == kUnitWhole) return;  // its CTA writes the row
+    // (also where there is nothing to join: this kernel ends behind the main one)
     pdl_wait();
+    if (desc == kUnitWhole) return;  // its CTA writes the row
   } else {
     pdl_wait();
     desc = a.unit_desc[(long long)r * units + g * a.row_blocks + rb];

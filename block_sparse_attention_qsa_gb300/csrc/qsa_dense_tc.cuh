@@ -55,7 +55,7 @@ namespace {
 constexpr int kTileTc = 128;
 constexpr float kRefBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
-constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing: any score passes it
+constexpr float kNoRef = -3.40282347e38f;  // the reference of a row that has seen nothing: the lowest value
 constexpr int kBadRing = 16;      // page marks of the tiles in flight
 
 // D: head dim, RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax
@@ -251,6 +251,52 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
     }
   }
   return v[0];
+}
+
+// arithmetic on pairs of FP32 values: one instruction each
+__device__ __forceinline__ uint64_t pack2(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+  return unpack2(r);
+}
+// Scores of two rows in the exp2 domain less the rows' references: x scale + nmu
+// (nmu = -mu), the product rounded, as it was for the maximum that mu was made
+// from. (One fused operation would leave the product's rounding error over, which
+// from scores of 2^28 on is more than E4M3 has room for, and later more than any
+// weight. `one` is 1, but the assembler does not know: a multiplication and an
+// addition of pairs it fuses, .rn or not.)
+__device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float2 nmu) {
+  return fma2(mul2(x, scale), one, nmu);
+}
+__device__ __forceinline__ float2 pair(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 pair(const uint32_t* v) {
+  return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 template <class C>
@@ -556,11 +602,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       else
         group_sync(3, 128 * WGS);
       const int2 all = s_all[buf];
-      float mu[RC], l[RC];
+      float nmu[RC], l[RC];  // the rows' references (negated) and sums
       const float sc = FP8 ? 0.f : s_scale[buf][0];
 #pragma unroll
       for (int r = 0; r < RC; ++r) {
-        mu[r] = 0.f;
+        nmu[r] = 0.f;
         l[r] = 0.f;
       }
 
@@ -590,13 +636,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
               Tmem<RC>::load(s_addr + 32, u);
               tc_wait_ld();
 #pragma unroll
-              for (int r = 0; r < RC; ++r)
-                y[r] = fmaf(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r])), s_scale[buf][row_off + r],
-                            -mu[r]);
+              for (int r = 0; r < RC; r += 2) {
+                const float2 x = less(fma2(pair(u + r), both(0.03125f), pair(v + r)),
+                                      pair(&s_scale[buf][row_off + r]), both(a.one), pair(nmu + r));
+                y[r] = x.x;
+                y[r + 1] = x.y;
+              }
             } else {
               tc_wait_ld();
 #pragma unroll
-              for (int r = 0; r < RC; ++r) y[r] = fmaf(__uint_as_float(v[r]), sc, -mu[r]);
+              for (int r = 0; r < RC; r += 2) {
+                const float2 x = less(pair(v + r), both(sc), both(a.one), pair(nmu + r));
+                y[r] = x.x;
+                y[r + 1] = x.y;
+              }
             }
           }
           if (edge) {
@@ -608,13 +661,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           }
           if (moved) break;
           if (!raw) {
-            bool grew = false;
+            float top = kNegInf;
 #pragma unroll
-            for (int r = 0; r < RC; ++r) grew |= y[r] > kRefMost;
-            if (!group_any(1 + wg, 128, grew)) break;
+            for (int r = 0; r < RC; r += 2) top = max3(top, y[r], y[r + 1]);
+            if (!group_any(1 + wg, 128, top > kRefMost)) break;
             raw = true;
 #pragma unroll
-            for (int r = 0; r < RC; ++r) mu[r] = 0.f;
+            for (int r = 0; r < RC; ++r) nmu[r] = 0.f;
             continue;
           }
           {
@@ -633,7 +686,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           group_sync(1 + wg, 128);
 #pragma unroll
           for (int r = 0; r < RC; ++r) {
-            mu[r] = s_mu[wg][r];
+            nmu[r] = -s_mu[wg][r];
             l[r] *= s_red[wg][0][r];
           }
           if (k > 0) {  // what O holds so far
@@ -655,9 +708,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           moved = true;
         }
 #pragma unroll
-        for (int r = 0; r < RC; ++r) {
+        for (int r = 0; r < RC; r += 2) {
           y[r] = exp2_sfu(y[r]);
-          l[r] += y[r];
+          y[r + 1] = exp2_sfu(y[r + 1]);
+          const float2 x = add2(pair(l + r), pair(y + r));
+          l[r] = x.x;
+          l[r + 1] = x.y;
         }
         if (k == 0 && tid == 0) s_keep = 0;
         if (edge) {
@@ -753,7 +809,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           for (int r = 0; r < RC; r += 2) {
             hi[r / 2] = e4m3x2(y[r], y[r + 1]);
             const float2 f = h2_to_f2(e4m3x2_to_h2(hi[r / 2]));
-            lo[r / 2] = e4m3x2((y[r] - f.x) * 32.f, (y[r + 1] - f.y) * 32.f);
+            const float2 x = mul2(add2(pair(y + r), make_float2(-f.x, -f.y)), both(32.f));
+            lo[r / 2] = e4m3x2(x.x, x.y);
           }
           const int c0 = col / 16;  // a 16-byte chunk has 16 rows: hi in chunks 0 and 1, lo in 2 and 3
           if constexpr (RC == 8) {
@@ -805,7 +862,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const float ref = s_mu[wg][t];
         const int orow = s_out[buf][row_off + t];
         if (!whole) {
-          piece[row_off + t] = ref == kNoRef ? kNegInf : ref;
+          piece[row_off + t] = sum == 0.f ? kNegInf : ref;
           piece[C::kRows + row_off + t] = sum;
         } else {
           s_red[wg][0][t] = sum == 0.f ? 0.f : (FP8 ? a.v_scale[g] : 1.f) / sum;
@@ -880,7 +937,7 @@ cudaError_t launch_tc(int rows, const qsa_dims& d, const DenseArgs& a, const voi
     default:
       if constexpr (D * (FP8 ? 1 : 2) <= 256) return launch_tc<D, FP8, 32, 2>(d, a, k, v, s);
   }
-  return cudaErrorInvalidValue;  // (not reached: dense_tc_rows)
+  return cudaErrorInvalidValue;  // (not reached: unit_rows)
 }
 
 }  // namespace

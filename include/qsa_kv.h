@@ -40,7 +40,7 @@ extern "C" {
  * dimension is contiguous. A NULL pointer to it means a contiguous tensor. A
  * stride of an input may be 0 (a broadcast input); the elements of an output
  * must not overlap, and one of its strides may be 0 only where its dimension
- * has one element. */
+ * has one element (the stride of such a dimension is not looked at). */
 typedef struct {
   int64_t batch, token, head;
 } qsa_strides;
@@ -161,7 +161,9 @@ qsa_status qsa_kv_gather(const qsa_dims* dims, int32_t n_tok, const void* k_cach
  * out. K and V outside a query's positions never reach its output, whatever
  * they hold. A row without positions (p = -1, or p below -1 or past the page
  * table, which is reported as kind 1) gives zeros and an lse of -infinity, as
- * does a row whose scores are all -infinity. A page id outside the cache is
+ * does a row whose scores are all -infinity. The sums before the division by
+ * the softmax's are FP32, with weights up to 2^8: values of 2^(119 - log2 of the
+ * positions) or more may overflow in them. A page id outside the cache is
  * reported (kind 2) and its positions are left out. The cache's positions are
  * split over the GPU and the pieces joined in a fixed order: the same call
  * gives the same bits. q and out are contiguous, as for qsa_sparse_attn. */

@@ -128,6 +128,16 @@ def test_rope_strides(qsa):
     assert torch.equal(want, packed)
 
 
+def test_rope_strides_of_single_elements(qsa):
+    # a dimension of one element has no stride: in place through another view
+    # of the same rows, and an odd stride of it does not matter
+    x = _normal((1, 1, 4, 64), 7)
+    want, rope, pos = torch.empty_like(x), qsa.make_rope(64), _i32([[1234]])
+    qsa.rope(rope, x, pos, want)
+    qsa.rope(rope, x.as_strided(x.shape, (9, 7, 64, 1)), pos, x.as_strided(x.shape, (1, 256, 64, 1)))
+    assert torch.equal(x, want)
+
+
 def test_rope_gradient(qsa):
     # inverse is the gradient: the transpose of the forward matrix (formula),
     # and <dy, rope(x + h e) - rope(x - h e)> / 2h (differences)
@@ -562,6 +572,68 @@ def test_attn_infinite_values_arrive(qsa):
     assert torch.isfinite(out[0, 2:, :, rest]).all()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_lowest_scores(qsa, kv):
+    # scores near the lowest FP32 value are still scores: 1.44 x 2.6 x 2^126 in
+    # the exp2 domain is -3.19e38
+    args, lse = _attn_case(qsa, [1, 2, 700], 1, 16, 2, 64, 64, kv, sm_scale=2.6)
+    d, q, kc, vc, ks, vs = args[:6]
+    q.zero_()
+    kc.zero_()
+    # q . k = -2^126 everywhere: BF16 -2^63 x 2^63, E4M3 -2^119 x 2^7 (code 0x70)
+    q[..., 0] = -2.0 ** (63 if kv == "bf16" else 119)
+    kc[..., 0] = 2.0 ** 63 if kv == "bf16" else 0x70
+    if kv == "fp8":
+        ks.fill_(1.0)
+    qsa.paged_attn(*args, lse=lse)
+    got, pos = R.f64(args[8]), args[7].cpu().numpy()
+    v = R.f64(vc) * (R.f64(vs)[None, :, None, None] if kv == "fp8" else 1.0)
+    table = args[6].cpu().numpy()
+    for r in range(3):
+        t = np.arange(pos[r, 0] + 1)
+        rows = v[table[r][t // 64], :, t % 64]  # [t][H_kv][D]
+        want, size = rows.mean(axis=0), np.abs(rows).mean(axis=0)
+        # equal weights, all exact: FP32 sums (2^-18 covers 700 of them) and one rounding
+        tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -18 * size
+        assert np.all(np.abs(got[r, 0] - np.repeat(want, 8, axis=0)) <= np.repeat(tol, 8, axis=0)), r
+    assert np.allclose(R.f64(lse), -2.6 * 2.0 ** 126, rtol=1e-6)
+    _ok(qsa, args[9])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("up", [24, 28, 32, 60])
+def test_attn_huge_scores(qsa, kv, up):
+    # scores of 2^up and more, whose FP32 steps are of any size: one weight is
+    # all there is (the reference's gap of a row's two largest scores says for
+    # which rows), and a row of one position gives its value
+    args, lse = _attn_case(qsa, [1, 2, 130, 700], 2, 16, 2, 128, 64, kv)
+    d, q, kc, vc, ks, vs = args[:6]
+    q.mul_(2.0 ** up)
+    qsa.paged_attn(*args, lse=lse)
+    k, v = R.f64(kc), R.f64(vc)
+    if kv == "fp8":
+        k, v = k * R.f64(ks)[None, :, None, None], v * R.f64(vs)[None, :, None, None]
+    got, got_lse, q64, pos, table = R.f64(args[8]), R.f64(lse), R.f64(q), args[7].cpu().numpy(), args[6].cpu().numpy()
+    sure = 0
+    for r, j in np.ndindex(pos.shape):
+        t = np.arange(pos[r, j] + 1)
+        if not len(t):
+            continue
+        for h in range(16):
+            rows = k[table[r][t // 64], h // 8, t % 64]
+            s = rows @ q64[r, j, h] / math.sqrt(128)
+            best, size = s.argmax(), (np.abs(rows) @ np.abs(q64[r, j, h])).max() / math.sqrt(128)
+            # FP32 sums of 128 products, Q down to 2^-23 of its largest value: 2^-15 of the sum of magnitudes
+            assert abs(got_lse[r, j, h] - s[best]) <= 2.0 ** -15 * size + 10
+            if np.delete(s, best).max(initial=-np.inf) < s[best] - 2.0 ** -14 * size - 40:
+                want = v[table[r][t[best] // 64], h // 8, t[best] % 64]
+                # one weight: the roundings of P and of the output, 2^-8 each
+                assert np.all(np.abs(got[r, j, h] - want) <= (2.0 ** -7 + 2.0 ** -14) * np.abs(want) + 2.0 ** -18), (r, j, h)
+                sure += 1
+    assert sure > 90  # of 7 x 16
+    _ok(qsa, args[9])
+
+
 def test_attn_reports_and_skips(qsa):
     ps, hk, D = 16, 2, 128
     table, num_pages = R.page_table([100, 100], ps, 9)
@@ -696,6 +768,84 @@ def test_other_stream_and_graph(qsa):
         torch.cuda.synchronize()
         assert torch.equal(out, ref[0])
     _ok(qsa, ws)
+
+
+def test_what_follows_waits_for_whole_units(qsa):
+    # every CTA has one whole unit, so the joining kernel has nothing to join:
+    # it still must not end before the kernel that writes the rows
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B, n = sms // 2, 8192
+    per = n // 256
+    d = _dims(qsa, B, per, B * per, "bf16", 1, ps=256)
+    kc, vc = (torch.randn((B * per, 2, 256, 128), device="cuda").to(torch.bfloat16) for _ in range(2))
+    pt = torch.randperm(B * per, device="cuda").to(torch.int32).view(B, per)
+    pos = torch.full((B, 1), n - 1, dtype=torch.int32, device="cuda")
+    q, ws = _normal((B, 1, 16, 128), 57), qsa.make_kv_workspace(d)
+    out, turned = torch.empty_like(q), torch.empty_like(q)
+    rope = qsa.make_rope(128)
+
+    def step():
+        qsa.paged_attn(d, q, kc, vc, None, None, pt, pos, out, ws)
+        qsa.rope(rope, out, pos, turned)
+
+    step()
+    torch.cuda.synchronize()
+    want = out.clone(), turned.clone()
+    assert not torch.isnan(out).any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        kept = out.clone()
+    for _ in range(5):
+        out.fill_(math.nan)
+        step()
+        got = out.clone()
+        assert torch.equal(got, want[0]) and torch.equal(turned, want[1])
+        out.fill_(math.nan)
+        qsa.paged_attn(d, q, kc, vc, None, None, pt, pos, out, ws)
+        assert torch.equal(out.clone(), want[0])
+        out.fill_(math.nan)
+        graph.replay()
+        assert torch.equal(kept, want[0]) and torch.equal(turned, want[1])
+    _ok(qsa, ws)
+
+
+def test_captured_branches(qsa):
+    # two branches of a captured graph (one rotates and appends, one reads
+    # older rows back) that meet in the attention
+    B, ps = 2, 64
+    ctx = [500, 130]
+    table, num_pages = R.page_table(ctx, ps, 61)
+    d = _dims(qsa, B, table.shape[1], num_pages)
+    kc, vc, _, _ = R.make_cache(num_pages, 2, ps, 128, "bf16", 62)
+    pt, pos = table.cuda(), _i32([[c - 1] for c in ctx])
+    old = _i32([[3, 77, 400], [0, 128, 5]])
+    qkv, rope = _normal((B, 1, 20, 128), 63), qsa.make_rope(128)
+    ws, ws2 = qsa.make_kv_workspace(d), qsa.make_kv_workspace(d)
+    q_rot, out = (torch.empty((B, 1, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ko, vo = (torch.zeros((B, 3, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step(main, other):
+        other.wait_stream(main)
+        qsa.kv_gather(d, kc, vc, None, None, pt, old, ko, vo, ws2, stream=other)
+        qsa.kv_append(d, qkv[:, :, 16:18], qkv[:, :, 18:], kc, vc, None, None, pt, pos, ws, rope=rope,
+                      q=qkv[:, :, :16], q_out=q_rot, stream=main)
+        main.wait_stream(other)
+        qsa.paged_attn(d, q_rot, kc, vc, None, None, pt, pos, out, ws, stream=main)
+
+    side = torch.cuda.Stream()
+    step(torch.cuda.current_stream(), side)
+    want = [t.clone() for t in (out, ko, vo, kc, vc)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(torch.cuda.current_stream(), side)
+    for _ in range(3):
+        for t in (out, ko, vo):
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip((out, ko, vo, kc, vc), want))
+    _ok(qsa, ws)
+    _ok(qsa, ws2)
 
 
 def test_two_graphs_share_a_workspace(qsa):
