@@ -19,7 +19,7 @@
 // widened in registers, and was bound by its warps' issue and latency: batch
 // 32, about 55,600 tokens, 4 verify queries x 16 heads over 2 KV heads of 128:
 // 318 us with a BF16 cache and 290 with E4M3, where the bytes take 273 and 136;
-// this kernel takes 267 and 154.
+// this kernel takes 267 and 149.
 //
 // E4M3 cache: the MMA's operands are E4M3 as well, so the cache's codes are
 // used as they are, and Q and P become two E4M3 terms each, x = hi + lo / 32,
@@ -41,8 +41,8 @@
 // softmax. S and P are double-buffered, so the tensor cores and the copies run
 // ahead of the softmax.
 //
-// Masks. A tile in which a row does not see every position
-// is an edge tile; there the thread that owns a position that no row sees
+// Masks. A tile in which a row does not see every position is an edge tile
+// (positions without a page are scored -inf, and the copies fill zeros); there the thread that owns a position that no row sees
 // zeroes its V row in shared memory, and a V row that only some rows see and
 // that is not finite is taken out of the MMA and added in FP32 to those rows.
 #pragma once
@@ -55,7 +55,7 @@ namespace {
 constexpr int kTileTc = 128;
 constexpr float kRefBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
-constexpr float kNoRef = -3.40282347e38f;  // the reference of a row that has seen nothing: the lowest value
+constexpr float kNoRef = __builtin_huge_valf();  // the reference of a row that has seen nothing (its scores are less 0)
 constexpr int kBadRing = 16;      // page marks of the tiles in flight
 
 // D: head dim, RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax
@@ -293,6 +293,11 @@ __device__ __forceinline__ float2 pair(const uint32_t* v) {
   return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   __shared__ __align__(16) float s_scale[2][FP8 ? C::kRows : 1];  // softmax scale of a row (BF16: of all)
   __shared__ int s_out[2][C::kRows];    // [buffer][row]: its row of q and out, -1: none
   __shared__ float s_red[WGS][4][RC];
-  __shared__ __align__(16) float s_mu[WGS][RC];
+  __shared__ __align__(16) float s_mu[WGS][RC], s_nmu[WGS][RC];
   __shared__ uint32_t s_odd[WGS][4];    // positions whose V is not finite
   __shared__ uint32_t s_see[WGS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -596,20 +601,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         Walk<kTile> following = at;
         if (following.next(a, s_share)) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
       }
-      if (t < RC) s_mu[wg][t] = kNoRef;
+      if (t < RC) {
+        s_mu[wg][t] = kNoRef;
+        s_nmu[wg][t] = 0.f;
+      }
       if constexpr (WGS == 1)
         group_sync(1 + wg, 128);  // the tables of this unit
       else
         group_sync(3, 128 * WGS);
       const int2 all = s_all[buf];
-      float nmu[RC], l[RC];  // the rows' references (negated) and sums
+      float l[RC];
       const float sc = FP8 ? 0.f : s_scale[buf][0];
 #pragma unroll
-      for (int r = 0; r < RC; ++r) {
-        nmu[r] = 0.f;
-        l[r] = 0.f;
-      }
-
+      for (int r = 0; r < RC; ++r) l[r] = 0.f;
+      bool fresh = true;  // a row has no reference yet
       for (int k = 0; k < n; ++k, ++it) {
         const bool ok = wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u);
         (void)ok;  // given up: the loop runs on without meaning, to the same barriers
@@ -618,75 +623,92 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(((it & 1) * BLK + blk) * N + col);
         const int p0 = (at.g.lo / kTile + at.t + k) * kTile, p = p0 + t;
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&s_bad[it % kBadRing]);
-        const bool edge = p0 < all.x || all.y - p0 < kTile || bad != 0;
+        const bool edge = p0 < all.x || all.y - p0 < kTile;
         const bool paged = !((bad >> (t >> 4)) & 1u);
         float y[RC];
-        // Scores (exp2 domain) less the reference. Where the reference has to
-        // move, and in a unit's first tile, they are taken as they are first
-        // (mu = 0), for the rows' maxima; then again. (One copy of the code:
-        // what runs once a unit runs from a cold instruction cache, where its
-        // length is its cost.)
-        bool raw = k == 0, moved = false;
-        while (true) {
-          {
-            uint32_t v[RC];
-            Tmem<RC>::load(s_addr, v);
-            if constexpr (FP8) {
-              uint32_t u[RC];
-              Tmem<RC>::load(s_addr + 32, u);
-              tc_wait_ld();
+        // Scores (exp2 domain) less the rows' references. (16 rows at a time, and
+        // the references from shared memory: with more in registers 64 rows of an
+        // E4M3 cache spilled, 155 us for 120.)
+        constexpr int kPart = RC < 16 ? RC : 16;
 #pragma unroll
-              for (int r = 0; r < RC; r += 2) {
-                const float2 x = less(fma2(pair(u + r), both(0.03125f), pair(v + r)),
-                                      pair(&s_scale[buf][row_off + r]), both(a.one), pair(nmu + r));
-                y[r] = x.x;
-                y[r + 1] = x.y;
-              }
-            } else {
-              tc_wait_ld();
+        for (int r0 = 0; r0 < RC; r0 += kPart) {
+          uint32_t v[kPart];
+          Tmem<kPart>::load(s_addr + r0, v);
+          if constexpr (FP8) {
+            uint32_t u[kPart];
+            Tmem<kPart>::load(s_addr + 32 + r0, u);
+            tc_wait_ld();
 #pragma unroll
-              for (int r = 0; r < RC; r += 2) {
-                const float2 x = less(pair(v + r), both(sc), both(a.one), pair(nmu + r));
-                y[r] = x.x;
-                y[r + 1] = x.y;
-              }
+            for (int r = 0; r < kPart; r += 2) {
+              const float2 x = less(fma2(pair(u + r), both(0.03125f), pair(v + r)),
+                                    pair(&s_scale[buf][row_off + r0 + r]), both(a.one), pair(&s_nmu[wg][r0 + r]));
+              y[r0 + r] = x.x;
+              y[r0 + r + 1] = x.y;
+            }
+          } else {
+            tc_wait_ld();
+#pragma unroll
+            for (int r = 0; r < kPart; r += 2) {
+              const float2 x = less(pair(v + r), both(sc), both(a.one), pair(&s_nmu[wg][r0 + r]));
+              y[r0 + r] = x.x;
+              y[r0 + r + 1] = x.y;
             }
           }
-          if (edge) {
+        }
+        if (edge || bad != 0) {
+#pragma unroll
+          for (int r = 0; r < RC; ++r) {
+            const int2 rg = s_rng[buf][row_off + r];
+            if (p < rg.x || p >= rg.y || !paged) y[r] = kNegInf;
+          }
+        }
+        // Where a score passes its reference by too much, and as long as a row of
+        // the unit has seen nothing yet, the references move to the maxima; scores
+        // and sums follow by the difference. (The warps' vote is 3 of the 149 us of
+        // batch 32 with E4M3. Voting through an mbarrier with the exponentials
+        // before its wait was slower, 152, and so was a second pass over the scores
+        // in place of the difference, for the length of its code.)
+        bool move = fresh;
+        if (fresh) {
+          if (k > 0) group_sync(1 + wg, 128);  // (s_red has been read)
+        } else {
+          float top = kNegInf;
+#pragma unroll
+          for (int r = 0; r < RC; r += 2) top = max3(top, y[r], y[r + 1]);
+          move = group_any(1 + wg, 128, top > kRefMost);
+        }
+        if (move) {
+          {
+            float top = 0.f;
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
-              const int2 rg = s_rng[buf][row_off + r];
-              if (p < rg.x || p >= rg.y || !paged) y[r] = kNegInf;
+              const float x = warp_max(y[r]);
+              if (lane == r) top = x;
             }
-          }
-          if (moved) break;
-          if (!raw) {
-            float top = kNegInf;
-#pragma unroll
-            for (int r = 0; r < RC; r += 2) top = max3(top, y[r], y[r + 1]);
-            if (!group_any(1 + wg, 128, top > kRefMost)) break;
-            raw = true;
-#pragma unroll
-            for (int r = 0; r < RC; ++r) nmu[r] = 0.f;
-            continue;
-          }
-          {
-            const float x = reduce_rows<RC>(y, [](float c, float d) { return fmaxf(c, d); });
-            if (lane < RC) s_red[wg][quarter][lane] = x;
+            if (lane < RC) s_red[wg][quarter][lane] = top;
           }
           group_sync(1 + wg, 128);
+          bool unseen = false;
           if (t < RC) {
             const float top = fmaxf(fmaxf(s_red[wg][0][t], s_red[wg][1][t]), fmaxf(s_red[wg][2][t], s_red[wg][3][t]));
             const float from = s_mu[wg][t];
-            const float to =
-                top > from + kRefMost || from == kNoRef ? fmaxf(top - kRefBelow, kNoRef) : from;
-            s_red[wg][0][t] = exp2_sfu(from - to);  // the row's factor
-            s_mu[wg][t] = to;
+            const bool none = from == kNoRef;
+            // by how much the row's reference moves
+            const float by = none ? (top > kNegInf ? top - kRefBelow : 0.f) : top > kRefMost ? top - kRefBelow : 0.f;
+            s_red[wg][0][t] = none ? 1.f : exp2_sfu(-by);  // the row's factor
+            s_red[wg][1][t] = by;
+            if (!none || top > kNegInf) {
+              const float to = (none ? 0.f : from) + by;
+              s_mu[wg][t] = to;
+              s_nmu[wg][t] = to == kNoRef ? 0.f : -to;
+            }
+            const int2 rg = s_rng[buf][row_off + t];
+            unseen = none && !(top > kNegInf) && rg.x < rg.y;
           }
-          group_sync(1 + wg, 128);
+          fresh = group_any(1 + wg, 128, unseen);
 #pragma unroll
           for (int r = 0; r < RC; ++r) {
-            nmu[r] = -s_mu[wg][r];
+            y[r] -= s_red[wg][1][r];
             l[r] *= s_red[wg][0][r];
           }
           if (k > 0) {  // what O holds so far
@@ -705,7 +727,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
             }
             tc_wait_st();
           }
-          moved = true;
         }
 #pragma unroll
         for (int r = 0; r < RC; r += 2) {
@@ -727,7 +748,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
                   make_uint4(0, 0, 0, 0);
           };
           bool odd = false;
-          if (p < at.g.lo || p >= at.g.hi || !paged) {
+          if (p < at.g.lo || p >= at.g.hi) {
             zero_row();
           } else if (p < all.x || p >= all.y) {  // (what every row sees cannot reach a row that does not)
 #pragma unroll 1
