@@ -253,32 +253,6 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
   return v[0];
 }
 
-// arithmetic on pairs of FP32 values: one instruction each
-__device__ __forceinline__ uint64_t pack2(float2 v) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
-  return unpack2(r);
-}
 // Scores of two rows in the exp2 domain less the rows' references: x scale + nmu
 // (nmu = -mu), the product rounded, as it was for the maximum that mu was made
 // from. (One fused operation would leave the product's rounding error over, which

@@ -8,9 +8,9 @@
 // 64-bit floating point; the remainder, a signed fraction of a turn, goes to
 // sincospi in FP32.
 //
-// Cache write. BF16: the rotated key rounded once. E4M3: x / scale[head] (an
-// FP32 division, correctly rounded), then to nearest even with clamping. The
-// rotated key is not rounded to BF16 in between.
+// Cache write. BF16: the rotated key rounded once. E4M3: x / scale[head] in
+// FP32, then to nearest even with clamping. The rotated key is not rounded to
+// BF16 in between.
 //
 // All of it is streaming: each input is read once and each output written
 // once, with nothing to reuse but the R / 2 (cos, sin) of a token, which all
@@ -26,7 +26,10 @@
 //    block barrier: an earlier layout (a block per four tokens, one item a
 //    thread, the table of angles shared through a barrier) was bound by the
 //    warps' waiting for one another, 76 us for 2 x 16,385 tokens of 16 + 2 + 2
-//    heads of 128 into an E4M3 cache.
+//    heads of 128 into an E4M3 cache. This one takes 56 (46 at HBM's copy
+//    rate), bound by issue and latency: with rotation and division on single
+//    values, the division the compiler's, it took 62. Six blocks an SM, or four
+//    passes deep, are slower there (61 to 62) and the same elsewhere.
 //  * pair_kernel for the rest: one pair a thread.
 //
 // All kernels here are launched with programmatic dependent launch and wait at
@@ -102,25 +105,99 @@ __device__ __forceinline__ bool check_token(const TokenArgs& a, int tok, int r, 
 // ---------------------------------------------------------------------------
 constexpr int kWideWarps = 4, kWideDeep = 5;
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
-  f[0] = bf_lo(w.x), f[1] = bf_hi(w.x), f[2] = bf_lo(w.y), f[3] = bf_hi(w.y);
-  f[4] = bf_lo(w.z), f[5] = bf_hi(w.z), f[6] = bf_lo(w.w), f[7] = bf_hi(w.w);
+// An item's 16 components as 8 pairs (a[e], b[e]): with IL neighbours of a
+// vector, else the same component of the two vectors.
+template <bool IL>
+__device__ __forceinline__ void unpack(const uint4& x0, const uint4& x1, float (&a)[8], float (&b)[8]) {
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (IL) {
+      a[e] = bf_lo(w[e]);
+      b[e] = bf_hi(w[e]);
+    } else {
+      float(&f)[8] = e < 4 ? a : b;
+      f[2 * e % 8] = bf_lo(w[e]);
+      f[2 * e % 8 + 1] = bf_hi(w[e]);
+    }
+  }
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf(f[0], f[1]), pack_bf(f[2], f[3]), pack_bf(f[4], f[5]), pack_bf(f[6], f[7]));
+// the two components that are in word e (two of BF16, half a one of codes)
+template <bool IL>
+__device__ __forceinline__ float2 of_word(const float (&a)[8], const float (&b)[8], int e) {
+  if constexpr (IL) return make_float2(a[e], b[e]);
+  const float(&f)[8] = e < 4 ? a : b;
+  return make_float2(f[2 * e % 8], f[2 * e % 8 + 1]);
 }
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
+template <bool IL>
+__device__ __forceinline__ uint4 pack(const float (&a)[8], const float (&b)[8], int e0) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = of_word<IL>(a, b, e0 + e);
+    w[e] = pack_bf(f.x, f.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool IL>
+__device__ __forceinline__ uint2 codes(const float (&a)[8], const float (&b)[8], int e0) {
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(f[2 * i] / scale, f[2 * i + 1] / scale);
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = of_word<IL>(a, b, e0 + e);
+    c[e] = e4m3x2(f.x, f.y);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
+// |x| or |y|, whichever is less (NaN if one is), with the product's sign
+__device__ __forceinline__ float min_signed(float x, float y) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// f[i] / scale. For a scale of usual size: a quotient by the scale's reciprocal
+// and one step with its exact remainder (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990), on pairs. What the
+// step adds is right to 2^-23 of itself, so the result is the division's, but
+// where the quotient is within 2^-46 of the middle of two FP32 values. Values
+// that are clamped to 448 anyway are cut at 512 scales first, so that nothing
+// overflows. The scale's sign goes to the value, and remainder and reciprocal are
+// negated: a zero then keeps its sign.
+struct Divisor {
+  float scale, size, nr, cut;
+  bool usual;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s), size(fabsf(s)) {
+    usual = size >= 0x1p-60f && size <= 0x1p60f;
+    nr = -1.f / size;
+    cut = -512.f * s;
+  }
+  __device__ __forceinline__ void operator()(float (&f)[8]) const {
+    if (usual) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 nx = make_float2(min_signed(f[i], cut), min_signed(f[i + 1], cut)), s2 = make_float2(size, size);
+        const float2 r2 = make_float2(nr, nr), q = mul2(nx, r2), y = fma2(fma2(q, s2, nx), r2, q);
+        f[i] = y.x;
+        f[i + 1] = y.y;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {  // (rotated through: an index that is not constant would put f in memory)
+        const float x = f[0] / scale, y = f[1] / scale;
+#pragma unroll
+        for (int e = 0; e < 6; ++e) f[e] = f[e + 2];
+        f[6] = x;
+        f[7] = y;
+      }
+    }
+  }
+};
 
 // grid (ceil(tokens / kWideWarps), parts of the passes); PER = head_dim / 16
 template <int PER, bool IL, bool FP8>
 __global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArgs a) {
   constexpr int kHeads = 32 / PER, D = 16 * PER;  // heads of a pass
-  __shared__ __align__(16) float2 s_cs[kWideWarps][kMaxHalf];
+  __shared__ __align__(16) float s_cs[kWideWarps][2][kMaxHalf];  // cosines, sines
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tok = (int)blockIdx.x * kWideWarps + warp;  // (below 2^31)
@@ -154,20 +231,22 @@ __global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArg
   load(p0);
   long long row;
   const bool live = check_token(a, tok, r, j, lane == 0 && blockIdx.y == 0, row);
-  float2 cs[8];
+  float cosv[8], sinv[8];
   if (half > 0) {
     const int pos = a.pos[tok];
     for (int f = lane; f < half; f += 32) {
       const float2 c = cos_sin(pos, a.rope.turns[f]);
-      s_cs[warp][f] = make_float2(c.x * a.rope.amplitude, c.y * a.rope.amplitude * a.sign);
+      s_cs[warp][0][f] = c.x * a.rope.amplitude;
+      s_cs[warp][1][f] = c.y * a.rope.amplitude * a.sign;
     }
     __syncwarp();
     if (in_rot) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 c = *reinterpret_cast<const float4*>(&s_cs[warp][i * 8 + e]);
-        cs[e] = make_float2(c.x, c.y);
-        cs[e + 1] = make_float2(c.z, c.w);
+      for (int e = 0; e < 8; e += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(&s_cs[warp][0][i * 8 + e]);
+        const float4 s = *reinterpret_cast<const float4*>(&s_cs[warp][1][i * 8 + e]);
+        cosv[e] = c.x, cosv[e + 1] = c.y, cosv[e + 2] = c.z, cosv[e + 3] = c.w;
+        sinv[e] = s.x, sinv[e + 1] = s.y, sinv[e + 2] = s.z, sinv[e + 3] = s.w;
       }
     }
   }
@@ -180,35 +259,37 @@ __global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArg
       const int h = (p + u) * kHeads + sub;
       if (p + u >= p1 || h >= heads) continue;
       const bool is_v = h >= a.hq + a.hk;
-      float f0[8], f1[8];
-      unpack8(x0[u], f0);
-      unpack8(x1[u], f1);
+      float xa[8], xb[8];
+      unpack<IL>(x0[u], x1[u], xa, xb);
       if (in_rot && !is_v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if constexpr (IL)  // pair e: adjacent components of the first or second vector
-            rotate(e < 4 ? f0[2 * e % 8] : f1[2 * e % 8], e < 4 ? f0[(2 * e + 1) % 8] : f1[(2 * e + 1) % 8], cs[e]);
-          else
-            rotate(f0[e], f1[e], cs[e]);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 c = make_float2(cosv[e], cosv[e + 1]), s = make_float2(sinv[e], sinv[e + 1]);
+          const float2 va = make_float2(xa[e], xa[e + 1]), vb = make_float2(xb[e], xb[e + 1]);
+          const float2 ya = fma2(va, c, mul2(vb, make_float2(-s.x, -s.y))), yb = fma2(vb, c, mul2(va, s));
+          xa[e] = ya.x, xa[e + 1] = ya.y;
+          xb[e] = yb.x, xb[e + 1] = yb.y;
         }
       }
       if (h < a.hq) {
         __nv_bfloat16* dst = qo + h * a.q_out.head + split;
-        *reinterpret_cast<uint4*>(dst) = pack8(f0);
-        *reinterpret_cast<uint4*>(dst + other) = pack8(f1);
+        *reinterpret_cast<uint4*>(dst) = pack<IL>(xa, xb, 0);
+        *reinterpret_cast<uint4*>(dst + other) = pack<IL>(xa, xb, 4);
       } else if (row >= 0) {
         const int g = is_v ? h - a.hq - a.hk : h - a.hq;
         const int o0 = is_v ? i * 16 : split, o1 = o0 + (is_v ? 8 : other);
         const long long at = row + (long long)g * a.page_size * D;
         uint8_t* cache = is_v ? a.v_cache : a.k_cache;
         if constexpr (FP8) {
-          const float scale = is_v ? a.v_scale[g] : a.k_scale[g];
-          *reinterpret_cast<uint2*>(cache + at + o0) = codes8(f0, scale);
-          *reinterpret_cast<uint2*>(cache + at + o1) = codes8(f1, scale);
+          const Divisor by(is_v ? a.v_scale[g] : a.k_scale[g]);
+          by(xa);
+          by(xb);
+          *reinterpret_cast<uint2*>(cache + at + o0) = codes<IL>(xa, xb, 0);
+          *reinterpret_cast<uint2*>(cache + at + o1) = codes<IL>(xa, xb, 4);
         } else {
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(cache) + at;
-          *reinterpret_cast<uint4*>(dst + o0) = pack8(f0);
-          *reinterpret_cast<uint4*>(dst + o1) = pack8(f1);
+          *reinterpret_cast<uint4*>(dst + o0) = pack<IL>(xa, xb, 0);
+          *reinterpret_cast<uint4*>(dst + o1) = pack<IL>(xa, xb, 4);
         }
       }
     }

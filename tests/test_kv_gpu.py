@@ -236,6 +236,33 @@ def test_append(qsa, case, kv, rot, layout, packed):
         assert torch.equal(c.transpose(1, 2)[other], b.transpose(1, 2)[other])
 
 
+@pytest.mark.parametrize("odd", [False, True])
+def test_append_every_value_by_every_scale(qsa, odd):
+    # every BF16 value by scales of all sizes: the codes of the FP32 quotient
+    # (odd: rows that cannot be read 16 bytes at a time)
+    scales = np.array([1.0, 0.013, 3.7e-5, 2.0 ** -61, 2.0 ** 75, -0.3, 1 / 448, 5.9e17, 3e38, 1e-41, 0.0, -1.7e-6,
+                       math.inf, 2.0 ** -60, 2.0 ** 60, 1.9999999], dtype=np.float32)
+    hk, D, ps, n = len(scales), 128, 64, 512
+    d = _dims(qsa, 1, n // ps, n // ps, "fp8", 1, hk, hk, D, ps)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(1, n, 1, D)
+    buf = torch.zeros((1, n, hk, D + 1), dtype=torch.bfloat16)
+    buf[..., :D] = x
+    k = buf.cuda()[..., :D] if odd else x.expand(1, n, hk, D).contiguous().cuda()
+    kc, vc = (torch.zeros((n // ps, hk, ps, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc, ws = torch.from_numpy(scales).cuda(), qsa.make_kv_workspace(d)
+    pt, pos = _i32([np.arange(n // ps)]), _i32([np.arange(n)])
+    qsa.kv_append(d, k, k, kc, vc, sc, sc, pt, pos, ws)
+    with np.errstate(all="ignore"):
+        quot = x.float().numpy()[0] / scales[None, :, None]  # [n][hk][D], FP32
+    lim = torch.from_numpy(np.clip(quot, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    want = lim.view(n // ps, ps, hk, D).transpose(1, 2).contiguous()
+    for got in (kc.cpu(), vc.cpu()):
+        nan = (want & 0x7f) == 0x7f
+        assert torch.equal((got & 0x7f)[nan], want[nan] & 0x7f)
+        assert torch.equal(got[~nan], want[~nan])
+    _ok(qsa, ws)
+
+
 def test_append_special_values(qsa):
     # E4M3: NaN stays NaN, infinities and large values clamp, ties go to even,
     # the range below the normals; BF16: every bit pattern is kept
