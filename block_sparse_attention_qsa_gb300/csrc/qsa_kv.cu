@@ -14,7 +14,7 @@
 //
 // All of it is streaming: each input is read once and each output written
 // once, with nothing to reuse but the R / 2 (cos, sin) of a token, which all
-// its heads share. Two kernels:
+// its heads share. Three kernels:
 //
 //  * wide_kernel, where rows can be read 16 bytes at a time and the rotated
 //    part is a multiple of 16 components: a warp takes a token. It works out
@@ -30,6 +30,17 @@
 //    rate), bound by issue and latency: with rotation and division on single
 //    values, the division the compiler's, it took 62. Six blocks an SM, or four
 //    passes deep, are slower there (61 to 62) and the same elsewhere.
+//  * row_kernel, where rows can be read 16 bytes at a time but the halves of the
+//    rotated part are not multiples of 8 components. A warp takes a token here
+//    too: rows go through shared memory 16 bytes at a time, in which a lane
+//    finds its pairs (lane, lane + 32, ...) of every head at any offset, without
+//    bank conflicts, and keeps their (cos, sin) in registers. 8,192 tokens of 16
+//    heads of 128, 90 components rotated: 15 us (10 at HBM's copy rate; the
+//    pair kernel 35); appends of 16 + 2 + 2 heads 19 us into BF16 and 24 into
+//    E4M3 (45 and 48). For multiples of 16 the wide kernel is the faster one: 19
+//    for 24 into E4M3, 56 for 72 at 2 x 16,385 tokens, 42 for 45 in the rotation
+//    of 32,768 alone. Chunks of two vectors a lane: with five,
+//    32 tokens took 3.3 to 4.3 us in place of 2.6 to 3.5, and long inputs the same.
 //  * pair_kernel for the rest: one pair a thread.
 //
 // All kernels here are launched with programmatic dependent launch and wait at
@@ -171,12 +182,24 @@ struct Divisor {
     nr = -1.f / size;
     cut = -512.f * s;
   }
+  // lane `from`'s
+  __device__ __forceinline__ Divisor(const Divisor& d, int from) {
+    scale = __shfl_sync(0xffffffffu, d.scale, from);
+    nr = __shfl_sync(0xffffffffu, d.nr, from);
+    size = fabsf(scale);
+    cut = -512.f * scale;
+    usual = size >= 0x1p-60f && size <= 0x1p60f;
+  }
+  __device__ __forceinline__ float2 quick(float2 x) const {
+    const float2 nx = make_float2(min_signed(x.x, cut), min_signed(x.y, cut)), s2 = make_float2(size, size);
+    const float2 r2 = make_float2(nr, nr), q = mul2(nx, r2);
+    return fma2(fma2(q, s2, nx), r2, q);
+  }
   __device__ __forceinline__ void operator()(float (&f)[8]) const {
     if (usual) {
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const float2 nx = make_float2(min_signed(f[i], cut), min_signed(f[i + 1], cut)), s2 = make_float2(size, size);
-        const float2 r2 = make_float2(nr, nr), q = mul2(nx, r2), y = fma2(fma2(q, s2, nx), r2, q);
+        const float2 y = quick(make_float2(f[i], f[i + 1]));
         f[i] = y.x;
         f[i + 1] = y.y;
       }
@@ -297,6 +320,145 @@ __global__ void __launch_bounds__(32 * kWideWarps, 5) wide_kernel(const TokenArg
 }
 
 // ---------------------------------------------------------------------------
+// 16 bytes at a time, pairs from shared memory
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 4, kRowDeep = 2;
+
+// grid (ceil(tokens / kRowWarps), parts of the chunks)
+template <int D, bool IL, bool FP8>
+__global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const TokenArgs a) {
+  constexpr int kVecs = D / 8, kHeads = kRowDeep * 32 / kVecs, kPairs = D / 64;  // vectors of a head, heads of a chunk
+  constexpr int kGroup = D == 64 ? 4 : D == 128 ? 2 : 1;  // heads at a time: four pairs a lane
+  static_assert(kHeads % kGroup == 0, "groups do not cross chunks");
+  __shared__ __align__(16) __nv_bfloat16 s_rows[kRowWarps][kHeads * D];
+  __shared__ __align__(16) uint8_t s_codes[FP8 ? kRowWarps : 1][FP8 ? kHeads * D : 16];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = (int)blockIdx.x * kRowWarps + warp;  // (below 2^31)
+  if (tok >= a.tokens) return;
+  const int r = (int)((unsigned)tok / (unsigned)a.n_tok), j = tok - r * a.n_tok;
+  const int half = a.rope.rot_dim >> 1, heads = a.hq + 2 * a.hk;
+  const int chunks = (heads + kHeads - 1) / kHeads, per_part = (chunks + gridDim.y - 1) / gridDim.y;
+  const int c0 = blockIdx.y * per_part, c1 = min(chunks, c0 + per_part);
+  const __nv_bfloat16* q = a.q.p + r * a.q.batch + j * a.q.token;
+  const __nv_bfloat16* k = a.k.p + r * a.k.batch + j * a.k.token;
+  const __nv_bfloat16* v = a.v.p + r * a.v.batch + j * a.v.token;
+  uint4 x[kRowDeep];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < kRowDeep; ++u) {
+      const int h = c * kHeads + (u * 32 + lane) / kVecs;
+      if (h < heads)
+        x[u] = ld16((h < a.hq             ? q + h * a.q.head
+                     : h < a.hq + a.hk ? k + (h - a.hq) * a.k.head
+                                       : v + (h - a.hq - a.hk) * a.v.head) +
+                    lane % kVecs * 8);
+    }
+  };
+  if (c0 < c1) load(c0);
+  long long row;
+  const bool live = check_token(a, tok, r, j, lane == 0 && blockIdx.y == 0, row);
+  if (!live) return;
+  // this lane's pairs: cosine and sine, and where their components are (two
+  // neighbours where they are not rotated)
+  float2 cs[kPairs];
+  int at_a[kPairs], at_b[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int e = lane + 32 * i;
+    const bool turn = e < half;
+    cs[i] = make_float2(1.f, 0.f);
+    if (turn) {
+      const float2 c = cos_sin(a.pos[tok], a.rope.turns[e]);
+      cs[i] = make_float2(c.x * a.rope.amplitude, c.y * a.rope.amplitude * a.sign);
+    }
+    at_a[i] = !IL && turn ? e : 2 * e;
+    at_b[i] = !IL && turn ? half + e : 2 * e + 1;
+  }
+  __nv_bfloat16* rows = s_rows[warp];
+  uint8_t* codes = s_codes[FP8 ? warp : 0];
+  __nv_bfloat16* qo = a.q_out.p + r * a.q_out.batch + j * a.q_out.token;
+  for (int c = c0; c < c1; ++c) {
+    const int h0 = c * kHeads, n = min(kHeads, heads - h0);
+#pragma unroll
+    for (int u = 0; u < kRowDeep; ++u) *reinterpret_cast<uint4*>(rows + (u * 32 + lane) * 8) = x[u];
+    __syncwarp();
+    if (c + 1 < c1) load(c + 1);
+    // scales: lane g has head g's of the chunk
+    Divisor mine(1.f);
+    if (FP8 && lane < n && h0 + lane >= a.hq) {
+      const int h = h0 + lane - a.hq;
+      mine = Divisor(h < a.hk ? a.k_scale[h] : a.v_scale[h - a.hk]);
+    }
+    // heads that are rotated and stay BF16, some at a time
+    const int turned = max(0, min(n, a.hq + (FP8 ? 0 : a.hk) - h0));
+    for (int g = 0; g < turned; g += kGroup) {
+      float fa[4], fb[4];
+#pragma unroll
+      for (int u = 0; u < kGroup * kPairs; ++u) {
+        const __nv_bfloat16* x0 = rows + (g + u / kPairs) * D;
+        if (lane + 32 * (u % kPairs) < half) {
+          fa[u] = __bfloat162float(x0[at_a[u % kPairs]]);
+          fb[u] = __bfloat162float(x0[at_b[u % kPairs]]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kGroup * kPairs; ++u) {
+        __nv_bfloat16* x0 = rows + (g + u / kPairs) * D;
+        if (lane + 32 * (u % kPairs) < half && g + u / kPairs < turned) {
+          rotate(fa[u], fb[u], cs[u % kPairs]);
+          x0[at_a[u % kPairs]] = __float2bfloat16_rn(fa[u]);
+          x0[at_b[u % kPairs]] = __float2bfloat16_rn(fb[u]);
+        }
+      }
+    }
+    if constexpr (FP8) {
+      for (int g = turned; g < n; ++g) {  // heads that become codes
+        const Divisor by(mine, g);
+        const bool is_k = h0 + g < a.hq + a.hk;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const int oa = is_k ? at_a[i] : 2 * (lane + 32 * i), ob = is_k ? at_b[i] : oa + 1;
+          float2 f = make_float2(__bfloat162float(rows[g * D + oa]), __bfloat162float(rows[g * D + ob]));
+          if (is_k && lane + 32 * i < half) rotate(f.x, f.y, cs[i]);
+          f = by.usual ? by.quick(f) : make_float2(f.x / by.scale, f.y / by.scale);
+          const uint32_t w = e4m3x2(f.x, f.y);
+          codes[g * D + oa] = (uint8_t)w;
+          codes[g * D + ob] = (uint8_t)(w >> 8);
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kRowDeep; ++u) {
+      const int h = h0 + (u * 32 + lane) / kVecs, at = lane % kVecs * 8;
+      if (h >= heads) continue;
+      const uint4 y = *reinterpret_cast<const uint4*>(rows + (u * 32 + lane) * 8);
+      if (h < a.hq) {
+        *reinterpret_cast<uint4*>(qo + h * a.q_out.head + at) = y;
+      } else if (!FP8 && row >= 0) {
+        const bool is_v = h >= a.hq + a.hk;
+        const int g = is_v ? h - a.hq - a.hk : h - a.hq;
+        __nv_bfloat16* cache = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache);
+        *reinterpret_cast<uint4*>(cache + row + (long long)g * a.page_size * D + at) = y;
+      }
+    }
+    if (FP8 && row >= 0) {
+      for (int w = lane; w < n * (D / 16); w += 32) {
+        const int h = h0 + w / (D / 16);
+        if (h < a.hq) continue;
+        const bool is_v = h >= a.hq + a.hk;
+        const int g = is_v ? h - a.hq - a.hk : h - a.hq;
+        uint8_t* cache = is_v ? a.v_cache : a.k_cache;
+        *reinterpret_cast<uint4*>(cache + row + (long long)g * a.page_size * D + w % (D / 16) * 16) =
+            *reinterpret_cast<const uint4*>(codes + w * 16);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // one pair (or two components that are not rotated) a thread
 // ---------------------------------------------------------------------------
 constexpr int kPairTok = 4, kPairThreads = 256;
@@ -402,9 +564,26 @@ cudaError_t launch_wide(const TokenArgs& a, cudaStream_t s) {
                              : launch_wide<16, FP8>(a, s);
 }
 
+template <int D, bool FP8>
+cudaError_t launch_row(const TokenArgs& a, cudaStream_t s) {
+  const int heads = kRowDeep * 32 / (D / 8), chunks = (a.hq + 2 * a.hk + heads - 1) / heads;
+  const unsigned gx = (unsigned)((a.tokens + kRowWarps - 1) / kRowWarps);
+  const unsigned gy = (unsigned)std::max<long long>(1, std::min<long long>(chunks, 2LL * device_sm_count() / gx));
+  return a.rope.interleaved ? launch_k(row_kernel<D, true, FP8>, dim3(gx, gy), dim3(32 * kRowWarps), 0, s, true, a)
+                            : launch_k(row_kernel<D, false, FP8>, dim3(gx, gy), dim3(32 * kRowWarps), 0, s, true, a);
+}
+template <bool FP8>
+cudaError_t launch_row(const TokenArgs& a, cudaStream_t s) {
+  return a.head_dim == 64    ? launch_row<64, FP8>(a, s)
+         : a.head_dim == 128 ? launch_row<128, FP8>(a, s)
+                             : launch_row<256, FP8>(a, s);
+}
+
 cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
-  if (a.rope.rot_dim % 16 == 0 && vec8(a.q) && vec8(a.q_out) && vec8(a.k) && vec8(a.v))
-    return a.fp8 ? launch_wide<true>(a, s) : launch_wide<false>(a, s);
+  if (vec8(a.q) && vec8(a.q_out) && vec8(a.k) && vec8(a.v)) {
+    if (a.rope.rot_dim % 16 == 0) return a.fp8 ? launch_wide<true>(a, s) : launch_wide<false>(a, s);
+    return a.fp8 ? launch_row<true>(a, s) : launch_row<false>(a, s);
+  }
   const int pairs = (a.hq + 2 * a.hk) * (a.head_dim / 2);
   const dim3 grid((unsigned)((a.tokens + kPairTok - 1) / kPairTok),
                   (unsigned)((pairs + kPairThreads - 1) / kPairThreads));

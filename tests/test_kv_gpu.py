@@ -184,7 +184,7 @@ APPENDS = [
 @pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"n{c[2]}-{c[3]}/{c[4]}-d{c[5]}-p{c[6]}")
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("rot,layout", [(0, "half"), (1, "half"), (1, "interleaved"), (6, "half"), (6, "interleaved")])
-@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("packed", [False, True, "odd"])  # odd: rows that cannot be read 16 bytes at a time
 def test_append(qsa, case, kv, rot, layout, packed):
     starts, lengths, n, hq, hk, D, ps = case
     rot = {0: 0, 1: D}.get(rot, rot)  # none, all of the head, three pairs
@@ -193,7 +193,7 @@ def test_append(qsa, case, kv, rot, layout, packed):
     table, num_pages = R.page_table([s + m for s, m in zip(starts, lengths)], ps, 3)
     kc, vc, ks, vs = R.make_cache(num_pages, hk, ps, D, kv, 21)
     before = [f.clone() for f in (kc, vc)]
-    qkv = _normal((B, n, hq + 2 * hk, D), 22)
+    qkv = _normal((B, n, hq + 2 * hk, D + (packed == "odd")), 22)[..., :D]
     qkv[0, 0, hq, 0] = 1e4  # past the largest code: clamped
     q, k, v = (qkv[:, :, :hq], qkv[:, :, hq:hq + hk], qkv[:, :, hq + hk:])
     if not packed:
