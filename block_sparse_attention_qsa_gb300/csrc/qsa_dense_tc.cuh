@@ -256,7 +256,7 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
 // Scores of two rows in the exp2 domain less the rows' references: x scale + nmu
 // (nmu = -mu), the product rounded, as it was for the maximum that mu was made
 // from. (One fused operation would leave the product's rounding error over, which
-// from scores of 2^28 on is more than E4M3 has room for, and later more than any
+// from scores of 2^26 on is more than E4M3 has room for, and later more than any
 // weight. `one` is 1, but the assembler does not know: a multiplication and an
 // addition of pairs it fuses, .rn or not.)
 __device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float2 nmu) {
