@@ -178,6 +178,7 @@ APPENDS = [
     ([250, 3], [9, 9], 9, 4, 4, 256, 256),
     ([1], [701], 701, 8, 8, 128, 32),
     ([7, 7, 7, 7, 7], [2, 1, 2, 0, 2], 2, 64, 1, 128, 128),
+    ([15, 0], [3, 2], 3, 1024, 128, 64, 16),
 ]
 
 
@@ -496,6 +497,20 @@ def test_attn_positions_of_any_order(qsa, kv):
     pos = [[5, 900, -1, 0], [-1, -1, -1, -1], [1000, 10, 1000, 500]]
     for window in (0, 300):
         _attn_case(qsa, [901, 64, 1001], 4, 16, 2, 128, 32, kv, window=window, q_pos=pos, max_pages=200)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hk,n_q", [(1024, 1, 4), (1023, 1, 1), (512, 512, 2), (1024, 256, 4)])
+def test_attn_most_heads(qsa, kv, hq, hk, n_q):
+    # many blocks of rows of one KV head, and more units than positions
+    _attn_case(qsa, [130, 3], n_q, hq, hk, 64, 32, kv)
+
+
+@pytest.mark.parametrize("window", [129, 2 ** 31 - 1])
+def test_attn_window_past_the_context(qsa, window):
+    args, lse = _attn_case(qsa, [128, 5], 2, 16, 2, 128, 64, "bf16", window=window)
+    whole, lse2 = _attn_case(qsa, [128, 5], 2, 16, 2, 128, 64, "bf16")
+    assert torch.equal(args[8], whole[8]) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
