@@ -41,10 +41,11 @@
 // softmax. S and P are double-buffered, so the tensor cores and the copies run
 // ahead of the softmax.
 //
-// Masks. A tile in which a row does not see every position is an edge tile
-// (positions without a page are scored -inf, and the copies fill zeros); there the thread that owns a position that no row sees
-// zeroes its V row in shared memory, and a V row that only some rows see and
-// that is not finite is taken out of the MMA and added in FP32 to those rows.
+// Masks. A tile in which a row does not see every position is an edge tile.
+// There the thread that owns a position that no row sees zeroes its V row in
+// shared memory, and a V row that only some rows see and that is not finite is
+// taken out of the MMA and added in FP32 to those rows. (Positions without a
+// page: the copies fill zeros, and their scores become -inf.)
 #pragma once
 
 #include "qsa_dense.cuh"
