@@ -1043,3 +1043,60 @@ def test_a_request_from_prefill_to_decode(qsa, kv):
     else:
         v = x[:, :, 18:].float()
         assert torch.all((vo.float() - v).abs() <= 2.0 ** -4 * v.abs() + 2.0 ** -10 * vs.max() + 2.0 ** -8 * v.abs())
+
+
+@pytest.mark.parametrize("how", ["rope", "append", "attention"])
+def test_what_follows_reads_what_was_written(qsa, how):
+    # qsa_sparse_attn_rows loads its queries before it waits for the kernel in
+    # front of it: whatever of this library wrote them, in calls back to back,
+    # they are there
+    B, n_q, n = 32, 4, 3000
+    per = -(-n // 64)
+    d = qsa.make_dims(B, n_q, n // 4, per, B * per)
+    kc, vc, _, _ = R.make_cache(B * per, 2, 64, 128, "bf16", 81)
+    pt = torch.randperm(B * per, device="cuda").to(torch.int32).view(B, per)
+    pos = _i32(np.tile(np.arange(n - n_q, n), (B, 1)))
+    sel = torch.full((B, n_q, d.width), -1, dtype=torch.int32, device="cuda")
+    sel[:, :, :512] = torch.arange(512, dtype=torch.int32, device="cuda") * 5  # below every query's position
+    ws = torch.zeros(max(qsa.workspace_size(d), qsa.kv_workspace_size(d)), dtype=torch.uint8, device="cuda")
+    rows = torch.empty_like(sel)
+    qsa.resolve(d, sel, pos, pt, rows, ws)
+    rope = qsa.make_rope(128)
+    xs = [_normal((B, n_q, 20, 128), 82 + i) for i in range(3)]
+    ws2 = qsa.make_kv_workspace(d)
+
+    def make_q(x, q):
+        if how == "rope":
+            qsa.rope(rope, x[:, :, :16], pos, q)
+        elif how == "append":
+            qsa.kv_append(d, x[:, :, 16:18], x[:, :, 18:], kc, vc, None, None, pt, pos, ws2, rope=rope,
+                          q=x[:, :, :16], q_out=q)
+        else:
+            qsa.paged_attn(d, x[:, :, :16].contiguous(), kc, vc, None, None, pt, pos, q, ws2)
+
+    def calls():
+        for i in range(12):
+            make_q(xs[i % 3], qs[i])
+            qsa.sparse_attn_rows(d, qs[i], kc, vc, None, None, rows, outs[i], ws)
+
+    qs, outs = ([torch.full((B, n_q, 16, 128), math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(12)]
+                for _ in range(2))
+    want = []
+    for i in range(12):
+        make_q(xs[i % 3], qs[i])
+        torch.cuda.synchronize()
+        qsa.sparse_attn_rows(d, qs[i], kc, vc, None, None, rows, outs[i], ws)
+        torch.cuda.synchronize()
+        want.append(outs[i].clone())
+        assert not torch.isnan(want[i]).any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for go in (calls, graph.replay, graph.replay):
+        for t in qs + outs:
+            t.fill_(math.nan)
+        go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    _ok(qsa, ws)
+    _ok(qsa, ws2)
