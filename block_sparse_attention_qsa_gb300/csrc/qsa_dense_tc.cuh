@@ -24,10 +24,19 @@
 // E4M3 cache: the MMA's operands are E4M3 as well, so the cache's codes are
 // used as they are, and Q and P become two E4M3 terms each, x = hi + lo / 32,
 // as 32 + 32 columns. A code has 4 significant bits, so the two together have
-// 8, as many as BF16: Q (its row scaled by a power of two to at most 2^8) is
-// exact down to 2^-15 of its row's largest value and off by at most 2^-23 of
-// that below; P keeps 2^-8 of each weight, like the BF16 path's rounding,
-// down to 2^-20 of the largest.
+// 8, as many as BF16. Q: its row is scaled by a power of two so that its
+// largest value is in [2^7, 2^8); lo / 32 ends in steps of 2^-14, so a component
+// is off by at most 2^-15, that is 2^-22 of the row's largest value. P: a
+// weight from 2^-6 on (the row's largest is 2^6 to 2^8) is off by at most 2^-8
+// of itself, as it is in BF16. Below that its steps are of 2^-14, and a long
+// tail of weights of that size and less would be lost, or counted double, all
+// in the same direction: 61,204 equal keys 14.6 nats below one other gave 0.973
+// for 1, a million 0.69. So lo is rounded up or down by the position's place in
+// an equidistributed sequence (see `dither`) in proportion to what is cut off:
+// each such weight is off by less than 2^-14 with mean zero. The errors of a
+// tail of sum S then have a variance of at most 2^-14 S, which is at most 2^-11
+// (one standard deviation) of the row's sum, S + 2^6 or more, however many
+// positions there are.
 //
 // The reference of a row: weights are 2^(s - mu), where mu only has to keep
 // the largest weight between 1 and 2^8 (E4M3 ends at 448): it starts 6 below
@@ -262,6 +271,14 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
 // addition of pairs it fuses, .rn or not.)
 __device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float2 nmu) {
   return fma2(mul2(x, scale), one, nmu);
+}
+// What is added to lo of a position's weights before it is rounded to E4M3, whose
+// steps are of 2^-9 there: between -2^-10 and 2^-10 (exclusive: a weight of 0
+// stays 0), equidistributed over any run of positions (multiples of the golden
+// ratio, modulo 1). It depends on the position alone, so that a call gives the
+// same bits however its work is split.
+__device__ __forceinline__ float dither(int p) {
+  return (float)(((int)((uint32_t)p * 0x9e3779b9u) >> 8) | 1) * 0x1p-33f;
 }
 __device__ __forceinline__ float2 pair(const float* v) { return make_float2(v[0], v[1]); }
 __device__ __forceinline__ float2 pair(const uint32_t* v) {
@@ -800,12 +817,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         uint8_t* prow = s_p + ((it & 1) * BLK + blk) * C::kP + t * 64;
         const int x4 = (t >> 1) & 3;
         if constexpr (FP8) {
+          const float dith = dither(p);
           uint32_t hi[RC / 2], lo[RC / 2];
 #pragma unroll
           for (int r = 0; r < RC; r += 2) {
             hi[r / 2] = e4m3x2(y[r], y[r + 1]);
             const float2 f = h2_to_f2(e4m3x2_to_h2(hi[r / 2]));
-            const float2 x = mul2(add2(pair(y + r), make_float2(-f.x, -f.y)), both(32.f));
+            const float2 x = fma2(add2(pair(y + r), make_float2(-f.x, -f.y)), both(32.f), both(dith));
             lo[r / 2] = e4m3x2(x.x, x.y);
           }
           const int c0 = col / 16;  // a 16-byte chunk has 16 rows: hi in chunks 0 and 1, lo in 2 and 3

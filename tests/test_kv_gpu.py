@@ -747,6 +747,71 @@ def test_attn_closed_forms(qsa):
     assert (lse[1] - math.log(700)).abs().max().item() <= 2.0 ** -20 * 8
 
 
+@pytest.mark.parametrize("v_kind", ["ones", "apart", "alternating", "normal"])
+@pytest.mark.parametrize("kv,D,n_q,T,gap", [
+    ("bf16", 128, 1, 61204, 14.6), ("fp8", 128, 1, 61204, 14.6), ("fp8", 128, 1, 61204, 14.2),
+    ("fp8", 128, 4, 61204, 14.0), ("fp8", 64, 1, 400001, 14.6), ("fp8", 64, 4, 61203, 13.0),
+    ("fp8", 256, 2, 61204, 15.5), ("fp8", 64, 2, 1000000, 14.6), ("fp8", 64, 1, 1000000, 17.3)])
+def test_attn_long_flat_tail(qsa, kv, D, n_q, T, gap, v_kind):
+    # one key `gap` nats above a long tail of equal ones: each weight of the tail
+    # is next to nothing, their sum is not. As many requests as give every CTA
+    # about a whole unit (they read the same pages), since a piece without the
+    # large key has a reference of its own.
+    #
+    # Tolerance: half a BF16 step of the result (2^-8), the weights' own rounding
+    # (2^-8 of each), and with an E4M3 cache what weights below 2^-6 (the largest
+    # is at least 2^6) lose: each is off by less than a step of 2^-14, up or down
+    # with mean zero, a variance of at most 2^-14 times the weight. Over a tail
+    # of sum S that is sqrt(2^-14 S) of S + 2^6 or more, at most 2^-11; six times
+    # that are allowed. Nothing in it grows with the number of positions.
+    ps, hk = 256, 2
+    B = -(-torch.cuda.get_device_properties(0).multi_processor_count // hk)
+    pages = -(-T // ps)
+    code = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    g = torch.Generator("cuda").manual_seed(17)
+
+    def cache(x):  # [T] or [T][D] values that the type holds, the same for every head
+        c = torch.zeros((pages * ps, D), device="cuda")
+        c[:T] = x if x.dim() == 2 else x[:, None]
+        c = c.to(code).view(pages, 1, ps, D).expand(pages, hk, ps, D).contiguous()
+        return c if kv == "bf16" else c.view(torch.uint8)
+
+    k = torch.zeros((T, D), device="cuda")
+    k[0, 0] = 1.0
+    v = torch.ones((T, D), device="cuda")
+    if v_kind == "apart":
+        v[0] = -1.0
+    elif v_kind == "alternating":
+        v[::2] = -0.5
+    elif v_kind == "normal":
+        v = torch.randn((T, D), generator=g, device="cuda") + 0.5
+    kc, vc = cache(k), cache(v)
+    v64 = R.f64(vc.transpose(1, 2)[:, :, 0].reshape(pages * ps, D)[:T])
+    d = _dims(qsa, B, pages, pages, kv, n_q, 16, hk, D, ps, sm_scale=gap)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").flip(0)
+    kc, vc = kc.flip(0).contiguous(), vc.flip(0).contiguous()
+    q = torch.zeros((B, n_q, 16, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    pos = _i32([[T - n_q + j for j in range(n_q)]] * B)
+    one, ws = torch.ones(hk, device="cuda"), qsa.make_kv_workspace(d)
+    out, lse = torch.empty_like(q), torch.empty((B, n_q, 16), device="cuda")
+    qsa.paged_attn(d, q, kc, vc, one, one, table.repeat(B, 1), pos, out, ws, lse=lse)
+    _ok(qsa, ws)
+    for j in range(n_q):
+        n = T - n_q + j + 1
+        w = np.full(n, math.exp(-float(np.float32(gap))))
+        w[0] = 1.0
+        want, big = w @ v64[:n] / w.sum(), np.abs(v64[:n]).max(0)
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 6 * 2.0 ** -11 + 2.0 ** -18) * big
+        err = np.abs(R.f64(out[:, j]) - want)
+        assert np.all(err <= tol), (j, err.max(), (err - tol).max())
+        # a thread adds its position of every tile of 128 to its part of the sum in turn: n / 128 FP32
+        # additions, each off by at most 2^-24 of the part (the largest key's: 2^6, to which a tail weight
+        # of less than 2^-18 adds nothing)
+        sums = n / 128 * 2.0 ** -24
+        assert np.abs(R.f64(lse[:, j]) - gap - math.log(w.sum())).max() <= 2.0 ** -18 * (1 + gap) + sums
+
+
 def test_attn_without_lse_and_repeated(qsa):
     # the same bits on every call, with and without lse, whatever ws held before
     args, lse = _attn_case(qsa, [3000, 41, 1, 777], 4, 16, 2, 128, 64, "fp8")
