@@ -309,9 +309,10 @@ qsa_status qsa_sparse_attn_rows(const qsa_dims* dims, const void* q, const void*
   WsLayout w;
   if ((st = check_ws(dims, ws, ws_bytes, &w)) != QSA_OK) return st;
   const AttnPlan pl{w.units, w.tiles, w.grid, w.cl};
+  // (the caller's own kernel may be in front, and have written q)
   return from_cuda(launch_attn(*dims, q, k_cache, v_cache, k_scale, v_scale, sel_row, out,
                                at<int32_t>(ws, w.tickets), at<float>(ws, w.partials), pl,
-                               static_cast<cudaStream_t>(stream), true));
+                               static_cast<cudaStream_t>(stream), true, false));
 }
 
 }  // extern "C"

@@ -237,6 +237,7 @@ struct AttnArgs {
   long long total;  // units * tiles: the tile stream the CTAs share
   int tiles, grid, n_kv, page_size, width;
   int cl;  // cluster form: CTAs per unit (its cluster), else 0
+  bool q_early;  // the query may be read before the kernel in front of this one is waited for
   float sm_scale;
 };
 
@@ -312,10 +313,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FP8>) attn_kernel(const A
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(reinterpret_cast<uint8_t*>(sQ[buf]) + tid * 16);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   };
-  stage_q(u, 0);  // the query is not produced by the previous kernel
+  // The selection comes from the kernel in front. The query does not where that
+  // one is this library's own, launched after whatever wrote the query ended; else
+  // anything may have written it just now, and only behind the wait is it there.
+  if (a.q_early) stage_q(u, 0);
+  pdl_wait();
+  if (!a.q_early) stage_q(u, 0);
   asm volatile("cp.async.commit_group;" ::: "memory");
-
-  pdl_wait();  // the selection is
   QSA_MARK(1);
 
   // Row look-ahead: the selection entries of tile w + 2 are loaded while tile w
@@ -893,7 +897,8 @@ cudaError_t launch_draft_resolve(const qsa_dims& d, const int32_t* sel_pos, cons
 
 cudaError_t launch_attn(const qsa_dims& d, const void* q, const void* k_cache, const void* v_cache,
                         const float* k_scale, const float* v_scale, const int32_t* sel_row, void* out,
-                        int32_t* tickets, float* partials, const AttnPlan& plan, cudaStream_t s, bool pdl) {
+                        int32_t* tickets, float* partials, const AttnPlan& plan, cudaStream_t s, bool pdl,
+                        bool q_early) {
   AttnArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_cache = k_cache;
@@ -914,6 +919,7 @@ cudaError_t launch_attn(const qsa_dims& d, const void* q, const void* k_cache, c
   a.width = d.width;
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf((float)d.head_dim);
   a.cl = 0;
+  a.q_early = q_early;
   const bool fp8 = d.kv_dtype == QSA_KV_FP8_E4M3;
   if (plan.cl > 1 && plan.cl <= kMaxCluster && plan.cl <= plan.tiles) {
     // one cluster of cl CTAs per unit, if the device can place such clusters

@@ -219,8 +219,11 @@ cudaError_t launch_draft_resolve(const qsa_dims& d, const int32_t* sel_pos, cons
 // selected positions -> cache rows (KV head 0) with all index checks
 cudaError_t launch_resolve(const qsa_dims& d, const int32_t* sel_pos, const int32_t* q_pos,
                            const int32_t* page_table, int32_t* sel_row, int32_t* err, cudaStream_t s);
+// q_early: q is read before the kernel in front is waited for (pdl): that kernel
+// does not write it, and started after the one that did had ended
 cudaError_t launch_attn(const qsa_dims& d, const void* q, const void* k_cache, const void* v_cache,
                         const float* k_scale, const float* v_scale, const int32_t* sel_row, void* out,
-                        int32_t* tickets, float* partials, const AttnPlan& plan, cudaStream_t s, bool pdl);
+                        int32_t* tickets, float* partials, const AttnPlan& plan, cudaStream_t s, bool pdl,
+                        bool q_early = true);
 
 }  // namespace qsa

@@ -45,7 +45,7 @@
 //
 // All kernels here are launched with programmatic dependent launch and wait at
 // their start for what is before them in the stream; none lets its own
-// successor start early (other entry points read their query before they wait).
+// successor start early.
 #include <algorithm>
 
 #include "qsa_kv_internal.cuh"

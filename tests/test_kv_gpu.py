@@ -1165,3 +1165,55 @@ def test_what_follows_reads_what_was_written(qsa, how):
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     _ok(qsa, ws)
     _ok(qsa, ws2)
+
+
+@pytest.mark.parametrize("B", [1, 32])
+def test_rows_attention_reads_queries_behind_its_wait(qsa, B):
+    # qsa_sparse_attn_rows behind a kernel that lets its successor start at once
+    # and then writes the queries: qsa_resolve is one, its cache rows 16,128 ..
+    # 16,639 taken as the bits of BF16 queries (0.5 to 3.1 in every second place).
+    # B 1: the cluster form, 32: equal shares of the stream
+    n_q, n, ps = 4, 600, 64
+    per = -(-n // ps)
+    d = qsa.make_dims(B, n_q, n // 4, per, B * per)
+    kc, vc, _, _ = R.make_cache(B * per, 2, ps, 128, "bf16", 91)
+    pt = torch.randperm(B * per, device="cuda").to(torch.int32).view(B, per)
+    pos = _i32(np.tile(np.arange(n - n_q, n), (B, 1)))
+    g = torch.Generator("cuda").manual_seed(92)
+    sel = torch.full((B, n_q, d.width), -1, dtype=torch.int32, device="cuda")
+    sel[:, :, :512] = torch.randint(0, n - n_q, (B, n_q, 512), generator=g, device="cuda", dtype=torch.int32)
+    ws = torch.zeros(qsa.workspace_size(d), dtype=torch.uint8, device="cuda")
+    rows = torch.empty_like(sel)
+    qsa.resolve(d, sel, pos, pt, rows, ws)
+    # the kernel that writes the queries
+    d2 = qsa.make_dims(B, n_q, 64, 4, 130)
+    pt2 = _i32([[126, 127, 128, 129]] * B)
+    pos2 = torch.full((B, n_q), 255, dtype=torch.int32, device="cuda")
+    sel2 = [torch.randint(0, 256, sel.shape, generator=g, device="cuda", dtype=torch.int32) for _ in range(3)]
+    ws2 = torch.zeros(qsa.workspace_size(d2), dtype=torch.uint8, device="cuda")
+    made = [torch.empty_like(sel) for _ in range(12)]
+    qs = [m.view(-1)[:B * n_q * 1024].view(torch.bfloat16).view(B, n_q, 16, 128) for m in made]
+    outs = [torch.empty((B, n_q, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(12)]
+
+    def calls(sync=False):
+        for i in range(12):
+            qsa.resolve(d2, sel2[i % 3], pos2, pt2, made[i], ws2)
+            if sync:
+                torch.cuda.synchronize()
+            qsa.sparse_attn_rows(d, qs[i], kc, vc, None, None, rows, outs[i], ws)
+
+    calls(sync=True)
+    want = [o.clone() for o in outs]
+    assert torch.isfinite(want[0]).all() and not torch.equal(want[0], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for go in (calls, graph.replay, graph.replay):
+        for m, o in zip(made, outs):
+            m.fill_(-1)  # NaN
+            o.fill_(math.nan)
+        go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    _ok(qsa, ws)
+    _ok(qsa, ws2)
