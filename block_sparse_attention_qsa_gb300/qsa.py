@@ -14,12 +14,16 @@ tracing build, libqsa_trace.so, for timeline.py).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
+import warnings
 from typing import Optional, Tuple
 
 import numpy as np
 import torch
+
+from . import _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("QSA_LIBRARY") or os.path.join(_HERE, "libqsa.so")
@@ -148,14 +152,37 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-try:
-    from . import _fast
-except ImportError as e:
-    raise ImportError(f"the binding's fast path is not built ({e}); run __graft_entry__.build()") from e
-_fast.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-             for f in ("qsa_rope", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn")),
-           getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-           getattr(torch._C, "_cuda_getCurrentRawStream", None))
+class _NoFast:
+    """Stands for the module _fast where it is not there: takes no call."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    rope = kv_append = kv_gather = paged_attn = _none
+
+
+def _load_fast():
+    """The module _fast (csrc/qsa_fast.cpp) built for this Python and torch. It
+    only shortens the host's part of a call, so the binding does without where
+    it is missing or does not load, and says so."""
+    path = _build.fast_path()
+    try:
+        spec = importlib.util.spec_from_file_location(f"{__package__}._fast", path)
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+    except ImportError as e:
+        warnings.warn(f"the binding's fast path is not there ({e}): calls of the operators round the paged cache take "
+                      "longer on the host; __graft_entry__.build() makes it", RuntimeWarning)
+        return _NoFast
+    fast.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                for f in ("qsa_rope", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn")),
+              getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+              getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return fast
+
+
+_fast = _load_fast()
 
 
 def status_str(status: int) -> str:
@@ -502,7 +529,8 @@ def make_rope(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling
 # Each function below first hands its arguments to _fast, which makes the call
 # if all of them are as expected and returns its status. Where one is not, it
 # returns None, and the checks here say what is wrong with it (or, for what
-# _fast does not take, such as an empty tensor, make the call).
+# _fast does not take, such as an empty tensor, make the call; they make every
+# call where _fast is not there).
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 

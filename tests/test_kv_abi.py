@@ -5,6 +5,9 @@ import ctypes
 import math
 import os
 import re
+import subprocess
+import sys
+import sysconfig
 
 import numpy as np
 import pytest
@@ -219,3 +222,69 @@ def test_binding_refuses_host_tensors_and_bad_arguments(qsa):
         qsa.paged_attn(d, x, cache, cache, None, None, pos, pos, x, ws, window=1 << 32)
     with pytest.raises(KeyError):
         qsa.make_rope(128, layout="other", device="cpu")
+
+
+# --------------------------------------------------------------------------
+# the binding's fast path
+# --------------------------------------------------------------------------
+def _python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+
+
+def test_fast_path_is_built_for_this_python_and_torch(qsa):
+    from block_sparse_attention_qsa_gb300 import _build
+
+    path = _build.fast_path()
+    assert os.path.exists(path) and qsa._fast.__file__ == path
+    assert torch.__version__ in path and path.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def test_build_makes_a_missing_fast_path_and_nothing_else(qsa, monkeypatch, tmp_path):
+    # (after a change of Python or torch: the library is newer than every source)
+    from block_sparse_attention_qsa_gb300 import _build
+
+    monkeypatch.setattr(_build, "fast_path", lambda: str(tmp_path / "_fast.other.so"))
+    before = os.path.getmtime(_build.LIB)
+    assert _build.build() == _build.LIB
+    assert (tmp_path / "_fast.other.so").exists() and os.path.getmtime(_build.LIB) == before
+    made = os.path.getmtime(tmp_path / "_fast.other.so")
+    _build.build()
+    assert os.path.getmtime(tmp_path / "_fast.other.so") == made
+
+
+def test_build_goes_on_without_a_fast_path(qsa, monkeypatch, tmp_path):
+    from block_sparse_attention_qsa_gb300 import _build
+
+    monkeypatch.setattr(_build, "fast_path", lambda: str(tmp_path / "_fast.other.so"))
+    monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    with pytest.warns(RuntimeWarning, match="not built"):
+        assert _build.build() == _build.LIB
+
+
+@pytest.mark.parametrize("stale", [False, True])
+def test_binding_works_without_its_fast_path(qsa, stale, tmp_path):
+    # missing, or a file that this Python cannot load: the library is all that
+    # the binding needs, and a call gets the same checks
+    path = tmp_path / "_fast.other.so"
+    if stale:
+        path.write_bytes(b"built for something else")
+    r = _python(f"""
+import warnings
+from block_sparse_attention_qsa_gb300 import _build
+_build.fast_path = lambda: {str(path)!r}
+with warnings.catch_warnings(record=True) as w:
+    warnings.simplefilter("always")
+    from block_sparse_attention_qsa_gb300 import qsa
+assert any("fast path is not there" in str(x.message) for x in w), w
+assert qsa.rope_table(64)[1] == 1.0 and qsa.workspace_size(qsa.make_dims(1, 1, 16, 1, 1)) > 0
+import torch
+t = torch.zeros((1, 1, 2, 128), dtype=torch.bfloat16)
+try:
+    qsa.rope(qsa.make_rope(64, device="cpu"), t, torch.zeros((1, 1), dtype=torch.int32), t)
+except ValueError as e:
+    assert "cuda" in str(e).lower(), e
+else:
+    raise AssertionError("a host tensor was taken")
+print("fine")
+""")
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr

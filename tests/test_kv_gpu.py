@@ -1217,3 +1217,28 @@ def test_rows_attention_reads_queries_behind_its_wait(qsa, B):
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     _ok(qsa, ws)
     _ok(qsa, ws2)
+
+
+def test_calls_without_the_fast_path(qsa, monkeypatch):
+    # the binding's own checks make the same calls
+    ctx, n_q, ps = [300, 64], 2, 64
+    args, lse = _attn_case(qsa, ctx, n_q, 16, 2, 128, ps, "fp8")
+    d, q, kc, vc, ks, vs, table, pos, out, ws = args
+    x, rope = _normal((2, n_q, 20, 128), 95), qsa.make_rope(128)
+
+    def calls():
+        kc2, vc2, q_out, y = kc.clone(), vc.clone(), torch.empty_like(q), torch.empty_like(q)
+        ko, vo = (torch.empty((2, n_q, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        o, l = torch.empty_like(out), torch.empty_like(lse)
+        qsa.kv_append(d, x[:, :, 16:18], x[:, :, 18:], kc2, vc2, ks, vs, table, pos, ws, rope=rope, q=x[:, :, :16],
+                      q_out=q_out)
+        qsa.kv_gather(d, kc2, vc2, ks, vs, table, pos, ko, vo, ws)
+        qsa.rope(rope, x[:, :, :16], pos, y, inverse=True, stream=torch.cuda.current_stream())
+        qsa.paged_attn(d, q_out, kc2, vc2, ks, vs, table, pos, o, ws, lse=l, window=100)
+        _ok(qsa, ws)
+        return kc2, vc2, q_out, y, ko, vo, o, l
+
+    want = calls()
+    assert qsa._fast is not qsa._NoFast
+    monkeypatch.setattr(qsa, "_fast", qsa._NoFast)
+    assert all(torch.equal(a, b) for a, b in zip(calls(), want))
