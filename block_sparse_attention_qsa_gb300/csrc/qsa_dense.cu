@@ -36,7 +36,7 @@ DenseWs dense_ws(const qsa_dims& d, int num_sms) {
 
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
-                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s) {
+                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s, bool short_k) {
   const int sms = device_sm_count();
   const DenseWs w = dense_ws(d, sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -66,9 +66,9 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.one = 1.f;
   const int rows = unit_rows(d);
   switch (d.head_dim) {
-    case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, s);
-    case 128: return launch_dense_128(rows, d, a, k_cache, v_cache, s);
-    default: return launch_dense_256(rows, d, a, k_cache, v_cache, s);
+    case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, short_k, s);
+    case 128: return launch_dense_128(rows, d, a, k_cache, v_cache, short_k, s);
+    default: return launch_dense_256(rows, d, a, k_cache, v_cache, short_k, s);
   }
 }
 

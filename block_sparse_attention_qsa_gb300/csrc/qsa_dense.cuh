@@ -540,8 +540,10 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled encode_tiled();  // cuTensorMapEncodeTiled through the runtime, or null
 
 // the cache [num_pages][n_kv_heads][page_size][head_dim] with boxes of one
-// page's (or `tile`) positions of one head, `line` (64 or 128) bytes of a row wide
-inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cache, int tile, int line) {
+// page's (or `tile`) positions of one head, `line` (64 or 128) bytes of a row
+// wide; short_box: of half as many positions (qsa_test_paged_attn_timeout)
+inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cache, int tile, int line,
+                           bool short_box) {
   const EncodeTiled enc = encode_tiled();
   if (!enc) return false;
   const int eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2;
@@ -549,7 +551,8 @@ inline bool make_cache_map(CUtensorMap* map, const qsa_dims& d, const void* cach
                               (cuuint64_t)d.num_pages};
   const cuuint64_t row = (cuuint64_t)d.head_dim * eb;
   const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.n_kv_heads};
-  const cuuint32_t box[4] = {(cuuint32_t)(line / eb), (cuuint32_t)std::min(tile, d.page_size), 1, 1};
+  const int rows = std::min(tile, d.page_size) / (short_box ? 2 : 1);
+  const cuuint32_t box[4] = {(cuuint32_t)(line / eb), (cuuint32_t)rows, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -574,12 +577,13 @@ cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
                   dim3(32 * kJoinRows), 0, s, true, a);
 }
 
-// the kernels by head dim (qsa_dense_64.cu, _128.cu, _256.cu); rows: of a unit
+// the kernels by head dim (qsa_dense_64.cu, _128.cu, _256.cu); rows: of a unit;
+// short_k: K's copies bring half of what the kernel waits for
 cudaError_t launch_dense_64(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
-                            cudaStream_t s);
+                            bool short_k, cudaStream_t s);
 cudaError_t launch_dense_128(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
-                             cudaStream_t s);
+                             bool short_k, cudaStream_t s);
 cudaError_t launch_dense_256(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
-                             cudaStream_t s);
+                             bool short_k, cudaStream_t s);
 
 }  // namespace qsa

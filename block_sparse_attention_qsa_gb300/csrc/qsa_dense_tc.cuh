@@ -928,10 +928,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
 }
 
 template <int D, bool FP8, int RC, int WGS>
-cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, cudaStream_t s) {
+cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, bool short_k,
+                      cudaStream_t s) {
   using C = Tc<D, FP8, RC, WGS>;
   alignas(64) CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, d, k_cache, kTileTc, C::kLine) || !make_cache_map(&tv, d, v_cache, kTileTc, C::kLine))
+  if (!make_cache_map(&tk, d, k_cache, kTileTc, C::kLine, short_k) ||
+      !make_cache_map(&tv, d, v_cache, kTileTc, C::kLine, false))
     return cudaErrorInvalidValue;
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(dense_tc_kernel<C>, C::kSmem);
@@ -943,13 +945,14 @@ cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const
 }
 
 template <int D, bool FP8>
-cudaError_t launch_tc(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, cudaStream_t s) {
+cudaError_t launch_tc(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, bool short_k,
+                      cudaStream_t s) {
   switch (rows) {
-    case 8: return launch_tc<D, FP8, 8, 1>(d, a, k, v, s);
-    case 16: return launch_tc<D, FP8, 16, 1>(d, a, k, v, s);
-    case 32: return launch_tc<D, FP8, 16, 2>(d, a, k, v, s);
+    case 8: return launch_tc<D, FP8, 8, 1>(d, a, k, v, short_k, s);
+    case 16: return launch_tc<D, FP8, 16, 1>(d, a, k, v, short_k, s);
+    case 32: return launch_tc<D, FP8, 16, 2>(d, a, k, v, short_k, s);
     default:
-      if constexpr (D * (FP8 ? 1 : 2) <= 256) return launch_tc<D, FP8, 32, 2>(d, a, k, v, s);
+      if constexpr (D * (FP8 ? 1 : 2) <= 256) return launch_tc<D, FP8, 32, 2>(d, a, k, v, short_k, s);
   }
   return cudaErrorInvalidValue;  // (not reached: unit_rows)
 }

@@ -76,6 +76,21 @@ qsa_status check_rope(const qsa_rope_args* r, int head_dim, Rope* out) {
   return QSA_OK;
 }
 
+qsa_status paged_attn(const qsa_dims* dims, int32_t window, const void* q, const void* k_cache,
+                      const void* v_cache, const float* k_scale, const float* v_scale,
+                      const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream, bool short_k) {
+  const qsa_status st = check_kv_dims(dims);
+  if (st != QSA_OK) return st;
+  if (window < 0 || !q || !k_cache || !v_cache || !page_table || !q_pos || !out) return QSA_ERR_INVALID_ARG;
+  if (dims->kv_dtype == QSA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return QSA_ERR_INVALID_ARG;
+  if (!aligned_all(16, {q, k_cache, v_cache, out}) || !aligned_all(4, {k_scale, v_scale, page_table, q_pos, lse}))
+    return QSA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < dense_ws(*dims, device_sm_count()).total) return QSA_ERR_WORKSPACE;
+  return from_cuda(launch_paged_attn(*dims, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out,
+                                     lse, ws, static_cast<cudaStream_t>(stream), short_k));
+}
+
 }  // namespace
 
 extern "C" {
@@ -188,15 +203,16 @@ qsa_status qsa_paged_attn(const qsa_dims* dims, int32_t window, const void* q, c
                           const void* v_cache, const float* k_scale, const float* v_scale,
                           const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
                           size_t ws_bytes, void* stream) {
-  const qsa_status st = check_kv_dims(dims);
-  if (st != QSA_OK) return st;
-  if (window < 0 || !q || !k_cache || !v_cache || !page_table || !q_pos || !out) return QSA_ERR_INVALID_ARG;
-  if (dims->kv_dtype == QSA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return QSA_ERR_INVALID_ARG;
-  if (!aligned_all(16, {q, k_cache, v_cache, out}) || !aligned_all(4, {k_scale, v_scale, page_table, q_pos, lse}))
-    return QSA_ERR_INVALID_ARG;
-  if (!ws || !aligned(ws, 256) || ws_bytes < dense_ws(*dims, device_sm_count()).total) return QSA_ERR_WORKSPACE;
-  return from_cuda(launch_paged_attn(*dims, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out,
-                                     lse, ws, static_cast<cudaStream_t>(stream)));
+  return paged_attn(dims, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, lse, ws, ws_bytes,
+                    stream, false);
+}
+
+qsa_status qsa_test_paged_attn_timeout(const qsa_dims* dims, int32_t window, const void* q, const void* k_cache,
+                                       const void* v_cache, const float* k_scale, const float* v_scale,
+                                       const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  return paged_attn(dims, window, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, lse, ws, ws_bytes,
+                    stream, true);
 }
 
 }  // extern "C"

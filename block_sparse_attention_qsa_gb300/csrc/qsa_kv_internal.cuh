@@ -37,9 +37,11 @@ struct DenseWs {
   size_t units, parts, total;
 };
 DenseWs dense_ws(const qsa_dims& d, int num_sms);
+// short_k: the failure-detection test (qsa_test_paged_attn_timeout)
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
-                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s);
+                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s,
+                              bool short_k = false);
 
 // 16-byte loads and stores of streamed data
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }

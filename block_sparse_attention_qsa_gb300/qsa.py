@@ -45,6 +45,7 @@ EXPORTS = (
 # and those of include/qsa_kv.h, the operators round the paged cache
 KV_EXPORTS = (
     "qsa_rope_table", "qsa_rope", "qsa_kv_workspace_size", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn",
+    "qsa_test_paged_attn_timeout",
 )
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
@@ -140,6 +141,7 @@ def _load() -> ctypes.CDLL:
         "qsa_kv_append": (I, [D, N, R, P, S, P, S, P, S, P, S, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_gather": (I, [D, N, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_paged_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_test_paged_attn_timeout": (I, [D, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -715,6 +717,11 @@ def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos
         return
     if st is not None:
         _check(st, "qsa_paged_attn")
+    _paged_attn(lib.qsa_paged_attn, "qsa_paged_attn", d, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out,
+                ws, lse, window, stream)
+
+
+def _paged_attn(fn, name, d, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, ws, lse, window, stream):
     dev = _current_device()
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 or a number of positions below 2^31")
@@ -726,9 +733,18 @@ def paged_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos
     pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
     lp = None if lse is None else _want_on(dev, lse, "lse", (B, n_q, H), _F32)
     w, nb = _ws_on(dev, ws)
-    st = lib.qsa_paged_attn(d, window, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
+    st = fn(d, window, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
     if st:
-        _check(st, "qsa_paged_attn")
+        _check(st, name)
+
+
+def test_paged_attn_timeout(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, ws, lse=None,
+                            window: int = 0, stream=None):
+    """qsa_test_paged_attn_timeout: paged_attn with copies of half the bytes its
+    kernel waits for, so that its bounded waits run out (about a second);
+    check_errors then reports ERR_TIMEOUT. For failure-detection tests."""
+    _paged_attn(lib.qsa_test_paged_attn_timeout, "qsa_test_paged_attn_timeout", d, q, k_cache, v_cache, k_scale,
+                v_scale, page_table, q_pos, out, ws, lse, window, stream)
 
 
 def check_errors(ws: torch.Tensor, stream=None) -> Tuple[int, Tuple[int, int, int, int]]:

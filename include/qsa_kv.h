@@ -172,6 +172,16 @@ qsa_status qsa_paged_attn(const qsa_dims* dims, int32_t window, const void* q, c
                           const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
                           size_t ws_bytes, void* stream);
 
+/* Test hook for failure detection: qsa_paged_attn with copies of K that bring
+ * half of the bytes its kernel waits for. Every CTA's bounded wait runs out
+ * (about a second), the kernel stops, frees what it holds and records a timeout
+ * (kind 5, QSA_ERR_TIMEOUT); out and lse hold nothing of meaning. The next call
+ * on the same workspace is complete again. */
+qsa_status qsa_test_paged_attn_timeout(const qsa_dims* dims, int32_t window, const void* q, const void* k_cache,
+                                       const void* v_cache, const float* k_scale, const float* v_scale,
+                                       const int32_t* page_table, const int32_t* q_pos, void* out, float* lse,
+                                       void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

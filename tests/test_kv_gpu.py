@@ -1242,3 +1242,31 @@ def test_calls_without_the_fast_path(qsa, monkeypatch):
     assert qsa._fast is not qsa._NoFast
     monkeypatch.setattr(qsa, "_fast", qsa._NoFast)
     assert all(torch.equal(a, b) for a, b in zip(calls(), want))
+
+
+@pytest.mark.parametrize("kv,D,n_q", [("bf16", 128, 1), ("fp8", 64, 4), ("bf16", 256, 2), ("fp8", 128, 4)])
+def test_attn_wait_runs_out_and_reports_a_timeout(qsa, kv, D, n_q):
+    # Failure detection without a fault: the test hook's copies of K bring half
+    # of the bytes that the kernel waits for, so every CTA's wait for its first
+    # tile runs out (about a second). The timeout is reported, every role of the
+    # kernel ends and its tensor memory is free: the next calls, which need all
+    # of it again, are complete.
+    import time
+
+    args, lse = _attn_case(qsa, [1500, 70, 0, 300], n_q, 16, 2, D, 64, kv)
+    out, ws = args[8], args[9]
+    want, want_lse = out.clone(), lse.clone()
+    torch.cuda.synchronize()
+    t0 = time.time()
+    qsa.test_paged_attn_timeout(*args, lse=lse)
+    torch.cuda.synchronize()
+    waited = time.time() - t0
+    st, info = qsa.check_errors(ws)
+    assert st == qsa.ERR_TIMEOUT and info[0] == 5, info
+    assert 0.2 < waited < 30, waited
+    for _ in range(3):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        qsa.paged_attn(*args, lse=lse)
+        _ok(qsa, ws)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
