@@ -207,10 +207,13 @@ struct Walk {
   long long unit;
   int r, x, t, n, tiles;
   Range g;
-  __device__ __forceinline__ bool cut(const Share& sh) {  // the share's tiles of this unit
+  __device__ __forceinline__ int start(const Share& sh) const {  // the share's first tile of this unit
     const long long first = unit + sh.split.seg, w0 = sh.w0;
-    t = w0 > first ? (int)(w0 - first) : 0;
-    n = (int)min((long long)tiles, sh.w1 - first) - t;
+    return w0 > first ? (int)(w0 - first) : 0;
+  }
+  __device__ __forceinline__ bool cut(const Share& sh) {  // the share's tiles of this unit
+    t = start(sh);
+    n = (int)min((long long)tiles, sh.w1 - (unit + sh.split.seg)) - t;
     return n > 0;
   }
   __device__ __forceinline__ bool next(const DenseArgs& a, const Share& sh) {

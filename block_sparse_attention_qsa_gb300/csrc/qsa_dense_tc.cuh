@@ -67,6 +67,7 @@ constexpr float kRefBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kRefMost = 8.f;   // log2 of a weight that moves the reference
 constexpr float kNoRef = __builtin_huge_valf();  // the reference of a row that has seen nothing (its scores are less 0)
 constexpr int kBadRing = 16;      // page marks of the tiles in flight
+constexpr int kRun = 256;         // tiles of a run: O in tensor memory holds no more (a power of two)
 
 // D: head dim, RC: rows of a softmax warpgroup (8, 16 or 32), WGS: softmax
 // warpgroups, BLK: blocks of up to 32 rows, each one set of MMA columns
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], fin;
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_bad[kBadRing];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
-  __shared__ int s_keep;                // a unit's first PV adds to what O holds
+  __shared__ int s_keep;                // a run's first PV adds to what O holds
   __shared__ volatile int s_abort;
   __shared__ long long s_scan[C::kThreads / 32];
   __shared__ Share s_share;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
                                      wait(&slot_full[slot], (uint32_t)(it / C::kNV) & 1u));
           if (!ok) break;
           tc_after();
-          const bool fresh = k == 0 && *reinterpret_cast<volatile int*>(&s_keep) == 0;
+          const bool fresh = k % kRun == 0 && *reinterpret_cast<volatile int*>(&s_keep) == 0;
           // A: positions as k. Its 128 rows are components: one line of 128,
           // or two of 64 (leading offset: a line), or one of 64 twice (leading
           // offset 0; the upper half of O is then a copy)
@@ -583,30 +584,40 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       mbar_arrive(smem_u32(&q_full[buf]));
     };
 
+    // A segment goes by in runs of kRun tiles, whose O and sums are added up in
+    // FP32 where the segment's piece is (or would be, for a unit that is whole).
+    // The tensor cores add to an accumulator by cutting off, not by rounding: one
+    // that grows steadily loses about half of its last bit at each step (8 a tile
+    // with BF16, 4 with E4M3): 0.4 % over 1,000,000 positions in one CTA, 2 % over
+    // 4,000,000. A run loses at most 2^-12, and a thread's part of a row's sum has
+    // no more than kRun terms.
     stage_q(at, 0);
     int it = 0, seg = 0;
-    do {
-      const int n = at.n, buf = seg % C::kQBufs;
-      if constexpr (C::kQBufs == 1) {
-        if (seg > 0) stage_q(at, 0);
-      } else {
-        Walk<kTile> following = at;
-        if (following.next(a, s_share)) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
+    bool last;
+    do {  // (at.t, at.n: what is left of the segment)
+      const int n = min(kRun, at.n), buf = seg % C::kQBufs;
+      if (at.t == at.start(s_share)) {
+        if constexpr (C::kQBufs == 1) {
+          if (seg > 0) stage_q(at, 0);
+        } else {
+          Walk<kTile> following = at;
+          if (following.next(a, s_share)) stage_q(following, buf ^ 1);  // (the rows of the unit before are done with)
+        }
+        if (t < RC) {
+          s_mu[wg][t] = kNoRef;
+          s_nmu[wg][t] = 0.f;
+        }
+        if constexpr (WGS == 1)
+          group_sync(1 + wg, 128);  // the tables of this unit
+        else
+          group_sync(3, 128 * WGS);
       }
-      if (t < RC) {
-        s_mu[wg][t] = kNoRef;
-        s_nmu[wg][t] = 0.f;
-      }
-      if constexpr (WGS == 1)
-        group_sync(1 + wg, 128);  // the tables of this unit
-      else
-        group_sync(3, 128 * WGS);
       const int2 all = s_all[buf];
       float l[RC];
       const float sc = FP8 ? 0.f : s_scale[buf][0];
 #pragma unroll
       for (int r = 0; r < RC; ++r) l[r] = 0.f;
-      bool fresh = true;  // a row has no reference yet
+      bool fresh = true;  // a row has no reference yet (asked anew in each run)
       for (int k = 0; k < n; ++k, ++it) {
         const bool ok = wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u);
         (void)ok;  // given up: the loop runs on without meaning, to the same barriers
@@ -855,11 +866,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         mbar_arrive(smem_u32(&p_full[it & 1]));
       }
 
-      // ---- the segment's end: component t of every row ----
+      // ---- the run's end: component t of every row ----
       const int g = at.x / a.row_blocks;
-      const bool whole = n == at.tiles;
+      last = n == at.n;
+      const int start = at.start(s_share);
+      const bool whole = start == 0 && at.t + at.n == at.tiles, done = whole && last, more = at.t > start;
       const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
-      if (a.batch > kJoinScan && tid == 0 && at.t == 0)
+      if (a.batch > kJoinScan && tid == 0 && start == 0 && last)
         a.unit_desc[(long long)at.r * units + at.x] =
             whole ? kUnitWhole : unit_pieces(blockIdx.x, s_share.split.last_cta(at.unit, at.tiles), pslot);
       const float part = reduce_rows<RC>(l, [](float c, float d) { return c + d; });
@@ -871,11 +884,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       if (lane < RC) s_red[wg][quarter][lane] = part;
       group_sync(1 + wg, 128);
       float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
-      if (t < RC) {  // a row's sum, its factor, and lse
-        const float sum = (s_red[wg][0][t] + s_red[wg][1][t]) + (s_red[wg][2][t] + s_red[wg][3][t]);
+      if (t < RC) {  // a row's sum, its factors, and lse
+        float sum = (s_red[wg][0][t] + s_red[wg][1][t]) + (s_red[wg][2][t] + s_red[wg][3][t]);
         const float ref = s_mu[wg][t];
         const int orow = s_out[buf][row_off + t];
-        if (!whole) {
+        if (more) {  // the runs before, to the reference of now (which every row has that had weights)
+          const float before = piece[C::kRows + row_off + t];
+          const float f = before == 0.f ? 0.f : exp2_sfu(piece[row_off + t] - ref);
+          sum = fmaf(before, f, sum);
+          s_red[wg][1][t] = f;
+        }
+        if (!done) {
           piece[row_off + t] = sum == 0.f ? kNegInf : ref;
           piece[C::kRows + row_off + t] = sum;
         } else {
@@ -883,34 +902,41 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
           if (a.lse && orow >= 0) a.lse[orow] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
       }
-      if (whole) group_sync(1 + wg, 128);
+      if (done || more) group_sync(1 + wg, 128);
+      constexpr int kPart = RC < 16 ? RC : 16;  // rows at a time
 #pragma unroll 1
-      for (int mb = 0; mb < MB; ++mb) {
-        const uint32_t addr = o_addr + (uint32_t)(mb * (BLK * N));
-        uint32_t o[RC];
-        Tmem<RC>::load(addr, o);
+      for (int i = 0; i < MB * (RC / kPart); ++i) {
+        const int mb = i / (RC / kPart), r0 = i % (RC / kPart) * kPart;
+        const uint32_t addr = o_addr + (uint32_t)(mb * (BLK * N) + r0);
+        uint32_t o[kPart];
+        Tmem<kPart>::load(addr, o);
         if constexpr (FP8) {
-          uint32_t u[RC];
-          Tmem<RC>::load(addr + 32, u);
+          uint32_t u[kPart];
+          Tmem<kPart>::load(addr + 32, u);
           tc_wait_ld();
 #pragma unroll
-          for (int r = 0; r < RC; ++r)
+          for (int r = 0; r < kPart; ++r)
             o[r] = __float_as_uint(fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(o[r])));
         } else {
           tc_wait_ld();
         }
         const int comp = mb * 128 + t;
         if (D < 128 && t >= D) continue;  // (a copy; no more barriers here)
-        if (!whole) {
-          float* dst = piece + 2 * C::kRows + row_off * D + comp;
+        float* dst = piece + 2 * C::kRows + (row_off + r0) * D + comp;
+        if (more) {
 #pragma unroll
-          for (int r = 0; r < RC; ++r) dst[r * D] = __uint_as_float(o[r]);  // (rows that are none: never read)
+          for (int r = 0; r < kPart; ++r)
+            o[r] = __float_as_uint(fmaf(dst[r * D], s_red[wg][1][r0 + r], __uint_as_float(o[r])));
+        }
+        if (!done) {
+#pragma unroll
+          for (int r = 0; r < kPart; ++r) dst[r * D] = __uint_as_float(o[r]);  // (rows that are none: of no meaning)
         } else {
 #pragma unroll
-          for (int r = 0; r < RC; ++r) {
-            const int orow = s_out[buf][row_off + r];
+          for (int r = 0; r < kPart; ++r) {
+            const int orow = s_out[buf][row_off + r0 + r];
             // a row that sees nothing (factor 0) is zero whatever O holds
-            const float f = s_red[wg][0][r];
+            const float f = s_red[wg][0][r0 + r];
             if (orow >= 0)
               a.out[(size_t)orow * D + comp] = __float2bfloat16_rn(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
           }
@@ -918,8 +944,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       }
       tc_before();
       group_sync(1 + wg, 128);  // no warp still reads this unit's tables
-      ++seg;
-    } while (at.next(a, s_share));
+      at.t += n;
+      at.n -= n;
+      if (last) ++seg;
+    } while (!last || at.next(a, s_share));
   }
   tc_before();
   __syncthreads();

@@ -805,11 +805,78 @@ def test_attn_long_flat_tail(qsa, kv, D, n_q, T, gap, v_kind):
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 6 * 2.0 ** -11 + 2.0 ** -18) * big
         err = np.abs(R.f64(out[:, j]) - want)
         assert np.all(err <= tol), (j, err.max(), (err - tol).max())
-        # a thread adds its position of every tile of 128 to its part of the sum in turn: n / 128 FP32
-        # additions, each off by at most 2^-24 of the part (the largest key's: 2^6, to which a tail weight
-        # of less than 2^-18 adds nothing)
-        sums = n / 128 * 2.0 ** -24
+        # a thread adds its position of up to 256 tiles to its part of the sum in turn: FP32 additions, each off
+        # by at most 2^-24 of the part (the largest key's: 2^6, to which a tail weight of less than 2^-18 adds nothing)
+        sums = 256 * 2.0 ** -24
         assert np.abs(R.f64(lse[:, j]) - gap - math.log(w.sum())).max() <= 2.0 ** -18 * (1 + gap) + sums
+
+
+@pytest.mark.parametrize("kv,D,n_q,hq,T,window", [
+    ("bf16", 128, 1, 16, 61204, 0), ("bf16", 64, 1, 16, 400001, 0), ("bf16", 64, 4, 32, 1000000, 0),
+    ("bf16", 256, 1, 16, 400001, 350000), ("fp8", 128, 4, 16, 1000000, 0), ("fp8", 64, 4, 32, 1000000, 700001),
+    ("fp8", 64, 1, 16, 4000000, 0), ("fp8", 256, 4, 32, 400001, 0)])
+def test_attn_long_sums(qsa, kv, D, n_q, hq, T, window):
+    # Keys of every size and the same value at every position: whatever the
+    # weights, the output is that value, bit for bit, as long as sums over a unit
+    # that one CTA has to itself are right to 2^-10 or so (half a BF16 step of 1.75
+    # is 2^-8.8 of it; the weights' own roundings, at most 2^-8 each, are as often
+    # up as down, and T of them leave next to nothing).
+    ps, hk = 256, 2
+    B = -(-torch.cuda.get_device_properties(0).multi_processor_count // (hk * (2 if hq * n_q > 128 else 1)))
+    pages = -(-T // ps)
+    code = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    k = torch.randn((pages, 1, ps, D), generator=torch.Generator("cuda").manual_seed(18), device="cuda").to(code)
+    v = torch.full((pages, hk, ps, D), 1.75, device="cuda").to(code)
+    one = torch.ones(hk, device="cuda")
+    q = torch.randn((1, 1, hq, D), generator=torch.Generator("cuda").manual_seed(19), device="cuda").to(torch.bfloat16)
+    s = k[:, 0].reshape(-1, D)[:T].double() @ q[0, 0].double().t() * float(np.float32(1 / math.sqrt(D)))
+    kc, vc = k.expand(pages, hk, ps, D).contiguous(), v
+    if kv == "fp8":
+        kc, vc = kc.view(torch.uint8), vc.view(torch.uint8)
+    d = _dims(qsa, B, pages, pages, kv, n_q, hq, hk, D, ps)
+    pos, ws = _i32([[T - n_q + j for j in range(n_q)]] * B), qsa.make_kv_workspace(d)
+    q = q.expand(B, n_q, hq, D).contiguous()
+    out, lse = torch.empty_like(q), torch.empty((B, n_q, hq), device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1)
+    qsa.paged_attn(d, q, kc, vc, one, one, table, pos, out, ws, lse=lse, window=window)
+    _ok(qsa, ws)
+    assert torch.all(out == 1.75), (out.min().item(), out.max().item())
+    for j in range(n_q):
+        n = T - n_q + j + 1
+        want = torch.logsumexp(s[max(0, n - window) if window else 0:n], 0)
+        # the scores' FP32 sums (see _attn_tol) and those of the weights
+        size = (k[:, 0].reshape(-1, D)[:n].float().abs() @ q[0, 0].float().abs().t()).max().item() / math.sqrt(D)
+        assert (lse[:, j].double() - want).abs().max().item() <= (D / 8 + 8) * 2.0 ** -23 * size + 2.0 ** -16
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("fp8", 128), ("bf16", 256), ("fp8", 64)])
+@pytest.mark.parametrize("T,window", [(32768, 0), (32770, 0), (65537, 0), (70000, 33000)])
+def test_attn_long_units_end_to_end(qsa, kv, D, T, window):
+    # units long enough for more than one run of tiles in a CTA, the last run of
+    # one tile or of an edge alone, with the newest token's V NaN: only the last
+    # query sees it. Every request is the same, so is every answer.
+    ps, hk, hq, n_q = 64, 2, 16, 4
+    B = -(-torch.cuda.get_device_properties(0).multi_processor_count // hk)
+    table, pages = R.page_table([T], ps, 23)
+    kc, vc, ks, vs = R.make_cache(pages, hk, ps, D, kv, 24)
+    d = _dims(qsa, B, table.shape[1], pages, kv, n_q, hq, hk, D, ps)
+    q = _normal((1, n_q, hq, D), 25).expand(B, n_q, hq, D).contiguous()
+    pos, ws = _i32([[T - n_q + j for j in range(n_q)]] * B), qsa.make_kv_workspace(d)
+    out, lse = torch.empty_like(q), torch.empty((B, n_q, hq), device="cuda")
+    args = [q, kc, vc, ks, vs, table.cuda().repeat(B, 1), pos, out, ws]
+    qsa.paged_attn(d, *args, lse=lse, window=window)
+    _ok(qsa, ws)
+    clean = out.clone()
+    # (the units' first and last pieces are cut at other places: equal up to the roundings)
+    one = _dims(qsa, 1, table.shape[1], pages, kv, n_q, hq, hk, D, ps)
+    for r in (0, B // 2 + 1):
+        _compare_attn((one, q[:1], kc, vc, ks, vs, table.cuda(), pos[:1], out[r:r + 1], ws), lse[r:r + 1], window)
+    vc[int(table[0, (T - 1) // ps]), :, (T - 1) % ps] = math.nan if kv == "bf16" else 0x7F
+    qsa.paged_attn(d, *args, lse=lse, window=window)
+    _ok(qsa, ws)
+    assert torch.isnan(out[:, 3]).all()
+    err = (out[:, :3].float() - clean[:, :3].float()).abs().max().item()
+    assert err <= 2.0 ** -7 * clean.float().abs().max().item(), err
 
 
 def test_attn_without_lse_and_repeated(qsa):
