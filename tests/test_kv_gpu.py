@@ -490,6 +490,42 @@ def test_attn_many_requests(qsa, D, B):
     _attn_case(qsa, ctx, 1, 4, 2, D, 16, "bf16")
 
 
+@pytest.mark.parametrize("gap", [1, 31, 32, 33, 64, 1000, 262144])
+def test_attn_empty_requests_between(qsa, gap):
+    # runs of free slots between live requests, one of them longer than any: the
+    # CTA that has live ones on both sides gets past them (a second's wait of its
+    # roles for one another is not near; one slot after the other, the longest took
+    # 86 ms)
+    import time
+
+    ps, D, hq = 16, 64, 2
+    live = np.unique(np.r_[np.arange(400), 400 + gap + np.arange(3), 403 + 2 * gap + 33 * np.arange(4)])
+    B = int(live[-1]) + 1 + gap % 50
+    kc, vc, ks, vs = R.make_cache(8, 1, ps, D, "bf16", 5)
+    d = _dims(qsa, B, 4, 8, "bf16", 1, hq, 1, D, ps)
+    ws, q = qsa.make_kv_workspace(d), _normal((1, 1, hq, D), 6).expand(B, 1, hq, D).contiguous()
+    table = _i32([[3, 0, 7, 5]]).repeat(B, 1)
+    pos = torch.full((B, 1), -1, dtype=torch.int32)
+    pos[live, 0] = torch.from_numpy((live % 7 * 8 + 2).astype(np.int32))
+    pos = pos.cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((B, 1, hq), 7.0, device="cuda")
+    took = []
+    for _ in range(3):
+        torch.cuda.synchronize()
+        t = time.time()
+        qsa.paged_attn(d, q, kc, vc, None, None, table, pos, out, ws, lse=lse)
+        torch.cuda.synchronize()
+        took.append(time.time() - t)
+    _ok(qsa, ws)
+    assert min(took) < 0.04, took
+    seen = torch.from_numpy(live).cuda()
+    _compare_attn((_dims(qsa, len(live), 4, 8, "bf16", 1, hq, 1, D, ps), q[seen], kc, vc, ks, vs, table[seen], pos[seen],
+                   out[seen], ws), lse[seen])
+    rest = torch.ones(B, dtype=torch.bool, device="cuda")
+    rest[seen] = False
+    assert torch.all(out[rest] == 0) and torch.all(lse[rest] == -math.inf)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_attn_positions_of_any_order(qsa, kv):
     # queries far apart, the same position twice, padding rows between, a page
