@@ -172,7 +172,9 @@ struct Split {
     const long long tiles = (load & ((1LL << 40) - 1)) * units;
     seg = tiles > a.grid ? kSegCost : 0;
     const long long all = slots(load) * units;
-    static_assert(((kSegCost + 1) & kSegCost) == 0, "the least share, kSegCost + 1 slots, is a power of two");
+    // shares of kSegCost + 1 slots, or one less where that does not divide: such
+    // a one may hold no tile (Walk::cut)
+    static_assert(((kSegCost + 1) & kSegCost) == 0, "a division by a power of two");
     const long long most = seg ? (all + kSegCost) / (kSegCost + 1) : all;
     ctas = (int)min((long long)a.grid, most);
     q = ctas > 0 ? quot(all, ctas) : 0;

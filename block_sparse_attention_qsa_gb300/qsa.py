@@ -648,9 +648,10 @@ def _ws_on(dev: int, ws: torch.Tensor):
 def kv_append(d: Dims, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws, rope: Optional[Rope] = None,
               q=None, q_out=None, stream=None):
     """New keys and values (bf16 [B][n][H_kv][D], any strides) into the cache
-    at positions pos [B][n] (consecutive per request, -1 for no token): keys
-    rotated by ``rope`` if given, both quantised for an E4M3 cache. With q
-    (bf16 [B][n][H_q][D]) the same tokens' queries are rotated into q_out."""
+    at positions pos [B][n] (consecutive per request; -1 for no token, behind
+    the request's tokens, not in front of them): keys rotated by ``rope`` if
+    given, both quantised for an E4M3 cache. With q (bf16 [B][n][H_q][D]) the
+    same tokens' queries are rotated into q_out."""
     if rope is None or isinstance(rope, Rope):
         st = _fast.kv_append(d, k, v, k_cache, v_cache, k_scale, v_scale, page_table, pos, ws,
                              None if rope is None else rope.args, None if rope is None else rope.device_index, q,

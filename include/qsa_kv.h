@@ -125,7 +125,8 @@ qsa_status qsa_kv_workspace_size(const qsa_dims* dims, size_t* bytes);
  * rotated into q_out; q needs a rope.
  *
  * The tokens of a request are consecutive: pos[r][j] is pos[r][0] + j, or -1
- * for no token. One that is neither is reported (kind 6), one past the page
+ * for no token (a padded batch has its padding behind the tokens, not in front
+ * of them). One that is neither is reported (kind 6), one past the page
  * table is reported (kind 1), and both are skipped, their q_out row too. A
  * page id outside the cache is reported (kind 2) and the token's K and V are
  * not written. Requests must not share a page that the call writes to.
@@ -157,16 +158,26 @@ qsa_status qsa_kv_gather(const qsa_dims* dims, int32_t n_tok, const void* k_cach
  * g = h / (n_q_heads / n_kv_heads): out = softmax(sm_scale * q K^T) V over the
  * positions max(0, p - window + 1) .. p (window 0: 0 .. p), and
  * lse[r][j][h] = ln(sum of exp) of those scores where lse is not NULL (fp32
- * [batch][n_q][n_q_heads]). FP32 softmax statistics and accumulation, BF16
- * out. K and V outside a query's positions never reach its output, whatever
- * they hold. A row without positions (p = -1, or p below -1 or past the page
- * table, which is reported as kind 1) gives zeros and an lse of -infinity, as
- * does a row whose scores are all -infinity. The sums before the division by
- * the softmax's are FP32, with weights up to 2^8: values of 2^(119 - log2 of the
- * positions) or more may overflow in them. A page id outside the cache is
- * reported (kind 2) and its positions are left out. The cache's positions are
- * split over the GPU and the pieces joined in a fixed order: the same call
- * gives the same bits. q and out are contiguous, as for qsa_sparse_attn. */
+ * [batch][n_q][n_q_heads]). K and V outside a query's positions never reach
+ * its output, whatever they hold. A row without positions (p = -1, or p below
+ * -1 or past the page table, which is reported as kind 1) gives zeros and an
+ * lse of -infinity, as does a row whose scores are all -infinity. A page id
+ * outside the cache is reported (kind 2) and its positions are left out. The
+ * cache's positions are split over the GPU and the pieces joined in a fixed
+ * order: the same call gives the same bits. q and out are contiguous, as for
+ * qsa_sparse_attn.
+ *
+ * FP32 softmax statistics and accumulation, BF16 out. The sums before the
+ * division by the softmax's have weights up to 2^8: values of 2^(119 - log2 of
+ * the positions) or more may overflow in them. What has fewer bits:
+ *  - the weights of the second product (not those in the softmax's sum), each
+ *    off by at most 2^-8 of itself. With an E4M3 cache that holds from 2^-12 of
+ *    a row's largest weight on; smaller ones are off by less than 2^-20 of it,
+ *    as often up as down, so that a long tail of them keeps its sum: what it
+ *    adds to the output's error has a standard deviation of at most 2^-11 of
+ *    the largest |V|, at any length;
+ *  - with an E4M3 cache, the queries: a component is off by at most 2^-22 of
+ *    its head's largest. */
 qsa_status qsa_paged_attn(const qsa_dims* dims, int32_t window, const void* q, const void* k_cache,
                           const void* v_cache, const float* k_scale, const float* v_scale,
                           const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
