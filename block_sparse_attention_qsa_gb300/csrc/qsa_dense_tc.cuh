@@ -276,8 +276,8 @@ __device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float
 // What is added to lo of a position's weights before it is rounded to E4M3, whose
 // steps are of 2^-9 there: between -2^-10 and 2^-10 (exclusive: a weight of 0
 // stays 0), equidistributed over any run of positions (multiples of the golden
-// ratio, modulo 1). It depends on the position alone, so that a call gives the
-// same bits however its work is split.
+// ratio, modulo 1). It depends on the position alone: the same call gives the
+// same bits.
 __device__ __forceinline__ float dither(int p) {
   return (float)(((int)((uint32_t)p * 0x9e3779b9u) >> 8) | 1) * 0x1p-33f;
 }
