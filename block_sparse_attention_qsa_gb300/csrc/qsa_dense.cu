@@ -36,7 +36,8 @@ DenseWs dense_ws(const qsa_dims& d, int num_sms) {
 
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
-                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s, bool short_k) {
+                              const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s, bool short_k,
+                              const Prefix& prefix) {
   const int sms = device_sm_count();
   const DenseWs w = dense_ws(d, sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -45,6 +46,8 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.page_table = page_table;
+  a.prefix_table = prefix.table;
+  a.prefix_len = prefix.len;
   a.q_pos = q_pos;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;

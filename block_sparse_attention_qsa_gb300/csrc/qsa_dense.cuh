@@ -41,6 +41,7 @@ struct DenseArgs {
   const float* k_scale;
   const float* v_scale;
   const int32_t* page_table;
+  const int32_t* prefix_table;  // the pages of positions below prefix_len, which all requests share
   const int32_t* q_pos;
   __nv_bfloat16* out;
   float* lse;
@@ -49,6 +50,7 @@ struct DenseArgs {
   int32_t* err;
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
   int page_size, page_shift, max_pages, num_pages, window, grid;
+  int prefix_len;  // whole pages
   float sm_scale;
   float one;  // 1
 };
@@ -378,9 +380,11 @@ struct PageFeed {
   __device__ __forceinline__ int page_of(const DenseArgs& a, const Walk<TILE>& at, int i) const {
     const unsigned p = (unsigned)(first_box + i) << box_shift;  // (a box that is seen starts below 2^31)
     if (i >= n_boxes || p >= (unsigned)at.g.hi || p + (1u << box_shift) <= (unsigned)at.g.lo) return -1;
-    const int page = a.page_table[(size_t)at.r * a.max_pages + (p >> a.page_shift)];
+    const bool shared = p < (unsigned)a.prefix_len;
+    const int32_t* table = shared ? a.prefix_table : a.page_table + (size_t)at.r * a.max_pages;
+    const int page = table[p >> a.page_shift];
     if ((unsigned)page < (unsigned)a.num_pages) return page;
-    record_error(a.err, kErrPage, at.r, 0, page);
+    record_error(a.err, kErrPage, shared ? -1 : at.r, 0, page);
     return -1;
   }
   __device__ __forceinline__ void start(const DenseArgs& a, const Walk<TILE>& at) {

@@ -1,0 +1,220 @@
+// Eviction from the paged cache by accumulated attention weight.
+//
+// Of a request's n > keep tokens the first `sinks`, the last `recent` and the
+// heaviest between them stay. A cluster of CTAs takes a request and finds the
+// weight of the last one that stays by a radix selection (three digits of the
+// weight's order-preserving key, the counts of the CTAs added up through
+// distributed shared memory), then numbers those that stay in the order of
+// their positions. A second kernel, chained with programmatic dependent
+// launch, copies their K and V.
+#include <algorithm>
+
+#include "qsa_serve_internal.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;
+
+__device__ __forceinline__ uint64_t warp_inclusive(uint64_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ void st_peer_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// Sum of x over the threads before this one in the block; *all: over the block.
+__device__ __forceinline__ uint64_t block_exclusive(uint64_t x, uint64_t (&scan)[kSelWarps], uint64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t inc = warp_inclusive(x);
+  if (lane == 31) scan[warp] = inc;
+  __syncthreads();
+  uint64_t before = inc - x, total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    before += w < warp ? scan[w] : 0;
+    total += scan[w];
+  }
+  __syncthreads();
+  *all = total;
+  return before;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ uint32_t s_hist[kBins];
+  __shared__ uint64_t s_scan[kSelWarps], s_slice[kMaxCluster];
+  __shared__ uint32_t s_bin, s_left;
+  const int tid = threadIdx.x;
+  const int rank = (int)cluster_rank(), ctas = (int)cluster_size(), r = blockIdx.x / ctas;
+  pdl_wait();
+  pdl_trigger();
+  // (positions are below 2^31; unsigned, so that a step past the last one is still a number)
+  const unsigned cap = (unsigned)(a.max_pages * a.page_size), cap_out = (unsigned)(a.out_pages * a.page_size);
+  const unsigned keep = (unsigned)a.keep;
+  unsigned n = (unsigned)a.len[r];
+  if (n > cap) {
+    if (rank == 0 && tid == 0) record_error(a.err, kErrLength, r, 0, (int)n);
+    n = 0;
+  }
+  const float* w = a.weight + (long long)r * cap;
+  float* w_out = a.weight_out + (long long)r * cap_out;
+  int32_t* kept = a.kept + (long long)r * a.keep;
+  const unsigned left = min(n, keep), first = (unsigned)(rank * kSelThreads + tid), step = (unsigned)(ctas * kSelThreads);
+  for (unsigned i = left + first; i < cap_out; i += step) {
+    w_out[i] = 0.f;
+    if (i < keep) kept[i] = -1;
+  }
+  cluster_sync();  // every CTA has read len (and has started)
+  if (rank == 0 && tid == 0) a.new_len[r] = (int)left;
+  if (n <= keep) {
+    for (unsigned i = first; i < n; i += step) {
+      kept[i] = (int)i;
+      w_out[i] = w[i];
+    }
+    return;  // (the whole cluster)
+  }
+  // positions lo .. hi - 1 are chosen from, `need` of them
+  const unsigned lo = (unsigned)a.sinks, hi = n - (unsigned)a.recent;
+  const unsigned slice = (n + ctas - 1) / ctas, s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
+  uint32_t need = (uint32_t)(a.keep - a.sinks - a.recent), prefix = 0, mask = 0;
+  if (need > 0) {
+#pragma unroll 1
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;  // (the last digit has a bit of the second's)
+      for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+      __syncthreads();
+      for (unsigned t = max(s0, lo) + tid; t < min(s1, hi); t += kSelThreads) {
+        const uint32_t k = order_key(w[t]);
+        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & (kBins - 1)], 1u);
+      }
+      cluster_sync();
+      // every CTA adds up all counts, from the largest digit down (4 a thread)
+      uint32_t c[4];
+      uint64_t mine = 0, all;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int bin = kBins - 1 - (tid * 4 + i);
+        c[i] = 0;
+        for (int p = 0; p < ctas; ++p) c[i] += ld_peer(peer_addr(&s_hist[bin], p));
+        mine += c[i];
+      }
+      const uint64_t before = block_exclusive(mine, s_scan, &all);
+      if (before < need && need <= before + mine) {  // one thread
+        uint32_t b = (uint32_t)before;
+        int i = 0;
+        while (b + c[i] < need) b += c[i++];
+        s_bin = (uint32_t)(kBins - 1 - (tid * 4 + i));
+        s_left = need - b;
+      }
+      cluster_sync();  // (and the counts have been read by every CTA)
+      prefix |= s_bin << shift;
+      mask |= (uint32_t)(kBins - 1) << shift;
+      need = s_left;
+    }
+  }
+  // Those above the last one's key stay, and the first `need` that equal it.
+  const uint32_t last = need > 0 ? prefix : 0xffffffffu;  // (no weight has that key)
+  const unsigned per = (s1 - s0 + kSelThreads - 1) / kSelThreads;
+  const unsigned t0 = min(s0 + tid * per, s1), t1 = min(t0 + per, s1);
+  uint64_t count = 0;  // those that equal it << 32 | those that stay anyway
+  for (unsigned t = t0; t < t1; ++t) {
+    const bool sure = t < lo || t >= hi;
+    const uint32_t k = order_key(w[t]);
+    count += sure || k > last ? 1ull : k == last ? 1ull << 32 : 0ull;
+  }
+  uint64_t all;
+  uint64_t before = block_exclusive(count, s_scan, &all);
+  if (tid < ctas) st_peer_u64(peer_addr(&s_slice[rank], tid), all);
+  cluster_sync();
+  for (int p = 0; p < rank; ++p) before += s_slice[p];
+  uint32_t ties = (uint32_t)(before >> 32), at = (uint32_t)before + min(ties, need);
+  for (unsigned t = t0; t < t1; ++t) {
+    const bool sure = t < lo || t >= hi;
+    const float x = w[t];
+    const uint32_t k = order_key(x);
+    bool stays = sure || k > last;
+    if (!stays && k == last) stays = ties++ < need;
+    if (stays) {
+      kept[at] = (int)t;
+      w_out[at] = x;
+      ++at;
+    }
+  }
+}
+
+// K and V of the tokens that stay. A block takes kCopyTok of them, whose rows
+// are worked out first, and up to 256 items; an item is 16 bytes of the same
+// head of K or V in every token.
+constexpr int kCopyTok = 32, kCopyDeep = 4;
+
+__global__ void __launch_bounds__(256) evict_copy_kernel(const EvictArgs a) {
+  __shared__ long long s_src[kCopyTok], s_dst[kCopyTok];
+  const int tid = threadIdx.x;
+  const int per_req = (int)((a.keep + kCopyTok - 1LL) / kCopyTok), r = blockIdx.x / per_req;
+  const int i0 = (blockIdx.x - r * per_req) * kCopyTok, n = min(kCopyTok, a.keep - i0);
+  const int vecs = a.row_bytes / 16, per = a.hk * vecs, items = 2 * per;
+  pdl_wait();
+  if (tid < n) {
+    const int i = i0 + tid, t = a.kept[(long long)r * a.keep + i];
+    long long src = -1, dst = -1;
+    if (t >= 0) {
+      const int from = a.page_table[(long long)r * a.max_pages + t / a.page_size];
+      const int to = a.page_table_out[(long long)r * a.out_pages + i / a.page_size];
+      const bool bad_from = (unsigned)from >= (unsigned)a.num_pages, bad_to = (unsigned)to >= (unsigned)a.num_pages;
+      if (bad_from || bad_to) {
+        if (blockIdx.y == 0) record_error(a.err, kErrPage, r, 0, bad_from ? from : to);
+      } else {
+        src = ((long long)from * a.hk * a.page_size + t % a.page_size) * a.row_bytes;
+        dst = ((long long)to * a.hk * a.page_size + i % a.page_size) * a.row_bytes;
+        if (src == dst) src = -1;
+      }
+    }
+    s_src[tid] = src;
+    s_dst[tid] = dst;
+  }
+  const int here = min(256, items - (int)blockIdx.y * 256), lanes = 256 / here;
+  const int sub = tid / here, item = (int)blockIdx.y * 256 + tid - sub * here;
+  const bool is_v = item >= per;
+  const int h = is_v ? item - per : item, g = h / vecs;
+  uint8_t* cache = (is_v ? a.v_cache : a.k_cache) + ((long long)g * a.page_size) * a.row_bytes + (h - g * vecs) * 16;
+  __syncthreads();
+  if (sub >= lanes) return;
+  for (int t0 = sub; t0 < n; t0 += kCopyDeep * lanes) {
+    uint4 x[kCopyDeep];
+#pragma unroll
+    for (int u = 0; u < kCopyDeep; ++u) {
+      const int t = t0 + u * lanes;
+      if (t < n && s_src[t] >= 0) x[u] = ld16(cache + s_src[t]);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyDeep; ++u) {
+      const int t = t0 + u * lanes;
+      if (t < n && s_src[t] >= 0) *reinterpret_cast<uint4*>(cache + s_dst[t]) = x[u];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
+  // CTAs of a request: enough that few requests use the whole GPU, each with 2,048 positions or more
+  const int cap = a.max_pages * a.page_size;
+  unsigned c = 1;
+  while (c < kMaxCluster && (long long)a.batch * c < 2LL * device_sm_count() && cap / (2 * (int)c) >= 2048) c *= 2;
+  cudaError_t e = launch_clusters(evict_select_kernel, dim3((unsigned)a.batch * c), dim3(kSelThreads), c, s, a);
+  if (e != cudaSuccess) return e;
+  const int vecs = a.row_bytes / 16, items = 2 * a.hk * vecs;
+  const long long gx = (long long)a.batch * ((a.keep + kCopyTok - 1LL) / kCopyTok);  // (below 2^31: qsa_kv_evict)
+  return launch_k(evict_copy_kernel, dim3((unsigned)gx, (unsigned)((items + 255) / 256)), dim3(256), 0, s, true, a);
+}
+
+}  // namespace qsa

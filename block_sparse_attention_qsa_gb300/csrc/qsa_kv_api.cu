@@ -2,15 +2,9 @@
 // host side of the rotary frequencies.
 #include <math.h>
 
-#include <initializer_list>
-
 #include "qsa_kv_internal.cuh"
 
-using namespace qsa;
-
-namespace {
-
-constexpr double kPi = 3.14159265358979323846;
+namespace qsa {
 
 qsa_status check_kv_dims(const qsa_dims* d) {
   if (!d) return QSA_ERR_INVALID_ARG;
@@ -31,17 +25,13 @@ qsa_status check_kv_dims(const qsa_dims* d) {
   return QSA_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace qsa
 
-bool aligned_all(uintptr_t a, std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!aligned(p, a)) return false;
-  return true;
-}
+using namespace qsa;
 
-bool check_header(const void* ws, size_t bytes) { return ws && aligned(ws, 256) && bytes >= 256; }
+namespace {
 
-qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
+constexpr double kPi = 3.14159265358979323846;
 
 // (a dimension of one element has no stride, whatever the caller's says)
 Strided strided(const void* p, const qsa_strides* s, int batch, int n_tok, int heads, int dim) {

@@ -1,12 +1,26 @@
 // Declarations shared by the translation units of the entry points in qsa_kv.h.
 #pragma once
 
+#include <initializer_list>
+
 #include "qsa_internal.cuh"
 #include "qsa_kv.h"
 
 namespace qsa {
 
 constexpr int kErrOrder = 6;  // qsa_kv_append: a request's tokens are not consecutive
+
+// the checks of qsa_dims that all entry points round the cache begin with
+qsa_status check_kv_dims(const qsa_dims* d);
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool aligned_all(uintptr_t a, std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned(p, a)) return false;
+  return true;
+}
+inline bool check_header(const void* ws, size_t bytes) { return ws && aligned(ws, 256) && bytes >= 256; }
+inline qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
 
 // A rotation, or none (turns null).
 struct Rope {
@@ -37,11 +51,16 @@ struct DenseWs {
   size_t units, parts, total;
 };
 DenseWs dense_ws(const qsa_dims& d, int num_sms);
+// The pages of positions below `len`, for every request (null: none, len 0).
+struct Prefix {
+  const int32_t* table;
+  int len;
+};
 // short_k: the failure-detection test (qsa_test_paged_attn_timeout)
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
                               const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s,
-                              bool short_k = false);
+                              bool short_k = false, const Prefix& prefix = Prefix{nullptr, 0});
 
 // 16-byte loads and stores of streamed data
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }

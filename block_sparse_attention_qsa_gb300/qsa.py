@@ -47,6 +47,10 @@ KV_EXPORTS = (
     "qsa_rope_table", "qsa_rope", "qsa_kv_workspace_size", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn",
     "qsa_test_paged_attn_timeout",
 )
+# and those of include/qsa_serve.h, the operators for serving a batch in a bounded cache
+SERVE_EXPORTS = (
+    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_kv_weight", "qsa_kv_evict", "qsa_verify_drafts",
+)
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
 
@@ -54,6 +58,8 @@ MAX_DRAFT_GAP = 64  # QSA_MAX_DRAFT_GAP
 MAX_CHUNK = 65536  # QSA_MAX_CHUNK
 MAX_SCORE_BATCH = 16384  # QSA_MAX_SCORE_BATCH
 MAX_KV_HEADS = 1024  # QSA_MAX_KV_HEADS
+MAX_DRAFTS = 31  # QSA_MAX_DRAFTS
+MAX_VOCAB = 1 << 24  # QSA_MAX_VOCAB
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # qsa_rope_layout
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}  # qsa_rope_scaling
@@ -104,6 +110,12 @@ class RopeArgs(ctypes.Structure):
     ]
 
 
+class ProbStrides(ctypes.Structure):
+    """qsa_prob_strides: element strides of [batch][row][vocab] probabilities."""
+
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libqsa.so is not built ({LIB_PATH}); run __graft_entry__.build()")
@@ -142,6 +154,14 @@ def _load() -> ctypes.CDLL:
         "qsa_kv_gather": (I, [D, N, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_paged_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_test_paged_attn_timeout": (I, [D, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+    })
+    F, T = ctypes.c_float, ctypes.POINTER(ProbStrides)
+    sig.update({
+        "qsa_prefix_workspace_size": (I, [D, N, ctypes.POINTER(SZ)]),
+        "qsa_prefix_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_kv_weight": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_kv_evict": (I, [D, N, N, N, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_verify_drafts": (I, [N, N, N, N, P, T, P, T, P, P, P, P, P, SZ, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -746,6 +766,148 @@ def test_paged_attn_timeout(d: Dims, q, k_cache, v_cache, k_scale, v_scale, page
     check_errors then reports ERR_TIMEOUT. For failure-detection tests."""
     _paged_attn(lib.qsa_test_paged_attn_timeout, "qsa_test_paged_attn_timeout", d, q, k_cache, v_cache, k_scale,
                 v_scale, page_table, q_pos, out, ws, lse, window, stream)
+
+
+# ---------------------------------------------------------------------------
+# operators for serving a batch in a bounded cache (include/qsa_serve.h)
+# ---------------------------------------------------------------------------
+def prefix_workspace_size(d: Dims, prefix_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.qsa_prefix_workspace_size(ctypes.byref(d), prefix_pages, ctypes.byref(n)), "qsa_prefix_workspace_size")
+    return n.value
+
+
+def make_prefix_workspace(d: Dims, prefix_pages: int, device="cuda", stream=None) -> torch.Tensor:
+    """Allocate and zero a workspace for prefix_attn with ``d`` and up to
+    ``prefix_pages`` shared pages; the other operators round the cache can be
+    called on it too (torch owns the memory)."""
+    n = prefix_workspace_size(d, prefix_pages)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    _check(lib.qsa_workspace_init(ctypes.c_void_p(ws.data_ptr()), n, _stream(stream)), "qsa_workspace_init")
+    return ws
+
+
+def prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, ws, lse=None,
+                stream=None):
+    """paged_attn of a batch whose requests share a prefix: positions below
+    prefix_table.numel() * page_size of every request live in the pages that
+    prefix_table (int32 [n], n may be 0) names, the others in those of the
+    request's page_table row. ws is make_prefix_workspace's."""
+    dev = _current_device()
+    B, n_q, H = d.batch, d.n_q, d.n_q_heads
+    shape = (B, n_q, H, d.head_dim)
+    qp = _want_on(dev, q, "q", shape, _BF16)
+    op = _want_on(dev, out, "out", shape, _BF16)
+    kc, vc, ksc, vsc, pt = _cache_ptrs(dev, d, k_cache, v_cache, k_scale, v_scale, page_table)
+    if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be a tensor of one dimension")
+    n = prefix_table.shape[0]
+    xp = _want_on(dev, prefix_table, "prefix_table", (n,), _I32)
+    pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
+    lp = None if lse is None else _want_on(dev, lse, "lse", (B, n_q, H), _F32)
+    w, nb = _ws_on(dev, ws)
+    st = lib.qsa_prefix_attn(d, n, xp, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
+    if st:
+        _check(st, "qsa_prefix_attn")
+
+
+def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, decay: float = 1.0, stream=None):
+    """weight (fp32 [B][max_pages * page_size]) = decay * weight + the softmax
+    weight that each position gets from the newest tokens' query heads, given
+    the lse that paged_attn or prefix_attn returned for them (fp32
+    [B][n_q][H_q]). Positions that no query sees are left as they are."""
+    dev = _current_device()
+    B, n_q, H = d.batch, d.n_q, d.n_q_heads
+    fp8 = d.kv_dtype == KV_FP8_E4M3
+    qp = _want_on(dev, q, "q", (B, n_q, H, d.head_dim), _BF16)
+    kc = _want_on(dev, k_cache, "k_cache", (d.num_pages, d.n_kv_heads, d.page_size, d.head_dim),
+                  torch.uint8 if fp8 else _BF16)
+    ks = _want_on(dev, k_scale, "k_scale", (d.n_kv_heads,), _F32) if fp8 or k_scale is not None else None
+    pt = _want_on(dev, page_table, "page_table", (B, d.max_pages), _I32)
+    pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
+    lp = _want_on(dev, lse, "lse", (B, n_q, H), _F32)
+    wp = _want_on(dev, weight, "weight", (B, d.max_pages * d.page_size), _F32)
+    w, nb = _ws_on(dev, ws)
+    st = lib.qsa_kv_weight(d, decay, qp, kc, ks, pt, pp, lp, wp, w, nb, _stream(stream))
+    if st:
+        _check(st, "qsa_kv_weight")
+
+
+def kv_evict(d: Dims, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length, ws,
+             sinks: int = 0, recent: int = 0, stream=None):
+    """Of each request's length[r] tokens at most kept.shape[1] stay: the first
+    ``sinks``, the last ``recent`` and those with the most weight between. Their
+    old positions go to kept (int32 [B][keep], ascending, -1 behind the last),
+    their number to new_length (int32 [B]; it may be length), their K and V to
+    the pages of page_table_out (int32 [B][n]), their weights to weight_out
+    (fp32 [B][n * page_size], 0 behind the last)."""
+    dev = _current_device()
+    B, ps = d.batch, d.page_size
+    shape = (d.num_pages, d.n_kv_heads, ps, d.head_dim)
+    dt = torch.uint8 if d.kv_dtype == KV_FP8_E4M3 else _BF16
+    kc = _want_on(dev, k_cache, "k_cache", shape, dt)
+    vc = _want_on(dev, v_cache, "v_cache", shape, dt)
+    pt = _want_on(dev, page_table, "page_table", (B, d.max_pages), _I32)
+    for t, name in ((page_table_out, "page_table_out"), (kept, "kept")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a tensor of two dimensions")
+    n, keep = page_table_out.shape[1], kept.shape[1]
+    po = _want_on(dev, page_table_out, "page_table_out", (B, n), _I32)
+    kp = _want_on(dev, kept, "kept", (B, keep), _I32)
+    lp = _want_on(dev, length, "length", (B,), _I32)
+    np_ = _want_on(dev, new_length, "new_length", (B,), _I32)
+    wi = _want_on(dev, weight, "weight", (B, d.max_pages * ps), _F32)
+    wo = _want_on(dev, weight_out, "weight_out", (B, n * ps), _F32)
+    w, nb = _ws_on(dev, ws)
+    st = lib.qsa_kv_evict(d, keep, sinks, recent, n, lp, wi, pt, po, kc, vc, wo, kp, np_, w, nb, _stream(stream))
+    if st:
+        _check(st, "qsa_kv_evict")
+
+
+PROB_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # qsa_prob_dtype
+
+
+def _want_probs(dev: int, t: torch.Tensor, name: str, shape, dtype):
+    """(address, strides) of [batch][row][vocab] probabilities on the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the QSA path has no CPU implementation)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), ProbStrides(t.stride(0), t.stride(1))
+
+
+def verify_drafts(target, draft, tokens, uniform, accepted, out_tokens, ws, stream=None):
+    """Verifies drafted tokens (int32 [B][n], -1 behind a request's last; a row
+    that begins with -2 is no request) against the target's probabilities
+    [B][n + 1][V] (fp32 or bf16, any strides with a contiguous last dimension)
+    with the random numbers uniform (fp32 [B][n + 1], in [0, 1)); draft are the
+    probabilities [B][n][V] they were sampled from, None if they were not
+    sampled. Writes the number accepted (int32 [B]) and those tokens with the
+    next one behind them, then -1 (int32 [B][n + 1]). ws: any workspace."""
+    dev = _current_device()
+    if not isinstance(target, torch.Tensor) or target.dim() != 3 or target.dtype not in PROB_DTYPES:
+        raise ValueError("target must be a float32 or bfloat16 tensor [B][n + 1][V]")
+    B, n, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    tp, ts = _want_probs(dev, target, "target", (B, n + 1, V), target.dtype)
+    qp, qs = (None, None) if draft is None else _want_probs(dev, draft, "draft", (B, n, V), target.dtype)
+    xp = _want_on(dev, tokens, "tokens", (B, n), _I32)
+    up = _want_on(dev, uniform, "uniform", (B, n + 1), _F32)
+    ap = _want_on(dev, accepted, "accepted", (B,), _I32)
+    op = _want_on(dev, out_tokens, "out_tokens", (B, n + 1), _I32)
+    w, nb = _ws_on(dev, ws)
+    st = lib.qsa_verify_drafts(B, n, V, PROB_DTYPES[target.dtype], tp, ts, qp, qs, xp, up, ap, op, w, nb,
+                               _stream(stream))
+    if st:
+        _check(st, "qsa_verify_drafts")
 
 
 def check_errors(ws: torch.Tensor, stream=None) -> Tuple[int, Tuple[int, int, int, int]]:
