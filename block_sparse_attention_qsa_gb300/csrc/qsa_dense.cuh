@@ -45,7 +45,7 @@ struct DenseArgs {
   const int32_t* q_pos;
   __nv_bfloat16* out;
   float* lse;
-  long long* unit_desc;  // where each unit's pieces are (see unit_* below)
+  long long* unit_desc;  // where each unit's pieces are (see unit_* below); null: the stream has no pieces
   float* parts;          // [grid][2] pieces: m[rows], l[rows], acc[rows][D]
   int32_t* err;
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
@@ -329,7 +329,7 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)
   if (blockIdx.x == 0) {
     for (int r = r0; r < r1; ++r) {
       report_positions(a, r);
-      if (a.batch > kJoinScan && range_of(a, r).tiles(TILE) == 0)
+      if (a.unit_desc && a.batch > kJoinScan && range_of(a, r).tiles(TILE) == 0)
         for (int x = 0; x < units; ++x) a.unit_desc[(long long)r * units + x] = kUnitEmpty;
     }
   }
