@@ -1,4 +1,4 @@
-#include "qsa_dense.cuh"
+#include "qsa_prefix.cuh"
 
 namespace qsa {
 
@@ -34,6 +34,91 @@ DenseWs dense_ws(const qsa_dims& d, int num_sms) {
   return w;
 }
 
+static cudaError_t launch_dense(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache,
+                                const void* v_cache, bool short_k, cudaStream_t s) {
+  switch (d.head_dim) {
+    case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, short_k, s);
+    case 128: return launch_dense_128(rows, d, a, k_cache, v_cache, short_k, s);
+    default: return launch_dense_256(rows, d, a, k_cache, v_cache, short_k, s);
+  }
+}
+
+// The prefix's work: units, and the parts that its tiles are cut into, of at
+// most kMaxPart tiles each (an accumulator in tensor memory holds no more, see
+// kRun in qsa_dense_tc.cuh).
+constexpr int kMaxPart = 256, kWaves = 3;
+struct PrefixPlan {
+  int rows, row_tiles, units, tiles, splits;
+  size_t pieces;  // at most, for this prefix and shorter ones
+};
+static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
+  PrefixPlan p;
+  p.rows = d.batch * d.n_q * (d.n_q_heads / d.n_kv_heads);
+  p.row_tiles = (p.rows + kPrefixRows - 1) / kPrefixRows;
+  const int at_once = d.head_dim == 256 || p.row_tiles == 1 ? 1 : 2;  // row tiles of a CTA
+  p.units = d.n_kv_heads * ((p.row_tiles + at_once - 1) / at_once);
+  const int tile = d.head_dim == 256 ? 64 : 128;
+  p.tiles = (prefix_len + tile - 1) / tile;
+  const int least = (p.tiles + kMaxPart - 1) / kMaxPart;
+  // Parts for 1 to kWaves full waves of CTAs; a CTA's time is its tiles and
+  // about as much as 4 for its beginning and its piece.
+  const int most = std::max(1, kWaves * sms / p.units);
+  p.splits = std::max(least, 1);
+  long long best = 1LL << 62;
+  for (int k = 1; k <= kWaves; ++k) {
+    const int s = std::min(p.tiles, std::max(least, std::max(1, k * sms / p.units)));
+    const long long waves = ((long long)p.units * s + sms - 1) / sms;
+    const long long cost = waves * ((p.tiles + s - 1) / s + 4);
+    if (cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
+  p.pieces = (size_t)d.n_kv_heads * p.row_tiles * std::max(least, std::min(p.tiles, most));
+  return p;
+}
+
+struct PrefixWs {
+  size_t whole, parts, total;
+};
+static PrefixWs prefix_ws_layout(const qsa_dims& d, int prefix_len, int sms) {
+  PrefixWs w;
+  const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads), per = unit_rows(d);
+  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per), row = (d.head_dim + 2) * sizeof(float);
+  w.whole = dense_ws(d, sms).total;
+  w.parts = align_up(w.whole + units * per * row, 256);
+  w.total = align_up(w.parts + prefix_plan(d, prefix_len, sms).pieces * kPrefixRows * row, 256);
+  return w;
+}
+size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms) {
+  return prefix_len > 0 ? prefix_ws_layout(d, prefix_len, num_sms).total : dense_ws(d, num_sms).total;
+}
+
+static cudaError_t launch_with_prefix(const qsa_dims& d, DenseArgs a, int rows, uint8_t* ws, const void* k_cache,
+                                      const void* v_cache, cudaStream_t s) {
+  const PrefixWs w = prefix_ws_layout(d, a.prefix_len, a.grid);
+  const PrefixPlan plan = prefix_plan(d, a.prefix_len, a.grid);
+  a.whole = reinterpret_cast<float*>(ws + w.whole);
+  a.row_blocks = (a.n_q * a.group + rows - 1) / rows;
+  cudaError_t e = launch_dense(rows, d, a, k_cache, v_cache, false, s);
+  if (e != cudaSuccess) return e;
+  PrefixArgs p = {};
+  p.a = a;
+  p.parts = reinterpret_cast<float*>(ws + w.parts);
+  p.rows = plan.rows;
+  p.row_tiles = plan.row_tiles;
+  p.units = plan.units;
+  p.splits = plan.splits;
+  p.tiles = plan.tiles;
+  p.own_rows = rows;
+  switch (d.head_dim) {
+    case 64: return launch_prefix_64(d, p, k_cache, v_cache, s);
+    case 128: return launch_prefix_128(d, p, k_cache, v_cache, s);
+    default: return launch_prefix_256(d, p, k_cache, v_cache, s);
+  }
+}
+
+// Own positions, prefix (if there is one), joint.
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
                               const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s, bool short_k,
@@ -68,11 +153,8 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
   a.one = 1.f;
   const int rows = unit_rows(d);
-  switch (d.head_dim) {
-    case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, short_k, s);
-    case 128: return launch_dense_128(rows, d, a, k_cache, v_cache, short_k, s);
-    default: return launch_dense_256(rows, d, a, k_cache, v_cache, short_k, s);
-  }
+  if (prefix.len > 0) return launch_with_prefix(d, a, rows, base, k_cache, v_cache, s);
+  return launch_dense(rows, d, a, k_cache, v_cache, short_k, s);
 }
 
 }  // namespace qsa

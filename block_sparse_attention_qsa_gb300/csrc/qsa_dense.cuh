@@ -47,6 +47,7 @@ struct DenseArgs {
   float* lse;
   long long* unit_desc;  // where each unit's pieces are (see unit_* below); null: the stream has no pieces
   float* parts;          // [grid][2] pieces: m[rows], l[rows], acc[rows][D]
+  float* whole;          // with a shared prefix: [unit] the pieces of units that are one CTA's
   int32_t* err;
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
   int page_size, page_shift, max_pages, num_pages, window, grid;
@@ -129,6 +130,16 @@ __device__ __forceinline__ bool valid_pos(const DenseArgs& a, int p) { return p 
 __device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
   return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
+// Whether every query of a request at positions p sees the whole prefix. If so,
+// the prefix is left to the kernel that takes it for all requests
+// (qsa_prefix.cuh), and the request's unit is what lies behind it; else the
+// request is worked on by itself, from position 0. (No window in either case.)
+__device__ __forceinline__ bool sees_prefix(const DenseArgs& a, const int (&p)[kMaxNq]) {
+  bool all = true;
+#pragma unroll
+  for (int j = 0; j < kMaxNq; ++j) all &= !valid_pos(a, p[j]) || p[j] >= a.prefix_len - 1;
+  return all;
+}
 __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
   int p[kMaxNq];
 #pragma unroll
@@ -140,7 +151,8 @@ __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
     g.lo = min(g.lo, low_of(a, p[j]));
     g.hi = max(g.hi, p[j] + 1);
   }
-  return g.hi > 0 ? g : Range{0, 0};
+  if (a.prefix_len > 0 && sees_prefix(a, p)) g.lo = a.prefix_len;
+  return g.hi > g.lo ? g : Range{0, 0};
 }
 
 // quotient of non-negative numbers; most streams fit the 32-bit division

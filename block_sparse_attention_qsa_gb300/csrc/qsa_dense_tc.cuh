@@ -155,15 +155,6 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
   return v[0];
 }
 
-// Scores of two rows in the exp2 domain less the rows' references: x scale + nmu
-// (nmu = -mu), the product rounded, as it was for the maximum that mu was made
-// from. (One fused operation would leave the product's rounding error over, which
-// from scores of 2^26 on is more than E4M3 has room for, and later more than any
-// weight. `one` is 1, but the assembler does not know: a multiplication and an
-// addition of pairs it fuses, .rn or not.)
-__device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float2 nmu) {
-  return fma2(mul2(x, scale), one, nmu);
-}
 // What is added to lo of a position's weights before it is rounded to E4M3, whose
 // steps are of 2^-9 there: between -2^-10 and 2^-10 (exclusive: a weight of 0
 // stays 0), equidistributed over any run of positions (multiples of the golden
@@ -172,22 +163,6 @@ __device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float
 __device__ __forceinline__ float dither(int p) {
   return (float)(((int)((uint32_t)p * 0x9e3779b9u) >> 8) | 1) * 0x1p-33f;
 }
-__device__ __forceinline__ float2 pair(const float* v) { return make_float2(v[0], v[1]); }
-__device__ __forceinline__ float2 pair(const uint32_t* v) {
-  return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                   const __grid_constant__ CUtensorMap tm_v,
@@ -456,7 +431,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         if (row_off + t < rows) {
           const int i = rb * C::kRows + row_off + t, j = i / a.group, h = g * a.group + (i - j * a.group);
           const int p = a.q_pos[(size_t)u.r * a.n_q + j];
-          if (valid_pos(a, p)) rg = make_int2(low_of(a, p), p + 1);
+          if (valid_pos(a, p)) rg = make_int2(a.prefix_len > 0 ? u.g.lo : low_of(a, p), p + 1);
           o = (u.r * a.n_q + j) * a.n_q_heads + h;
         }
         s_rng[buf][row_off + t] = rg;
@@ -466,7 +441,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         int2 all = make_int2(0, 0x7fffffff);
         for (int j = rb * C::kRows / a.group; j <= (rb * C::kRows + rows - 1) / a.group; ++j) {
           const int p = a.q_pos[(size_t)u.r * a.n_q + j];
-          all.x = max(all.x, valid_pos(a, p) ? low_of(a, p) : 0);
+          all.x = max(all.x, !valid_pos(a, p) ? 0 : a.prefix_len > 0 ? u.g.lo : low_of(a, p));
           all.y = min(all.y, valid_pos(a, p) ? p + 1 : 0);
         }
         s_all[buf] = all;
@@ -761,7 +736,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       const int g = at.x / a.row_blocks;
       last = n == at.n;
       const int start = at.start(s_share);
-      const bool whole = start == 0 && at.t + at.n == at.tiles, done = whole && last, more = at.t > start;
+      const bool whole = start == 0 && at.t + at.n == at.tiles, more = at.t > start;
+      const bool done = whole && last && a.prefix_len == 0;  // (with a shared prefix a whole unit is a piece too)
       const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
       if (a.batch > kJoinScan && tid == 0 && start == 0 && last)
         a.unit_desc[(long long)at.r * units + at.x] =
@@ -774,7 +750,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       tc_after();
       if (lane < RC) s_red[wg][quarter][lane] = part;
       group_sync(1 + wg, 128);
-      float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
+      float* piece = whole && a.prefix_len > 0 ? a.whole + ((size_t)at.r * units + at.x) * C::kPieceFloats
+                                               : a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
       if (t < RC) {  // a row's sum, its factors, and lse
         float sum = (s_red[wg][0][t] + s_red[wg][1][t]) + (s_red[wg][2][t] + s_red[wg][3][t]);
         const float ref = s_mu[wg][t];
@@ -860,6 +837,7 @@ cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
   e = launch_k(dense_tc_kernel<C>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
+  if (a.prefix_len > 0) return cudaSuccess;  // (joined with the prefix's pieces)
   return launch_join<D, C::kRows, FP8, kTileTc>(a, s);
 }
 

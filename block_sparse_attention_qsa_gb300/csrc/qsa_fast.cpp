@@ -1,4 +1,5 @@
-// Python fast path of the operators round the paged cache (the module _fast).
+// Python fast path of the operators round the paged cache and of those for
+// serving a batch (the module _fast).
 //
 // A decode step calls these operators once a layer, next to kernels of a few
 // microseconds, and checking a dozen tensors' types, shapes and devices from
@@ -13,7 +14,7 @@
 
 #include <initializer_list>
 
-#include "qsa_kv.h"
+#include "qsa_serve.h"
 
 namespace {
 
@@ -21,6 +22,10 @@ decltype(&qsa_rope) p_rope;
 decltype(&qsa_kv_append) p_append;
 decltype(&qsa_kv_gather) p_gather;
 decltype(&qsa_paged_attn) p_attn;
+decltype(&qsa_prefix_attn) p_prefix;
+decltype(&qsa_kv_weight) p_weight;
+decltype(&qsa_kv_evict) p_evict;
+decltype(&qsa_verify_drafts) p_verify;
 PyObject* g_current_device;  // torch.cuda's current device and raw stream, as Python callables
 PyObject* g_raw_stream;
 
@@ -271,15 +276,138 @@ PyObject* fast_attn(PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(rope, kv_append, kv_gather, paged_attn, current_device, raw_stream): the
-// entry points' addresses and torch's two callables
+// prefix_attn(d, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, lse, ws, stream)
+PyObject* fast_prefix(PyObject* const* a, Py_ssize_t n) {
+  if (n != 13) Py_RETURN_NONE;
+  Where w;
+  if (!w.get(a[12])) Py_RETURN_NONE;
+  Struct<qsa_dims> d(a[0]);
+  const at::Tensor* xt = tensor(a[6], w.device, at::kInt);
+  if (!d.p || !xt || xt->dim() != 1 || xt->size(0) > INT32_MAX) Py_RETURN_NONE;
+  const int64_t B = d.p->batch, nq = d.p->n_q, H = d.p->n_q_heads, D = d.p->head_dim, pages = xt->size(0);
+  void* shared = dense(a[6], w.device, at::kInt, {pages});
+  void* q = dense(a[1], w.device, at::kBFloat16, {B, nq, H, D});
+  void* out = dense(a[9], w.device, at::kBFloat16, {B, nq, H, D});
+  void* pos = dense(a[8], w.device, at::kInt, {B, nq});
+  void* lse = a[10] == Py_None ? nullptr : dense(a[10], w.device, at::kFloat, {B, nq, H});
+  Cache c;
+  PyObject* const cache[5] = {a[2], a[3], a[4], a[5], a[7]};
+  const Workspace ws(a[11], w.device);
+  if (!shared || !q || !out || !pos || (a[10] != Py_None && !lse) || !c.get(*d.p, w.device, cache) || !ws.p)
+    Py_RETURN_NONE;
+  return call([&] {
+    return p_prefix(d.p, (int32_t)pages, i32(shared), q, c.k, c.v, c.ks, c.vs, i32(c.table), i32(pos), out,
+                    static_cast<float*>(lse), ws.p, ws.bytes, w.stream);
+  });
+}
+
+// kv_weight(d, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, stream)
+PyObject* fast_weight(PyObject* const* a, Py_ssize_t n) {
+  if (n != 11 || !PyFloat_Check(a[1])) Py_RETURN_NONE;
+  Where w;
+  if (!w.get(a[10])) Py_RETURN_NONE;
+  Struct<qsa_dims> d(a[0]);
+  if (!d.p) Py_RETURN_NONE;
+  const int64_t B = d.p->batch, nq = d.p->n_q, H = d.p->n_q_heads, D = d.p->head_dim, hk = d.p->n_kv_heads;
+  const bool fp8 = d.p->kv_dtype == QSA_KV_FP8_E4M3, scaled = fp8 || a[4] != Py_None;
+  void* q = dense(a[2], w.device, at::kBFloat16, {B, nq, H, D});
+  void* k = dense(a[3], w.device, fp8 ? at::kByte : at::kBFloat16, {d.p->num_pages, hk, d.p->page_size, D});
+  void* ks = scaled ? dense(a[4], w.device, at::kFloat, {hk}) : nullptr;
+  void* table = dense(a[5], w.device, at::kInt, {B, d.p->max_pages});
+  void* pos = dense(a[6], w.device, at::kInt, {B, nq});
+  void* lse = dense(a[7], w.device, at::kFloat, {B, nq, H});
+  void* weight = dense(a[8], w.device, at::kFloat, {B, (int64_t)d.p->max_pages * d.p->page_size});
+  const Workspace ws(a[9], w.device);
+  if (!q || !k || (scaled && !ks) || !table || !pos || !lse || !weight || !ws.p) Py_RETURN_NONE;
+  const float decay = (float)PyFloat_AS_DOUBLE(a[1]);
+  return call([&] {
+    return p_weight(d.p, decay, q, k, static_cast<float*>(ks), i32(table), i32(pos), static_cast<float*>(lse),
+                    static_cast<float*>(weight), ws.p, ws.bytes, w.stream);
+  });
+}
+
+// kv_evict(d, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length, ws, sinks,
+//          recent, stream)
+PyObject* fast_evict(PyObject* const* a, Py_ssize_t n) {
+  if (n != 14) Py_RETURN_NONE;
+  Where w;
+  if (!w.get(a[13])) Py_RETURN_NONE;
+  Struct<qsa_dims> d(a[0]);
+  const at::Tensor *po = tensor(a[4], w.device, at::kInt), *kt = tensor(a[8], w.device, at::kInt);
+  long sinks, recent;
+  if (!d.p || !po || po->dim() != 2 || !kt || kt->dim() != 2 || !small_int(a[11], sinks) || !small_int(a[12], recent))
+    Py_RETURN_NONE;
+  const int64_t B = d.p->batch, D = d.p->head_dim, hk = d.p->n_kv_heads, ps = d.p->page_size;
+  const int64_t pages = po->size(1), keep = kt->size(1);
+  if (pages > INT32_MAX || keep > INT32_MAX) Py_RETURN_NONE;
+  const at::ScalarType type = d.p->kv_dtype == QSA_KV_FP8_E4M3 ? at::kByte : at::kBFloat16;
+  void* k = dense(a[1], w.device, type, {d.p->num_pages, hk, ps, D});
+  void* v = dense(a[2], w.device, type, {d.p->num_pages, hk, ps, D});
+  void* table = dense(a[3], w.device, at::kInt, {B, d.p->max_pages});
+  void* table_out = dense(a[4], w.device, at::kInt, {B, pages});
+  void* len = dense(a[5], w.device, at::kInt, {B});
+  void* weight = dense(a[6], w.device, at::kFloat, {B, d.p->max_pages * ps});
+  void* weight_out = dense(a[7], w.device, at::kFloat, {B, pages * ps});
+  void* kept = dense(a[8], w.device, at::kInt, {B, keep});
+  void* new_len = dense(a[9], w.device, at::kInt, {B});
+  const Workspace ws(a[10], w.device);
+  if (!k || !v || !table || !table_out || !len || !weight || !weight_out || !kept || !new_len || !ws.p) Py_RETURN_NONE;
+  return call([&] {
+    return p_evict(d.p, (int32_t)keep, (int32_t)sinks, (int32_t)recent, (int32_t)pages, i32(len),
+                   static_cast<float*>(weight), i32(table), i32(table_out), k, v, static_cast<float*>(weight_out),
+                   static_cast<int32_t*>(kept), static_cast<int32_t*>(new_len), ws.p, ws.bytes, w.stream);
+  });
+}
+
+// Probabilities [batch][row][vocab] with a contiguous last dimension.
+struct Probs {
+  const void* p = nullptr;
+  qsa_prob_strides st;
+  Probs(const at::Tensor* t, int64_t B, int64_t rows, int64_t V) {
+    if (t && t->dim() == 3 && t->size(0) == B && t->size(1) == rows && t->size(2) == V &&
+        (V <= 1 || t->stride(2) == 1)) {
+      p = t->data_ptr();
+      st = {t->stride(0), t->stride(1)};
+    }
+  }
+};
+
+// verify_drafts(target, draft, tokens, uniform, accepted, out_tokens, ws, stream)
+PyObject* fast_verify(PyObject* const* a, Py_ssize_t n) {
+  if (n != 8 || !THPVariable_Check(a[0])) Py_RETURN_NONE;
+  Where w;
+  if (!w.get(a[7])) Py_RETURN_NONE;
+  const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16) Py_RETURN_NONE;
+  const at::Tensor* tt = tensor(a[0], w.device, type);
+  if (!tt || tt->dim() != 3) Py_RETURN_NONE;
+  const int64_t B = tt->size(0), nd = tt->size(1) - 1, V = tt->size(2);
+  if (B > INT32_MAX || nd > INT32_MAX || V > INT32_MAX) Py_RETURN_NONE;
+  const bool sampled = a[1] != Py_None;
+  const Probs t(tt, B, nd + 1, V), q(sampled ? tensor(a[1], w.device, type) : nullptr, B, nd, V);
+  void* tokens = dense(a[2], w.device, at::kInt, {B, nd});
+  void* u = dense(a[3], w.device, at::kFloat, {B, nd + 1});
+  void* accepted = dense(a[4], w.device, at::kInt, {B});
+  void* out = dense(a[5], w.device, at::kInt, {B, nd + 1});
+  const Workspace ws(a[6], w.device);
+  if (!t.p || (sampled && !q.p) || !tokens || !u || !accepted || !out || !ws.p) Py_RETURN_NONE;
+  return call([&] {
+    return p_verify((int32_t)B, (int32_t)nd, (int32_t)V, type == at::kFloat ? QSA_PROB_F32 : QSA_PROB_BF16, t.p, &t.st,
+                    q.p, &q.st, i32(tokens), static_cast<float*>(u), static_cast<int32_t*>(accepted),
+                    static_cast<int32_t*>(out), ws.p, ws.bytes, w.stream);
+  });
+}
+
+// bind(rope, kv_append, kv_gather, paged_attn, prefix_attn, kv_weight, kv_evict, verify_drafts, current_device,
+// raw_stream): the entry points' addresses and torch's two callables
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 6 arguments");
+  constexpr int kPoints = 8;
+  if (n != kPoints + 2) {
+    PyErr_SetString(PyExc_TypeError, "bind takes 10 arguments");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[kPoints];
+  for (int i = 0; i < kPoints; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
@@ -290,8 +418,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_append = reinterpret_cast<decltype(p_append)>(p[1]);
   p_gather = reinterpret_cast<decltype(p_gather)>(p[2]);
   p_attn = reinterpret_cast<decltype(p_attn)>(p[3]);
-  Py_XSETREF(g_current_device, Py_NewRef(a[4]));
-  Py_XSETREF(g_raw_stream, Py_NewRef(a[5]));
+  p_prefix = reinterpret_cast<decltype(p_prefix)>(p[4]);
+  p_weight = reinterpret_cast<decltype(p_weight)>(p[5]);
+  p_evict = reinterpret_cast<decltype(p_evict)>(p[6]);
+  p_verify = reinterpret_cast<decltype(p_verify)>(p[7]);
+  Py_XSETREF(g_current_device, Py_NewRef(a[kPoints]));
+  Py_XSETREF(g_raw_stream, Py_NewRef(a[kPoints + 1]));
   Py_RETURN_NONE;
 }
 
@@ -314,6 +446,10 @@ PyMethodDef kMethods[] = {QSA_METHOD("bind", bind),
                           QSA_METHOD("kv_append", guarded<fast_append>),
                           QSA_METHOD("kv_gather", guarded<fast_gather>),
                           QSA_METHOD("paged_attn", guarded<fast_attn>),
+                          QSA_METHOD("prefix_attn", guarded<fast_prefix>),
+                          QSA_METHOD("kv_weight", guarded<fast_weight>),
+                          QSA_METHOD("kv_evict", guarded<fast_evict>),
+                          QSA_METHOD("verify_drafts", guarded<fast_verify>),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -56,6 +56,7 @@ struct Prefix {
   const int32_t* table;
   int len;
 };
+size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms);  // bytes of workspace with a prefix
 // short_k: the failure-detection test (qsa_test_paged_attn_timeout)
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,

@@ -17,7 +17,7 @@ qsa_status qsa_prefix_workspace_size(const qsa_dims* dims, int32_t prefix_pages,
   const qsa_status st = check_kv_dims(dims);
   if (st != QSA_OK) return st;
   if (!bytes || prefix_pages < 0 || prefix_pages > dims->max_pages) return QSA_ERR_INVALID_ARG;
-  *bytes = dense_ws(*dims, device_sm_count()).total;
+  *bytes = prefix_ws(*dims, prefix_pages * dims->page_size, device_sm_count());
   return QSA_OK;
 }
 

@@ -40,6 +40,14 @@ __device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
   }
 }
+// kind::f16 with A in tensor memory: a row a lane, two values a column
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, "
+      "p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
 // true in one thread of the warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -116,6 +124,31 @@ struct Tmem<32> {
                  : "memory");
   }
 };
+
+// Scores of two rows in the exp2 domain less the rows' references: x scale + nmu
+// (nmu = -mu), the product rounded, as it was for the maximum that mu was made
+// from. (One fused operation would leave the product's rounding error over, which
+// from scores of 2^26 on is more than E4M3 has room for, and later more than any
+// weight. `one` is 1, but the assembler does not know: a multiplication and an
+// addition of pairs it fuses, .rn or not.)
+__device__ __forceinline__ float2 less(float2 x, float2 scale, float2 one, float2 nmu) {
+  return fma2(mul2(x, scale), one, nmu);
+}
+__device__ __forceinline__ float2 pair(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 pair(const uint32_t* v) {
+  return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 }  // namespace
 }  // namespace qsa

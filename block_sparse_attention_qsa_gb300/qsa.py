@@ -181,7 +181,7 @@ class _NoFast:
     def _none(*args):
         return None
 
-    rope = kv_append = kv_gather = paged_attn = _none
+    rope = kv_append = kv_gather = paged_attn = prefix_attn = kv_weight = kv_evict = verify_drafts = _none
 
 
 def _load_fast():
@@ -198,7 +198,8 @@ def _load_fast():
                       "longer on the host; __graft_entry__.build() makes it", RuntimeWarning)
         return _NoFast
     fast.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                for f in ("qsa_rope", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn")),
+                for f in ("qsa_rope", "qsa_kv_append", "qsa_kv_gather", "qsa_paged_attn", "qsa_prefix_attn",
+                          "qsa_kv_weight", "qsa_kv_evict", "qsa_verify_drafts")),
               getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
               getattr(torch._C, "_cuda_getCurrentRawStream", None))
     return fast
@@ -794,6 +795,11 @@ def prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, pa
     prefix_table.numel() * page_size of every request live in the pages that
     prefix_table (int32 [n], n may be 0) names, the others in those of the
     request's page_table row. ws is make_prefix_workspace's."""
+    st = _fast.prefix_attn(d, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, lse, ws, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_prefix_attn")
     dev = _current_device()
     B, n_q, H = d.batch, d.n_q, d.n_q_heads
     shape = (B, n_q, H, d.head_dim)
@@ -817,6 +823,11 @@ def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, 
     weight that each position gets from the newest tokens' query heads, given
     the lse that paged_attn or prefix_attn returned for them (fp32
     [B][n_q][H_q]). Positions that no query sees are left as they are."""
+    st = _fast.kv_weight(d, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_kv_weight")
     dev = _current_device()
     B, n_q, H = d.batch, d.n_q, d.n_q_heads
     fp8 = d.kv_dtype == KV_FP8_E4M3
@@ -842,6 +853,12 @@ def kv_evict(d: Dims, k_cache, v_cache, page_table, page_table_out, length, weig
     their number to new_length (int32 [B]; it may be length), their K and V to
     the pages of page_table_out (int32 [B][n]), their weights to weight_out
     (fp32 [B][n * page_size], 0 behind the last)."""
+    st = _fast.kv_evict(d, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length, ws,
+                        sinks, recent, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_kv_evict")
     dev = _current_device()
     B, ps = d.batch, d.page_size
     shape = (d.num_pages, d.n_kv_heads, ps, d.head_dim)
@@ -893,6 +910,11 @@ def verify_drafts(target, draft, tokens, uniform, accepted, out_tokens, ws, stre
     probabilities [B][n][V] they were sampled from, None if they were not
     sampled. Writes the number accepted (int32 [B]) and those tokens with the
     next one behind them, then -1 (int32 [B][n + 1]). ws: any workspace."""
+    st = _fast.verify_drafts(target, draft, tokens, uniform, accepted, out_tokens, ws, stream)
+    if st == OK:
+        return
+    if st is not None:
+        _check(st, "qsa_verify_drafts")
     dev = _current_device()
     if not isinstance(target, torch.Tensor) or target.dim() != 3 or target.dtype not in PROB_DTYPES:
         raise ValueError("target must be a float32 or bfloat16 tensor [B][n + 1][V]")

@@ -158,7 +158,8 @@ def test_prefix_all_padding_and_all_apart(qsa, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-@pytest.mark.parametrize("prefix,own,n_q", [(313, [1, 900], 4), (157, [33] * 40, 1), (641, [3, 5000, 1], 1), (40, [70] * 20, 4)])
+@pytest.mark.parametrize("prefix,own,n_q", [(313, [1, 900], 4), (157, [33] * 40, 1), (641, [3, 5000, 1], 1), (40, [70] * 20, 4),
+                                            (391, [5, 64, 300] * 3, 4), (782, [4] * 24, 1)])
 def test_prefix_long_and_wide(qsa, kv, prefix, own, n_q):
     _prefix_case(qsa, prefix, own, n_q, kv=kv)
 
