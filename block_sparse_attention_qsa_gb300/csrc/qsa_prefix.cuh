@@ -9,13 +9,22 @@
 //   S[row][position] = Q K^T     (both from shared memory, S in tensor memory)
 //   O[row][d]       += P V       (P in tensor memory, where S was)
 // One thread owns one row of S and O (a TMEM lane): maxima, references and sums
-// of a row's softmax need no other thread. The two row tiles take turns on the
-// tensor cores: while one's softmax runs, the other's products do.
+// of a row's softmax need no other thread. Each row tile has a warp that issues
+// its products, and the two take turns (P V, then the next S), so that one's
+// products run while the other's softmax does: left to themselves both fell
+// into step, softmax beside softmax and products behind products (a tile pair
+// of 128 positions took 3,650 cycles; in turns 2,830, where the tensor cores'
+// own time is 2,110), and one warp issuing for both lost as much, for what it
+// does next waits until its MMAs have left the queue. Products with 64
+// positions a step were slower (4,800): an MMA with Q from shared memory takes
+// 66 cycles with 64 columns as with 128.
 //
-// The reference of a row: weights are 2^(s - mu), where mu only has to keep the
-// largest weight between 1 and 2^8. It starts 6 below the row's first maximum
-// and moves when a score passes mu + 8, which after a row's first tiles hardly
-// happens; then O is rescaled in tensor memory by the row's thread.
+// The reference of a row: weights are 2^(s - mu), where mu only has to keep them
+// in range. It starts 6 below the row's first tile's maximum, so that no maximum
+// is needed before the exponentials of the tiles behind it; it moves when a
+// weight has passed kMost (O is then rescaled in tensor memory by the row's
+// thread before the next tile), and at once where there is no room left
+// (kLimit).
 //
 // An E4M3 cache is widened to FP16 on its way (exactly: a code has 4 significant
 // bits), by a warpgroup between the copies' buffers and the products'; with 256
@@ -63,7 +72,7 @@ template <int D_, bool FP8_, int NT_>
 struct Pc {
   static constexpr bool FP8 = FP8_;
   static constexpr int D = D_, NT = NT_;
-  static constexpr int T = D > 128 ? 64 : 128;  // positions of a tile (tensor memory: two S, NT O)
+  static constexpr int T = D > 128 ? 64 : 128;  // positions of a tile of K or V in shared memory
   static constexpr int kLines = D / 64;         // 128-byte lines of a row in 16 bits
   static constexpr int kSlot = T * D * 2;       // K or V of a tile
   static constexpr int kQ = 128 * D * 2;        // a row tile's Q
@@ -79,19 +88,40 @@ struct Pc {
   static constexpr int kSmem = (kUsed > kOut ? kUsed : kOut) + 1024;
   static constexpr int kSoft = NT * 128;        // softmax threads
   static constexpr int kWiden = FP8 ? 128 : 0;  // threads that widen
-  static constexpr int kThreads = kSoft + kWiden + 64;
+  static constexpr int kThreads = kSoft + kWiden + 128;
   static constexpr int kCopyWarp = (kSoft + kWiden) / 32, kMmaWarp = kCopyWarp + 1;
-  static constexpr uint32_t kO = 2 * T;
-  static constexpr uint32_t kNeed = 2 * T + NT * D;
+  // Registers: a softmax thread holds a row of S. A launch of 256, 384 or 512
+  // threads has 255, 168 or 128 a thread, of which the other warpgroups give
+  // some up; the sums stay the launch's.
+  static constexpr int kRegs = kThreads == 256 ? 255 : kThreads == 384 ? 168 : 128;
+  static constexpr int kSoftRegs = kThreads == 512 ? 184 : FP8 ? 232 : 216;
+  static constexpr int kOtherRegs = kThreads == 512 ? 72 : FP8 ? 136 : 72;
+  static constexpr bool kSplit = kThreads > 256;
+  static_assert(!kSplit || NT * kSoftRegs + (kThreads / 128 - NT) * kOtherRegs <= kThreads / 128 * kRegs, "registers");
+  static constexpr uint32_t kO = 2 * T;         // tensor memory: two S buffers (P where S was), then O
+  static constexpr uint32_t kNeed = kO + NT * D;
   static constexpr uint32_t kTmem = kNeed <= 256 ? 256 : 512;
+  // log2 of a weight that moves its row's reference before the next tile, and of
+  // one that there is no room for: FP16 ends at 2^16; with BF16 the sums keep
+  // room for V. (With 2^8, as in qsa_dense_tc.cuh, where the rows of a warp are
+  // fewer and their tiles more, half of the warps' tiles began with a move.)
+  static constexpr float kMost = FP8 ? 13.f : 20.f, kLimit = FP8 ? 15.f : 24.f;
   static constexpr int kPieceFloats = kPrefixRows * (D + 2);
   static_assert(kSlots >= 4 && kStages >= 1 && kNeed <= 512 && kSmem + kStatic <= kMaxSmem, "memory");
 };
 constexpr int kBadTiles = 16;      // page marks of the tiles in flight
-constexpr float kBelow = 6.f, kMost = 8.f;
+constexpr float kBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kNone = __builtin_huge_valf();  // the reference of a row that has seen nothing
 constexpr float kHuge = 16777216.f;  // from a reference of this size on, a product less it is not fused (see less())
 
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 template <bool FP8>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (FP8) {
@@ -115,7 +145,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   uint8_t* stage = s_q + NT * C::kQ;
   __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
   __shared__ __align__(8) uint64_t stage_full[C::kStages], stage_empty[C::kStages];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full, fin;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2], q_full, turn[2], fin[2];  // p_full: [half][buffer]
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_bad[kBadTiles];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
   __shared__ volatile int s_abort;
@@ -132,7 +162,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     s_abort = 0;
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(smem_u32(&slot_full[s]), FP8 ? 128 : 1);
-      mbar_init(smem_u32(&slot_empty[s]), 1);
+      mbar_init(smem_u32(&slot_empty[s]), NT);
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&stage_full[s]), 1);
@@ -140,11 +170,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&s_full[b]), 1);
-      mbar_init(smem_u32(&p_full[b]), 128);
+      mbar_init(smem_u32(&p_full[0][b]), 128);
+      mbar_init(smem_u32(&p_full[1][b]), 128);
+      mbar_init(smem_u32(&pv_half[b]), 1);
+      mbar_init(smem_u32(&turn[b]), 1);
+      mbar_init(smem_u32(&fin[b]), 1);
       mbar_init(smem_u32(&pv_done[b]), 1);
     }
     mbar_init(smem_u32(&q_full), C::kSoft);
-    mbar_init(smem_u32(&fin), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::kMmaWarp) {
@@ -163,119 +196,141 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   const uint32_t tmem = s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
-  if (warp == C::kCopyWarp) {
-    // ---- copies: K then V of each tile ----
-    Walk<T> at{};
-    at.t = t0;
-    at.n = n;
-    at.r = 0;
-    at.g = Range{0, a.prefix_len};
-    PageFeed<T> feed(a);
-    feed.start(a, at);
-    constexpr int kLine = FP8 ? C::kStageLine : 128, kCopyLines = FP8 ? C::kStageLines : kLines;
-    constexpr int kRing = FP8 ? C::kStages : C::kSlots, kBytes = FP8 ? C::kStage : C::kSlot;
-    uint8_t* base = FP8 ? stage : ring;
-    uint64_t* full = FP8 ? stage_full : slot_full;
-    uint64_t* empty = FP8 ? stage_empty : slot_empty;
-    const int line = lane / feed.boxes;  // this lane's line of a K or V tile; at most 32 copies
-    const uint32_t dst = (uint32_t)(line * (T * kLine) + (feed.my_box << feed.box_shift) * kLine);
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int page = feed.of_tile(a, at, i);
-      const uint32_t bad = feed.bad_groups(page);
+  if (tid >= C::kSoft + C::kWiden) {
+    if constexpr (C::kSplit) fewer_regs<C::kOtherRegs>();  // (a whole warpgroup, two warps of which have no work)
+    if (warp == C::kCopyWarp) {
+      // ---- copies: K then V of each tile ----
+      Walk<T> at{};
+      at.t = t0;
+      at.n = n;
+      at.r = 0;
+      at.g = Range{0, a.prefix_len};
+      PageFeed<T> feed(a);
+      feed.start(a, at);
+      constexpr int kLine = FP8 ? C::kStageLine : 128, kCopyLines = FP8 ? C::kStageLines : kLines;
+      constexpr int kRing = FP8 ? C::kStages : C::kSlots, kBytes = FP8 ? C::kStage : C::kSlot;
+      uint8_t* base = FP8 ? stage : ring;
+      uint64_t* full = FP8 ? stage_full : slot_full;
+      uint64_t* empty = FP8 ? stage_empty : slot_empty;
+      const int line = lane / feed.boxes;  // this lane's line of a K or V tile; at most 32 copies
+      const uint32_t dst = (uint32_t)(line * (T * kLine) + (feed.my_box << feed.box_shift) * kLine);
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int page = feed.of_tile(a, at, i);
+        const uint32_t bad = feed.bad_groups(page);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (!__all_sync(kFull, wait(&empty[slot], phase ^ 1u))) {
-          ok = false;
-          break;
+        for (int v = 0; v < 2; ++v) {
+          if (!__all_sync(kFull, wait(&empty[slot], phase ^ 1u))) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full[slot]);
+          if (lane == 0) {
+            if (v == 0) s_bad[i % kBadTiles] = bad;
+            mbar_expect_tx(bar, kBytes);
+          }
+          __syncwarp();
+          if (line < kCopyLines)
+            tma_load_4d(smem_u32(base + slot * kBytes) + dst, v ? &tm_v : &tm_k, line * (FP8 ? kLine : kLine / 2),
+                        feed.slot_of(a, i), g, page < 0 ? a.num_pages : page /* outside: zeros */, bar);
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
-        const uint32_t bar = smem_u32(&full[slot]);
-        if (lane == 0) {
-          if (v == 0) s_bad[i % kBadTiles] = bad;
-          mbar_expect_tx(bar, kBytes);
+      }
+      if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
+        for (int s = 0; s < kRing; ++s) {
+          const uint32_t par = s < slot ? phase : phase ^ 1u;
+          const long long start = clock64();
+          while (!mbar_try_wait(smem_u32(&full[s]), par) && clock64() - start < kWaitCycles / 64) {
+          }
+        }
+      }
+    } else if (warp < C::kMmaWarp + NT) {
+      // ---- both products of a row tile (a warp each; the whole warp walks the loop, one elected thread issues) ----
+      // With one row tile S of tile i + 1 is computed before P of tile i is there
+      // (two buffers); with two, the other row tile's products fill that time.
+      const bool one = elect_one();
+      constexpr uint32_t kTypes = FP8 ? 0u : kTypeBf16;
+      constexpr uint32_t kDescS = instr_desc(kTypes, false, false, T, 128);
+      constexpr uint32_t kDescO = instr_desc(kTypes, false, true, D, 128);
+      const int x = warp - C::kMmaWarp;
+      bool ok = wait(&q_full, 0);
+      auto slot_ready = [&](int q) { return wait(&slot_full[q % C::kSlots], (uint32_t)(q / C::kSlots) & 1u); };
+      auto buffer = [&](int i) { return NT == 2 ? x : i & 1; };
+      auto phase = [&](int i) { return (uint32_t)(NT == 2 ? i : i >> 1) & 1u; };
+      auto score = [&](int i) {
+        const int slot = 2 * i % C::kSlots, b = buffer(i);
+        ok = ok && slot_ready(2 * i);
+        // P of the step before in this buffer, which S overwrites, has been read
+        constexpr int kBack = NT == 2 ? 1 : 2;
+        if (i >= kBack) ok = ok && wait(&pv_done[b], phase(i - kBack));
+        ok = __all_sync(kFull, ok);
+        if (!ok) return;
+        tc_after();
+        // (passed on before S is issued: behind its MMAs the arrival would wait for them)
+        if (NT == 2 && i > 0 && one) mbar_arrive(smem_u32(&turn[x ^ 1]));
+        const uint64_t dq = smem_desc(smem_u32(s_q + x * C::kQ), 16, 1024, 2);
+        const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 1024, 2);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          // (addresses are in units of 16 bytes)
+          const uint32_t ln = (uint32_t)(ks / 4), in = (uint32_t)(ks % 4) * 2u;
+          if (one)
+            mma_tc<false>(tmem + (uint32_t)(b * T), dq + (ln * (128 * 128 / 16) + in), dk + (ln * (T * 128 / 16) + in),
+                          kDescS, ks > 0);
+        }
+        if (one) {
+          commit_tc(&s_full[b]);
+          commit_tc(&slot_empty[slot]);
         }
         __syncwarp();
-        if (line < kCopyLines)
-          tma_load_4d(smem_u32(base + slot * kBytes) + dst, v ? &tm_v : &tm_k, line * (FP8 ? kLine : kLine / 2),
-                      feed.slot_of(a, i), g, page < 0 ? a.num_pages : page /* outside: zeros */, bar);
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (s_abort) {  // copies in flight land before the CTA leaves (bounded)
-      for (int s = 0; s < kRing; ++s) {
-        const uint32_t par = s < slot ? phase : phase ^ 1u;
-        const long long start = clock64();
-        while (!mbar_try_wait(smem_u32(&full[s]), par) && clock64() - start < kWaitCycles / 64) {
-        }
-      }
-    }
-  } else if (warp == C::kMmaWarp) {
-    // ---- both products (the whole warp walks the loop, one elected thread issues) ----
-    // Step u is row tile u % NT of tile u / NT; S and P of it are in buffer u % 2.
-    const bool one = elect_one();
-    constexpr uint32_t kTypes = FP8 ? 0u : kTypeBf16;
-    constexpr uint32_t kDescS = instr_desc(kTypes, false, false, T, 128);
-    constexpr uint32_t kDescO = instr_desc(kTypes, false, true, D, 128);
-    const int steps = NT * n;
-    bool ok = __all_sync(kFull, wait(&q_full, 0));
-    auto slot_ready = [&](int q) { return wait(&slot_full[q % C::kSlots], (uint32_t)(q / C::kSlots) & 1u); };
-    auto score = [&](int u) {
-      const int x = u % NT, i = u / NT, q = 2 * i, slot = q % C::kSlots;
-      if (x == 0) ok = __all_sync(kFull, slot_ready(q));
-      // P of step u - 2, which S of this one overwrites, has been read
-      if (u >= 2) ok = __all_sync(kFull, ok && wait(&pv_done[u & 1], (uint32_t)((u - 2) >> 1) & 1u));
-      if (!ok) return;
-      tc_after();
-      const uint64_t dq = smem_desc(smem_u32(s_q + x * C::kQ), 16, 1024, 2);
-      const uint64_t dk = smem_desc(smem_u32(ring + slot * C::kSlot), 16, 1024, 2);
+      };
+      score(0);
+      if (NT == 1 && n > 1 && ok) score(1);
+      for (int i = 0; i < n && ok; ++i) {
+        const int q = 2 * i + 1, slot = q % C::kSlots, b = buffer(i);
+        // V: positions as k; its columns are lines of 64 (leading offset: a line)
+        const uint64_t dv = smem_desc(smem_u32(ring + slot * C::kSlot), kLines > 1 ? T * 128 : 0, 1024, 2);
+        ok = slot_ready(q);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        // (addresses are in units of 16 bytes)
-        const uint32_t ln = (uint32_t)(ks / 4), in = (uint32_t)(ks % 4) * 2u;
-        if (one)
-          mma_tc<false>(tmem + (uint32_t)((u & 1) * T), dq + (ln * (128 * 128 / 16) + in), dk + (ln * (T * 128 / 16) + in),
-                        kDescS, ks > 0);
+        for (int h = 0; h < 2; ++h) {  // half of the positions as soon as their weights are there
+          ok = __all_sync(kFull, ok && wait(&p_full[h][b], phase(i)));
+          // the row tiles take turns
+          if (NT == 2 && h == 0 && i + x > 0) ok = __all_sync(kFull, ok && wait(&turn[x], (uint32_t)(i - 1 + x) & 1u));
+          if (!ok) break;
+          tc_after();
+#pragma unroll
+          for (int ks = h * (T / 32); ks < (h + 1) * (T / 32); ++ks)
+            if (one)
+              mma_ts(tmem + C::kO + (uint32_t)(x * D), tmem + (uint32_t)(b * T + ks * 8), dv + (uint32_t)(ks * 128), kDescO,
+                     i > 0 || ks > 0);
+          if (one && h == 0) commit_tc(&pv_half[b]);
+        }
+        if (!ok) break;
+        if (one) {
+          commit_tc(&pv_done[b]);
+          commit_tc(&slot_empty[slot]);
+        }
+        __syncwarp();
+        if (i + (NT == 2 ? 1 : 2) < n)
+          score(i + (NT == 2 ? 1 : 2));
+        else if (NT == 2 && one)
+          mbar_arrive(smem_u32(&turn[x ^ 1]));
       }
-      if (one) {
-        commit_tc(&s_full[u & 1]);
-        if (x == NT - 1) commit_tc(&slot_empty[slot]);
+      // the tensor cores are done before the CTA gives its memory back
+      if (one) commit_tc(&fin[x]);
+      const long long start = clock64();
+      while (!mbar_try_wait(smem_u32(&fin[x]), 0) && clock64() - start < 2 * kWaitCycles) {
       }
       __syncwarp();
-    };
-    if (ok) score(0);
-    if (ok && steps > 1) score(1);
-    for (int u = 0; u < steps && ok; ++u) {
-      const int x = u % NT, i = u / NT, q = 2 * i + 1, slot = q % C::kSlots;
-      ok = __all_sync(kFull, wait(&p_full[u & 1], (uint32_t)(u >> 1) & 1u) && (x > 0 || slot_ready(q)));
-      if (!ok) break;
-      tc_after();
-      // V: positions as k; its columns are lines of 64 (leading offset: a line)
-      const uint64_t dv = smem_desc(smem_u32(ring + slot * C::kSlot), kLines > 1 ? T * 128 : 0, 1024, 2);
-#pragma unroll
-      for (int ks = 0; ks < T / 16; ++ks)
-        if (one)
-          mma_ts(tmem + C::kO + (uint32_t)(x * D), tmem + (uint32_t)((u & 1) * T + ks * 8), dv + (uint32_t)(ks * 128), kDescO,
-                 i > 0 || ks > 0);
-      if (one) {
-        commit_tc(&pv_done[u & 1]);
-        if (x == NT - 1) commit_tc(&slot_empty[slot]);
-      }
-      __syncwarp();
-      if (u + 2 < steps) score(u + 2);
     }
-    // the tensor cores are done before the CTA gives its memory back
-    if (one) commit_tc(&fin);
-    const long long start = clock64();
-    while (!mbar_try_wait(smem_u32(&fin), 0) && clock64() - start < 2 * kWaitCycles) {
-    }
-    __syncwarp();
   } else if (FP8 && tid >= C::kSoft) {
     // ---- E4M3 codes to FP16 tiles ----
+    if constexpr (C::kSplit) fewer_regs<C::kOtherRegs>();
     const int w = warp - C::kSoft / 32;
     // Eight lanes take the four 16-byte chunks of a line's half at rows r and
     // r + 4, and write the two chunks of each in opposite orders: no two in one
@@ -314,39 +369,56 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     }
   } else {
     // ---- softmax: a row a thread ----
+    if constexpr (C::kSplit) more_regs<C::kSoftRegs>();
     const int x = NT == 2 ? warp >> 2 : 0, t = tid & 127, rt = rt0 + x;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float base_scale = a.sm_scale * kLog2e * (FP8 ? fabsf(a.k_scale[g]) : 1.f);
     {
-      constexpr int kLanes = D / 8, kPass = 128 / kLanes;  // 8 components a lane
+      // 8 components a lane, kPass rows a pass; 16 passes' loads in flight
+      constexpr int kLanes = D / 8, kPass = 128 / kLanes, kPasses = 128 / kPass, kDeep = kPasses < 16 ? kPasses : 16;
       uint8_t* dst = s_q + x * C::kQ;
-#pragma unroll 4
-      for (int r = t / kLanes; r < 128; r += kPass) {
-        const int c = t % kLanes, row = rt * 128 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < pa.rows) {
-          const int rj = row / a.group, h = g * a.group + (row - rj * a.group);
-          v = ld16(a.q + ((size_t)rj * a.n_q_heads + h) * D + c * 8);
+      const int c = t % kLanes, step_j = kPass / a.group, step_h = kPass - step_j * a.group;
+      int row = rt * 128 + t / kLanes, rj = row / a.group, hg = row - rj * a.group;
+      const float sign = FP8 && a.k_scale[g] < 0.f ? -1.f : 1.f;
+#pragma unroll 1
+      for (int z0 = 0; z0 < kPasses; z0 += kDeep) {
+        uint4 w[kDeep];
+#pragma unroll
+        for (int z = 0; z < kDeep; ++z) {
+          w[z] = make_uint4(0, 0, 0, 0);
+          if (row < pa.rows) w[z] = ld16(a.q + ((size_t)rj * a.n_q_heads + g * a.group + hg) * D + c * 8);
+          row += kPass;
+          rj += step_j;
+          hg += step_h;
+          if (hg >= a.group) {
+            hg -= a.group;
+            ++rj;
+          }
         }
-        if constexpr (FP8) {
-          uint32_t big = 0;  // magnitudes of BF16 values order like their bit patterns
-          uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
+        for (int z = 0; z < kDeep; ++z) {
+          const int r = (z0 + z) * kPass + t / kLanes;
+          uint4 v = w[z];
+          if constexpr (FP8) {
+            uint32_t big = 0;  // magnitudes of BF16 values order like their bit patterns
+            uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
-          // 2^-sh brings the row's largest value into [2^14, 2^15)
-          const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
-          // (a row with an infinity or NaN: every component NaN, as its scores
-          // are; a negative scale of K goes into Q, so that a larger product is
-          // a larger score)
-          const float down = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a.k_scale[g] < 0.f ? -pow2(-sh) : pow2(-sh);
+            for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) wd[e] = pack16<true>(bf_lo(wd[e]) * down, bf_hi(wd[e]) * down);
-          v = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-          if (c == 0) s_scale[x * 128 + r] = base_scale * pow2(sh);
+            for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+            // 2^-sh brings the row's largest value into [2^14, 2^15)
+            const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
+            // (a row with an infinity or NaN: every component NaN, as its scores
+            // are; a negative scale of K goes into Q, so that a larger product is
+            // a larger score)
+            const float down = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : sign * pow2(-sh);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wd[e] = pack16<true>(bf_lo(wd[e]) * down, bf_hi(wd[e]) * down);
+            v = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+            if (c == 0) s_scale[x * 128 + r] = base_scale * pow2(sh);
+          }
+          *reinterpret_cast<uint4*>(dst + c / 8 * (128 * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
         }
-        *reinterpret_cast<uint4*>(dst + c / 8 * (128 * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
       }
       async_fence();
       mbar_arrive(smem_u32(&q_full));
@@ -354,121 +426,142 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     if constexpr (FP8) {  // (a row's scale is written by another thread of its warpgroup)
       asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
     }
-    const float sc = FP8 ? s_scale[x * 128 + t] : base_scale;
-    float mu = kNone;
+    float sc = FP8 ? s_scale[x * 128 + t] : base_scale;
+    if (FP8 && sc == 0.f) sc = 0x1p-126f;  // (every score is about 0; a product with an absent position's -inf is no NaN)
+    float mu = kNone, pending = 0.f;  // pending: how far the tile before went past the reference
     float2 l = make_float2(0.f, 0.f);
+    const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(x * D);
+    // The reference moves to `to`: the sum and, where it holds anything, O follow.
+    // `bar` is the products of P so far.
+    auto move_to = [&](float to, bool any, uint64_t* bar, uint32_t parity) {
+      const float f = mu == kNone ? 1.f : exp2_sfu(mu - to);
+      mu = to;
+      l = mul2(l, both(f));
+      if (!any) return;
+      wait(bar, parity);
+      __syncwarp();
+      tc_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        uint32_t o[16];
+        Tmem<16>::load(o_addr + c0, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        Tmem<16>::store(o_addr + c0, o);
+      }
+      tc_wait_st();
+    };
     for (int i = 0; i < n; ++i) {
-      const int u = NT * i + x, b = u & 1;
-      wait(&s_full[b], (uint32_t)(u >> 1) & 1u);  // (given up: on without meaning, to the end)
+      const int b = NT == 2 ? x : i & 1;
+      const uint32_t phase = (uint32_t)(NT == 2 ? i : i >> 1) & 1u;
+      // the products of the tile before: its buffer, its phase
+      uint64_t* before = &pv_done[NT == 2 ? x : (i - 1) & 1];
+      const uint32_t before_phase = (uint32_t)(NT == 2 ? i - 1 : (i - 1) >> 1) & 1u;
+      wait(&s_full[b], phase);  // (given up: on without meaning, to the end)
       __syncwarp();
       tc_after();
       const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&s_bad[i % kBadTiles]);
       const uint32_t addr = tmem + lane_base + (uint32_t)(b * T);
-      // The largest product first, half of the columns at a time; the first
-      // half's stay in registers.
-      uint32_t v[64];
-      float top = kNegInf;
-      auto load64 = [&](int c0) {
-        uint32_t h[32];
-        Tmem<32>::load(addr + c0, h);
+      // 32 columns at a time, the next ones on their way
+      constexpr int kParts = T / 32;
+      uint32_t v[2][32];
+      Tmem<32>::load(addr, v[0]);
+      if (i == 0) {  // the first maximum
+        float top = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = h[e];
-        Tmem<32>::load(addr + c0 + 32, h);
+        for (int k = 0; k < kParts; ++k) {
+          tc_wait_ld(v[k & 1]);
+          Tmem<32>::load(addr + (uint32_t)((k + 1) % kParts * 32), v[(k + 1) & 1]);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[32 + e] = h[e];
-        tc_wait_ld();
-      };
-      if (bad == 0) {
-#pragma unroll
-        for (int c0 = T - 64; c0 >= 0; c0 -= 64) {
-          load64(c0);
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) top = max3(top, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          for (int e = 0; e < 32; ++e)
+            if (!((bad >> (2 * k + (e >> 4))) & 1u)) top = fmaxf(top, __uint_as_float(v[k & 1][e]));
         }
-      } else {
-#pragma unroll 1
-        for (int c0 = 0; c0 < T; c0 += 16) {
-          if ((bad >> (c0 >> 4)) & 1u) continue;
-          uint32_t h[16];
-          Tmem<16>::load(addr + c0, h);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(h[e]));
-        }
+        top *= sc;
+        if (top > kNegInf && top < kNone) mu = top - kBelow;
+      } else if (__any_sync(kFull, pending > C::kMost)) {
+        move_to(pending > C::kMost ? mu + (pending - kBelow) : mu, true, before, before_phase);
       }
-      top *= sc;
-      const bool none = mu == kNone;
-      const float up = none ? (top > kNegInf ? kMost + 1.f : 0.f) : top - mu;
-      if (__any_sync(kFull, up > kMost)) {
-        float f = 1.f;
-        if (up > kMost) {
-          const float to = top == kNone ? 0.f : top - kBelow;  // (an infinite score: its row is NaN)
-          if (!none) f = exp2_sfu(mu - to);
-          mu = to;
-        }
-        l = mul2(l, both(f));
-        if (i > 0) {  // what O holds so far
-          const int before = u - NT;
-          wait(&pv_done[before & 1], (uint32_t)(before >> 1) & 1u);
-          __syncwarp();
-          tc_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            Tmem<16>::load(tmem + lane_base + C::kO + (uint32_t)(x * D + c0), o);
-            tc_wait_ld();
+      pending = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            Tmem<16>::store(tmem + lane_base + C::kO + (uint32_t)(x * D + c0), o);
-          }
-          tc_wait_st();
-        }
-      }
-      const float nmu = mu == kNone ? 0.f : -mu;
-      if (bad == 0 && !__any_sync(kFull, fabsf(nmu) >= kHuge)) {
+      for (int h = 0; h < 2; ++h) {
+        const float nmu = mu == kNone ? 0.f : -mu;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float tops[2] = {kNegInf, kNegInf};
+        uint32_t p[T / 4];
 #pragma unroll
-        for (int c0 = 0; c0 < T; c0 += 64) {
-          if (c0 > 0) load64(c0);
-          uint32_t p[32];
+        for (int k = h * (kParts / 2); k < (h + 1) * (kParts / 2); ++k) {
+          uint32_t(&w)[32] = v[k & 1];
+          tc_wait_ld(w);
+          if (k + 1 < kParts) Tmem<32>::load(addr + (uint32_t)((k + 1) * 32), v[(k + 1) & 1]);
+          if (((bad >> (2 * k)) & 3u) != 0) {  // positions without a page
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float2 y = fma2(pair(v + e), both(sc), both(nmu));
+            for (int e = 0; e < 32; ++e)
+              if ((bad >> (2 * k + (e >> 4))) & 1u) w[e] = __float_as_uint(kNegInf);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 y = fma2(pair(w + e), both(sc), both(nmu));
+            tops[(e >> 1) & 1] = max3(tops[(e >> 1) & 1], y.x, y.y);
             y = make_float2(exp2_sfu(y.x), exp2_sfu(y.y));
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
-            p[e / 2] = pack16<FP8>(y.x, y.y);
+            p[(k - h * (kParts / 2)) * 16 + e / 2] = pack16<FP8>(y.x, y.y);
           }
-          Tmem<32>::store(addr + (uint32_t)(c0 / 2), p);
         }
-        l = add2(l, add2(sum[0], sum[1]));
-      } else {
-        // positions without a page, or references so large that a fused product's rounding would show
+        const float top = fmaxf(tops[0], tops[1]);
+        if (!__any_sync(kFull, top > C::kLimit || mu == kNone || fabsf(mu) >= kHuge)) {
+          pending = fmaxf(pending, top);
+          l = add2(l, add2(sum[0], sum[1]));
+          Tmem<T / 4>::store(addr + (uint32_t)(h * (T / 4)), p);
+        } else {
+          // A weight with no room left, a row that has seen nothing yet, or a
+          // reference so large that a fused product's rounding would show: again
+          // from tensor memory, maximum first, and with the product rounded.
+          float big = kNegInf;
 #pragma unroll 1
-        for (int c0 = 0; c0 < T; c0 += 16) {
-          uint32_t h[16], p[8];
-          Tmem<16>::load(addr + c0, h);
-          tc_wait_ld();
-          const bool gone = (bad >> (c0 >> 4)) & 1u;
+          for (int c0 = h * (T / 2); c0 < (h + 1) * (T / 2); c0 += 16) {
+            uint32_t s16[16];
+            Tmem<16>::load(addr + c0, s16);
+            tc_wait_ld();
+            if ((bad >> (c0 >> 4)) & 1u) continue;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 y = less(pair(h + e), both(sc), both(a.one), both(nmu));
-            y = gone ? make_float2(0.f, 0.f) : make_float2(exp2_sfu(y.x), exp2_sfu(y.y));
-            l = add2(l, y);
-            p[e / 2] = pack16<FP8>(y.x, y.y);
+            for (int e = 0; e < 16; ++e) big = fmaxf(big, __uint_as_float(s16[e]));
           }
-          Tmem<8>::store(addr + (uint32_t)(c0 / 2), p);
-          tc_wait_st();
+          big *= sc;
+          const bool up = mu == kNone ? big > kNegInf : big - mu > C::kMost;
+          const float to = !up ? mu : big == kNone ? 0.f : big - kBelow;  // (an infinite score: its row is NaN)
+          if (h == 0)
+            move_to(to, i > 0, before, before_phase);
+          else
+            move_to(to, true, &pv_half[b], phase);
+          const float less_mu = mu == kNone ? 0.f : -mu;
+#pragma unroll 1
+          for (int c0 = h * (T / 2); c0 < (h + 1) * (T / 2); c0 += 16) {
+            uint32_t s16[16], q[8];
+            Tmem<16>::load(addr + c0, s16);
+            tc_wait_ld();
+            const bool gone = (bad >> (c0 >> 4)) & 1u;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float2 y = less(pair(s16 + e), both(sc), both(a.one), both(less_mu));
+              y = gone ? make_float2(0.f, 0.f) : make_float2(exp2_sfu(y.x), exp2_sfu(y.y));
+              l = add2(l, y);
+              q[e / 2] = pack16<FP8>(y.x, y.y);
+            }
+            Tmem<8>::store(addr + (uint32_t)(c0 / 2), q);
+            tc_wait_st();
+          }
         }
+        tc_wait_st();
+        tc_before();
+        mbar_arrive(smem_u32(&p_full[h][b]));
       }
-      tc_wait_st();
-      tc_before();
-      mbar_arrive(smem_u32(&p_full[b]));
     }
 
     // ---- the piece: through shared memory, which nothing uses any more, so that rows leave whole ----
-    // (not pv_done of the last step: the other row tile's phases are not followed
-    // here, and a parity does not tell the last but one from the one before it)
-    wait(&fin, 0);
+    // (the other row tile's products may still read it: both warps' ends)
+#pragma unroll
+    for (int z = 0; z < NT; ++z) wait(&fin[z], 0);
     __syncwarp();
     tc_after();
     const float sum = l.x + l.y;
@@ -491,9 +584,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     }
     constexpr int kVecs = D / 4;  // of a row
     float* dst = piece + 256 + (size_t)((warp & 3) * 32) * D;
-    for (int z = lane; z < live * kVecs; z += 32) {
+#pragma unroll 8
+    for (int z = lane; z < 32 * kVecs; z += 32) {
       const int r = z / kVecs, c = z % kVecs;
-      *reinterpret_cast<uint4*>(dst + r * D + c * 4) = *reinterpret_cast<const uint4*>(out + r * C::kOutPitch + c * 4);
+      if (r < live)
+        *reinterpret_cast<uint4*>(dst + r * D + c * 4) = *reinterpret_cast<const uint4*>(out + r * C::kOutPitch + c * 4);
     }
   }
   tc_before();
@@ -650,9 +745,16 @@ cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k,
   constexpr int kLine = FP8 ? C::kStageLine : 128;
   if (!make_cache_map(&tk, d, k, C::T, kLine, false) || !make_cache_map(&tv, d, v, C::T, kLine, false))
     return cudaErrorInvalidValue;
-  static DeviceSlots slots;
+  static DeviceSlots slots, regs;
   cudaError_t e = slots.raise_smem(prefix_kernel<C>, C::kSmem);
   if (e != cudaSuccess) return e;
+  if (C::kSplit) {  // the warpgroups' shares are of what the launch has
+    const int n = regs.get([] {
+      cudaFuncAttributes at;
+      return cudaFuncGetAttributes(&at, prefix_kernel<C>) == cudaSuccess ? at.numRegs : 0;
+    });
+    if (n != C::kRegs) return cudaErrorInvalidKernelImage;
+  }
   e = launch_k(prefix_kernel<C>, dim3((unsigned)a.units * a.splits), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
   // 4 warps a row where rows are few; with a warp a row their loads fill the GPU
