@@ -18,6 +18,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
+constexpr unsigned kHeld = 16384;  // weights of a slice that are held in shared memory
 
 __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x) {
   const int lane = threadIdx.x & 31;
@@ -27,6 +28,9 @@ __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x) {
     if (lane >= o) x += y;
   }
   return x;
+}
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void st_peer_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -50,7 +54,8 @@ __device__ __forceinline__ uint64_t block_exclusive(uint64_t x, uint64_t (&scan)
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t s_hist[kBins];
+  extern __shared__ float s_w[];  // the first kHeld weights of the slice
+  __shared__ uint32_t s_hist[kBins], s_sum[kBins];  // this CTA's counts, the cluster's
   __shared__ uint64_t s_scan[kSelWarps], s_slice[kMaxCluster];
   __shared__ uint32_t s_bin, s_left;
   const int tid = threadIdx.x;
@@ -85,26 +90,51 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   // positions lo .. hi - 1 are chosen from, `need` of them
   const unsigned lo = (unsigned)a.sinks, hi = n - (unsigned)a.recent;
   const unsigned slice = (n + ctas - 1) / ctas, s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
-  uint32_t need = (uint32_t)(a.keep - a.sinks - a.recent), prefix = 0, mask = 0;
+  const unsigned held = min(s1 - s0, a.held);
+  for (unsigned i = tid; i < held; i += kSelThreads) s_w[i] = w[s0 + i];
+  auto key_at = [&](unsigned t) { return order_key(t - s0 < held ? s_w[t - s0] : w[t]); };
+  uint32_t need = keep - a.sinks - a.recent, prefix = 0, mask = 0;
   if (need > 0) {
+    const unsigned c0 = max(s0, lo), c1 = max(c0, min(s1, hi));  // the slice's part of them
+    const int own_bins = kBins / ctas;
 #pragma unroll 1
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;  // (the last digit has a bit of the second's)
       for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
       __syncthreads();
-      for (unsigned t = max(s0, lo) + tid; t < min(s1, hi); t += kSelThreads) {
-        const uint32_t k = order_key(w[t]);
-        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & (kBins - 1)], 1u);
+      for (unsigned t = c0 + tid; t - tid < c1; t += kSelThreads) {
+        const uint32_t k = t < c1 ? key_at(t) : 0;
+        const bool in = t < c1 && (k & mask) == prefix;
+        const uint32_t bin = (k >> shift) & (kBins - 1);
+        // the lanes with the first such lane's digit count as one (many equal weights are usual)
+        const uint32_t any = __ballot_sync(kFull, in);
+        if (any == 0) continue;
+        const int first_lane = __ffs(any) - 1;
+        const uint32_t their = __shfl_sync(kFull, bin, first_lane);  // (every lane takes part)
+        const uint32_t same = __ballot_sync(kFull, in && bin == their);
+        if ((tid & 31) == first_lane)
+          atomicAdd(&s_hist[bin], (uint32_t)__popc(same));
+        else if (in && !((same >> (tid & 31)) & 1u))
+          atomicAdd(&s_hist[bin], 1u);
+      }
+      // each CTA adds up a part of the bins for all of them
+      cluster_sync();
+      for (int i = tid; i < own_bins; i += kSelThreads) {
+        const int bin = rank * own_bins + i;
+        uint32_t c = 0;
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p) c += p < ctas ? ld_peer(peer_addr(&s_hist[bin], p)) : 0;
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p)
+          if (p < ctas) st_peer_u32(peer_addr(&s_sum[bin], p), c);
       }
       cluster_sync();
-      // every CTA adds up all counts, from the largest digit down (4 a thread)
+      // the digit of the last one that stays, from the largest down (4 a thread)
       uint32_t c[4];
       uint64_t mine = 0, all;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int bin = kBins - 1 - (tid * 4 + i);
-        c[i] = 0;
-        for (int p = 0; p < ctas; ++p) c[i] += ld_peer(peer_addr(&s_hist[bin], p));
+        c[i] = s_sum[kBins - 1 - (tid * 4 + i)];
         mine += c[i];
       }
       const uint64_t before = block_exclusive(mine, s_scan, &all);
@@ -115,11 +145,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         s_bin = (uint32_t)(kBins - 1 - (tid * 4 + i));
         s_left = need - b;
       }
-      cluster_sync();  // (and the counts have been read by every CTA)
+      __syncthreads();
       prefix |= s_bin << shift;
       mask |= (uint32_t)(kBins - 1) << shift;
       need = s_left;
     }
+  } else {
+    __syncthreads();
   }
   // Those above the last one's key stay, and the first `need` that equal it.
   const uint32_t last = need > 0 ? prefix : 0xffffffffu;  // (no weight has that key)
@@ -128,7 +160,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   uint64_t count = 0;  // those that equal it << 32 | those that stay anyway
   for (unsigned t = t0; t < t1; ++t) {
     const bool sure = t < lo || t >= hi;
-    const uint32_t k = order_key(w[t]);
+    const uint32_t k = key_at(t);
     count += sure || k > last ? 1ull : k == last ? 1ull << 32 : 0ull;
   }
   uint64_t all;
@@ -139,7 +171,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   uint32_t ties = (uint32_t)(before >> 32), at = (uint32_t)before + min(ties, need);
   for (unsigned t = t0; t < t1; ++t) {
     const bool sure = t < lo || t >= hi;
-    const float x = w[t];
+    const float x = t - s0 < held ? s_w[t - s0] : w[t];
     const uint32_t k = order_key(x);
     bool stays = sure || k > last;
     if (!stays && k == last) stays = ties++ < need;
@@ -205,12 +237,16 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictArgs a) {
 
 }  // namespace
 
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
+cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s) {
   // CTAs of a request: enough that few requests use the whole GPU, each with 2,048 positions or more
   const int cap = a.max_pages * a.page_size;
   unsigned c = 1;
   while (c < kMaxCluster && (long long)a.batch * c < 2LL * device_sm_count() && cap / (2 * (int)c) >= 2048) c *= 2;
-  cudaError_t e = launch_clusters(evict_select_kernel, dim3((unsigned)a.batch * c), dim3(kSelThreads), c, s, a);
+  a.held = std::min(kHeld, ((unsigned)cap + c - 1) / c);
+  static DeviceSlots slots;
+  cudaError_t e = slots.raise_smem(evict_select_kernel, kHeld * sizeof(float));
+  if (e != cudaSuccess) return e;
+  e = launch_clusters(evict_select_kernel, dim3((unsigned)a.batch * c), dim3(kSelThreads), c, a.held * sizeof(float), s, a);
   if (e != cudaSuccess) return e;
   const int vecs = a.row_bytes / 16, items = 2 * a.hk * vecs;
   const long long gx = (long long)a.batch * ((a.keep + kCopyTok - 1LL) / kCopyTok);  // (below 2^31: qsa_kv_evict)

@@ -26,8 +26,9 @@ struct EvictArgs {
   int32_t* err;
   int batch, keep, sinks, recent, out_pages;
   int hk, row_bytes, page_size, max_pages, num_pages;
+  unsigned held;  // weights of a CTA's slice in shared memory (set by the launcher)
 };
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s);
 
 struct VerifyArgs {
   const void* target;
@@ -44,11 +45,12 @@ cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s);
 
 // launch_k with thread-block clusters of `cluster` CTAs (along x)
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, cudaStream_t s,
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem, cudaStream_t s,
                             Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

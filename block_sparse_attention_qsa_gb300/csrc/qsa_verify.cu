@@ -11,10 +11,13 @@
 // the CTA in whose slice u S falls reads the one segment again that holds it.
 // So the row (or two) that is sampled from is read from HBM once.
 //
-// Weights are summed as integers, multiples of 2^-60: p and q are FP32 values
-// of at most 1, so a multiple of 2^-60 is cut off 10^-18 at most, and integer
-// sums do not depend on how the row is split: the threshold floor(u S) falls
-// between the same two tokens in any order, and both passes agree.
+// The sums are exact, so that they do not depend on how the row is split: the
+// threshold floor(u S) falls between the same two tokens in any order, and both
+// readings of a segment agree. A weight is p, or p - q where p > q, each rounded
+// to a multiple of 2^-54. As 64-bit integers these cost the integer pipe 36
+// cycles a value and warp, and 256 rows of 150,001 tokens (FP32, sampled drafts)
+// 81 us; the conversion instruction to 64 bits was slower still, 158. So they
+// are added in FP32 without rounding (see Exact), which takes 11 additions.
 #include "qsa_serve_internal.cuh"
 
 namespace qsa {
@@ -23,19 +26,47 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kDeep = 8;  // values a thread has on their way, of each row
 
 __device__ __forceinline__ float load(const float* p) { return *p; }
 __device__ __forceinline__ float load(const __nv_bfloat16* p) {
   return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
-// a probability in 2^-60ths, cut off; negative and NaN 0, above 1 as 1
-__device__ __forceinline__ uint64_t fixed60(float x) {
-  const float p = fminf(fmaxf(x, 0.f), 1.f);  // (a NaN becomes 0)
-  const uint32_t b = __float_as_uint(p), e = b >> 23;
-  const uint64_t m = (uint64_t)((b & 0x7fffffu) | (e ? 0x800000u : 0u)) << 37;  // p = m 2^(e - 127 - 60)
-  return m >> min(127u - e, 63u);
-}
+// A probability in 2^-54ths; negative and NaN 0, above 1 as 1.
+__device__ __forceinline__ int64_t fixed54(float x) { return __float2ll_rn(__saturatef(x) * 0x1p54f); }
+
+// Exact sums of values of at most 1 in magnitude, each rounded to a multiple of
+// 2^-54. A value is taken apart on three fixed grids: x + M, with M 1.5 2^23 times
+// the grid, is rounded to the grid, and what is left is exact again. The parts
+// on the grid of 2^-20 add up without rounding to below 2^4, those on 2^-37 (at
+// most 2^-21 each) to 2^-13, those on 2^-54 (at most 2^-38) to 2^-30, that is
+// for kMost values. The last part's rounding is to nearest, ties to even, and so
+// is the whole value's.
+struct Exact {
+  static constexpr int kMost = 256;
+  static constexpr float kM1 = 1.5f * 0x1p3f, kM2 = 1.5f * 0x1p-14f, kM3 = 1.5f * 0x1p-31f;
+  float2 a1, a2, a3;  // less the sums
+  __device__ __forceinline__ Exact() : a1(make_float2(0.f, 0.f)), a2(a1), a3(a1) {}
+  static __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+  // M - (x + M): less x's part on the grid
+  static __device__ __forceinline__ float2 part(float2 x, float m) { return fma2(add2(x, pair(m)), pair(-1.f), pair(m)); }
+  __device__ __forceinline__ void add(float2 x) {
+    const float2 t1 = part(x, kM1);
+    a1 = add2(a1, t1);
+    x = add2(x, t1);
+    const float2 t2 = part(x, kM2);
+    a2 = add2(a2, t2);
+    x = add2(x, t2);
+    a3 = add2(a3, part(x, kM3));
+  }
+  __device__ __forceinline__ int64_t sum() const {  // in 2^-54ths
+    const int i1 = __float2int_rn(a1.x * 0x1p20f) + __float2int_rn(a1.y * 0x1p20f);
+    const int i2 = __float2int_rn(a2.x * 0x1p37f) + __float2int_rn(a2.y * 0x1p37f);
+    const int i3 = __float2int_rn(a3.x * 0x1p54f) + __float2int_rn(a3.y * 0x1p54f);
+    return -((int64_t)i1 * (1LL << 34) + (int64_t)i2 * (1LL << 17) + i3);
+  }
+};
 __device__ __forceinline__ float as_uniform(float u) { return fminf(fmaxf(u, 0.f), 0x1.fffffep-1f); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -63,23 +94,97 @@ struct Weights {
   const T* q;  // null: none
   int token;   // -1: none
   __device__ __forceinline__ uint64_t at(int v) const {
-    const uint64_t x = fixed60(load(p + v));
+    const float x = load(p + v);
     if (q) {
-      const uint64_t y = fixed60(load(q + v));
-      return x > y ? x - y : 0;
+      const float y = load(q + v);
+      return __saturatef(x) > __saturatef(y) ? (uint64_t)(fixed54(x) - fixed54(y)) : 0;
     }
-    return v == token ? 0 : x;
+    return v == token ? 0 : (uint64_t)fixed54(x);
   }
-  // sum over first + lane, first + lane + 32, ... below end
+  // two weights into a sum
+  static __device__ __forceinline__ void add_less(Exact& s, float p0, float q0, float p1, float q1) {
+    p0 = __saturatef(p0), q0 = __saturatef(q0), p1 = __saturatef(p1), q1 = __saturatef(q1);
+    const bool m0 = p0 > q0, m1 = p1 > q1;
+    s.add(make_float2(m0 ? p0 : 0.f, m1 ? p1 : 0.f));
+    s.add(make_float2(m0 ? -q0 : 0.f, m1 ? -q1 : 0.f));
+  }
+  // sum over a lane's share of first .. end - 1, kDeep loads of a row in flight
   __device__ __forceinline__ uint64_t sum(int first, int end) const {
-    uint64_t s = 0;
-    for (int v = first + (int)(threadIdx.x & 31); v < end; v += 32) s += at(v);
-    return s;
+    const int lane = threadIdx.x & 31;
+    int64_t all = 0;
+    int v = first + lane;
+    while (v + 32 * (kDeep - 1) < end) {
+      Exact s;
+      for (int z = 0; z < Exact::kMost / 2 / kDeep && v + 32 * (kDeep - 1) < end; ++z, v += 32 * kDeep) {
+        float x[kDeep], y[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) x[i] = load(p + v + 32 * i);
+        if (q) {
+#pragma unroll
+          for (int i = 0; i < kDeep; ++i) y[i] = load(q + v + 32 * i);
+#pragma unroll
+          for (int i = 0; i < kDeep; i += 2) add_less(s, x[i], y[i], x[i + 1], y[i + 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kDeep; ++i) x[i] = v + 32 * i == token ? 0.f : __saturatef(x[i]);
+#pragma unroll
+          for (int i = 0; i < kDeep; i += 2) s.add(make_float2(x[i], x[i + 1]));
+        }
+      }
+      all += s.sum();
+    }
+    for (; v < end; v += 32) all += (int64_t)at(v);
+    return (uint64_t)all;
+  }
+  // the same where both rows and `first` are at 16-byte boundaries
+  __device__ __forceinline__ uint64_t sum_vec(int first, int end) const {
+    constexpr int kVec = 16 / sizeof(T), kStep = 32 * kVec, kLoads = kDeep / 4;
+    int64_t all = 0;
+    int v = first + (int)(threadIdx.x & 31) * kVec;
+    while (v + kStep * (kLoads - 1) + kVec <= end) {
+      Exact s;
+      for (int z = 0; z < Exact::kMost / 2 / (kVec * kLoads) && v + kStep * (kLoads - 1) + kVec <= end;
+           ++z, v += kStep * kLoads) {
+        uint4 x[kLoads], y[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) x[i] = ld16(p + v + kStep * i);
+        if (q) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) y[i] = ld16(q + v + kStep * i);
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2)
+              add_less(s, value(x[i], e), value(y[i], e), value(x[i], e + 1), value(y[i], e + 1));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+              const int at0 = v + kStep * i + e;
+              s.add(make_float2(at0 == token ? 0.f : __saturatef(value(x[i], e)),
+                                at0 + 1 == token ? 0.f : __saturatef(value(x[i], e + 1))));
+            }
+        }
+      }
+      all += s.sum();
+    }
+    for (; v < end; v += kStep)
+      for (int e = 0; e < kVec && v + e < end; ++e) all += (int64_t)at(v + e);
+    return (uint64_t)all;
+  }
+  static __device__ __forceinline__ float value(const uint4& x, int e) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[e]);
+    else
+      return e & 1 ? bf_hi(w[e / 2]) : bf_lo(w[e / 2]);
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+// VEC: all rows are at 16-byte boundaries
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   __shared__ uint64_t s_slice[2][kMaxCluster];  // [try][CTA]
   __shared__ uint64_t s_seg[kWarps], s_scan[kWarps];
   __shared__ int s_m, s_end;
@@ -114,11 +219,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   const int m = s_m, end = s_end;
   if (rank == 0) {
     if (threadIdx.x < m) out[threadIdx.x] = tokens[threadIdx.x];
-    if (threadIdx.x > m && threadIdx.x <= a.n_draft) out[threadIdx.x] = -1;
-    if (threadIdx.x == 0) {
-      a.accepted[r] = m;
-      if (end == 2) out[0] = -1;
-    }
+    if (threadIdx.x >= m && threadIdx.x <= a.n_draft) out[threadIdx.x] = -1;  // (the next token comes behind a barrier)
+    if (threadIdx.x == 0) a.accepted[r] = m;
   }
   cluster_wait();
   if (end == 2) return;  // (the whole cluster)
@@ -131,12 +233,16 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
       w.token = tokens[m];
   }
   // this CTA's slice and its warps' segments
-  const int slice = (a.vocab + ctas - 1) / ctas, s0 = min(rank * slice, a.vocab), s1 = min(s0 + slice, a.vocab);
-  const int seg = ((s1 - s0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+  // (multiples of 256 values, which keeps 16-byte boundaries)
+  constexpr int kUnit = 256;
+  const int slice = (a.vocab + ctas * kUnit - 1) / (ctas * kUnit) * kUnit;
+  const int s0 = min(rank * slice, a.vocab), s1 = min(s0 + slice, a.vocab);
+  const int seg = (s1 - s0 + kWarps * kUnit - 1) / (kWarps * kUnit) * kUnit;
   const uint64_t u = (uint64_t)((double)as_uniform(uniform[a.n_draft]) * 18446744073709551616.0);
   for (int pass = 0; pass < 2; ++pass) {
     const int g0 = min(s0 + warp * seg, s1);
-    const uint64_t mine = warp_sum(w.sum(g0, min(g0 + seg, s1)));
+    const int g1 = min(g0 + seg, s1);
+    const uint64_t mine = warp_sum(VEC ? w.sum_vec(g0, g1) : w.sum(g0, g1));
     if (lane == 0) s_seg[warp] = mine;
     __syncthreads();
     if (warp == 0) {
@@ -155,7 +261,6 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         w.token = -1;
         continue;
       }
-      if (rank == 0 && threadIdx.x == 0) out[m] = -1;
       return;
     }
     const uint64_t t = __umul64hi(total, u);  // floor(u S)
@@ -193,8 +298,12 @@ cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
   // CTAs of a request: enough that few requests use the whole GPU, each with 4,096 tokens or more
   unsigned c = 1;
   while (c < kMaxCluster && (long long)a.batch * c < 2LL * device_sm_count() && a.vocab / (2 * (int)c) >= 4096) c *= 2;
-  auto kern = bf16 ? verify_kernel<__nv_bfloat16> : verify_kernel<float>;
-  return launch_clusters(kern, dim3((unsigned)a.batch * c), dim3(kThreads), c, s, a);
+  const long long each = bf16 ? 8 : 4;  // values of 16 bytes
+  bool vec = aligned_all(16, {a.target, a.draft}) && (a.target_batch | a.target_row) % each == 0;
+  if (a.draft) vec = vec && (a.draft_batch | a.draft_row) % each == 0;
+  auto kern = bf16 ? (vec ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>)
+                   : (vec ? verify_kernel<float, true> : verify_kernel<float, false>);
+  return launch_clusters(kern, dim3((unsigned)a.batch * c), dim3(kThreads), c, 0, s, a);
 }
 
 }  // namespace qsa

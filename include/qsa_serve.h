@@ -132,12 +132,12 @@ typedef struct {
  * Writes accepted[r] = m and out_tokens[r] = x[0 .. m - 1], y, then -1
  * (n_draft + 1 entries). The distribution so sampled is the target's.
  *
- * The test is exact. The sums are exact sums of the weights' multiples of
- * 2^-60 (a smaller rest is dropped), so the result does not depend on their
- * order and is that of the formula in 64 bits. A row's weights must sum to
- * less than 16; they need not sum to 1. A probability that is negative or NaN
- * counts as 0, one above 1 as 1. A u below 0 or NaN counts as 0, one of 1 or
- * more as the largest below 1. Where p_m is 0 everywhere, y is -1.
+ * The test is exact. So are the sums, of probabilities rounded to multiples of
+ * 2^-54: the result does not depend on an order, and is that of the formula in
+ * 64 bits. A row's probabilities must sum to less than 16; they need not sum to
+ * 1. One that is negative or NaN counts as 0, one above 1 as 1. A u below 0 or
+ * NaN counts as 0, one of 1 or more as the largest below 1. Where p_m so rounded
+ * is 0 everywhere, y is -1.
  *
  * A token outside 0..vocab - 1 other than -1 ends the drafts too; it is
  * reported (kind 7), but for -2 as a request's first token, which stands for

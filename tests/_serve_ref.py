@@ -64,10 +64,13 @@ def evict(w, n, keep, sinks, recent):
     return np.sort(np.concatenate([np.arange(sinks), best, np.arange(n - recent, n)])).astype(int)
 
 
-def fixed60(p):
+def clean(p):
     p = np.asarray(p, dtype=np.float64)
-    p = np.where(np.isnan(p), 0.0, np.clip(p, 0.0, 1.0))
-    return np.floor(p * 2.0 ** 60).astype(np.uint64)  # (24 significant bits: exact)
+    return np.where(np.isnan(p), 0.0, np.clip(p, 0.0, 1.0))
+
+
+def fixed54(p):
+    return np.rint(clean(p) * 2.0 ** 54).astype(np.int64)  # (24 significant bits: the product is exact)
 
 
 def uniform(u):
@@ -85,30 +88,28 @@ def verify(target, draft, tokens, u):
     if tokens[0] == -2:
         return 0, out
     m, rejected = 0, False
-    clean = lambda x: 0.0 if math.isnan(x) else min(max(x, 0.0), 1.0)  # noqa: E731
     while m < n and 0 <= tokens[m] < V:
-        q = clean(float(draft[m, tokens[m]])) if draft is not None else 1.0
-        if not uniform(u[m]) * q < clean(float(target[m, tokens[m]])):
+        q = float(clean(draft[m, tokens[m]])) if draft is not None else 1.0
+        if not uniform(u[m]) * q < float(clean(target[m, tokens[m]])):
             rejected = True
             break
         out[m] = int(tokens[m])
         m += 1
-    p = fixed60(target[m])
+    p = fixed54(target[m])
     w = p
     if rejected:
         if draft is not None:
-            q = fixed60(draft[m])
-            w = np.where(p > q, p - q, np.uint64(0))
+            w = np.where(clean(target[m]) > clean(draft[m]), p - fixed54(draft[m]), 0)
         else:
             w = p.copy()
             w[tokens[m]] = 0
         if not w.any():
             w = p
-    cum = np.cumsum(w, dtype=np.uint64)
+    cum = np.cumsum(w, dtype=np.int64)
     total = int(cum[-1])
     if total:
         t = total * int(uniform(u[n]) * 2.0 ** 64) >> 64
-        out[m] = int(np.searchsorted(cum, np.uint64(t), side="right"))
+        out[m] = int(np.searchsorted(cum, t, side="right"))
     return m, out
 
 
