@@ -1,12 +1,20 @@
 // Eviction from the paged cache by accumulated attention weight.
 //
 // Of a request's n > keep tokens the first `sinks`, the last `recent` and the
-// heaviest between them stay. A cluster of CTAs takes a request and finds the
-// weight of the last one that stays by a radix selection (three digits of the
-// weight's order-preserving key, the counts of the CTAs added up through
-// distributed shared memory), then numbers those that stay in the order of
-// their positions. A second kernel, chained with programmatic dependent
-// launch, copies their K and V.
+// heaviest between them stay. A cluster of CTAs takes a request, each a slice of
+// its positions, and finds the weight of the last one that stays by a radix
+// selection on the weight's order-preserving key: counts by the key's first 11
+// bits, added up through distributed shared memory; then the keys that share the
+// last one's first digit, which are few, go to every CTA, and each finds the
+// other two digits by itself. (Where they are many, equal weights for instance,
+// all three digits are counted in the cluster.) What stays is then numbered in
+// the order of the positions. A barrier of a cluster takes about 0.7 us and a
+// digit of the cluster two of them; that, not the weights' bytes, is the time of
+// this kernel: 61,201 positions in three digits of the cluster, with the lanes
+// that hit the same count one after the other, took 37 us.
+//
+// A second kernel, chained with programmatic dependent launch, copies K and V of
+// the tokens that stay (the bytes of which are the bound for a batch).
 #include <algorithm>
 
 #include "qsa_serve_internal.cuh"
@@ -19,6 +27,9 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr unsigned kHeld = 16384;  // weights of a slice that are held in shared memory
+constexpr unsigned kCand = 2048;   // keys with the last one's first digit that every CTA can take
+constexpr uint32_t kZeroKey = 0x80000000u;  // of a weight of 0
+constexpr int kSlice = 4096;       // positions of a CTA, more or less
 
 __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x) {
   const int lane = threadIdx.x & 31;
@@ -53,13 +64,35 @@ __device__ __forceinline__ uint64_t block_exclusive(uint64_t x, uint64_t (&scan)
   return before;
 }
 
+// The same for 32-bit counts whose block total the caller does not need; `scan`
+// is read behind one barrier (the caller has another before it is written again).
+__device__ __forceinline__ uint32_t block_before(uint32_t x, uint32_t (&scan)[kSelWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) scan[warp] = inc;
+  __syncthreads();
+  const uint32_t other = lane < warp ? scan[lane] : 0;  // (at most 32 warps)
+  return inc - x + __reduce_add_sync(kFull, other);
+}
+
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ float s_w[];  // the first kHeld weights of the slice
-  __shared__ uint32_t s_hist[kBins], s_sum[kBins];  // this CTA's counts, the cluster's
+  extern __shared__ float s_w[];  // the first a.held weights of the slice
+  __shared__ uint32_t s_hist[kBins], s_sum[kBins], s_cand[kCand], s_own[kCand];  // this CTA's counts, the cluster's
   __shared__ uint64_t s_scan[kSelWarps], s_slice[kMaxCluster];
-  __shared__ uint32_t s_bin, s_left;
+  __shared__ uint32_t s_bin, s_left, s_same, s_at, s_count[kSelWarps];
   const int tid = threadIdx.x;
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size(), r = blockIdx.x / ctas;
+  auto sync = [&]() {
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
   pdl_wait();
   pdl_trigger();
   // (positions are below 2^31; unsigned, so that a step past the last one is still a number)
@@ -78,77 +111,113 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     w_out[i] = 0.f;
     if (i < keep) kept[i] = -1;
   }
-  cluster_sync();  // every CTA has read len (and has started)
-  if (rank == 0 && tid == 0) a.new_len[r] = (int)left;
   if (n <= keep) {
     for (unsigned i = first; i < n; i += step) {
       kept[i] = (int)i;
       w_out[i] = w[i];
     }
+    sync();  // every CTA has read len, which new_len may be
+    if (rank == 0 && tid == 0) a.new_len[r] = (int)left;
     return;  // (the whole cluster)
   }
   // positions lo .. hi - 1 are chosen from, `need` of them
   const unsigned lo = (unsigned)a.sinks, hi = n - (unsigned)a.recent;
   const unsigned slice = (n + ctas - 1) / ctas, s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
   const unsigned held = min(s1 - s0, a.held);
+#pragma unroll 8
   for (unsigned i = tid; i < held; i += kSelThreads) s_w[i] = w[s0 + i];
   auto key_at = [&](unsigned t) { return order_key(t - s0 < held ? s_w[t - s0] : w[t]); };
   uint32_t need = keep - a.sinks - a.recent, prefix = 0, mask = 0;
   if (need > 0) {
     const unsigned c0 = max(s0, lo), c1 = max(c0, min(s1, hi));  // the slice's part of them
-    const int own_bins = kBins / ctas;
+    bool gathered = false;
+    unsigned cands = 0;
 #pragma unroll 1
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;  // (the last digit has a bit of the second's)
       for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+      if (tid == 0) s_at = 0;
       __syncthreads();
-      for (unsigned t = c0 + tid; t - tid < c1; t += kSelThreads) {
-        const uint32_t k = t < c1 ? key_at(t) : 0;
-        const bool in = t < c1 && (k & mask) == prefix;
-        const uint32_t bin = (k >> shift) & (kBins - 1);
-        // the lanes with the first such lane's digit count as one (many equal weights are usual)
-        const uint32_t any = __ballot_sync(kFull, in);
-        if (any == 0) continue;
-        const int first_lane = __ffs(any) - 1;
-        const uint32_t their = __shfl_sync(kFull, bin, first_lane);  // (every lane takes part)
-        const uint32_t same = __ballot_sync(kFull, in && bin == their);
-        if ((tid & 31) == first_lane)
-          atomicAdd(&s_hist[bin], (uint32_t)__popc(same));
-        else if (in && !((same >> (tid & 31)) & 1u))
-          atomicAdd(&s_hist[bin], 1u);
+      const unsigned from = gathered ? 0 : c0, to = gathered ? cands : c1;
+      uint32_t zeros = 0;  // of them there may be many: a warp adds them at once
+#pragma unroll 4
+      for (unsigned t = from + tid; t < to; t += kSelThreads) {
+        const uint32_t k = gathered ? s_cand[t] : key_at(t);
+        if ((k & mask) != prefix) continue;
+        if (k == kZeroKey)
+          ++zeros;
+        else
+          atomicAdd(&s_hist[(k >> shift) & (kBins - 1)], 1u);
       }
-      // each CTA adds up a part of the bins for all of them
-      cluster_sync();
-      for (int i = tid; i < own_bins; i += kSelThreads) {
-        const int bin = rank * own_bins + i;
-        uint32_t c = 0;
+      zeros = __reduce_add_sync(kFull, zeros);
+      if ((tid & 31) == 0 && zeros > 0) atomicAdd(&s_hist[(kZeroKey >> shift) & (kBins - 1)], zeros);
+      const uint32_t* counts = s_hist;
+      if (ctas > 1 && !gathered) {
+        // each CTA adds up a part of the bins for all of them
+        cluster_sync();
+        const int per = kBins / ctas;
+        for (int i = tid; i < per; i += kSelThreads) {
+          const int bin = rank * per + i;
+          uint32_t c = 0;
 #pragma unroll
-        for (int p = 0; p < kMaxCluster; ++p) c += p < ctas ? ld_peer(peer_addr(&s_hist[bin], p)) : 0;
+          for (int p = 0; p < kMaxCluster; ++p) c += p < ctas ? ld_peer(peer_addr(&s_hist[bin], p)) : 0;
 #pragma unroll
-        for (int p = 0; p < kMaxCluster; ++p)
-          if (p < ctas) st_peer_u32(peer_addr(&s_sum[bin], p), c);
+          for (int p = 0; p < kMaxCluster; ++p)
+            if (p < ctas) st_peer_u32(peer_addr(&s_sum[bin], p), c);
+        }
+        cluster_sync();
+        counts = s_sum;
+      } else {
+        __syncthreads();
       }
-      cluster_sync();
-      // the digit of the last one that stays, from the largest down (4 a thread)
-      uint32_t c[4];
-      uint64_t mine = 0, all;
+      // the digit of the last one that stays, from the largest down
+      constexpr int kPer = kBins / kSelThreads;
+      uint32_t c[kPer];
+      uint32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = s_sum[kBins - 1 - (tid * 4 + i)];
+      for (int i = 0; i < kPer; ++i) {
+        c[i] = counts[kBins - 1 - (tid * kPer + i)];
         mine += c[i];
       }
-      const uint64_t before = block_exclusive(mine, s_scan, &all);
+      const uint32_t before = block_before(mine, s_count);
       if (before < need && need <= before + mine) {  // one thread
-        uint32_t b = (uint32_t)before;
+        uint32_t b = before;
         int i = 0;
         while (b + c[i] < need) b += c[i++];
-        s_bin = (uint32_t)(kBins - 1 - (tid * 4 + i));
+        s_bin = (uint32_t)(kBins - 1 - (tid * kPer + i));
         s_left = need - b;
+        s_same = c[i];
       }
       __syncthreads();
-      prefix |= s_bin << shift;
+      const uint32_t bin = s_bin;
+      prefix |= bin << shift;
       mask |= (uint32_t)(kBins - 1) << shift;
       need = s_left;
+      if (ctas > 1 && d == 0 && s_same <= kCand) {
+        // the keys with that digit go to every CTA, this one's behind those of the CTAs before it
+        for (unsigned t = c0 + tid; t - tid < c1; t += kSelThreads) {
+          const uint32_t k = t < c1 ? key_at(t) : 0;
+          const bool in = t < c1 && (k & mask) == prefix;
+          const uint32_t lanes = __ballot_sync(kFull, in);
+          if (lanes == 0) continue;
+          const int lane = tid & 31, leader = __ffs(lanes) - 1;
+          uint32_t at = 0;
+          if (lane == leader) at = atomicAdd(&s_at, (uint32_t)__popc(lanes));
+          at = __shfl_sync(kFull, at, leader) + __popc(lanes & ((1u << lane) - 1u));
+          if (in) s_own[at] = k;
+        }
+        uint32_t at = 0;
+        for (int p = 0; p < rank; ++p) at += ld_peer(peer_addr(&s_hist[bin], p));
+        __syncthreads();
+        const uint32_t own = s_at;
+        for (uint32_t i = tid; i < own * (uint32_t)ctas; i += kSelThreads) {
+          const uint32_t p = i / own, j = i - p * own;
+          st_peer_u32(peer_addr(&s_cand[at + j], p), s_own[j]);
+        }
+        cluster_sync();
+        gathered = true;
+        cands = s_same;
+      }
     }
   } else {
     __syncthreads();
@@ -165,9 +234,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   uint64_t all;
   uint64_t before = block_exclusive(count, s_scan, &all);
-  if (tid < ctas) st_peer_u64(peer_addr(&s_slice[rank], tid), all);
-  cluster_sync();
-  for (int p = 0; p < rank; ++p) before += s_slice[p];
+  if (ctas > 1) {
+    if (need == 0) cluster_sync();  // (no other before it: every CTA has started)
+    if (tid < ctas) st_peer_u64(peer_addr(&s_slice[rank], tid), all);
+    cluster_sync();
+    for (int p = 0; p < rank; ++p) before += s_slice[p];
+  }
+  if (rank == 0 && tid == 0) a.new_len[r] = (int)left;  // (every CTA has read len)
   uint32_t ties = (uint32_t)(before >> 32), at = (uint32_t)before + min(ties, need);
   for (unsigned t = t0; t < t1; ++t) {
     const bool sure = t < lo || t >= hi;
@@ -238,10 +311,10 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s) {
-  // CTAs of a request: enough that few requests use the whole GPU, each with 2,048 positions or more
+  // CTAs of a request: few, for their barriers; more only where the slices would be long
   const int cap = a.max_pages * a.page_size;
   unsigned c = 1;
-  while (c < kMaxCluster && (long long)a.batch * c < 2LL * device_sm_count() && cap / (2 * (int)c) >= 2048) c *= 2;
+  while (c < kMaxCluster && (long long)a.batch * c < device_sm_count() && cap / (int)c > kSlice) c *= 2;
   a.held = std::min(kHeld, ((unsigned)cap + c - 1) / c);
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(evict_select_kernel, kHeld * sizeof(float));

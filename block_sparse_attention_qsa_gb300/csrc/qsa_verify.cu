@@ -17,7 +17,11 @@
 // to a multiple of 2^-54. As 64-bit integers these cost the integer pipe 36
 // cycles a value and warp, and 256 rows of 150,001 tokens (FP32, sampled drafts)
 // 81 us; the conversion instruction to 64 bits was slower still, 158. So they
-// are added in FP32 without rounding (see Exact), which takes 11 additions.
+// are added in FP32 without rounding (see Exact), 11 additions for two values:
+// 60 us, where the bytes take 38. What is left is those additions (16-bit
+// probabilities take 54), the SM that has four CTAs where others have three, and
+// the beginning and end of a CTA; a ring of bulk copies to shared memory in place
+// of the loads was slower (92), and so were shares for smaller or more CTAs.
 #include "qsa_serve_internal.cuh"
 
 namespace qsa {
@@ -33,16 +37,14 @@ __device__ __forceinline__ float load(const __nv_bfloat16* p) {
   return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
-// A probability in 2^-54ths; negative and NaN 0, above 1 as 1.
-__device__ __forceinline__ int64_t fixed54(float x) { return __float2ll_rn(__saturatef(x) * 0x1p54f); }
-
 // Exact sums of values of at most 1 in magnitude, each rounded to a multiple of
 // 2^-54. A value is taken apart on three fixed grids: x + M, with M 1.5 2^23 times
 // the grid, is rounded to the grid, and what is left is exact again. The parts
 // on the grid of 2^-20 add up without rounding to below 2^4, those on 2^-37 (at
 // most 2^-21 each) to 2^-13, those on 2^-54 (at most 2^-38) to 2^-30, that is
 // for kMost values. The last part's rounding is to nearest, ties to even, and so
-// is the whole value's.
+// is the whole value's. A probability that is negative or NaN is 0, one above 1
+// is 1 (saturated).
 struct Exact {
   static constexpr int kMost = 256;
   static constexpr float kM1 = 1.5f * 0x1p3f, kM2 = 1.5f * 0x1p-14f, kM3 = 1.5f * 0x1p-31f;
@@ -60,11 +62,25 @@ struct Exact {
     x = add2(x, t2);
     a3 = add2(a3, part(x, kM3));
   }
+  // a probability in 2^-54ths: the parts as integers, which are in the sums' last bits
+  static __device__ __forceinline__ int64_t of(float x) {
+    x = __saturatef(x);
+    const float s1 = __fadd_rn(x, kM1);
+    x = __fsub_rn(x, __fsub_rn(s1, kM1));
+    const float s2 = __fadd_rn(x, kM2);
+    x = __fsub_rn(x, __fsub_rn(s2, kM2));
+    const float s3 = __fadd_rn(x, kM3);
+    return combine(__float_as_int(s1) - __float_as_int(kM1), __float_as_int(s2) - __float_as_int(kM2),
+                   __float_as_int(s3) - __float_as_int(kM3));
+  }
+  static __device__ __forceinline__ int64_t combine(int i1, int i2, int i3) {
+    return (int64_t)i1 * (1LL << 34) + (int64_t)i2 * (1LL << 17) + i3;
+  }
   __device__ __forceinline__ int64_t sum() const {  // in 2^-54ths
     const int i1 = __float2int_rn(a1.x * 0x1p20f) + __float2int_rn(a1.y * 0x1p20f);
     const int i2 = __float2int_rn(a2.x * 0x1p37f) + __float2int_rn(a2.y * 0x1p37f);
     const int i3 = __float2int_rn(a3.x * 0x1p54f) + __float2int_rn(a3.y * 0x1p54f);
-    return -((int64_t)i1 * (1LL << 34) + (int64_t)i2 * (1LL << 17) + i3);
+    return -combine(i1, i2, i3);
   }
 };
 __device__ __forceinline__ float as_uniform(float u) { return fminf(fmaxf(u, 0.f), 0x1.fffffep-1f); }
@@ -97,9 +113,9 @@ struct Weights {
     const float x = load(p + v);
     if (q) {
       const float y = load(q + v);
-      return __saturatef(x) > __saturatef(y) ? (uint64_t)(fixed54(x) - fixed54(y)) : 0;
+      return __saturatef(x) > __saturatef(y) ? (uint64_t)(Exact::of(x) - Exact::of(y)) : 0;
     }
-    return v == token ? 0 : (uint64_t)fixed54(x);
+    return v == token ? 0 : (uint64_t)Exact::of(x);
   }
   // two weights into a sum
   static __device__ __forceinline__ void add_less(Exact& s, float p0, float q0, float p1, float q1) {
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     // the segment that holds it
     uint64_t rest = t - before;
     int g = 0;
-    while (rest >= s_seg[g]) rest -= s_seg[g++];
+    while (g < kWarps - 1 && rest >= s_seg[g]) rest -= s_seg[g++];
     const int b0 = s0 + g * seg, n = min(seg, s1 - b0), per = (n + kThreads - 1) / kThreads;
     const int v0 = b0 + min((int)threadIdx.x * per, n), v1 = b0 + min((int)(threadIdx.x + 1) * per, n);
     uint64_t own = 0;
@@ -281,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     if (front <= rest && rest - front < own) {  // one thread
       rest -= front;
       int v = v0;
-      for (;; ++v) {
+      for (; v < v1 - 1; ++v) {
         const uint64_t x = w.at(v);
         if (rest < x) break;
         rest -= x;
