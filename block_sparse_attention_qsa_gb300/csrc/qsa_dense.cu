@@ -78,6 +78,18 @@ static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
   return p;
 }
 
+// Whether every request reads the prefix by itself: where those bytes are few,
+// the two kernels of a shared one cost more than they save. (Own parts of 1 to
+// 200 tokens, shared and alone: 32 requests x 1 query, BF16, 256 tokens shared
+// 14.8 and 11.2 us, 1,024 tokens 16.0 and 12.8, 4,096 tokens, 860 KB an SM, 17.8
+// and 19.1; x 4 queries, E4M3, 4,096 tokens, 430 KB, 35.3 and 25.0.)
+constexpr long long kAloneBytes = 640 * 1024;  // an SM
+static bool alone(const qsa_dims& d, int prefix_len, int rows, int sms) {
+  const int all = d.n_q * (d.n_q_heads / d.n_kv_heads), eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2;
+  const long long reads = (long long)d.batch * d.n_kv_heads * ((all + rows - 1) / rows);
+  return d.batch == 1 || reads * prefix_len * 2 * d.head_dim * eb <= kAloneBytes * sms;
+}
+
 struct PrefixWs {
   size_t whole, parts, total;
 };
@@ -153,7 +165,10 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
   a.one = 1.f;
   const int rows = unit_rows(d);
-  if (prefix.len > 0) return launch_with_prefix(d, a, rows, base, k_cache, v_cache, s);
+  if (prefix.len > 0 && !(prefix.alone < 0 ? alone(d, prefix.len, rows, sms) : prefix.alone)) {
+    a.shared_len = prefix.len;
+    return launch_with_prefix(d, a, rows, base, k_cache, v_cache, s);
+  }
   return launch_dense(rows, d, a, k_cache, v_cache, short_k, s);
 }
 

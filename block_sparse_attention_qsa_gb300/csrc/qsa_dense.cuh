@@ -52,6 +52,7 @@ struct DenseArgs {
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
   int page_size, page_shift, max_pages, num_pages, window, grid;
   int prefix_len;  // whole pages
+  int shared_len;  // prefix_len, or 0: every request is worked on by itself, its prefix too
   float sm_scale;
   float one;  // 1
 };
@@ -137,7 +138,7 @@ __device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
 __device__ __forceinline__ bool sees_prefix(const DenseArgs& a, const int (&p)[kMaxNq]) {
   bool all = true;
 #pragma unroll
-  for (int j = 0; j < kMaxNq; ++j) all &= !valid_pos(a, p[j]) || p[j] >= a.prefix_len - 1;
+  for (int j = 0; j < kMaxNq; ++j) all &= !valid_pos(a, p[j]) || p[j] >= a.shared_len - 1;
   return all;
 }
 __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
@@ -151,7 +152,7 @@ __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
     g.lo = min(g.lo, low_of(a, p[j]));
     g.hi = max(g.hi, p[j] + 1);
   }
-  if (a.prefix_len > 0 && sees_prefix(a, p)) g.lo = a.prefix_len;
+  if (a.shared_len > 0 && sees_prefix(a, p)) g.lo = a.shared_len;
   return g.hi > g.lo ? g : Range{0, 0};
 }
 

@@ -52,16 +52,17 @@ struct DenseWs {
 };
 DenseWs dense_ws(const qsa_dims& d, int num_sms);
 // The pages of positions below `len`, for every request (null: none, len 0).
+// alone: 1 every request reads them by itself, 0 they are read once for all, -1 by their bytes.
 struct Prefix {
   const int32_t* table;
-  int len;
+  int len, alone;
 };
 size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms);  // bytes of workspace with a prefix
 // short_k: the failure-detection test (qsa_test_paged_attn_timeout)
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
                               const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s,
-                              bool short_k = false, const Prefix& prefix = Prefix{nullptr, 0});
+                              bool short_k = false, const Prefix& prefix = Prefix{nullptr, 0, -1});
 
 // 16-byte loads and stores of streamed data
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }

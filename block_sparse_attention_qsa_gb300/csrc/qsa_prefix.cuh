@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
 #pragma unroll 1
       for (int z0 = 0; z0 < kPasses; z0 += kDeep) {
         uint4 w[kDeep];
+        uint32_t bigs[FP8 ? kDeep : 1];
 #pragma unroll
         for (int z = 0; z < kDeep; ++z) {
           w[z] = make_uint4(0, 0, 0, 0);
@@ -397,15 +398,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
         }
 #pragma unroll
         for (int z = 0; z < kDeep; ++z) {
+          if constexpr (FP8) {  // magnitudes of BF16 values order like their bit patterns
+            const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
+            bigs[z] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bigs[z] = max(bigs[z], max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
+          }
+        }
+        if constexpr (FP8) {  // (all rows' shuffles side by side)
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+            for (int z = 0; z < kDeep; ++z) bigs[z] = max(bigs[z], __shfl_xor_sync(kFull, bigs[z], o));
+        }
+#pragma unroll
+        for (int z = 0; z < kDeep; ++z) {
           const int r = (z0 + z) * kPass + t / kLanes;
           uint4 v = w[z];
           if constexpr (FP8) {
-            uint32_t big = 0;  // magnitudes of BF16 values order like their bit patterns
             uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) big = max(big, max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+            const uint32_t big = bigs[z];
             // 2^-sh brings the row's largest value into [2^14, 2^15)
             const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
             // (a row with an infinity or NaN: every component NaN, as its scores
@@ -757,7 +769,8 @@ cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k,
   }
   e = launch_k(prefix_kernel<C>, dim3((unsigned)a.units * a.splits), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  // 4 warps a row where rows are few; with a warp a row their loads fill the GPU
+  // 4 warps a row where rows are few; else a warp a row (2,048 rows of 20 to 25
+  // pieces: 4 warps each made the whole call 6 us slower)
   const unsigned rows = (unsigned)(a.a.batch * a.a.n_q * a.a.n_q_heads);
   if (rows < 8u * a.a.grid)
     return launch_k(prefix_join_kernel<D, FP8, 4>, dim3(rows), dim3(128), 0, s, true, a);

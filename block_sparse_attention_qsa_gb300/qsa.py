@@ -49,7 +49,8 @@ KV_EXPORTS = (
 )
 # and those of include/qsa_serve.h, the operators for serving a batch in a bounded cache
 SERVE_EXPORTS = (
-    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_kv_weight", "qsa_kv_evict", "qsa_verify_drafts",
+    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_test_prefix_attn", "qsa_kv_weight", "qsa_kv_evict",
+    "qsa_verify_drafts",
 )
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
@@ -159,6 +160,7 @@ def _load() -> ctypes.CDLL:
     sig.update({
         "qsa_prefix_workspace_size": (I, [D, N, ctypes.POINTER(SZ)]),
         "qsa_prefix_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_test_prefix_attn": (I, [D, N, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_weight": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_evict": (I, [D, N, N, N, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_verify_drafts": (I, [N, N, N, N, P, T, P, T, P, P, P, P, P, SZ, P]),
@@ -800,6 +802,12 @@ def prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, pa
         return
     if st is not None:
         _check(st, "qsa_prefix_attn")
+    _prefix_attn(lib.qsa_prefix_attn, "qsa_prefix_attn", d, (), q, k_cache, v_cache, k_scale, v_scale, prefix_table,
+                 page_table, q_pos, out, ws, lse, stream)
+
+
+def _prefix_attn(fn, name, d, extra, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, ws,
+                 lse, stream):
     dev = _current_device()
     B, n_q, H = d.batch, d.n_q, d.n_q_heads
     shape = (B, n_q, H, d.head_dim)
@@ -813,9 +821,17 @@ def prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, pa
     pp = _want_on(dev, q_pos, "q_pos", (B, n_q), _I32)
     lp = None if lse is None else _want_on(dev, lse, "lse", (B, n_q, H), _F32)
     w, nb = _ws_on(dev, ws)
-    st = lib.qsa_prefix_attn(d, n, xp, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
+    st = fn(d, *extra, n, xp, qp, kc, vc, ksc, vsc, pt, pp, op, lp, w, nb, _stream(stream))
     if st:
-        _check(st, "qsa_prefix_attn")
+        _check(st, name)
+
+
+def test_prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, ws, lse=None,
+                     alone: bool = False, stream=None):
+    """qsa_test_prefix_attn: prefix_attn with the prefix read once for all
+    requests, or with ``alone`` by each for itself, whatever its size. For tests."""
+    _prefix_attn(lib.qsa_test_prefix_attn, "qsa_test_prefix_attn", d, (int(alone),), q, k_cache, v_cache, k_scale,
+                 v_scale, prefix_table, page_table, q_pos, out, ws, lse, stream)
 
 
 def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, decay: float = 1.0, stream=None):

@@ -41,21 +41,34 @@ qsa_status qsa_prefix_workspace_size(const qsa_dims* dims, int32_t prefix_pages,
  *
  * The shared positions are read once for all requests, whose query rows are
  * worked on together, and each request's own positions once for the request;
- * a request one of whose queries does not see the whole prefix is worked on
- * by itself. The pieces are joined in a fixed order: the same call gives the
- * same bits. Out, lse, empty rows and errors are as for qsa_paged_attn; a page
- * id of the prefix outside the cache is reported (kind 2) for request -1.
+ * a request one of whose queries does not see the whole prefix is worked on by
+ * itself, and so are all of them where the prefix's bytes are few. The pieces
+ * are joined in a fixed order: the same call gives the same bits. Out, lse,
+ * empty rows and errors are as for qsa_paged_attn; a page id of the prefix
+ * outside the cache is reported (kind 2) for request -1.
  *
- * FP32 softmax statistics and accumulation, BF16 out. Over the prefix the
- * weights of the second product have fewer bits (not those in the softmax's
- * sum): BF16 (off by at most 2^-8 of themselves) with a BF16 cache; FP16 (off
- * by at most 2^-11 of themselves, or 2^-31 of the row's largest) with an E4M3
- * cache, whose queries are FP16 then too, scaled by a power of two: a component
- * is off by at most 2^-39 of its head's largest. */
+ * FP32 softmax statistics and accumulation, BF16 out. What has fewer bits over
+ * a request's own positions (and over the prefix, where it is read alone) is
+ * said at qsa_paged_attn. Over a prefix read once, the weights of the second
+ * product (not those in the softmax's sum) are BF16 (off by at most 2^-8 of
+ * themselves) with a BF16 cache and FP16 (2^-11 of themselves, or 2^-31 of the
+ * largest weight so far) with an E4M3 cache, whose queries are FP16 then too,
+ * scaled by a power of two: a component is off by at most 2^-39 of its head's
+ * largest. The sums before the division by the softmax's have weights up to
+ * 2^24 (BF16) or 2^15 there: values of 2^(103 - log2 of the positions) or more
+ * may overflow in them. */
 qsa_status qsa_prefix_attn(const qsa_dims* dims, int32_t prefix_pages, const int32_t* prefix_table, const void* q,
                            const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                            const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
                            size_t ws_bytes, void* stream);
+
+/* Test hook: qsa_prefix_attn with the choice made for it that it makes by the
+ * prefix's bytes: alone 0, the prefix is read once for all requests; 1, each
+ * request reads it by itself (what it does for small ones). */
+qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages, const int32_t* prefix_table,
+                                const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* page_table, const int32_t* q_pos, void* out,
+                                float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* The attention weight that each cached position gets from the newest tokens:
  *   weight[r][t] = decay * weight[r][t]

@@ -95,6 +95,11 @@ def test_prefix_attn_refusals(qsa):
         assert call(0, e) == want, field
 
 
+    for alone in (-1, 2):
+        assert qsa.lib.qsa_test_prefix_attn(good[0], alone, *good[1:]) == qsa.ERR_INVALID_ARG
+    assert qsa.lib.qsa_test_prefix_attn(good[0], 0, *_with(good, 3, None)[1:]) == qsa.ERR_INVALID_ARG
+
+
 @no_device
 def test_kv_weight_refusals(qsa):
     d = qsa.make_dims(3, 2, 100, 10, 40, kv_dtype="fp8")

@@ -86,8 +86,12 @@ class Prefixed:
         self.args = (self.d, self.q, self.kc, self.vc, self.ks, self.vs, self.prefix.cuda(), self.table.cuda(),
                      _i32(self.q_pos.tolist()), self.out, self.ws)
 
-    def run(self, qsa, **kw):
-        qsa.prefix_attn(*self.args, lse=self.lse, **kw)
+    def run(self, qsa, alone=None, **kw):
+        """alone: None as prefix_attn chooses, else as told."""
+        if alone is None:
+            qsa.prefix_attn(*self.args, lse=self.lse, **kw)
+        else:
+            qsa.test_prefix_attn(*self.args, lse=self.lse, alone=alone, **kw)
         return self
 
     def compare(self, skip=(), gone=None):
@@ -119,9 +123,23 @@ class Prefixed:
 
 
 def _prefix_case(qsa, *a, **kw):
-    c = Prefixed(qsa, *a, **kw).run(qsa)
+    """The prefix read once for all requests, and by each for itself; what
+    prefix_attn chooses is one of the two, bit for bit."""
+    c = Prefixed(qsa, *a, **kw)
+    both = []
+    for alone in (True, False):
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        c.run(qsa, alone=alone)
+        _ok(qsa, c.ws)
+        c.compare()
+        both.append((c.out.clone(), c.lse.clone()))
+    c.run(qsa)
     _ok(qsa, c.ws)
-    return c.compare()
+    assert any(torch.equal(c.out, o) and torch.equal(c.lse, l) for o, l in both)
+    c.out.copy_(both[1][0])
+    c.lse.copy_(both[1][1])
+    return c
 
 
 HEADS = [(16, 2, 128), (8, 1, 64), (4, 4, 256), (12, 4, 64), (7, 1, 128), (32, 2, 128), (24, 1, 256), (40, 1, 64)]
@@ -159,9 +177,16 @@ def test_prefix_all_padding_and_all_apart(qsa, kv):
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("prefix,own,n_q", [(313, [1, 900], 4), (157, [33] * 40, 1), (641, [3, 5000, 1], 1), (40, [70] * 20, 4),
-                                            (391, [5, 64, 300] * 3, 4), (782, [4] * 24, 1)])
+                                            (391, [5, 64, 300], 4)])
 def test_prefix_long_and_wide(qsa, kv, prefix, own, n_q):
     _prefix_case(qsa, prefix, own, n_q, kv=kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_long_parts(qsa, kv, D):
+    # many heads: few parts of the prefix each, so that a CTA's ring of tiles goes round several times
+    _prefix_case(qsa, 40, [3] * 17, 1, 640, 80, D, 64, kv)
 
 
 @pytest.mark.parametrize("D,B,hq,hk", [(128, 300, 8, 1), (64, 700, 4, 2), (256, 257, 4, 1)])
@@ -189,10 +214,11 @@ def test_prefix_of_every_page(qsa):
     table = c.table[:, :8].contiguous()
     d = _dims(qsa, 3, 8, c.d.num_pages, "bf16", 2, ps=16)
     ws = qsa.make_prefix_workspace(d, 8)
-    qsa.prefix_attn(d, *c.args[1:7], table.cuda(), c.args[8], c.out, ws, lse=c.lse)
-    _ok(qsa, ws)
     c.d = d
-    c.compare()
+    for alone in (False, True):
+        qsa.test_prefix_attn(d, *c.args[1:7], table.cuda(), c.args[8], c.out, ws, lse=c.lse, alone=alone)
+        _ok(qsa, ws)
+        c.compare()
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
@@ -237,10 +263,11 @@ def test_prefix_what_is_masked_never_arrives(qsa, kv, bad, D):
     page, slot = int(c.prefix[3]), 5  # position 53
     for x in (c.kc, c.vc):
         x[page, :, slot] = code
-    c.run(qsa)
-    _ok(qsa, c.ws)
-    c.compare(skip=[(0, 0), (0, 1), (2, 0), (2, 1)])
-    assert torch.isnan(c.out[0].float()).all() and torch.isnan(c.out[2].float()).all()
+    for alone in (True, False):
+        c.run(qsa, alone=alone)
+        _ok(qsa, c.ws)
+        c.compare(skip=[(0, 0), (0, 1), (2, 0), (2, 1)])
+        assert torch.isnan(c.out[0].float()).all() and torch.isnan(c.out[2].float()).all()
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
@@ -250,32 +277,36 @@ def test_prefix_not_finite_queries_stay_in_their_rows(qsa, kv, bad):
         c.q[1, 0, 5, 7] = bad
         c.q[3] = bad
     c = Prefixed(qsa, 10, [30, 4, 9, 2], 2, kv=kv, mutate=poison,
-                 q_pos=[[668, 669], [642, 643], [647, 648], [-1, -1]]).run(qsa)
-    _ok(qsa, c.ws)
-    assert torch.isnan(c.out[1, 0, 5].float()).all()
+                 q_pos=[[668, 669], [642, 643], [647, 648], [-1, -1]])
     q = c.q.clone()
-    c.q[1, 0, 5] = 0
-    c.q[3] = 0
-    c.compare(skip=[(1, 0)])
     good = [h for h in range(16) if h != 5]
-    first = c.out[1, 0, good].clone()
-    c.q.copy_(q)
-    c.q[1, 0, 5] = 1
-    c.q[3] = 1
-    c.run(qsa)
-    assert torch.equal(c.out[1, 0, good], first)
+    for alone in (True, False):
+        c.q.copy_(q)
+        c.run(qsa, alone=alone)
+        _ok(qsa, c.ws)
+        assert torch.isnan(c.out[1, 0, 5].float()).all()
+        first = c.out[1, 0, good].clone()
+        c.q[1, 0, 5] = 0
+        c.q[3] = 0
+        c.compare(skip=[(1, 0)])
+        c.q[1, 0, 5] = 1
+        c.q[3] = 1
+        c.run(qsa, alone=alone)
+        assert torch.equal(c.out[1, 0, good], first)
 
 
 def test_prefix_infinite_values_arrive(qsa):
     def poison(c):
         c.vc[int(c.prefix[2]), 0, 1, 3] = math.inf
         c.vc[int(c.prefix[2]), 1, 1, 4] = -math.inf
-    c = Prefixed(qsa, 6, [9, 1], 1, mutate=poison).run(qsa)
-    _ok(qsa, c.ws)
-    out = c.out.float()
-    assert (out[:, :, :8, 3] == math.inf).all() and (out[:, :, 8:, 4] == -math.inf).all()
-    out[:, :, :8, 3] = out[:, :, 8:, 4] = 0
-    assert torch.isfinite(out).all()
+    c = Prefixed(qsa, 6, [9, 1], 1, mutate=poison)
+    for alone in (True, False):
+        c.run(qsa, alone=alone)
+        _ok(qsa, c.ws)
+        out = c.out.float()
+        assert (out[:, :, :8, 3] == math.inf).all() and (out[:, :, 8:, 4] == -math.inf).all()
+        out[:, :, :8, 3] = out[:, :, 8:, 4] = 0
+        assert torch.isfinite(out).all()
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
@@ -290,6 +321,50 @@ def test_prefix_one_key_far_above(qsa, kv, D):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("rate", [0.02, 0.2, 1.5, -0.2])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_rising_scores(qsa, kv, rate, D):
+    # scores that rise (or fall) by `rate` a position: references move between tiles, and within them
+    def ramp(c):
+        t = torch.arange(c.full.shape[1] * 32, device="cuda").float()
+        for r in range(c.full.shape[0]):
+            row = c.full[r].long().cuda()
+            ok = row >= 0
+            k = torch.zeros((c.full.shape[1], 32, D), device="cuda")
+            k[..., 3] = (t * rate if rate > 0 else (t - 700) * rate).view(-1, 32)
+            if kv == "fp8":  # (a code's value times its scale)
+                k = (k / c.ks[0]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            else:
+                k = k.to(torch.bfloat16)
+            c.kc[row[ok], 0] = k[ok]
+        c.q.zero_()
+        c.q[..., 3] = 1.0
+    _prefix_case(qsa, 22, [90, 5, 33], 2, 4, 1, D, 32, kv=kv, mutate=ramp, sm_scale=1.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("up", [10, 24, 30, 60])
+def test_prefix_huge_equal_scores(qsa, kv, up):
+    # every score is 2^up or so: the weights are equal, the output is the mean of V and lse is near the score
+    def flat(c):
+        c.q.fill_(2.0 ** (up - 7))
+        c.kc.fill_(1.0) if kv == "bf16" else c.kc.fill_(0x38)
+        c.ks.fill_(1.0)
+    c = Prefixed(qsa, 22, [90, 5, 33], 2, 4, 1, 128, 32, kv=kv, mutate=flat, sm_scale=1.0)
+    for alone in (True, False):
+        c.run(qsa, alone=alone)
+        _ok(qsa, c.ws)
+        v = R.f64(c.vc) * (float(c.vs[0]) if kv == "fp8" else 1.0)
+        for r in range(3):
+            for j in range(2):
+                rows = R.rows(v, c.full.numpy()[r], int(c.q_pos[r, j]) + 1)[:, 0]
+                ref, mag = rows.mean(0), np.abs(rows).mean(0)
+                tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -18) * mag
+                assert np.all(np.abs(R.f64(c.out)[r, j] - ref) <= tol), (alone, r, j)
+                assert np.allclose(R.f64(c.lse)[r, j], 2.0 ** up + math.log(len(rows)), rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prefix_lowest_scores(qsa, kv):
     # every score is far below 0, or -infinity (BF16)
     def low(c):
@@ -300,9 +375,11 @@ def test_prefix_lowest_scores(qsa, kv):
         def lowest(c):
             c.q.fill_(-1.0)
             c.kc.fill_(math.inf)
-        c = Prefixed(qsa, 6, [40, 3], 2, mutate=lowest).run(qsa)
-        _ok(qsa, c.ws)
-        assert (c.out == 0).all() and (c.lse == -math.inf).all()
+        c = Prefixed(qsa, 6, [40, 3], 2, mutate=lowest)
+        for alone in (True, False):
+            c.run(qsa, alone=alone)
+            _ok(qsa, c.ws)
+            assert (c.out == 0).all() and (c.lse == -math.inf).all()
 
 
 @pytest.mark.parametrize("kv,D,T", [("bf16", 128, 300000), ("fp8", 128, 300000), ("bf16", 64, 1000000), ("fp8", 64, 260000)])
@@ -323,7 +400,7 @@ def test_prefix_long_sums(qsa, kv, D, T):
     q = _normal((2, 1, 4, D), 5)
     out, lse = torch.empty_like(q), torch.empty((2, 1, 4), device="cuda")
     pos = _i32([[pages * ps + 9], [pages * ps - 1]])
-    qsa.prefix_attn(d, q, kc, vc, one, one, shared, table, pos, out, ws, lse=lse)
+    qsa.test_prefix_attn(d, q, kc, vc, one, one, shared, table, pos, out, ws, lse=lse)
     _ok(qsa, ws)
     assert (out.float() - 1).abs().max().item() <= 2.0 ** -7 + 2.0 ** -12
     want = torch.log((pos.double() + 1)).unsqueeze(-1)
@@ -331,33 +408,34 @@ def test_prefix_long_sums(qsa, kv, D, T):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-def test_prefix_reports_bad_pages(qsa, kv):
+@pytest.mark.parametrize("alone", [True, False])
+def test_prefix_reports_bad_pages(qsa, kv, alone):
     c = Prefixed(qsa, 12, [50, 9], 2, ps=32, kv=kv)
     for bad in (-1, c.d.num_pages, 2 ** 31 - 1):
         t = c.args[6]
         t.copy_(c.prefix)
         t[7] = bad
-        c.run(qsa)
+        c.run(qsa, alone=alone)
         st, info = qsa.check_errors(c.ws)
         assert st == qsa.ERR_BAD_INDEX and info == (2, -1, 0, bad)
         c.compare(gone=np.arange(7 * 32, 8 * 32))
     c.args[6].copy_(c.prefix)
     own = c.args[7].clone()
     c.args[7][1, 12] = -3  # request 1's own page
-    c.run(qsa)
+    c.run(qsa, alone=alone)
     st, info = qsa.check_errors(c.ws)
     assert st == qsa.ERR_BAD_INDEX and info == (2, 1, 0, -3)
     c.compare(skip=[(1, 0), (1, 1)])
     c.args[7].copy_(own)
     # every page of the prefix is bad: what is left is the own part
     c.args[6].fill_(-1)
-    c.run(qsa)
+    c.run(qsa, alone=alone)
     assert qsa.check_errors(c.ws)[0] == qsa.ERR_BAD_INDEX
     c.compare(gone=np.arange(12 * 32))
     c.args[6].copy_(c.prefix)
     c.args[8][0, 1] = c.d.max_pages * 32  # past the table
     c.q_pos[0, 1] = c.d.max_pages * 32
-    c.run(qsa)
+    c.run(qsa, alone=alone)
     st, info = qsa.check_errors(c.ws)
     assert st == qsa.ERR_BAD_INDEX and info == (1, 0, 1, c.d.max_pages * 32)
     c.compare()
@@ -369,9 +447,9 @@ def test_prefix_same_bits_streams_and_graphs(qsa, kv, prefix, own, n_q):
     out, lse = c.out.clone(), c.lse.clone()
     for _ in range(3):
         c.out.zero_()
-        c.run(qsa)
+        c.run(qsa, alone=False)
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
-    qsa.prefix_attn(*c.args)  # without lse
+    qsa.test_prefix_attn(*c.args)  # without lse
     assert torch.equal(c.out, out)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -381,7 +459,7 @@ def test_prefix_same_bits_streams_and_graphs(qsa, kv, prefix, own, n_q):
     graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
     for g, x in zip(graphs, (c, other)):
         with torch.cuda.graph(g, stream=side):
-            x.run(qsa)
+            x.run(qsa, alone=False)
     # two graphs that share a workspace, replayed in turn, and eager calls between
     for _ in range(3):
         c.out.zero_()
@@ -392,14 +470,14 @@ def test_prefix_same_bits_streams_and_graphs(qsa, kv, prefix, own, n_q):
         assert torch.equal(c.out, out)
         other.compare()
     c.out.zero_()
-    c.run(qsa, stream=side)
+    c.run(qsa, alone=False, stream=side)
     side.synchronize()
     assert torch.equal(c.out, out)
     # back to back with no wait between: the pieces of one are not another's
     outs = []
     for x in (c, other, c, other):
         y = torch.empty_like(x.out)
-        qsa.prefix_attn(*x.args[:9], y, c.ws)
+        qsa.test_prefix_attn(*x.args[:9], y, c.ws)
         outs.append(y)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], out) and torch.equal(outs[2], out) and torch.equal(outs[1], outs[3])
@@ -419,10 +497,11 @@ def test_prefix_offsets_past_32_bits(qsa, kv):
     d = _dims(qsa, 2, c.d.max_pages, num_pages, kv, 2)
     ws = qsa.make_prefix_workspace(d, 20)
     up = num_pages - n
-    qsa.prefix_attn(d, c.q, kc, vc, c.ks, c.vs, c.args[6] + up, _up(c.args[7], up), c.args[8], c.out, ws,
-                    lse=c.lse)
-    _ok(qsa, ws)
-    c.compare()
+    for alone in (True, False):
+        qsa.test_prefix_attn(d, c.q, kc, vc, c.ks, c.vs, c.args[6] + up, _up(c.args[7], up), c.args[8], c.out, ws,
+                             lse=c.lse, alone=alone)
+        _ok(qsa, ws)
+        c.compare()
 
 
 def test_prefix_refusals(qsa):
@@ -1130,8 +1209,32 @@ def test_verify_refusals(qsa):
 # --------------------------------------------------------------------------
 # together
 # --------------------------------------------------------------------------
+def test_calls_without_the_fast_path(qsa, monkeypatch):
+    # the binding's own checks make the same calls
+    c = Prefixed(qsa, 40, [70] * 20, 4, kv="fp8")
+    w = Weighed(qsa, [700, 64, 3001], 4, decay=0.5)
+    target, draft, tokens, u = _sampled(5, 3, 9001, torch.bfloat16, 3)
+    ws = qsa.make_kv_workspace(qsa.make_dims(1, 1, 1, 1, 1))
+
+    def everything():
+        e = Evicted(qsa, [300, 20, 99], 50, 2, 10).run(qsa)
+        c.run(qsa)
+        w.weight.copy_(w.old)
+        w.run(qsa)
+        accepted, out = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros((5, 4), dtype=torch.int32, device="cuda")
+        qsa.verify_drafts(target, draft, tokens, u, accepted, out, ws)
+        return [x.clone() for x in (c.out, c.lse, w.weight, e.kc, e.vc, e.kept, e.weight_out, e.new_length, accepted, out)]
+
+    fast = everything()
+    assert qsa._fast is not qsa._NoFast
+    monkeypatch.setattr(qsa, "_fast", qsa._NoFast)
+    for a, b in zip(fast, everything()):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("attend", ["prefix_attn", "test_prefix_attn"])  # (the second reads the prefix once)
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-def test_a_batch_branched_from_one_context(qsa, kv):
+def test_a_batch_branched_from_one_context(qsa, kv, attend):
     """Three requests over a shared prefix: drafts verified, the cache's weights
     kept, the requests brought back to their bound, and decoded on from there."""
     B, n_q, hk, hq, D, ps, prefix = 3, 4, 2, 16, 128, 32, 6
@@ -1150,7 +1253,7 @@ def test_a_batch_branched_from_one_context(qsa, kv):
     pos = _i32([[L + n + j for j in range(n_q)] for n in own])
     q_rot, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((B, n_q, hq), device="cuda")
     qsa.kv_append(d, k, v, kc, vc, c.ks, c.vs, table, pos, ws, rope=rope, q=q, q_out=q_rot)
-    qsa.prefix_attn(d, q_rot, kc, vc, c.ks, c.vs, shared, table, pos, out, ws, lse=lse)
+    getattr(qsa, attend)(d, q_rot, kc, vc, c.ks, c.vs, shared, table, pos, out, ws, lse=lse)
     weight = torch.zeros((B, d.max_pages * ps), device="cuda")
     qsa.kv_weight(d, q_rot, kc, c.ks, table, pos, lse, weight, ws)
     # the model's head stands outside; its probabilities are given
@@ -1172,7 +1275,7 @@ def test_a_batch_branched_from_one_context(qsa, kv):
     q1 = _normal((B, 1, hq, D), 76)
     out1, lse1 = torch.empty_like(q1), torch.empty((B, 1, hq), device="cuda")
     last = (new_length - 1).view(B, 1).contiguous()
-    qsa.prefix_attn(d1, q1, kc, vc, c.ks, c.vs, shared, table_out, last, out1, ws1, lse=lse1)
+    getattr(qsa, attend)(d1, q1, kc, vc, c.ks, c.vs, shared, table_out, last, out1, ws1, lse=lse1)
     _ok(qsa, ws)
     _ok(qsa, ws1)
 
