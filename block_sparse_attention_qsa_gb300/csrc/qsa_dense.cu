@@ -48,8 +48,9 @@ static cudaError_t launch_dense(int rows, const qsa_dims& d, const DenseArgs& a,
 // kRun in qsa_dense_tc.cuh).
 constexpr int kMaxPart = 256, kWaves = 3;
 struct PrefixPlan {
-  int rows, row_tiles, units, tiles, splits;
-  size_t pieces;  // at most, for this prefix and shorter ones
+  int rows, row_tiles, units, tiles;
+  int least, splits, most;  // parts: at least, one kernel after the other, at most
+  int room;                 // what a workspace has room for
 };
 static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
   PrefixPlan p;
@@ -59,14 +60,13 @@ static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
   p.units = d.n_kv_heads * ((p.row_tiles + at_once - 1) / at_once);
   const int tile = d.head_dim == 256 ? 64 : 128;
   p.tiles = (prefix_len + tile - 1) / tile;
-  const int least = (p.tiles + kMaxPart - 1) / kMaxPart;
+  p.least = std::max(1, (p.tiles + kMaxPart - 1) / kMaxPart);
   // Parts for 1 to kWaves full waves of CTAs; a CTA's time is its tiles and
   // about as much as 4 for its beginning and its piece.
-  const int most = std::max(1, kWaves * sms / p.units);
-  p.splits = std::max(least, 1);
+  p.splits = p.least;
   long long best = 1LL << 62;
   for (int k = 1; k <= kWaves; ++k) {
-    const int s = std::min(p.tiles, std::max(least, std::max(1, k * sms / p.units)));
+    const int s = std::min(p.tiles, std::max(p.least, k * sms / p.units));
     const long long waves = ((long long)p.units * s + sms - 1) / sms;
     const long long cost = waves * ((p.tiles + s - 1) / s + 4);
     if (cost < best) {
@@ -74,7 +74,9 @@ static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
       p.splits = s;
     }
   }
-  p.pieces = (size_t)d.n_kv_heads * p.row_tiles * std::max(least, std::min(p.tiles, most));
+  p.most = std::max(p.splits, std::min(p.tiles, (sms - 1) / p.units));
+  // (never less for a longer prefix: a workspace serves shorter ones too)
+  p.room = std::max(p.least, std::min(p.tiles, std::max(1, kWaves * sms / p.units)));
   return p;
 }
 
@@ -99,7 +101,8 @@ static PrefixWs prefix_ws_layout(const qsa_dims& d, int prefix_len, int sms) {
   const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per), row = (d.head_dim + 2) * sizeof(float);
   w.whole = dense_ws(d, sms).total;
   w.parts = align_up(w.whole + units * per * row, 256);
-  w.total = align_up(w.parts + prefix_plan(d, prefix_len, sms).pieces * kPrefixRows * row, 256);
+  const PrefixPlan p = prefix_plan(d, prefix_len, sms);
+  w.total = align_up(w.parts + (size_t)d.n_kv_heads * p.row_tiles * p.room * kPrefixRows * row, 256);
   return w;
 }
 size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms) {
@@ -112,6 +115,22 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, DenseArgs a, int rows, 
   const PrefixPlan plan = prefix_plan(d, a.prefix_len, a.grid);
   a.whole = reinterpret_cast<float*>(ws + w.whole);
   a.row_blocks = (a.n_q * a.group + rows - 1) / rows;
+  // What a tile takes a CTA, measured (head dim 128): of the own positions 1.25 us
+  // for 64 KB on 40 SMs, and about as much for 32 KB; of the prefix, two row
+  // tiles, 1.5 us with a BF16 cache and 2.3 with E4M3. A CTA's beginning and end
+  // take the first kernel 9 us, the second 15.
+  const int eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2, bytes = 256 * d.head_dim * eb;
+  SharedCost& c = a.shared;
+  c.units = plan.units;
+  c.tiles = plan.tiles;
+  c.least = plan.least;
+  c.most = std::min(plan.most, 254);
+  c.parts = plan.splits;
+  c.own_ns = std::max(bytes / 52, 1150);
+  c.own_hbm_ns = bytes / 6800;
+  c.part_ns = (d.head_dim == 64 ? 1000 : 1500) * (eb == 1 ? 3 : 2) / 2;
+  c.own_begin_ns = 9000;
+  c.part_begin_ns = 15000;
   cudaError_t e = launch_dense(rows, d, a, k_cache, v_cache, false, s);
   if (e != cudaSuccess) return e;
   PrefixArgs p = {};
@@ -120,8 +139,8 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, DenseArgs a, int rows, 
   p.rows = plan.rows;
   p.row_tiles = plan.row_tiles;
   p.units = plan.units;
-  p.splits = plan.splits;
-  p.tiles = plan.tiles;
+  p.room = plan.room;
+  p.most = plan.most;
   p.own_rows = rows;
   switch (d.head_dim) {
     case 64: return launch_prefix_64(d, p, k_cache, v_cache, s);

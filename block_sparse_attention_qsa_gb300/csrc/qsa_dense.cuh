@@ -36,6 +36,16 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxSmem = 232448;  // 227 KB a CTA
 constexpr long long kWaitCycles = 1LL << 31;  // bound of every wait: about one second
 
+// What the host knows of the two kernels that share the GPU when a prefix is read
+// once (shared_plan): CTAs of a part of the prefix, its tiles, the fewest and
+// most parts, and the parts if the kernels run one after the other; what a tile
+// takes a CTA of either kernel, one of the own positions its HBM, and a CTA's
+// beginning and end (ns).
+struct SharedCost {
+  int units, tiles, least, most, parts;
+  int own_ns, own_hbm_ns, part_ns, own_begin_ns, part_begin_ns;
+};
+
 struct DenseArgs {
   const __nv_bfloat16* q;
   const float* k_scale;
@@ -53,6 +63,7 @@ struct DenseArgs {
   int page_size, page_shift, max_pages, num_pages, window, grid;
   int prefix_len;  // whole pages
   int shared_len;  // prefix_len, or 0: every request is worked on by itself, its prefix too
+  SharedCost shared;
   float sm_scale;
   float one;  // 1
 };
@@ -156,6 +167,10 @@ __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
   return g.hi > g.lo ? g : Range{0, 0};
 }
 
+// With more requests than this the main kernel writes unit descriptors; with
+// fewer the joining kernel works them out itself while it waits.
+constexpr int kJoinScan = 256;
+
 // quotient of non-negative numbers; most streams fit the 32-bit division
 __device__ __forceinline__ long long quot(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
@@ -176,6 +191,36 @@ constexpr int kSegCost = 3;
 // unit of each.
 __device__ __forceinline__ long long load_of(int tiles) { return tiles > 0 ? (1LL << 40) + tiles : 0; }
 
+// How the GPU is divided when a prefix is read once: `own` CTAs for the requests'
+// own positions, and the prefix in `parts` parts, a CTA each a unit. The first
+// kernel is bound by HBM and the second by the tensor cores, so the two run side
+// by side on SMs of their own where that ends earlier than one after the other,
+// each on all. The host does not know the lengths; every CTA of either kernel,
+// and the joining one, comes to the same division from q_pos. (A whole warp;
+// tiles: of all units of the own positions. Many requests: one after the other,
+// which takes no pass over q_pos.)
+struct SharedPlan {
+  int own, parts;
+};
+__device__ __forceinline__ SharedPlan shared_plan(const DenseArgs& a, long long tiles) {
+  const SharedCost& c = a.shared;
+  if (a.batch > kJoinScan) return SharedPlan{a.grid, c.parts};
+  const unsigned own = (unsigned)min(tiles, 1LL << 20), lane = threadIdx.x & 31;  // (products below 2^32)
+  auto own_time = [&](unsigned ctas) {
+    return own == 0 ? 0u : c.own_begin_ns + max(own * (unsigned)c.own_ns / ctas, own * (unsigned)c.own_hbm_ns);
+  };
+  auto part_time = [&](unsigned parts) { return c.part_begin_ns + (c.tiles + parts - 1) / parts * c.part_ns; };
+  // (time << 8 | parts), or parts 255: one after the other
+  const unsigned long long waves = ((unsigned long long)c.units * c.parts + a.grid - 1) / a.grid;
+  unsigned long long best = (own_time(a.grid) + waves * part_time(c.parts)) << 8 | 255u;
+  for (unsigned p = c.least + lane; p <= (unsigned)c.most && p * c.units < (unsigned)a.grid; p += 32)
+    best = min(best, (unsigned long long)max(own_time(a.grid - p * c.units), part_time(p)) << 8 | p);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(kFull, best, o));
+  const int parts = (int)(best & 255u);
+  return parts == 255 ? SharedPlan{a.grid, c.parts} : SharedPlan{a.grid - parts * c.units, parts};
+}
+
 struct Split {
   long long q;
   int ctas, rem, seg;
@@ -185,13 +230,14 @@ struct Split {
   __device__ __forceinline__ void init(const DenseArgs& a, long long load) {
     const int units = a.n_kv_heads * a.row_blocks;
     const long long tiles = (load & ((1LL << 40) - 1)) * units;
-    seg = tiles > a.grid ? kSegCost : 0;
+    const int grid = a.shared_len > 0 ? shared_plan(a, tiles).own : a.grid;
+    seg = tiles > grid ? kSegCost : 0;
     const long long all = slots(load) * units;
     // shares of kSegCost + 1 slots, or one less where that does not divide: such
     // a one may hold no tile (Walk::cut)
     static_assert(((kSegCost + 1) & kSegCost) == 0, "a division by a power of two");
     const long long most = seg ? (all + kSegCost) / (kSegCost + 1) : all;
-    ctas = (int)min((long long)a.grid, most);
+    ctas = (int)min((long long)grid, most);
     q = ctas > 0 ? quot(all, ctas) : 0;
     rem = (int)(all - q * ctas);
   }
@@ -260,10 +306,6 @@ struct Walk {
     return cut(sh);
   }
 };
-
-// With more requests than this the main kernel writes unit descriptors; with
-// fewer the joining kernel works them out itself while it waits.
-constexpr int kJoinScan = 256;
 
 // Positions that are none are reported once, by block 0.
 __device__ __forceinline__ void report_positions(const DenseArgs& a, int r) {

@@ -34,14 +34,14 @@
 // component is off by at most 2^-25, that is 2^-39 of the row's largest.
 //
 // A unit is a KV head and a group of row tiles; the prefix's tiles of every
-// unit are cut into the same number of equal parts, one CTA each, chosen on the
-// host so that the last wave of CTAs is full (plan). A CTA leaves (reference,
-// sum, acc) of its rows in the workspace; a last kernel joins them with the
-// pieces of the requests' own positions, in the order of the positions.
+// unit are cut into the same number of equal parts, one CTA each. A CTA leaves
+// (reference, sum, acc) of its rows in the workspace; a last kernel joins them
+// with the pieces of the requests' own positions, in the order of the positions.
 //
 // The chain: own positions, prefix, joint, each launched while the one before
-// runs out. The prefix kernel reads nothing that the first writes, so it does
-// not wait for it before its work, only before its end.
+// runs. The prefix kernel reads nothing that the first writes, so it does not
+// wait for it before its work, only before its end; and the first one leaves it
+// SMs of its own (shared_plan in qsa_dense.cuh).
 #pragma once
 
 #include "qsa_serve_internal.cuh"
@@ -53,11 +53,12 @@ constexpr int kPrefixRows = 128;  // of a row tile
 
 struct PrefixArgs {
   DenseArgs a;
-  float* parts;    // [KV head][row tile][split] pieces: m[128], l[128], acc[128][D]
+  float* parts;    // [KV head][row tile][part] pieces: m[128], l[128], acc[128][D]
   int rows;        // of a KV head
   int row_tiles;   // of a KV head
   int units;       // KV heads x groups of row tiles
-  int splits, tiles;
+  int most;        // parts at most
+  int room;        // parts there is room for
   int own_rows;    // of a unit of the requests' own positions
 };
 
@@ -80,8 +81,13 @@ struct Pc {
   static constexpr int kStageLine = D < 128 ? D : 128, kStageLines = D / kStageLine;
   static constexpr int kStatic = 2048;
   static constexpr int kRoom = kMaxSmem - kStatic - 1024 - NT * kQ;
-  static constexpr int kSlots = FP8 ? 4 : (kRoom / kSlot < 8 ? kRoom / kSlot : 8);
-  static constexpr int kStages = FP8 ? ((kRoom - 4 * kSlot) / kStage < 8 ? (kRoom - 4 * kSlot) / kStage : 8) : 1;
+  // E4M3: what the products read is there soon after the copies have landed, so
+  // the room is for copies on their way (four tiles of codes and three of FP16 at
+  // head dim 128: 84 us at batch 32, two and four 93)
+  static constexpr int kFit = kRoom / kSlot < 8 ? kRoom / kSlot : 8;
+  static constexpr int kSlots = FP8 ? (kFit < 8 ? 3 : 4) : kFit;
+  static constexpr int kLeft = (kRoom - kSlots * kSlot) / kStage;
+  static constexpr int kStages = FP8 ? (kLeft < 8 ? kLeft : 8) : 1;
   static constexpr int kUsed = NT * kQ + kSlots * kSlot + (FP8 ? kStages * kStage : 0);
   static constexpr int kOutPitch = D + 4;       // floats of a row on its way out
   static constexpr int kOut = NT * 128 * kOutPitch * 4;
@@ -98,6 +104,11 @@ struct Pc {
   static constexpr int kOtherRegs = kThreads == 512 ? 72 : FP8 ? 136 : 72;
   static constexpr bool kSplit = kThreads > 256;
   static_assert(!kSplit || NT * kSoftRegs + (kThreads / 128 - NT) * kOtherRegs <= kThreads / 128 * kRegs, "registers");
+  // query rows on their way: kLanes threads a row, 16 bytes each, kPass rows a pass
+  static constexpr int kLanes = D / 8, kPass = 128 / kLanes, kPasses = 128 / kPass;
+  static __device__ __forceinline__ int q_at(int x, int r, int c) {  // byte of 16-byte chunk c of row r of row tile x
+    return x * kQ + c / 8 * (128 * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+  }
   static constexpr uint32_t kO = 2 * T;         // tensor memory: two S buffers (P where S was), then O
   static constexpr uint32_t kNeed = kO + NT * D;
   static constexpr uint32_t kTmem = kNeed <= 256 ? 256 : 512;
@@ -107,7 +118,7 @@ struct Pc {
   // fewer and their tiles more, half of the warps' tiles began with a move.)
   static constexpr float kMost = FP8 ? 13.f : 20.f, kLimit = FP8 ? 15.f : 24.f;
   static constexpr int kPieceFloats = kPrefixRows * (D + 2);
-  static_assert(kSlots >= 4 && kStages >= 1 && kNeed <= 512 && kSmem + kStatic <= kMaxSmem, "memory");
+  static_assert(kSlots >= 3 && kStages >= 1 && kNeed <= 512 && kSmem + kStatic <= kMaxSmem, "memory");
 };
 constexpr int kBadTiles = 16;      // page marks of the tiles in flight
 constexpr float kBelow = 6.f;  // log2 of a row's first largest weight
@@ -130,6 +141,17 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   } else {
     return pack_bf(lo, hi);
   }
+}
+
+// Tiles of the requests' own positions, a unit of each; a whole warp.
+__device__ __forceinline__ long long own_tiles(const DenseArgs& a) {
+  int all = 0;
+  for (int q = threadIdx.x & 31; q < a.batch; q += 32) all += min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
+  return __reduce_add_sync(kFull, all);
+}
+// parts of the prefix in this call
+__device__ __forceinline__ int prefix_parts(const DenseArgs& a) {
+  return a.batch > kJoinScan ? a.shared.parts : shared_plan(a, own_tiles(a) * (a.n_kv_heads * a.row_blocks)).parts;
 }
 
 template <class C>
@@ -155,8 +177,35 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   // the CTA's unit and its part of the prefix (CTAs of one part are neighbours: they read the same K and V)
   const int split = blockIdx.x / pa.units, unit = blockIdx.x - split * pa.units;
   const int groups = (pa.row_tiles + NT - 1) / NT, g = unit / groups, rt0 = (unit - g * groups) * NT;
-  const int t0 = (int)((long long)split * pa.tiles / pa.splits);
-  const int n = (int)((long long)(split + 1) * pa.tiles / pa.splits) - t0;
+  if (tid < C::kSoft) {
+    // the query rows on their way, before anything that has to be waited for
+    const int x = tid >> 7, t = tid & 127, c = t % C::kLanes;
+    const int step_j = C::kPass / a.group, step_h = C::kPass - step_j * a.group;
+    int row = (rt0 + x) * 128 + t / C::kLanes, rj = row / a.group, hg = row - rj * a.group;
+#pragma unroll 4
+    for (int z = 0; z < C::kPasses; ++z) {
+      const bool live = row < pa.rows;  // (behind the last: zeros)
+      const void* src = live ? a.q + ((size_t)rj * a.n_q_heads + g * a.group + hg) * D + c * 8 : a.q;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(s_q + C::q_at(x, z * C::kPass + t / C::kLanes, c))),
+                   "l"(src), "r"(live ? 16 : 0)
+                   : "memory");
+      row += C::kPass;
+      rj += step_j;
+      hg += step_h;
+      if (hg >= a.group) {
+        hg -= a.group;
+        ++rj;
+      }
+    }
+  }
+  const int parts = prefix_parts(a);
+  if (split >= parts) {  // (part 0 always has CTAs: the kernel's end is theirs)
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  const int t0 = (int)((long long)split * a.shared.tiles / parts);
+  const int n = (int)((long long)(split + 1) * a.shared.tiles / parts) - t0;
 
   if (tid == 0) {
     s_abort = 0;
@@ -373,68 +422,46 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     const int x = NT == 2 ? warp >> 2 : 0, t = tid & 127, rt = rt0 + x;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float base_scale = a.sm_scale * kLog2e * (FP8 ? fabsf(a.k_scale[g]) : 1.f);
-    {
-      // 8 components a lane, kPass rows a pass; 16 passes' loads in flight
-      constexpr int kLanes = D / 8, kPass = 128 / kLanes, kPasses = 128 / kPass, kDeep = kPasses < 16 ? kPasses : 16;
-      uint8_t* dst = s_q + x * C::kQ;
-      const int c = t % kLanes, step_j = kPass / a.group, step_h = kPass - step_j * a.group;
-      int row = rt * 128 + t / kLanes, rj = row / a.group, hg = row - rj * a.group;
-      const float sign = FP8 && a.k_scale[g] < 0.f ? -1.f : 1.f;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (FP8) {  // in place: a thread's own 16 bytes of 16 rows at a time, the rows' shuffles side by side
+      const float sign = a.k_scale[g] < 0.f ? -1.f : 1.f;
+      constexpr int kDeep = C::kPasses < 16 ? C::kPasses : 16;
 #pragma unroll 1
-      for (int z0 = 0; z0 < kPasses; z0 += kDeep) {
+      for (int z0 = 0; z0 < C::kPasses; z0 += kDeep) {
         uint4 w[kDeep];
-        uint32_t bigs[FP8 ? kDeep : 1];
+        uint32_t bigs[kDeep];
 #pragma unroll
         for (int z = 0; z < kDeep; ++z) {
-          w[z] = make_uint4(0, 0, 0, 0);
-          if (row < pa.rows) w[z] = ld16(a.q + ((size_t)rj * a.n_q_heads + g * a.group + hg) * D + c * 8);
-          row += kPass;
-          rj += step_j;
-          hg += step_h;
-          if (hg >= a.group) {
-            hg -= a.group;
-            ++rj;
-          }
+          w[z] = *reinterpret_cast<const uint4*>(s_q + C::q_at(x, (z0 + z) * C::kPass + t / C::kLanes, t % C::kLanes));
+          const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
+          bigs[z] = 0;  // magnitudes of BF16 values order like their bit patterns
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bigs[z] = max(bigs[z], max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
         }
+#pragma unroll
+        for (int o = 1; o < C::kLanes; o <<= 1)
+#pragma unroll
+          for (int z = 0; z < kDeep; ++z) bigs[z] = max(bigs[z], __shfl_xor_sync(kFull, bigs[z], o));
 #pragma unroll
         for (int z = 0; z < kDeep; ++z) {
-          if constexpr (FP8) {  // magnitudes of BF16 values order like their bit patterns
-            const uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
-            bigs[z] = 0;
+          const int r = (z0 + z) * C::kPass + t / C::kLanes, c = t % C::kLanes;
+          const uint32_t big = bigs[z];
+          uint32_t wd[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
+          // 2^-sh brings the row's largest value into [2^14, 2^15)
+          const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
+          // (a row with an infinity or NaN: every component NaN, as its scores
+          // are; a negative scale of K goes into Q, so that a larger product is
+          // a larger score)
+          const float down = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : sign * pow2(-sh);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bigs[z] = max(bigs[z], max((wd[e] << 16) & 0x7fff0000u, wd[e] & 0x7fff0000u));
-          }
-        }
-        if constexpr (FP8) {  // (all rows' shuffles side by side)
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1)
-#pragma unroll
-            for (int z = 0; z < kDeep; ++z) bigs[z] = max(bigs[z], __shfl_xor_sync(kFull, bigs[z], o));
-        }
-#pragma unroll
-        for (int z = 0; z < kDeep; ++z) {
-          const int r = (z0 + z) * kPass + t / kLanes;
-          uint4 v = w[z];
-          if constexpr (FP8) {
-            uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t big = bigs[z];
-            // 2^-sh brings the row's largest value into [2^14, 2^15)
-            const int sh = big == 0 ? 0 : min(126, max(-126, (int)(big >> 23) - 127 - 14));
-            // (a row with an infinity or NaN: every component NaN, as its scores
-            // are; a negative scale of K goes into Q, so that a larger product is
-            // a larger score)
-            const float down = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : sign * pow2(-sh);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wd[e] = pack16<true>(bf_lo(wd[e]) * down, bf_hi(wd[e]) * down);
-            v = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-            if (c == 0) s_scale[x * 128 + r] = base_scale * pow2(sh);
-          }
-          *reinterpret_cast<uint4*>(dst + c / 8 * (128 * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v;
+          for (int e = 0; e < 4; ++e) wd[e] = pack16<true>(bf_lo(wd[e]) * down, bf_hi(wd[e]) * down);
+          *reinterpret_cast<uint4*>(s_q + C::q_at(x, r, c)) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+          if (c == 0) s_scale[x * 128 + r] = base_scale * pow2(sh);
         }
       }
-      async_fence();
-      mbar_arrive(smem_u32(&q_full));
     }
+    async_fence();
+    mbar_arrive(smem_u32(&q_full));
     if constexpr (FP8) {  // (a row's scale is written by another thread of its warpgroup)
       asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
     }
@@ -578,7 +605,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     tc_after();
     const float sum = l.x + l.y;
     const int row0 = rt * 128 + (warp & 3) * 32, live = min(32, pa.rows - row0);  // rows of this warp
-    float* piece = pa.parts + ((size_t)(g * pa.row_tiles + rt) * pa.splits + split) * C::kPieceFloats;
+    float* piece = pa.parts + ((size_t)(g * pa.row_tiles + rt) * pa.room + split) * C::kPieceFloats;
     float* out = reinterpret_cast<float*>(ring) + (size_t)(x * 128 + (warp & 3) * 32) * C::kOutPitch;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -594,14 +621,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
       piece[t] = sum == 0.f ? kNegInf : mu;
       piece[128 + t] = sum;
     }
-    constexpr int kVecs = D / 4;  // of a row
-    float* dst = piece + 256 + (size_t)((warp & 3) * 32) * D;
-#pragma unroll 8
-    for (int z = lane; z < 32 * kVecs; z += 32) {
-      const int r = z / kVecs, c = z % kVecs;
-      if (r < live)
-        *reinterpret_cast<uint4*>(dst + r * D + c * 4) = *reinterpret_cast<const uint4*>(out + r * C::kOutPitch + c * 4);
+    async_fence();
+    __syncwarp();
+    if (lane < live) {  // a row each, by bulk copies
+      float* dst = piece + 256 + (size_t)((warp & 3) * 32 + lane) * D;
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                   "r"(smem_u32(out + lane * C::kOutPitch)), "n"(D * 4)
+                   : "memory");
     }
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_before();
   __syncthreads();
@@ -629,6 +657,7 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
   // the request's own positions
   int c0 = 0, c1 = -1, first_slot = 0;  // pieces of CTAs c0 .. c1
   bool whole = false;
+  int parts = a.shared.parts;
   auto unpack = [&](long long desc) {
     whole = desc == kUnitWhole;
     if (desc >= 0) {
@@ -650,6 +679,7 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
       below += __shfl_xor_sync(kFull, below, o);
     }
     const int tiles = range_of(a, r).tiles(TILE);
+    parts = shared_plan(a, (all & ((1LL << 40) - 1)) * units).parts;
     if (tiles > 0) {
       Split sp;
       sp.init(a, all);
@@ -662,12 +692,12 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
 #pragma unroll
   for (int q = 0; q < kMaxNq; ++q) p[q] = q < a.n_q ? a.q_pos[(size_t)r * a.n_q + q] : -1;
   const int mine = a.q_pos[(size_t)r * a.n_q + j];
-  const int pre = sees_prefix(a, p) && valid_pos(a, mine) ? pa.splits : 0;
+  const int pre = sees_prefix(a, p) && valid_pos(a, mine) ? parts : 0;
   const float vscale = FP8 ? a.v_scale[g] : 1.f;
   pdl_wait();
   if (a.batch > kJoinScan) unpack(a.unit_desc[(long long)r * units + x]);
   const int row = rj * a.group + hg, rt = row / kPrefixRows, pre_row = row % kPrefixRows;
-  const float* pre_parts = pa.parts + (size_t)(g * pa.row_tiles + rt) * pa.splits * (kPrefixRows * (D + 2));
+  const float* pre_parts = pa.parts + (size_t)(g * pa.row_tiles + rt) * pa.room * (kPrefixRows * (D + 2));
   const int own = whole ? 1 : c1 - c0 + 1, own_piece = pa.own_rows * (D + 2);
   float m = kNegInf, l = 0.f, acc[E];
 #pragma unroll
@@ -767,7 +797,7 @@ cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k,
     });
     if (n != C::kRegs) return cudaErrorInvalidKernelImage;
   }
-  e = launch_k(prefix_kernel<C>, dim3((unsigned)a.units * a.splits), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
+  e = launch_k(prefix_kernel<C>, dim3((unsigned)a.units * a.most), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
   // 4 warps a row where rows are few; else a warp a row (2,048 rows of 20 to 25
   // pieces: 4 warps each made the whole call 6 us slower)
