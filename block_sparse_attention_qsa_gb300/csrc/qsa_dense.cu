@@ -98,7 +98,8 @@ struct PrefixWs {
 static PrefixWs prefix_ws_layout(const qsa_dims& d, int prefix_len, int sms) {
   PrefixWs w;
   const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads), per = unit_rows(d);
-  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per), row = (d.head_dim + 2) * sizeof(float);
+  const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per);
+  const size_t row = (d.head_dim + 2) * sizeof(float);
   w.whole = dense_ws(d, sms).total;
   w.parts = align_up(w.whole + units * per * row, 256);
   const PrefixPlan p = prefix_plan(d, prefix_len, sms);

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const float* w = a.weight + (long long)r * cap;
   float* w_out = a.weight_out + (long long)r * cap_out;
   int32_t* kept = a.kept + (long long)r * a.keep;
-  const unsigned left = min(n, keep), first = (unsigned)(rank * kSelThreads + tid), step = (unsigned)(ctas * kSelThreads);
+  const unsigned left = min(n, keep);
+  const unsigned first = (unsigned)(rank * kSelThreads + tid), step = (unsigned)(ctas * kSelThreads);
   for (unsigned i = left + first; i < cap_out; i += step) {
     w_out[i] = 0.f;
     if (i < keep) kept[i] = -1;
@@ -319,7 +320,8 @@ cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s) {
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(evict_select_kernel, kHeld * sizeof(float));
   if (e != cudaSuccess) return e;
-  e = launch_clusters(evict_select_kernel, dim3((unsigned)a.batch * c), dim3(kSelThreads), c, a.held * sizeof(float), s, a);
+  e = launch_clusters(evict_select_kernel, dim3((unsigned)a.batch * c), dim3(kSelThreads), c,
+                      a.held * sizeof(float), s, a);
   if (e != cudaSuccess) return e;
   const int vecs = a.row_bytes / 16, items = 2 * a.hk * vecs;
   const long long gx = (long long)a.batch * ((a.keep + kCopyTok - 1LL) / kCopyTok);  // (below 2^31: qsa_kv_evict)

@@ -57,7 +57,7 @@ struct PrefixArgs {
   int rows;        // of a KV head
   int row_tiles;   // of a KV head
   int units;       // KV heads x groups of row tiles
-  int most;        // parts at most
+  int most;        // parts at most: the grid's
   int room;        // parts there is room for
   int own_rows;    // of a unit of the requests' own positions
 };
@@ -120,7 +120,7 @@ struct Pc {
   static constexpr int kPieceFloats = kPrefixRows * (D + 2);
   static_assert(kSlots >= 3 && kStages >= 1 && kNeed <= 512 && kSmem + kStatic <= kMaxSmem, "memory");
 };
-constexpr int kBadTiles = 16;      // page marks of the tiles in flight
+constexpr int kBadTiles = 16;  // page marks of the tiles in flight
 constexpr float kBelow = 6.f;  // log2 of a row's first largest weight
 constexpr float kNone = __builtin_huge_valf();  // the reference of a row that has seen nothing
 constexpr float kHuge = 16777216.f;  // from a reference of this size on, a product less it is not fused (see less())
@@ -146,7 +146,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // Tiles of the requests' own positions, a unit of each; a whole warp.
 __device__ __forceinline__ long long own_tiles(const DenseArgs& a) {
   int all = 0;
-  for (int q = threadIdx.x & 31; q < a.batch; q += 32) all += min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
+  for (int q = threadIdx.x & 31; q < a.batch; q += 32)
+    all += min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
   return __reduce_add_sync(kFull, all);
 }
 // parts of the prefix in this call
@@ -167,8 +168,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   uint8_t* stage = s_q + NT * C::kQ;
   __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
   __shared__ __align__(8) uint64_t stage_full[C::kStages], stage_empty[C::kStages];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2], q_full, turn[2], fin[2];  // p_full: [half][buffer]
+  __shared__ __align__(8) uint64_t s_full[2], pv_half[2], pv_done[2], q_full, turn[2], fin[2];
+  __shared__ __align__(8) uint64_t p_full[2][2];  // [half][buffer]
   __shared__ uint32_t s_tmem;
+  __shared__ int s_parts;
   __shared__ uint32_t s_bad[kBadTiles];  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
   __shared__ volatile int s_abort;
   __shared__ float s_scale[C::kSoft];    // E4M3: a row's softmax scale
@@ -199,14 +202,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
       }
     }
   }
-  const int parts = prefix_parts(a);
-  if (split >= parts) {  // (part 0 always has CTAs: the kernel's end is theirs)
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    return;
-  }
-  const int t0 = (int)((long long)split * a.shared.tiles / parts);
-  const int n = (int)((long long)(split + 1) * a.shared.tiles / parts) - t0;
-
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < C::kSlots; ++s) {
@@ -235,6 +230,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (warp == C::kCopyWarp) {
+    const int parts = prefix_parts(a);
+    if (lane == 0) s_parts = parts;
+  }
   // (The kernel in front, the own positions', was launched by the same call;
   // its CTAs let this one start behind their own wait, so all that this kernel
   // reads is older, and what it writes is read by nothing that still runs.)
@@ -243,9 +242,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   __syncthreads();
   tc_after();
   const uint32_t tmem = s_tmem;
+  const int parts = s_parts;
+  const bool spare = split >= parts;  // (part 0 always has CTAs: the kernel's end is theirs)
+  const int t0 = (int)((long long)split * a.shared.tiles / parts);
+  const int n = spare ? 0 : (int)((long long)(split + 1) * a.shared.tiles / parts) - t0;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
-  if (tid >= C::kSoft + C::kWiden) {
+  if (spare) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (tid >= C::kSoft + C::kWiden) {
     if constexpr (C::kSplit) fewer_regs<C::kOtherRegs>();  // (a whole warpgroup, two warps of which have no work)
     if (warp == C::kCopyWarp) {
       // ---- copies: K then V of each tile ----
@@ -355,8 +360,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
 #pragma unroll
           for (int ks = h * (T / 32); ks < (h + 1) * (T / 32); ++ks)
             if (one)
-              mma_ts(tmem + C::kO + (uint32_t)(x * D), tmem + (uint32_t)(b * T + ks * 8), dv + (uint32_t)(ks * 128), kDescO,
-                     i > 0 || ks > 0);
+              mma_ts(tmem + C::kO + (uint32_t)(x * D), tmem + (uint32_t)(b * T + ks * 8), dv + (uint32_t)(ks * 128),
+                     kDescO, i > 0 || ks > 0);
           if (one && h == 0) commit_tc(&pv_half[b]);
         }
         if (!ok) break;
@@ -397,9 +402,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
       for (int z = w; z < T / 8 * kLines; z += 4) {
         const int r = z / kLines * 8 + r8, ln = z % kLines, c = ln * 4 + c4;  // 16 codes: chunk c of the row
         const int sw = kChunks8 == 8 ? (c % 8) ^ (r & 7) : (c % 4) ^ ((r >> 1) & 3);
-        const uint4 x = *reinterpret_cast<const uint4*>(src + c / kChunks8 * (T * C::kStageLine) + r * C::kStageLine + sw * 16);
-        const uint4 lo = make_uint4(e4m3x2_to_h2(x.x), e4m3x2_to_h2(x.x >> 16), e4m3x2_to_h2(x.y), e4m3x2_to_h2(x.y >> 16));
-        const uint4 hi = make_uint4(e4m3x2_to_h2(x.z), e4m3x2_to_h2(x.z >> 16), e4m3x2_to_h2(x.w), e4m3x2_to_h2(x.w >> 16));
+        const uint8_t* from = src + c / kChunks8 * (T * C::kStageLine) + r * C::kStageLine + sw * 16;
+        const uint4 x = *reinterpret_cast<const uint4*>(from);
+        auto widen = [](uint32_t u, uint32_t v) {
+          return make_uint4(e4m3x2_to_h2(u), e4m3x2_to_h2(u >> 16), e4m3x2_to_h2(v), e4m3x2_to_h2(v >> 16));
+        };
+        const uint4 lo = widen(x.x, x.y), hi = widen(x.z, x.w);
         uint8_t* row = dst + ln * (T * 128) + r * 128;
         *reinterpret_cast<uint4*>(row + (((2 * c4 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
         *reinterpret_cast<uint4*>(row + (((2 * c4 + 1 - flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
@@ -423,9 +431,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float base_scale = a.sm_scale * kLog2e * (FP8 ? fabsf(a.k_scale[g]) : 1.f);
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if constexpr (FP8) {  // in place: a thread's own 16 bytes of 16 rows at a time, the rows' shuffles side by side
+    if constexpr (FP8) {  // in place: a thread's own 16 bytes of kDeep rows at a time, the rows' shuffles side by side
       const float sign = a.k_scale[g] < 0.f ? -1.f : 1.f;
-      constexpr int kDeep = C::kPasses < 16 ? C::kPasses : 16;
+      constexpr int kDeep = 4;  // (16: its code, read once, took 1.5 us longer)
 #pragma unroll 1
       for (int z0 = 0; z0 < C::kPasses; z0 += kDeep) {
         uint4 w[kDeep];
@@ -466,7 +474,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
       asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
     }
     float sc = FP8 ? s_scale[x * 128 + t] : base_scale;
-    if (FP8 && sc == 0.f) sc = 0x1p-126f;  // (every score is about 0; a product with an absent position's -inf is no NaN)
+    // (every score is about 0 then; a product with an absent position's -inf is no NaN)
+    if (FP8 && sc == 0.f) sc = 0x1p-126f;
     float mu = kNone, pending = 0.f;  // pending: how far the tile before went past the reference
     float2 l = make_float2(0.f, 0.f);
     const uint32_t o_addr = tmem + lane_base + C::kO + (uint32_t)(x * D);
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   tc_after();
   if (warp == C::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
-  pdl_wait();  // this kernel's end stands for the own positions' too
+  if (!spare) pdl_wait();  // this kernel's end stands for the own positions' too
 }
 
 // Joins the pieces of a row: the prefix's parts, then those of the request's own
@@ -804,8 +813,8 @@ cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k,
   const unsigned rows = (unsigned)(a.a.batch * a.a.n_q * a.a.n_q_heads);
   if (rows < 8u * a.a.grid)
     return launch_k(prefix_join_kernel<D, FP8, 4>, dim3(rows), dim3(128), 0, s, true, a);
-  return launch_k(prefix_join_kernel<D, FP8, 1>, dim3((rows + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinRows), 0, s, true,
-                  a);
+  return launch_k(prefix_join_kernel<D, FP8, 1>, dim3((rows + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinRows), 0, s,
+                  true, a);
 }
 
 }  // namespace

@@ -9,10 +9,10 @@ namespace {
 
 bool needs_scales(const qsa_dims& d) { return d.kv_dtype == QSA_KV_FP8_E4M3; }
 
-qsa_status prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages, const int32_t* prefix_table, const void* q,
-                       const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
-                       const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
-                       size_t ws_bytes, void* stream) {
+qsa_status prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages, const int32_t* prefix_table,
+                       const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, const int32_t* page_table, const int32_t* q_pos, void* out, float* lse,
+                       void* ws, size_t ws_bytes, void* stream) {
   const qsa_status st = check_kv_dims(dims);
   if (st != QSA_OK) return st;
   if (prefix_pages < 0 || prefix_pages > dims->max_pages || (prefix_pages > 0 && !prefix_table))
@@ -46,8 +46,8 @@ qsa_status qsa_prefix_attn(const qsa_dims* dims, int32_t prefix_pages, const int
                            const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                            const int32_t* page_table, const int32_t* q_pos, void* out, float* lse, void* ws,
                            size_t ws_bytes, void* stream) {
-  return prefix_attn(dims, -1, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out,
-                     lse, ws, ws_bytes, stream);
+  return prefix_attn(dims, -1, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos,
+                     out, lse, ws, ws_bytes, stream);
 }
 
 qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages, const int32_t* prefix_table,
@@ -55,8 +55,8 @@ qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t pre
                                 const float* v_scale, const int32_t* page_table, const int32_t* q_pos, void* out,
                                 float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (alone != 0 && alone != 1) return QSA_ERR_INVALID_ARG;
-  return prefix_attn(dims, alone, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out,
-                     lse, ws, ws_bytes, stream);
+  return prefix_attn(dims, alone, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos,
+                     out, lse, ws, ws_bytes, stream);
 }
 
 qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const void* k_cache, const float* k_scale,
@@ -87,7 +87,11 @@ qsa_status qsa_kv_evict(const qsa_dims* dims, int32_t keep, int32_t sinks, int32
   if (!len || !weight || !page_table || !page_table_out || !k_cache || !v_cache || !weight_out || !kept || !new_len)
     return QSA_ERR_INVALID_ARG;
   if (!aligned_all(16, {k_cache, v_cache}) ||
-      !aligned_all(4, {len, weight, page_table, page_table_out, weight_out, kept, new_len}) || weight == weight_out)
+      !aligned_all(4, {len, weight, page_table, page_table_out, weight_out, kept, new_len}))
+    return QSA_ERR_INVALID_ARG;
+  // (a request's new weights are written while others' old ones are still read)
+  if (weight < weight_out + dims->batch * cap &&
+      weight_out < weight + (long long)dims->batch * dims->max_pages * dims->page_size)
     return QSA_ERR_INVALID_ARG;
   if (!check_header(ws, ws_bytes)) return QSA_ERR_WORKSPACE;
   EvictArgs a = {};

@@ -45,8 +45,8 @@ cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s);
 
 // launch_k with thread-block clusters of `cluster` CTAs (along x)
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem, cudaStream_t s,
-                            Args&&... args) {
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem,
+                            cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;

@@ -52,7 +52,9 @@ struct Exact {
   __device__ __forceinline__ Exact() : a1(make_float2(0.f, 0.f)), a2(a1), a3(a1) {}
   static __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
   // M - (x + M): less x's part on the grid
-  static __device__ __forceinline__ float2 part(float2 x, float m) { return fma2(add2(x, pair(m)), pair(-1.f), pair(m)); }
+  static __device__ __forceinline__ float2 part(float2 x, float m) {
+    return fma2(add2(x, pair(m)), pair(-1.f), pair(m));
+  }
   __device__ __forceinline__ void add(float2 x) {
     const float2 t1 = part(x, kM1);
     a1 = add2(a1, t1);

@@ -797,7 +797,8 @@ def prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, pa
     prefix_table.numel() * page_size of every request live in the pages that
     prefix_table (int32 [n], n may be 0) names, the others in those of the
     request's page_table row. ws is make_prefix_workspace's."""
-    st = _fast.prefix_attn(d, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, lse, ws, stream)
+    st = _fast.prefix_attn(d, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, lse, ws,
+                           stream)
     if st == OK:
         return
     if st is not None:
@@ -869,8 +870,8 @@ def kv_evict(d: Dims, k_cache, v_cache, page_table, page_table_out, length, weig
     their number to new_length (int32 [B]; it may be length), their K and V to
     the pages of page_table_out (int32 [B][n]), their weights to weight_out
     (fp32 [B][n * page_size], 0 behind the last)."""
-    st = _fast.kv_evict(d, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length, ws,
-                        sinks, recent, stream)
+    st = _fast.kv_evict(d, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length,
+                        ws, sinks, recent, stream)
     if st == OK:
         return
     if st is not None:

@@ -109,10 +109,10 @@ qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const
  * keep is 1..out_pages * page_size, sinks and recent at least 0 with sinks +
  * recent <= keep. weight is fp32 [batch][max_pages * page_size], weight_out
  * fp32 [batch][out_pages * page_size] (they must not overlap), kept int32
- * [batch][keep], new_len int32 [batch] (it may be len). A length below 0 or
- * past the page table is reported (kind 8) and taken as 0, a page id outside
- * the cache is reported (kind 2) and its tokens are not copied. ws needs 256
- * bytes (its header). */
+ * [batch][keep], new_len int32 [batch] (it may be len); no other output may
+ * overlap an input. A length below 0 or past the page table is reported (kind
+ * 8) and taken as 0, a page id outside the cache is reported (kind 2) and its
+ * tokens are not copied. ws needs 256 bytes (its header). */
 qsa_status qsa_kv_evict(const qsa_dims* dims, int32_t keep, int32_t sinks, int32_t recent, int32_t out_pages,
                         const int32_t* len, const float* weight, const int32_t* page_table,
                         const int32_t* page_table_out, void* k_cache, void* v_cache, float* weight_out, int32_t* kept,
@@ -159,9 +159,9 @@ typedef struct {
  *
  * target and draft are fp32 or bf16 (prob_dtype), tokens int32
  * [batch][n_draft], uniform fp32 [batch][n_draft + 1], accepted int32 [batch],
- * out_tokens int32 [batch][n_draft + 1]. n_draft is 1..QSA_MAX_DRAFTS, vocab
- * 1..QSA_MAX_VOCAB, batch 1..2^22. ws needs 256 bytes (its header): any
- * workspace of the library. */
+ * out_tokens int32 [batch][n_draft + 1], neither of which may overlap an input.
+ * n_draft is 1..QSA_MAX_DRAFTS, vocab 1..QSA_MAX_VOCAB, batch 1..2^22. ws needs
+ * 256 bytes (its header): any workspace of the library. */
 qsa_status qsa_verify_drafts(int32_t batch, int32_t n_draft, int32_t vocab, int32_t prob_dtype, const void* target,
                              const qsa_prob_strides* target_strides, const void* draft,
                              const qsa_prob_strides* draft_strides, const int32_t* tokens, const float* uniform,

@@ -964,6 +964,12 @@ def test_evict_refusals(qsa):
     same = torch.zeros((2, c.weight.shape[1]), device="cuda")
     table = torch.zeros((2, same.shape[1] // 64), dtype=torch.int32, device="cuda")
     call(qsa.QSAError, "INVALID_ARG", weight=same, weight_out=same, page_table_out=table)
+    both = torch.full((2 * same.numel() - 1,), 7.0, device="cuda")  # the last element of one is the first of the other
+    call(qsa.QSAError, "INVALID_ARG", weight=both[:same.numel()].view_as(same),
+         weight_out=both[same.numel() - 1:].view_as(same), page_table_out=table)
+    call(qsa.QSAError, "INVALID_ARG", weight_out=both[:same.numel()].view_as(same),
+         weight=both[same.numel() - 1:].view_as(same), page_table_out=table)
+    assert (both == 7).all()
     _ok(qsa, c.ws)
     assert (c.kept == 7).all() and (c.weight_out == 7).all()
 
