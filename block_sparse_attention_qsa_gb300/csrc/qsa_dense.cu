@@ -34,8 +34,9 @@ DenseWs dense_ws(const qsa_dims& d, int num_sms) {
   return w;
 }
 
-static cudaError_t launch_dense(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache,
-                                const void* v_cache, bool short_k, cudaStream_t s) {
+template <class A>
+static cudaError_t launch_dense(int rows, const qsa_dims& d, const A& a, const void* k_cache, const void* v_cache,
+                                bool short_k, cudaStream_t s) {
   switch (d.head_dim) {
     case 64: return launch_dense_64(rows, d, a, k_cache, v_cache, short_k, s);
     case 128: return launch_dense_128(rows, d, a, k_cache, v_cache, short_k, s);
@@ -110,7 +111,7 @@ size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms) {
   return prefix_len > 0 ? prefix_ws_layout(d, prefix_len, num_sms).total : dense_ws(d, num_sms).total;
 }
 
-static cudaError_t launch_with_prefix(const qsa_dims& d, DenseArgs a, int rows, uint8_t* ws, const void* k_cache,
+static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows, uint8_t* ws, const void* k_cache,
                                       const void* v_cache, cudaStream_t s) {
   const PrefixWs w = prefix_ws_layout(d, a.prefix_len, a.grid);
   const PrefixPlan plan = prefix_plan(d, a.prefix_len, a.grid);
@@ -121,7 +122,7 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, DenseArgs a, int rows, 
   // tiles, 1.5 us with a BF16 cache and 2.3 with E4M3. A CTA's beginning and end
   // take the first kernel 9 us, the second 15.
   const int eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2, bytes = 256 * d.head_dim * eb;
-  SharedCost& c = a.shared;
+  SharedCost& c = a.cost;
   c.units = plan.units;
   c.tiles = plan.tiles;
   c.least = plan.least;
@@ -163,8 +164,6 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.page_table = page_table;
-  a.prefix_table = prefix.table;
-  a.prefix_len = prefix.len;
   a.q_pos = q_pos;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
@@ -185,11 +184,15 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   a.sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.f / sqrtf((float)d.head_dim);
   a.one = 1.f;
   const int rows = unit_rows(d);
-  if (prefix.len > 0 && !(prefix.alone < 0 ? alone(d, prefix.len, rows, sms) : prefix.alone)) {
-    a.shared_len = prefix.len;
-    return launch_with_prefix(d, a, rows, base, k_cache, v_cache, s);
-  }
-  return launch_dense(rows, d, a, k_cache, v_cache, short_k, s);
+  if (prefix.len == 0) return launch_dense(rows, d, a, k_cache, v_cache, short_k, s);
+  SharedArgs x = {};
+  static_cast<DenseArgs&>(x) = a;
+  x.prefix_table = prefix.table;
+  x.prefix_len = prefix.len;
+  if (prefix.alone < 0 ? alone(d, prefix.len, rows, sms) : prefix.alone)
+    return launch_dense(rows, d, x, k_cache, v_cache, short_k, s);
+  x.shared_len = prefix.len;
+  return launch_with_prefix(d, x, rows, base, k_cache, v_cache, s);
 }
 
 }  // namespace qsa

@@ -51,21 +51,28 @@ struct DenseArgs {
   const float* k_scale;
   const float* v_scale;
   const int32_t* page_table;
-  const int32_t* prefix_table;  // the pages of positions below prefix_len, which all requests share
   const int32_t* q_pos;
   __nv_bfloat16* out;
   float* lse;
   long long* unit_desc;  // where each unit's pieces are (see unit_* below); null: the stream has no pieces
   float* parts;          // [grid][2] pieces: m[rows], l[rows], acc[rows][D]
-  float* whole;          // with a shared prefix: [unit] the pieces of units that are one CTA's
   int32_t* err;
   int batch, n_q, n_q_heads, n_kv_heads, group, row_blocks;
   int page_size, page_shift, max_pages, num_pages, window, grid;
-  int prefix_len;  // whole pages
-  int shared_len;  // prefix_len, or 0: every request is worked on by itself, its prefix too
-  SharedCost shared;
   float sm_scale;
   float one;  // 1
+  static constexpr bool kShared = false;
+};
+// With a prefix that all requests share. (Kernels of their own: what the prefix
+// adds made the others 1 to 6 % slower, one request of 50,004 tokens 18.4 us ->
+// 19.5.)
+struct SharedArgs : DenseArgs {
+  const int32_t* prefix_table;  // the pages of positions below prefix_len
+  float* whole;                 // [unit] the pieces of units that are one CTA's
+  int prefix_len;               // whole pages
+  int shared_len;  // prefix_len, or 0: every request is worked on by itself, its prefix too
+  SharedCost cost;
+  static constexpr bool kShared = true;
 };
 
 // Unit descriptors: written whole, without positions, or the pieces of CTAs
@@ -146,13 +153,14 @@ __device__ __forceinline__ int low_of(const DenseArgs& a, int p) {
 // the prefix is left to the kernel that takes it for all requests
 // (qsa_prefix.cuh), and the request's unit is what lies behind it; else the
 // request is worked on by itself, from position 0. (No window in either case.)
-__device__ __forceinline__ bool sees_prefix(const DenseArgs& a, const int (&p)[kMaxNq]) {
+__device__ __forceinline__ bool sees_prefix(const SharedArgs& a, const int (&p)[kMaxNq]) {
   bool all = true;
 #pragma unroll
   for (int j = 0; j < kMaxNq; ++j) all &= !valid_pos(a, p[j]) || p[j] >= a.shared_len - 1;
   return all;
 }
-__device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
+template <class A>
+__device__ __forceinline__ Range range_of(const A& a, int r) {
   int p[kMaxNq];
 #pragma unroll
   for (int j = 0; j < kMaxNq; ++j) p[j] = j < a.n_q ? a.q_pos[(size_t)r * a.n_q + j] : -1;
@@ -163,8 +171,19 @@ __device__ __forceinline__ Range range_of(const DenseArgs& a, int r) {
     g.lo = min(g.lo, low_of(a, p[j]));
     g.hi = max(g.hi, p[j] + 1);
   }
-  if (a.shared_len > 0 && sees_prefix(a, p)) g.lo = a.shared_len;
+  if constexpr (A::kShared) {
+    if (a.shared_len > 0 && sees_prefix(a, p)) g.lo = a.shared_len;
+  }
   return g.hi > g.lo ? g : Range{0, 0};
+}
+
+// The first position that a query at p sees, in a unit whose positions are g.
+template <class A>
+__device__ __forceinline__ int first_seen(const A& a, const Range& g, int p) {
+  if constexpr (A::kShared) {
+    if (a.shared_len > 0) return g.lo;
+  }
+  return low_of(a, p);
 }
 
 // With more requests than this the main kernel writes unit descriptors; with
@@ -202,8 +221,8 @@ __device__ __forceinline__ long long load_of(int tiles) { return tiles > 0 ? (1L
 struct SharedPlan {
   int own, parts;
 };
-__device__ __forceinline__ SharedPlan shared_plan(const DenseArgs& a, long long tiles) {
-  const SharedCost& c = a.shared;
+__device__ __forceinline__ SharedPlan shared_plan(const SharedArgs& a, long long tiles) {
+  const SharedCost& c = a.cost;
   if (a.batch > kJoinScan) return SharedPlan{a.grid, c.parts};
   const unsigned own = (unsigned)min(tiles, 1LL << 20), lane = threadIdx.x & 31;  // (products below 2^32)
   auto own_time = [&](unsigned ctas) {
@@ -227,10 +246,14 @@ struct Split {
   __device__ __forceinline__ long long slots(long long load) const {
     return (load & ((1LL << 40) - 1)) + (load >> 40) * seg;
   }
-  __device__ __forceinline__ void init(const DenseArgs& a, long long load) {
+  template <class A>
+  __device__ __forceinline__ void init(const A& a, long long load) {
     const int units = a.n_kv_heads * a.row_blocks;
     const long long tiles = (load & ((1LL << 40) - 1)) * units;
-    const int grid = a.shared_len > 0 ? shared_plan(a, tiles).own : a.grid;
+    int grid = a.grid;
+    if constexpr (A::kShared) {
+      if (a.shared_len > 0) grid = shared_plan(a, tiles).own;
+    }
     seg = tiles > grid ? kSegCost : 0;
     const long long all = slots(load) * units;
     // shares of kSegCost + 1 slots, or one less where that does not divide: such
@@ -283,7 +306,8 @@ struct Walk {
   // time, a lane each: one after the other, 262,144 empty ones between two took
   // 86 ms, and at 2^22 the roles that meanwhile wait for one another came near
   // the limit of their waits.)
-  __device__ __forceinline__ bool next(const DenseArgs& a, const Share& sh) {
+  template <class A>
+  __device__ __forceinline__ bool next(const A& a, const Share& sh) {
     unit += sh.split.seg + tiles;
     if (unit + sh.split.seg >= sh.w1) return false;
     if (++x == a.n_kv_heads * a.row_blocks) {
@@ -320,8 +344,8 @@ __device__ __forceinline__ void report_positions(const DenseArgs& a, int r) {
 // block's only barrier (up to 32 requests: every warp works it all out by
 // itself, a lane a request), or has several (each thread sums the tiles of a
 // contiguous run of requests, one block scan; units without a tile are marked).
-template <int TILE, int THREADS>
-__device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)[THREADS / 32], Share& sh,
+template <int TILE, int THREADS, class A>
+__device__ __forceinline__ bool find_start(const A& a, long long (&scan)[THREADS / 32], Share& sh,
                                            Walk<TILE>& at) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.n_kv_heads * a.row_blocks;  // of a request
@@ -390,7 +414,8 @@ __device__ __forceinline__ bool find_start(const DenseArgs& a, long long (&scan)
   }
   if ((int)blockIdx.x >= sp.ctas) return false;
   const long long w0 = sp.begin(blockIdx.x);
-  if (sp.slots(before) * units <= w0 && w0 < sp.slots(before + mine) * units) {  // one thread: w0 is in one of its requests
+  // one thread: w0 is in one of its requests
+  if (sp.slots(before) * units <= w0 && w0 < sp.slots(before + mine) * units) {
     sh.split = sp;
     sh.w0 = w0;
     sh.w1 = sp.begin(blockIdx.x + 1);
@@ -432,24 +457,33 @@ struct PageFeed {
     boxes = TILE >> box_shift;
     my_box = (int)(threadIdx.x & 31) & (boxes - 1);
   }
-  __device__ __forceinline__ int page_of(const DenseArgs& a, const Walk<TILE>& at, int i) const {
+  template <class A>
+  __device__ __forceinline__ int page_of(const A& a, const Walk<TILE>& at, int i) const {
     const unsigned p = (unsigned)(first_box + i) << box_shift;  // (a box that is seen starts below 2^31)
     if (i >= n_boxes || p >= (unsigned)at.g.hi || p + (1u << box_shift) <= (unsigned)at.g.lo) return -1;
-    const bool shared = p < (unsigned)a.prefix_len;
-    const int32_t* table = shared ? a.prefix_table : a.page_table + (size_t)at.r * a.max_pages;
+    const int32_t* table = a.page_table + (size_t)at.r * a.max_pages;
+    int r = at.r;
+    if constexpr (A::kShared) {
+      if (p < (unsigned)a.prefix_len) {
+        table = a.prefix_table;
+        r = -1;
+      }
+    }
     const int page = table[p >> a.page_shift];
     if ((unsigned)page < (unsigned)a.num_pages) return page;
-    record_error(a.err, kErrPage, shared ? -1 : at.r, 0, page);
+    record_error(a.err, kErrPage, r, 0, page);
     return -1;
   }
-  __device__ __forceinline__ void start(const DenseArgs& a, const Walk<TILE>& at) {
+  template <class A>
+  __device__ __forceinline__ void start(const A& a, const Walk<TILE>& at) {
     first_box = (at.g.lo / TILE + at.t) * boxes;
     n_boxes = at.n * boxes;
     cur = page_of(a, at, threadIdx.x & 31);
     nxt = page_of(a, at, 32 + (threadIdx.x & 31));
   }
   // page of this lane's box of the segment's tile k
-  __device__ __forceinline__ int of_tile(const DenseArgs& a, const Walk<TILE>& at, int k) {
+  template <class A>
+  __device__ __forceinline__ int of_tile(const A& a, const Walk<TILE>& at, int k) {
     const int b0 = k * boxes;
     if (b0 > 0 && (b0 & 31) == 0) {
       cur = nxt;
@@ -654,13 +688,20 @@ cudaError_t launch_join(const DenseArgs& a, cudaStream_t s) {
                   dim3(32 * kJoinRows), 0, s, true, a);
 }
 
-// the kernels by head dim (qsa_dense_64.cu, _128.cu, _256.cu); rows: of a unit;
-// short_k: K's copies bring half of what the kernel waits for
+// the kernels by head dim (qsa_dense_64.cu, _128.cu, _256.cu; with a shared
+// prefix qsa_shared_64.cu, _128.cu, _256.cu); rows: of a unit; short_k: K's
+// copies bring half of what the kernel waits for
 cudaError_t launch_dense_64(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
                             bool short_k, cudaStream_t s);
 cudaError_t launch_dense_128(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
                              bool short_k, cudaStream_t s);
 cudaError_t launch_dense_256(int rows, const qsa_dims& d, const DenseArgs& a, const void* k_cache, const void* v_cache,
+                             bool short_k, cudaStream_t s);
+cudaError_t launch_dense_64(int rows, const qsa_dims& d, const SharedArgs& a, const void* k_cache, const void* v_cache,
+                            bool short_k, cudaStream_t s);
+cudaError_t launch_dense_128(int rows, const qsa_dims& d, const SharedArgs& a, const void* k_cache, const void* v_cache,
+                             bool short_k, cudaStream_t s);
+cudaError_t launch_dense_256(int rows, const qsa_dims& d, const SharedArgs& a, const void* k_cache, const void* v_cache,
                              bool short_k, cudaStream_t s);
 
 }  // namespace qsa

@@ -163,10 +163,10 @@ __device__ __forceinline__ float reduce_rows(float (&v)[RC], Op op) {
 __device__ __forceinline__ float dither(int p) {
   return (float)(((int)((uint32_t)p * 0x9e3779b9u) >> 8) | 1) * 0x1p-33f;
 }
-template <class C>
+template <class C, class A>
 __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                   const __grid_constant__ CUtensorMap tm_v,
-                                                                  const DenseArgs a) {
+                                                                  const A a) {
   constexpr bool FP8 = C::FP8;
   constexpr int RC = C::RC, WGS = C::WGS, BLK = C::BLK, N = C::N, kTile = kTileTc, D = C::D, MB = C::MB;
   constexpr int kLine = C::kLine, kLines = C::kLines, kChunks = C::kChunks;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         if (row_off + t < rows) {
           const int i = rb * C::kRows + row_off + t, j = i / a.group, h = g * a.group + (i - j * a.group);
           const int p = a.q_pos[(size_t)u.r * a.n_q + j];
-          if (valid_pos(a, p)) rg = make_int2(a.shared_len > 0 ? u.g.lo : low_of(a, p), p + 1);
+          if (valid_pos(a, p)) rg = make_int2(first_seen(a, u.g, p), p + 1);
           o = (u.r * a.n_q + j) * a.n_q_heads + h;
         }
         s_rng[buf][row_off + t] = rg;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
         int2 all = make_int2(0, 0x7fffffff);
         for (int j = rb * C::kRows / a.group; j <= (rb * C::kRows + rows - 1) / a.group; ++j) {
           const int p = a.q_pos[(size_t)u.r * a.n_q + j];
-          all.x = max(all.x, !valid_pos(a, p) ? 0 : a.shared_len > 0 ? u.g.lo : low_of(a, p));
+          all.x = max(all.x, valid_pos(a, p) ? first_seen(a, u.g, p) : 0);
           all.y = min(all.y, valid_pos(a, p) ? p + 1 : 0);
         }
         s_all[buf] = all;
@@ -737,7 +737,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       last = n == at.n;
       const int start = at.start(s_share);
       const bool whole = start == 0 && at.t + at.n == at.tiles, more = at.t > start;
-      const bool done = whole && last && a.shared_len == 0;  // (with a shared prefix a whole unit is a piece too)
+      bool apart = false;  // with a shared prefix a whole unit is a piece too
+      if constexpr (A::kShared) apart = a.shared_len > 0;
+      const bool done = whole && last && !apart;
       const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
       if (a.batch > kJoinScan && tid == 0 && start == 0 && last)
         a.unit_desc[(long long)at.r * units + at.x] =
@@ -750,8 +752,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       tc_after();
       if (lane < RC) s_red[wg][quarter][lane] = part;
       group_sync(1 + wg, 128);
-      float* piece = whole && a.shared_len > 0 ? a.whole + ((size_t)at.r * units + at.x) * C::kPieceFloats
-                                               : a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
+      float* piece = a.parts + ((size_t)blockIdx.x * 2 + pslot) * C::kPieceFloats;
+      if constexpr (A::kShared) {
+        if (whole && apart) piece = a.whole + ((size_t)at.r * units + at.x) * C::kPieceFloats;
+      }
       if (t < RC) {  // a row's sum, its factors, and lse
         float sum = (s_red[wg][0][t] + s_red[wg][1][t]) + (s_red[wg][2][t] + s_red[wg][3][t]);
         const float ref = s_mu[wg][t];
@@ -823,8 +827,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
   if (warp == C::kPvWarp) free_tmem();
 }
 
-template <int D, bool FP8, int RC, int WGS>
-cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const void* v_cache, bool short_k,
+template <int D, bool FP8, int RC, int WGS, class A>
+cudaError_t launch_tc(const qsa_dims& d, A a, const void* k_cache, const void* v_cache, bool short_k,
                       cudaStream_t s) {
   using C = Tc<D, FP8, RC, WGS>;
   alignas(64) CUtensorMap tk, tv;
@@ -832,17 +836,19 @@ cudaError_t launch_tc(const qsa_dims& d, DenseArgs a, const void* k_cache, const
       !make_cache_map(&tv, d, v_cache, kTileTc, C::kLine, false))
     return cudaErrorInvalidValue;
   static DeviceSlots slots;
-  cudaError_t e = slots.raise_smem(dense_tc_kernel<C>, C::kSmem);
+  cudaError_t e = slots.raise_smem(dense_tc_kernel<C, A>, C::kSmem);
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.n_q * a.group + C::kRows - 1) / C::kRows;
-  e = launch_k(dense_tc_kernel<C>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
+  e = launch_k(dense_tc_kernel<C, A>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
-  if (a.shared_len > 0) return cudaSuccess;  // (joined with the prefix's pieces)
+  if constexpr (A::kShared) {
+    if (a.shared_len > 0) return cudaSuccess;  // (joined with the prefix's pieces)
+  }
   return launch_join<D, C::kRows, FP8, kTileTc>(a, s);
 }
 
-template <int D, bool FP8>
-cudaError_t launch_tc(int rows, const qsa_dims& d, const DenseArgs& a, const void* k, const void* v, bool short_k,
+template <int D, bool FP8, class A>
+cudaError_t launch_tc(int rows, const qsa_dims& d, const A& a, const void* k, const void* v, bool short_k,
                       cudaStream_t s) {
   switch (rows) {
     case 8: return launch_tc<D, FP8, 8, 1>(d, a, k, v, short_k, s);

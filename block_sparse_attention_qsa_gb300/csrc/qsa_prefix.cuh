@@ -52,7 +52,7 @@ namespace qsa {
 constexpr int kPrefixRows = 128;  // of a row tile
 
 struct PrefixArgs {
-  DenseArgs a;
+  SharedArgs a;
   float* parts;    // [KV head][row tile][part] pieces: m[128], l[128], acc[128][D]
   int rows;        // of a KV head
   int row_tiles;   // of a KV head
@@ -144,15 +144,15 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // Tiles of the requests' own positions, a unit of each; a whole warp.
-__device__ __forceinline__ long long own_tiles(const DenseArgs& a) {
+__device__ __forceinline__ long long own_tiles(const SharedArgs& a) {
   int all = 0;
   for (int q = threadIdx.x & 31; q < a.batch; q += 32)
     all += min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
   return __reduce_add_sync(kFull, all);
 }
 // parts of the prefix in this call
-__device__ __forceinline__ int prefix_parts(const DenseArgs& a) {
-  return a.batch > kJoinScan ? a.shared.parts : shared_plan(a, own_tiles(a) * (a.n_kv_heads * a.row_blocks)).parts;
+__device__ __forceinline__ int prefix_parts(const SharedArgs& a) {
+  return a.batch > kJoinScan ? a.cost.parts : shared_plan(a, own_tiles(a) * (a.n_kv_heads * a.row_blocks)).parts;
 }
 
 template <class C>
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
                                                                 const PrefixArgs pa) {
   constexpr bool FP8 = C::FP8;
   constexpr int D = C::D, T = C::T, NT = C::NT, kLines = C::kLines;
-  const DenseArgs& a = pa.a;
+  const SharedArgs& a = pa.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = ring + C::kSlots * C::kSlot;
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   const uint32_t tmem = s_tmem;
   const int parts = s_parts;
   const bool spare = split >= parts;  // (part 0 always has CTAs: the kernel's end is theirs)
-  const int t0 = (int)((long long)split * a.shared.tiles / parts);
-  const int n = spare ? 0 : (int)((long long)(split + 1) * a.shared.tiles / parts) - t0;
+  const int t0 = (int)((long long)split * a.cost.tiles / parts);
+  const int n = spare ? 0 : (int)((long long)(split + 1) * a.cost.tiles / parts) - t0;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &s_abort, a.err); };
 
   if (spare) {
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
 template <int D, bool FP8, int WARPS>
 __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefix_join_kernel(const PrefixArgs pa) {
   constexpr int E = D / 32, kBatch = 8, TILE = 128;
-  const DenseArgs& a = pa.a;
+  const SharedArgs& a = pa.a;
   __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
   const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0;
   const int orow = WARPS > 1 ? blockIdx.x : blockIdx.x * kJoinRows + (threadIdx.x >> 5);
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
   // the request's own positions
   int c0 = 0, c1 = -1, first_slot = 0;  // pieces of CTAs c0 .. c1
   bool whole = false;
-  int parts = a.shared.parts;
+  int parts = a.cost.parts;
   auto unpack = [&](long long desc) {
     whole = desc == kUnitWhole;
     if (desc >= 0) {
