@@ -94,14 +94,15 @@ static bool alone(const qsa_dims& d, int prefix_len, int rows, int sms) {
 }
 
 struct PrefixWs {
-  size_t whole, parts, total;
+  size_t count, whole, parts, total;
 };
 static PrefixWs prefix_ws_layout(const qsa_dims& d, int prefix_len, int sms) {
   PrefixWs w;
   const int rows = d.n_q * (d.n_q_heads / d.n_kv_heads), per = unit_rows(d);
   const size_t units = (size_t)d.batch * d.n_kv_heads * ((rows + per - 1) / per);
   const size_t row = (d.head_dim + 2) * sizeof(float);
-  w.whole = dense_ws(d, sms).total;
+  w.count = dense_ws(d, sms).total;
+  w.whole = w.count + 256;
   w.parts = align_up(w.whole + units * per * row, 256);
   const PrefixPlan p = prefix_plan(d, prefix_len, sms);
   w.total = align_up(w.parts + (size_t)d.n_kv_heads * p.row_tiles * p.room * kPrefixRows * row, 256);
@@ -137,6 +138,7 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows,
   if (e != cudaSuccess) return e;
   PrefixArgs p = {};
   p.a = a;
+  p.n_parts = reinterpret_cast<int32_t*>(ws + w.count);
   p.parts = reinterpret_cast<float*>(ws + w.parts);
   p.rows = plan.rows;
   p.row_tiles = plan.row_tiles;

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) dense_tc_kernel(const __grid_c
       if constexpr (A::kShared) apart = a.shared_len > 0;
       const bool done = whole && last && !apart;
       const int pslot = seg == 0 ? 0 : 1;  // a CTA's first segment has its slot 0, a later one (its last) slot 1
-      if (a.batch > kJoinScan && tid == 0 && start == 0 && last)
+      if ((apart || a.batch > kJoinScan) && tid == 0 && start == 0 && last)
         a.unit_desc[(long long)at.r * units + at.x] =
             whole ? kUnitWhole : unit_pieces(blockIdx.x, s_share.split.last_cta(at.unit, at.tiles), pslot);
       const float part = reduce_rows<RC>(l, [](float c, float d) { return c + d; });

@@ -53,6 +53,7 @@ constexpr int kPrefixRows = 128;  // of a row tile
 
 struct PrefixArgs {
   SharedArgs a;
+  int32_t* n_parts;  // the parts of this call, from the kernel
   float* parts;    // [KV head][row tile][part] pieces: m[128], l[128], acc[128][D]
   int rows;        // of a KV head
   int row_tiles;   // of a KV head
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
   if (warp == C::kCopyWarp) {
     const int parts = prefix_parts(a);
     if (lane == 0) s_parts = parts;
+    if (lane == 0 && blockIdx.x == 0) *pa.n_parts = parts;
   }
   // (The kernel in front, the own positions', was launched by the same call;
   // its CTAs let this one start behind their own wait, so all that this kernel
@@ -653,7 +655,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
 // them; WARPS 1: a block of kJoinRows rows.
 template <int D, bool FP8, int WARPS>
 __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefix_join_kernel(const PrefixArgs pa) {
-  constexpr int E = D / 32, kBatch = 8, TILE = 128;
+  // (pieces on their way: 12 for a warp a row, 8 where 4 share one; 8 for a warp
+  // 1.2 us slower at 2,048 rows, 12 for 4 warps 2 us at 1,024)
+  constexpr int E = D / 32, kBatch = WARPS > 1 ? 8 : 12, TILE = 128;
   const SharedArgs& a = pa.a;
   __shared__ float s_m[WARPS], s_l[WARPS], s_acc[WARPS > 1 ? WARPS : 1][WARPS > 1 ? D : 1];
   const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0;
@@ -663,48 +667,28 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
   const int g = h / a.group, hg = h - g * a.group;
   const int i = j * a.group + hg, rb = i / pa.own_rows, own_row = i - rb * pa.own_rows;
   const int units = a.n_kv_heads * a.row_blocks, x = g * a.row_blocks + rb;
-  // the request's own positions
+  int p[kMaxNq];
+#pragma unroll
+  for (int q = 0; q < kMaxNq; ++q) p[q] = q < a.n_q ? a.q_pos[(size_t)r * a.n_q + q] : -1;
+  const int mine = a.q_pos[(size_t)r * a.n_q + j];
+  const bool sees = sees_prefix(a, p) && valid_pos(a, mine), has_own = range_of(a, r).tiles(TILE) > 0;
+  const float vscale = FP8 ? a.v_scale[g] : 1.f;
+  pdl_wait();
+  // The pieces: both kernels leave word of them. (Worked out here from q_pos, as
+  // dense_join_kernel does, they took every block 3 us where rows are many: 64
+  // requests x 16 heads 10.5 us from the prefix kernel's end to this one's.)
+  const int pre = sees ? *pa.n_parts : 0;
   int c0 = 0, c1 = -1, first_slot = 0;  // pieces of CTAs c0 .. c1
   bool whole = false;
-  int parts = a.cost.parts;
-  auto unpack = [&](long long desc) {
+  if (has_own) {
+    const long long desc = a.unit_desc[(long long)r * units + x];
     whole = desc == kUnitWhole;
     if (desc >= 0) {
       c0 = (int)(desc & 0xffffff);
       c1 = (int)((desc >> 24) & 0xffffff);
       first_slot = (int)(desc >> 48);
     }
-  };
-  if (a.batch <= kJoinScan) {
-    long long all = 0, below = 0;
-    for (int q = lane; q < a.batch; q += 32) {
-      const long long t = load_of(range_of(a, q).tiles(TILE));
-      all += t;
-      below += q < r ? t : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(kFull, all, o);
-      below += __shfl_xor_sync(kFull, below, o);
-    }
-    const int tiles = range_of(a, r).tiles(TILE);
-    parts = shared_plan(a, (all & ((1LL << 40) - 1)) * units).parts;
-    if (tiles > 0) {
-      Split sp;
-      sp.init(a, all);
-      const long long u = sp.slots(below) * units + (long long)x * (sp.seg + tiles);
-      const int f = sp.first_cta(u), e = sp.last_cta(u, tiles);
-      unpack(f == e ? kUnitWhole : unit_pieces(f, e, sp.piece_slot(u, f)));
-    }
   }
-  int p[kMaxNq];
-#pragma unroll
-  for (int q = 0; q < kMaxNq; ++q) p[q] = q < a.n_q ? a.q_pos[(size_t)r * a.n_q + q] : -1;
-  const int mine = a.q_pos[(size_t)r * a.n_q + j];
-  const int pre = sees_prefix(a, p) && valid_pos(a, mine) ? parts : 0;
-  const float vscale = FP8 ? a.v_scale[g] : 1.f;
-  pdl_wait();
-  if (a.batch > kJoinScan) unpack(a.unit_desc[(long long)r * units + x]);
   const int row = rj * a.group + hg, rt = row / kPrefixRows, pre_row = row % kPrefixRows;
   const float* pre_parts = pa.parts + (size_t)(g * pa.row_tiles + rt) * pa.room * (kPrefixRows * (D + 2));
   const int own = whole ? 1 : c1 - c0 + 1, own_piece = pa.own_rows * (D + 2);
@@ -809,7 +793,7 @@ cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k,
   e = launch_k(prefix_kernel<C>, dim3((unsigned)a.units * a.most), dim3(C::kThreads), C::kSmem, s, true, tk, tv, a);
   if (e != cudaSuccess) return e;
   // 4 warps a row where rows are few; else a warp a row (2,048 rows of 20 to 25
-  // pieces: 4 warps each made the whole call 6 us slower)
+  // pieces: 4 warps each made the whole call 1.8 us slower, 2 no faster)
   const unsigned rows = (unsigned)(a.a.batch * a.a.n_q * a.a.n_q_heads);
   if (rows < 8u * a.a.grid)
     return launch_k(prefix_join_kernel<D, FP8, 4>, dim3(rows), dim3(128), 0, s, true, a);
