@@ -19,23 +19,33 @@
 
 #include "qsa_serve_internal.cuh"
 
+#ifndef QX
+#define QX 1
+#endif
+#ifndef KT
+#define KT 512
+#endif
 namespace qsa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = KT, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr unsigned kHeld = 16384;  // weights of a slice that are held in shared memory
 constexpr unsigned kCand = 2048;   // keys with the last one's first digit that every CTA can take
 constexpr uint32_t kZeroKey = 0x80000000u;  // of a weight of 0
-constexpr int kSlice = 4096;       // positions of a CTA, more or less
+#ifndef KS
+#define KS 4096
+#endif
+constexpr int kSlice = KS;       // positions of a CTA, more or less
 
-__device__ __forceinline__ uint64_t warp_inclusive(uint64_t x) {
+// Sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t warp_inclusive(uint32_t x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(kFull, x, o);
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
   return x;
@@ -47,33 +57,11 @@ __device__ __forceinline__ void st_peer_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Sum of x over the threads before this one in the block; *all: over the block.
-__device__ __forceinline__ uint64_t block_exclusive(uint64_t x, uint64_t (&scan)[kSelWarps], uint64_t* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint64_t inc = warp_inclusive(x);
-  if (lane == 31) scan[warp] = inc;
-  __syncthreads();
-  uint64_t before = inc - x, total = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    before += w < warp ? scan[w] : 0;
-    total += scan[w];
-  }
-  __syncthreads();
-  *all = total;
-  return before;
-}
-
-// The same for 32-bit counts whose block total the caller does not need; `scan`
-// is read behind one barrier (the caller has another before it is written again).
+// Sum of x over the threads before this one in the block; `scan` is read behind
+// one barrier (the caller has another before it is written again).
 __device__ __forceinline__ uint32_t block_before(uint32_t x, uint32_t (&scan)[kSelWarps]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t inc = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += y;
-  }
+  const uint32_t inc = warp_inclusive(x);
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   const uint32_t other = lane < warp ? scan[lane] : 0;  // (at most 32 warps)
@@ -81,11 +69,11 @@ __device__ __forceinline__ uint32_t block_before(uint32_t x, uint32_t (&scan)[kS
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ float s_w[];  // the first a.held weights of the slice
+  extern __shared__ __align__(16) float s_w[];  // the first a.held weights of the slice
   __shared__ uint32_t s_hist[kBins], s_sum[kBins], s_cand[kCand], s_own[kCand];  // this CTA's counts, the cluster's
   __shared__ uint64_t s_scan[kSelWarps], s_slice[kMaxCluster];
   __shared__ uint32_t s_bin, s_left, s_same, s_at, s_count[kSelWarps];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size(), r = blockIdx.x / ctas;
   auto sync = [&]() {
     if (ctas > 1)
@@ -108,11 +96,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int32_t* kept = a.kept + (long long)r * a.keep;
   const unsigned left = min(n, keep);
   const unsigned first = (unsigned)(rank * kSelThreads + tid), step = (unsigned)(ctas * kSelThreads);
-  for (unsigned i = left + first; i < cap_out; i += step) {
-    w_out[i] = 0.f;
-    if (i < keep) kept[i] = -1;
-  }
+  auto fill = [&]() {  // behind the last one that stays
+    for (unsigned i = left + first; i < cap_out; i += step) {
+      w_out[i] = 0.f;
+      if (i < keep) kept[i] = -1;
+    }
+  };
   if (n <= keep) {
+    fill();
     for (unsigned i = first; i < n; i += step) {
       kept[i] = (int)i;
       w_out[i] = w[i];
@@ -123,10 +114,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   // positions lo .. hi - 1 are chosen from, `need` of them
   const unsigned lo = (unsigned)a.sinks, hi = n - (unsigned)a.recent;
-  const unsigned slice = (n + ctas - 1) / ctas, s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
+  const unsigned slice = ((n + ctas - 1) / ctas + 3) & ~3u;  // (16-byte boundaries)
+  const unsigned s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
   const unsigned held = min(s1 - s0, a.held);
+  const unsigned vecs = (reinterpret_cast<uintptr_t>(w + s0) & 15) == 0 ? held / 4 : 0;
+#pragma unroll 4
+  for (unsigned i = tid; i < vecs; i += kSelThreads)
+    reinterpret_cast<uint4*>(s_w)[i] = ld16(reinterpret_cast<const uint4*>(w + s0) + i);
 #pragma unroll 8
-  for (unsigned i = tid; i < held; i += kSelThreads) s_w[i] = w[s0 + i];
+  for (unsigned i = 4 * vecs + tid; i < held; i += kSelThreads) s_w[i] = w[s0 + i];
+  fill();
   auto key_at = [&](unsigned t) { return order_key(t - s0 < held ? s_w[t - s0] : w[t]); };
   uint32_t need = keep - a.sinks - a.recent, prefix = 0, mask = 0;
   if (need > 0) {
@@ -196,24 +193,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       need = s_left;
       if (ctas > 1 && d == 0 && s_same <= kCand) {
         // the keys with that digit go to every CTA, this one's behind those of the CTAs before it
-        for (unsigned t = c0 + tid; t - tid < c1; t += kSelThreads) {
-          const uint32_t k = t < c1 ? key_at(t) : 0;
-          const bool in = t < c1 && (k & mask) == prefix;
-          const uint32_t lanes = __ballot_sync(kFull, in);
-          if (lanes == 0) continue;
-          const int lane = tid & 31, leader = __ffs(lanes) - 1;
+        uint32_t front = 0;
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p) front += p < rank ? ld_peer(peer_addr(&s_hist[bin], p)) : 0;
+        for (unsigned b0 = c0; b0 < c1; b0 += 32 * kSelThreads) {  // a bit of `hits` each
+          const int steps = (int)min(32u, (c1 - b0 + kSelThreads - 1) / kSelThreads);
+          uint32_t hits = 0;
+#pragma unroll 4
+          for (int i = 0; i < steps; ++i) {
+            const unsigned t = b0 + i * kSelThreads + tid;
+            if (t < c1 && (key_at(t) & mask) == prefix) hits |= 1u << i;
+          }
+          const uint32_t inc = warp_inclusive(__popc(hits));
           uint32_t at = 0;
-          if (lane == leader) at = atomicAdd(&s_at, (uint32_t)__popc(lanes));
-          at = __shfl_sync(kFull, at, leader) + __popc(lanes & ((1u << lane) - 1u));
-          if (in) s_own[at] = k;
+          if (lane == 31 && inc > 0) at = atomicAdd(&s_at, inc);
+          at = __shfl_sync(kFull, at, 31) + inc - __popc(hits);
+          for (; hits; hits &= hits - 1) s_own[at++] = key_at(b0 + (__ffs(hits) - 1) * kSelThreads + tid);
         }
-        uint32_t at = 0;
-        for (int p = 0; p < rank; ++p) at += ld_peer(peer_addr(&s_hist[bin], p));
         __syncthreads();
         const uint32_t own = s_at;
-        for (uint32_t i = tid; i < own * (uint32_t)ctas; i += kSelThreads) {
-          const uint32_t p = i / own, j = i - p * own;
-          st_peer_u32(peer_addr(&s_cand[at + j], p), s_own[j]);
+        for (uint32_t j = tid; j < own; j += kSelThreads) {
+          const uint32_t k = s_own[j];
+#pragma unroll
+          for (int p = 0; p < kMaxCluster; ++p)
+            if (p < ctas) st_peer_u32(peer_addr(&s_cand[front + j], p), k);
         }
         cluster_sync();
         gathered = true;
@@ -225,16 +228,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   // Those above the last one's key stay, and the first `need` that equal it.
   const uint32_t last = need > 0 ? prefix : 0xffffffffu;  // (no weight has that key)
-  const unsigned per = (s1 - s0 + kSelThreads - 1) / kSelThreads;
-  const unsigned t0 = min(s0 + tid * per, s1), t1 = min(t0 + per, s1);
-  uint64_t count = 0;  // those that equal it << 32 | those that stay anyway
-  for (unsigned t = t0; t < t1; ++t) {
-    const bool sure = t < lo || t >= hi;
+  // A warp takes a contiguous part, 32 positions at a time.
+  const unsigned part = (s1 - s0 + kSelThreads - 1) / kSelThreads * 32;
+  const unsigned t0 = min(s0 + warp * part, s1), t1 = min(t0 + part, s1);
+  uint32_t stay = 0, same = 0;
+#pragma unroll 4
+  for (unsigned t = t0 + lane; t < t1; t += 32) {
     const uint32_t k = key_at(t);
-    count += sure || k > last ? 1ull : k == last ? 1ull << 32 : 0ull;
+    const bool anyway = t < lo || t >= hi || k > last;
+    stay += anyway;
+    same += !anyway && k == last;
   }
-  uint64_t all;
-  uint64_t before = block_exclusive(count, s_scan, &all);
+  stay = __reduce_add_sync(kFull, stay);
+  same = __reduce_add_sync(kFull, same);
+  if (lane == 0) s_scan[warp] = (uint64_t)same << 32 | stay;
+  __syncthreads();
+  uint64_t before = 0, all = 0;  // those that equal it << 32 | those that stay anyway
+#pragma unroll
+  for (int v = 0; v < kSelWarps; ++v) {
+    const uint64_t c = s_scan[v];
+    before += v < warp ? c : 0;
+    all += c;
+  }
   if (ctas > 1) {
     if (need == 0) cluster_sync();  // (no other before it: every CTA has started)
     if (tid < ctas) st_peer_u64(peer_addr(&s_slice[rank], tid), all);
@@ -243,17 +258,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   if (rank == 0 && tid == 0) a.new_len[r] = (int)left;  // (every CTA has read len)
   uint32_t ties = (uint32_t)(before >> 32), at = (uint32_t)before + min(ties, need);
-  for (unsigned t = t0; t < t1; ++t) {
-    const bool sure = t < lo || t >= hi;
-    const float x = t - s0 < held ? s_w[t - s0] : w[t];
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 2
+  for (unsigned b0 = t0; b0 < t1; b0 += 32) {
+    const unsigned t = b0 + lane;
+    const bool in = t < t1;
+    const float x = !in ? 0.f : t - s0 < held ? s_w[t - s0] : w[t];
     const uint32_t k = order_key(x);
-    bool stays = sure || k > last;
-    if (!stays && k == last) stays = ties++ < need;
+    const bool anyway = in && (t < lo || t >= hi || k > last), equal = in && !anyway && k == last;
+    const uint32_t equals = __ballot_sync(kFull, equal);
+    const bool stays = anyway || (equal && ties + __popc(equals & below) < need);
+    const uint32_t lanes = __ballot_sync(kFull, stays);
     if (stays) {
-      kept[at] = (int)t;
-      w_out[at] = x;
-      ++at;
+      const uint32_t to = at + __popc(lanes & below);
+      kept[to] = (int)t;
+      w_out[to] = x;
     }
+    ties += __popc(equals);
+    at += __popc(lanes);
   }
 }
 
@@ -315,8 +337,8 @@ cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s) {
   // CTAs of a request: few, for their barriers; more only where the slices would be long
   const int cap = a.max_pages * a.page_size;
   unsigned c = 1;
-  while (c < kMaxCluster && (long long)a.batch * c < device_sm_count() && cap / (int)c > kSlice) c *= 2;
-  a.held = std::min(kHeld, ((unsigned)cap + c - 1) / c);
+  while (c < kMaxCluster && (long long)a.batch * c * QX < device_sm_count() && cap / (int)c > kSlice) c *= 2;
+  a.held = std::min(kHeld, (((unsigned)cap + c - 1) / c + 3) & ~3u);
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(evict_select_kernel, kHeld * sizeof(float));
   if (e != cudaSuccess) return e;
