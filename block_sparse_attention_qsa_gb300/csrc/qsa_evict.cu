@@ -8,37 +8,35 @@
 // last one's first digit, which are few, go to every CTA, and each finds the
 // other two digits by itself. (Where they are many, equal weights for instance,
 // all three digits are counted in the cluster.) What stays is then numbered in
-// the order of the positions. A barrier of a cluster takes about 0.7 us and a
-// digit of the cluster two of them; that, not the weights' bytes, is the time of
-// this kernel: 61,201 positions in three digits of the cluster, with the lanes
-// that hit the same count one after the other, took 37 us.
+// the order of the positions, a warp 32 of them at a time. A barrier of a
+// cluster takes about 0.7 us and a digit of the cluster two of them; that and
+// the waits for memory, not the weights' bytes, are the time of this kernel:
+// 61,201 positions take one request 18.6 us and 32 requests 27 (37 in three
+// digits of the cluster; 31 with a contiguous share a thread, and the keys
+// gathered one atomic at a time).
 //
 // A second kernel, chained with programmatic dependent launch, copies K and V of
-// the tokens that stay (the bytes of which are the bound for a batch).
+// the tokens that stay, the bytes of which are the bound for a batch: 32 requests
+// from 50,001-61,201 to 16,385 tokens (BF16, 2 KV heads of 128) 160 us, 6.7 TB/s,
+// the whole call 187.5.
 #include <algorithm>
 
 #include "qsa_serve_internal.cuh"
 
-#ifndef QX
-#define QX 1
-#endif
-#ifndef KT
-#define KT 512
-#endif
 namespace qsa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSelThreads = KT, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr unsigned kHeld = 16384;  // weights of a slice that are held in shared memory
 constexpr unsigned kCand = 2048;   // keys with the last one's first digit that every CTA can take
 constexpr uint32_t kZeroKey = 0x80000000u;  // of a weight of 0
-#ifndef KS
-#define KS 4096
-#endif
-constexpr int kSlice = KS;       // positions of a CTA, more or less
+// Positions of a CTA, more or less. (4,200 in slices of 2,112, 1,056 and 528:
+// one request 14.2, 13.1 and 12.3 us for the whole call, 32 of them 54.7, 52.9
+// and 54.7.)
+constexpr int kSlice = 2048;
 
 // Sum over the lanes up to this one.
 __device__ __forceinline__ uint32_t warp_inclusive(uint32_t x) {
@@ -337,7 +335,7 @@ cudaError_t launch_kv_evict(EvictArgs a, cudaStream_t s) {
   // CTAs of a request: few, for their barriers; more only where the slices would be long
   const int cap = a.max_pages * a.page_size;
   unsigned c = 1;
-  while (c < kMaxCluster && (long long)a.batch * c * QX < device_sm_count() && cap / (int)c > kSlice) c *= 2;
+  while (c < kMaxCluster && (long long)a.batch * c < device_sm_count() && cap / (int)c > kSlice) c *= 2;
   a.held = std::min(kHeld, (((unsigned)cap + c - 1) / c + 3) & ~3u);
   static DeviceSlots slots;
   cudaError_t e = slots.raise_smem(evict_select_kernel, kHeld * sizeof(float));
