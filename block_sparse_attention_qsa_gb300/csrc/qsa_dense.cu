@@ -81,16 +81,14 @@ static PrefixPlan prefix_plan(const qsa_dims& d, int prefix_len, int sms) {
   return p;
 }
 
-// Whether every request reads the prefix by itself: where those bytes are few,
-// the two kernels of a shared one cost more than they save. (Own parts of 1 to
-// 200 tokens, shared and alone: 32 requests x 1 query, BF16, 256 tokens shared
-// 14.8 and 11.2 us, 1,024 tokens 16.0 and 12.8, 4,096 tokens, 860 KB an SM, 17.8
-// and 19.1; x 4 queries, E4M3, 4,096 tokens, 430 KB, 35.3 and 25.0.)
-constexpr long long kAloneBytes = 640 * 1024;  // an SM
+// Whether every request reads the prefix by itself: where its tiles are few, the
+// two kernels of a shared one cost more than they save.
+constexpr long long kAloneBytes = 640 * 1024, kAloneTile = 32 * 1024;  // an SM; a tile, at least
 static bool alone(const qsa_dims& d, int prefix_len, int rows, int sms) {
   const int all = d.n_q * (d.n_q_heads / d.n_kv_heads), eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2;
   const long long reads = (long long)d.batch * d.n_kv_heads * ((all + rows - 1) / rows);
-  return d.batch == 1 || reads * prefix_len * 2 * d.head_dim * eb <= kAloneBytes * sms;
+  const long long tile = std::max(kAloneTile, 256LL * d.head_dim * eb);
+  return d.batch == 1 || reads * ((prefix_len + 127) / 128) * tile <= kAloneBytes * sms;
 }
 
 struct PrefixWs {
@@ -118,10 +116,12 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows,
   const PrefixPlan plan = prefix_plan(d, a.prefix_len, a.grid);
   a.whole = reinterpret_cast<float*>(ws + w.whole);
   a.row_blocks = (a.n_q * a.group + rows - 1) / rows;
-  // What a tile takes a CTA, measured (head dim 128): of the own positions 1.25 us
-  // for 64 KB on 40 SMs, and about as much for 32 KB; of the prefix, two row
+  // What things take, measured (head dim 128): a tile of the own positions 1.25 us
+  // a CTA for 64 KB on 40 SMs, and not much less for 32 KB; beginning a unit of
+  // one tile, of which a CTA has several, 5 to 6 us; a tile of the prefix, two row
   // tiles, 1.5 us with a BF16 cache and 2.3 with E4M3. A CTA's beginning and end
-  // take the first kernel 9 us, the second 15.
+  // take the first kernel 9 us, the second 15. (Without the units, 32 requests of
+  // 4 to 60 own tokens over 50,048 had 8 SMs for them: 73 us, now 55.)
   const int eb = d.kv_dtype == QSA_KV_FP8_E4M3 ? 1 : 2, bytes = 256 * d.head_dim * eb;
   SharedCost& c = a.cost;
   c.units = plan.units;
@@ -129,7 +129,8 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows,
   c.least = plan.least;
   c.most = std::min(plan.most, 254);
   c.parts = plan.splits;
-  c.own_ns = std::max(bytes / 52, 1150);
+  c.own_ns = std::max(bytes / 52, 1000);
+  c.unit_ns = 5000;
   c.own_hbm_ns = bytes / 6800;
   c.part_ns = (d.head_dim == 64 ? 1000 : 1500) * (eb == 1 ? 3 : 2) / 2;
   c.own_begin_ns = 9000;

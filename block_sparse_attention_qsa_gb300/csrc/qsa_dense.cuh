@@ -39,11 +39,11 @@ constexpr long long kWaitCycles = 1LL << 31;  // bound of every wait: about one 
 // What the host knows of the two kernels that share the GPU when a prefix is read
 // once (shared_plan): CTAs of a part of the prefix, its tiles, the fewest and
 // most parts, and the parts if the kernels run one after the other; what a tile
-// takes a CTA of either kernel, one of the own positions its HBM, and a CTA's
-// beginning and end (ns).
+// and a unit of the own positions take a CTA, a tile HBM, a tile of the prefix a
+// CTA, and a CTA's beginning and end in either kernel (ns).
 struct SharedCost {
   int units, tiles, least, most, parts;
-  int own_ns, own_hbm_ns, part_ns, own_begin_ns, part_begin_ns;
+  unsigned own_ns, unit_ns, own_hbm_ns, part_ns, own_begin_ns, part_begin_ns;
 };
 
 struct DenseArgs {
@@ -214,20 +214,19 @@ __device__ __forceinline__ long long load_of(int tiles) { return tiles > 0 ? (1L
 // own positions, and the prefix in `parts` parts, a CTA each a unit. The first
 // kernel is bound by HBM and the second by the tensor cores, so the two run side
 // by side on SMs of their own where that ends earlier than one after the other,
-// each on all. The host does not know the lengths; every CTA of either kernel,
-// and the joining one, comes to the same division from q_pos. (A whole warp;
-// tiles: of all units of the own positions. Many requests: one after the other,
-// which takes no pass over q_pos.)
+// each on all. The host does not know the lengths; every CTA of either kernel
+// comes to the same division from q_pos. (A whole warp; tiles and units: of the
+// own positions of all requests. Many requests: one after the other, which takes
+// no pass over q_pos.)
 struct SharedPlan {
   int own, parts;
 };
-__device__ __forceinline__ SharedPlan shared_plan(const SharedArgs& a, long long tiles) {
+__device__ __forceinline__ SharedPlan shared_plan(const SharedArgs& a, long long tiles, long long units) {
   const SharedCost& c = a.cost;
   if (a.batch > kJoinScan) return SharedPlan{a.grid, c.parts};
-  const unsigned own = (unsigned)min(tiles, 1LL << 20), lane = threadIdx.x & 31;  // (products below 2^32)
-  auto own_time = [&](unsigned ctas) {
-    return own == 0 ? 0u : c.own_begin_ns + max(own * (unsigned)c.own_ns / ctas, own * (unsigned)c.own_hbm_ns);
-  };
+  const unsigned own = (unsigned)min(tiles, 1LL << 18), lane = threadIdx.x & 31;  // (products below 2^32)
+  const unsigned work = own * c.own_ns + (unsigned)min(units, 1LL << 18) * c.unit_ns;
+  auto own_time = [&](unsigned ctas) { return own == 0 ? 0u : c.own_begin_ns + max(work / ctas, own * c.own_hbm_ns); };
   auto part_time = [&](unsigned parts) { return c.part_begin_ns + (c.tiles + parts - 1) / parts * c.part_ns; };
   // (time << 8 | parts), or parts 255: one after the other
   const unsigned long long waves = ((unsigned long long)c.units * c.parts + a.grid - 1) / a.grid;
@@ -252,7 +251,7 @@ struct Split {
     const long long tiles = (load & ((1LL << 40) - 1)) * units;
     int grid = a.grid;
     if constexpr (A::kShared) {
-      if (a.shared_len > 0) grid = shared_plan(a, tiles).own;
+      if (a.shared_len > 0) grid = shared_plan(a, tiles, (load >> 40) * units).own;
     }
     seg = tiles > grid ? kSegCost : 0;
     const long long all = slots(load) * units;

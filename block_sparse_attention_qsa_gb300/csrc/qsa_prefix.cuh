@@ -42,6 +42,14 @@
 // runs. The prefix kernel reads nothing that the first writes, so it does not
 // wait for it before its work, only before its end; and the first one leaves it
 // SMs of its own (shared_plan in qsa_dense.cuh).
+//
+// Measured: 32 requests x 4 queries x 16 heads (2 KV heads of 128) over 50,048
+// shared and 4 to 6,401 own tokens, BF16: 66 us for the whole call, of which this
+// kernel has 57 on two thirds of the SMs (tensor cores busy 39 % of the time of
+// all, 53 % of its own SMs', HBM 11 %); E4M3 72. Both products at the measured
+// BF16 rate on all SMs: 29.6. What is between: the SMs that the own positions'
+// kernel has, 10 us of beginnings, ends and the join, the wait of the tensor
+// cores for softmax in each tile.
 #pragma once
 
 #include "qsa_serve_internal.cuh"
@@ -144,16 +152,17 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// Tiles of the requests' own positions, a unit of each; a whole warp.
-__device__ __forceinline__ long long own_tiles(const SharedArgs& a) {
-  int all = 0;
-  for (int q = threadIdx.x & 31; q < a.batch; q += 32)
-    all += min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
-  return __reduce_add_sync(kFull, all);
-}
-// parts of the prefix in this call
+// Parts of the prefix in this call (a whole warp).
 __device__ __forceinline__ int prefix_parts(const SharedArgs& a) {
-  return a.batch > kJoinScan ? a.cost.parts : shared_plan(a, own_tiles(a) * (a.n_kv_heads * a.row_blocks)).parts;
+  if (a.batch > kJoinScan) return a.cost.parts;
+  int tiles = 0, some = 0;  // of the requests' own positions, a unit of each
+  for (int q = threadIdx.x & 31; q < a.batch; q += 32) {
+    const int t = min(range_of(a, q).tiles(128), 1 << 20);  // (no sum past 2^28)
+    tiles += t;
+    some += t > 0;
+  }
+  const long long units = a.n_kv_heads * a.row_blocks;
+  return shared_plan(a, __reduce_add_sync(kFull, tiles) * units, __reduce_add_sync(kFull, some) * units).parts;
 }
 
 template <class C>

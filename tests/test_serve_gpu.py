@@ -189,6 +189,24 @@ def test_prefix_long_parts(qsa, kv, D):
     _prefix_case(qsa, 40, [3] * 17, 1, 640, 80, D, 64, kv)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_long_own_positions(qsa, kv):
+    # one CTA has all 259 tiles of a request's own positions, more than an accumulator in tensor memory holds at
+    # once; the requests' tables name the same pages
+    B = 152
+    c = Prefixed(qsa, 4, [259 * 128 - 5], 1, 1, 1, 64, kv=kv)
+    c.B, c.q = B, _normal((B, 1, 1, 64), 5)
+    c.q_pos, c.full = np.repeat(c.q_pos, B, 0), c.full.expand(B, -1)
+    c.d = _dims(qsa, B, c.table.shape[1], c.d.num_pages, kv, 1, 1, 1, 64)
+    c.ws = qsa.make_prefix_workspace(c.d, 4)
+    c.out = torch.full((B, 1, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.lse = torch.full((B, 1, 1), 7.0, device="cuda")
+    c.args = (c.d, c.q, *c.args[2:7], c.table.expand(B, -1).contiguous().cuda(), _i32(c.q_pos.tolist()), c.out, c.ws)
+    c.run(qsa, alone=False)
+    _ok(qsa, c.ws)
+    c.compare()
+
+
 @pytest.mark.parametrize("D,B,hq,hk", [(128, 300, 8, 1), (64, 700, 4, 2), (256, 257, 4, 1)])
 def test_prefix_many_requests(qsa, D, B, hq, hk):
     rng = np.random.RandomState(3)
