@@ -686,7 +686,8 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
   // The pieces: both kernels leave word of them. (Worked out here from q_pos, as
   // dense_join_kernel does, they took every block 3 us where rows are many: 64
   // requests x 16 heads 10.5 us from the prefix kernel's end to this one's.)
-  const int pre = sees ? *pa.n_parts : 0;
+  // (Bounded, so that a workspace that was overwritten leads to no read outside it.)
+  const int pre = sees ? max(0, min(*pa.n_parts, pa.room)) : 0;
   int c0 = 0, c1 = -1, first_slot = 0;  // pieces of CTAs c0 .. c1
   bool whole = false;
   if (has_own) {
@@ -694,8 +695,8 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
     whole = desc == kUnitWhole;
     if (desc >= 0) {
       c0 = (int)(desc & 0xffffff);
-      c1 = (int)((desc >> 24) & 0xffffff);
-      first_slot = (int)(desc >> 48);
+      c1 = min((int)((desc >> 24) & 0xffffff), a.grid - 1);
+      first_slot = (int)(desc >> 48) & 1;
     }
   }
   const int row = rj * a.group + hg, rt = row / kPrefixRows, pre_row = row % kPrefixRows;
