@@ -30,6 +30,21 @@ qsa_status prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages
                                  Prefix{prefix_table, prefix_pages * dims->page_size, alone}));
 }
 
+qsa_status kv_weight(const qsa_dims* dims, float decay, const void* q, const void* k_cache, const float* k_scale,
+                     const int32_t* page_table, const int32_t* q_pos, const float* lse, float* weight, void* ws,
+                     size_t ws_bytes, void* stream, bool short_k) {
+  const qsa_status st = check_kv_dims(dims);
+  if (st != QSA_OK) return st;
+  if (!(decay >= 0.f && decay <= 1.f)) return QSA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !page_table || !q_pos || !lse || !weight) return QSA_ERR_INVALID_ARG;
+  if (needs_scales(*dims) && !k_scale) return QSA_ERR_INVALID_ARG;
+  if (!aligned_all(16, {q, k_cache}) || !aligned_all(4, {k_scale, page_table, q_pos, lse, weight}))
+    return QSA_ERR_INVALID_ARG;
+  if (!check_header(ws, ws_bytes)) return QSA_ERR_WORKSPACE;
+  return from_cuda(launch_kv_weight(*dims, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight,
+                                    static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream), short_k));
+}
+
 }  // namespace
 
 extern "C" {
@@ -62,16 +77,13 @@ qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t pre
 qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const void* k_cache, const float* k_scale,
                          const int32_t* page_table, const int32_t* q_pos, const float* lse, float* weight, void* ws,
                          size_t ws_bytes, void* stream) {
-  const qsa_status st = check_kv_dims(dims);
-  if (st != QSA_OK) return st;
-  if (!(decay >= 0.f && decay <= 1.f)) return QSA_ERR_INVALID_ARG;
-  if (!q || !k_cache || !page_table || !q_pos || !lse || !weight) return QSA_ERR_INVALID_ARG;
-  if (needs_scales(*dims) && !k_scale) return QSA_ERR_INVALID_ARG;
-  if (!aligned_all(16, {q, k_cache}) || !aligned_all(4, {k_scale, page_table, q_pos, lse, weight}))
-    return QSA_ERR_INVALID_ARG;
-  if (!check_header(ws, ws_bytes)) return QSA_ERR_WORKSPACE;
-  return from_cuda(launch_kv_weight(*dims, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight,
-                                    static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
+  return kv_weight(dims, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, ws_bytes, stream, false);
+}
+
+qsa_status qsa_test_kv_weight_timeout(const qsa_dims* dims, float decay, const void* q, const void* k_cache,
+                                      const float* k_scale, const int32_t* page_table, const int32_t* q_pos,
+                                      const float* lse, float* weight, void* ws, size_t ws_bytes, void* stream) {
+  return kv_weight(dims, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, ws_bytes, stream, true);
 }
 
 qsa_status qsa_kv_evict(const qsa_dims* dims, int32_t keep, int32_t sinks, int32_t recent, int32_t out_pages,

@@ -9,9 +9,10 @@ namespace qsa {
 constexpr int kErrToken = 7;   // qsa_verify_drafts: a drafted token outside the vocabulary
 constexpr int kErrLength = 8;  // qsa_kv_evict: a length outside the page table
 
+// short_k: the failure-detection test (qsa_test_kv_weight_timeout)
 cudaError_t launch_kv_weight(const qsa_dims& d, float decay, const void* q, const void* k_cache, const float* k_scale,
                              const int32_t* page_table, const int32_t* q_pos, const float* lse, float* weight,
-                             int32_t* err, cudaStream_t s);
+                             int32_t* err, cudaStream_t s, bool short_k);
 
 struct EvictArgs {
   const int32_t* len;

@@ -106,7 +106,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) weight_kernel(const __grid_con
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&q_full[b]), 128);
-      mbar_init(smem_u32(&q_empty[b]), 256 + 1);
+      // (One arrival a warp of the sums and the tensor cores'. The 32 of a warp are
+      // counted at once: where the sums run on past a wait that was given up and the
+      // last commit never comes, 256 + 1 of them would take the count below zero.)
+      mbar_init(smem_u32(&q_empty[b]), 8 + 1);
     }
     mbar_init(smem_u32(&fin), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -238,15 +241,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) weight_kernel(const __grid_con
     // ---- query rows of the steps ahead ----
     const int t = tid - 256;
     int st = 0;
-    bool ok = true;
     do {
       int n = 0;
-      for (int left = at.n; left > 0 && ok; left -= n) {
+      for (int left = at.n; left > 0; left -= n) {
         n = min(kRunTiles, left);
-        for (int x = 0; x < steps && ok; ++x, ++st) {
+        for (int x = 0; x < steps; ++x, ++st) {
           const int buf = st & 1, g = x / a.blocks, first = x % a.blocks * kRows, rows = rows_of(x);
           const int pad = (rows + 15) / 16 * 16;
-          if (st >= 2) ok = wait(&q_empty[buf], (uint32_t)((st - 2) >> 1) & 1u);
+          // (Given up: on without meaning, to the same barriers. What one thread sees of
+          // a wait that ran out its neighbour may not: no loop here may end by it.)
+          if (st >= 2) wait(&q_empty[buf], (uint32_t)((st - 2) >> 1) & 1u);
+          __syncwarp();
           const float base = w.sm_scale * kLog2e * (FP8 ? w.k_scale[g] : 1.f);
           uint8_t* dst = s_q + buf * C::kQ;
           constexpr int kLanes = D / 8, kPass = 128 / kLanes;  // 8 components a lane
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) weight_kernel(const __grid_con
           mbar_arrive(smem_u32(&q_full[buf]));
         }
       }
-    } while (ok && at.next(w, s_share));
+    } while (at.next(w, s_share));
   } else {
     // ---- sums ----
     const int wg = warp >> 2, t = tid & 127;
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) weight_kernel(const __grid_con
               weight[p] = a.decay == 0.f ? acc : fmaf(a.decay, old, acc);
           }
           it += n;
-          mbar_arrive(smem_u32(&q_empty[buf]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&q_empty[buf]));
         }
       }
     } while (at.next(w, s_share));
@@ -403,10 +409,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) weight_kernel(const __grid_con
 }
 
 template <int D, bool FP8>
-cudaError_t launch(const qsa_dims& d, const WeightArgs& a, const void* k_cache, cudaStream_t s) {
+cudaError_t launch(const qsa_dims& d, const WeightArgs& a, const void* k_cache, bool short_k, cudaStream_t s) {
   using C = Wc<D, FP8>;
   alignas(64) CUtensorMap tk;
-  if (!make_cache_map(&tk, d, k_cache, kTile, C::kLine, false)) return cudaErrorInvalidValue;
+  if (!make_cache_map(&tk, d, k_cache, kTile, C::kLine, short_k)) return cudaErrorInvalidValue;
   static DeviceSlots slots;
   const cudaError_t e = slots.raise_smem(weight_kernel<C>, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -417,7 +423,7 @@ cudaError_t launch(const qsa_dims& d, const WeightArgs& a, const void* k_cache, 
 
 cudaError_t launch_kv_weight(const qsa_dims& d, float decay, const void* q, const void* k_cache, const float* k_scale,
                              const int32_t* page_table, const int32_t* q_pos, const float* lse, float* weight,
-                             int32_t* err, cudaStream_t s) {
+                             int32_t* err, cudaStream_t s, bool short_k) {
   WeightArgs a = {};
   DenseArgs& w = a.w;
   w.q = static_cast<const __nv_bfloat16*>(q);
@@ -443,9 +449,9 @@ cudaError_t launch_kv_weight(const qsa_dims& d, float decay, const void* q, cons
   a.decay = decay;
   const bool fp8 = d.kv_dtype == QSA_KV_FP8_E4M3;
   switch (d.head_dim) {
-    case 64: return fp8 ? launch<64, true>(d, a, k_cache, s) : launch<64, false>(d, a, k_cache, s);
-    case 128: return fp8 ? launch<128, true>(d, a, k_cache, s) : launch<128, false>(d, a, k_cache, s);
-    default: return fp8 ? launch<256, true>(d, a, k_cache, s) : launch<256, false>(d, a, k_cache, s);
+    case 64: return fp8 ? launch<64, true>(d, a, k_cache, short_k, s) : launch<64, false>(d, a, k_cache, short_k, s);
+    case 128: return fp8 ? launch<128, true>(d, a, k_cache, short_k, s) : launch<128, false>(d, a, k_cache, short_k, s);
+    default: return fp8 ? launch<256, true>(d, a, k_cache, short_k, s) : launch<256, false>(d, a, k_cache, short_k, s);
   }
 }
 

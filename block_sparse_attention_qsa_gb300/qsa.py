@@ -49,8 +49,8 @@ KV_EXPORTS = (
 )
 # and those of include/qsa_serve.h, the operators for serving a batch in a bounded cache
 SERVE_EXPORTS = (
-    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_test_prefix_attn", "qsa_kv_weight", "qsa_kv_evict",
-    "qsa_verify_drafts",
+    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_test_prefix_attn", "qsa_kv_weight",
+    "qsa_test_kv_weight_timeout", "qsa_kv_evict", "qsa_verify_drafts",
 )
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
@@ -162,6 +162,7 @@ def _load() -> ctypes.CDLL:
         "qsa_prefix_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_test_prefix_attn": (I, [D, N, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_weight": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_test_kv_weight_timeout": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_evict": (I, [D, N, N, N, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_verify_drafts": (I, [N, N, N, N, P, T, P, T, P, P, P, P, P, SZ, P]),
     })
@@ -845,6 +846,11 @@ def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, 
         return
     if st is not None:
         _check(st, "qsa_kv_weight")
+    _kv_weight(lib.qsa_kv_weight, "qsa_kv_weight", d, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, decay,
+               stream)
+
+
+def _kv_weight(fn, name, d, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, decay, stream):
     dev = _current_device()
     B, n_q, H = d.batch, d.n_q, d.n_q_heads
     fp8 = d.kv_dtype == KV_FP8_E4M3
@@ -857,9 +863,18 @@ def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, 
     lp = _want_on(dev, lse, "lse", (B, n_q, H), _F32)
     wp = _want_on(dev, weight, "weight", (B, d.max_pages * d.page_size), _F32)
     w, nb = _ws_on(dev, ws)
-    st = lib.qsa_kv_weight(d, decay, qp, kc, ks, pt, pp, lp, wp, w, nb, _stream(stream))
+    st = fn(d, decay, qp, kc, ks, pt, pp, lp, wp, w, nb, _stream(stream))
     if st:
-        _check(st, "qsa_kv_weight")
+        _check(st, name)
+
+
+def test_kv_weight_timeout(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, decay: float = 1.0,
+                           stream=None):
+    """qsa_test_kv_weight_timeout: kv_weight with copies of half the bytes its
+    kernel waits for, so that its bounded waits run out (about a second);
+    check_errors then reports ERR_TIMEOUT. For failure-detection tests."""
+    _kv_weight(lib.qsa_test_kv_weight_timeout, "qsa_test_kv_weight_timeout", d, q, k_cache, k_scale, page_table, q_pos,
+               lse, weight, ws, decay, stream)
 
 
 def kv_evict(d: Dims, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length, ws,

@@ -90,6 +90,14 @@ qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const
                          const int32_t* page_table, const int32_t* q_pos, const float* lse, float* weight, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* Test hook for failure detection: qsa_kv_weight with copies of K that bring
+ * half of the bytes its kernel waits for, as qsa_test_paged_attn_timeout (kind
+ * 5, QSA_ERR_TIMEOUT). weight holds nothing of meaning where a query sees it;
+ * the next call on the same workspace is complete again. */
+qsa_status qsa_test_kv_weight_timeout(const qsa_dims* dims, float decay, const void* q, const void* k_cache,
+                                      const float* k_scale, const int32_t* page_table, const int32_t* q_pos,
+                                      const float* lse, float* weight, void* ws, size_t ws_bytes, void* stream);
+
 /* Eviction: of the len[r] tokens that request r has cached (positions 0 ..
  * len[r] - 1), at most `keep` stay: the first `sinks`, the last `recent`, and
  * of those between the ones with the largest weight[r][t], the lower position

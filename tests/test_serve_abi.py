@@ -122,6 +122,15 @@ def test_kv_weight_refusals(qsa):
 
 
 @no_device
+def test_kv_weight_timeout_hook_refuses_as_kv_weight(qsa):
+    d = qsa.make_dims(3, 2, 100, 10, 40)
+    good = [d, 0.5, F, F, None, F, F, F, F, F, 256, None]
+    for i, x, st in ((0, None, qsa.ERR_INVALID_ARG), (1, 2.0, qsa.ERR_INVALID_ARG), (3, OFF8, qsa.ERR_INVALID_ARG),
+                     (7, None, qsa.ERR_INVALID_ARG), (10, 255, qsa.ERR_WORKSPACE)):
+        assert qsa.lib.qsa_test_kv_weight_timeout(*_with(good, i, x)) == st, i
+
+
+@no_device
 def test_kv_evict_refusals(qsa):
     d = qsa.make_dims(3, 2, 100, 10, 40)
     #        keep sinks recent out_pages len weight pt  pto kc vc weight_out kept new_len ws

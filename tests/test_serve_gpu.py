@@ -775,6 +775,32 @@ def test_weight_refusals(qsa):
     assert torch.equal(w, c.old)
 
 
+@pytest.mark.parametrize("kv,hq,hk,D,n_q", [("bf16", 16, 2, 128, 4), ("fp8", 24, 8, 64, 2), ("bf16", 40, 5, 256, 4)])
+def test_weight_wait_runs_out_and_reports_a_timeout(qsa, kv, hq, hk, D, n_q):
+    # As for the dense attention: the hook's copies of K bring half of the bytes,
+    # every CTA's wait for its first tile runs out, and all of its roles end,
+    # those too that have steps ahead of them when the wait is given up (a CTA
+    # has 2, 8 and 5 here): the next calls are complete.
+    import time
+
+    c = Weighed(qsa, [1500, 70, 0, 3000], n_q, hq, hk, D, kv=kv, decay=0.5).run(qsa)
+    _ok(qsa, c.ws)
+    want = c.weight.clone()
+    torch.cuda.synchronize()
+    t0 = time.time()
+    qsa.test_kv_weight_timeout(*c.args, decay=c.decay)
+    torch.cuda.synchronize()
+    waited = time.time() - t0
+    st, info = qsa.check_errors(c.ws)
+    assert st == qsa.ERR_TIMEOUT and info[0] == 5, info
+    assert 0.2 < waited < 30, waited
+    for _ in range(3):
+        c.weight.copy_(c.old)
+        c.run(qsa)
+        _ok(qsa, c.ws)
+        assert torch.equal(c.weight, want)
+
+
 # --------------------------------------------------------------------------
 # eviction
 # --------------------------------------------------------------------------
