@@ -115,7 +115,7 @@ size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms) {
 }
 
 static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows, uint8_t* ws, const void* k_cache,
-                                      const void* v_cache, cudaStream_t s) {
+                                      const void* v_cache, bool short_k, cudaStream_t s) {
   const PrefixWs w = prefix_ws_layout(d, a.prefix_len, a.grid);
   const PrefixPlan plan = prefix_plan(d, a.prefix_len, a.grid);
   a.whole = reinterpret_cast<float*>(ws + w.whole);
@@ -152,9 +152,9 @@ static cudaError_t launch_with_prefix(const qsa_dims& d, SharedArgs a, int rows,
   p.most = plan.most;
   p.own_rows = rows;
   switch (d.head_dim) {
-    case 64: return launch_prefix_64(d, p, k_cache, v_cache, s);
-    case 128: return launch_prefix_128(d, p, k_cache, v_cache, s);
-    default: return launch_prefix_256(d, p, k_cache, v_cache, s);
+    case 64: return launch_prefix_64(d, p, k_cache, v_cache, short_k, s);
+    case 128: return launch_prefix_128(d, p, k_cache, v_cache, short_k, s);
+    default: return launch_prefix_256(d, p, k_cache, v_cache, short_k, s);
   }
 }
 
@@ -199,7 +199,7 @@ cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, cons
   if (prefix.alone < 0 ? alone(d, prefix.len, rows, sms) : prefix.alone)
     return launch_dense(rows, d, x, k_cache, v_cache, short_k, s);
   x.shared_len = prefix.len;
-  return launch_with_prefix(d, x, rows, base, k_cache, v_cache, s);
+  return launch_with_prefix(d, x, rows, base, k_cache, v_cache, short_k, s);
 }
 
 }  // namespace qsa

@@ -58,7 +58,8 @@ struct Prefix {
   int len, alone;
 };
 size_t prefix_ws(const qsa_dims& d, int prefix_len, int num_sms);  // bytes of workspace with a prefix
-// short_k: the failure-detection test (qsa_test_paged_attn_timeout)
+// short_k: the failure-detection tests (qsa_test_paged_attn_timeout; with a prefix
+// that is read once, its kernel's copies: qsa_test_prefix_attn_timeout)
 cudaError_t launch_paged_attn(const qsa_dims& d, int window, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, const int32_t* page_table,
                               const int32_t* q_pos, void* out, float* lse, void* ws, cudaStream_t s,

@@ -71,9 +71,13 @@ struct PrefixArgs {
   int own_rows;    // of a unit of the requests' own positions
 };
 
-cudaError_t launch_prefix_64(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, cudaStream_t s);
-cudaError_t launch_prefix_128(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, cudaStream_t s);
-cudaError_t launch_prefix_256(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, cudaStream_t s);
+// short_k: the failure-detection test (qsa_test_prefix_attn_timeout)
+cudaError_t launch_prefix_64(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, bool short_k,
+                             cudaStream_t s);
+cudaError_t launch_prefix_128(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, bool short_k,
+                              cudaStream_t s);
+cudaError_t launch_prefix_256(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, bool short_k,
+                              cudaStream_t s);
 
 namespace {
 
@@ -405,8 +409,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const __grid_con
     int st = 0, slot = 0;
     uint32_t st_phase = 0, phase = 0;
     for (int q = 0; q < 2 * n; ++q) {
-      wait(&stage_full[st], st_phase);
-      wait(&slot_empty[slot], phase ^ 1u);  // (given up: on without meaning, to the end)
+      // (Given up: nothing is waited for here any more but the kernel's end. An
+      // arrival for a copy that has not landed would let the next one be announced
+      // at a barrier whose phase is not over, and its count fall below zero.)
+      if (!__all_sync(kFull, wait(&stage_full[st], st_phase) && wait(&slot_empty[slot], phase ^ 1u))) break;
       const uint8_t* src = stage + st * C::kStage;
       uint8_t* dst = ring + slot * C::kSlot;
 #pragma unroll 4
@@ -784,11 +790,12 @@ __global__ void __launch_bounds__(WARPS > 1 ? 32 * WARPS : 32 * kJoinRows) prefi
 }
 
 template <int D, bool FP8, int NT>
-cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, cudaStream_t s) {
+cudaError_t launch_prefix(const qsa_dims& d, const PrefixArgs& a, const void* k, const void* v, bool short_k,
+                          cudaStream_t s) {
   using C = Pc<D, FP8, NT>;
   alignas(64) CUtensorMap tk, tv;
   constexpr int kLine = FP8 ? C::kStageLine : 128;
-  if (!make_cache_map(&tk, d, k, C::T, kLine, false) || !make_cache_map(&tv, d, v, C::T, kLine, false))
+  if (!make_cache_map(&tk, d, k, C::T, kLine, short_k) || !make_cache_map(&tv, d, v, C::T, kLine, false))
     return cudaErrorInvalidValue;
   static DeviceSlots slots, regs;
   cudaError_t e = slots.raise_smem(prefix_kernel<C>, C::kSmem);

@@ -12,7 +12,7 @@ bool needs_scales(const qsa_dims& d) { return d.kv_dtype == QSA_KV_FP8_E4M3; }
 qsa_status prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages, const int32_t* prefix_table,
                        const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                        const float* v_scale, const int32_t* page_table, const int32_t* q_pos, void* out, float* lse,
-                       void* ws, size_t ws_bytes, void* stream) {
+                       void* ws, size_t ws_bytes, void* stream, bool short_k = false) {
   const qsa_status st = check_kv_dims(dims);
   if (st != QSA_OK) return st;
   if (prefix_pages < 0 || prefix_pages > dims->max_pages || (prefix_pages > 0 && !prefix_table))
@@ -26,7 +26,7 @@ qsa_status prefix_attn(const qsa_dims* dims, int32_t alone, int32_t prefix_pages
   qsa_prefix_workspace_size(dims, prefix_pages, &need);
   if (!ws || !aligned(ws, 256) || ws_bytes < need) return QSA_ERR_WORKSPACE;
   return from_cuda(launch_paged_attn(*dims, 0, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos, out, lse, ws,
-                                 static_cast<cudaStream_t>(stream), false,
+                                 static_cast<cudaStream_t>(stream), short_k,
                                  Prefix{prefix_table, prefix_pages * dims->page_size, alone}));
 }
 
@@ -72,6 +72,15 @@ qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t pre
   if (alone != 0 && alone != 1) return QSA_ERR_INVALID_ARG;
   return prefix_attn(dims, alone, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos,
                      out, lse, ws, ws_bytes, stream);
+}
+
+qsa_status qsa_test_prefix_attn_timeout(const qsa_dims* dims, int32_t prefix_pages, const int32_t* prefix_table,
+                                        const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* page_table, const int32_t* q_pos,
+                                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (prefix_pages < 1) return QSA_ERR_INVALID_ARG;
+  return prefix_attn(dims, 0, prefix_pages, prefix_table, q, k_cache, v_cache, k_scale, v_scale, page_table, q_pos,
+                     out, lse, ws, ws_bytes, stream, true);
 }
 
 qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const void* k_cache, const float* k_scale,

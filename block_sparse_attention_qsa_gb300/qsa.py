@@ -49,8 +49,8 @@ KV_EXPORTS = (
 )
 # and those of include/qsa_serve.h, the operators for serving a batch in a bounded cache
 SERVE_EXPORTS = (
-    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_test_prefix_attn", "qsa_kv_weight",
-    "qsa_test_kv_weight_timeout", "qsa_kv_evict", "qsa_verify_drafts",
+    "qsa_prefix_workspace_size", "qsa_prefix_attn", "qsa_test_prefix_attn", "qsa_test_prefix_attn_timeout",
+    "qsa_kv_weight", "qsa_test_kv_weight_timeout", "qsa_kv_evict", "qsa_verify_drafts",
 )
 TRACE_SCORE, TRACE_TOPK, TRACE_ATTN = 0, 1, 2  # qsa_trace_read tables
 TRACE_SLOTS, TRACE_CTAS = 8, 4096
@@ -161,6 +161,7 @@ def _load() -> ctypes.CDLL:
         "qsa_prefix_workspace_size": (I, [D, N, ctypes.POINTER(SZ)]),
         "qsa_prefix_attn": (I, [D, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_test_prefix_attn": (I, [D, N, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "qsa_test_prefix_attn_timeout": (I, [D, N, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_weight": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_test_kv_weight_timeout": (I, [D, F, P, P, P, P, P, P, P, P, SZ, P]),
         "qsa_kv_evict": (I, [D, N, N, N, N, P, P, P, P, P, P, P, P, P, P, SZ, P]),
@@ -833,6 +834,16 @@ def test_prefix_attn(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_tabl
     """qsa_test_prefix_attn: prefix_attn with the prefix read once for all
     requests, or with ``alone`` by each for itself, whatever its size. For tests."""
     _prefix_attn(lib.qsa_test_prefix_attn, "qsa_test_prefix_attn", d, (int(alone),), q, k_cache, v_cache, k_scale,
+                 v_scale, prefix_table, page_table, q_pos, out, ws, lse, stream)
+
+
+def test_prefix_attn_timeout(d: Dims, q, k_cache, v_cache, k_scale, v_scale, prefix_table, page_table, q_pos, out, ws,
+                             lse=None, stream=None):
+    """qsa_test_prefix_attn_timeout: prefix_attn with the prefix read once, by
+    copies of half the bytes its kernel waits for, so that its bounded waits run
+    out (about a second); check_errors then reports ERR_TIMEOUT. For
+    failure-detection tests."""
+    _prefix_attn(lib.qsa_test_prefix_attn_timeout, "qsa_test_prefix_attn_timeout", d, (), q, k_cache, v_cache, k_scale,
                  v_scale, prefix_table, page_table, q_pos, out, ws, lse, stream)
 
 

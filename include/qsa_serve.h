@@ -70,6 +70,14 @@ qsa_status qsa_test_prefix_attn(const qsa_dims* dims, int32_t alone, int32_t pre
                                 const float* v_scale, const int32_t* page_table, const int32_t* q_pos, void* out,
                                 float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* Test hook for failure detection: qsa_prefix_attn with the prefix read once (at
+ * least one page) and copies of its K that bring half of the bytes its kernel
+ * waits for, as qsa_test_paged_attn_timeout (kind 5, QSA_ERR_TIMEOUT). */
+qsa_status qsa_test_prefix_attn_timeout(const qsa_dims* dims, int32_t prefix_pages, const int32_t* prefix_table,
+                                        const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* page_table, const int32_t* q_pos,
+                                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* The attention weight that each cached position gets from the newest tokens:
  *   weight[r][t] = decay * weight[r][t]
  *                + sum over j with t <= q_pos[r][j], and over query heads h, of

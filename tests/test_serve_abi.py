@@ -101,6 +101,15 @@ def test_prefix_attn_refusals(qsa):
 
 
 @no_device
+def test_prefix_timeout_hook_refuses_as_prefix_attn(qsa):
+    d = qsa.make_dims(3, 2, 100, 10, 40)
+    good = [d, 4, F, F, F, F, None, None, F, F, F, F, F, BIG, None]
+    for i, x, st in ((0, None, qsa.ERR_INVALID_ARG), (1, 0, qsa.ERR_INVALID_ARG), (1, 11, qsa.ERR_INVALID_ARG),
+                     (2, None, qsa.ERR_INVALID_ARG), (10, OFF8, qsa.ERR_INVALID_ARG), (13, 255, qsa.ERR_WORKSPACE)):
+        assert qsa.lib.qsa_test_prefix_attn_timeout(*_with(good, i, x)) == st, i
+
+
+@no_device
 def test_kv_weight_refusals(qsa):
     d = qsa.make_dims(3, 2, 100, 10, 40, kv_dtype="fp8")
     good = [d, 0.5, F, F, F, F, F, F, F, F, 256, None]

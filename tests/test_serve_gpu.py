@@ -555,6 +555,37 @@ def test_prefix_refusals(qsa):
             qsa.prefix_workspace_size(d, bad)
 
 
+@pytest.mark.parametrize("kv,D,prefix,own,n_q,hk", [
+    ("bf16", 128, 40, [5, 300, 70, 0], 4, 2), ("fp8", 128, 300, [70] * 20, 4, 2), ("fp8", 64, 9, [33, 1], 1, 4),
+    ("bf16", 64, 200, [9] * 40, 2, 1), ("bf16", 256, 70, [9, 500], 2, 2), ("fp8", 256, 70, [9, 500], 2, 2)])
+def test_prefix_wait_runs_out_and_reports_a_timeout(qsa, kv, D, prefix, own, n_q, hk):
+    # As for the dense attention: the prefix's copies of K bring half of the
+    # bytes, every CTA's wait for its first tile runs out, and all of its roles
+    # end: the next calls are complete. (One row tile a CTA, two, and with an
+    # E4M3 cache the warpgroup that widens; few tiles a CTA and more than the
+    # copies have room for.)
+    import time
+
+    c = Prefixed(qsa, prefix, own, n_q, 16, hk, D, kv=kv)
+    c.run(qsa, alone=False)
+    _ok(qsa, c.ws)
+    want, want_lse = c.out.clone(), c.lse.clone()
+    torch.cuda.synchronize()
+    t0 = time.time()
+    qsa.test_prefix_attn_timeout(*c.args, lse=c.lse)
+    torch.cuda.synchronize()
+    waited = time.time() - t0
+    st, info = qsa.check_errors(c.ws)
+    assert st == qsa.ERR_TIMEOUT and info[0] == 5, info
+    assert 0.2 < waited < 30, waited
+    for _ in range(3):
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        c.run(qsa, alone=False)
+        _ok(qsa, c.ws)
+        assert torch.equal(c.out, want) and torch.equal(c.lse, want_lse)
+
+
 # --------------------------------------------------------------------------
 # attention weight of the cached positions
 # --------------------------------------------------------------------------
