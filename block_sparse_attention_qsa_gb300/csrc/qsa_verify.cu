@@ -219,13 +219,15 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     // m: drafts accepted; end 0: draft m was rejected, 1: there was none, 2: no request
     const int x = lane < a.n_draft ? tokens[lane] : -1;
     const bool valid = (unsigned)x < (unsigned)a.vocab;
+    // (rows behind the last draft are not looked at: a padded request may have none)
+    const int drafts = __ffs(~__ballot_sync(kFull, valid)) - 1;  // (lane 31 is never a draft)
     bool ok = false;
-    if (valid) {
+    if (lane < drafts) {
       const float p = fminf(fmaxf(load(target + lane * a.target_row + x), 0.f), 1.f);
       const float q = draft ? fminf(fmaxf(load(draft + lane * a.draft_row + x), 0.f), 1.f) : 1.f;
       ok = (double)as_uniform(uniform[lane]) * (double)q < (double)p;
     }
-    const int m = min(a.n_draft, __ffs(~__ballot_sync(kFull, ok)) - 1);  // (lane 31 is never a draft)
+    const int m = __ffs(~__ballot_sync(kFull, ok)) - 1;
     if (lane == min(m, 31)) {
       const bool none = m == 0 && x == -2;
       s_m = m;

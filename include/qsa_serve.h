@@ -170,8 +170,10 @@ typedef struct {
  *
  * A token outside 0..vocab - 1 other than -1 ends the drafts too; it is
  * reported (kind 7), but for -2 as a request's first token, which stands for
- * no request (a padded batch): accepted[r] = 0, out_tokens[r] = -1 everywhere,
- * nothing else is read.
+ * no request (a padded batch): accepted[r] = 0, out_tokens[r] = -1 everywhere.
+ * Of target and draft, only the rows of a request's drafts up to their end, and
+ * target's one behind them, are read: a request that is none needs no rows. Its
+ * other tokens and random numbers have no effect.
  *
  * target and draft are fp32 or bf16 (prob_dtype), tokens int32
  * [batch][n_draft], uniform fp32 [batch][n_draft + 1], accepted int32 [batch],

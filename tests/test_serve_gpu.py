@@ -1256,6 +1256,34 @@ def test_verify_offsets_past_32_bits(qsa):
     assert (out[:-2] == -1).all() and (accepted[:-2] == 0).all()
 
 
+@pytest.mark.parametrize("dt,V", [(torch.float32, 3001), (torch.bfloat16, 40000)])
+def test_verify_rows_that_are_not_there(qsa, dt, V):
+    # Padded requests whose other tokens are in the vocabulary, and drafts that
+    # end early with such tokens behind the end: through the C entry point, with
+    # rows of the first requests only (what lies behind them belongs to another
+    # tensor) and NaN in the rows behind the end. None of it is looked at.
+    B, live, n = 6, 3, 4
+    target, draft, tokens, u = _sampled(B, n, V, dt, 17, 0.9)
+    u[:, :n] = 0
+    tokens[live:, 0] = -2
+    tokens[0, 2] = -1
+    target[0, 3:], draft[0, 2:] = math.nan, math.nan
+    want, want_out = _verify_case(qsa, target, draft, tokens, u)
+    assert want.tolist() == [2, n, n, 0, 0, 0] and (want_out[live:] == -1).all()
+    held = torch.full((2, B * (n + 1) * V), math.nan, dtype=dt, device="cuda")
+    held[0, :live * (n + 1) * V] = target[:live].reshape(-1)
+    held[1, :live * n * V] = draft[:live].reshape(-1)
+    ws = qsa.make_kv_workspace(qsa.make_dims(1, 1, 1, 1, 1))
+    accepted = torch.full((B,), 77, dtype=torch.int32, device="cuda")
+    out = torch.full((B, n + 1), 77, dtype=torch.int32, device="cuda")
+    st = qsa.lib.qsa_verify_drafts(B, n, V, qsa.PROB_DTYPES[dt], held[0].data_ptr(), None, held[1].data_ptr(), None,
+                                   tokens.data_ptr(), u.data_ptr(), accepted.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == qsa.OK
+    _ok(qsa, ws)
+    assert torch.equal(accepted, want) and torch.equal(out, want_out)
+
+
 def test_verify_refusals(qsa):
     target, draft, tokens, u = _sampled(4, 3, 100, torch.float32, 16)
     ws = qsa.make_kv_workspace(qsa.make_dims(1, 1, 1, 1, 1))
