@@ -8,6 +8,7 @@ namespace qsa {
 
 constexpr int kErrToken = 7;   // qsa_verify_drafts: a drafted token outside the vocabulary
 constexpr int kErrLength = 8;  // qsa_kv_evict: a length outside the page table
+constexpr int kErrHeavy = 9;   // qsa_verify_drafts: weights that sum to 16 or more
 
 // short_k: the failure-detection test (qsa_test_kv_weight_timeout)
 cudaError_t launch_kv_weight(const qsa_dims& d, float decay, const void* q, const void* k_cache, const float* k_scale,

@@ -44,7 +44,8 @@ __device__ __forceinline__ float load(const __nv_bfloat16* p) {
 // most 2^-21 each) to 2^-13, those on 2^-54 (at most 2^-38) to 2^-30, that is
 // for kMost values. The last part's rounding is to nearest, ties to even, and so
 // is the whole value's. A probability that is negative or NaN is 0, one above 1
-// is 1 (saturated).
+// is 1 (saturated). Where the first sums came near 2^4, which no row of
+// probabilities does, the values are added again as integers (full()).
 struct Exact {
   static constexpr int kMost = 256;
   static constexpr float kM1 = 1.5f * 0x1p3f, kM2 = 1.5f * 0x1p-14f, kM3 = 1.5f * 0x1p-31f;
@@ -78,6 +79,9 @@ struct Exact {
   static __device__ __forceinline__ int64_t combine(int i1, int i2, int i3) {
     return (int64_t)i1 * (1LL << 34) + (int64_t)i2 * (1LL << 17) + i3;
   }
+  // whether a sum on the grid of 2^-20 may have passed 2^4 on its way (a weight's
+  // two values are at most 1, so never by more than 1 past its end)
+  __device__ __forceinline__ bool full() const { return fminf(a1.x, a1.y) <= -14.f; }
   __device__ __forceinline__ int64_t sum() const {  // in 2^-54ths
     const int i1 = __float2int_rn(a1.x * 0x1p20f) + __float2int_rn(a1.y * 0x1p20f);
     const int i2 = __float2int_rn(a2.x * 0x1p37f) + __float2int_rn(a2.y * 0x1p37f);
@@ -85,6 +89,10 @@ struct Exact {
     return -combine(i1, i2, i3);
   }
 };
+// Sums of weights are kept at most kHeavy, 16 in 2^-54ths, so that none of them
+// passes 64 bits; a row with that much is no row of probabilities (reported).
+constexpr uint64_t kHeavy = 1ULL << 58;
+__device__ __forceinline__ uint64_t at_most_heavy(uint64_t x) { return x < kHeavy ? x : kHeavy; }
 __device__ __forceinline__ float as_uniform(float u) { return fminf(fmaxf(u, 0.f), 0x1.fffffep-1f); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -129,8 +137,9 @@ struct Weights {
   // sum over a lane's share of first .. end - 1, kDeep loads of a row in flight
   __device__ __forceinline__ uint64_t sum(int first, int end) const {
     const int lane = threadIdx.x & 31;
-    int64_t all = 0;
+    uint64_t all = 0;
     int v = first + lane;
+    bool full = false;
     while (v + 32 * (kDeep - 1) < end) {
       Exact s;
       for (int z = 0; z < Exact::kMost / 2 / kDeep && v + 32 * (kDeep - 1) < end; ++z, v += 32 * kDeep) {
@@ -149,16 +158,22 @@ struct Weights {
           for (int i = 0; i < kDeep; i += 2) s.add(make_float2(x[i], x[i + 1]));
         }
       }
-      all += s.sum();
+      all = at_most_heavy(all + (uint64_t)s.sum());
+      full |= s.full();
     }
-    for (; v < end; v += 32) all += (int64_t)at(v);
-    return (uint64_t)all;
+    if (full) {  // all of them again, as integers
+      all = 0;
+      v = first + lane;
+    }
+    for (; v < end; v += 32) all = at_most_heavy(all + at(v));
+    return all;
   }
   // the same where both rows and `first` are at 16-byte boundaries
   __device__ __forceinline__ uint64_t sum_vec(int first, int end) const {
     constexpr int kVec = 16 / sizeof(T), kStep = 32 * kVec, kLoads = kDeep / 4;
-    int64_t all = 0;
+    uint64_t all = 0;
     int v = first + (int)(threadIdx.x & 31) * kVec;
+    bool full = false;
     while (v + kStep * (kLoads - 1) + kVec <= end) {
       Exact s;
       for (int z = 0; z < Exact::kMost / 2 / (kVec * kLoads) && v + kStep * (kLoads - 1) + kVec <= end;
@@ -185,11 +200,16 @@ struct Weights {
             }
         }
       }
-      all += s.sum();
+      all = at_most_heavy(all + (uint64_t)s.sum());
+      full |= s.full();
+    }
+    if (full) {  // all of them again, as integers
+      all = 0;
+      v = first + (int)(threadIdx.x & 31) * kVec;
     }
     for (; v < end; v += kStep)
-      for (int e = 0; e < kVec && v + e < end; ++e) all += (int64_t)at(v + e);
-    return (uint64_t)all;
+      for (int e = 0; e < kVec && v + e < end; ++e) all = at_most_heavy(all + at(v + e));
+    return all;
   }
   static __device__ __forceinline__ float value(const uint4& x, int e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -262,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   for (int pass = 0; pass < 2; ++pass) {
     const int g0 = min(s0 + warp * seg, s1);
     const int g1 = min(g0 + seg, s1);
-    const uint64_t mine = warp_sum(VEC ? w.sum_vec(g0, g1) : w.sum(g0, g1));
+    const uint64_t mine = at_most_heavy(warp_sum(VEC ? w.sum_vec(g0, g1) : w.sum(g0, g1)));
     if (lane == 0) s_seg[warp] = mine;
     __syncthreads();
     if (warp == 0) {
-      const uint64_t own = warp_sum(lane < kWarps ? s_seg[lane] : 0);
+      const uint64_t own = at_most_heavy(warp_sum(lane < kWarps ? s_seg[lane] : 0));
       if (lane < ctas) st_peer_u64(peer_addr(&s_slice[pass][rank], lane), own);
     }
     cluster_sync();
@@ -281,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         w.token = -1;
         continue;
       }
+      return;
+    }
+    if (total >= kHeavy) {
+      if (rank == 0 && threadIdx.x == 0) record_error(a.err, kErrHeavy, r, m, 0);
       return;
     }
     const uint64_t t = __umul64hi(total, u);  // floor(u S)

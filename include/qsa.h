@@ -355,8 +355,8 @@ qsa_status qsa_draft_attn(const qsa_dims* dims, const void* q, const void* k_cac
  * 4 int32: error kind (1 query position, 2 page id, 3 selected position,
  * 4 draft query not after its reused selection, 5 a bounded wait inside a
  * kernel gave up, 6 new tokens of a request that are not consecutive, see
- * qsa_kv.h, 7 a drafted token, 8 a request's length, see qsa_serve.h), request,
- * query, offending value. */
+ * qsa_kv.h, 7 a drafted token, 8 a request's length, 9 a row that is no row of
+ * probabilities, see qsa_serve.h), request, query, offending value. */
 qsa_status qsa_check_errors(void* ws, void* stream, int32_t* info);
 
 #ifdef __cplusplus

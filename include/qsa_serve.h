@@ -16,7 +16,8 @@
  * the supported geometry those of qsa_kv.h. Errors found on the device go to
  * the workspace header (qsa_check_errors): kinds as in qsa.h, and
  *   7  a drafted token outside the vocabulary (request, draft, token),
- *   8  a request's length outside its page table (request, 0, length).
+ *   8  a request's length outside its page table (request, 0, length),
+ *   9  weights to sample from that sum to 16 or more (request, row, 0).
  */
 #ifndef QSA_SERVE_H_
 #define QSA_SERVE_H_
@@ -163,10 +164,10 @@ typedef struct {
  *
  * The test is exact. So are the sums, of probabilities rounded to multiples of
  * 2^-54: the result does not depend on an order, and is that of the formula in
- * 64 bits. A row's probabilities must sum to less than 16; they need not sum to
- * 1. One that is negative or NaN counts as 0, one above 1 as 1. A u below 0 or
- * NaN counts as 0, one of 1 or more as the largest below 1. Where p_m so rounded
- * is 0 everywhere, y is -1.
+ * 64 bits. A probability that is negative or NaN counts as 0, one above 1 as 1;
+ * a row's need not sum to 1, but weights to sample from that sum to 16 or more
+ * are reported (kind 9), and y is -1. A u below 0 or NaN counts as 0, one of 1
+ * or more as the largest below 1. Where p_m so rounded is 0 everywhere, y is -1.
  *
  * A token outside 0..vocab - 1 other than -1 ends the drafts too; it is
  * reported (kind 7), but for -2 as a request's first token, which stands for

@@ -1196,6 +1196,71 @@ def test_verify_tiny_probabilities(qsa):
     _verify_case(qsa, target, draft, tokens, u)
 
 
+def _heavy(dt, V, ones, rest=0.0, seed=19):
+    """Two requests, a draft each: `ones` probabilities of 1, all of them a
+    thread's where V is 2^20 (every 256th token of a warp's first 4,096), and
+    about `rest` in all the others."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    row = torch.rand(V, generator=g, device="cuda") * (2 * rest / V)
+    row[torch.arange(ones, device="cuda") * (256 if V > 4096 else 1)] = 1.0
+    return row.to(dt).expand(2, 2, V).contiguous(), torch.zeros((2, 1), dtype=torch.int32, device="cuda"), g
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [40, 1001, 1 << 20, (1 << 20) + 1])
+def test_verify_rows_that_sum_to_nearly_16(qsa, dt, V):
+    # sums of up to 16 less 2^-24, with the largest of them in one thread's hands
+    target, tokens, g = _heavy(dt, V, 15, 0.9)
+    tokens[:] = -1  # sampled from the first row
+    for u in (0.0, 0.3, 0.93, 0.95, 1.0 - 2.0 ** -24):
+        _verify_case(qsa, target, None, tokens, torch.full((2, 2), u, device="cuda"))
+    if dt == torch.float32:
+        target[:, 0] = 0
+        target[:, 0, :16] = 1.0
+        target[:, 0, 15] = 1.0 - 2.0 ** -24
+        for u in (0.0, 0.5, 0.99, 1.0 - 2.0 ** -24):
+            _verify_case(qsa, target, None, tokens, torch.full((2, 2), u, device="cuda"))
+    # p of far more than 16, and p - q of 15 and a little in the same places
+    target, tokens, _ = _heavy(dt, V, 15)
+    draft = (torch.rand((2, 1, V), generator=g, device="cuda") / 2).to(dt)
+    target[:, :1] = draft
+    at = torch.arange(15, device="cuda") * (256 if V > 4096 else 1)
+    target[:, 0, at], draft[:, 0, at] = 1.0, 0.0
+    target[:, 0, V - 1] = draft[:, 0, V - 1] + 0.25
+    tokens[:] = 20 if V <= 4096 else 21
+    target[:, 0, int(tokens[0, 0])] = 0.0  # (rejected)
+    for u in (0.0, 0.3, 0.95, 0.99, 1.0 - 2.0 ** -24):
+        _verify_case(qsa, target, draft, tokens, torch.full((2, 2), u, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,ones", [(40, 16), (40, 40), (1001, 17), (1001, 1001), (40000, 40000), (1 << 20, 16),
+                                    ((1 << 20) + 1, 17), (1 << 24, 1 << 24)])
+def test_verify_reports_rows_that_sum_to_16_or_more(qsa, dt, V, ones):
+    # (their exact sums are past what the kernel's hold: 2^24 ones are 2^78 of its steps)
+    target, tokens, _ = _heavy(dt, V, min(ones, 17))
+    if ones > 17:
+        target[:] = 1.0
+    u = torch.full((2, 2), 0.99, device="cuda")
+    ws = qsa.make_kv_workspace(qsa.make_dims(1, 1, 1, 1, 1))
+    for first, row in ((-1, 0), (0, 1)):  # no draft, and one that is accepted
+        tokens[:] = first
+        tokens[1] = -2
+        accepted = torch.full((2,), 77, dtype=torch.int32, device="cuda")
+        out = torch.full((2, 2), 77, dtype=torch.int32, device="cuda")
+        qsa.verify_drafts(target, None, tokens, u, accepted, out, ws)
+        st, info = qsa.check_errors(ws)
+        assert st == qsa.ERR_BAD_INDEX and info == (9, 0, row, 0)
+        assert accepted.tolist() == [row, 0] and out.tolist() == [[0, -1] if row else [-1, -1], [-1, -1]]
+    # the rows beside it are sampled from as ever
+    target[1] = 0
+    target[1, :, 7] = 0.5
+    tokens[:] = -1
+    qsa.verify_drafts(target, None, tokens, u, accepted, out, ws)
+    st, info = qsa.check_errors(ws)
+    assert info == (9, 0, 0, 0) and out.tolist() == [[-1, -1], [7, -1]]
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_verify_strides(qsa, dt):
     B, n, V = 5, 3, 9001
