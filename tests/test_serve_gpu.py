@@ -915,6 +915,39 @@ def test_evict_long_and_many(qsa, lengths, keep):
     _evict_case(qsa, lengths, keep, 4, 16, 1, 64, 16)
 
 
+@pytest.mark.parametrize("lengths,keep,sinks,recent", [([30000, 12000, 7], 6000, 2000, 4000), ([30000], 64, 0, 64),
+                                                       ([20001, 30000], 9000, 9000, 0)])
+def test_evict_nothing_to_choose_over_several_ctas(qsa, lengths, keep, sinks, recent):
+    _evict_case(qsa, lengths, keep, sinks, recent, 1, 64, 16)
+
+
+@pytest.mark.parametrize("kind", ["mixed", "equal"])
+def test_evict_slices_longer_than_what_is_held(qsa, kind):
+    # 160 requests have a CTA each, which holds 16,384 weights of 20,000 positions
+    # in shared memory; where all are equal, the last of them that stays is in front
+    # of the end of those, at it and behind it
+    lengths = [20000, 16384, 16385, 19999, 16400] + [0, 3, 50] * 51 + [20000, 17]
+    assert len(lengths) == 160
+    for keep in ((9000,) if kind == "mixed" else (16380, 16390, 17000)):
+        _evict_case(qsa, lengths, keep, 4, 6, 1, 64, 16, "fp8",
+                    mutate=None if kind == "mixed" else lambda c: c.weight.fill_(0.5))
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("lengths,keep", [([30000, 9001, 40], 5000), ([700, 1001], 300)])
+def test_evict_weights_at_any_offset(qsa, offset, lengths, keep):
+    # arrays that start at multiples of 4 bytes, not of 16
+    c = Evicted(qsa, lengths, keep, 4, 16, 1, 64, 16)
+    for i in (6, 7):
+        t = c.args[i]
+        c.args[i] = torch.full((t.numel() + offset,), 7.0, device="cuda")[offset:].view(t.shape).copy_(t)
+        assert c.args[i].data_ptr() % 16 == 4 * offset
+    c.weight_out = c.args[7]
+    c.run(qsa)
+    _ok(qsa, c.ws)
+    c.compare()
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "special", "negative", "close", "ascending", "descending"])
 def test_evict_weights(qsa, kind):
     def mutate(c):
@@ -1178,6 +1211,27 @@ def test_verify_rows_without_weight(qsa, dt):
     target[5, 0] = math.nan
     target[5, 0, 3] = 2.0             # above 1 as 1
     _verify_case(qsa, target, draft, tokens, u)
+    _verify_case(qsa, target, None, tokens, u)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [40000, 40001])
+def test_verify_rows_without_weight_over_several_ctas(qsa, dt, V):
+    # the difference is 0 everywhere: a second pass of the cluster, over the
+    # target's row as it is; and rows without anything, for which y is -1
+    n = 2
+    target, draft, tokens, u = _sampled(5, n, V, dt, 23)
+    u[:, :n] = 1.0
+    draft[0], draft[1] = target[0, :n], target[1, :n]
+    target[2, 0] = 0                  # nothing at all
+    draft[3, 0] = 1.0                 # p is below q everywhere
+    target[4, 0] = 0
+    target[4, 0, V - 1] = 2.0 ** -40  # the last token alone, in the target
+    draft[4, 0] = 2.0 ** -30
+    for x in (0.0, 0.4, 0.9, 1.0 - 2.0 ** -24):
+        u[:, n] = x
+        _verify_case(qsa, target, draft, tokens, u)
+    tokens[4, 0] = V - 1  # greedy, and the only token that has weight is the rejected one
     _verify_case(qsa, target, None, tokens, u)
 
 
