@@ -14,7 +14,7 @@
 // The sums are exact, so that they do not depend on how the row is split: the
 // threshold floor(u S) falls between the same two tokens in any order, and both
 // readings of a segment agree. A weight is p, or p - q where p > q, each rounded
-// to a multiple of 2^-54. As 64-bit integers these cost the integer pipe 36
+// to a multiple of 2^-54 (what is smaller has no weight). As 64-bit integers these cost the integer pipe 36
 // cycles a value and warp, and 256 rows of 150,001 tokens (FP32, sampled drafts)
 // 81 us; the conversion instruction to 64 bits was slower still, 158. So they
 // are added in FP32 without rounding (see Exact), 11 additions for two values:

@@ -156,18 +156,24 @@ typedef struct {
  *   draft j is accepted while  u[j] q_j(x[j]) < p_j(x[j]);
  *   with m the number accepted, the next token y is sampled with u[n_draft]
  *     from max(p_m - q_m, 0) where draft m was rejected, and from p_m where
- *     there was none left (or where that difference is 0 everywhere);
+ *     there was none left (or where that difference, rounded as below, is 0
+ *     everywhere);
  *   sampled: the lowest y with  u[n_draft] sum_v w(v) < sum_{v <= y} w(v).
  * draft NULL: the drafts were not sampled; q_j is 1 at x[j] and 0 elsewhere.
  * Writes accepted[r] = m and out_tokens[r] = x[0 .. m - 1], y, then -1
  * (n_draft + 1 entries). The distribution so sampled is the target's.
  *
- * The test is exact. So are the sums, of probabilities rounded to multiples of
- * 2^-54: the result does not depend on an order, and is that of the formula in
- * 64 bits. A probability that is negative or NaN counts as 0, one above 1 as 1;
- * a row's need not sum to 1, but weights to sample from that sum to 16 or more
- * are reported (kind 9), and y is -1. A u below 0 or NaN counts as 0, one of 1
- * or more as the largest below 1. Where p_m so rounded is 0 everywhere, y is -1.
+ * The test is exact. For the sampling every probability is rounded to a multiple
+ * of 2^-54; the sums of those are exact, so that the result does not depend on an
+ * order and is the formula's for probabilities so rounded. Against the ones given
+ * a weight is off by at most 2^-54, and all of them together by vocab times that
+ * (2^-36 with 150,001 tokens): where the weights sum to S, what is sampled is off
+ * by at most vocab 2^-54 / S. A token whose p - q is less than 2^-54 may have no
+ * weight, a row of nothing but values of 2^-55 or less none at all. A
+ * probability that is negative or NaN counts as 0, one above 1 as 1; a row's
+ * need not sum to 1, but weights to sample from that sum to 16 or more are
+ * reported (kind 9), and y is -1. A u below 0 or NaN counts as 0, one of 1 or
+ * more as the largest below 1. Where p_m so rounded is 0 everywhere, y is -1.
  *
  * A token outside 0..vocab - 1 other than -1 ends the drafts too; it is
  * reported (kind 7), but for -2 as a request's first token, which stands for

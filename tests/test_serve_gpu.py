@@ -1250,6 +1250,26 @@ def test_verify_tiny_probabilities(qsa):
     _verify_case(qsa, target, draft, tokens, u)
 
 
+def test_verify_differences_below_the_rounding(qsa):
+    # p - q of 2^-56 everywhere, by p's and q's roundings to 2^-54 nothing: sampled
+    # from p; one difference of 2^-53 among them has all the weight; values of
+    # 2^-55 and below (ties go to even) none
+    V, n = 2000, 1
+    p = 2.0 ** -32
+    target = torch.full((4, n + 1, V), p, device="cuda")
+    draft = torch.full((4, n, V), p * (1 - 2.0 ** -24), device="cuda")
+    tokens = torch.full((4, n), 9, dtype=torch.int32, device="cuda")
+    assert (target[0, 0] > draft[0, 0]).all()
+    draft[:, :, 9] = 0.5
+    draft[1, 0, 1234] = p * (1 - 2.0 ** -21)
+    target[2] = 2.0 ** -55
+    target[3] = 2.0 ** -55
+    target[3, 0, 77] = 1.5 * 2.0 ** -55
+    u = torch.full((4, n + 1), 0.5, device="cuda")
+    accepted, out = _verify_case(qsa, target, draft, tokens, u)
+    assert accepted.tolist() == [0] * 4 and out[:, 0].tolist() == [V // 2, 1234, -1, 77]
+
+
 def _heavy(dt, V, ones, rest=0.0, seed=19):
     """Two requests, a draft each: `ones` probabilities of 1, all of them a
     thread's where V is 2^20 (every 256th token of a warp's first 4,096), and
