@@ -851,7 +851,8 @@ def kv_weight(d: Dims, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, 
     """weight (fp32 [B][max_pages * page_size]) = decay * weight + the softmax
     weight that each position gets from the newest tokens' query heads, given
     the lse that paged_attn or prefix_attn returned for them (fp32
-    [B][n_q][H_q]). Positions that no query sees are left as they are."""
+    [B][n_q][H_q]). Positions that no query sees are left as they are. A q_pos of
+    -1 leaves a token out: a draft that was not accepted."""
     st = _fast.kv_weight(d, decay, q, k_cache, k_scale, page_table, q_pos, lse, weight, ws, stream)
     if st == OK:
         return
@@ -895,7 +896,9 @@ def kv_evict(d: Dims, k_cache, v_cache, page_table, page_table_out, length, weig
     old positions go to kept (int32 [B][keep], ascending, -1 behind the last),
     their number to new_length (int32 [B]; it may be length), their K and V to
     the pages of page_table_out (int32 [B][n]), their weights to weight_out
-    (fp32 [B][n * page_size], 0 behind the last)."""
+    (fp32 [B][n * page_size], 0 behind the last). Keys stay as they were rotated:
+    later tokens are rotated at their true positions (rope) and then appended at
+    new_length and on without a rope."""
     st = _fast.kv_evict(d, k_cache, v_cache, page_table, page_table_out, length, weight, weight_out, kept, new_length,
                         ws, sinks, recent, stream)
     if st == OK:

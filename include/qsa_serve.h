@@ -8,8 +8,9 @@
  * from one context attend with qsa_prefix_attn (which also gives their lse),
  * qsa_verify_drafts turns the target's probabilities of the verified tokens
  * into the tokens that stay, qsa_kv_weight keeps account of which positions
- * are attended to, and qsa_kv_evict brings a request that has grown too long
- * back to its bound.
+ * are attended to (by the tokens that stay: see there), and qsa_kv_evict brings
+ * a request that has grown too long back to its bound (how its later tokens are
+ * rotated: see there).
  *
  * Cache, page table, scales, positions, error record and execution rules are
  * those of qsa.h and qsa_kv.h, the fields of qsa_dims that are looked at and
@@ -92,7 +93,10 @@ qsa_status qsa_test_prefix_attn_timeout(const qsa_dims* dims, int32_t prefix_pag
  * weight holds is not read. A row whose lse is -infinity, or whose position is
  * -1 (or outside the page table: reported, kind 1), adds nothing. A position
  * whose page id is outside the cache is reported (kind 2) and gets no new
- * weight. FP32 scores, exponentials and sums, added in a fixed order (the same
+ * weight. Called behind qsa_verify_drafts, with a q_pos of -1 for the drafts that
+ * were not accepted, it leaves them out, and their places' weights as they were:
+ * a later token takes what weight holds at its place, so that has to be 0 where
+ * no token is (weight starts as zeros; an eviction leaves 0). FP32 scores, exponentials and sums, added in a fixed order (the same
  * call gives the same bits); with an E4M3 cache a component of q is off by at
  * most 2^-22 of its head's largest. ws needs 256 bytes (its header). */
 qsa_status qsa_kv_weight(const qsa_dims* dims, float decay, const void* q, const void* k_cache, const float* k_scale,
@@ -120,8 +124,16 @@ qsa_status qsa_test_kv_weight_timeout(const qsa_dims* dims, float decay, const v
  * new_len - 1. A token whose new place is its old one is not copied, so a page
  * of both tables at the same index whose positions all stay where they are (a
  * shared prefix below `sinks`) may be in both; every other page that the call
- * writes to must not be read by it or written for another request. Keys stay
- * as they were rotated.
+ * writes to must not be read by it or written for another request.
+ *
+ * Keys stay as they were rotated, at the tokens' true positions, which from here
+ * on are no longer their places (the caller keeps the number of tokens that a
+ * request has had). So the tokens that follow are rotated and placed apart:
+ * qsa_rope of their queries and keys at the true positions, then qsa_kv_append
+ * without a rope at new_len and on (a rotated key is rounded to BF16 on the way,
+ * in front of an E4M3 code too), then attention and weights with these places as
+ * q_pos. qsa_kv_append's own rotation is at the place, which is wrong here, and
+ * nothing can report it.
  *
  * keep is 1..out_pages * page_size, sinks and recent at least 0 with sinks +
  * recent <= keep. weight is fp32 [batch][max_pages * page_size], weight_out

@@ -1547,3 +1547,94 @@ def test_a_batch_branched_from_one_context(qsa, kv, attend):
         tol, tol_l = S.attn_tol(ref, mag, rl, qk, D, kv, small)
         assert np.all(np.abs(R.f64(out1)[r, 0] - ref) <= tol) and np.all(np.abs(R.f64(lse1)[r, 0] - rl) <= tol_l)
     assert torch.equal(kc[shared.long()], c.kc[shared.long()])  # the prefix was not touched
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_decoding_on_after_an_eviction(qsa, kv):
+    """Requests decoded on from a bounded cache as qsa_serve.h says: tokens
+    rotated at their true positions and appended at their places, the weights
+    taken of the tokens that verification keeps; evicted again."""
+    B, n_q, hk, hq, D, ps, keep, sinks, recent = 3, 3, 2, 8, 64, 16, 64, 4, 16
+    lengths = [150, 97, 33]
+    rope, top = qsa.make_rope(D), max(lengths)
+    table, pages = R.page_table(lengths, ps, 81, spare=0)
+    width, more = -(-(keep + 2 * n_q) // ps), 2 * B * -(-(keep + 2 * n_q) // ps)
+    kc, vc, ks, vs = R.make_cache(pages + more, hk, ps, D, kv, 82)
+    tables = [table] + [(torch.arange(B * width, dtype=torch.int32) + pages + i * B * width).view(B, width) for i in range(2)]
+    d = _dims(qsa, B, table.shape[1], pages + more, kv, n_q, hq, hk, D, ps)
+    d1 = _dims(qsa, B, width, pages + more, kv, n_q, hq, hk, D, ps)
+    ws = qsa.make_kv_workspace(d)
+    k, v = _normal((B, top, hk, D), 83), _normal((B, top, hk, D), 84)
+    pos = torch.arange(top, dtype=torch.int32).expand(B, -1).clone()
+    for r, n in enumerate(lengths):
+        pos[r, n:] = -1
+    qsa.kv_append(d, k, v, kc, vc, ks, vs, table.cuda(), pos.cuda(), ws, rope=rope)
+    w, amp = R.frequencies(D)
+    key_of = [list(R.rotate(R.f64(k)[r, :n], np.arange(n), w, amp, "half")) for r, n in enumerate(lengths)]
+    value_of = [list(R.f64(v)[r, :n]) for r, n in enumerate(lengths)]
+    true = [list(range(n)) for n in lengths]  # of the token at each place
+    had = list(lengths)
+    g = torch.Generator(device="cuda").manual_seed(85)
+    weight = torch.rand((B, table.shape[1] * ps), generator=g, device="cuda")
+    weight[pos_behind(lengths, weight.shape[1])] = 0
+    length = _i32(lengths)
+    now, dims = tables[0], d
+    for step, (after, accepted) in enumerate(zip(tables[1:], ([2, 0, 1], [1, 2, 0]))):
+        # bounded again
+        out_w = torch.empty((B, width * ps), device="cuda")
+        kept, place = torch.empty((B, keep), dtype=torch.int32, device="cuda"), torch.empty_like(length)
+        qsa.kv_evict(dims, kc, vc, now.cuda(), after.cuda(), length, weight, out_w, kept, place, ws, sinks=sinks, recent=recent)
+        for r in range(B):
+            stay = S.evict(weight[r].cpu().numpy(), int(length[r]), keep, sinks, recent)
+            assert kept[r, :len(stay)].tolist() == stay.tolist()
+            true[r] = [true[r][i] for i in stay]
+        now, dims, weight, length = after, d1, out_w, place.clone()
+        assert any(int(length[r]) < had[r] for r in range(B))
+        # n_q tokens more: rotated where they truly are, appended where there is room
+        q, k, v = (_normal((B, n_q, h, D), 90 + 3 * step + i) for i, h in enumerate((hq, hk, hk)))
+        j = torch.arange(n_q, device="cuda")
+        at, true_at = ((x.view(B, 1) + j).to(torch.int32) for x in (length, _i32(had)))
+        q_rot, k_rot = torch.empty_like(q), torch.empty_like(k)
+        qsa.rope(rope, q, true_at, q_rot)
+        qsa.rope(rope, k, true_at, k_rot)
+        qsa.kv_append(d1, k_rot, v, kc, vc, ks, vs, now.cuda(), at, ws)
+        out, lse = torch.empty_like(q), torch.empty((B, n_q, hq), device="cuda")
+        qsa.paged_attn(d1, q_rot, kc, vc, ks, vs, now.cuda(), at, out, ws, lse=lse)
+        m = _i32(accepted)
+        seen = torch.where(j <= m.view(B, 1), at, -1).to(torch.int32)
+        old = weight.clone()
+        qsa.kv_weight(d1, q_rot, kc, ks, now.cuda(), seen, lse, weight, ws, decay=0.5)
+        _ok(qsa, ws)
+        sc = [R.f64(s)[None, :, None] if kv == "fp8" else 1.0 for s in (ks, vs)]
+        for r in range(B):
+            n = int(length[r])
+            key_of[r] += list(R.rotate(R.f64(k)[r], np.arange(had[r], had[r] + n_q), w, amp, "half"))
+            value_of[r] += list(R.f64(v)[r])
+            true[r] += list(range(had[r], had[r] + n_q))
+            kk, vv = (R.rows(R.f64(x), now.numpy()[r], n + n_q) * s for x, s in zip((kc, vc), sc))
+            # the cache holds the tokens at their true positions: a key is rounded to
+            # BF16 and, with E4M3, to half a step of its code (2^-10 of the scale next
+            # to 0); the rotation's own arithmetic is FP32
+            for have, want in ((kk, key_of), (vv, value_of)):
+                want = np.array([want[r][t] for t in true[r]])
+                tol = (2.0 ** -8 + 2.0 ** -20) * np.abs(want) + 2.0 ** -20 * np.abs(want).max(-1, keepdims=True)
+                if kv == "fp8":
+                    tol = tol + 2.0 ** -4 * (np.abs(want) + tol) + 2.0 ** -10 * (sc[0] if have is kk else sc[1])
+                assert np.all(np.abs(have - want) <= tol)
+            for i in range(n_q):
+                ref, rl, mag, qk, small = R.attention(R.f64(q_rot)[r, i], kk, vv, 1 / math.sqrt(D), 0, n + i + 1)
+                tol, tol_l = S.attn_tol(ref, mag, rl, qk, D, kv, small)
+                assert np.all(np.abs(R.f64(out)[r, i] - ref) <= tol) and np.all(np.abs(R.f64(lse)[r, i] - rl) <= tol_l)
+            # rejected drafts: no weight from them, none at their places
+            top = n + accepted[r] + 1
+            want, tol = S.weights(R.f64(q_rot)[r], kk[:top], 1 / math.sqrt(D), R.f64(lse)[r], seen[r].tolist(),
+                                  R.f64(old)[r, :top], 0.5, kv == "fp8")
+            assert np.all(np.abs(R.f64(weight)[r, :top] - want) <= tol) and (weight[r, top:] == 0).all()
+            true[r] = true[r][:top]
+            had[r] += accepted[r] + 1
+            key_of[r], value_of[r] = key_of[r][:had[r]], value_of[r][:had[r]]
+        length = (length + m + 1).to(torch.int32)
+
+
+def pos_behind(lengths, n):
+    return torch.arange(n, device="cuda").view(1, -1) >= _i32(lengths).view(-1, 1)
