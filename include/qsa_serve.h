@@ -135,6 +135,15 @@ qsa_status qsa_test_kv_weight_timeout(const qsa_dims* dims, float decay, const v
  * q_pos. qsa_kv_append's own rotation is at the place, which is wrong here, and
  * nothing can report it.
  *
+ * K, V and weights move, and nothing else: the call is for the dense attention
+ * (qsa_paged_attn, qsa_prefix_attn). qsa.h's sparse step chooses through a
+ * compressed key of each 4 neighbouring positions, held beside the cache or in
+ * its pages, and 4 places that are neighbours now were other blocks before. A
+ * caller who wants that step on an evicted request puts the tokens' index keys
+ * into their new order by `kept` and compresses all of them anew
+ * (qsa_compress_keys or _paged, block_lo NULL); a block is then 4 tokens that
+ * have become neighbours.
+ *
  * keep is 1..out_pages * page_size, sinks and recent at least 0 with sinks +
  * recent <= keep. weight is fp32 [batch][max_pages * page_size], weight_out
  * fp32 [batch][out_pages * page_size] (they must not overlap), kept int32

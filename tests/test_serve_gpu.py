@@ -1638,3 +1638,60 @@ def test_decoding_on_after_an_eviction(qsa, kv):
 
 def pos_behind(lengths, n):
     return torch.arange(n, device="cuda").view(1, -1) >= _i32(lengths).view(-1, 1)
+
+
+def test_sparse_step_after_an_eviction(qsa):
+    """The sparse step on an evicted cache, its compressed keys made anew from the
+    index keys in their new order, against the oracle on the tokens that stay."""
+    from block_sparse_attention_qsa_gb300 import synth
+    from oracle import qsa_oracle as O
+
+    B, n_q, keep, sinks, recent = 2, 4, 2500, 4, 100
+    spec = synth.Spec("evicted", B, n_q, [3000, 2700], 1, "bf16", True, 4243)
+    inp = {k: v.cuda() for k, v in synth.make_inputs(spec).items()}
+    d = qsa.dims_for_spec(spec)
+    ps, pages = d.page_size, inp["k_cache"].shape[0]
+    width = -(-keep // ps)
+    blank = torch.zeros((B * width, *inp["k_cache"].shape[1:]), dtype=torch.bfloat16, device="cuda")
+    kc, vc = torch.cat([inp["k_cache"], blank]), torch.cat([inp["v_cache"], blank])
+    k0, v0 = kc.clone(), vc.clone()
+    table_out = (torch.arange(B * width, dtype=torch.int32, device="cuda") + pages).view(B, width)
+    length = inp["q_pos"].amax(1) + 1
+    g = torch.Generator(device="cuda").manual_seed(91)
+    weight = torch.rand((B, d.max_pages * ps), generator=g, device="cuda")
+    weight_out, kept = torch.empty((B, width * ps), device="cuda"), torch.empty((B, keep), dtype=torch.int32, device="cuda")
+    d_all = _dims(qsa, B, d.max_pages, pages + B * width, "bf16", n_q, 16, 2, 128, ps)
+    new_length = torch.empty_like(length)
+    ws = qsa.make_kv_workspace(d_all)
+    qsa.kv_evict(d_all, kc, vc, inp["page_table"], table_out, length, weight, weight_out, kept, new_length, ws,
+                 sinks=sinks, recent=recent)
+    _ok(qsa, ws)
+    assert new_length.tolist() == [keep] * B
+    # the newest n_q tokens are the verify queries', at the end of either order
+    q_pos = (new_length.view(B, 1) - n_q + torch.arange(n_q, device="cuda")).to(torch.int32)
+    order = kept.long()
+    idx = torch.stack([inp["idx_keys"][r][order[r]] for r in range(B)]).contiguous()
+    blocks = keep // 4
+    d1 = qsa.make_dims(B, n_q, blocks, width, pages + B * width, 1, "bf16", ps)
+    comp = torch.zeros((B, blocks, 1, 128), dtype=torch.bfloat16, device="cuda")
+    ws1 = qsa.make_workspace(d1)
+    qsa.compress_keys(d1, idx, q_pos, comp, ws1)
+    out = torch.empty((B, n_q, 16, 128), dtype=torch.bfloat16, device="cuda")
+    sel = torch.empty((B, n_q, 2051), dtype=torch.int32, device="cuda")
+    qsa.decode(d1, inp["q_idx"], comp, inp["q"], kc, vc, inp["k_scale"], inp["v_scale"], table_out, q_pos, out, ws1,
+               sel_pos=sel)
+    _ok(qsa, ws1)
+    # the oracle: a cache in which the tokens that stay lie in their order, taken from the cache before the call
+    bits = lambda t: t.contiguous().cpu().view(torch.int16).numpy().view(np.uint16)  # noqa: E731
+    at = torch.arange(keep, device="cuda")
+    for r in range(B):
+        page = inp["page_table"][r].long()[order[r] // ps]
+        for x in (k0, v0):
+            x[table_out[r].long()[at // ps], :, at % ps] = x[page, :, order[r] % ps]
+    npi = {"q_idx": bits(inp["q_idx"]), "q": bits(inp["q"]), "k_cache": bits(k0), "v_cache": bits(v0),
+           "page_table": table_out.cpu().numpy(), "q_pos": q_pos.cpu().numpy(),
+           "kc": np.stack([O.compress_keys(bits(idx[r]), blocks) for r in range(B)])}
+    ref = O.decode_step(npi, "bf16")
+    for (r, j), o in ref["out"].items():
+        assert np.array_equal(sel[r, j].cpu().numpy(), ref["sel_pos"][(r, j)])
+        assert np.max(np.abs(out[r, j].float().cpu().numpy() - o)) <= 1e-2
