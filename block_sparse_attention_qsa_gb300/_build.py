@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -74,6 +75,31 @@ def _fast_cmd(out: str):
             os.path.join(CSRC, "qsa_fast.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def check_registers(log: str) -> int:
+    """Raises where the compiler's report has a prefix_kernel whose registers are
+    not those that its warpgroups share out: a thread's part of 65,536, in steps
+    of 8. Its setmaxnreg would wait for registers that the launch does not have
+    (the library refuses such a launch, with no more than a CUDA error). Kernels of
+    up to 256 threads share nothing out. Returns the kernels seen."""
+    seen, kernel = 0, None
+    for line in log.splitlines():
+        entry = re.search(r"Compiling entry function '(\w+)'", line)
+        if entry:  # prefix_kernel<Pc<head dim, E4M3, row tiles>>
+            kernel = re.search(r"prefix_kernelI\w*?2PcILi(\d+)ELb([01])ELi(\d+)E", entry.group(1))
+        used = re.search(r"Used (\d+) registers", line)
+        if used and kernel:
+            seen += 1
+            threads = 128 * (int(kernel.group(3)) + int(kernel.group(2)) + 1)
+            want = 65536 // threads // 8 * 8
+            if threads > 256 and int(used.group(1)) != want:
+                raise RuntimeError(
+                    f"prefix_kernel of head dim {kernel.group(1)}, {'E4M3' if kernel.group(2) == '1' else 'BF16'}, "
+                    f"{kernel.group(3)} row tiles: {used.group(1)} registers a thread, its warpgroups share out {want}: "
+                    "this compiler needs other shares (kSoftRegs, kOtherRegs in qsa_prefix.cuh)")
+            kernel = None
+    return seen
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: bool = False) -> str:
     """Compile and link libqsa.so (or, with ``trace``, libqsa_trace.so), and
     the fast path's module; returns the library's path. Of the two, what is
@@ -95,7 +121,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
         for src in sources():
             obj = os.path.join(bdir, os.path.basename(src)[:-3] + ".o")
             objs.append(obj)
-            cmds.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
+            report = ["-Xptxas", "-v"] if os.path.basename(src).startswith("qsa_prefix") else []
+            cmds.append([cc, *ARCH, *FLAGS, *report, *extra_flags, "-c", src, "-o", obj])
 
     def run(cmd):
         if verbose:
@@ -117,6 +144,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
         logs = list(ex.map(run, cmds))
         if made_fast:
             made_fast.result()
+    if make_lib and check_registers("\n".join(logs)) == 0:
+        warnings.warn("the compiler's report names no prefix_kernel: its registers were not checked", RuntimeWarning)
     if verbose:
         for lg in logs:
             if lg.strip():

@@ -201,3 +201,47 @@ def test_binding_refuses_host_tensors(qsa):
         qsa.verify_drafts(p[0], None, t, torch.zeros((1, 2)), one, torch.zeros((1, 2), dtype=i32), ws)
     with pytest.raises(TypeError, match="tensor"):
         qsa.prefix_attn(d, None, kc, kc, None, None, one, t, t, q, ws)
+
+
+REPORT = """ptxas info    : 0 bytes gmem
+ptxas info    : Compiling entry function '_ZN3qsa1_18prefix_join_kernelILi64ELb0ELi4EEEvNS_10PrefixArgsE' for 'sm_103a'
+ptxas info    : Used 77 registers, used 1 barriers
+ptxas info    : Compiling entry function '_ZN3qsa1_prefix_kernelINS0_2PcILi%dELb%dELi%dEEEEEv14CUtensorMap_st' for 'sm_103a'
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used %d registers, used 16 barriers, 1424 bytes smem
+"""
+
+
+def test_build_checks_the_registers_that_warpgroups_share_out():
+    from block_sparse_attention_qsa_gb300 import _build
+
+    # (head dim, E4M3, row tiles, registers): 512, 384 and 256 threads
+    for good in ((128, 1, 2, 128), (64, 0, 2, 168), (256, 1, 1, 168), (128, 0, 1, 158), (256, 0, 1, 110)):
+        assert _build.check_registers(REPORT % good) == 1
+    for bad in ((128, 1, 2, 120), (64, 0, 2, 160), (256, 1, 1, 166)):
+        with pytest.raises(RuntimeError, match=f"head dim {bad[0]}.*{bad[3]} registers"):
+            _build.check_registers(REPORT % (64, 1, 2, 128) + REPORT % bad)
+    assert _build.check_registers("ptxas info    : Used 77 registers") == 0
+
+
+def test_build_stops_at_registers_that_do_not_add_up(monkeypatch, tmp_path):
+    from block_sparse_attention_qsa_gb300 import _build
+
+    linked, asked = [], []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", REPORT % (128, 1, 2, 120)
+
+    def run(cmd, **kw):
+        (linked if "-shared" in cmd else asked).append(cmd)
+        return Done()
+
+    for name, to in (("LIB", "lib.so"), ("BUILD", "b")):
+        monkeypatch.setattr(_build, name, str(tmp_path / to))
+    monkeypatch.setattr(_build, "sources", lambda: [str(tmp_path / "qsa_prefix_128.cu")])
+    monkeypatch.setattr(_build, "_newest_input", lambda: 0.0)
+    monkeypatch.setattr(_build, "fast_path", lambda: __file__)  # (there already)
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    with pytest.raises(RuntimeError, match="120 registers a thread"):
+        _build.build()
+    assert len(asked) == 1 and asked[0][asked[0].index("-Xptxas") + 1] == "-v" and not linked
