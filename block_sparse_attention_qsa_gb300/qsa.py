@@ -785,7 +785,8 @@ def prefix_workspace_size(d: Dims, prefix_pages: int) -> int:
 def make_prefix_workspace(d: Dims, prefix_pages: int, device="cuda", stream=None) -> torch.Tensor:
     """Allocate and zero a workspace for prefix_attn with ``d`` and up to
     ``prefix_pages`` shared pages; the other operators round the cache can be
-    called on it too (torch owns the memory)."""
+    called on it too (torch owns the memory: 30 to 60 MB for a long prefix at
+    head dim 128)."""
     n = prefix_workspace_size(d, prefix_pages)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     assert ws.data_ptr() % 256 == 0

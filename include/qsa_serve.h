@@ -31,7 +31,11 @@ extern "C" {
 
 /* Bytes of workspace for qsa_prefix_attn with these dims and this many shared
  * pages (at least qsa_kv_workspace_size's, so that qsa_kv.h's entry points can
- * be called on the same one). */
+ * be called on the same one; enough for fewer shared pages too). Where a long
+ * prefix is read in parts there is room for the pieces of three waves of them: 3
+ * to 6 pieces of 128 query rows an SM, head_dim + 2 floats a row (30 to 60 MB
+ * with head dim 128, more with the batch from about 250 requests x 4 queries over
+ * 8 KV heads on). A call mostly fills a third of it. */
 qsa_status qsa_prefix_workspace_size(const qsa_dims* dims, int32_t prefix_pages, size_t* bytes);
 
 /* Dense attention of a batch that shares a prefix: qsa_paged_attn (window 0)
