@@ -18,10 +18,13 @@
 // cycles a value and warp, and 256 rows of 150,001 tokens (FP32, sampled drafts)
 // 81 us; the conversion instruction to 64 bits was slower still, 158. So they
 // are added in FP32 without rounding (see Exact), 11 additions for two values:
-// 60 us, where the bytes take 38. What is left is those additions (16-bit
-// probabilities take 54), the SM that has four CTAs where others have three, and
-// the beginning and end of a CTA; a ring of bulk copies to shared memory in place
-// of the loads was slower (92), and so were shares for smaller or more CTAs.
+// 59 us, where the bytes take 37.5 (16-bit probabilities 53, at odd rows 57, the
+// bytes 18.8). Nothing is busy all the time: HBM 52 % (16 bits 28), the additions'
+// pipe 43 % of the SMs' busy time (50), issue slots 42 (49). A warp waits half of
+// its time for loads, which it issues only behind the additions of those before;
+// and 512 CTAs have 304 places, so that an SM has work for 79 % of the time, the
+// least busy one for 47. A ring of bulk copies to shared memory in place of the
+// loads was slower (92 us), and so were shares for smaller or more CTAs.
 #include "qsa_serve_internal.cuh"
 
 namespace qsa {
